@@ -9,7 +9,8 @@ Entry points mirror the C ABI in include/moe.h (workspace_bytes, max_tiles,
 route_blocks, route, forward, forward_residual, forward_timed, route_noalloc,
 status_read, status_string, test_route_stall, test_decode_stall) and
 include/attention.h (attn_workspace_bytes, attn_decode, attn_decode_timed) and
-include/gdn.h (gdn_scan, gdn_scan_timed).
+include/gdn.h (gdn_scan, gdn_scan_timed) and include/kv8.h (kv8_write,
+kv8_read, kv8_workspace_bytes, kv8_attn).
 """
 from __future__ import annotations
 
@@ -38,6 +39,15 @@ class AttnShape(ctypes.Structure):
 
 class GdnShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "Hqk", "Hv", "Dk", "Dv")]
+
+
+class Kv8Shape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "Hq", "Hkv", "D", "L_max", "block", "format", "q_stride",
+                                              "kv_stride")]
+
+
+class Kv8CacheC(ctypes.Structure):
+    _fields_ = [(n, P) for n in ("k_codes", "v_codes", "k_scales", "v_scales")]
 
 
 class QMat(ctypes.Structure):
@@ -106,6 +116,13 @@ def lib() -> ctypes.CDLL:
         L.moe_gdn_scan_timed.argtypes = [gp, P, P, P, P, P, P, P, P, P, P, ctypes.POINTER(P), P]
         L.moe_gdn_scan.restype = i32
         L.moe_gdn_scan_timed.restype = i32
+        kp, cp = ctypes.POINTER(Kv8Shape), ctypes.POINTER(Kv8CacheC)
+        L.moe_kv8_write.argtypes = [kp, P, P, P, P, cp, P, P]
+        L.moe_kv8_read.argtypes = [kp, cp, P, P, P, P, P, P]
+        L.moe_kv8_workspace_bytes.argtypes = [kp, ctypes.POINTER(sz)]
+        L.moe_kv8_attn.argtypes = [kp, P, cp, P, P, ctypes.c_float, P, P, sz, P]
+        for f in ("moe_kv8_write", "moe_kv8_read", "moe_kv8_workspace_bytes", "moe_kv8_attn"):
+            getattr(L, f).restype = i32
         for f in ("moe_workspace_bytes", "moe_max_tiles", "moe_route_blocks", "moe_route", "moe_forward",
                   "moe_forward_timed", "moe_forward_residual",
                   "moe_status_read", "moe_test_route_stall", "moe_test_decode_stall"):
@@ -343,3 +360,122 @@ def gdn_scan_timed(shape, q, k, v, gate, beta, offsets, state_in, state_out, o, 
     _check(lib().moe_gdn_scan_timed(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(gate), _ptr(beta),
                                     _ptr(offsets), _ptr(state_in), _ptr(state_out), _ptr(o), _ptr(status), ev,
                                     _stream(stream)), "moe_gdn_scan_timed")
+
+
+# ------------------------------------------------------- 8-bit KV cache ---
+
+KV8_INT8, KV8_E4M3 = 0, 1
+
+
+def kv8_shape(B, T, Hq, Hkv, D, L_max, block=64, format=KV8_INT8, q_stride=0, kv_stride=0) -> Kv8Shape:
+    """A call over B sequences with T packed tokens in all. q_stride and
+    kv_stride: elements between the tokens of q and of k_new, v_new (0:
+    packed), for tokens that are column ranges of one projection's output."""
+    return Kv8Shape(B, T, Hq, Hkv, D, L_max, block, format, q_stride, kv_stride)
+
+
+class Kv8Cache:
+    """An 8-bit KV cache's tensors: codes [B, Hkv, L_max, D] (uint8, or
+    float8_e4m3fn for KV8_E4M3) and scales fp32 [B, Hkv, ceil(L_max / block)],
+    contiguous."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+
+
+def kv8_alloc_cache(shape: Kv8Shape, device) -> Kv8Cache:
+    """An empty cache for `shape` (its contents need no initialisation)."""
+    dt = torch.float8_e4m3fn if shape.format == KV8_E4M3 else torch.uint8
+    codes = [torch.empty(shape.B, shape.Hkv, shape.L_max, shape.D, dtype=dt, device=device) for _ in range(2)]
+    nblk = -(-shape.L_max // shape.block)
+    return Kv8Cache(*codes, *[torch.empty(shape.B, shape.Hkv, nblk, device=device) for _ in range(2)])
+
+
+def _kv8_refuse(where, what):
+    raise MoeError(MOE_ERR_INVALID_ARG, where, what)
+
+
+def _kv8_tensor(where, name, t, dev, dtype, dims, strides):
+    """t's address, after the checks the C entry points cannot make: type,
+    sizes, strides (of dimensions longer than one) and device."""
+    if t.dtype != dtype:
+        _kv8_refuse(where, f"{name} is {t.dtype}, not {dtype}")
+    if t.shape != dims:
+        _kv8_refuse(where, f"{name} has shape {tuple(t.shape)}, not {dims}")
+    if t.stride() != strides and any(n > 1 and a != b for n, a, b in zip(dims, t.stride(), strides)):
+        _kv8_refuse(where, f"{name} has strides {t.stride()}, not {strides}")
+    if t.get_device() != dev:
+        _kv8_refuse(where, f"{name} is on {t.device}, not on the current device, cuda:{dev}")
+    return t.data_ptr()
+
+
+def _kv8_cache(where, shape, cache, dev) -> Kv8CacheC:
+    B, H, L, D, nblk = shape.B, shape.Hkv, shape.L_max, shape.D, -(-shape.L_max // max(shape.block, 1))
+    dims, strides = (B, H, L, D), (H * L * D, L * D, D, 1)
+    sdims, sstrides = (B, H, nblk), (H * nblk, nblk, 1)
+    k, v, f32 = cache.k, cache.v, torch.float32
+    dt = torch.float8_e4m3fn if shape.format == KV8_E4M3 and k.dtype == torch.float8_e4m3fn else torch.uint8
+    return Kv8CacheC(_kv8_tensor(where, "k", k, dev, dt, dims, strides),
+                     _kv8_tensor(where, "v", v, dev, dt, dims, strides),
+                     _kv8_tensor(where, "k_scale", cache.k_scale, dev, f32, sdims, sstrides),
+                     _kv8_tensor(where, "v_scale", cache.v_scale, dev, f32, sdims, sstrides))
+
+
+def _kv8_tables(where, shape, dev, offsets, per_sequence, name):
+    i32, B = torch.int32, shape.B
+    return (_kv8_tensor(where, "offsets", offsets, dev, i32, (B + 1,), (1,)),
+            _kv8_tensor(where, name, per_sequence, dev, i32, (B,), (1,)))
+
+
+def kv8_write(shape, k_new, v_new, offsets, starts, cache: Kv8Cache, status=None, stream=None):
+    """moe_kv8_write: quantises k_new, v_new bf16 [T, Hkv, D] into `cache`;
+    sequence b's tokens offsets[b] .. offsets[b+1]-1 go to its positions
+    starts[b] .. (int32 [B+1] and [B]). status: an optional zeroed int32
+    device word."""
+    w, dev = "moe_kv8_write", torch.cuda.current_device()
+    T, H, D = shape.T, shape.Hkv, shape.D
+    dims, strides = (T, H, D), (shape.kv_stride or H * D, D, 1)
+    k = _kv8_tensor(w, "k_new", k_new, dev, torch.bfloat16, dims, strides)
+    v = _kv8_tensor(w, "v_new", v_new, dev, torch.bfloat16, dims, strides)
+    off, st = _kv8_tables(w, shape, dev, offsets, starts, "starts")
+    c = _kv8_cache(w, shape, cache, dev)
+    _check(lib().moe_kv8_write(shape, k, v, off, st, c, _ptr(status), _stream(stream)), w)
+
+
+def kv8_read(shape, cache: Kv8Cache, offsets, starts, k_out, v_out, status=None, stream=None):
+    """moe_kv8_read: positions starts[b] .. of every sequence as bf16, packed
+    in k_out, v_out [T, Hkv, D]."""
+    w, dev = "moe_kv8_read", torch.cuda.current_device()
+    T, H, D = shape.T, shape.Hkv, shape.D
+    dims, strides = (T, H, D), (H * D, D, 1)
+    k = _kv8_tensor(w, "k_out", k_out, dev, torch.bfloat16, dims, strides)
+    v = _kv8_tensor(w, "v_out", v_out, dev, torch.bfloat16, dims, strides)
+    off, st = _kv8_tables(w, shape, dev, offsets, starts, "starts")
+    c = _kv8_cache(w, shape, cache, dev)
+    _check(lib().moe_kv8_read(shape, c, off, st, k, v, _ptr(status), _stream(stream)), w)
+
+
+def kv8_workspace_bytes(shape: Kv8Shape) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().moe_kv8_workspace_bytes(ctypes.byref(shape), ctypes.byref(n)), "moe_kv8_workspace_bytes")
+    return n.value
+
+
+def kv8_alloc_workspace(shape: Kv8Shape, device) -> torch.Tensor:
+    return torch.empty(kv8_workspace_bytes(shape), dtype=torch.uint8, device=device)
+
+
+def kv8_attn(shape, q, cache: Kv8Cache, offsets, lens, o, workspace, scale=None, stream=None):
+    """moe_kv8_attn: q bf16 [T, Hq, D], the last tokens of every sequence
+    (offsets int32 [B+1]) over its lens[b] cached positions (int32 [B]); o bf16
+    [T, Hq, D]. The workspace's first int32 is the call's device status word."""
+    w, dev = "moe_kv8_attn", torch.cuda.current_device()
+    T, H, D = shape.T, shape.Hq, shape.D
+    qp = _kv8_tensor(w, "q", q, dev, torch.bfloat16, (T, H, D), (shape.q_stride or H * D, D, 1))
+    op = _kv8_tensor(w, "o", o, dev, torch.bfloat16, (T, H, D), (H * D, D, 1))
+    off, ln = _kv8_tables(w, shape, dev, offsets, lens, "lens")
+    c = _kv8_cache(w, shape, cache, dev)
+    n = workspace.numel() * workspace.element_size()
+    wp = _kv8_tensor(w, "workspace", workspace, dev, torch.uint8, (n,), (1,))
+    s = 1.0 / (D ** 0.5) if scale is None else float(scale)
+    _check(lib().moe_kv8_attn(shape, qp, c, off, ln, s, op, wp, n, _stream(stream)), w)

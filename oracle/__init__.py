@@ -37,3 +37,4 @@ from .moe import (  # noqa: F401
 )
 from .attention import gqa_decode_attention  # noqa: F401,E402
 from .gated_deltanet import gated_delta_scan  # noqa: F401,E402
+from . import kv8  # noqa: F401,E402
