@@ -374,13 +374,67 @@ def kv8_shape(B, T, Hq, Hkv, D, L_max, block=64, format=KV8_INT8, q_stride=0, kv
     return Kv8Shape(B, T, Hq, Hkv, D, L_max, block, format, q_stride, kv_stride)
 
 
+def _kv8_refuse(where, what):
+    raise MoeError(MOE_ERR_INVALID_ARG, where, what)
+
+
+def _kv8_tensor(where, name, t, dev, dtype, dims, strides):
+    """t's address, after the checks the C entry points cannot make: type,
+    sizes, strides (of dimensions longer than one) and device. The usual
+    tensor passes the first line; a call makes four of these checks."""
+    if t.dtype is dtype and t.shape == dims and t.stride() == strides and t.get_device() == dev:
+        return t.data_ptr()
+    if t.dtype is not dtype:
+        _kv8_refuse(where, f"{name} is {t.dtype}, not {dtype}")
+    if t.shape != dims:
+        _kv8_refuse(where, f"{name} has shape {tuple(t.shape)}, not {dims}")
+    if any(n > 1 and a != b for n, a, b in zip(dims, t.stride(), strides)) and t.numel() > 0:
+        _kv8_refuse(where, f"{name} has strides {t.stride()}, not {strides}")
+    if t.get_device() != dev:
+        _kv8_refuse(where, f"{name} is on {t.device}, not on cuda:{dev}")
+    return t.data_ptr()
+
+
 class Kv8Cache:
-    """An 8-bit KV cache's tensors: codes [B, Hkv, L_max, D] (uint8, or
-    float8_e4m3fn for KV8_E4M3) and scales fp32 [B, Hkv, ceil(L_max / block)],
-    contiguous."""
+    """An 8-bit KV cache: codes [B, Hkv, L_max, D] (uint8, or float8_e4m3fn
+    for KV8_E4M3) and scales fp32 [B, Hkv, ceil(L_max / block)], contiguous, on
+    one device. The tensors are checked here, once, and belong to the cache
+    from then on (read them as .k, .v, .k_scale, .v_scale)."""
+
+    __slots__ = ("_t", "_c", "_dims", "_nblk", "_e4m3", "_dev")
 
     def __init__(self, k, v, k_scale, v_scale):
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        w = "Kv8Cache"
+        if k.dim() != 4 or k_scale.dim() != 3 or k.dtype not in (torch.uint8, torch.float8_e4m3fn):
+            _kv8_refuse(w, f"k is {k.dtype} {tuple(k.shape)}, k_scale {tuple(k_scale.shape)}: codes are uint8 or "
+                           "float8_e4m3fn [B, Hkv, L_max, D], scales [B, Hkv, blocks]")
+        dims, dev = tuple(k.shape), k.get_device()
+        B, H, L, D = dims
+        nblk = k_scale.shape[2]
+        strides, sdims, sstrides = (H * L * D, L * D, D, 1), (B, H, nblk), (H * nblk, nblk, 1)
+        self._c = Kv8CacheC(_kv8_tensor(w, "k", k, dev, k.dtype, dims, strides),
+                            _kv8_tensor(w, "v", v, dev, k.dtype, dims, strides),
+                            _kv8_tensor(w, "k_scale", k_scale, dev, torch.float32, sdims, sstrides),
+                            _kv8_tensor(w, "v_scale", v_scale, dev, torch.float32, sdims, sstrides))
+        self._t = (k, v, k_scale, v_scale)
+        self._dims, self._nblk, self._e4m3, self._dev = dims, nblk, k.dtype is torch.float8_e4m3fn, dev
+
+    k = property(lambda self: self._t[0])
+    v = property(lambda self: self._t[1])
+    k_scale = property(lambda self: self._t[2])
+    v_scale = property(lambda self: self._t[3])
+
+    def _device(self, where, shape):
+        """The cache's device, after checking that it is the current one and
+        that the cache is one of `shape`."""
+        L = shape.L_max
+        if self._dims != (shape.B, shape.Hkv, L, shape.D) or self._nblk != -(-L // max(shape.block, 1)) or (
+                self._e4m3 and shape.format != KV8_E4M3):
+            _kv8_refuse(where, f"the cache holds {self._t[0].dtype} codes {self._dims} in {self._nblk} blocks, the shape "
+                               f"says otherwise")
+        if self._dev != torch.cuda.current_device():
+            _kv8_refuse(where, f"the cache is on {self._t[0].device}, not on the current device")
+        return self._dev
 
 
 def kv8_alloc_cache(shape: Kv8Shape, device) -> Kv8Cache:
@@ -391,40 +445,9 @@ def kv8_alloc_cache(shape: Kv8Shape, device) -> Kv8Cache:
     return Kv8Cache(*codes, *[torch.empty(shape.B, shape.Hkv, nblk, device=device) for _ in range(2)])
 
 
-def _kv8_refuse(where, what):
-    raise MoeError(MOE_ERR_INVALID_ARG, where, what)
-
-
-def _kv8_tensor(where, name, t, dev, dtype, dims, strides):
-    """t's address, after the checks the C entry points cannot make: type,
-    sizes, strides (of dimensions longer than one) and device."""
-    if t.dtype != dtype:
-        _kv8_refuse(where, f"{name} is {t.dtype}, not {dtype}")
-    if t.shape != dims:
-        _kv8_refuse(where, f"{name} has shape {tuple(t.shape)}, not {dims}")
-    if t.stride() != strides and any(n > 1 and a != b for n, a, b in zip(dims, t.stride(), strides)):
-        _kv8_refuse(where, f"{name} has strides {t.stride()}, not {strides}")
-    if t.get_device() != dev:
-        _kv8_refuse(where, f"{name} is on {t.device}, not on the current device, cuda:{dev}")
-    return t.data_ptr()
-
-
-def _kv8_cache(where, shape, cache, dev) -> Kv8CacheC:
-    B, H, L, D, nblk = shape.B, shape.Hkv, shape.L_max, shape.D, -(-shape.L_max // max(shape.block, 1))
-    dims, strides = (B, H, L, D), (H * L * D, L * D, D, 1)
-    sdims, sstrides = (B, H, nblk), (H * nblk, nblk, 1)
-    k, v, f32 = cache.k, cache.v, torch.float32
-    dt = torch.float8_e4m3fn if shape.format == KV8_E4M3 and k.dtype == torch.float8_e4m3fn else torch.uint8
-    return Kv8CacheC(_kv8_tensor(where, "k", k, dev, dt, dims, strides),
-                     _kv8_tensor(where, "v", v, dev, dt, dims, strides),
-                     _kv8_tensor(where, "k_scale", cache.k_scale, dev, f32, sdims, sstrides),
-                     _kv8_tensor(where, "v_scale", cache.v_scale, dev, f32, sdims, sstrides))
-
-
-def _kv8_tables(where, shape, dev, offsets, per_sequence, name):
-    i32, B = torch.int32, shape.B
-    return (_kv8_tensor(where, "offsets", offsets, dev, i32, (B + 1,), (1,)),
-            _kv8_tensor(where, name, per_sequence, dev, i32, (B,), (1,)))
+def _kv8_stream(stream, dev):
+    # the handle of torch.cuda.current_stream(), without making a Stream object
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def kv8_write(shape, k_new, v_new, offsets, starts, cache: Kv8Cache, status=None, stream=None):
@@ -432,27 +455,35 @@ def kv8_write(shape, k_new, v_new, offsets, starts, cache: Kv8Cache, status=None
     sequence b's tokens offsets[b] .. offsets[b+1]-1 go to its positions
     starts[b] .. (int32 [B+1] and [B]). status: an optional zeroed int32
     device word."""
-    w, dev = "moe_kv8_write", torch.cuda.current_device()
-    T, H, D = shape.T, shape.Hkv, shape.D
+    w = "moe_kv8_write"
+    dev = cache._device(w, shape)
+    T, H, D, B = shape.T, shape.Hkv, shape.D, shape.B
     dims, strides = (T, H, D), (shape.kv_stride or H * D, D, 1)
-    k = _kv8_tensor(w, "k_new", k_new, dev, torch.bfloat16, dims, strides)
-    v = _kv8_tensor(w, "v_new", v_new, dev, torch.bfloat16, dims, strides)
-    off, st = _kv8_tables(w, shape, dev, offsets, starts, "starts")
-    c = _kv8_cache(w, shape, cache, dev)
-    _check(lib().moe_kv8_write(shape, k, v, off, st, c, _ptr(status), _stream(stream)), w)
+    rc = lib().moe_kv8_write(shape, _kv8_tensor(w, "k_new", k_new, dev, torch.bfloat16, dims, strides),
+                             _kv8_tensor(w, "v_new", v_new, dev, torch.bfloat16, dims, strides),
+                             _kv8_tensor(w, "offsets", offsets, dev, torch.int32, (B + 1,), (1,)),
+                             _kv8_tensor(w, "starts", starts, dev, torch.int32, (B,), (1,)), cache._c,
+                             None if status is None else _kv8_tensor(w, "status", status, dev, torch.int32, (1,), (1,)),
+                             _kv8_stream(stream, dev))
+    if rc:
+        _check(rc, w)
 
 
 def kv8_read(shape, cache: Kv8Cache, offsets, starts, k_out, v_out, status=None, stream=None):
     """moe_kv8_read: positions starts[b] .. of every sequence as bf16, packed
     in k_out, v_out [T, Hkv, D]."""
-    w, dev = "moe_kv8_read", torch.cuda.current_device()
-    T, H, D = shape.T, shape.Hkv, shape.D
+    w = "moe_kv8_read"
+    dev = cache._device(w, shape)
+    T, H, D, B = shape.T, shape.Hkv, shape.D, shape.B
     dims, strides = (T, H, D), (H * D, D, 1)
-    k = _kv8_tensor(w, "k_out", k_out, dev, torch.bfloat16, dims, strides)
-    v = _kv8_tensor(w, "v_out", v_out, dev, torch.bfloat16, dims, strides)
-    off, st = _kv8_tables(w, shape, dev, offsets, starts, "starts")
-    c = _kv8_cache(w, shape, cache, dev)
-    _check(lib().moe_kv8_read(shape, c, off, st, k, v, _ptr(status), _stream(stream)), w)
+    rc = lib().moe_kv8_read(shape, cache._c, _kv8_tensor(w, "offsets", offsets, dev, torch.int32, (B + 1,), (1,)),
+                            _kv8_tensor(w, "starts", starts, dev, torch.int32, (B,), (1,)),
+                            _kv8_tensor(w, "k_out", k_out, dev, torch.bfloat16, dims, strides),
+                            _kv8_tensor(w, "v_out", v_out, dev, torch.bfloat16, dims, strides),
+                            None if status is None else _kv8_tensor(w, "status", status, dev, torch.int32, (1,), (1,)),
+                            _kv8_stream(stream, dev))
+    if rc:
+        _check(rc, w)
 
 
 def kv8_workspace_bytes(shape: Kv8Shape) -> int:
@@ -469,13 +500,16 @@ def kv8_attn(shape, q, cache: Kv8Cache, offsets, lens, o, workspace, scale=None,
     """moe_kv8_attn: q bf16 [T, Hq, D], the last tokens of every sequence
     (offsets int32 [B+1]) over its lens[b] cached positions (int32 [B]); o bf16
     [T, Hq, D]. The workspace's first int32 is the call's device status word."""
-    w, dev = "moe_kv8_attn", torch.cuda.current_device()
-    T, H, D = shape.T, shape.Hq, shape.D
-    qp = _kv8_tensor(w, "q", q, dev, torch.bfloat16, (T, H, D), (shape.q_stride or H * D, D, 1))
-    op = _kv8_tensor(w, "o", o, dev, torch.bfloat16, (T, H, D), (H * D, D, 1))
-    off, ln = _kv8_tables(w, shape, dev, offsets, lens, "lens")
-    c = _kv8_cache(w, shape, cache, dev)
-    n = workspace.numel() * workspace.element_size()
-    wp = _kv8_tensor(w, "workspace", workspace, dev, torch.uint8, (n,), (1,))
-    s = 1.0 / (D ** 0.5) if scale is None else float(scale)
-    _check(lib().moe_kv8_attn(shape, qp, c, off, ln, s, op, wp, n, _stream(stream)), w)
+    w = "moe_kv8_attn"
+    dev = cache._device(w, shape)
+    T, H, D, B, n = shape.T, shape.Hq, shape.D, shape.B, workspace.numel()
+    dims = (T, H, D)
+    rc = lib().moe_kv8_attn(shape, _kv8_tensor(w, "q", q, dev, torch.bfloat16, dims, (shape.q_stride or H * D, D, 1)),
+                            cache._c, _kv8_tensor(w, "offsets", offsets, dev, torch.int32, (B + 1,), (1,)),
+                            _kv8_tensor(w, "lens", lens, dev, torch.int32, (B,), (1,)),
+                            D ** -0.5 if scale is None else scale,
+                            _kv8_tensor(w, "o", o, dev, torch.bfloat16, dims, (H * D, D, 1)),
+                            _kv8_tensor(w, "workspace", workspace, dev, torch.uint8, (n,), (1,)), n,
+                            _kv8_stream(stream, dev))
+    if rc:
+        _check(rc, w)

@@ -4,7 +4,7 @@
 // and walk the visible positions with the running maximum and sum of a
 // softmax, so the scores are never stored.
 #include "kernels.h"
-#include "kv8.cuh"
+#include "kv8_attn.h"
 
 #include <type_traits>
 
@@ -13,20 +13,6 @@ namespace kv8 {
 
 constexpr int kWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f;
-
-struct AttnArgs {
-  const uint16_t* q;
-  const uint8_t* k;
-  const uint8_t* v;
-  const float* ks;
-  const float* vs;
-  const int32_t* offsets;
-  const int32_t* lens;
-  uint16_t* o;
-  int32_t* status;
-  int B, T, Hq, Hkv, L_max, nblk, block, q_stride;
-  float scale_log2;
-};
 
 template <int D, bool kE4m3>
 __global__ void __launch_bounds__(kWarps * 32) kv8_rows_kernel(const AttnArgs p) {
@@ -56,7 +42,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_rows_kernel(const AttnArgs p)
     }
   }
   bad = __any_sync(0xffffffffu, bad);
-  if (row == 0 && lane == 0) *p.status = bad ? (int32_t)MOE_ERR_INVALID_ARG : 0;
+  if (row == 0 && lane == 0) *static_cast<int32_t*>(p.workspace) = bad ? (int32_t)MOE_ERR_INVALID_ARG : 0;
   if (bad || t >= p.T) return;
   const int g = h / (p.Hq / p.Hkv);
   const size_t pair = (size_t)b * p.Hkv + g;
@@ -101,7 +87,10 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_rows_kernel(const AttnArgs p)
 
 namespace {
 
-size_t workspace_bytes(const moe_kv8_shape&) { return 256; }
+// Few query tokens per sequence: the split-context kernels; more: one warp per row.
+bool few(const moe_kv8_shape& s) { return s.T <= 8 * s.B; }
+
+size_t workspace_bytes(const moe_kv8_shape& s) { return few(s) ? split_workspace_bytes(s) : 256; }
 
 moe_status attn(const moe_kv8_shape* shape, const void* q, const moe_kv8_cache* cache, const int32_t* offsets,
                 const int32_t* lens, float scale, void* o, void* workspace, size_t ws_bytes, void* stream) {
@@ -121,8 +110,10 @@ moe_status attn(const moe_kv8_shape* shape, const void* q, const moe_kv8_cache* 
   }
   if (!q || !offsets || !lens || !o) return MOE_ERR_INVALID_ARG;
   AttnArgs p{static_cast<const uint16_t*>(q), cache->k_codes, cache->v_codes, cache->k_scales, cache->v_scales, offsets,
-             lens, static_cast<uint16_t*>(o), status, s.B, s.T, s.Hq, s.Hkv, s.L_max,
-             (s.L_max + s.block - 1) / s.block, s.block, s.q_stride ? s.q_stride : s.Hq * s.D, scale * kLog2e};
+             lens, static_cast<uint16_t*>(o), workspace, s.B, s.T, s.Hq, s.Hkv, s.D, s.L_max,
+             (s.L_max + s.block - 1) / s.block, s.block, s.format == MOE_KV8_E4M3,
+             s.q_stride ? s.q_stride : s.Hq * s.D, scale * kLog2e};
+  if (few(s)) return launch_split(p, st);
   const unsigned grid = (unsigned)(((long long)s.T * s.Hq + kWarps - 1) / kWarps);
   auto go = [&](auto d) {
     constexpr int D = decltype(d)::value;

@@ -1,0 +1,1013 @@
+// Attention over the 8-bit KV cache for few query tokens per sequence
+// (decode, verification of a few draft tokens), sm_103a.
+//
+// What bounds it is the cache's bytes: every position is read once per
+// (sequence, KV head, row tile), where a row tile is 8 kNT rows and a row one
+// (query token, query head of the KV head). The positions a tile can see are
+// cut into units of 64 and all units of the call are laid end to end in the
+// order (sequence, KV head, row tile, position); block c of a grid of C takes
+// the contiguous run [c N / C, (c+1) N / C), so the bytes spread evenly over
+// the SMs whatever the lengths are.
+//
+// kv8_split_kernel — warp 4 streams each unit's K and V codes (64 x D bytes
+// each) into a shared-memory ring by TMA; warps 0-3 take 16 positions each:
+//   S^T  = K Q^T     mma.sync m16n8k16 in fp16: M = 16 positions, N = 8 rows;
+//   online softmax per row on the base-2 scale;
+//   O^T += V^T P^T   M = 16 head dims, N = 8 rows, K = 16 positions.
+// Codes become fp16 operands in registers, after the ldmatrix:
+//   int8 K  the byte u = code + 128 as an fp16 subnormal, u 2^-24 (one byte
+//           permute per two values); the accumulators start at -128 sum(q) to
+//           take the 128 out again;
+//   int8 V  1024 + u by the same permute, minus 1152 (the sums over many
+//           positions must not carry an offset that cancels in the end);
+//   e4m3    the conversion instruction, exact in fp16.
+// ldmatrix moves 16-bit units, so a transposed load of V leaves the two bytes
+// of a unit, two neighbouring head dims, in one lane: they become rows g and
+// g + 8 of the MMA (dims 2g and 2g + 1), a renaming of rows that only the
+// store of O has to know. The same holds for the order of K's head dims
+// within 16, which the Q fragments share.
+//
+// Scales: a warp's 16 positions lie in one cache block. K's scale multiplies
+// the score. V's scale is folded into the softmax weight: with
+//   x_j = score_j + log2 s_v(j),  w_j = 2^(x_j - m + 14),  m = max x,
+// O = sum w_j code_j and L = sum w_j / s_v(j) give o = O / L. w <= 2^14 fits
+// fp16, whose subnormals reach 2^-38 below the largest weight; L sums the
+// fp32 weights, so it also keeps blocks whose values are all zero (s_v taken
+// as the smallest scale there). q goes to fp16 with its row's largest
+// magnitude in [1, 2), an exact step apart from values 2^-14 and more below it.
+//
+// kv8_merge_kernel — one block per (query token, query head, 64 head dims)
+// combines the partial states of the grid blocks that covered its tile, in a
+// fixed order:  M = max m_c,  o = sum 2^(m_c - M) O_c / sum 2^(m_c - M) L_c.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <type_traits>
+
+#include "kernels.h"
+#include "kv8_attn.h"
+#include "tc_ptx.cuh"
+
+namespace bgmoe {
+namespace kv8 {
+namespace split {
+
+using tc::elect_one;
+using tc::mbar_arrive;
+using tc::mbar_arrive_expect_tx;
+using tc::mbar_init;
+using tc::mbar_wait;
+using tc::smem_u32;
+
+constexpr int kPos = 64;            // positions per unit (= ring stage)
+constexpr int kConsumers = 4;       // warps, 16 positions each
+constexpr int kThreads = (kConsumers + 1) * 32;
+constexpr int kMaxCtas = 256;       // workspace bound on the grid
+constexpr long long kTimeoutNs = 1000000000ll;
+constexpr float kMinusBig = -1e30f; // running-max start: finite, so 2^(m - m_new) is never NaN
+constexpr float kWeightBits = 14.f; // the largest weight is 2^14
+
+template <int D, int kNT>
+struct Smem {
+  static constexpr int kSlabs = D < 128 ? 1 : D / 128;    // TMA boxes of up to 128 bytes by 64 rows
+  static constexpr int kSlab = kPos * (D < 128 ? D : 128);
+  static constexpr int kStageBytes = 2 * kSlabs * kSlab;  // K then V
+  // A warp's softmax state as its lanes hold it: D/4 accumulators, then two
+  // maxima and two sums, for each of the kNT groups; stored [value][lane].
+  static constexpr int kStateFloats = (D / 4 + 4) * kNT;
+  static constexpr int kStateBytes = kStateFloats * 32 * 4;
+  static constexpr int kMergeBytes = 3 * kStateBytes;     // warps 2, 3 (first fold) and warp 1 (second fold)
+  static constexpr int kFit = (220 * 1024 - kMergeBytes) / kStageBytes;
+  static constexpr int kStages = kFit > 12 ? 12 : kFit;
+  static constexpr int kCtlOffset = kStages * kStageBytes + kMergeBytes;
+  static constexpr int kBytes = kCtlOffset + 256 + 1024;  // + alignment slack
+  static_assert(kStages >= 3 && kBytes <= 227 * 1024, "shared memory");
+};
+
+template <int kStages>
+struct Ctl {
+  uint64_t full[kStages];
+  uint64_t empty[kStages];
+  uint64_t mrg_full;   // first fold: warps 2 and 3 have stored their states
+  uint64_t mrg_free;   // first fold: warps 0 and 1 have read them
+  uint64_t mrg2_full;  // second fold: warp 1 has stored its state
+  uint64_t mrg2_free;  // second fold: warp 0 has read it
+  int abort;
+};
+
+struct Params {
+  const uint16_t* q;
+  const float* ks;
+  const float* vs;
+  const int32_t* offsets;
+  const int32_t* lens;
+  float* part;       // [slots][RT] m, then [slots][RT] l, then [slots][RT][D] O
+  int32_t* flags;    // [C]: every grid block's outcome (0 or a moe_status), written each call
+  long long slots;
+  float scale_log2;
+  int B, T, Hq, Hkv, L_max, nblk, shift, q_stride;  // shift: log2 of the cache's block
+  long long timeout_ns;
+};
+
+// Row tile rt of a sequence with n query tokens over len positions: the units
+// of the positions that its last row sees.
+__device__ __forceinline__ int tile_units(int n, int len, int r, int RT, int rt) {
+  const int last = min(n * r, (rt + 1) * RT) - 1;
+  const int see = len - n + last / r + 1;
+  return see > 0 ? (see + kPos - 1) / kPos : 0;
+}
+__device__ __forceinline__ int seq_tiles(int n, int r, int RT) { return (n * r + RT - 1) / RT; }
+__device__ __forceinline__ long long seq_units(int n, int len, int r, int RT) {
+  long long u = 0;
+  for (int rt = 0; rt < seq_tiles(n, r, RT); ++rt) u += tile_units(n, len, r, RT, rt);
+  return u;
+}
+
+// The grid block whose run holds unit s: the largest c with floor(c*N/C) <= s.
+__device__ __forceinline__ int cta_of(long long s, long long N, int C) { return (int)(((s + 1) * C - 1) / N); }
+
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// d += A * B, A 16x16 (row), B 16x8 (col), fp16 in, fp32 accumulate.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
+  return h;
+}
+
+// Bytes 0, 1 and bytes 2, 3 of a K word as fp16 pairs (int8: u 2^-24).
+template <bool kE4m3>
+__device__ __forceinline__ void k_pairs(uint32_t w, uint32_t& p01, uint32_t& p23) {
+  if (kE4m3) {
+    p01 = e4m3x2_f16x2(w);
+    p23 = e4m3x2_f16x2(w >> 16);
+  } else {
+    p01 = __byte_perm(w, 0u, 0x4140);
+    p23 = __byte_perm(w, 0u, 0x4342);
+  }
+}
+
+// Bytes 0, 2 and bytes 1, 3 of a V word as fp16 pairs (int8: the code).
+template <bool kE4m3>
+__device__ __forceinline__ void v_pairs(uint32_t w, uint32_t& p02, uint32_t& p13) {
+  if (kE4m3) {
+    const uint32_t x = __byte_perm(w, 0u, 0x3120);
+    p02 = e4m3x2_f16x2(x);
+    p13 = e4m3x2_f16x2(x >> 16);
+  } else {
+    const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
+    const uint32_t a = __byte_perm(w, 0x64646464u, 0x4240), b = __byte_perm(w, 0x64646464u, 0x4341);
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
+    p02 = *reinterpret_cast<const uint32_t*>(&x);
+    p13 = *reinterpret_cast<const uint32_t*>(&y);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Place in the run: unit i of the nb units of row tile rt of KV head g of
+// sequence b; `tile` numbers the row tiles of the call.
+struct Cursor {
+  int b, g, rt, i, nb, n, len, lo, tile;
+  __device__ void sequence(const Params& p) {  // tables of sequence b (b < B)
+    lo = __ldg(p.offsets + b);
+    n = __ldg(p.offsets + b + 1) - lo;
+    len = __ldg(p.lens + b);
+  }
+  // The next unit; the caller knows that there is one.
+  __device__ void advance(const Params& p, int r, int RT) {
+    if (++i < nb) return;
+    i = 0;
+    do {
+      ++tile;
+      if (++rt >= seq_tiles(n, r, RT)) {
+        rt = 0;
+        if (++g >= p.Hkv) {
+          g = 0;
+          do {
+            if (++b >= p.B) return;
+            sequence(p);
+          } while (n == 0);
+        }
+      }
+      nb = tile_units(n, len, r, RT, rt);
+    } while (nb == 0);
+  }
+};
+
+template <int D, int kNT, bool kE4m3>
+__global__ void __launch_bounds__(kThreads, 1)
+    kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Params p) {
+  using S = Smem<D, kNT>;
+  constexpr int kStages = S::kStages;
+  constexpr int RT = 8 * kNT;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Ctl<kStages>* ctl = reinterpret_cast<Ctl<kStages>*>(smem + S::kCtlOffset);
+  static_assert(sizeof(Ctl<kStages>) <= 256, "control block");
+  float* mrg = reinterpret_cast<float*>(smem + kStages * S::kStageBytes);
+  __shared__ long long s_lo, s_hi;
+  __shared__ Cursor s_cur;
+  __shared__ int s_bad;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int C = gridDim.x, c = blockIdx.x;
+  const int r = p.Hq / p.Hkv;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&ctl->full[s], 1);
+      mbar_init(&ctl->empty[s], kConsumers);
+    }
+    mbar_init(&ctl->mrg_full, 2);
+    mbar_init(&ctl->mrg_free, 2);
+    mbar_init(&ctl->mrg2_full, 1);
+    mbar_init(&ctl->mrg2_free, 1);
+    ctl->abort = 0;
+    tc::fence_barrier_init();
+  }
+  if (warp == kConsumers) {
+    tc::prefetch_tmap(&tm_k);
+    tc::prefetch_tmap(&tm_v);
+  }
+  // Launched with programmatic dependent launch: the setup above overlaps the
+  // previous kernel on the stream. Everything below may read what earlier
+  // kernels wrote or overwrite what they read (the partial states and flags),
+  // so it waits for them first. Only then may this call's merge launch: it
+  // reads the tables before its own wait.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (warp == 0) {
+    // Check the tables, count the units and find where this block's run starts.
+    long long total = 0;
+    bool bad = false;
+    for (int base = 0; base < p.B; base += 32) {
+      const int b = base + lane;
+      long long v = 0;
+      if (b < p.B) {
+        const int lo = __ldg(p.offsets + b), hi = __ldg(p.offsets + b + 1), len = __ldg(p.lens + b);
+        if (offsets_bad(lo, hi, b, p.B, p.T) || len < 0 || len > p.L_max) bad = true;
+        else v = seq_units(hi - lo, len, r, RT);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      total += v;
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    total *= p.Hkv;
+    const long long lo = (long long)c * total / C, hi = (long long)(c + 1) * total / C;
+    if (!bad && lo < hi) {
+      long long acc = 0;
+      int tiles = 0;
+      for (int base = 0; base < p.B; base += 32) {
+        const int b = base + lane;
+        long long v = 0;
+        int nt = 0;
+        if (b < p.B) {
+          const int n = __ldg(p.offsets + b + 1) - __ldg(p.offsets + b);
+          v = seq_units(n, __ldg(p.lens + b), r, RT) * p.Hkv;
+          nt = seq_tiles(n, r, RT) * p.Hkv;
+        }
+        long long incl = v;
+        int tincl = nt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+          const int u = __shfl_up_sync(0xffffffffu, tincl, o);
+          if (lane >= o) {
+            incl += t;
+            tincl += u;
+          }
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, acc + incl > lo);
+        if (hit) {
+          if (lane == __ffs(hit) - 1) {
+            Cursor k;
+            k.b = b;
+            k.sequence(p);
+            long long off = lo - (acc + incl - v);
+            const long long per = v / p.Hkv;
+            k.g = (int)(off / per);
+            off -= k.g * per;
+            k.rt = 0;
+            k.nb = tile_units(k.n, k.len, r, RT, 0);
+            while (off >= k.nb) {
+              off -= k.nb;
+              k.nb = tile_units(k.n, k.len, r, RT, ++k.rt);
+            }
+            k.i = (int)off;
+            k.tile = tiles + tincl - nt + k.g * (nt / p.Hkv) + k.rt;
+            s_cur = k;
+          }
+          break;
+        }
+        acc += __shfl_sync(0xffffffffu, incl, 31);
+        tiles += __shfl_sync(0xffffffffu, tincl, 31);
+      }
+    }
+    if (lane == 0) {
+      s_lo = lo;
+      s_hi = hi;
+      s_bad = bad;
+    }
+  }
+  __syncthreads();
+  if (s_bad || s_lo >= s_hi) {
+    if (threadIdx.x == 0) p.flags[c] = s_bad ? (int32_t)MOE_ERR_INVALID_ARG : 0;
+    return;
+  }
+  const long long lo = s_lo, hi = s_hi;
+  Cursor cur = s_cur;
+
+  volatile int* abort_flag = &ctl->abort;
+  const uint64_t deadline = global_timer_ns() + (uint64_t)p.timeout_ns;
+  auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, deadline)) != 0;
+  };
+
+  if (warp == kConsumers) {
+    // ------------------------------------------------------------ producer
+    int s = 0, ph = 0, issued = 0;
+    for (long long j = lo; j < hi; ++j) {
+      if (issued >= kStages && !warp_wait(&ctl->empty[s], ph ^ 1)) break;
+      if (elect_one()) {
+        uint8_t* st = smem + s * S::kStageBytes;
+        const int pair = cur.b * p.Hkv + cur.g;
+        mbar_arrive_expect_tx(&ctl->full[s], (uint32_t)S::kStageBytes);
+#pragma unroll
+        for (int sl = 0; sl < S::kSlabs; ++sl) {
+          tma_load_3d(st + sl * S::kSlab, &tm_k, sl * 128, cur.i * kPos, pair, &ctl->full[s]);
+          tma_load_3d(st + (S::kSlabs + sl) * S::kSlab, &tm_v, sl * 128, cur.i * kPos, pair, &ctl->full[s]);
+        }
+      }
+      __syncwarp();
+      ++issued;
+      if (++s == kStages) {
+        s = 0;
+        ph ^= 1;
+      }
+      cur.advance(p, r, RT);
+    }
+    if (lane == 0 && *abort_flag) {  // let this block's own copies land before it exits
+      int dummy = 0;
+      const uint64_t dl = global_timer_ns() + 100000000ull;
+      for (int k = issued - kStages < 0 ? 0 : issued - kStages; k < issued; ++k)
+        mbar_wait(&ctl->full[k % kStages], (k / kStages) & 1, &dummy, dl);
+    }
+  } else {
+    // ----------------------------------------------------------- consumers
+    const int gq = lane >> 2, m4 = lane & 3;
+    // ldmatrix row addresses (relative to a slab): lanes 0-7, 8-15, 16-23,
+    // 24-31 address the four 8 x 16-byte matrices (positions +0, +8 of the
+    // low 16 dims, then of the high 16)
+    const int row = 16 * warp + (lane & 7) + ((lane >> 3) & 1) * 8;
+    const int ch = lane >> 4;
+    // TMA swizzle: 16-byte chunk ^= row % 8 (128-byte rows), (row / 2) % 4 (64-byte rows)
+    const int sw = D < 128 ? (row >> 1) & 3 : row & 7;
+
+    uint32_t qf[kNT][D / 16][2];   // Q as the B operand: row 8 nt + gq, dims 16 ks + 4 m4 .. + 3
+    float acc[kNT][D / 16][4];
+    float m[kNT][2], l[kNT][2];    // of rows 8 nt + 2 m4, + 1
+    float rq[kNT][2], off[kNT][2]; // score factor of the row's power of two; -128 sum(q) (int8)
+    int lim[kNT][2];               // visible positions
+    auto load_q = [&]() {
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) {
+        const int rr = cur.rt * RT + 8 * nt + gq;
+        const bool live = rr < cur.n * r;
+        const uint16_t* qrow = p.q + (size_t)(cur.lo + (live ? rr / r : 0)) * p.q_stride +
+                               (size_t)(cur.g * r + (live ? rr % r : 0)) * D + 4 * m4;
+        uint2 w[D / 16];
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          w[ks] = live ? __ldg(reinterpret_cast<const uint2*>(qrow + 16 * ks)) : make_uint2(0u, 0u);
+        uint32_t mx = 0u;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) mx = __vmaxu2(mx, __vmaxu2(w[ks].x & 0x7FFF7FFFu, w[ks].y & 0x7FFF7FFFu));
+        mx = max(mx & 0xFFFFu, mx >> 16);
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        // 2^-e with e the exponent of the largest magnitude (an infinity or a
+        // NaN makes the whole row NaN whatever e is)
+        const int e = min((int)(mx >> 7), 253);
+        const float down = __uint_as_float((uint32_t)(254 - e) << 23);
+        float sum = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          qf[nt][ks][0] = pack_f16(bf16_bits_to_f32(w[ks].x & 0xFFFFu) * down, bf16_bits_to_f32(w[ks].x >> 16) * down);
+          qf[nt][ks][1] = pack_f16(bf16_bits_to_f32(w[ks].y & 0xFFFFu) * down, bf16_bits_to_f32(w[ks].y >> 16) * down);
+          if (!kE4m3) {
+            const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&qf[nt][ks][0]));
+            const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&qf[nt][ks][1]));
+            sum += (a.x + a.y) + (b.x + b.y);
+          }
+        }
+        if (!kE4m3) {
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        }
+        const float up = ldexpf(p.scale_log2, e - 127);
+        const int see = live ? cur.len - cur.n + rr / r + 1 : 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {  // from the lanes of row 2 m4 + k
+          const int src = (2 * m4 + k) * 4;
+          rq[nt][k] = __shfl_sync(0xffffffffu, up, src);
+          lim[nt][k] = __shfl_sync(0xffffffffu, see, src);
+          off[nt][k] = kE4m3 ? 0.f : __shfl_sync(0xffffffffu, sum, src) * -7.62939453125e-06f;  // -128 2^-24
+        }
+      }
+    };
+    auto reset = [&]() {
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) {
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt) acc[nt][mt][0] = acc[nt][mt][1] = acc[nt][mt][2] = acc[nt][mt][3] = 0.f;
+        m[nt][0] = m[nt][1] = kMinusBig;
+        l[nt][0] = l[nt][1] = 0.f;
+      }
+    };
+    // The scales of this warp's 16 positions of the unit at a cursor (a group
+    // past the context repeats the last visible block's: it is not used).
+    auto load_scales = [&](const Cursor& k, float& sk, float& sv) {
+      const int pos = min(k.i * kPos + 16 * warp, k.len - 1);
+      const size_t at = (size_t)(k.b * p.Hkv + k.g) * p.nblk + (pos >> p.shift);
+      sk = __ldg(p.ks + at);
+      sv = __ldg(p.vs + at);
+    };
+    reset();
+    load_q();
+    float sk, sv;
+    load_scales(cur, sk, sv);
+
+    int s = 0, ph = 0, flushes = 0;
+    for (long long j = lo; j < hi; ++j) {
+      Cursor nxt = cur;
+      float skn = 0.f, svn = 0.f;
+      if (j + 1 < hi) {  // the next unit's scales travel while this one is computed
+        nxt.advance(p, r, RT);
+        load_scales(nxt, skn, svn);
+      }
+      if (!warp_wait(&ctl->full[s], ph)) break;
+      const uint32_t sK = smem_u32(smem + s * S::kStageBytes);
+      const uint32_t sV = sK + S::kSlabs * S::kSlab;
+      auto chunk_addr = [&](uint32_t base, int kk) -> uint32_t {  // dims 32 kk .. + 31
+        constexpr int kPerSlab = D < 128 ? 2 : 4;
+        const int cc = (kk % kPerSlab) * 2 + ch;
+        return base + (kk / kPerSlab) * S::kSlab + row * (D < 128 ? 64 : 128) + ((cc ^ sw) << 4);
+      };
+      const int pos0 = cur.i * kPos + 16 * warp;  // first position of this warp's 16
+      if (pos0 < cur.len) {
+        float x[kNT][4];
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+          x[nt][0] = x[nt][2] = off[nt][0];
+          x[nt][1] = x[nt][3] = off[nt][1];
+        }
+        float y[4] = {0.f, 0.f, 0.f, 0.f};  // one row group: a second accumulator halves the dependent chain
+#pragma unroll
+        for (int kk = 0; kk < D / 32; ++kk) {
+          uint32_t w[4], a0, a1, a2, a3;
+          ldsm_x4(chunk_addr(sK, kk), w);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            k_pairs<kE4m3>(w[2 * h], a0, a2);
+            k_pairs<kE4m3>(w[2 * h + 1], a1, a3);
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) {
+              if (kNT == 1 && h == 1) mma_f16(y, a0, a1, a2, a3, qf[nt][2 * kk + h][0], qf[nt][2 * kk + h][1]);
+              else mma_f16(x[nt], a0, a1, a2, a3, qf[nt][2 * kk + h][0], qf[nt][2 * kk + h][1]);
+            }
+          }
+        }
+        const float svx = sv > 0.f ? sv : kScaleFloor;
+        const float lsv = log2f(svx), rsv = 1.f / svx;
+        const int pr = pos0 + gq;
+        uint32_t pb[kNT][2];
+        float al[kNT][2];
+        bool grew = false;
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+          const float a[2] = {rq[nt][0] * sk, rq[nt][1] * sk};
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float d = x[nt][e];
+            if (kNT == 1) d += y[e];
+            if (!kE4m3) d *= 16777216.f;
+            w[e] = pr + (e >> 1) * 8 < lim[nt][e & 1] ? fmaf(d, a[e & 1], lsv) : -INFINITY;
+          }
+          float nm[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float mx = fmaxf(w[k], w[k + 2]);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            nm[k] = fmaxf(m[nt][k], mx);
+            al[nt][k] = exp2f(m[nt][k] - nm[k]);
+            grew |= al[nt][k] != 1.f;
+            m[nt][k] = nm[k];
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = exp2f(w[e] - nm[e & 1] + kWeightBits);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) l[nt][k] = fmaf(w[k] + w[k + 2], rsv, l[nt][k] * al[nt][k]);
+          // P^T as the B operand: rows (k) = positions, columns (n) = query rows
+          pb[nt][0] = movmatrix_trans(pack_f16(w[0], w[1]));
+          pb[nt][1] = movmatrix_trans(pack_f16(w[2], w[3]));
+        }
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt) {
+              acc[nt][mt][0] *= al[nt][0];
+              acc[nt][mt][1] *= al[nt][1];
+              acc[nt][mt][2] *= al[nt][0];
+              acc[nt][mt][3] *= al[nt][1];
+            }
+        }
+        // V bytes past the context may hold anything, a NaN of e4m3 included: zero them
+        const bool tail = pos0 + 16 > cur.len;
+        const int kp = pos0 + 2 * m4;
+        const uint32_t mlo = (kp < cur.len ? 0x0000FFFFu : 0u) | (kp + 1 < cur.len ? 0xFFFF0000u : 0u);
+        const uint32_t mhi = (kp + 8 < cur.len ? 0x0000FFFFu : 0u) | (kp + 9 < cur.len ? 0xFFFF0000u : 0u);
+#pragma unroll
+        for (int kk = 0; kk < D / 32; ++kk) {
+          uint32_t w[4], a0, a1, a2, a3;
+          ldsm_x4_trans(chunk_addr(sV, kk), w);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            v_pairs<kE4m3>(w[2 * h], a0, a1);      // positions 0-7: dims 2g, 2g + 1
+            v_pairs<kE4m3>(w[2 * h + 1], a2, a3);  // positions 8-15
+            if (kE4m3 && tail) {
+              a0 &= mlo;
+              a1 &= mlo;
+              a2 &= mhi;
+              a3 &= mhi;
+            }
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) mma_f16(acc[nt][2 * kk + h], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->empty[s]);
+      if (++s == kStages) {
+        s = 0;
+        ph ^= 1;
+      }
+
+      if (cur.i == cur.nb - 1 || j == hi - 1) {
+        // ---- the run leaves this tile: merge the four warps' states. The
+        // warps hold their accumulators in the same lane layout, so a warp
+        // folds another's state in lane by lane: warps 2, 3 into 0, 1, then
+        // warp 1 into warp 0 (a fixed order), and warp 0 stores the result.
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], o);
+        auto put = [&](float* st) {
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) {
+            float* sn = st + nt * (D / 4 + 4) * 32 + lane;
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) sn[(4 * mt + k) * 32] = acc[nt][mt][k];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              sn[(D / 4 + k) * 32] = m[nt][k];
+              sn[(D / 4 + 2 + k) * 32] = l[nt][k];
+            }
+          }
+        };
+        auto take = [&](const float* st) {
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) {
+            const float* sn = st + nt * (D / 4 + 4) * 32 + lane;
+            float f1[2], f2[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float m2 = sn[(D / 4 + k) * 32], nm = fmaxf(m[nt][k], m2);
+              f1[k] = exp2f(m[nt][k] - nm);
+              f2[k] = exp2f(m2 - nm);
+              m[nt][k] = nm;
+              l[nt][k] = l[nt][k] * f1[k] + sn[(D / 4 + 2 + k) * 32] * f2[k];
+            }
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                acc[nt][mt][k] = acc[nt][mt][k] * f1[k & 1] + sn[(4 * mt + k) * 32] * f2[k & 1];
+          }
+        };
+        float* st1 = mrg + (warp & 1) * S::kStateFloats * 32;  // first-fold slot of warp 2 / warp 3
+        float* st2 = mrg + 2 * S::kStateFloats * 32;           // second-fold slot
+        bool fail = false;
+        if (warp >= 2) {
+          fail = flushes > 0 && !warp_wait(&ctl->mrg_free, (flushes - 1) & 1);
+          if (!fail) {
+            put(st1);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->mrg_full);
+          }
+        } else {
+          fail = !warp_wait(&ctl->mrg_full, flushes & 1);
+          if (!fail) {
+            take(st1);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->mrg_free);
+            if (warp == 1) {
+              fail = flushes > 0 && !warp_wait(&ctl->mrg2_free, (flushes - 1) & 1);
+              if (!fail) {
+                put(st2);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->mrg2_full);
+              }
+            } else {
+              fail = !warp_wait(&ctl->mrg2_full, flushes & 1);
+              if (!fail) {
+                take(st2);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->mrg2_free);
+                const size_t slot = (size_t)c + cur.tile;
+                float* pm = p.part + slot * RT;
+                float* pl = p.part + (size_t)p.slots * RT + slot * RT;
+                float* po = p.part + (size_t)2 * p.slots * RT + slot * RT * D;
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt) {
+                  const int r0 = 8 * nt + 2 * m4;
+#pragma unroll
+                  for (int mt = 0; mt < D / 16; ++mt) {
+                    const int d = 16 * mt + 2 * gq;
+                    *reinterpret_cast<float2*>(po + r0 * D + d) = make_float2(acc[nt][mt][0], acc[nt][mt][2]);
+                    *reinterpret_cast<float2*>(po + (r0 + 1) * D + d) = make_float2(acc[nt][mt][1], acc[nt][mt][3]);
+                  }
+                  if (lane < 4) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                      pm[r0 + k] = m[nt][k];
+                      pl[r0 + k] = l[nt][k];
+                    }
+                  }
+                }
+              }
+            }
+          }
+        }
+        if (fail) break;
+        ++flushes;
+        reset();
+        cur = nxt;
+        if (j + 1 < hi) load_q();
+      } else {
+        cur = nxt;
+      }
+      sk = skn;
+      sv = svn;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) p.flags[c] = *abort_flag ? (int32_t)MOE_ERR_DEVICE_TIMEOUT : 0;
+}
+
+struct MergeParams {
+  const int32_t* offsets;
+  const int32_t* lens;
+  const float* part;
+  const int32_t* flags;
+  uint16_t* o;
+  int32_t* status;
+  long long slots;
+  int B, T, Hq, Hkv, D, L_max, RT, C;
+};
+
+// Thread t holds dims 4(t%16) .. +3 of the block's 64-dim slice and takes the
+// covering grid blocks c0 + t/16, c0 + t/16 + 8, ...: its loads of up to 8
+// partial states are all issued before any is used, then merged with a
+// running maximum; the 8 partial lanes are merged in a fixed order at the end.
+constexpr int kMergeLanes = 8;
+constexpr int kMergeBatch = 8;
+
+__global__ void __launch_bounds__(128) kv8_merge_kernel(const MergeParams p) {
+  // The next call's split kernel may launch now: it waits for this grid to
+  // finish before it touches the workspace.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // Everything up to the dependency wait reads only the tables, which the
+  // split kernel does not write: it overlaps that kernel's tail.
+  const int r = p.Hq / p.Hkv, RT = p.RT;
+  const int slice = blockIdx.y;
+  const int t = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq;
+  const int f = threadIdx.x & 15, pl = threadIdx.x >> 4;
+  const int d = slice * 64 + 4 * f;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ long long s_before[4], s_total[4];
+  __shared__ int s_tiles[4], s_seq, s_first_bad[4];
+  __shared__ float s_m[kMergeLanes], s_l[kMergeLanes];
+  __shared__ float4 s_o[kMergeLanes][16];
+  long long before = 0, total = 0;
+  int tiles = 0;
+  bool bad = false;
+  for (int bb = threadIdx.x; bb < p.B; bb += blockDim.x) {
+    const int lo = __ldg(p.offsets + bb), hi = __ldg(p.offsets + bb + 1), len = __ldg(p.lens + bb);
+    if (offsets_bad(lo, hi, bb, p.B, p.T) || len < 0 || len > p.L_max) {
+      bad = true;
+      continue;
+    }
+    const long long v = seq_units(hi - lo, len, r, RT);
+    total += v;
+    if (hi <= t) {
+      before += v;
+      tiles += seq_tiles(hi - lo, r, RT);
+    } else if (lo <= t) {
+      s_seq = bb;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+  }
+  if (lane == 0) {
+    s_before[warp] = before;
+    s_total[warp] = total;
+    s_tiles[warp] = tiles;
+  }
+  bad = __syncthreads_or(bad);
+  int c0 = 0, c1 = -1, slot0 = 0;
+  long long N = 1;
+  const int C = p.C;
+  if (!bad) {
+    before = s_before[0] + s_before[1] + s_before[2] + s_before[3];
+    total = s_total[0] + s_total[1] + s_total[2] + s_total[3];
+    tiles = s_tiles[0] + s_tiles[1] + s_tiles[2] + s_tiles[3];
+    const int b = s_seq, lo = __ldg(p.offsets + b), n = __ldg(p.offsets + b + 1) - lo, len = __ldg(p.lens + b);
+    const int g = h / r, row = (t - lo) * r + h % r, rt = row / RT;
+    const int nb = tile_units(n, len, r, RT, rt);
+    N = total * p.Hkv;
+    long long per = 0, start = before * p.Hkv;
+    for (int k = 0; k < seq_tiles(n, r, RT); ++k) {
+      if (k == rt) start += per;
+      per += tile_units(n, len, r, RT, k);
+    }
+    start += per * g;
+    slot0 = (tiles * p.Hkv + g * seq_tiles(n, r, RT) + rt) * RT + row % RT;
+    if (nb > 0 && len - n + (t - lo) >= 0) {
+      c0 = cta_of(start, N, C);
+      c1 = cta_of(start + nb - 1, N, C);
+    }
+  }
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    // the call's status: the outcome of the lowest-numbered grid block that failed
+    int first = 0x7fffffff;
+    for (int cc = threadIdx.x; cc < C; cc += blockDim.x)
+      if (__ldcg(p.flags + cc) != 0) first = min(first, cc);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
+    if (lane == 0) s_first_bad[warp] = first;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      first = min(min(s_first_bad[0], s_first_bad[1]), min(s_first_bad[2], s_first_bad[3]));
+      *p.status = first == 0x7fffffff ? 0 : __ldcg(p.flags + first);
+    }
+  }
+  if (bad) return;
+  uint2* out = reinterpret_cast<uint2*>(p.o + ((size_t)t * p.Hq + h) * p.D + d);
+  if (c1 < c0) {  // no visible position
+    if (pl == 0) *out = make_uint2(0u, 0u);
+    return;
+  }
+
+  const float* pm = p.part;
+  const float* pl_ = p.part + (size_t)p.slots * RT;
+  const float* po = p.part + (size_t)2 * p.slots * RT;
+  float M = kMinusBig, L = 0.f;
+  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  int failed = 0;
+  for (int base = c0 + pl; base <= c1; base += kMergeLanes * kMergeBatch) {
+    float mc[kMergeBatch], lc[kMergeBatch];
+    float4 oc[kMergeBatch];
+#pragma unroll
+    for (int u = 0; u < kMergeBatch; ++u) {
+      const int cc = base + u * kMergeLanes;
+      // with fewer units than grid blocks some runs are empty (no slot written)
+      const bool live = cc <= c1 && (long long)cc * N / C != (long long)(cc + 1) * N / C;
+      const size_t at = (size_t)(live ? cc : c0) * RT + slot0;
+      failed |= live ? __ldcg(p.flags + cc) : 0;
+      mc[u] = live ? __ldcg(pm + at) : kMinusBig;
+      lc[u] = live ? __ldcg(pl_ + at) : 0.f;
+      oc[u] = live ? __ldcg(reinterpret_cast<const float4*>(po + at * p.D + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < kMergeBatch; ++u) {
+      const float nm = fmaxf(M, mc[u]);
+      const float fo = exp2f(M - nm), fc = exp2f(mc[u] - nm);
+      O.x = O.x * fo + oc[u].x * fc;
+      O.y = O.y * fo + oc[u].y * fc;
+      O.z = O.z * fo + oc[u].z * fc;
+      O.w = O.w * fo + oc[u].w * fc;
+      L = L * fo + lc[u] * fc;
+      M = nm;
+    }
+  }
+  if (f == 0) {
+    s_m[pl] = M;
+    s_l[pl] = L;
+  }
+  s_o[pl][f] = O;
+  if (__syncthreads_or(failed)) return;  // a covering grid block gave up: o is left as it was
+  if (pl == 0) {
+    float Mt = kMinusBig;
+#pragma unroll
+    for (int w = 0; w < kMergeLanes; ++w) Mt = fmaxf(Mt, s_m[w]);
+    float Lt = 0.f;
+    float4 Ot = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kMergeLanes; ++w) {
+      const float e = exp2f(s_m[w] - Mt);
+      Lt += e * s_l[w];
+      Ot.x += e * s_o[w][f].x;
+      Ot.y += e * s_o[w][f].y;
+      Ot.z += e * s_o[w][f].z;
+      Ot.w += e * s_o[w][f].w;
+    }
+    const float inv = 1.f / Lt;
+    const __nv_bfloat162 a = __floats2bfloat162_rn(Ot.x * inv, Ot.y * inv);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(Ot.z * inv, Ot.w * inv);
+    *out = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+}
+
+// ================================================================= host ===
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      ptr = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }();
+  return fn;
+}
+
+// 3-D map of codes [pairs][L_max][D] with boxes of 64 rows by up to 128
+// bytes, swizzled by their row length; rows past L_max read as zeros.
+cudaError_t codes_map(CUtensorMap* m, const void* base, int D, int L_max, int pairs) {
+  auto fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)L_max, (cuuint64_t)pairs};
+  const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)L_max * D};
+  const cuuint32_t box[3] = {(cuuint32_t)(D < 128 ? D : 128), (cuuint32_t)kPos, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, D < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+int sm_count() {
+  static int sms[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (sms[dev] == 0 && cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    sms[dev] = 0;
+  return sms[dev];
+}
+
+// Groups of 8 rows per tile: as many as the average sequence's rows fill, up
+// to what the accumulators of D head dims leave registers for (a wider tile
+// reads the cache fewer times, a narrower one holds fewer idle rows).
+int groups(int B, int T, int r, int D) {
+  const long long rows = (long long)((T + B - 1) / B) * r;
+  const int most = D == 256 ? 2 : 4;
+  return rows <= 8 ? 1 : rows <= 16 || most == 2 ? 2 : 4;
+}
+
+// Row tiles of a call: at most one more per sequence than full tiles.
+long long max_tiles(int B, int T, int r, int Hkv, int RT) {
+  const long long rows = (long long)T * r, whole = rows / RT, part = rows < B ? rows : B;
+  return (whole + part) * Hkv;
+}
+
+template <int D, int kNT, bool kE4m3>
+cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const Params& prm, int grid, cudaStream_t stream) {
+  static SmemLimitMemo smem_memo;
+  cudaError_t e = ensure_smem(kv8_split_kernel<D, kNT, kE4m3>, Smem<D, kNT>::kBytes, &smem_memo);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Smem<D, kNT>::kBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv8_split_kernel<D, kNT, kE4m3>, tk, tv, prm);
+}
+
+template <int D, bool kE4m3>
+cudaError_t launch_groups(int nt, const CUtensorMap& tk, const CUtensorMap& tv, const Params& prm, int grid,
+                          cudaStream_t stream) {
+  if (nt == 1) return launch<D, 1, kE4m3>(tk, tv, prm, grid, stream);
+  if (nt == 2) return launch<D, 2, kE4m3>(tk, tv, prm, grid, stream);
+  if constexpr (D < 256) return launch<D, 4, kE4m3>(tk, tv, prm, grid, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace split
+
+size_t split_workspace_bytes(const moe_kv8_shape& s) {
+  using namespace split;
+  const int r = s.Hq / s.Hkv, RT = 8 * groups(s.B, s.T, r, s.D);
+  const size_t slots = (size_t)kMaxCtas + max_tiles(s.B, s.T, r, s.Hkv, RT);
+  return 256 + kMaxCtas * sizeof(int32_t) + slots * RT * (2 + (size_t)s.D) * sizeof(float);
+}
+
+moe_status launch_split(const AttnArgs& a, cudaStream_t stream) {
+  using namespace split;
+  const int sms = sm_count();
+  if (sms <= 0) return cuda_fail(cudaErrorInvalidDevice, "device query");
+  const int grid = sms < kMaxCtas ? sms : kMaxCtas;
+  const int r = a.Hq / a.Hkv, nt = groups(a.B, a.T, r, a.D), RT = 8 * nt;
+  CUtensorMap tk, tv;
+  cudaError_t e = codes_map(&tk, a.k, a.D, a.L_max, a.B * a.Hkv);
+  if (e == cudaSuccess) e = codes_map(&tv, a.v, a.D, a.L_max, a.B * a.Hkv);
+  if (e != cudaSuccess) return cuda_fail(e, "tensor map");
+
+  int32_t* status = static_cast<int32_t*>(a.workspace);
+  int32_t* flags = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(a.workspace) + 256);
+  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + 256 + kMaxCtas * sizeof(int32_t));
+  const long long slots = kMaxCtas + max_tiles(a.B, a.T, r, a.Hkv, RT);
+  const int shift = a.block == 16 ? 4 : a.block == 32 ? 5 : 6;
+  const Params prm{a.q, a.ks, a.vs, a.offsets, a.lens, part, flags, slots, a.scale_log2, a.B, a.T, a.Hq, a.Hkv,
+                   a.L_max, a.nblk, shift, a.q_stride, kTimeoutNs};
+  auto go = [&](auto fp8) {
+    constexpr bool kE4m3 = decltype(fp8)::value;
+    return a.D == 64    ? launch_groups<64, kE4m3>(nt, tk, tv, prm, grid, stream)
+           : a.D == 128 ? launch_groups<128, kE4m3>(nt, tk, tv, prm, grid, stream)
+                        : launch_groups<256, kE4m3>(nt, tk, tv, prm, grid, stream);
+  };
+  e = a.e4m3 ? go(std::true_type{}) : go(std::false_type{});
+  if (e != cudaSuccess) return cuda_fail(e, "split kernel launch");
+
+  const MergeParams mp{a.offsets, a.lens, part, flags, a.o, status, slots, a.B, a.T, a.Hq, a.Hkv, a.D, a.L_max, RT, grid};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.T * (unsigned)a.Hq, (unsigned)(a.D / 64));
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kv8_merge_kernel, mp);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "merge kernel launch");
+}
+
+}  // namespace kv8
+}  // namespace bgmoe

@@ -11,9 +11,10 @@
  *                 of a block with largest magnitude a is fp32(a / 127);
  *   MOE_KV8_E4M3  code an e4m3 number (finite, |code| <= 448); the scale is
  *                 the smallest power of two with a / scale <= 448.
- * A scale is at least 2^-60, or 0 for a block of zeros only. Bytes that a
- * write never stores have the value their bits say without special cases (0 is
- * code -128 of int8, 0x7F and 0xFF are +-480 in e4m3): no byte is a NaN.
+ * A scale is at least 2^-60, or 0 for a block of zeros only. Three bytes are
+ * never stored: 0 in int8, which would be code -128, and 0x7F and 0xFF in
+ * e4m3, which write and read take as +-480 and attention as NaN. Bytes past a
+ * context may hold anything.
  *
  * Write: sequence b's new tokens go to positions starts[b], starts[b] + 1, ...
  *   A block that held no earlier token of the sequence takes the scale of its

@@ -90,10 +90,10 @@ def test_binding_refuses_tensors_of_the_wrong_kind(moelib, monkeypatch):
     assert cache.k.shape == (1, 2, 20, 64) and cache.k_scale.shape == (1, 2, 2)
 
     def refused(text, **kw):
-        a = dict(k=k, v=v, off=off, st=st, cache=cache, sh=sh)
+        a = dict(k=k, v=v, off=off, st=st, cache=cache, sh=sh, status=None)
         a.update(kw)
         with pytest.raises(moelib.MoeError, match=text) as e:
-            moelib.kv8_write(a["sh"], a["k"], a["v"], a["off"], a["st"], a["cache"], stream=0)
+            moelib.kv8_write(a["sh"], a["k"], a["v"], a["off"], a["st"], a["cache"], a["status"], stream=0)
         assert e.value.status == moelib.MOE_ERR_INVALID_ARG
 
     refused("k_new is torch.float32", k=k.float())
@@ -103,11 +103,26 @@ def test_binding_refuses_tensors_of_the_wrong_kind(moelib, monkeypatch):
     refused("offsets is torch.int64", off=off.long())
     refused("offsets has shape", off=off[:1])
     refused("starts has shape", st=torch.zeros(2, dtype=torch.int32))
-    c = moelib.Kv8Cache(cache.k.to(torch.int8), cache.v, cache.k_scale, cache.v_scale)
-    refused("k is torch.int8", cache=c)
-    c = moelib.Kv8Cache(cache.k, cache.v[:, :, :19], cache.k_scale, cache.v_scale)
-    refused("v has shape", cache=c)
-    c = moelib.Kv8Cache(cache.k, cache.v, cache.k_scale[:, :, :1], cache.v_scale)
-    refused("k_scale has shape", cache=c)
+    refused("status is torch.int64", status=torch.zeros(1, dtype=torch.int64))
+    for text, c in [("k is torch.int8", (cache.k.to(torch.int8), cache.v, cache.k_scale, cache.v_scale)),
+                    ("v has shape", (cache.k, cache.v[:, :, :19], cache.k_scale, cache.v_scale)),
+                    ("v is torch.int8", (cache.k, cache.v.to(torch.int8), cache.k_scale, cache.v_scale)),
+                    ("k has strides", (cache.k.transpose(1, 2), cache.v, cache.k_scale, cache.v_scale)),
+                    ("k_scale is torch.float64", (cache.k, cache.v, cache.k_scale.double(), cache.v_scale)),
+                    ("v_scale has shape", (cache.k, cache.v, cache.k_scale, cache.v_scale[:, :, :1])),
+                    ("scales", (cache.k, cache.v, cache.k_scale[0], cache.v_scale))]:
+        with pytest.raises(moelib.MoeError, match=text):
+            moelib.Kv8Cache(*c)
+    c = moelib.Kv8Cache(cache.k, cache.v, cache.k_scale[:, :, :1].contiguous(), cache.v_scale[:, :, :1].contiguous())
+    refused("the cache holds", cache=c)
+    refused("the cache holds", sh=moelib.kv8_shape(B=1, T=3, Hq=4, Hkv=2, D=64, L_max=33, block=16, kv_stride=256))
+    fp8 = moelib.kv8_alloc_cache(moelib.kv8_shape(B=1, T=3, Hq=4, Hkv=2, D=64, L_max=20, block=16, format=1), "cpu")
+    refused("the cache holds", cache=fp8)
+    q, ws = torch.zeros(3, 4, 64, dtype=torch.bfloat16), torch.zeros(1 << 16, dtype=torch.uint8)
+    for text, kw in [("q is torch.float16", dict(q=q.half())), ("o has shape", dict(o=q[:1])),
+                     ("lens is torch.int64", dict(st=st.long())), ("workspace is torch.float32", dict(ws=ws.float()))]:
+        a = {**dict(q=q, o=q, st=st, ws=ws), **kw}
+        with pytest.raises(moelib.MoeError, match=text):
+            moelib.kv8_attn(sh, a["q"], cache, off, a["st"], a["o"], a["ws"], stream=0)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     refused("not on the current device")
