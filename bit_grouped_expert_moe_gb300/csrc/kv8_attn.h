@@ -24,5 +24,63 @@ struct AttnArgs {
 size_t split_workspace_bytes(const moe_kv8_shape& s);
 moe_status launch_split(const AttnArgs& a, cudaStream_t stream);
 
+// Tensor-core tile kernels (kv8_tiles.cu), for many.
+size_t tiles_workspace_bytes(const moe_kv8_shape& s);
+moe_status launch_tiles(const AttnArgs& a, cudaStream_t stream);
+
+int sm_count();  // of the current device, or 0 (kv8_attn.cu)
+
+// How the work is laid out, by both kinds: the rows of a (sequence, KV head)
+// are its r = Hq / Hkv query heads of every query token, token by token; row
+// tiles are RT consecutive rows; a tile's units are the runs of KT positions
+// that its last row sees: none, when a sequence has more queries than
+// positions.
+__device__ __forceinline__ int seq_tiles(int n, int r, int RT) { return (n * r + RT - 1) / RT; }
+__device__ __forceinline__ int tile_units(int n, int len, int r, int RT, int KT, int rt) {
+  const int last = min(n * r, (rt + 1) * RT) - 1;
+  const int see = len - n + last / r + 1;
+  return see > 0 ? (see + KT - 1) / KT : 0;
+}
+
+// sum_{i < n} floor((a i + b) / m) for a, b >= 0, by the Euclidean recursion
+// on (m, a): whole parts of a / m and b / m are summed directly, and what is
+// left counts lattice points under a line, which are counted along the other
+// axis.
+__device__ inline long long floor_sum(long long n, long long m, long long a, long long b) {
+  long long sum = 0;
+  while (true) {
+    sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const long long top = a * n + b;
+    if (top < m) return sum;
+    n = top / m;
+    b = top % m;
+    const long long t = m;
+    m = a;
+    a = t;
+  }
+}
+
+// Units of the tiles before tile k of a sequence. A whole tile's
+// ceil((len - n + floor(last / r) + 1) / KT), with last = RT (rt + 1) - 1, is
+// floor((RT rt + c) / (r KT)) with c = RT - 1 + r (len - n + KT), a line in rt.
+__device__ inline long long units_before(int n, int len, int r, int RT, int KT, int k) {
+  const int all = seq_tiles(n, r, RT);
+  long long sum = 0;
+  if (k <= 4) {
+    for (int rt = 0; rt < k; ++rt) sum += tile_units(n, len, r, RT, KT, rt);
+    return sum;
+  }
+  if (k == all) sum += tile_units(n, len, r, RT, KT, --k);  // the last tile may be ragged
+  const long long c = RT - 1 + (long long)r * ((long long)len - n + KT);
+  const long long k0 = c < 0 ? (-c + RT - 1) / RT : 0;      // tiles before see nothing
+  if (k0 < k) sum += floor_sum(k - k0, (long long)r * KT, RT, c + RT * k0);
+  return sum;
+}
+
+// The grid block whose run [c N / C, (c + 1) N / C) holds unit s.
+__device__ __forceinline__ int cta_of(long long s, long long N, int C) { return (int)(((s + 1) * C - 1) / N); }
+
 }  // namespace kv8
 }  // namespace bgmoe

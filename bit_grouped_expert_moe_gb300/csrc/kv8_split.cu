@@ -55,6 +55,7 @@ using tc::elect_one;
 using tc::mbar_arrive;
 using tc::mbar_arrive_expect_tx;
 using tc::mbar_init;
+using tc::mbar_test_wait;
 using tc::mbar_wait;
 using tc::smem_u32;
 
@@ -108,22 +109,10 @@ struct Params {
   long long timeout_ns;
 };
 
-// Row tile rt of a sequence with n query tokens over len positions: the units
-// of the positions that its last row sees.
-__device__ __forceinline__ int tile_units(int n, int len, int r, int RT, int rt) {
-  const int last = min(n * r, (rt + 1) * RT) - 1;
-  const int see = len - n + last / r + 1;
-  return see > 0 ? (see + kPos - 1) / kPos : 0;
-}
-__device__ __forceinline__ int seq_tiles(int n, int r, int RT) { return (n * r + RT - 1) / RT; }
+// Units of a whole sequence and KV head.
 __device__ __forceinline__ long long seq_units(int n, int len, int r, int RT) {
-  long long u = 0;
-  for (int rt = 0; rt < seq_tiles(n, r, RT); ++rt) u += tile_units(n, len, r, RT, rt);
-  return u;
+  return units_before(n, len, r, RT, kPos, seq_tiles(n, r, RT));
 }
-
-// The grid block whose run holds unit s: the largest c with floor(c*N/C) <= s.
-__device__ __forceinline__ int cta_of(long long s, long long N, int C) { return (int)(((s + 1) * C - 1) / N); }
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -226,7 +215,7 @@ struct Cursor {
           } while (n == 0);
         }
       }
-      nb = tile_units(n, len, r, RT, rt);
+      nb = tile_units(n, len, r, RT, kPos, rt);
     } while (nb == 0);
   }
 };
@@ -326,10 +315,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             k.g = (int)(off / per);
             off -= k.g * per;
             k.rt = 0;
-            k.nb = tile_units(k.n, k.len, r, RT, 0);
+            k.nb = tile_units(k.n, k.len, r, RT, kPos, 0);
             while (off >= k.nb) {
               off -= k.nb;
-              k.nb = tile_units(k.n, k.len, r, RT, ++k.rt);
+              k.nb = tile_units(k.n, k.len, r, RT, kPos, ++k.rt);
             }
             k.i = (int)off;
             k.tile = tiles + tincl - nt + k.g * (nt / p.Hkv) + k.rt;
@@ -356,9 +345,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   Cursor cur = s_cur;
 
   volatile int* abort_flag = &ctl->abort;
-  const uint64_t deadline = global_timer_ns() + (uint64_t)p.timeout_ns;
+  // Each wait has its own limit (a long call may run for longer than one), set
+  // only where the phase has not completed already.
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, deadline)) != 0;
+    bool ok = mbar_test_wait(bar, parity);
+    if (!ok) ok = mbar_wait(bar, parity, abort_flag, global_timer_ns() + (uint64_t)p.timeout_ns);
+    return __all_sync(0xffffffffu, ok) != 0;
   };
 
   if (warp == kConsumers) {
@@ -782,14 +774,9 @@ __global__ void __launch_bounds__(128) kv8_merge_kernel(const MergeParams p) {
     tiles = s_tiles[0] + s_tiles[1] + s_tiles[2] + s_tiles[3];
     const int b = s_seq, lo = __ldg(p.offsets + b), n = __ldg(p.offsets + b + 1) - lo, len = __ldg(p.lens + b);
     const int g = h / r, row = (t - lo) * r + h % r, rt = row / RT;
-    const int nb = tile_units(n, len, r, RT, rt);
+    const int nb = tile_units(n, len, r, RT, kPos, rt);
     N = total * p.Hkv;
-    long long per = 0, start = before * p.Hkv;
-    for (int k = 0; k < seq_tiles(n, r, RT); ++k) {
-      if (k == rt) start += per;
-      per += tile_units(n, len, r, RT, k);
-    }
-    start += per * g;
+    const long long start = before * p.Hkv + seq_units(n, len, r, RT) * g + units_before(n, len, r, RT, kPos, rt);
     slot0 = (tiles * p.Hkv + g * seq_tiles(n, r, RT) + rt) * RT + row % RT;
     if (nb > 0 && len - n + (t - lo) >= 0) {
       c0 = cta_of(start, N, C);
@@ -906,15 +893,6 @@ cudaError_t codes_map(CUtensorMap* m, const void* base, int D, int L_max, int pa
                         CU_TENSOR_MAP_INTERLEAVE_NONE, D < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
-int sm_count() {
-  static int sms[64] = {0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  if (sms[dev] == 0 && cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    sms[dev] = 0;
-  return sms[dev];
 }
 
 // Groups of 8 rows per tile: as many as the average sequence's rows fill, up

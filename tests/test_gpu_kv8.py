@@ -505,3 +505,49 @@ def test_cache_offsets_past_32_bits(moelib, cuda_dev):
     n = (start + 301 + np.arange(20))[:, None, None]
     want, o_abs = (np.stack([x[:, :301 + i].sum(1) for i in range(20)]) / n for x in (V, np.abs(V)))
     assert (np.abs(o.double().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want) + 2.1 * 2.0 ** -11 * o_abs).all()
+
+
+def _plain_attention_gpu(p, q, news, lens):
+    """fp64 attention on the GPU from the oracle's arrays, for sizes the numpy
+    oracle is too slow for. Returns o and the same sums over |V|."""
+    B, Hkv, D, L = p.dims
+    r = q.shape[1] // Hkv
+    out, out_abs = [], []
+    at = np.arange(L) // p.block
+    off = _packed(news)
+    for b, (n, ln) in enumerate(zip(news, lens)):
+        K, V = (torch.from_numpy(kv8.value_of(p.codes[i][b, :, :ln], p.scales[i][b][:, at[:ln]][:, :, None], p.fmt)).to(DEV)
+                for i in range(2))
+        x = q[off[b]:off[b + 1]].to(DEV).double().view(n, Hkv, r, D)
+        o, oa = (torch.zeros(n, Hkv, r, D, dtype=torch.float64, device=DEV) for _ in range(2))
+        for g in range(Hkv):
+            s = torch.einsum("nrd,jd->nrj", x[:, g], K[g]) * D ** -0.5
+            hide = torch.arange(ln, device=DEV) > ln - n + torch.arange(n, device=DEV)[:, None]
+            w = torch.softmax(s.masked_fill(hide[:, None], -torch.inf), -1)
+            o[:, g], oa[:, g] = w @ V[g], w @ V[g].abs()
+        out.append(o.view(n, -1, D)), out_abs.append(oa.view(n, -1, D))
+    return torch.cat(out).cpu().numpy(), torch.cat(out_abs).cpu().numpy()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("Hq,Hkv,D,block,lens,news", [
+    (16, 2, 256, 64, [2500], [2500]),             # several tiles per run, of 1 to 20 units
+    (16, 2, 256, 32, [7000, 900], [700, 900]),    # tiles longer than a run
+    (16, 4, 128, 16, [3000, 2000], [1500, 2000]),
+    (8, 2, 64, 64, [5000], [3000]),
+    (10, 2, 64, 64, [2000, 1, 800], [1600, 1, 900]),
+])
+def test_attention_of_long_prompts(moelib, cuda_dev, Hq, Hkv, D, block, lens, news, fmt):
+    """Runs of many units and tiles per block, against fp64, and the same bits
+    every time."""
+    p = Pair(moelib, len(lens), Hkv, D, max(lens), block, fmt, seed=71)
+    gen = p.fill(lens, seed=72)
+    q = (_rand(gen, sum(news), Hq, D) * 1.5).to(torch.bfloat16)
+    got = p.attend(q, news, lens)
+    seen = torch.cat([torch.arange(n) >= n - ln for n, ln in zip(news, lens)]).numpy()
+    assert (got.cpu()[~seen] == 0).all()
+    want, o_abs = _plain_attention_gpu(p, q, news, lens)
+    want[~seen], o_abs[~seen] = 0, 0
+    p.compare(got.double().cpu().numpy(), want, o_abs, q, lens)
+    for _ in range(20):
+        assert torch.equal(got, p.attend(q, news, lens))
