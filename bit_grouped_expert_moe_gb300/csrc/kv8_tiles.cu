@@ -16,24 +16,29 @@
 //   S = Q K^T  128 x 128 x D, both operands in shared memory, S in TMEM;
 //   P = 2^(x - m + 7) in fp16, written over S in TMEM;
 //   O += P V   128 x D x 128, A = P from TMEM, B = V from shared memory as it
-//              lies in the cache, position by position (an MN-major operand).
-// S is double buffered, so the product S of the next unit runs while the
+//              lies in the cache, position by position (an MN-major operand)
+// (N in halves of 128 head dims at D = 256, which share a stage's layout
+// with K.) S is double buffered, so the product S of the next unit runs while the
 // softmax of this one is computed (TMEM: D columns of O, 2 x 128 of S).
 //
-// Warp roles (512 threads):
-//   warp 0       TMEM allocation and the single MMA-issuing thread
-//   warps 4-7    softmax: thread = row (TMEM lane); at a tile's end the output
-//   warps 8-15   codes -> fp16 operands: 16-byte global loads two ring stages
-//                ahead in registers, converted and stored with the 128-byte
-//                swizzle; they also bring Q in (bf16 -> fp16, row by row)
-// The ring's stages are 128 positions x 128 head dims of K or 64 x 256 of V
-// (32 KB of fp16) and come in the order the MMAs use them: K of unit u + 1,
-// then V of unit u.
+// Warp roles (640 threads; setmaxnreg moves registers to the softmax):
+//   warps 0-7    softmax: a thread has one row (TMEM lane) and half of the unit's
+//                positions, which stay in registers from the maximum to the
+//                weights; the two halves' maxima meet in shared memory. At a
+//                tile's end, half of the output row each
+//   warps 8-11   K codes -> fp16 operands: 16-byte global loads a stage ahead in
+//                registers, converted and stored with the 128-byte swizzle
+//   warps 12-15  the same for V; both bring Q in (bf16 -> fp16, a warp per row)
+//   warp 16      TMEM allocation and the single MMA-issuing thread
+// A stage is 128 positions x 128 head dims of K or V (32 KB of fp16; 64 dims
+// at D = 64), two of each, the same layout for both. Every role is one warp's
+// chain of dependent instructions per scheduler, at 4 to 5 cycles each, so
+// what counts is how few a unit takes: few and large stages, fixed addresses,
+// one loop body per role, and the unit's work spread over the roles.
 //
-// Codes and scales as in kv8_split.cu: int8 K enters as u 2^-24 (u = code +
-// 128, an fp16 subnormal, one byte permute per pair) and the row's constant
-// 128 sum(q) comes off in the fused multiply-add that applies the scales; V is
-// exact; with x = score + log2 s_v the weights carry V's scale and
+// Codes are exact in fp16: 1024 + u (u = code + 128, by a byte permute) minus
+// 1152 for int8, the conversion instruction for e4m3. Scales as in
+// kv8_split.cu: with x = score + log2 s_v the weights carry V's scale and
 // L = sum w / s_v. The running maximum m of a row is raised only when a score
 // passes it by more than 8 (on the base-2 scale), so that O in TMEM is
 // rarely rescaled: w <= 2^15.
@@ -53,9 +58,16 @@ using namespace tc;
 
 constexpr int kRows = 128;          // rows of a tile (MMA M)
 constexpr int kKeys = 128;          // positions of a unit
-constexpr int kThreads = 512;
-constexpr int kConvWarps = 8;
-constexpr int kConvThreads = kConvWarps * 32;
+constexpr int kSoftWarps = 8;
+constexpr int kMmaWarp = 16;
+constexpr int kThreads = 20 * 32;
+// Registers per thread: 96 at launch (640 x 96 in all), then 120 for the 8
+// softmax warps, 96 for the 8 converting ones and 48 for the rest:
+// 256 x 120 + 256 x 96 + 128 x 48 = 640 x 96.
+constexpr int kSoftRegs = 120, kConvRegs = 96, kMmaRegs = 48;
+static_assert(256 * kSoftRegs + 256 * kConvRegs + 128 * kMmaRegs <= kThreads * 96, "register shares");
+constexpr int kGroupWarps = 4;      // converting warps of K, and of V
+constexpr int kGroupThreads = kGroupWarps * 32;
 constexpr int kMaxCtas = 256;       // workspace bound on the grid
 constexpr long long kTimeoutNs = 1000000000ll;
 constexpr float kMinusBig = -1e30f;
@@ -66,28 +78,29 @@ constexpr uint32_t kColS = 256;     // S buffers at columns 256 and 384, O from 
 
 template <int D>
 struct Cfg {
-  static constexpr int kKParts = D > 128 ? D / 128 : 1;  // ring stages of a unit's K ...
-  static constexpr int kKDims = D / kKParts;             // ... by head dims
-  static constexpr int kVParts = D > 128 ? D / 128 : 1;  // ... and of its V
-  static constexpr int kVKeys = kKeys / kVParts;         // ... by positions
-  static constexpr int kStageBytes = kKeys * kKDims * 2; // = kVKeys * D * 2
-  static constexpr int kStages = D == 64 ? 8 : 4;
+  static constexpr int kDims = D < 128 ? D : 128;        // head dims of a ring stage
+  static constexpr int kParts = D / kDims;               // stages of a unit's K (and V)
+  static constexpr int kStageBytes = kKeys * kDims * 2;
   static constexpr int kQBytes = kRows * D * 2;
-  static constexpr int kLoads = kStageBytes / 2 / 16 / kConvThreads;  // 16-byte loads per thread and stage
-  static constexpr int kCtlOffset = kQBytes + kStages * kStageBytes;
-  static constexpr int kBytes = kCtlOffset + 4096 + 1024;  // + alignment slack
+  static constexpr int kPieces = kDims / 16;             // 16-code pieces of a stage's row
+  static constexpr int kStep = kGroupThreads / kPieces;  // rows between a thread's pieces
+  static constexpr int kLoads = kKeys / kStep;           // pieces per thread and stage
+  static constexpr int kOutPitch = 80;                   // bytes: 32 bf16 and padding
+  static constexpr int kOutBytes = kSoftWarps * 32 * kOutPitch;
+  static constexpr int kOutOffset = kQBytes + 4 * kStageBytes;
+  static constexpr int kCtlOffset = kOutOffset + kOutBytes;
+  static constexpr int kBytes = kCtlOffset + 5120 + 1024;  // + alignment slack
+  static_assert(kStep % 8 == 0, "a thread's rows share their swizzle");
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
 struct RowConst {  // of a tile's rows, written with its Q
   float scale[kRows];   // scale * log2(e) * 2^e, e the row's power of two
-  float shift[kRows];   // -128 sum(q) 2^-24 (int8)
   int see[kRows];       // visible positions (0 for rows past the last)
 };
 
-template <int kStages>
 struct Ctl {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[2][2], empty[2][2];  // [K, V][stage]
   uint64_t q_full, q_empty;
   uint64_t rc_full[2], rc_empty[2];  // row constants of every second tile
   uint64_t s_full[2], p_full[2];
@@ -97,10 +110,12 @@ struct Ctl {
   // wait for its weights.
   uint64_t pv_done[2];
   uint64_t o_empty;       // O of a finished tile has been read
+  uint64_t mx_full[4];    // both halves of a lane quadrant have stored their maxima (or sums)
   uint64_t mma_done;
   uint32_t tmem;
   int abort;
   RowConst rc[2];
+  float mx[2][2][kRows];  // [unit parity][half]
 };
 
 struct RunInfo {  // where a block's run starts, for the merge kernel
@@ -123,8 +138,16 @@ struct Params {
   int32_t* flags;    // [C]
   float scale_log2;
   int B, T, Hq, Hkv, L_max, nblk, shift, q_stride;
+  unsigned long long rmagic;  // ceil(2^36 / r), r = Hq / Hkv
   long long timeout_ns;
 };
+
+// x / r for rows x < n r of n <= 2^24 tokens and r <= 64: with the magic off by
+// less than r / r from 2^36 / r, x (magic - 2^36 / r) < 2^30 < 2^36 / r keeps the
+// floor, and x magic < 2^24 (2^36 + r) stays in 64 bits.
+__device__ __forceinline__ int div_r(int x, unsigned long long rmagic) {
+  return (int)(((unsigned long long)(unsigned)x * rmagic) >> 36);
+}
 
 constexpr size_t slot_floats(int D) { return (size_t)kRows * (D + 2); }
 
@@ -180,23 +203,115 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return d;
 }
 
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// TMEM loads of 16 or 64 columns of this thread's lane. The registers pass
+// through the wait, so nothing can use them before it.
+__device__ __forceinline__ void tmem_ld_16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld_64(uint32_t taddr, uint32_t (&r)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr + 32));
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+  asm volatile(""
+               : "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+  asm volatile(""
+               : "+r"(r[32]), "+r"(r[33]), "+r"(r[34]), "+r"(r[35]), "+r"(r[36]), "+r"(r[37]), "+r"(r[38]),
+                 "+r"(r[39]), "+r"(r[40]), "+r"(r[41]), "+r"(r[42]), "+r"(r[43]), "+r"(r[44]), "+r"(r[45]),
+                 "+r"(r[46]), "+r"(r[47])
+               :
+               : "memory");
+  asm volatile(""
+               : "+r"(r[48]), "+r"(r[49]), "+r"(r[50]), "+r"(r[51]), "+r"(r[52]), "+r"(r[53]), "+r"(r[54]),
+                 "+r"(r[55]), "+r"(r[56]), "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]),
+                 "+r"(r[62]), "+r"(r[63])
+               :
+               : "memory");
+}
+
 __device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          taddr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st_32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D[tmem] (+)= A[tmem] B[smem]
-__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
+// The MMA warp runs its loop with all lanes, so descriptors and addresses stay
+// in uniform registers, and each instruction is predicated on the one lane that
+// issues it: a branch around the instructions would move every operand through
+// vector registers first.
+// D[tmem] (+)= A[smem] B[smem]
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate, uint32_t leader) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
-          d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] B[smem]
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate, uint32_t leader) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+// Arrives on `bar` once every MMA the leader has issued so far is done.
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t leader) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+      "r"(leader)
       : "memory");
 }
 
@@ -213,8 +328,32 @@ __device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr, uint32_t block
   return d;
 }
 
+template <int kOffset = 0>
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+  asm volatile("st.shared.v4.b32 [%0 + %5], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w), "n"(kOffset)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+// v <- 16 bytes at p + kOffset, if `on` (a predicate: no branch).
+template <int kOffset>
+__device__ __forceinline__ void ldg128_if(uint4& v, const uint8_t* p, bool on) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %5, 0;\n @q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4 + %6];\n}\n"
+      : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+      : "l"(p), "r"((int)on), "n"(kOffset));
+}
+
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -222,58 +361,58 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Four codes as four fp16 values in order. int8: K as u 2^-24, V as the code.
-template <bool kE4m3, bool kV>
+// Four codes as four fp16 values in order.
+template <bool kE4m3>
 __device__ __forceinline__ void convert4(uint32_t w, uint32_t& p01, uint32_t& p23) {
   if (kE4m3) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(p01) : "h"((uint16_t)w));
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(p23) : "h"((uint16_t)(w >> 16)));
-  } else if (kV) {
+  } else {
     const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1024 + 128
     const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
     const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
     const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
     p01 = *reinterpret_cast<const uint32_t*>(&x);
     p23 = *reinterpret_cast<const uint32_t*>(&y);
-  } else {
-    p01 = __byte_perm(w, 0u, 0x4140);
-    p23 = __byte_perm(w, 0u, 0x4342);
   }
 }
 
 template <int D, bool kE4m3>
 __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) {
   using F = Cfg<D>;
-  constexpr int kStages = F::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;                  // 64-dim slabs of 128 rows x 128 bytes
-  uint8_t* sR = smem + F::kQBytes;     // ring
-  Ctl<kStages>* ctl = reinterpret_cast<Ctl<kStages>*>(smem + F::kCtlOffset);
-  static_assert(sizeof(Ctl<kStages>) <= 4096, "control block");
+  uint8_t* sR = smem + F::kQBytes;     // stages: two of K, two of V
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + F::kCtlOffset);
+  static_assert(sizeof(Ctl) <= 5120, "control block");
   __shared__ long long s_lo, s_hi;
   __shared__ Cursor s_cur;
   __shared__ int s_bad;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // The warp's number through a shuffle, which the compiler knows to be
+  // uniform: the roles' loops then run on uniform registers, where the MMA
+  // instructions take their descriptors from.
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int C = gridDim.x, c = blockIdx.x;
   const int r = p.Hq / p.Hkv;
 
   if (threadIdx.x == 32) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&ctl->full[s], kConvWarps);
-      mbar_init(&ctl->empty[s], 1);
-    }
-    mbar_init(&ctl->q_full, kConvWarps);
+    mbar_init(&ctl->q_full, 2 * kGroupWarps);
     mbar_init(&ctl->q_empty, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl->rc_full[i], kConvWarps);
-      mbar_init(&ctl->rc_empty[i], 4);
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(&ctl->full[i][s], kGroupWarps);
+        mbar_init(&ctl->empty[i][s], 1);
+      }
+      mbar_init(&ctl->rc_full[i], 2 * kGroupWarps);
+      mbar_init(&ctl->rc_empty[i], kSoftWarps);
       mbar_init(&ctl->s_full[i], 1);
-      mbar_init(&ctl->p_full[i], 4);
+      mbar_init(&ctl->p_full[i], kSoftWarps);
       mbar_init(&ctl->pv_done[i], 1);
     }
-    mbar_init(&ctl->o_empty, 4);
+    mbar_init(&ctl->o_empty, kSoftWarps);
+    for (int i = 0; i < 4; ++i) mbar_init(&ctl->mx_full[i], 2);
     mbar_init(&ctl->mma_done, 1);
     ctl->abort = 0;
     fence_barrier_init();
@@ -369,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
     if (threadIdx.x == 0) p.flags[c] = 0;
     return;
   }
-  if (warp == 0) {
+  if (warp == kMmaWarp) {
     tmem_alloc(&ctl->tmem, kTmemCols);
     tmem_relinquish();
   }
@@ -389,101 +528,116 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
     return __all_sync(0xffffffffu, ok) != 0;
   };
 
-  if (warp == 0) {
-    // ------------------------------------------------------- MMA issuer
-    constexpr uint32_t idesc_s = idesc_f16_f32(kRows, kKeys);
-    constexpr uint32_t idesc_o = idesc_f16_f32(kRows, D) | (1u << 16);  // B is MN-major
-    const uint64_t dq = sw128_desc(smem_u32(sQ));
-    int s = 0, ph = 0, tq = 0, to = 0;  // ring place; tiles whose Q has been waited for, whose O has been started
-    auto next_stage = [&]() {
-      if (++s == kStages) {
-        s = 0;
-        ph ^= 1;
-      }
-    };
-    Cursor nxt = cur;                   // unit u + 1
-    bool fresh = true;                  // unit u + 1 starts a tile (in this run)
-    bool ok = true, ofresh = false;     // ofresh: unit u starts one
-    for (int u = -1; ok && u < U; ++u) {
-      bool nfresh = fresh;
-      if (u + 1 < U) {
-        // S of unit u + 1
-        if (nfresh) ok = warp_wait(&ctl->q_full, tq++ & 1);
-        const uint32_t d = tmem + kColS + 128 * ((u + 1) & 1);
-        const bool ends = nxt.last() || u + 2 == U;
-        for (int h = 0; ok && h < F::kKParts; ++h) {
-          if (!warp_wait(&ctl->full[s], ph)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t dk = sw128_desc(smem_u32(sR + s * F::kStageBytes));
-          if (elect_one()) {
+  if (warp >= kMmaWarp) {
+    fewer_registers<kMmaRegs>();
+    if (warp == kMmaWarp) {
+      // ----------------------------------------------------- MMA issuer
+      constexpr uint32_t idesc_s = idesc_f16_f32(kRows, kKeys);
+      constexpr uint32_t idesc_o = idesc_f16_f32(kRows, F::kDims) | (1u << 16);  // B is MN-major
+      const uint64_t dq = sw128_desc(smem_u32(sQ));
+      const uint32_t leader = elect_one();
+      const uint64_t dk = sw128_desc(smem_u32(sR));
+      const uint64_t dv = sw128_mn_desc(smem_u32(sR) + 2 * F::kStageBytes, kKeys * 128);
+      int tq = 0, to = 0;              // tiles whose Q has been waited for, whose O has been started
+      Cursor nxt = cur;
+      // both stages of a unit's K or V (D <= 128: its one), tested together
+      auto wait_stages = [&](int kv, int u) -> bool {
+        if (F::kParts == 1) return warp_wait(&ctl->full[kv][u & 1], (u >> 1) & 1);
+        const bool both = mbar_test_wait(&ctl->full[kv][0], u & 1) && mbar_test_wait(&ctl->full[kv][1], u & 1);
+        return __all_sync(0xffffffffu, both) || (warp_wait(&ctl->full[kv][0], u & 1) && warp_wait(&ctl->full[kv][1], u & 1));
+      };
+      auto score = [&](int u, bool first, bool ends) -> bool {  // S of unit u
+        if (first && !warp_wait(&ctl->q_full, tq++ & 1)) return false;
+        if (!wait_stages(0, u)) return false;
+        tc_fence_after();
+        const uint32_t d = tmem + kColS + 128 * (u & 1);
 #pragma unroll
-            for (int kk = 0; kk < F::kKDims / 16; ++kk) {
-              const uint32_t in = (kk >> 2) * (kKeys * 128 / 16) + (kk & 3) * 2;  // 64-dim slabs of 128 rows
-              mma_f16(d, dq + (uint32_t)(h * (F::kKDims / 64)) * (kRows * 128 / 16) + in, dk + in, idesc_s, (h | kk) != 0);
-            }
-            mma_commit(&ctl->empty[s]);
-            if (h == F::kKParts - 1) {
-              mma_commit(&ctl->s_full[(u + 1) & 1]);
-              if (ends) mma_commit(&ctl->q_empty);
-            }
+        for (int h = 0; h < F::kParts; ++h) {
+          const int st = F::kParts == 2 ? h : u & 1;
+#pragma unroll
+          for (int kk = 0; kk < F::kDims / 16; ++kk) {
+            const uint32_t in = (kk >> 2) * (kKeys * 128 / 16) + (kk & 3) * 2;  // 64-dim slabs of 128 rows
+            mma_ss(d, dq + h * (F::kDims / 64) * (kRows * 128 / 16) + in, dk + st * (F::kStageBytes / 16) + in, idesc_s,
+                   kk > 0 || h > 0, leader);
           }
-          __syncwarp();
-          next_stage();
+          commit(&ctl->empty[0][st], leader);
         }
-        fresh = nxt.last();
-        if (u + 2 < U) nxt.advance(p, r);
-      }
-      if (ok && u >= 0) {
-        // O of unit u
-        ok = warp_wait(&ctl->p_full[u & 1], (u >> 1) & 1);
-        if (ok && ofresh) {
-          if (to > 0) ok = warp_wait(&ctl->o_empty, (to - 1) & 1);
+        commit(&ctl->s_full[u & 1], leader);
+        if (ends) commit(&ctl->q_empty, leader);
+        return true;
+      };
+      auto output = [&](int u, bool first) -> bool {  // O of unit u
+        if (!warp_wait(&ctl->p_full[u & 1], (u >> 1) & 1)) return false;
+        if (first) {
+          if (to > 0 && !warp_wait(&ctl->o_empty, (to - 1) & 1)) return false;
           ++to;
         }
+        if (!wait_stages(1, u)) return false;
+        tc_fence_after();
         const uint32_t a = tmem + kColS + 128 * (u & 1);
-        for (int h = 0; ok && h < F::kVParts; ++h) {
-          if (!warp_wait(&ctl->full[s], ph)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t dv = sw128_mn_desc(smem_u32(sR + s * F::kStageBytes), F::kVKeys * 128);
-          if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < F::kVKeys / 16; ++kk)
-              mma_f16_ta(tmem, a + (h * F::kVKeys + kk * 16) / 2, dv + kk * (16 * 128 / 16), idesc_o,
-                         !(ofresh && h == 0 && kk == 0));
-            mma_commit(&ctl->empty[s]);
-            if (h == F::kVParts - 1) mma_commit(&ctl->pv_done[u & 1]);
-          }
-          __syncwarp();
-          next_stage();
+        for (int h = 0; h < F::kParts; ++h) {
+          const int st = F::kParts == 2 ? h : u & 1;
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            mma_ts(tmem + h * F::kDims, a + kk * 8, dv + st * (F::kStageBytes / 16) + kk * (16 * 128 / 16), idesc_o,
+                   kk > 0 ? 1u : (uint32_t)!first, leader);
+          commit(&ctl->empty[1][st], leader);
+        }
+        commit(&ctl->pv_done[u & 1], leader);
+        return true;
+      };
+      // S of unit u + 1 goes ahead of O of unit u, whose weights the softmax
+      // makes meanwhile; not where u + 1 starts a tile, whose Q may be long in
+      // coming. (One call site each: the code stays short.)
+      bool ok = true, sfirst = true, ofirst = true;  // unit su, ou starts a tile (in this run)
+      int su = 0, ou = 0;              // units scored and put out so far
+#pragma unroll 1
+      while (ok && ou < U) {
+        if (su < U && su <= ou + 1 && (su == ou || !sfirst)) {
+          const bool last = nxt.last();
+          ok = score(su, sfirst, last || su + 1 == U);
+          sfirst = last;
+          if (++su < U) nxt.advance(p, r);
+        } else {
+          ok = output(ou, ofirst);
+          // with su == ou + 1 the next unit's sfirst is this one's end; with
+          // su == ou + 2 unit ou + 1 is of the same tile
+          ++ou;
+          ofirst = su == ou && sfirst;
         }
       }
-      ofresh = nfresh;
+      commit(&ctl->mma_done, leader);
     }
-    if (elect_one()) mma_commit(&ctl->mma_done);  // arrives once every issued MMA has finished
-    __syncwarp();
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp < kSoftWarps) {
     // --------------------------------------------------------- softmax
-    const int row = (warp & 3) * 32 + lane;
-    const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    float m = kMinusBig, l = 0.f, rs = 0.f, sh = 0.f;
-    int see = 0, tile = 0;
+    more_registers<kSoftRegs>();
+    const int quad = warp & 3, half = warp >> 2;
+    const int row = quad * 32 + lane;
+    const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
+    float m = kMinusBig, l = 0.f, rs = 0.f;
+    int see = 0, tile = 0, met = 0;
     bool fresh = true, mid = cur.i > 0;  // the tile's first unit in this run; the tile began in an earlier run
-    bool ok = true;
-    // scales of a unit's cache blocks: lane k holds those of the k-th 16 positions
+    // this thread's value and its partner's, once both are there
+    auto meet = [&](float v, float& other) -> bool {
+      ctl->mx[met & 1][half][row] = v;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->mx_full[quad]);
+      if (!warp_wait(&ctl->mx_full[quad], met & 1)) return false;
+      other = ctl->mx[met & 1][half ^ 1][row];
+      ++met;
+      return true;
+    };
+    // scales of this half of a unit: lane k holds those of its k-th 16 positions
     auto load_scales = [&](const Cursor& k, float& sk, float& sv) {
-      const int pos = min(k.i * kKeys + 16 * (lane & 7), k.len - 1);
+      const int pos = min(k.i * kKeys + 64 * half + 16 * (lane & 3), k.len - 1);
       const size_t at = (size_t)(k.b * p.Hkv + k.g) * p.nblk + (pos >> p.shift);
       sk = __ldg(p.ks + at);
       sv = __ldg(p.vs + at);
     };
     float sk, sv;
     load_scales(cur, sk, sv);
+#pragma unroll 1
     for (int u = 0; u < U; ++u) {
       Cursor nxt = cur;
       float skn = 0.f, svn = 0.f;
@@ -492,109 +646,83 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
         load_scales(nxt, skn, svn);
       }
       if (fresh) {
-        if (!warp_wait(&ctl->rc_full[tile & 1], (tile >> 1) & 1)) {
-          ok = false;
-          break;
-        }
+        if (!warp_wait(&ctl->rc_full[tile & 1], (tile >> 1) & 1)) break;
         const RowConst& rc = ctl->rc[tile & 1];
-        rs = rc.scale[row] * (kE4m3 ? 1.f : 16777216.f);
-        sh = rc.shift[row];
+        rs = rc.scale[row];
         see = rc.see[row];
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->rc_empty[tile & 1]);
         m = kMinusBig;
         l = 0.f;
       }
-      if (!warp_wait(&ctl->s_full[u & 1], (u >> 1) & 1)) {
-        ok = false;
-        break;
-      }
+      const float svx = sv > 0.f ? sv : kScaleFloor;
+      const float lsv = __log2f(svx), rsv = __fdividef(1.f, svx);
+      if (!warp_wait(&ctl->s_full[u & 1], (u >> 1) & 1)) break;
       tc_fence_after();
       const uint32_t ts = lane_addr + kColS + 128 * (u & 1);
-      const float svx = sv > 0.f ? sv : kScaleFloor;
-      const float lsv = log2f(svx), rsv = 1.f / svx;
-      const int left = see - cur.i * kKeys;  // visible positions from the unit's first on
-      const bool masked = __any_sync(0xffffffffu, left < kKeys);
-      // the unit's maximum
-      float mx = -INFINITY;
+      uint32_t x[64];
+      tmem_ld_64(ts + 64 * half, x);
+      // Scores on the base-2 scale, with V's scale: a x + b, a and b per 16
+      // positions. a is kept above zero, so hidden positions (x = -inf) stay
+      // hidden and a group's largest x gives its largest score.
+      const int left = see - cur.i * kKeys - 64 * half;  // visible positions from this half's first on
+      if (__any_sync(0xffffffffu, left < 64)) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float x[32];
-        tmem_ld_32(ts + 32 * j, x);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float a = rs * __shfl_sync(0xffffffffu, sk, 2 * j + h);
-          const float b = fmaf(a, sh, __shfl_sync(0xffffffffu, lsv, 2 * j + h));
-          const uint64_t a2 = pack2(a, a), b2 = pack2(b, b);
-          if (!masked) {
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              const float2 y = unpack2(fma2(pack2(x[16 * h + e], x[16 * h + e + 1]), a2, b2));
-              mx = fmaxf(mx, fmaxf(y.x, y.y));
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (32 * j + 16 * h + e < left) mx = fmaxf(mx, fmaf(x[16 * h + e], a, b));
-          }
-        }
+        for (int e = 0; e < 64; ++e)
+          if (e >= left) x[e] = 0xFF800000u;  // -inf
       }
-      const bool raise = mx > m + kSlack;
+      float mx = -INFINITY;
+      float a[4], b[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        a[h] = fmaxf(rs * __shfl_sync(0xffffffffu, sk, h), 1e-35f);
+        b[h] = __shfl_sync(0xffffffffu, lsv, h);
+        float g = fmaxf(__uint_as_float(x[16 * h]), __uint_as_float(x[16 * h + 1]));
+#pragma unroll
+        for (int e = 16 * h + 2; e < 16 * h + 16; e += 2)
+          g = fmaxf(g, fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+        mx = fmaxf(mx, fmaf(g, a[h], b[h]));
+      }
+      float other;
+      if (!meet(mx, other)) break;
+      mx = fmaxf(mx, other);
       if (fresh) {
         m = fmaxf(mx, kMinusBig);
-      } else if (__any_sync(0xffffffffu, raise)) {
+      } else if (__any_sync(0xffffffffu, mx > m + kSlack)) {
         // O and L to the new maximum, once the products of the last unit are in
-        const float nm = raise ? mx : m, f = ex2(m - nm);
+        const float nm = mx > m + kSlack ? mx : m, f = ex2(m - nm);
         m = nm;
         l *= f;
-        if (!warp_wait(&ctl->pv_done[(u - 1) & 1], ((u - 1) >> 1) & 1)) {
-          ok = false;
-          break;
-        }
+        if (!warp_wait(&ctl->pv_done[(u - 1) & 1], ((u - 1) >> 1) & 1)) break;
         tc_fence_after();
-        for (int j = 0; j < D / 32; ++j) {
-          float x[32];
-          tmem_ld_32(lane_addr + 32 * j, x);
+#pragma unroll 1
+        for (int j = half * (D / 2); j < (half + 1) * (D / 2); j += 16) {
+          uint32_t w[16];
+          tmem_ld_16(lane_addr + j, w);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t w[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(x[16 * h + e] * f);
-            tmem_st_16(lane_addr + 32 * j + 16 * h, w);
-          }
+          for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
+          tmem_st_16(lane_addr + j, w);
         }
       }
-      // weights, over S
+      // weights, over S (both halves have read it)
       const float top = kWeightBits - m;
+      uint32_t w[32];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float x[32];
-        tmem_ld_32(ts + 32 * j, x);
-        uint32_t w[16];
+      for (int h = 0; h < 4; ++h) {
+        uint64_t s2 = 0ull;
+        const float bt = b[h] + top;
+        const uint64_t a2 = pack2(a[h], a[h]), b2 = pack2(bt, bt);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float a = rs * __shfl_sync(0xffffffffu, sk, 2 * j + h);
-          const float b = fmaf(a, sh, __shfl_sync(0xffffffffu, lsv, 2 * j + h)) + top;
-          const float rv = __shfl_sync(0xffffffffu, rsv, 2 * j + h);
-          const uint64_t a2 = pack2(a, a), b2 = pack2(b, b);
-          float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            float2 y = unpack2(fma2(pack2(x[16 * h + e], x[16 * h + e + 1]), a2, b2));
-            if (masked) {
-              y.x = 32 * j + 16 * h + e < left ? y.x : -INFINITY;
-              y.y = 32 * j + 16 * h + e + 1 < left ? y.y : -INFINITY;
-            }
-            y.x = ex2(y.x);
-            y.y = ex2(y.y);
-            s0 += y.x;
-            s1 += y.y;
-            w[8 * h + e / 2] = pack_f16(y.x, y.y);
-          }
-          l = fmaf(s0 + s1, rv, l);
+        for (int e = 16 * h; e < 16 * h + 16; e += 2) {
+          const float2 y = unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), a2, b2));
+          const float w0 = ex2(y.x), w1 = ex2(y.y);
+          s2 = add2(s2, pack2(w0, w1));
+          w[e / 2] = pack_f16(w0, w1);
         }
-        tmem_st_16(ts + 16 * j, w);
+        const float2 s = unpack2(s2);
+        l = fmaf(s.x + s.y, __shfl_sync(0xffffffffu, rsv, h), l);
       }
+      tmem_st_32(ts + 32 * half, w);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -603,43 +731,59 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
       fresh = cur.last();
       if (cur.last() || u + 1 == U) {
         // ---- the run leaves this tile: its rows' outputs, or the partial state
-        if (!warp_wait(&ctl->pv_done[u & 1], (u >> 1) & 1)) {
-          ok = false;
-          break;
-        }
+        if (!meet(l, other)) break;
+        l += other;
+        if (!warp_wait(&ctl->pv_done[u & 1], (u >> 1) & 1)) break;
         tc_fence_after();
-        const int rho = cur.rt * kRows + row;
+        const int d0 = half * (D / 2);
         if (!mid && cur.last()) {
           const float inv = see > 0 ? 1.f / l : 0.f;
-          const bool live = rho < cur.n * r && see > 0;
-          uint16_t* orow = p.o + ((size_t)(cur.lo + (live ? rho / r : 0)) * p.Hq + (size_t)cur.g * r +
-                                  (live ? rho % r : 0)) * D;
-          for (int j = 0; j < D / 32; ++j) {
-            float x[32];
-            tmem_ld_32(lane_addr + 32 * j, x);
-            if (live) {
+          // 32 rows by 32 dims at a time through shared memory: 4 lanes write
+          // a row's 64 bytes, 8 rows at once
+          const uint32_t stage = smem_u32(smem + F::kOutOffset) + warp * (32 * F::kOutPitch);
+          uint16_t* orow[4];
 #pragma unroll
-              for (int e = 0; e < 32; e += 8) {
-                uint32_t w[4];
+          for (int k = 0; k < 4; ++k) {
+            const int rk = cur.rt * kRows + quad * 32 + 8 * k + (lane >> 2), tok = div_r(rk, p.rmagic);
+            const bool live = rk < cur.n * r && cur.len - cur.n + tok >= 0;
+            orow[k] = live ? p.o + ((size_t)(cur.lo + tok) * p.Hq + (size_t)cur.g * r + rk - tok * r) * D + 8 * (lane & 3)
+                           : nullptr;
+          }
+#pragma unroll 1
+          for (int j = d0; j < d0 + D / 2; j += 32) {
+            float v[32];
+            tmem_ld_32(lane_addr + j, v);
+            __syncwarp();
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const __nv_bfloat162 y = __floats2bfloat162_rn(x[e + 2 * k] * inv, x[e + 2 * k + 1] * inv);
-                  w[k] = *reinterpret_cast<const uint32_t*>(&y);
-                }
-                *reinterpret_cast<uint4*>(orow + 32 * j + e) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int e = 0; e < 32; e += 8) {
+              uint32_t z[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const __nv_bfloat162 y = __floats2bfloat162_rn(v[e + 2 * k] * inv, v[e + 2 * k + 1] * inv);
+                z[k] = *reinterpret_cast<const uint32_t*>(&y);
               }
+              sts128(stage + lane * F::kOutPitch + 2 * e, z[0], z[1], z[2], z[3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint4 y = lds128(stage + (8 * k + (lane >> 2)) * F::kOutPitch + 16 * (lane & 3));
+              if (orow[k]) *reinterpret_cast<uint4*>(orow[k] + j) = y;
             }
           }
         } else {
           float* part = p.part + (size_t)(2 * c + (mid ? 0 : 1)) * slot_floats(D) + row;
-          for (int j = 0; j < D / 32; ++j) {
-            float x[32];
-            tmem_ld_32(lane_addr + 32 * j, x);
+#pragma unroll 1
+          for (int j = d0; j < d0 + D / 2; j += 32) {
+            float v[32];
+            tmem_ld_32(lane_addr + j, v);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) part[(size_t)(32 * j + e) * kRows] = x[e];
+            for (int e = 0; e < 32; ++e) part[(size_t)(j + e) * kRows] = v[e];
           }
-          part[(size_t)D * kRows] = m;
-          part[(size_t)(D + 1) * kRows] = l;
+          if (half == 0) {
+            part[(size_t)D * kRows] = m;
+            part[(size_t)(D + 1) * kRows] = l;
+          }
         }
         tc_fence_before();
         __syncwarp();
@@ -652,119 +796,101 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
       sk = skn;
       sv = svn;
     }
-    (void)ok;
-  } else if (warp >= 8) {
+  } else {
     // ---------------------------------------------- codes -> fp16 operands
-    const int t = threadIdx.x - 256;
-    constexpr int kKPieces = F::kKDims / 16, kVPieces = D / 16;  // 16-code pieces of a stage's row
-    const int kpiece = t % kKPieces, kkey = t / kKPieces, vpiece = t % kVPieces, vkey = t / kVPieces;
-    // Of the 8 lanes that store together, the upper 4 (the next 64-dim slab,
-    // whose rows lie on the same banks) store their second chunk first.
-    const int flip = D >= 128 ? (lane >> 2) & 1 : 0;
-    struct Ref {  // a unit's codes
-      size_t at;  // of its first position's first code
-      int keys;   // positions that exist
-    };
-    auto ref = [&](const Cursor& k) -> Ref {
-      return Ref{((size_t)(k.b * p.Hkv + k.g) * p.L_max + (size_t)k.i * kKeys) * D, k.len - k.i * kKeys};
-    };
-    auto load_k = [&](const Ref& f, int h, uint4 (&w)[F::kLoads]) {
-#pragma unroll
-      for (int i = 0; i < F::kLoads; ++i) {
-        const int key = kkey + i * (kConvThreads / kKPieces);
-        w[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (key < f.keys) w[i] = ldg_nc_v4(p.codes[0] + f.at + (size_t)key * D + h * F::kKDims + kpiece * 16);
+    fewer_registers<kConvRegs>();
+    const int kv = (warp - kSoftWarps) / kGroupWarps;            // 0: K (and Q), 1: V
+    const int t = threadIdx.x - 32 * (kSoftWarps + kv * kGroupWarps);
+    // This thread's pieces of a stage: head dims 16 piece .. + 15 of rows key,
+    // key + kStep, ... Of the 8 lanes that store together, the upper 4 (the
+    // next 64-dim slab, whose rows lie on the same banks) store their second
+    // 16-byte chunk first.
+    const int piece = t % F::kPieces, key = t / F::kPieces;
+    const bool flip = D >= 128 && (lane & 4);
+    const uint32_t stage0 = smem_u32(sR) + kv * (2 * F::kStageBytes) + (uint32_t)(piece >> 2) * (kKeys * 128) + key * 128;
+    const uint32_t ch = (uint32_t)(piece & 3) * 2, sw = key & 7;
+    const uint32_t b0 = stage0 + (((ch + (flip ? 1 : 0)) ^ sw) << 4), b1 = stage0 + (((ch + (flip ? 0 : 1)) ^ sw) << 4);
+
+    // The place of the loads, one stage ahead of the stores.
+    Cursor cn = cur;
+    const uint8_t* src;  // this thread's first piece of the unit
+    int keys;            // positions of the unit from the thread's first on
+    bool whole;          // all of the unit's positions exist
+    auto each_piece = [&](auto f) {
+      f(std::integral_constant<int, 0>{});
+      f(std::integral_constant<int, 1>{});
+      f(std::integral_constant<int, 2>{});
+      f(std::integral_constant<int, 3>{});
+      if constexpr (F::kLoads == 8) {
+        f(std::integral_constant<int, 4>{});
+        f(std::integral_constant<int, 5>{});
+        f(std::integral_constant<int, 6>{});
+        f(std::integral_constant<int, 7>{});
       }
     };
-    auto load_v = [&](const Ref& f, int h, uint4 (&w)[F::kLoads]) {
-#pragma unroll
-      for (int i = 0; i < F::kLoads; ++i) {
-        const int key = h * F::kVKeys + vkey + i * (kConvThreads / kVPieces);
-        w[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (key < f.keys) w[i] = ldg_nc_v4(p.codes[1] + f.at + (size_t)key * D + vpiece * 16);
-        else if (!kE4m3) w[i] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-      }
+    auto place = [&]() {
+      src = p.codes[kv] + ((size_t)(cn.b * p.Hkv + cn.g) * p.L_max + (size_t)cn.i * kKeys + key) * D + piece * 16;
+      keys = cn.len - cn.i * kKeys - key;
+      whole = keys + key >= kKeys;
     };
-    auto store_piece = [&](uint32_t base, int rows, int key, int piece, const uint4& w, auto is_v) {
-      constexpr bool kV = decltype(is_v)::value;
-      uint32_t x[8];
-      convert4<kE4m3, kV>(w.x, x[0], x[1]);
-      convert4<kE4m3, kV>(w.y, x[2], x[3]);
-      convert4<kE4m3, kV>(w.z, x[4], x[5]);
-      convert4<kE4m3, kV>(w.w, x[6], x[7]);
-      const uint32_t rowa = base + (uint32_t)(piece >> 2) * (rows * 128) + key * 128;
-      const uint32_t ch = (uint32_t)(piece & 3) * 2, sw = key & 7;
-      const uint32_t a0 = rowa + (((ch + flip) ^ sw) << 4), a1 = rowa + (((ch + (flip ^ 1)) ^ sw) << 4);
-      if (flip) {
-        sts128(a0, x[4], x[5], x[6], x[7]);
-        sts128(a1, x[0], x[1], x[2], x[3]);
-      } else {
-        sts128(a0, x[0], x[1], x[2], x[3]);
-        sts128(a1, x[4], x[5], x[6], x[7]);
-      }
+    place();
+    const uint32_t none = kE4m3 ? 0u : 0x80808080u;  // positions past the context: code 0
+    uint4 w[F::kLoads];
+    auto load1 = [&](auto index, int h) {
+      constexpr int i = decltype(index)::value;
+      if (!whole) w[i] = make_uint4(none, none, none, none);
+      ldg128_if<i * F::kStep * D>(w[i], src + h * F::kDims, i * F::kStep < keys);
     };
-    int s = 0, ph = 0, filled = 0;
-    auto acquire = [&]() -> bool {
-      if (filled >= kStages && !warp_wait(&ctl->empty[s], ph ^ 1)) return false;
-      tc_fence_after();
-      return true;
-    };
-    auto publish = [&]() {
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->full[s]);
-      ++filled;
-      if (++s == kStages) {
-        s = 0;
-        ph ^= 1;
-      }
-    };
-    // Q of the tile at a cursor: two threads per row
+    each_piece([&](auto index) { load1(index, 0); });
+
+    // Q of the tile at a cursor: D / 8 lanes per row, 16 bytes each
     int tile = 0;
     auto load_q = [&](const Cursor& k) -> bool {
       if (tile > 0 && !warp_wait(&ctl->q_empty, (tile - 1) & 1)) return false;
       if (tile > 1 && !warp_wait(&ctl->rc_empty[tile & 1], ((tile >> 1) - 1) & 1)) return false;
       tc_fence_after();
-      const int row = t >> 1, half = t & 1;
-      const int rho = k.rt * kRows + row;
-      const bool live = rho < k.n * r;
-      const uint16_t* src = p.q + (size_t)(k.lo + (live ? rho / r : 0)) * p.q_stride +
-                            (size_t)(k.g * r + (live ? rho % r : 0)) * D + half * (D / 2);
-      uint32_t mx = 0u;
-#pragma unroll 4
-      for (int i = 0; i < D / 16; ++i) {
-        const uint4 w = live ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0u, 0u, 0u, 0u);
-        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
-                                   __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
-      }
-      mx = max(mx & 0xFFFFu, mx >> 16);
-      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      const int e = min((int)(mx >> 7), 253);
-      const float down = __uint_as_float((uint32_t)(254 - e) << 23);  // 2^-(e - 127)
-      float sum = 0.f;
-#pragma unroll 4
-      for (int i = 0; i < D / 16; ++i) {
-        const uint4 w = live ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-        uint32_t x[4];
+      constexpr int kLanes = D / 8, kAtOnce = 256 / D, kBatch = 4;  // rows of a load; loads in flight
+      const int ln = lane % kLanes, r0 = (warp - kSoftWarps) * (kRows / (2 * kGroupWarps));
+      RowConst& rc = ctl->rc[tile & 1];
+#pragma unroll 1
+      for (int base = r0; base < r0 + kRows / (2 * kGroupWarps); base += kBatch * kAtOnce) {
+        uint4 v[kBatch];
+        int tok[kBatch];  // the row's token, or n past the last
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[j] = pack_f16(bf16_bits_to_f32(in[j] & 0xFFFFu) * down, bf16_bits_to_f32(in[j] >> 16) * down);
-          if (!kE4m3) {
-            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
-            sum += y.x + y.y;
+        for (int i = 0; i < kBatch; ++i) {
+          const int rho = k.rt * kRows + base + i * kAtOnce + lane / kLanes;
+          tok[i] = rho < k.n * r ? div_r(rho, p.rmagic) : k.n;
+          v[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (tok[i] < k.n)
+            v[i] = __ldg(reinterpret_cast<const uint4*>(p.q + (size_t)(k.lo + tok[i]) * p.q_stride +
+                                                        (size_t)(k.g * r + rho - tok[i] * r) * D) + ln);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int row = base + i * kAtOnce + lane / kLanes;
+          uint32_t mx = __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu),
+                                 __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
+          mx = max(mx & 0xFFFFu, mx >> 16);
+          if (kLanes == 32) {
+            mx = __reduce_max_sync(0xffffffffu, mx);
+          } else {
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          }
+          const int e = min((int)(mx >> 7), 253);
+          const float down = __uint_as_float((uint32_t)(254 - e) << 23);  // 2^-(e - 127)
+          const uint32_t in[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          uint32_t x[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            x[j] = pack_f16(bf16_bits_to_f32(in[j] & 0xFFFFu) * down, bf16_bits_to_f32(in[j] >> 16) * down);
+          sts128(smem_u32(sQ) + (ln >> 3) * (kRows * 128) + row * 128 + (((ln & 7) ^ (row & 7)) << 4), x[0], x[1], x[2],
+                 x[3]);
+          if (ln == 0) {
+            rc.scale[row] = ldexpf(p.scale_log2, e - 127);
+            rc.see[row] = tok[i] < k.n ? max(k.len - k.n + tok[i] + 1, 0) : 0;
           }
         }
-        const int d = half * (D / 2) + 8 * i;
-        sts128(smem_u32(sQ) + (d >> 6) * (kRows * 128) + row * 128 + ((((d >> 3) & 7) ^ (row & 7)) << 4), x[0], x[1],
-               x[2], x[3]);
-      }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      if (half == 0) {
-        RowConst& rc = ctl->rc[tile & 1];
-        rc.scale[row] = ldexpf(p.scale_log2, e - 127);
-        rc.shift[row] = kE4m3 ? 0.f : sum * -7.62939453125e-06f;  // -128 2^-24
-        rc.see[row] = live ? max(k.len - k.n + rho / r + 1, 0) : 0;
       }
       fence_proxy_async();
       __syncwarp();
@@ -776,83 +902,54 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
       return true;
     };
 
-    // Loads run two stages ahead of the stores. With two parts each of K and
-    // V, buffer h holds part h: K of unit u + 1, then V of u, then K of u + 2;
-    // with one part each, buffer 0 holds K and buffer 1 V.
-    uint4 w0[F::kLoads], w1[F::kLoads];
-    Cursor ck = cur;               // unit u + 1 (its Q)
-    Cursor cn = cur;               // unit u + 2
-    Ref f0 = ref(cur), f1 = f0;    // units u + 1 and u + 2 (f0 becomes unit u's when V comes)
-    constexpr bool kTwo = F::kKParts == 2;
-    load_k(f0, 0, w0);
-    if (kTwo) load_k(f0, 1, w1);
-    Ref fu = f0;                   // unit u
     bool ok = true, fresh = true;
-    for (int u = -1; ok && u < U; ++u) {
-      // here f0: unit u + 1, fu: unit u
-      if (u + 2 < U) {
-        cn.advance(p, r);
-        f1 = ref(cn);
+#pragma unroll 1
+    for (int u = 0; ok && u < U; ++u) {
+      if (fresh && !load_q(cn)) break;
+      fresh = cn.last();
+#pragma unroll
+      for (int h = 0; h < F::kParts; ++h) {
+        const int j = u * F::kParts + h, st = F::kParts == 2 ? h : j & 1;
+        ok = ok && (j < 2 || warp_wait(&ctl->empty[kv][st], ((j >> 1) - 1) & 1));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t to = st * F::kStageBytes;
+        bool more = true;                    // a next stage to load
+        if (h == F::kParts - 1) {
+          more = u + 1 < U;
+          if (more) {
+            if (cn.last()) {
+              cn.advance(p, r);
+              place();
+            } else {
+              ++cn.i;
+              src += kKeys * D;
+              keys -= kKeys;
+              whole = keys + key >= kKeys;
+            }
+          }
+        }
+        auto piece_of = [&](auto index) {
+          constexpr int i = decltype(index)::value;
+          uint32_t x[8];
+          convert4<kE4m3>(flip ? w[i].z : w[i].x, x[0], x[1]);
+          convert4<kE4m3>(flip ? w[i].w : w[i].y, x[2], x[3]);
+          convert4<kE4m3>(flip ? w[i].x : w[i].z, x[4], x[5]);
+          convert4<kE4m3>(flip ? w[i].y : w[i].w, x[6], x[7]);
+          sts128<i * F::kStep * 128>(b0 + to, x[0], x[1], x[2], x[3]);
+          sts128<i * F::kStep * 128>(b1 + to, x[4], x[5], x[6], x[7]);
+          if (more) load1(index, h == F::kParts - 1 ? 0 : h + 1);
+        };
+        each_piece(piece_of);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->full[kv][st]);
       }
-      if (u + 1 < U) {
-        if (fresh && !load_q(ck)) break;
-        fresh = ck.last();
-        if (!acquire()) break;
-#pragma unroll
-        for (int i = 0; i < F::kLoads; ++i)
-          store_piece(smem_u32(sR + s * F::kStageBytes), kKeys, kkey + i * (kConvThreads / kKPieces), kpiece, w0[i],
-                      std::false_type{});
-        publish();
-      }
-      if (kTwo) {
-        if (u >= 0) load_v(fu, 0, w0);
-        if (u + 1 < U) {
-          if (!acquire()) break;
-#pragma unroll
-          for (int i = 0; i < F::kLoads; ++i)
-            store_piece(smem_u32(sR + s * F::kStageBytes), kKeys, kkey + i * (kConvThreads / kKPieces), kpiece, w1[i],
-                        std::false_type{});
-          publish();
-        }
-        if (u >= 0) {
-          load_v(fu, 1, w1);
-          if (!acquire()) break;
-#pragma unroll
-          for (int i = 0; i < F::kLoads; ++i)
-            store_piece(smem_u32(sR + s * F::kStageBytes), F::kVKeys, vkey + i * (kConvThreads / kVPieces), vpiece,
-                        w0[i], std::true_type{});
-          publish();
-        }
-        if (u + 2 < U) load_k(f1, 0, w0);
-        if (u >= 0) {
-          if (!acquire()) break;
-#pragma unroll
-          for (int i = 0; i < F::kLoads; ++i)
-            store_piece(smem_u32(sR + s * F::kStageBytes), F::kVKeys, vkey + i * (kConvThreads / kVPieces), vpiece,
-                        w1[i], std::true_type{});
-          publish();
-        }
-        if (u + 2 < U) load_k(f1, 1, w1);
-      } else {
-        if (u + 2 < U) load_k(f1, 0, w0);
-        if (u >= 0) {
-          if (!acquire()) break;
-#pragma unroll
-          for (int i = 0; i < F::kLoads; ++i)
-            store_piece(smem_u32(sR + s * F::kStageBytes), F::kVKeys, vkey + i * (kConvThreads / kVPieces), vpiece,
-                        w1[i], std::true_type{});
-          publish();
-        }
-        if (u + 1 < U) load_v(f0, 0, w1);
-      }
-      fu = f0;
-      f0 = f1;
-      ck = cn;
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == kMmaWarp) {
     int dummy = 0;  // no MMA may still be running when TMEM is freed
     mbar_wait(&ctl->mma_done, 0, &dummy, global_timer_ns() + 100000000ull);
     tc_fence_after();
@@ -957,7 +1054,8 @@ moe_status launch_tiles(const AttnArgs& a, cudaStream_t stream) {
   float* part = reinterpret_cast<float*>(ws + 256 + kMaxCtas * (sizeof(int32_t) + sizeof(RunInfo)));
   const int shift = a.block == 16 ? 4 : a.block == 32 ? 5 : 6;
   const Params prm{a.q, {a.k, a.v}, a.ks, a.vs, a.offsets, a.lens, a.o, part, info, flags, a.scale_log2,
-                   a.B, a.T, a.Hq, a.Hkv, a.L_max, a.nblk, shift, a.q_stride, kTimeoutNs};
+                   a.B, a.T, a.Hq, a.Hkv, a.L_max, a.nblk, shift, a.q_stride,
+                   ((1ull << 36) + a.Hq / a.Hkv - 1) / (a.Hq / a.Hkv), kTimeoutNs};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
