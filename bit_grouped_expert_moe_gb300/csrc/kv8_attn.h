@@ -79,6 +79,13 @@ __device__ inline long long units_before(int n, int len, int r, int RT, int KT, 
   return sum;
 }
 
+// Tiles at the start of a sequence whose rows see no position.
+__device__ __forceinline__ int empty_tiles(int n, int len, int r, int RT) {
+  if (n <= len) return 0;
+  const int all = seq_tiles(n, r, RT);  // the last row sees len positions
+  return len == 0 ? all : min(all - 1, (r * (n - len) + RT) / RT - 1);
+}
+
 // The grid block whose run [c N / C, (c + 1) N / C) holds unit s.
 __device__ __forceinline__ int cta_of(long long s, long long N, int C) { return (int)(((s + 1) * C - 1) / N); }
 

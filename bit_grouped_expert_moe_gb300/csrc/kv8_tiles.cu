@@ -70,6 +70,10 @@ constexpr int kGroupWarps = 4;      // converting warps of K, and of V
 constexpr int kGroupThreads = kGroupWarps * 32;
 constexpr int kMaxCtas = 256;       // workspace bound on the grid
 constexpr long long kTimeoutNs = 1000000000ll;
+// A run also pays for every tile it begins (Q, the first unit's chain, the
+// output), about as much as two units: the runs are cut on a scale where a
+// tile with units takes kTileCost more places than units, before its first.
+constexpr int kTileCost = 2;
 constexpr float kMinusBig = -1e30f;
 constexpr float kWeightBits = 7.f;  // weights are 2^7 at the row's m ...
 constexpr float kSlack = 8.f;       // ... which scores may pass by this much
@@ -95,8 +99,7 @@ struct Cfg {
 };
 
 struct RowConst {  // of a tile's rows, written with its Q
-  float scale[kRows];   // scale * log2(e) * 2^e, e the row's power of two
-  int see[kRows];       // visible positions (0 for rows past the last)
+  uint8_t e[kRows];     // biased exponent of the row's largest magnitude
 };
 
 struct Ctl {
@@ -119,11 +122,17 @@ struct Ctl {
 };
 
 struct RunInfo {  // where a block's run starts, for the merge kernel
-  long long units;  // units of the call (0: nothing to do or bad tables)
-  long long lo;     // the run's first unit
+  long long places; // of the call (0: nothing to do or bad tables)
+  long long lo;     // the run's first place
   int b, g, rt, i, nb;
-  int live;         // the run is not empty
+  int live;         // there is a unit at or after it
 };
+
+// Places of the tiles before tile k of a sequence: their units, and kTileCost
+// for each that has units.
+__device__ __forceinline__ long long places_before(int n, int len, int r, int k) {
+  return units_before(n, len, r, kRows, kKeys, k) + (long long)kTileCost * max(k - empty_tiles(n, len, r, kRows), 0);
+}
 
 struct Params {
   const uint16_t* q;
@@ -133,7 +142,7 @@ struct Params {
   const int32_t* offsets;
   const int32_t* lens;
   uint16_t* o;
-  float* part;       // [2 C] slots of [D][128] O, then [128] m, [128] L
+  float* part;       // [2 C] slots of [128][D] O, then [128] m, [128] L
   RunInfo* info;     // [C]
   int32_t* flags;    // [C]
   float scale_log2;
@@ -386,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
   uint8_t* sR = smem + F::kQBytes;     // stages: two of K, two of V
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + F::kCtlOffset);
   static_assert(sizeof(Ctl) <= 5120, "control block");
-  __shared__ long long s_lo, s_hi;
+  __shared__ long long s_unit[2];  // units before the run's start and end
   __shared__ Cursor s_cur;
   __shared__ int s_bad;
 
@@ -421,8 +430,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
   // this one, then let this call's merge launch (it waits in turn).
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (warp == 1) {
-    // Check the tables, count the units and find where this block's run starts.
+  if (warp == 1 || warp == 2) {
+    // Check the tables, count the call's places and find the unit at the run's
+    // start (warp 1) and end (warp 2).
     long long total = 0;
     bool bad = false;
     for (int base = 0; base < p.B; base += 32) {
@@ -431,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
       if (b < p.B) {
         const int lo = __ldg(p.offsets + b), hi = __ldg(p.offsets + b + 1), len = __ldg(p.lens + b);
         if (offsets_bad(lo, hi, b, p.B, p.T) || len < 0 || len > p.L_max) bad = true;
-        else v = units_before(hi - lo, len, r, kRows, kKeys, seq_tiles(hi - lo, r, kRows));
+        else v = places_before(hi - lo, len, r, seq_tiles(hi - lo, r, kRows));
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -439,57 +449,70 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
     }
     bad = __any_sync(0xffffffffu, bad);
     total *= p.Hkv;
-    const long long lo = (long long)c * total / C, hi = (long long)(c + 1) * total / C;
+    const long long at = (long long)(c + warp - 1) * total / C;
     Cursor k{};
-    if (!bad && lo < hi) {
-      long long acc = 0, off = 0, per = 0;
+    long long before = 0;  // units before the place
+    if (!bad) {
+      long long acc = 0, off = 0, per = 0, units = 0;
+      k.b = -1;            // at == total: past the last
       for (int base = 0; base < p.B; base += 32) {
         const int b = base + lane;
-        long long v = 0;
+        long long v = 0, w = 0;
         if (b < p.B) {
-          const int n = __ldg(p.offsets + b + 1) - __ldg(p.offsets + b);
-          v = units_before(n, __ldg(p.lens + b), r, kRows, kKeys, seq_tiles(n, r, kRows)) * p.Hkv;
+          const int n = __ldg(p.offsets + b + 1) - __ldg(p.offsets + b), len = __ldg(p.lens + b);
+          w = units_before(n, len, r, kRows, kKeys, seq_tiles(n, r, kRows)) * p.Hkv;
+          v = places_before(n, len, r, seq_tiles(n, r, kRows)) * p.Hkv;
         }
-        long long incl = v;
+        long long incl = v, wincl = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const long long t = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += t;
+          const long long x = __shfl_up_sync(0xffffffffu, incl, o), y = __shfl_up_sync(0xffffffffu, wincl, o);
+          if (lane >= o) {
+            incl += x;
+            wincl += y;
+          }
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, acc + incl > lo);
+        const unsigned hit = __ballot_sync(0xffffffffu, acc + incl > at);
         if (hit) {
           const int L = __ffs(hit) - 1;
           k.b = base + L;
-          off = lo - (acc + __shfl_sync(0xffffffffu, incl - v, L));
+          off = at - (acc + __shfl_sync(0xffffffffu, incl - v, L));
           per = __shfl_sync(0xffffffffu, v, L) / p.Hkv;
+          units = __shfl_sync(0xffffffffu, w, L) / p.Hkv;
+          before += __shfl_sync(0xffffffffu, wincl - w, L);
           break;
         }
         acc += __shfl_sync(0xffffffffu, incl, 31);
+        before += __shfl_sync(0xffffffffu, wincl, 31);
       }
-      k.sequence(p);
-      k.g = (int)(off / per);
-      off -= k.g * per;
-      // the last tile whose first unit is at or before off, 32 candidates a round
-      int a = 0, z = seq_tiles(k.n, r, kRows);
-      while (z - a > 1) {
-        const int step = (z - a + 31) / 32, cand = a + lane * step;
-        const bool in = cand < z && units_before(k.n, k.len, r, kRows, kKeys, cand) <= off;
-        const int last = 31 - __clz(__ballot_sync(0xffffffffu, in));
-        a += last * step;
-        z = min(z, a + step);
+      if (k.b >= 0) {
+        k.sequence(p);
+        k.g = (int)(off / per);
+        off -= k.g * per;
+        // the last tile whose first place is at or before off, 32 candidates a round
+        int a = 0, z = seq_tiles(k.n, r, kRows);
+        while (z - a > 1) {
+          const int step = (z - a + 31) / 32, cand = a + lane * step;
+          const bool in = cand < z && places_before(k.n, k.len, r, cand) <= off;
+          const int last = 31 - __clz(__ballot_sync(0xffffffffu, in));
+          a += last * step;
+          z = min(z, a + step);
+        }
+        // tiles without units share their successor's first place: the
+        // search ends on the last of them, which has some
+        k.rt = a;
+        k.i = max((int)(off - places_before(k.n, k.len, r, a)) - kTileCost, 0);
+        k.nb = tile_units(k.n, k.len, r, kRows, kKeys, a);
+        before += k.g * units + units_before(k.n, k.len, r, kRows, kKeys, a) + k.i;
       }
-      // tiles without units share their successor's first unit: the search
-      // ends on the last of them, which has some
-      k.rt = a;
-      k.i = (int)(off - units_before(k.n, k.len, r, kRows, kKeys, a));
-      k.nb = tile_units(k.n, k.len, r, kRows, kKeys, a);
     }
     if (lane == 0) {
-      s_lo = lo;
-      s_hi = hi;
-      s_bad = bad;
-      s_cur = k;
-      p.info[c] = RunInfo{bad ? 0 : total, lo, k.b, k.g, k.rt, k.i, k.nb, !bad && lo < hi};
+      s_unit[warp - 1] = before;
+      if (warp == 1) {
+        s_bad = bad;
+        s_cur = k;
+        p.info[c] = RunInfo{bad ? 0 : total, at, k.b, k.g, k.rt, k.i, k.nb, !bad && k.b >= 0};
+      }
     }
   }
   __syncthreads();
@@ -504,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
     uint4* z = reinterpret_cast<uint4*>(p.o + (size_t)lo * p.Hq * D);
     for (size_t i = threadIdx.x; i < pieces; i += kThreads) z[i] = make_uint4(0u, 0u, 0u, 0u);
   }
-  if (s_lo >= s_hi) {
+  if (s_unit[0] >= s_unit[1]) {
     if (threadIdx.x == 0) p.flags[c] = 0;
     return;
   }
@@ -516,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
-  const int U = (int)(s_hi - s_lo);
+  const int U = (int)(s_unit[1] - s_unit[0]);
   Cursor cur = s_cur;
 
   volatile int* abort_flag = &ctl->abort;
@@ -648,9 +671,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
       if (fresh) {
         if (!warp_wait(&ctl->rc_full[tile & 1], (tile >> 1) & 1)) break;
         const RowConst& rc = ctl->rc[tile & 1];
-        rs = rc.scale[row];
-        see = rc.see[row];
+        const int e = rc.e[row], rho = cur.rt * kRows + row;
         __syncwarp();
+        rs = p.scale_log2 * __uint_as_float(e > 0 ? (uint32_t)e << 23 : 0x00400000u);  // 2^(e - 127)
+        see = rho < cur.n * r ? max(cur.len - cur.n + div_r(rho, p.rmagic) + 1, 0) : 0;
         if (lane == 0) mbar_arrive(&ctl->rc_empty[tile & 1]);
         m = kMinusBig;
         l = 0.f;
@@ -772,17 +796,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
             }
           }
         } else {
-          float* part = p.part + (size_t)(2 * c + (mid ? 0 : 1)) * slot_floats(D) + row;
+          // 32 rows by 16 dims at a time, the same way
+          float* part = p.part + (size_t)(2 * c + (mid ? 0 : 1)) * slot_floats(D);
+          const uint32_t stage = smem_u32(smem + F::kOutOffset) + warp * (32 * F::kOutPitch);
+          float* prow = part + (size_t)(quad * 32 + (lane >> 2)) * D + 4 * (lane & 3);
 #pragma unroll 1
-          for (int j = d0; j < d0 + D / 2; j += 32) {
-            float v[32];
-            tmem_ld_32(lane_addr + j, v);
+          for (int j = d0; j < d0 + D / 2; j += 16) {
+            uint32_t v[16];
+            tmem_ld_16(lane_addr + j, v);
+            __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) part[(size_t)(j + e) * kRows] = v[e];
+            for (int e = 0; e < 16; e += 4)
+              sts128(stage + lane * F::kOutPitch + 4 * e, v[e], v[e + 1], v[e + 2], v[e + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              *reinterpret_cast<uint4*>(prow + (size_t)(8 * k) * D + j) =
+                  lds128(stage + (8 * k + (lane >> 2)) * F::kOutPitch + 16 * (lane & 3));
           }
           if (half == 0) {
-            part[(size_t)D * kRows] = m;
-            part[(size_t)(D + 1) * kRows] = l;
+            part[(size_t)D * kRows + row] = m;
+            part[(size_t)(D + 1) * kRows + row] = l;
           }
         }
         tc_fence_before();
@@ -845,29 +879,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
 
     // Q of the tile at a cursor: D / 8 lanes per row, 16 bytes each
     int tile = 0;
+    constexpr int kLanes = D / 8, kAtOnce = 256 / D, kBatch = 4;    // lanes per row; rows of a load; loads in flight
+    constexpr int kQRows = kRows / (2 * kGroupWarps * kAtOnce);     // loads of a lane
+    const int ln = lane % kLanes, qrow = (warp - kSoftWarps) * (kRows / (2 * kGroupWarps)) + lane / kLanes;
+    auto load_rows = [&](const Cursor& k, int base, uint4 (&v)[kBatch]) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int rho = k.rt * kRows + qrow + (base + i) * kAtOnce, tok = div_r(rho, p.rmagic);
+        v[i] = make_uint4(0u, 0u, 0u, 0u);
+        ldg128_if<0>(v[i], reinterpret_cast<const uint8_t*>(p.q + (size_t)(k.lo + tok) * p.q_stride +
+                                                            (size_t)(k.g * r + rho - tok * r) * D + ln * 8),
+                     rho < k.n * r);
+      }
+    };
     auto load_q = [&](const Cursor& k) -> bool {
+      uint4 v[kBatch];
+      load_rows(k, 0, v);  // on their way while the last tile's products end
       if (tile > 0 && !warp_wait(&ctl->q_empty, (tile - 1) & 1)) return false;
       if (tile > 1 && !warp_wait(&ctl->rc_empty[tile & 1], ((tile >> 1) - 1) & 1)) return false;
       tc_fence_after();
-      constexpr int kLanes = D / 8, kAtOnce = 256 / D, kBatch = 4;  // rows of a load; loads in flight
-      const int ln = lane % kLanes, r0 = (warp - kSoftWarps) * (kRows / (2 * kGroupWarps));
       RowConst& rc = ctl->rc[tile & 1];
-#pragma unroll 1
-      for (int base = r0; base < r0 + kRows / (2 * kGroupWarps); base += kBatch * kAtOnce) {
-        uint4 v[kBatch];
-        int tok[kBatch];  // the row's token, or n past the last
+#pragma unroll
+      for (int base = 0; base < kQRows; base += kBatch) {
+        if (base > 0) load_rows(k, base, v);
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-          const int rho = k.rt * kRows + base + i * kAtOnce + lane / kLanes;
-          tok[i] = rho < k.n * r ? div_r(rho, p.rmagic) : k.n;
-          v[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (tok[i] < k.n)
-            v[i] = __ldg(reinterpret_cast<const uint4*>(p.q + (size_t)(k.lo + tok[i]) * p.q_stride +
-                                                        (size_t)(k.g * r + rho - tok[i] * r) * D) + ln);
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int row = base + i * kAtOnce + lane / kLanes;
+          const int row = qrow + (base + i) * kAtOnce;
           uint32_t mx = __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu),
                                  __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
           mx = max(mx & 0xFFFFu, mx >> 16);
@@ -883,13 +920,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
           uint32_t x[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            x[j] = pack_f16(bf16_bits_to_f32(in[j] & 0xFFFFu) * down, bf16_bits_to_f32(in[j] >> 16) * down);
+            x[j] = pack_f16(__uint_as_float(in[j] << 16) * down, __uint_as_float(in[j] & 0xFFFF0000u) * down);
           sts128(smem_u32(sQ) + (ln >> 3) * (kRows * 128) + row * 128 + (((ln & 7) ^ (row & 7)) << 4), x[0], x[1], x[2],
                  x[3]);
-          if (ln == 0) {
-            rc.scale[row] = ldexpf(p.scale_log2, e - 127);
-            rc.see[row] = tok[i] < k.n ? max(k.len - k.n + tok[i] + 1, 0) : 0;
-          }
+          if (ln == 0) rc.e[row] = (uint8_t)e;
         }
       }
       fence_proxy_async();
@@ -969,19 +1003,17 @@ struct MergeParams {
   int Hq, Hkv, D, C;
 };
 
-constexpr int kMergeRows = 16;
-constexpr int kMergeThreads = 256;
+constexpr int kMergeRows = 8;       // rows of a block, a warp each
+constexpr int kMergeThreads = 32 * kMergeRows;
 
 // Block (c, y): if run c is the second of the runs that share a tile, the
-// tile's rows 16 y .. + 15. The first run of a tile left its state in its
-// second slot (a tile that the run's end cuts), the others in their first.
+// tile's rows 8 y .. + 7. The first run of a tile left its state in its second
+// slot (a tile that the run's end cuts), the others in their first.
 __global__ void __launch_bounds__(kMergeThreads) kv8_tiles_merge_kernel(const MergeParams p) {
-  __shared__ float s_f[kMaxCtas][kMergeRows];   // factor of each state and row
-  __shared__ float s_o[kMergeRows][256 + 1];
   __shared__ int s_first;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.x, C = p.C, t = threadIdx.x;
+  const int c = blockIdx.x, C = p.C, t = threadIdx.x, lane = t & 31;
   if (c == 0 && blockIdx.y == 0) {
     // the call's status: the outcome of the lowest-numbered grid block that failed
     if (t == 0) s_first = C;
@@ -993,46 +1025,56 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_tiles_merge_kernel(const Me
   }
   const RunInfo f = p.info[c];
   if (!f.live || f.i == 0) return;
-  const long long N = f.units, start = f.lo - f.i;
+  const long long N = f.places, start = f.lo - f.i;  // the place of the tile's first unit
   const int c0 = cta_of(start, N, C);
   if (c != cta_of((long long)(c0 + 1) * N / C, N, C)) return;  // a later one of the tile's runs
   const int c1 = cta_of(start + f.nb - 1, N, C);
-  const int r = p.Hq / p.Hkv, D = p.D, row0 = blockIdx.y * kMergeRows;
+  const int r = p.Hq / p.Hkv, D = p.D, row = blockIdx.y * kMergeRows + (t >> 5);
   const int lo = __ldg(p.offsets + f.b), n = __ldg(p.offsets + f.b + 1) - lo, len = __ldg(p.lens + f.b);
-  const int row = t % kMergeRows;
-  // every state's factor 2^(m_c - M) / L (empty runs have none)
-  auto live = [&](int cc) { return (long long)cc * N / C != (long long)(cc + 1) * N / C; };
-  auto slot = [&](int cc) { return p.part + (size_t)(2 * cc + (cc == c0 ? 1 : 0)) * slot_floats(D) + row0; };
-  int failed = 0;
-  for (int cc = c0 + t; cc <= c1; cc += kMergeThreads) failed |= live(cc) ? __ldcg(p.flags + cc) : 0;
-  if (__syncthreads_or(failed)) return;  // a run gave up: o is left as it was
-  if (t < kMergeRows) {
-    float M = kMinusBig, L = 0.f;
-    for (int cc = c0; cc <= c1; ++cc)
-      if (live(cc)) M = fmaxf(M, __ldcg(slot(cc) + (size_t)D * kRows + t));
-    for (int cc = c0; cc <= c1; ++cc) {
-      const float e = live(cc) ? exp2f(__ldcg(slot(cc) + (size_t)D * kRows + t) - M) : 0.f;
-      s_f[cc - c0][t] = e;
-      if (live(cc)) L += e * __ldcg(slot(cc) + (size_t)(D + 1) * kRows + t);
+  const int rho = f.rt * kRows + row, tok = rho / r;
+  if (rho >= n * r || len - n + tok < 0) return;
+  auto live = [&](int cc) { return cc <= c1 && (long long)cc * N / C != (long long)(cc + 1) * N / C; };  // not empty
+  auto slot = [&](int cc) { return p.part + (size_t)(2 * cc + (cc == c0 ? 1 : 0)) * slot_floats(D); };
+  // lane k weighs the states of runs c0 + k, c0 + 32 + k, ...
+  float M = kMinusBig;
+  bool failed = false;
+  for (int cc = c0 + lane; cc <= c1; cc += 32)
+    if (live(cc)) {
+      failed |= __ldcg(p.flags + cc) != 0;
+      M = fmaxf(M, __ldcg(slot(cc) + (size_t)D * kRows + row));
     }
-    const int rho = f.rt * kRows + row0 + t;
-    const float inv = rho < n * r && len - n + rho / r >= 0 ? 1.f / L : 0.f;
-    for (int cc = c0; cc <= c1; ++cc) s_f[cc - c0][t] *= inv;
+  if (__any_sync(0xffffffffu, failed)) return;  // a run gave up: o is left as it was
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float L = 0.f, acc[8];  // head dims lane * D / 32 .. of the row
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+  const int per = D / 32;
+  for (int base = c0; base <= c1; base += 32) {
+    const int mine = base + lane;
+    const float e = live(mine) ? exp2f(__ldcg(slot(mine) + (size_t)D * kRows + row) - M) : 0.f;
+    float l = live(mine) ? e * __ldcg(slot(mine) + (size_t)(D + 1) * kRows + row) : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    L += l;
+    for (int cc = base; cc <= min(c1, base + 31); ++cc) {
+      const float w = __shfl_sync(0xffffffffu, e, cc - base);
+      if (!live(cc)) continue;
+      const float* o = slot(cc) + (size_t)row * D + lane * per;
+#pragma unroll
+      for (int i = 0; i < 8; i += 2)
+        if (i < per) {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(o + i));
+          acc[i] = fmaf(w, x.x, acc[i]);
+          acc[i + 1] = fmaf(w, x.y, acc[i + 1]);
+        }
+    }
   }
-  __syncthreads();
-  for (int d = t / kMergeRows; d < D; d += kMergeThreads / kMergeRows) {
-    float acc = 0.f;
-    for (int cc = c0; cc <= c1; ++cc)
-      if (live(cc)) acc = fmaf(s_f[cc - c0][row], __ldcg(slot(cc) + (size_t)d * kRows + row), acc);
-    s_o[row][d] = acc;
-  }
-  __syncthreads();
-  for (int i = t; i < kMergeRows * D / 2; i += kMergeThreads) {
-    const int rr = i / (D / 2), d = 2 * (i % (D / 2)), rho = f.rt * kRows + row0 + rr;
-    if (rho >= n * r || len - n + rho / r < 0) continue;
-    const __nv_bfloat162 y = __floats2bfloat162_rn(s_o[rr][d], s_o[rr][d + 1]);
-    *reinterpret_cast<__nv_bfloat162*>(p.o + ((size_t)(lo + rho / r) * p.Hq + (size_t)f.g * r + rho % r) * D + d) = y;
-  }
+  const float inv = 1.f / L;
+  uint16_t* out = p.o + ((size_t)(lo + tok) * p.Hq + (size_t)f.g * r + rho - tok * r) * D + lane * per;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2)
+    if (i < per) *reinterpret_cast<__nv_bfloat162*>(out + i) = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
 }
 
 }  // namespace tiles
