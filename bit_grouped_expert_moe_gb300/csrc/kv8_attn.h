@@ -86,8 +86,24 @@ __device__ __forceinline__ int empty_tiles(int n, int len, int r, int RT) {
   return len == 0 ? all : min(all - 1, (r * (n - len) + RT) / RT - 1);
 }
 
-// The grid block whose run [c N / C, (c + 1) N / C) holds unit s.
-__device__ __forceinline__ int cta_of(long long s, long long N, int C) { return (int)(((s + 1) * C - 1) / N); }
+// N places dealt out to C grid blocks in contiguous runs, the first N % C of
+// them one place longer. 64-bit divisions cost hundreds of cycles, and there is
+// no work of another kind to hide them behind, so small numbers are divided in
+// 32 bits.
+__device__ __forceinline__ long long div_small(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+struct Runs {
+  long long per;  // N / C
+  int more;       // N % C
+  __device__ Runs(long long N, int C) : per(div_small(N, C)), more((int)(N - per * C)) {}
+  __device__ long long start(int c) const { return c * per + min(c, more); }
+  __device__ bool empty(int c) const { return per == 0 && c >= more; }
+  __device__ int of(long long s) const {  // the run that holds place s
+    const long long lead = more * (per + 1);
+    return s < lead ? (int)div_small(s, per + 1) : more + (int)div_small(s - lead, per);
+  }
+};
 
 }  // namespace kv8
 }  // namespace bgmoe

@@ -5,12 +5,14 @@
 // (sequence, KV head, row tile), where a row tile is 8 kNT rows and a row one
 // (query token, query head of the KV head). The positions a tile can see are
 // cut into units of 64 and all units of the call are laid end to end in the
-// order (sequence, KV head, row tile, position); block c of a grid of C takes
-// the contiguous run [c N / C, (c+1) N / C), so the bytes spread evenly over
-// the SMs whatever the lengths are.
+// order (sequence, KV head, row tile, position) and dealt out in equal
+// contiguous runs, one per block of a one-block-per-SM grid, so the bytes
+// spread evenly over the SMs whatever the lengths are.
 //
-// kv8_split_kernel — warp 4 streams each unit's K and V codes (64 x D bytes
-// each) into a shared-memory ring by TMA; warps 0-3 take 16 positions each:
+// kv8_split_kernel — warp 8 streams each unit's K and V codes (64 x D bytes
+// each) into a shared-memory ring by TMA. Four warps take 16 positions each;
+// the other four take every second unit, or, where 8 kNT rows by D head dims
+// are more than a warp's registers hold, the other half of the rows:
 //   S^T  = K Q^T     mma.sync m16n8k16 in fp16: M = 16 positions, N = 8 rows;
 //   online softmax per row on the base-2 scale;
 //   O^T += V^T P^T   M = 16 head dims, N = 8 rows, K = 16 positions.
@@ -38,7 +40,8 @@
 //
 // kv8_merge_kernel — one block per (query token, query head, 64 head dims)
 // combines the partial states of the grid blocks that covered its tile, in a
-// fixed order:  M = max m_c,  o = sum 2^(m_c - M) O_c / sum 2^(m_c - M) L_c.
+// fixed order:
+//   M = max m_c,  o = sum 2^(m_c - M) O_c / sum 2^(m_c - M) L_c.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <type_traits>
@@ -60,7 +63,7 @@ using tc::mbar_wait;
 using tc::smem_u32;
 
 constexpr int kPos = 64;            // positions per unit (= ring stage)
-constexpr int kConsumers = 4;       // warps, 16 positions each
+constexpr int kConsumers = 8;       // warps
 constexpr int kThreads = (kConsumers + 1) * 32;
 constexpr int kMaxCtas = 256;       // workspace bound on the grid
 constexpr long long kTimeoutNs = 1000000000ll;
@@ -68,31 +71,39 @@ constexpr float kMinusBig = -1e30f; // running-max start: finite, so 2^(m - m_ne
 constexpr float kWeightBits = 14.f; // the largest weight is 2^14
 
 template <int D, int kNT>
-struct Smem {
+struct Cfg {
+  static constexpr int kRowSplit = kNT * D > 256 ? 2 : 1;  // warps that share positions and split the rows
+  static constexpr int kNTw = kNT / kRowSplit;             // groups of 8 rows of a warp
+  static constexpr int kFold = kConsumers / kRowSplit;     // warps whose states belong to the same rows
+  static constexpr int kUsers = kRowSplit == 2 ? 8 : 4;    // warps that read a unit
   static constexpr int kSlabs = D < 128 ? 1 : D / 128;    // TMA boxes of up to 128 bytes by 64 rows
   static constexpr int kSlab = kPos * (D < 128 ? D : 128);
   static constexpr int kStageBytes = 2 * kSlabs * kSlab;  // K then V
   // A warp's softmax state as its lanes hold it: D/4 accumulators, then two
-  // maxima and two sums, for each of the kNT groups; stored [value][lane].
-  static constexpr int kStateFloats = (D / 4 + 4) * kNT;
-  static constexpr int kStateBytes = kStateFloats * 32 * 4;
-  static constexpr int kMergeBytes = 3 * kStateBytes;     // warps 2, 3 (first fold) and warp 1 (second fold)
-  static constexpr int kFit = (220 * 1024 - kMergeBytes) / kStageBytes;
+  // maxima and two sums, for each of its groups; stored [value][lane].
+  static constexpr int kStateFloats = (D / 4 + 4) * kNTw;
+  static constexpr int kFoldBytes = 4 * kStateFloats * 32 * 4;  // four slots
+  static constexpr int kQPitch = D * 2 + 32;              // bytes of a row of Q (the padding spreads the banks)
+  static constexpr int kQBytes = 8 * kNT * kQPitch;
+  static constexpr int kFit = (224 * 1024 - kFoldBytes - kQBytes) / kStageBytes;
   static constexpr int kStages = kFit > 12 ? 12 : kFit;
-  static constexpr int kCtlOffset = kStages * kStageBytes + kMergeBytes;
-  static constexpr int kBytes = kCtlOffset + 256 + 1024;  // + alignment slack
-  static_assert(kStages >= 3 && kBytes <= 227 * 1024, "shared memory");
+  static constexpr int kFoldOffset = kStages * kStageBytes;
+  static constexpr int kQOffset = kFoldOffset + kFoldBytes;
+  static constexpr int kCtlOffset = kQOffset + kQBytes;
+  static constexpr int kBytes = kCtlOffset + 768 + 1024;  // + alignment slack
+  static_assert(kNTw * D <= 256 && kStages >= 3 && kBytes <= 227 * 1024, "registers and shared memory");
 };
 
 template <int kStages>
 struct Ctl {
   uint64_t full[kStages];
   uint64_t empty[kStages];
-  uint64_t mrg_full;   // first fold: warps 2 and 3 have stored their states
-  uint64_t mrg_free;   // first fold: warps 0 and 1 have read them
-  uint64_t mrg2_full;  // second fold: warp 1 has stored its state
-  uint64_t mrg2_free;  // second fold: warp 0 has read it
+  uint64_t fold;  // all consumer warps, at each step of a fold
   int abort;
+  // of the tile's rows: score factor of the row's power of two, -128 sum(q)
+  // 2^-24 (int8), visible positions
+  float scale[32], shift[32];
+  int see[32];
 };
 
 struct Params {
@@ -223,14 +234,15 @@ struct Cursor {
 template <int D, int kNT, bool kE4m3>
 __global__ void __launch_bounds__(kThreads, 1)
     kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Params p) {
-  using S = Smem<D, kNT>;
+  using S = Cfg<D, kNT>;
+  constexpr int kNTw = S::kNTw;
   constexpr int kStages = S::kStages;
   constexpr int RT = 8 * kNT;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Ctl<kStages>* ctl = reinterpret_cast<Ctl<kStages>*>(smem + S::kCtlOffset);
-  static_assert(sizeof(Ctl<kStages>) <= 256, "control block");
-  float* mrg = reinterpret_cast<float*>(smem + kStages * S::kStageBytes);
+  static_assert(sizeof(Ctl<kStages>) <= 768, "control block");
+  float* mrg = reinterpret_cast<float*>(smem + S::kFoldOffset);
   __shared__ long long s_lo, s_hi;
   __shared__ Cursor s_cur;
   __shared__ int s_bad;
@@ -242,12 +254,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&ctl->full[s], 1);
-      mbar_init(&ctl->empty[s], kConsumers);
+      mbar_init(&ctl->empty[s], S::kUsers);
     }
-    mbar_init(&ctl->mrg_full, 2);
-    mbar_init(&ctl->mrg_free, 2);
-    mbar_init(&ctl->mrg2_full, 1);
-    mbar_init(&ctl->mrg2_free, 1);
+    mbar_init(&ctl->fold, kConsumers);
     ctl->abort = 0;
     tc::fence_barrier_init();
   }
@@ -263,72 +272,77 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 0) {
-    // Check the tables, count the units and find where this block's run starts.
-    long long total = 0;
+    // Check the tables and count the units (pass 0), then find where this
+    // block's run starts (pass 1): one copy of the code, which runs cold.
+    long long total = 0, acc = 0, lo = 0, hi = 0;
+    int tiles = 0;
     bool bad = false;
-    for (int base = 0; base < p.B; base += 32) {
+#pragma unroll 1
+    for (int base = 0, pass = 0; base < p.B;) {
       const int b = base + lane;
       long long v = 0;
+      int nt = 0;
       if (b < p.B) {
-        const int lo = __ldg(p.offsets + b), hi = __ldg(p.offsets + b + 1), len = __ldg(p.lens + b);
-        if (offsets_bad(lo, hi, b, p.B, p.T) || len < 0 || len > p.L_max) bad = true;
-        else v = seq_units(hi - lo, len, r, RT);
+        const int at = __ldg(p.offsets + b), end = __ldg(p.offsets + b + 1), len = __ldg(p.lens + b);
+        if (offsets_bad(at, end, b, p.B, p.T) || len < 0 || len > p.L_max) {
+          bad = true;
+        } else {
+          v = seq_units(end - at, len, r, RT) * p.Hkv;
+          nt = seq_tiles(end - at, r, RT) * p.Hkv;
+        }
       }
+      long long incl = v;
+      int tincl = nt;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      total += v;
-    }
-    bad = __any_sync(0xffffffffu, bad);
-    total *= p.Hkv;
-    const long long lo = (long long)c * total / C, hi = (long long)(c + 1) * total / C;
-    if (!bad && lo < hi) {
-      long long acc = 0;
-      int tiles = 0;
-      for (int base = 0; base < p.B; base += 32) {
-        const int b = base + lane;
-        long long v = 0;
-        int nt = 0;
-        if (b < p.B) {
-          const int n = __ldg(p.offsets + b + 1) - __ldg(p.offsets + b);
-          v = seq_units(n, __ldg(p.lens + b), r, RT) * p.Hkv;
-          nt = seq_tiles(n, r, RT) * p.Hkv;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+        const int u = __shfl_up_sync(0xffffffffu, tincl, o);
+        if (lane >= o) {
+          incl += t;
+          tincl += u;
         }
-        long long incl = v;
-        int tincl = nt;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long t = __shfl_up_sync(0xffffffffu, incl, o);
-          const int u = __shfl_up_sync(0xffffffffu, tincl, o);
-          if (lane >= o) {
-            incl += t;
-            tincl += u;
-          }
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, acc + incl > lo);
-        if (hit) {
-          if (lane == __ffs(hit) - 1) {
-            Cursor k;
-            k.b = b;
-            k.sequence(p);
-            long long off = lo - (acc + incl - v);
-            const long long per = v / p.Hkv;
-            k.g = (int)(off / per);
-            off -= k.g * per;
-            k.rt = 0;
-            k.nb = tile_units(k.n, k.len, r, RT, kPos, 0);
-            while (off >= k.nb) {
-              off -= k.nb;
-              k.nb = tile_units(k.n, k.len, r, RT, kPos, ++k.rt);
-            }
-            k.i = (int)off;
-            k.tile = tiles + tincl - nt + k.g * (nt / p.Hkv) + k.rt;
-            s_cur = k;
-          }
-          break;
-        }
-        acc += __shfl_sync(0xffffffffu, incl, 31);
-        tiles += __shfl_sync(0xffffffffu, tincl, 31);
       }
+      const long long all = __shfl_sync(0xffffffffu, incl, 31);
+      base += 32;
+      if (pass == 0) {
+        total += all;
+        if (base < p.B) continue;
+        // the last chunk: the runs are known; with one chunk the search goes on with it
+        bad = __any_sync(0xffffffffu, bad);
+        const Runs runs(total, C);
+        lo = runs.start(c);
+        hi = runs.start(c + 1);
+        if (bad || lo >= hi) break;
+        pass = 1;
+        if (p.B > 32) {
+          base = 0;
+          continue;
+        }
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, acc + incl > lo);
+      if (hit) {
+        if (lane == __ffs(hit) - 1) {
+          Cursor k;
+          k.b = b;
+          k.sequence(p);
+          long long off = lo - (acc + incl - v);
+          const long long per = div_small(v, p.Hkv);
+          k.g = (int)div_small(off, per);
+          off -= k.g * per;
+          k.rt = 0;
+          k.nb = tile_units(k.n, k.len, r, RT, kPos, 0);
+          while (off >= k.nb) {
+            off -= k.nb;
+            k.nb = tile_units(k.n, k.len, r, RT, kPos, ++k.rt);
+          }
+          k.i = (int)off;
+          k.tile = tiles + tincl - nt + k.g * (nt / p.Hkv) + k.rt;
+          s_cur = k;
+        }
+        break;
+      }
+      acc += all;
+      tiles += __shfl_sync(0xffffffffu, tincl, 31);
     }
     if (lane == 0) {
       s_lo = lo;
@@ -388,66 +402,104 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ldmatrix row addresses (relative to a slab): lanes 0-7, 8-15, 16-23,
     // 24-31 address the four 8 x 16-byte matrices (positions +0, +8 of the
     // low 16 dims, then of the high 16)
-    const int row = 16 * warp + (lane & 7) + ((lane >> 3) & 1) * 8;
+    const int pw = warp & 3, part = warp >> 2;  // the warp's 16 positions; its half of the units or of the rows
+    const int rows0 = S::kRowSplit == 2 ? part * 8 * kNTw : 0;
+    const int row = 16 * pw + (lane & 7) + ((lane >> 3) & 1) * 8;
     const int ch = lane >> 4;
     // TMA swizzle: 16-byte chunk ^= row % 8 (128-byte rows), (row / 2) % 4 (64-byte rows)
     const int sw = D < 128 ? (row >> 1) & 3 : row & 7;
 
-    uint32_t qf[kNT][D / 16][2];   // Q as the B operand: row 8 nt + gq, dims 16 ks + 4 m4 .. + 3
-    float acc[kNT][D / 16][4];
-    float m[kNT][2], l[kNT][2];    // of rows 8 nt + 2 m4, + 1
-    float rq[kNT][2], off[kNT][2]; // score factor of the row's power of two; -128 sum(q) (int8)
-    int lim[kNT][2];               // visible positions
-    auto load_q = [&]() {
+    uint32_t qf[kNTw][D / 16][2];   // Q as the B operand: row 8 nt + gq, dims 16 ks + 4 m4 .. + 3
+    float acc[kNTw][D / 16][4];
+    float m[kNTw][2], l[kNTw][2];    // of rows 8 nt + 2 m4, + 1
+    float rq[kNTw][2], off[kNTw][2]; // score factor of the row's power of two; -128 sum(q) (int8)
+    int lim[kNTw][2];               // visible positions
+    int folds = 0;
+    // All consumer warps have come this far.
+    auto together = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->fold);
+      return warp_wait(&ctl->fold, folds++ & 1);
+    };
+    // Q of a tile, a warp per row at a time, through shared memory into every
+    // warp's fragments. (Each warp fetching its own fragments took 4.7 us, at
+    // every tile: three times the instructions, all of them cold.)
+    const uint32_t sQ = smem_u32(smem + S::kQOffset);
+    auto load_q = [&]() -> bool {
+      constexpr int kPer = D / 32;  // head dims of a lane
+      if (!together()) return false;  // the last tile's Q is in its fragments
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) {
-        const int rr = cur.rt * RT + 8 * nt + gq;
+      for (int i = 0; i < kNT; ++i) {
+        const int rw = warp + 8 * i, rr = cur.rt * RT + rw, tok = rr / r;
         const bool live = rr < cur.n * r;
-        const uint16_t* qrow = p.q + (size_t)(cur.lo + (live ? rr / r : 0)) * p.q_stride +
-                               (size_t)(cur.g * r + (live ? rr % r : 0)) * D + 4 * m4;
-        uint2 w[D / 16];
+        const uint16_t* src = p.q + (size_t)(cur.lo + (live ? tok : 0)) * p.q_stride +
+                              (size_t)(cur.g * r + (live ? rr - tok * r : 0)) * D + kPer * lane;
+        uint32_t w[kPer / 2], mx = 0u;
+        if (kPer == 8) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(src));
+          w[0] = x.x;
+          w[1] = x.y;
+          w[2 % (kPer / 2)] = x.z;
+          w[3 % (kPer / 2)] = x.w;
+        } else if (kPer == 4) {
+          const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
+          w[0] = x.x;
+          w[1 % (kPer / 2)] = x.y;
+        } else {
+          w[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+        }
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          w[ks] = live ? __ldg(reinterpret_cast<const uint2*>(qrow + 16 * ks)) : make_uint2(0u, 0u);
-        uint32_t mx = 0u;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) mx = __vmaxu2(mx, __vmaxu2(w[ks].x & 0x7FFF7FFFu, w[ks].y & 0x7FFF7FFFu));
-        mx = max(mx & 0xFFFFu, mx >> 16);
-        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        for (int k = 0; k < kPer / 2; ++k) {
+          w[k] = live ? w[k] : 0u;
+          mx = __vmaxu2(mx, w[k] & 0x7FFF7FFFu);
+        }
+        mx = __reduce_max_sync(0xffffffffu, max(mx & 0xFFFFu, mx >> 16));
         // 2^-e with e the exponent of the largest magnitude (an infinity or a
         // NaN makes the whole row NaN whatever e is)
         const int e = min((int)(mx >> 7), 253);
         const float down = __uint_as_float((uint32_t)(254 - e) << 23);
         float sum = 0.f;
+        const uint32_t to = sQ + rw * S::kQPitch + 2 * kPer * lane;
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          qf[nt][ks][0] = pack_f16(bf16_bits_to_f32(w[ks].x & 0xFFFFu) * down, bf16_bits_to_f32(w[ks].x >> 16) * down);
-          qf[nt][ks][1] = pack_f16(bf16_bits_to_f32(w[ks].y & 0xFFFFu) * down, bf16_bits_to_f32(w[ks].y >> 16) * down);
-          if (!kE4m3) {
-            const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&qf[nt][ks][0]));
-            const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&qf[nt][ks][1]));
-            sum += (a.x + a.y) + (b.x + b.y);
-          }
+        for (int k = 0; k < kPer / 2; ++k) {
+          w[k] = pack_f16(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
+          const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+          sum += a.x + a.y;
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + 4 * k), "r"(w[k]) : "memory");
         }
         if (!kE4m3) {
-          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        }
-        const float up = ldexpf(p.scale_log2, e - 127);
-        const int see = live ? cur.len - cur.n + rr / r + 1 : 0;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {  // from the lanes of row 2 m4 + k
-          const int src = (2 * m4 + k) * 4;
-          rq[nt][k] = __shfl_sync(0xffffffffu, up, src);
-          lim[nt][k] = __shfl_sync(0xffffffffu, see, src);
-          off[nt][k] = kE4m3 ? 0.f : __shfl_sync(0xffffffffu, sum, src) * -7.62939453125e-06f;  // -128 2^-24
+          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        }
+        if (lane == 0) {
+          ctl->scale[rw] = p.scale_log2 * __uint_as_float(e > 0 ? (uint32_t)e << 23 : 0x00400000u);  // 2^(e - 127)
+          ctl->shift[rw] = kE4m3 ? 0.f : sum * -7.62939453125e-06f;  // -128 2^-24
+          ctl->see[rw] = live ? cur.len - cur.n + tok + 1 : 0;
         }
       }
+      if (!together()) return false;
+#pragma unroll
+      for (int nt = 0; nt < kNTw; ++nt) {
+        const uint32_t at = sQ + (rows0 + 8 * nt + gq) * S::kQPitch + 8 * m4;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                       : "=r"(qf[nt][ks][0]), "=r"(qf[nt][ks][1])
+                       : "r"(at + 32 * ks)
+                       : "memory");
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int rw = rows0 + 8 * nt + 2 * m4 + k;
+          rq[nt][k] = ctl->scale[rw];
+          off[nt][k] = ctl->shift[rw];
+          lim[nt][k] = ctl->see[rw];
+        }
+      }
+      return true;
     };
     auto reset = [&]() {
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) {
+      for (int nt = 0; nt < kNTw; ++nt) {
 #pragma unroll
         for (int mt = 0; mt < D / 16; ++mt) acc[nt][mt][0] = acc[nt][mt][1] = acc[nt][mt][2] = acc[nt][mt][3] = 0.f;
         m[nt][0] = m[nt][1] = kMinusBig;
@@ -457,24 +509,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The scales of this warp's 16 positions of the unit at a cursor (a group
     // past the context repeats the last visible block's: it is not used).
     auto load_scales = [&](const Cursor& k, float& sk, float& sv) {
-      const int pos = min(k.i * kPos + 16 * warp, k.len - 1);
+      const int pos = min(k.i * kPos + 16 * pw, k.len - 1);
       const size_t at = (size_t)(k.b * p.Hkv + k.g) * p.nblk + (pos >> p.shift);
       sk = __ldg(p.ks + at);
       sv = __ldg(p.vs + at);
     };
     reset();
-    load_q();
     float sk, sv;
     load_scales(cur, sk, sv);
+    bool good = load_q();
 
-    int s = 0, ph = 0, flushes = 0;
-    for (long long j = lo; j < hi; ++j) {
+    int s = 0, ph = 0;
+#pragma unroll 1
+    for (long long j = lo; good && j < hi; ++j) {
       Cursor nxt = cur;
       float skn = 0.f, svn = 0.f;
       if (j + 1 < hi) {  // the next unit's scales travel while this one is computed
         nxt.advance(p, r, RT);
         load_scales(nxt, skn, svn);
       }
+      const bool mine = S::kRowSplit == 2 || ((int)(j - lo) & 1) == part;
+      // every warp sees every phase, its own or not: a parity says nothing to
+      // a waiter that is two phases behind
       if (!warp_wait(&ctl->full[s], ph)) break;
       const uint32_t sK = smem_u32(smem + s * S::kStageBytes);
       const uint32_t sV = sK + S::kSlabs * S::kSlab;
@@ -483,11 +539,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int cc = (kk % kPerSlab) * 2 + ch;
         return base + (kk / kPerSlab) * S::kSlab + row * (D < 128 ? 64 : 128) + ((cc ^ sw) << 4);
       };
-      const int pos0 = cur.i * kPos + 16 * warp;  // first position of this warp's 16
-      if (pos0 < cur.len) {
-        float x[kNT][4];
+      const int pos0 = cur.i * kPos + 16 * pw;  // first position of this warp's 16
+      if (mine && pos0 < cur.len) {
+        float x[kNTw][4];
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
+        for (int nt = 0; nt < kNTw; ++nt) {
           x[nt][0] = x[nt][2] = off[nt][0];
           x[nt][1] = x[nt][3] = off[nt][1];
         }
@@ -501,8 +557,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             k_pairs<kE4m3>(w[2 * h], a0, a2);
             k_pairs<kE4m3>(w[2 * h + 1], a1, a3);
 #pragma unroll
-            for (int nt = 0; nt < kNT; ++nt) {
-              if (kNT == 1 && h == 1) mma_f16(y, a0, a1, a2, a3, qf[nt][2 * kk + h][0], qf[nt][2 * kk + h][1]);
+            for (int nt = 0; nt < kNTw; ++nt) {
+              if (kNTw == 1 && h == 1) mma_f16(y, a0, a1, a2, a3, qf[nt][2 * kk + h][0], qf[nt][2 * kk + h][1]);
               else mma_f16(x[nt], a0, a1, a2, a3, qf[nt][2 * kk + h][0], qf[nt][2 * kk + h][1]);
             }
           }
@@ -510,17 +566,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float svx = sv > 0.f ? sv : kScaleFloor;
         const float lsv = log2f(svx), rsv = 1.f / svx;
         const int pr = pos0 + gq;
-        uint32_t pb[kNT][2];
-        float al[kNT][2];
+        uint32_t pb[kNTw][2];
+        float al[kNTw][2];
         bool grew = false;
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
+        for (int nt = 0; nt < kNTw; ++nt) {
           const float a[2] = {rq[nt][0] * sk, rq[nt][1] * sk};
           float w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             float d = x[nt][e];
-            if (kNT == 1) d += y[e];
+            if (kNTw == 1) d += y[e];
             if (!kE4m3) d *= 16777216.f;
             w[e] = pr + (e >> 1) * 8 < lim[nt][e & 1] ? fmaf(d, a[e & 1], lsv) : -INFINITY;
           }
@@ -545,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt)
+          for (int nt = 0; nt < kNTw; ++nt)
 #pragma unroll
             for (int mt = 0; mt < D / 16; ++mt) {
               acc[nt][mt][0] *= al[nt][0];
@@ -574,31 +630,31 @@ __global__ void __launch_bounds__(kThreads, 1)
               a3 &= mhi;
             }
 #pragma unroll
-            for (int nt = 0; nt < kNT; ++nt) mma_f16(acc[nt][2 * kk + h], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+            for (int nt = 0; nt < kNTw; ++nt) mma_f16(acc[nt][2 * kk + h], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
           }
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->empty[s]);
+      if (mine && lane == 0) mbar_arrive(&ctl->empty[s]);
       if (++s == kStages) {
         s = 0;
         ph ^= 1;
       }
 
       if (cur.i == cur.nb - 1 || j == hi - 1) {
-        // ---- the run leaves this tile: merge the four warps' states. The
-        // warps hold their accumulators in the same lane layout, so a warp
-        // folds another's state in lane by lane: warps 2, 3 into 0, 1, then
-        // warp 1 into warp 0 (a fixed order), and warp 0 stores the result.
+        // ---- the run leaves this tile: fold the warps' states of the same
+        // rows. They have the same lane layout, so a warp folds another's
+        // state in lane by lane: the upper half into the lower, and so on (a
+        // fixed order). In later steps a warp writes the slot it has read.
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
+        for (int nt = 0; nt < kNTw; ++nt)
 #pragma unroll
           for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], o);
         auto put = [&](float* st) {
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) {
+          for (int nt = 0; nt < kNTw; ++nt) {
             float* sn = st + nt * (D / 4 + 4) * 32 + lane;
 #pragma unroll
             for (int mt = 0; mt < D / 16; ++mt)
@@ -613,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto take = [&](const float* st) {
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) {
+          for (int nt = 0; nt < kNTw; ++nt) {
             const float* sn = st + nt * (D / 4 + 4) * 32 + lane;
             float f1[2], f2[2];
 #pragma unroll
@@ -631,65 +687,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                 acc[nt][mt][k] = acc[nt][mt][k] * f1[k & 1] + sn[(4 * mt + k) * 32] * f2[k & 1];
           }
         };
-        float* st1 = mrg + (warp & 1) * S::kStateFloats * 32;  // first-fold slot of warp 2 / warp 3
-        float* st2 = mrg + 2 * S::kStateFloats * 32;           // second-fold slot
-        bool fail = false;
-        if (warp >= 2) {
-          fail = flushes > 0 && !warp_wait(&ctl->mrg_free, (flushes - 1) & 1);
-          if (!fail) {
-            put(st1);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl->mrg_full);
-          }
-        } else {
-          fail = !warp_wait(&ctl->mrg_full, flushes & 1);
-          if (!fail) {
-            take(st1);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl->mrg_free);
-            if (warp == 1) {
-              fail = flushes > 0 && !warp_wait(&ctl->mrg2_free, (flushes - 1) & 1);
-              if (!fail) {
-                put(st2);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->mrg2_full);
-              }
-            } else {
-              fail = !warp_wait(&ctl->mrg2_full, flushes & 1);
-              if (!fail) {
-                take(st2);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->mrg2_free);
-                const size_t slot = (size_t)c + cur.tile;
-                float* pm = p.part + slot * RT;
-                float* pl = p.part + (size_t)p.slots * RT + slot * RT;
-                float* po = p.part + (size_t)2 * p.slots * RT + slot * RT * D;
+        const int idx = S::kRowSplit == 2 ? pw : warp;
+        float* slots = mrg + (S::kRowSplit == 2 ? part : 0) * (S::kFold / 2) * S::kStateFloats * 32;
+        bool ok = together();  // nobody reads the last fold's slots any more
+#pragma unroll 1
+        for (int half = S::kFold / 2; half >= 1; half /= 2) {
+          const int base = half == S::kFold / 2 ? half : 0;  // the first step's writers have no slots of their own
+          if (ok && idx >= half && idx < 2 * half) put(slots + (idx - base) * S::kStateFloats * 32);
+          ok = ok && together();
+          if (ok && idx < half) take(slots + (idx + half - base) * S::kStateFloats * 32);
+        }
+        if (!ok) break;
+        if (idx == 0) {
+          const size_t slot = (size_t)c + cur.tile;
+          float* pm = p.part + slot * RT + rows0;
+          float* pl = p.part + (size_t)p.slots * RT + slot * RT + rows0;
+          float* po = p.part + (size_t)2 * p.slots * RT + (slot * RT + rows0) * D;
 #pragma unroll
-                for (int nt = 0; nt < kNT; ++nt) {
-                  const int r0 = 8 * nt + 2 * m4;
+          for (int nt = 0; nt < kNTw; ++nt) {
+            const int r0 = 8 * nt + 2 * m4;
 #pragma unroll
-                  for (int mt = 0; mt < D / 16; ++mt) {
-                    const int d = 16 * mt + 2 * gq;
-                    *reinterpret_cast<float2*>(po + r0 * D + d) = make_float2(acc[nt][mt][0], acc[nt][mt][2]);
-                    *reinterpret_cast<float2*>(po + (r0 + 1) * D + d) = make_float2(acc[nt][mt][1], acc[nt][mt][3]);
-                  }
-                  if (lane < 4) {
+            for (int mt = 0; mt < D / 16; ++mt) {
+              const int d = 16 * mt + 2 * gq;
+              *reinterpret_cast<float2*>(po + r0 * D + d) = make_float2(acc[nt][mt][0], acc[nt][mt][2]);
+              *reinterpret_cast<float2*>(po + (r0 + 1) * D + d) = make_float2(acc[nt][mt][1], acc[nt][mt][3]);
+            }
+            if (lane < 4) {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                      pm[r0 + k] = m[nt][k];
-                      pl[r0 + k] = l[nt][k];
-                    }
-                  }
-                }
+              for (int k = 0; k < 2; ++k) {
+                pm[r0 + k] = m[nt][k];
+                pl[r0 + k] = l[nt][k];
               }
             }
           }
         }
-        if (fail) break;
-        ++flushes;
         reset();
         cur = nxt;
-        if (j + 1 < hi) load_q();
+        if (j + 1 < hi) good = load_q();
       } else {
         cur = nxt;
       }
@@ -712,157 +746,147 @@ struct MergeParams {
   int B, T, Hq, Hkv, D, L_max, RT, C;
 };
 
-// Thread t holds dims 4(t%16) .. +3 of the block's 64-dim slice and takes the
-// covering grid blocks c0 + t/16, c0 + t/16 + 8, ...: its loads of up to 8
-// partial states are all issued before any is used, then merged with a
-// running maximum; the 8 partial lanes are merged in a fixed order at the end.
-constexpr int kMergeLanes = 8;
-constexpr int kMergeBatch = 8;
+// The block's 8 warps take the covering grid blocks c0 + warp, c0 + 8 + warp,
+// ..., a lane two head dims: every load of up to kMergeBatch states is issued
+// before any is used. Then the 8 are merged in shared memory.
+constexpr int kMergeWarps = 8;
+constexpr int kMergeBatch = 10;  // 8 warps times 10: the 76 states of a pair of two on 152 SMs at once
 
-__global__ void __launch_bounds__(128) kv8_merge_kernel(const MergeParams p) {
+__global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_kernel(const MergeParams p) {
   // The next call's split kernel may launch now: it waits for this grid to
   // finish before it touches the workspace.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // Everything up to the dependency wait reads only the tables, which the
   // split kernel does not write: it overlaps that kernel's tail.
-  const int r = p.Hq / p.Hkv, RT = p.RT;
-  const int slice = blockIdx.y;
-  const int t = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq;
-  const int f = threadIdx.x & 15, pl = threadIdx.x >> 4;
-  const int d = slice * 64 + 4 * f;
+  const int r = p.Hq / p.Hkv, RT = p.RT, C = p.C, D = p.D;
+  const int t = blockIdx.x / p.Hq, h = blockIdx.x - t * p.Hq;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  __shared__ long long s_before[4], s_total[4];
-  __shared__ int s_tiles[4], s_seq, s_first_bad[4];
-  __shared__ float s_m[kMergeLanes], s_l[kMergeLanes];
-  __shared__ float4 s_o[kMergeLanes][16];
+  __shared__ float s_m[kMergeWarps], s_l[kMergeWarps], s_o[kMergeWarps][64];
+  __shared__ int s_first;
+  // every warp: the sequence, and the units and tiles before it
   long long before = 0, total = 0;
-  int tiles = 0;
+  int tiles = 0, b = -1, lo = 0, n = 0, len = 0;
   bool bad = false;
-  for (int bb = threadIdx.x; bb < p.B; bb += blockDim.x) {
-    const int lo = __ldg(p.offsets + bb), hi = __ldg(p.offsets + bb + 1), len = __ldg(p.lens + bb);
-    if (offsets_bad(lo, hi, bb, p.B, p.T) || len < 0 || len > p.L_max) {
-      bad = true;
-      continue;
+  for (int base = 0; base < p.B; base += 32) {
+    const int bb = base + lane;
+    int lo1 = 0, hi1 = 0, len1 = 0, nt = 0;
+    long long v = 0;
+    if (bb < p.B) {
+      lo1 = __ldg(p.offsets + bb);
+      hi1 = __ldg(p.offsets + bb + 1);
+      len1 = __ldg(p.lens + bb);
+      if (offsets_bad(lo1, hi1, bb, p.B, p.T) || len1 < 0 || len1 > p.L_max) {
+        bad = true;
+      } else {
+        v = seq_units(hi1 - lo1, len1, r, RT);
+        nt = seq_tiles(hi1 - lo1, r, RT);
+      }
     }
-    const long long v = seq_units(hi - lo, len, r, RT);
-    total += v;
-    if (hi <= t) {
-      before += v;
-      tiles += seq_tiles(hi - lo, r, RT);
-    } else if (lo <= t) {
-      s_seq = bb;
-    }
-  }
+    const unsigned hit = __ballot_sync(0xffffffffu, lo1 <= t && t < hi1);
+    long long vb = hi1 <= t ? v : 0;
+    int tb = hi1 <= t ? nt : 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-    tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+    for (int o = 16; o > 0; o >>= 1) {
+      v += __shfl_xor_sync(0xffffffffu, v, o);
+      vb += __shfl_xor_sync(0xffffffffu, vb, o);
+      tb += __shfl_xor_sync(0xffffffffu, tb, o);
+    }
+    total += v;
+    before += vb;
+    tiles += tb;
+    if (hit) {
+      const int L = __ffs(hit) - 1;
+      b = base + L;
+      lo = __shfl_sync(0xffffffffu, lo1, L);
+      n = __shfl_sync(0xffffffffu, hi1 - lo1, L);
+      len = __shfl_sync(0xffffffffu, len1, L);
+    }
   }
-  if (lane == 0) {
-    s_before[warp] = before;
-    s_total[warp] = total;
-    s_tiles[warp] = tiles;
-  }
-  bad = __syncthreads_or(bad);
-  int c0 = 0, c1 = -1, slot0 = 0;
-  long long N = 1;
-  const int C = p.C;
-  if (!bad) {
-    before = s_before[0] + s_before[1] + s_before[2] + s_before[3];
-    total = s_total[0] + s_total[1] + s_total[2] + s_total[3];
-    tiles = s_tiles[0] + s_tiles[1] + s_tiles[2] + s_tiles[3];
-    const int b = s_seq, lo = __ldg(p.offsets + b), n = __ldg(p.offsets + b + 1) - lo, len = __ldg(p.lens + b);
-    const int g = h / r, row = (t - lo) * r + h % r, rt = row / RT;
-    const int nb = tile_units(n, len, r, RT, kPos, rt);
-    N = total * p.Hkv;
+  bad = __any_sync(0xffffffffu, bad);
+  int c0 = 0, c1 = -1;
+  size_t slot0 = 0;
+  if (!bad && b >= 0) {
+    const int g = h / r, row = (t - lo) * r + h - g * r, rt = row / RT, nb = tile_units(n, len, r, RT, kPos, rt);
+    const Runs runs(total * p.Hkv, C);
     const long long start = before * p.Hkv + seq_units(n, len, r, RT) * g + units_before(n, len, r, RT, kPos, rt);
-    slot0 = (tiles * p.Hkv + g * seq_tiles(n, r, RT) + rt) * RT + row % RT;
+    slot0 = ((size_t)tiles * p.Hkv + (size_t)g * seq_tiles(n, r, RT) + rt) * RT + row - rt * RT;
     if (nb > 0 && len - n + (t - lo) >= 0) {
-      c0 = cta_of(start, N, C);
-      c1 = cta_of(start + nb - 1, N, C);
+      c0 = runs.of(start);
+      c1 = runs.of(start + nb - 1);
     }
   }
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (blockIdx.x == 0 && blockIdx.y == 0) {
     // the call's status: the outcome of the lowest-numbered grid block that failed
-    int first = 0x7fffffff;
-    for (int cc = threadIdx.x; cc < C; cc += blockDim.x)
-      if (__ldcg(p.flags + cc) != 0) first = min(first, cc);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
-    if (lane == 0) s_first_bad[warp] = first;
+    if (threadIdx.x == 0) s_first = C;
     __syncthreads();
-    if (threadIdx.x == 0) {
-      first = min(min(s_first_bad[0], s_first_bad[1]), min(s_first_bad[2], s_first_bad[3]));
-      *p.status = first == 0x7fffffff ? 0 : __ldcg(p.flags + first);
-    }
+    for (int cc = threadIdx.x; cc < C; cc += kMergeWarps * 32)
+      if (__ldcg(p.flags + cc) != 0) atomicMin(&s_first, cc);
+    __syncthreads();
+    if (threadIdx.x == 0) *p.status = s_first == C ? 0 : __ldcg(p.flags + s_first);
   }
   if (bad) return;
-  uint2* out = reinterpret_cast<uint2*>(p.o + ((size_t)t * p.Hq + h) * p.D + d);
-  if (c1 < c0) {  // no visible position
-    if (pl == 0) *out = make_uint2(0u, 0u);
-    return;
-  }
 
   const float* pm = p.part;
-  const float* pl_ = p.part + (size_t)p.slots * RT;
-  const float* po = p.part + (size_t)2 * p.slots * RT;
-  float M = kMinusBig, L = 0.f;
-  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float* pl = p.part + (size_t)p.slots * RT;
+  const float* po = p.part + (size_t)2 * p.slots * RT + blockIdx.y * 64 + 2 * lane;
+  float M = kMinusBig, L = 0.f, Ox = 0.f, Oy = 0.f;
   int failed = 0;
-  for (int base = c0 + pl; base <= c1; base += kMergeLanes * kMergeBatch) {
+#pragma unroll 1
+  for (int base = c0 + warp; base <= c1; base += kMergeWarps * kMergeBatch) {
     float mc[kMergeBatch], lc[kMergeBatch];
-    float4 oc[kMergeBatch];
+    float2 oc[kMergeBatch];
 #pragma unroll
     for (int u = 0; u < kMergeBatch; ++u) {
-      const int cc = base + u * kMergeLanes;
-      // with fewer units than grid blocks some runs are empty (no slot written)
-      const bool live = cc <= c1 && (long long)cc * N / C != (long long)(cc + 1) * N / C;
-      const size_t at = (size_t)(live ? cc : c0) * RT + slot0;
-      failed |= live ? __ldcg(p.flags + cc) : 0;
-      mc[u] = live ? __ldcg(pm + at) : kMinusBig;
-      lc[u] = live ? __ldcg(pl_ + at) : 0.f;
-      oc[u] = live ? __ldcg(reinterpret_cast<const float4*>(po + at * p.D + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const int cc = base + u * kMergeWarps;
+      mc[u] = kMinusBig;
+      lc[u] = 0.f;
+      oc[u] = make_float2(0.f, 0.f);
+      if (cc <= c1) {
+        const size_t at = (size_t)cc * RT + slot0;
+        failed |= __ldcg(p.flags + cc);
+        mc[u] = __ldcg(pm + at);
+        lc[u] = __ldcg(pl + at);
+        oc[u] = __ldcg(reinterpret_cast<const float2*>(po + at * D));
+      }
     }
+    float nm = M;
+#pragma unroll
+    for (int u = 0; u < kMergeBatch; ++u) nm = fmaxf(nm, mc[u]);
+    const float f = exp2f(M - nm);
+    L *= f;
+    Ox *= f;
+    Oy *= f;
+    M = nm;
 #pragma unroll
     for (int u = 0; u < kMergeBatch; ++u) {
-      const float nm = fmaxf(M, mc[u]);
-      const float fo = exp2f(M - nm), fc = exp2f(mc[u] - nm);
-      O.x = O.x * fo + oc[u].x * fc;
-      O.y = O.y * fo + oc[u].y * fc;
-      O.z = O.z * fo + oc[u].z * fc;
-      O.w = O.w * fo + oc[u].w * fc;
-      L = L * fo + lc[u] * fc;
-      M = nm;
+      const float e = exp2f(mc[u] - M);
+      L = fmaf(lc[u], e, L);
+      Ox = fmaf(oc[u].x, e, Ox);
+      Oy = fmaf(oc[u].y, e, Oy);
     }
   }
-  if (f == 0) {
-    s_m[pl] = M;
-    s_l[pl] = L;
+  s_o[warp][2 * lane] = Ox;
+  s_o[warp][2 * lane + 1] = Oy;
+  if (lane == 0) {
+    s_m[warp] = M;
+    s_l[warp] = L;
   }
-  s_o[pl][f] = O;
   if (__syncthreads_or(failed)) return;  // a covering grid block gave up: o is left as it was
-  if (pl == 0) {
-    float Mt = kMinusBig;
+  if (threadIdx.x < 64) {
+    float Mt = kMinusBig, Lt = 0.f, Ot = 0.f;
 #pragma unroll
-    for (int w = 0; w < kMergeLanes; ++w) Mt = fmaxf(Mt, s_m[w]);
-    float Lt = 0.f;
-    float4 Ot = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = 0; w < kMergeWarps; ++w) Mt = fmaxf(Mt, s_m[w]);
 #pragma unroll
-    for (int w = 0; w < kMergeLanes; ++w) {
+    for (int w = 0; w < kMergeWarps; ++w) {
       const float e = exp2f(s_m[w] - Mt);
-      Lt += e * s_l[w];
-      Ot.x += e * s_o[w][f].x;
-      Ot.y += e * s_o[w][f].y;
-      Ot.z += e * s_o[w][f].z;
-      Ot.w += e * s_o[w][f].w;
+      Lt = fmaf(e, s_l[w], Lt);
+      Ot = fmaf(e, s_o[w][threadIdx.x], Ot);
     }
-    const float inv = 1.f / Lt;
-    const __nv_bfloat162 a = __floats2bfloat162_rn(Ot.x * inv, Ot.y * inv);
-    const __nv_bfloat162 b = __floats2bfloat162_rn(Ot.z * inv, Ot.w * inv);
-    *out = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    // c1 < c0: no visible position
+    p.o[((size_t)t * p.Hq + h) * D + blockIdx.y * 64 + threadIdx.x] =
+        __bfloat16_as_ushort(__float2bfloat16_rn(c1 < c0 ? 0.f : Ot / Lt));
   }
 }
 
@@ -896,7 +920,7 @@ cudaError_t codes_map(CUtensorMap* m, const void* base, int D, int L_max, int pa
 }
 
 // Groups of 8 rows per tile: as many as the average sequence's rows fill, up
-// to what the accumulators of D head dims leave registers for (a wider tile
+// to what two warps have registers for (a wider tile
 // reads the cache fewer times, a narrower one holds fewer idle rows).
 int groups(int B, int T, int r, int D) {
   const long long rows = (long long)((T + B - 1) / B) * r;
@@ -913,12 +937,12 @@ long long max_tiles(int B, int T, int r, int Hkv, int RT) {
 template <int D, int kNT, bool kE4m3>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const Params& prm, int grid, cudaStream_t stream) {
   static SmemLimitMemo smem_memo;
-  cudaError_t e = ensure_smem(kv8_split_kernel<D, kNT, kE4m3>, Smem<D, kNT>::kBytes, &smem_memo);
+  cudaError_t e = ensure_smem(kv8_split_kernel<D, kNT, kE4m3>, Cfg<D, kNT>::kBytes, &smem_memo);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Smem<D, kNT>::kBytes;
+  cfg.dynamicSmemBytes = Cfg<D, kNT>::kBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -976,7 +1000,7 @@ moe_status launch_split(const AttnArgs& a, cudaStream_t stream) {
   const MergeParams mp{a.offsets, a.lens, part, flags, a.o, status, slots, a.B, a.T, a.Hq, a.Hkv, a.D, a.L_max, RT, grid};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.T * (unsigned)a.Hq, (unsigned)(a.D / 64));
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

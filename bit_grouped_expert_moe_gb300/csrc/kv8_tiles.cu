@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
     }
     bad = __any_sync(0xffffffffu, bad);
     total *= p.Hkv;
-    const long long at = (long long)(c + warp - 1) * total / C;
+    const long long at = Runs(total, C).start(c + warp - 1);
     Cursor k{};
     long long before = 0;  // units before the place
     if (!bad) {
@@ -1026,23 +1026,22 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_tiles_merge_kernel(const Me
   const RunInfo f = p.info[c];
   if (!f.live || f.i == 0) return;
   const long long N = f.places, start = f.lo - f.i;  // the place of the tile's first unit
-  const int c0 = cta_of(start, N, C);
-  if (c != cta_of((long long)(c0 + 1) * N / C, N, C)) return;  // a later one of the tile's runs
-  const int c1 = cta_of(start + f.nb - 1, N, C);
+  const Runs runs(N, C);
+  const int c0 = runs.of(start);
+  if (c != c0 + 1) return;             // a later one of the tile's runs
+  const int c1 = runs.of(start + f.nb - 1);
   const int r = p.Hq / p.Hkv, D = p.D, row = blockIdx.y * kMergeRows + (t >> 5);
   const int lo = __ldg(p.offsets + f.b), n = __ldg(p.offsets + f.b + 1) - lo, len = __ldg(p.lens + f.b);
   const int rho = f.rt * kRows + row, tok = rho / r;
   if (rho >= n * r || len - n + tok < 0) return;
-  auto live = [&](int cc) { return cc <= c1 && (long long)cc * N / C != (long long)(cc + 1) * N / C; };  // not empty
   auto slot = [&](int cc) { return p.part + (size_t)(2 * cc + (cc == c0 ? 1 : 0)) * slot_floats(D); };
   // lane k weighs the states of runs c0 + k, c0 + 32 + k, ...
   float M = kMinusBig;
   bool failed = false;
-  for (int cc = c0 + lane; cc <= c1; cc += 32)
-    if (live(cc)) {
-      failed |= __ldcg(p.flags + cc) != 0;
-      M = fmaxf(M, __ldcg(slot(cc) + (size_t)D * kRows + row));
-    }
+  for (int cc = c0 + lane; cc <= c1; cc += 32) {
+    failed |= __ldcg(p.flags + cc) != 0;
+    M = fmaxf(M, __ldcg(slot(cc) + (size_t)D * kRows + row));
+  }
   if (__any_sync(0xffffffffu, failed)) return;  // a run gave up: o is left as it was
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -1052,14 +1051,13 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_tiles_merge_kernel(const Me
   const int per = D / 32;
   for (int base = c0; base <= c1; base += 32) {
     const int mine = base + lane;
-    const float e = live(mine) ? exp2f(__ldcg(slot(mine) + (size_t)D * kRows + row) - M) : 0.f;
-    float l = live(mine) ? e * __ldcg(slot(mine) + (size_t)(D + 1) * kRows + row) : 0.f;
+    const float e = mine <= c1 ? exp2f(__ldcg(slot(mine) + (size_t)D * kRows + row) - M) : 0.f;
+    float l = mine <= c1 ? e * __ldcg(slot(mine) + (size_t)(D + 1) * kRows + row) : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     L += l;
     for (int cc = base; cc <= min(c1, base + 31); ++cc) {
       const float w = __shfl_sync(0xffffffffu, e, cc - base);
-      if (!live(cc)) continue;
       const float* o = slot(cc) + (size_t)row * D + lane * per;
 #pragma unroll
       for (int i = 0; i < 8; i += 2)
