@@ -4,7 +4,7 @@
 // one conversion, so they are bound by memory, and at a decode step's sizes
 // by the latency of one dependent chain (tables, values, scale, codes).
 #include "kernels.h"
-#include "kv8.cuh"
+#include "kv8_attn.h"
 
 #include <type_traits>
 
@@ -12,7 +12,8 @@ namespace bgmoe {
 namespace kv8 {
 
 constexpr int kThreads = 256;
-constexpr int kReadTokens = 64;  // packed tokens per block of the read kernel
+constexpr int kReadTokens = 64;  // packed tokens per tile of the read kernel
+constexpr int kReadBlocks = 6;   // its thread blocks per SM, at most
 
 struct CacheArgs {
   uint8_t* codes[2];    // K, V
@@ -44,92 +45,108 @@ __device__ __forceinline__ bool tables_bad(const CacheArgs& p, Hit hit) {
   return __syncthreads_or(bad) != 0;
 }
 
-// One thread block per (touched cache block, KV head, K or V). Sequence b's
-// touched blocks are units floor(offsets[b] / kBlock) + 2 b + 0, 1, ...: n
+// A unit of work is one touched cache block of one KV head, K or V. Sequence b's
+// touched blocks are numbered floor(offsets[b] / kBlock) + 2 b + 0, 1, ...: n
 // tokens touch at most floor(n / kBlock) + 2 blocks, which is what the next
-// sequence's first unit leaves room for, so no prefix sum is needed and the
-// grid is floor(T / kBlock) + 2 B (units that touch nothing return).
+// sequence's first number leaves room for, so no prefix sum is needed and there
+// are floor(T / kBlock) + 2 B numbers (some of them touch nothing).
 //
-// The block's new values stay in registers between the maximum and the codes
-// (64 x 256 bf16 over 256 threads: 8 16-byte pieces each), so they are read
-// once, all loads in flight together.
+// A unit has 64 values per thread, kPer 16-byte pieces, which stay in registers
+// between the maximum and the codes, so they are read once, with all loads in
+// flight together: a warp for a block of 16 x 64 values, the whole thread block
+// of 256 for one of 64 x 256.
+template <int D, int kBlock>
+struct WriteCfg {
+  static constexpr int kUnitThreads = kBlock * D / 64 < 32 ? 32 : kBlock * D / 64;
+  static constexpr int kUnits = kThreads / kUnitThreads;              // units of a thread block
+  static constexpr int kPer = kBlock * D / 8 / kUnitThreads;          // pieces of a thread
+};
+
 template <int D, int kBlock, bool kE4m3>
-__global__ void __launch_bounds__(kThreads) kv8_write_kernel(const CacheArgs p) {
-  constexpr int kPieces = kBlock * D / 8;             // 16-byte pieces (8 values) of a full block
-  constexpr int kPer = (kPieces + kThreads - 1) / kThreads;
-  __shared__ int s_b, s_lo, s_n, s_start;
-  __shared__ uint32_t s_max[kThreads / 32];
-  const int unit = blockIdx.x, g = blockIdx.y, kv = blockIdx.z;
-  if (threadIdx.x == 0) s_b = -1;
+__global__ void __launch_bounds__(kThreads, 2) kv8_write_kernel(const CacheArgs p) {
+  using W = WriteCfg<D, kBlock>;
+  constexpr int kPer = W::kPer, kTU = W::kUnitThreads;
+  __shared__ int s_b[W::kUnits], s_lo[W::kUnits], s_n[W::kUnits], s_start[W::kUnits];
+  __shared__ uint32_t s_max[2][kThreads / 32];
+  // units in the order (number, head, K or V)
+  const int per = 2 * p.Hkv, first = blockIdx.x * W::kUnits, local = threadIdx.x / kTU, tu = threadIdx.x % kTU;
+  const int item = first + local, unit = item / per, g = (item - unit * per) >> 1, kv = item & 1;
+  if (threadIdx.x < W::kUnits) s_b[threadIdx.x] = -1;
   __syncthreads();
   const bool bad = tables_bad(p, [&](int b, int lo, int hi, int start) {
     const int u0 = lo / kBlock + 2 * b, u1 = hi / kBlock + 2 * (b + 1);
-    if (unit >= u0 && unit < u1) {
-      s_b = b;
-      s_lo = lo;
-      s_n = hi - lo;
-      s_start = start;
+    if (u1 <= first / per || u0 > (first + W::kUnits - 1) / per) return;
+    for (int k = 0; k < W::kUnits; ++k) {
+      const int u = (first + k) / per;
+      if (u >= u0 && u < u1) {
+        s_b[k] = b;
+        s_lo[k] = lo;
+        s_n[k] = hi - lo;
+        s_start[k] = start;
+      }
     }
   });
   if (bad) {
     if (threadIdx.x == 0) flag(p.status, (int32_t)MOE_ERR_INVALID_ARG);
     return;
   }
-  const int b = s_b;
-  if (b < 0) return;
-  const int n = s_n, start = s_start;
-  const int blk = start / kBlock + (unit - (s_lo / kBlock + 2 * b));
+  const int b = s_b[local];
+  const int n = b < 0 ? 0 : s_n[local], start = b < 0 ? 0 : s_start[local], lo = b < 0 ? 0 : s_lo[local];
+  const int blk = start / kBlock + (unit - (lo / kBlock + 2 * b));
   const int base = blk * kBlock;                       // the cache block's first position
   const int p0 = max(start, base), p1 = min(start + n, base + kBlock);  // its new positions
-  if (n == 0 || p0 >= p1) return;
+  // The threads of a unit share everything up to here, so a unit without new
+  // positions takes no part in the others' barriers.
+  if (b < 0 || n == 0 || p0 >= p1) return;
   const size_t pair = (size_t)b * p.Hkv + g;
-  uint8_t* codes = p.codes[kv] + (pair * p.L_max + base) * D;
-  float* scale = p.scales[kv] + pair * p.nblk + blk;
-  const float s_old = p0 > base ? *scale : 0.f;
-  const uint16_t* x = p.x[kv] + (size_t)g * D;
+  uint8_t* codes = (kv ? p.codes[1] : p.codes[0]) + (pair * p.L_max + base) * D;
+  float* scale = (kv ? p.scales[1] : p.scales[0]) + pair * p.nblk + blk;
   const int r0 = p0 - base, r1 = p1 - base;            // rows of the block
-  const int t0 = s_lo + (p0 - start);                  // the packed token of row r0
+  const uint16_t* x = (kv ? p.x[1] : p.x[0]) + (size_t)(lo + (p0 - start)) * p.stride + (size_t)g * D;  // of row r0
 
   uint4 v[kPer];
   uint32_t mx = 0;  // largest magnitude bits, two bf16 side by side
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int piece = threadIdx.x + i * kThreads;      // piece of the new rows, from row r0
+    const int piece = tu + i * kTU;                    // piece of the new rows, from row r0
     const int row = piece / (D / 8), c = piece % (D / 8);
     v[i] = make_uint4(0, 0, 0, 0);
-    if (row < r1 - r0) v[i] = ldg_nc_v4(x + (size_t)(t0 + row) * p.stride + c * 8);
+    if (row < r1 - r0) v[i] = ldg_nc_v4(x + (size_t)row * p.stride + c * 8);
   }
+  const float s_old = p0 > base ? *scale : 0.f;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) mx = __vmaxu2(mx, w[j] & 0x7FFF7FFFu);
   }
-  auto block_max = [&](uint32_t m2) -> uint32_t {      // over both halves and all threads
-    uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
-    m = __reduce_max_sync(0xffffffffu, m);
-    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
-    __syncthreads();
+  // Over both halves and all threads of the unit; a barrier of the unit's own
+  // (its threads have all read s_old when it is passed).
+  auto unit_max = [&](uint32_t m2, int turn) -> uint32_t {
+    uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16));
+    if (kTU > 32) {
+      if ((threadIdx.x & 31) == 0) s_max[turn][threadIdx.x >> 5] = m;
+      asm volatile("bar.sync %0, %1;" ::"r"(local + 1), "n"(kTU) : "memory");
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) m = max(m, s_max[w]);
+      for (int w = 0; w < kTU / 32; ++w) m = max(m, s_max[turn][local * (kTU / 32) + w]);
+    }
     return m;
   };
-  uint32_t m = block_max(mx);
+  uint32_t m = unit_max(mx, 0);
   if (m >= 0x7F80u) {  // an infinity or a NaN: the maximum again over finite values, then replace them
-    if (threadIdx.x == 0) flag(p.status, (int32_t)MOE_ERR_RANGE);
-    __syncthreads();   // s_max is read above
+    if (tu == 0) flag(p.status, (int32_t)MOE_ERR_RANGE);
     mx = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t lo = w[j] & 0x7FFFu, hi = (w[j] >> 16) & 0x7FFFu;
-        if (lo < 0x7F80u) mx = max(mx & 0xFFFFu, lo) | (mx & 0xFFFF0000u);
-        if (hi < 0x7F80u) mx = max(mx >> 16, hi) << 16 | (mx & 0xFFFFu);
+        const uint32_t a = w[j] & 0x7FFFu, z = (w[j] >> 16) & 0x7FFFu;
+        if (a < 0x7F80u) mx = max(mx & 0xFFFFu, a) | (mx & 0xFFFF0000u);
+        if (z < 0x7F80u) mx = max(mx >> 16, z) << 16 | (mx & 0xFFFFu);
       }
     }
-    m = block_max(mx);
+    m = unit_max(mx, 1);
     auto finite = [&](uint32_t h) -> uint32_t {        // one bf16
       const uint32_t a = h & 0x7FFFu;
       return a < 0x7F80u ? h : a == 0x7F80u ? (h & 0x8000u) | m : 0u;
@@ -145,7 +162,7 @@ __global__ void __launch_bounds__(kThreads) kv8_write_kernel(const CacheArgs p) 
   const float s_new = fmaxf(s_old, scale_of<kE4m3>(__uint_as_float(m << 16)));
   const float inv = inverse_scale(s_new);
   if (p0 > base && s_new > s_old) {  // the block's earlier codes, to the larger scale
-    for (int piece = threadIdx.x; piece < r0 * (D / 4); piece += kThreads) {
+    for (int piece = tu; piece < r0 * (D / 4); piece += kTU) {
       uint32_t* w = reinterpret_cast<uint32_t*>(codes) + piece;
       float f[4];
       decode4<kE4m3>(*w, f);
@@ -157,10 +174,11 @@ __global__ void __launch_bounds__(kThreads) kv8_write_kernel(const CacheArgs p) 
       *w = encode4<kE4m3>(f[0], f[1], f[2], f[3]);
     }
   }
-  if (threadIdx.x == 0 && (p0 == base || s_new != s_old)) *scale = s_new;
+  if (kTU == 32) __syncwarp();  // s_old has been read by all
+  if (tu == 0 && (p0 == base || s_new != s_old)) *scale = s_new;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int piece = threadIdx.x + i * kThreads;
+    const int piece = tu + i * kTU;
     const int row = piece / (D / 8), c = piece % (D / 8);
     if (row >= r1 - r0) continue;
     const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
@@ -175,59 +193,83 @@ __global__ void __launch_bounds__(kThreads) kv8_write_kernel(const CacheArgs p) 
   }
 }
 
-// One thread block per (64 packed tokens, KV head, K or V): the sequence of
-// every token is found first, then each thread turns 8-byte pieces of codes
-// into 16-byte pieces of bf16, so a warp reads and writes whole lines.
+// Thread blocks walk over tiles of 64 packed tokens of one KV head, K or V. The
+// tables are checked once; a tile's tokens find their sequence and position
+// (by bisection of the offsets), then each thread turns 16-byte pieces of
+// codes into 32 bytes of bf16. The next tile's codes are asked for before
+// this one's are converted.
 template <int D, int kBlock, bool kE4m3>
 __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const CacheArgs p) {
-  __shared__ int s_row[kReadTokens], s_seq[kReadTokens];  // cache position and sequence of each token
-  const int t0 = blockIdx.x * kReadTokens, g = blockIdx.y, kv = blockIdx.z;
-  const int nt = min(kReadTokens, p.T - t0);
-  const bool bad = tables_bad(p, [&](int b, int lo, int hi, int start) {
-    const int a = max(lo, t0), z = min(hi, t0 + nt);
-    for (int t = a; t < z; ++t) {
-      s_row[t - t0] = start + (t - lo);
-      s_seq[t - t0] = b;
-    }
-  });
-  if (bad) {
+  constexpr int kRow = D / 16;                          // pieces per token
+  constexpr int kPer = kReadTokens * kRow / kThreads;   // pieces per thread
+  __shared__ long long s_code[2][kReadTokens];          // first code of each token (head g), in bytes
+  __shared__ long long s_scale[2][kReadTokens];         // its scale
+  if (tables_bad(p, [](int, int, int, int) {})) {
     if (threadIdx.x == 0) flag(p.status, (int32_t)MOE_ERR_INVALID_ARG);
     return;
   }
-  constexpr int kRow = D / 8;                           // pieces per token
-  constexpr int kPer = kReadTokens * kRow / kThreads;
-  const uint8_t* codes = p.codes[kv];
-  const float* scales = p.scales[kv];
-  uint2 w[kPer];
+  const int per = 2 * p.Hkv, tiles = (p.T + kReadTokens - 1) / kReadTokens * per;
+  auto find = [&](int tile, int buf) {                  // by the first 64 threads
+    const int t = tile / per * kReadTokens + threadIdx.x, g = (tile % per) >> 1;
+    if (threadIdx.x >= kReadTokens || t >= p.T) return;
+    int b = 0, z = p.B;                                 // the last sequence that starts at or before t
+    while (z - b > 1) {
+      const int mid = (b + z) >> 1;
+      if (__ldg(p.offsets + mid) <= t) b = mid;
+      else z = mid;
+    }
+    const int pos = __ldg(p.starts + b) + t - __ldg(p.offsets + b);
+    const long long pair = (long long)b * p.Hkv + g;
+    s_code[buf][threadIdx.x] = (pair * p.L_max + pos) * D;
+    s_scale[buf][threadIdx.x] = pair * p.nblk + pos / kBlock;
+  };
+  uint4 w[kPer];
   float s[kPer];
+  auto load = [&](int tile, int buf) {
+    const int nt = min(kReadTokens, p.T - tile / per * kReadTokens);
+    const uint8_t* codes = tile & 1 ? p.codes[1] : p.codes[0];
+    const float* scales = tile & 1 ? p.scales[1] : p.scales[0];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int piece = threadIdx.x + i * kThreads, t = piece / kRow, c = piece % kRow;
-    w[i] = make_uint2(0, 0);
-    s[i] = 0.f;
-    if (t < nt) {
-      const size_t pair = (size_t)s_seq[t] * p.Hkv + g;
-      const int pos = s_row[t];
-      w[i] = __ldcs(reinterpret_cast<const uint2*>(codes + (pair * p.L_max + pos) * D + c * 8));
-      s[i] = __ldg(scales + pair * p.nblk + pos / kBlock);
+    for (int i = 0; i < kPer; ++i) {
+      const int piece = threadIdx.x + i * kThreads, t = piece / kRow, c = piece % kRow;
+      w[i] = make_uint4(0, 0, 0, 0);
+      s[i] = 0.f;
+      if (t < nt) {
+        w[i] = __ldcs(reinterpret_cast<const uint4*>(codes + s_code[buf][t] + c * 16));
+        s[i] = __ldg(scales + s_scale[buf][t]);
+      }
     }
-  }
+  };
+  int tile = blockIdx.x, buf = 0;
+  if (tile >= tiles) return;
+  find(tile, 0);
+  __syncthreads();
+  load(tile, 0);
+  for (; tile < tiles; tile += gridDim.x, buf ^= 1) {
+    const int next = tile + gridDim.x, t0 = tile / per * kReadTokens, g = (tile % per) >> 1;
+    uint16_t* out = tile & 1 ? p.out[1] : p.out[0];
+    if (next < tiles) find(next, buf ^ 1);
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int piece = threadIdx.x + i * kThreads, t = piece / kRow, c = piece % kRow;
-    if (t >= nt) continue;
-    uint32_t o[4];
+    for (int i = 0; i < kPer; ++i) {
+      const int piece = threadIdx.x + i * kThreads, t = piece / kRow, c = piece % kRow;
+      if (t0 + t >= p.T) continue;
+      const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+      uint32_t o[8];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float f[4];
-      decode4<kE4m3>(j ? w[i].y : w[i].x, f);
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(f[0] * s[i], f[1] * s[i]);
-      const __nv_bfloat162 hi = __floats2bfloat162_rn(f[2] * s[i], f[3] * s[i]);
-      o[2 * j] = *reinterpret_cast<const uint32_t*>(&lo);
-      o[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&hi);
+      for (int j = 0; j < 4; ++j) {
+        float f[4];
+        decode4<kE4m3>(in[j], f);
+        const __nv_bfloat162 a = __floats2bfloat162_rn(f[0] * s[i], f[1] * s[i]);
+        const __nv_bfloat162 z = __floats2bfloat162_rn(f[2] * s[i], f[3] * s[i]);
+        o[2 * j] = *reinterpret_cast<const uint32_t*>(&a);
+        o[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&z);
+      }
+      uint4* to = reinterpret_cast<uint4*>(out + ((size_t)(t0 + t) * p.Hkv + g) * D + c * 16);
+      __stcs(to, make_uint4(o[0], o[1], o[2], o[3]));
+      __stcs(to + 1, make_uint4(o[4], o[5], o[6], o[7]));
     }
-    __stcs(reinterpret_cast<uint4*>(p.out[kv] + ((size_t)(t0 + t) * p.Hkv + g) * D + c * 8),
-           make_uint4(o[0], o[1], o[2], o[3]));
+    if (next < tiles) load(next, buf ^ 1);
   }
 }
 
@@ -235,7 +277,7 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const CacheArgs p) {
 
 bool shape_ok(const moe_kv8_shape& s) {
   if (s.B < 1 || s.B > 4096 || s.T < 0 || s.T > (1 << 24)) return false;
-  if (s.Hkv < 1 || s.Hkv > 4096 || s.Hq < 1 || s.Hq % s.Hkv != 0) return false;
+  if (s.Hkv < 1 || s.Hkv > 4096 || s.Hq < 1 || s.Hq % s.Hkv != 0 || (long long)s.T * s.Hkv > (1 << 30)) return false;
   if (s.Hq / s.Hkv > 64 || (long long)s.B * s.Hkv > 65536) return false;
   if (s.D != 64 && s.D != 128 && s.D != 256) return false;
   if (s.L_max < 1 || s.L_max > (1 << 26) || (s.block != 16 && s.block != 32 && s.block != 64)) return false;
@@ -253,20 +295,24 @@ bool cache_ok(const moe_kv8_cache* c) {
 
 namespace {
 
-template <int D, bool kE4m3>
-void launch_write(const CacheArgs& p, int block, cudaStream_t s) {
-  const dim3 grid((unsigned)(p.T / block + 2 * p.B), (unsigned)p.Hkv, 2u);
-  if (block == 16) kv8_write_kernel<D, 16, kE4m3><<<grid, kThreads, 0, s>>>(p);
-  else if (block == 32) kv8_write_kernel<D, 32, kE4m3><<<grid, kThreads, 0, s>>>(p);
-  else kv8_write_kernel<D, 64, kE4m3><<<grid, kThreads, 0, s>>>(p);
+template <int D, int kBlock, bool kE4m3>
+void launch_one(const CacheArgs& p, bool write, int sms, cudaStream_t s) {
+  if (write) {
+    const long long items = ((long long)p.T / kBlock + 2 * p.B) * 2 * p.Hkv;
+    constexpr int kUnits = WriteCfg<D, kBlock>::kUnits;
+    kv8_write_kernel<D, kBlock, kE4m3><<<(unsigned)((items + kUnits - 1) / kUnits), kThreads, 0, s>>>(p);
+  } else {
+    const long long tiles = (long long)((p.T + kReadTokens - 1) / kReadTokens) * 2 * p.Hkv;
+    const long long most = (long long)sms * kReadBlocks;
+    kv8_read_kernel<D, kBlock, kE4m3><<<(unsigned)(tiles < most ? tiles : most), kThreads, 0, s>>>(p);
+  }
 }
 
 template <int D, bool kE4m3>
-void launch_read(const CacheArgs& p, int block, cudaStream_t s) {
-  const dim3 grid((unsigned)((p.T + kReadTokens - 1) / kReadTokens), (unsigned)p.Hkv, 2u);
-  if (block == 16) kv8_read_kernel<D, 16, kE4m3><<<grid, kThreads, 0, s>>>(p);
-  else if (block == 32) kv8_read_kernel<D, 32, kE4m3><<<grid, kThreads, 0, s>>>(p);
-  else kv8_read_kernel<D, 64, kE4m3><<<grid, kThreads, 0, s>>>(p);
+void launch_block(const CacheArgs& p, bool write, int block, int sms, cudaStream_t s) {
+  if (block == 16) launch_one<D, 16, kE4m3>(p, write, sms, s);
+  else if (block == 32) launch_one<D, 32, kE4m3>(p, write, sms, s);
+  else launch_one<D, 64, kE4m3>(p, write, sms, s);
 }
 
 moe_status cache_call(const moe_kv8_shape* shape, const moe_kv8_cache* cache, const int32_t* offsets,
@@ -302,10 +348,12 @@ moe_status cache_call(const moe_kv8_shape* shape, const moe_kv8_cache* cache, co
   p.stride = s.kv_stride ? s.kv_stride : s.Hkv * s.D;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool e4m3 = s.format == MOE_KV8_E4M3;
+  const int sms = sm_count();
+  if (sms <= 0) return cuda_fail(cudaErrorInvalidDevice, "device query");
   auto go = [&](auto d) {
     constexpr int D = decltype(d)::value;
-    if (write) e4m3 ? launch_write<D, true>(p, s.block, st) : launch_write<D, false>(p, s.block, st);
-    else e4m3 ? launch_read<D, true>(p, s.block, st) : launch_read<D, false>(p, s.block, st);
+    if (e4m3) launch_block<D, true>(p, write, s.block, sms, st);
+    else launch_block<D, false>(p, write, s.block, sms, st);
   };
   if (s.D == 64) go(std::integral_constant<int, 64>{});
   else if (s.D == 128) go(std::integral_constant<int, 128>{});

@@ -4,13 +4,13 @@
 // What bounds it is the cache's bytes: every position is read once per
 // (sequence, KV head, row tile), where a row tile is 8 kNT rows and a row one
 // (query token, query head of the KV head). The positions a tile can see are
-// cut into units of 64 and all units of the call are laid end to end in the
+// cut into units of 64 (D = 256) or 128 and all units of the call are laid end to end in the
 // order (sequence, KV head, row tile, position) and dealt out in equal
 // contiguous runs, one per block of a one-block-per-SM grid, so the bytes
 // spread evenly over the SMs whatever the lengths are.
 //
-// kv8_split_kernel — warp 8 streams each unit's K and V codes (64 x D bytes
-// each) into a shared-memory ring by TMA. Four warps take 16 positions each;
+// kv8_split_kernel — warp 8 streams each unit's K and V codes into a
+// shared-memory ring by TMA. Four warps take 16 or 32 positions each;
 // the other four take every second unit, or, where 8 kNT rows by D head dims
 // are more than a warp's registers hold, the other half of the rows:
 //   S^T  = K Q^T     mma.sync m16n8k16 in fp16: M = 16 positions, N = 8 rows;
@@ -31,9 +31,9 @@
 //
 // Scales: a warp's 16 positions lie in one cache block. K's scale multiplies
 // the score. V's scale is folded into the softmax weight: with
-//   x_j = score_j + log2 s_v(j),  w_j = 2^(x_j - m + 14),  m = max x,
-// O = sum w_j code_j and L = sum w_j / s_v(j) give o = O / L. w <= 2^14 fits
-// fp16, whose subnormals reach 2^-38 below the largest weight; L sums the
+//   x_j = score_j + log2 s_v(j),  w_j = 2^(x_j - m + 7),  m >= max x - 8,
+// O = sum w_j code_j and L = sum w_j / s_v(j) give o = O / L. w <= 2^15 fits
+// fp16, whose subnormals reach 2^-31 below a weight at m; L sums the
 // fp32 weights, so it also keeps blocks whose values are all zero (s_v taken
 // as the smallest scale there). q goes to fp16 with its row's largest
 // magnitude in [1, 2), an exact step apart from values 2^-14 and more below it.
@@ -62,13 +62,17 @@ using tc::mbar_test_wait;
 using tc::mbar_wait;
 using tc::smem_u32;
 
-constexpr int kPos = 64;            // positions per unit (= ring stage)
+// Positions per unit (= ring stage): 16 per warp of four, 32 at the smaller head
+// sizes, where two independent products hide one another's latency.
+constexpr int unit_positions(int D) { return D == 256 ? 64 : 128; }
 constexpr int kConsumers = 8;       // warps
 constexpr int kThreads = (kConsumers + 1) * 32;
 constexpr int kMaxCtas = 256;       // workspace bound on the grid
 constexpr long long kTimeoutNs = 1000000000ll;
 constexpr float kMinusBig = -1e30f; // running-max start: finite, so 2^(m - m_new) is never NaN
-constexpr float kWeightBits = 14.f; // the largest weight is 2^14
+// A row's m is raised to its largest score only when a score passes it by
+// more than kSlack: weights are 2^kWeightBits at m and fit fp16 up to there.
+constexpr float kWeightBits = 7.f, kSlack = 8.f;
 
 template <int D, int kNT>
 struct Cfg {
@@ -76,21 +80,23 @@ struct Cfg {
   static constexpr int kNTw = kNT / kRowSplit;             // groups of 8 rows of a warp
   static constexpr int kFold = kConsumers / kRowSplit;     // warps whose states belong to the same rows
   static constexpr int kUsers = kRowSplit == 2 ? 8 : 4;    // warps that read a unit
-  static constexpr int kSlabs = D < 128 ? 1 : D / 128;    // TMA boxes of up to 128 bytes by 64 rows
+  static constexpr int kStride = kRowSplit == 2 ? 1 : 2;   // from one unit of a warp to its next
+  static constexpr int kSlabs = D < 128 ? 1 : D / 128;    // TMA boxes of up to 128 bytes by kPos rows
+  static constexpr int kPos = unit_positions(D);
+  static constexpr int kMT = kPos / 64;                    // products of 16 positions of a warp
   static constexpr int kSlab = kPos * (D < 128 ? D : 128);
   static constexpr int kStageBytes = 2 * kSlabs * kSlab;  // K then V
-  // A warp's softmax state as its lanes hold it: D/4 accumulators, then two
-  // maxima and two sums, for each of its groups; stored [value][lane].
-  static constexpr int kStateFloats = (D / 4 + 4) * kNTw;
-  static constexpr int kFoldBytes = 4 * kStateFloats * 32 * 4;  // four slots
+  static constexpr int kFoldItems = kNTw * (D / 16) * 32;  // a warp's accumulators, four at a time
+  static constexpr int kFoldBytes = 4 * kFoldItems * 16;   // four slots
   static constexpr int kQPitch = D * 2 + 32;              // bytes of a row of Q (the padding spreads the banks)
   static constexpr int kQBytes = 8 * kNT * kQPitch;
-  static constexpr int kFit = (224 * 1024 - kFoldBytes - kQBytes) / kStageBytes;
-  static constexpr int kStages = kFit > 12 ? 12 : kFit;
+  static constexpr int kFit = (223 * 1024 - kFoldBytes - kQBytes) / kStageBytes;
+  // an even number: the warps that take every second unit have stages of their own
+  static constexpr int kStages = kFit > 12 ? 12 : kFit & ~1;
   static constexpr int kFoldOffset = kStages * kStageBytes;
   static constexpr int kQOffset = kFoldOffset + kFoldBytes;
   static constexpr int kCtlOffset = kQOffset + kQBytes;
-  static constexpr int kBytes = kCtlOffset + 768 + 1024;  // + alignment slack
+  static constexpr int kBytes = kCtlOffset + 2816 + 1024;  // + alignment slack
   static_assert(kNTw * D <= 256 && kStages >= 3 && kBytes <= 227 * 1024, "registers and shared memory");
 };
 
@@ -99,11 +105,13 @@ struct Ctl {
   uint64_t full[kStages];
   uint64_t empty[kStages];
   uint64_t fold;  // all consumer warps, at each step of a fold
+  uint64_t go;    // all consumer warps have asked for their first tile's Q and scales
   int abort;
   // of the tile's rows: score factor of the row's power of two, -128 sum(q)
   // 2^-24 (int8), visible positions
   float scale[32], shift[32];
   int see[32];
+  float m[kConsumers][32], l[kConsumers][32];  // the warps' states, at a fold
 };
 
 struct Params {
@@ -121,8 +129,14 @@ struct Params {
 };
 
 // Units of a whole sequence and KV head.
-__device__ __forceinline__ long long seq_units(int n, int len, int r, int RT) {
+__device__ __forceinline__ long long seq_units(int n, int len, int r, int RT, int kPos) {
   return units_before(n, len, r, RT, kPos, seq_tiles(n, r, RT));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
@@ -211,7 +225,7 @@ struct Cursor {
     len = __ldg(p.lens + b);
   }
   // The next unit; the caller knows that there is one.
-  __device__ void advance(const Params& p, int r, int RT) {
+  __device__ void advance(const Params& p, int r, int RT, int kPos) {
     if (++i < nb) return;
     i = 0;
     do {
@@ -233,15 +247,16 @@ struct Cursor {
 
 template <int D, int kNT, bool kE4m3>
 __global__ void __launch_bounds__(kThreads, 1)
-    kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Params p) {
+    kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const Params p) {
   using S = Cfg<D, kNT>;
-  constexpr int kNTw = S::kNTw;
+  constexpr int kNTw = S::kNTw, kPos = S::kPos, kMT = S::kMT;
   constexpr int kStages = S::kStages;
-  constexpr int RT = 8 * kNT;
+  constexpr int RT = 8 * kNT;  // rows of a tile
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Ctl<kStages>* ctl = reinterpret_cast<Ctl<kStages>*>(smem + S::kCtlOffset);
-  static_assert(sizeof(Ctl<kStages>) <= 768, "control block");
+  static_assert(sizeof(Ctl<kStages>) <= 2816, "control block");
   float* mrg = reinterpret_cast<float*>(smem + S::kFoldOffset);
   __shared__ long long s_lo, s_hi;
   __shared__ Cursor s_cur;
@@ -257,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->empty[s], S::kUsers);
     }
     mbar_init(&ctl->fold, kConsumers);
+    mbar_init(&ctl->go, kConsumers);
     ctl->abort = 0;
     tc::fence_barrier_init();
   }
@@ -287,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (offsets_bad(at, end, b, p.B, p.T) || len < 0 || len > p.L_max) {
           bad = true;
         } else {
-          v = seq_units(end - at, len, r, RT) * p.Hkv;
+          v = seq_units(end - at, len, r, RT, kPos) * p.Hkv;
           nt = seq_tiles(end - at, r, RT) * p.Hkv;
         }
       }
@@ -369,8 +385,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kConsumers) {
     // ------------------------------------------------------------ producer
+    // The first tile's Q and scales ask first: behind a ring's worth of codes
+    // from every SM they took 3 us more.
     int s = 0, ph = 0, issued = 0;
-    for (long long j = lo; j < hi; ++j) {
+    bool go = warp_wait(&ctl->go, 0);
+#pragma unroll 1
+    for (long long j = lo; go && j < hi; ++j) {
       if (issued >= kStages && !warp_wait(&ctl->empty[s], ph ^ 1)) break;
       if (elect_one()) {
         uint8_t* st = smem + s * S::kStageBytes;
@@ -388,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         s = 0;
         ph ^= 1;
       }
-      cur.advance(p, r, RT);
+      cur.advance(p, r, RT, kPos);
     }
     if (lane == 0 && *abort_flag) {  // let this block's own copies land before it exits
       int dummy = 0;
@@ -402,18 +422,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ldmatrix row addresses (relative to a slab): lanes 0-7, 8-15, 16-23,
     // 24-31 address the four 8 x 16-byte matrices (positions +0, +8 of the
     // low 16 dims, then of the high 16)
-    const int pw = warp & 3, part = warp >> 2;  // the warp's 16 positions; its half of the units or of the rows
+    const int pw = warp & 3, part = warp >> 2;  // the warp's 16 kMT positions; its half of the units or of the rows
     const int rows0 = S::kRowSplit == 2 ? part * 8 * kNTw : 0;
-    const int row = 16 * pw + (lane & 7) + ((lane >> 3) & 1) * 8;
+    const int row = 16 * kMT * pw + (lane & 7) + ((lane >> 3) & 1) * 8;
     const int ch = lane >> 4;
     // TMA swizzle: 16-byte chunk ^= row % 8 (128-byte rows), (row / 2) % 4 (64-byte rows)
+    constexpr int kRowBytes = D < 128 ? 64 : 128;
     const int sw = D < 128 ? (row >> 1) & 3 : row & 7;
 
     uint32_t qf[kNTw][D / 16][2];   // Q as the B operand: row 8 nt + gq, dims 16 ks + 4 m4 .. + 3
     float acc[kNTw][D / 16][4];
     float m[kNTw][2], l[kNTw][2];    // of rows 8 nt + 2 m4, + 1
-    float rq[kNTw][2], off[kNTw][2]; // score factor of the row's power of two; -128 sum(q) (int8)
-    int lim[kNTw][2];               // visible positions
+    float rq[kNTw][2], off[kNTw][2]; // score factor of the row's power of two; -128 sum(q) 2^-24 (int8)
+    int lim[kNTw][2];                // visible positions
     int folds = 0;
     // All consumer warps have come this far.
     auto together = [&]() -> bool {
@@ -421,37 +442,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&ctl->fold);
       return warp_wait(&ctl->fold, folds++ & 1);
     };
-    // Q of a tile, a warp per row at a time, through shared memory into every
-    // warp's fragments. (Each warp fetching its own fragments took 4.7 us, at
-    // every tile: three times the instructions, all of them cold.)
-    const uint32_t sQ = smem_u32(smem + S::kQOffset);
-    auto load_q = [&]() -> bool {
-      constexpr int kPer = D / 32;  // head dims of a lane
-      if (!together()) return false;  // the last tile's Q is in its fragments
+    // Q of a tile: a warp asks for one row at a time (fetch_q), converts it into
+    // shared memory and every warp takes its fragments from there (place_q).
+    // (Each warp fetching its own fragments took 4.7 us, at every tile: three
+    // times the instructions, all of them cold.)
+    constexpr int kPer = D / 32;  // head dims of a lane
+    uint32_t raw[kNT][kPer / 2];
+    auto fetch_q = [&](const Cursor& k) {
 #pragma unroll
       for (int i = 0; i < kNT; ++i) {
-        const int rw = warp + 8 * i, rr = cur.rt * RT + rw, tok = rr / r;
-        const bool live = rr < cur.n * r;
-        const uint16_t* src = p.q + (size_t)(cur.lo + (live ? tok : 0)) * p.q_stride +
-                              (size_t)(cur.g * r + (live ? rr - tok * r : 0)) * D + kPer * lane;
-        uint32_t w[kPer / 2], mx = 0u;
-        if (kPer == 8) {
-          const uint4 x = __ldg(reinterpret_cast<const uint4*>(src));
-          w[0] = x.x;
-          w[1] = x.y;
-          w[2 % (kPer / 2)] = x.z;
-          w[3 % (kPer / 2)] = x.w;
-        } else if (kPer == 4) {
-          const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
-          w[0] = x.x;
-          w[1 % (kPer / 2)] = x.y;
-        } else {
-          w[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
-        }
+        const int rr = k.rt * RT + warp + 8 * i, tok = rr / r;
+        const bool live = rr < k.n * r;
+        const uint16_t* src = p.q + (size_t)(k.lo + (live ? tok : 0)) * p.q_stride +
+                              (size_t)(k.g * r + (live ? rr - tok * r : 0)) * D + kPer * lane;
+        if constexpr (kPer == 8)
+          asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(raw[i][0]), "=r"(raw[i][1]), "=r"(raw[i][2]), "=r"(raw[i][3])
+                       : "l"(src));
+        else if constexpr (kPer == 4)
+          asm volatile("ld.global.nc.v2.b32 {%0, %1}, [%2];" : "=r"(raw[i][0]), "=r"(raw[i][1]) : "l"(src));
+        else
+          asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(raw[i][0]) : "l"(src));
+      }
+    };
+    const uint32_t sQ = smem_u32(smem + S::kQOffset);
+    auto place_q = [&](const Cursor& t) -> bool {
+#pragma unroll
+      for (int i = 0; i < kNT; ++i) {
+        const int rw = warp + 8 * i, rr = t.rt * RT + rw;
+        const bool live = rr < t.n * r;
+        uint32_t mx = 0u;
 #pragma unroll
         for (int k = 0; k < kPer / 2; ++k) {
-          w[k] = live ? w[k] : 0u;
-          mx = __vmaxu2(mx, w[k] & 0x7FFF7FFFu);
+          raw[i][k] = live ? raw[i][k] : 0u;
+          mx = __vmaxu2(mx, raw[i][k] & 0x7FFF7FFFu);
         }
         mx = __reduce_max_sync(0xffffffffu, max(mx & 0xFFFFu, mx >> 16));
         // 2^-e with e the exponent of the largest magnitude (an infinity or a
@@ -462,19 +486,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t to = sQ + rw * S::kQPitch + 2 * kPer * lane;
 #pragma unroll
         for (int k = 0; k < kPer / 2; ++k) {
-          w[k] = pack_f16(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
-          const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+          const uint32_t x = pack_f16(__uint_as_float(raw[i][k] << 16) * down,
+                                      __uint_as_float(raw[i][k] & 0xFFFF0000u) * down);
+          const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&x));
           sum += a.x + a.y;
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + 4 * k), "r"(w[k]) : "memory");
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + 4 * k), "r"(x) : "memory");
         }
         if (!kE4m3) {
-#pragma unroll
+#pragma unroll 1
           for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         }
         if (lane == 0) {
           ctl->scale[rw] = p.scale_log2 * __uint_as_float(e > 0 ? (uint32_t)e << 23 : 0x00400000u);  // 2^(e - 127)
           ctl->shift[rw] = kE4m3 ? 0.f : sum * -7.62939453125e-06f;  // -128 2^-24
-          ctl->see[rw] = live ? cur.len - cur.n + tok + 1 : 0;
+          ctl->see[rw] = live ? t.len - t.n + rr / r + 1 : 0;
         }
       }
       if (!together()) return false;
@@ -493,146 +518,179 @@ __global__ void __launch_bounds__(kThreads, 1)
           rq[nt][k] = ctl->scale[rw];
           off[nt][k] = ctl->shift[rw];
           lim[nt][k] = ctl->see[rw];
+          m[nt][k] = kMinusBig;
+          l[nt][k] = 0.f;
         }
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt) acc[nt][mt][0] = acc[nt][mt][1] = acc[nt][mt][2] = acc[nt][mt][3] = 0.f;
       }
       return true;
     };
-    auto reset = [&]() {
+    // The scales of this warp's positions of the unit at a cursor, 16 at a time
+    // (a group past the context repeats the last position's: it is not used).
+    auto load_scales = [&](const Cursor& k, float (&sk)[kMT], float (&sv)[kMT]) {
 #pragma unroll
-      for (int nt = 0; nt < kNTw; ++nt) {
-#pragma unroll
-        for (int mt = 0; mt < D / 16; ++mt) acc[nt][mt][0] = acc[nt][mt][1] = acc[nt][mt][2] = acc[nt][mt][3] = 0.f;
-        m[nt][0] = m[nt][1] = kMinusBig;
-        l[nt][0] = l[nt][1] = 0.f;
+      for (int t = 0; t < kMT; ++t) {
+        const int pos = min(k.i * kPos + 16 * (kMT * pw + t), k.len - 1);
+        const size_t at = (size_t)(k.b * p.Hkv + k.g) * p.nblk + (pos >> p.shift);
+        asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(sk[t]) : "l"(p.ks + at));
+        asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(sv[t]) : "l"(p.vs + at));
       }
     };
-    // The scales of this warp's 16 positions of the unit at a cursor (a group
-    // past the context repeats the last visible block's: it is not used).
-    auto load_scales = [&](const Cursor& k, float& sk, float& sv) {
-      const int pos = min(k.i * kPos + 16 * pw, k.len - 1);
-      const size_t at = (size_t)(k.b * p.Hkv + k.g) * p.nblk + (pos >> p.shift);
-      sk = __ldg(p.ks + at);
-      sv = __ldg(p.vs + at);
-    };
-    reset();
-    float sk, sv;
-    load_scales(cur, sk, sv);
-    bool good = load_q();
+    float skn[kMT], svn[kMT];  // of the next unit that is this warp's
+    fetch_q(cur);
+    {
+      Cursor own = cur;
+      if (S::kRowSplit == 1 && part == 1 && lo + 1 < hi) own.advance(p, r, RT, kPos);
+      load_scales(own, skn, svn);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl->go);
+    bool good = place_q(cur);
 
     int s = 0, ph = 0;
 #pragma unroll 1
     for (long long j = lo; good && j < hi; ++j) {
       Cursor nxt = cur;
-      float skn = 0.f, svn = 0.f;
-      if (j + 1 < hi) {  // the next unit's scales travel while this one is computed
-        nxt.advance(p, r, RT);
-        load_scales(nxt, skn, svn);
+      if (j + 1 < hi) {
+        nxt.advance(p, r, RT, kPos);
+        if (nxt.tile != cur.tile) fetch_q(nxt);  // it travels while this unit is computed
       }
       const bool mine = S::kRowSplit == 2 || ((int)(j - lo) & 1) == part;
-      // every warp sees every phase, its own or not: a parity says nothing to
-      // a waiter that is two phases behind
-      if (!warp_wait(&ctl->full[s], ph)) break;
+      float sk[kMT], sv[kMT];
+      if (mine) {
+#pragma unroll
+        for (int t = 0; t < kMT; ++t) {
+          sk[t] = skn[t];
+          sv[t] = svn[t];
+        }
+        if (j + S::kStride < hi) {  // the scales of this warp's next unit travel, too
+          Cursor own = nxt;
+          if (S::kStride == 2) own.advance(p, r, RT, kPos);
+          load_scales(own, skn, svn);
+        }
+        if (!warp_wait(&ctl->full[s], ph)) break;
+      }
       const uint32_t sK = smem_u32(smem + s * S::kStageBytes);
       const uint32_t sV = sK + S::kSlabs * S::kSlab;
-      auto chunk_addr = [&](uint32_t base, int kk) -> uint32_t {  // dims 32 kk .. + 31
+      auto chunk_addr = [&](uint32_t base, int kk, int t) -> uint32_t {  // dims 32 kk .. + 31 of the t-th 16 positions
         constexpr int kPerSlab = D < 128 ? 2 : 4;
         const int cc = (kk % kPerSlab) * 2 + ch;
-        return base + (kk / kPerSlab) * S::kSlab + row * (D < 128 ? 64 : 128) + ((cc ^ sw) << 4);
+        return base + (kk / kPerSlab) * S::kSlab + (row + 16 * t) * kRowBytes + ((cc ^ sw) << 4);
       };
-      const int pos0 = cur.i * kPos + 16 * pw;  // first position of this warp's 16
+      const int pos0 = cur.i * kPos + 16 * kMT * pw;  // this warp's first position
       if (mine && pos0 < cur.len) {
-        float x[kNTw][4];
+        float x[kMT][kNTw][4];
+        float y[4] = {0.f, 0.f, 0.f, 0.f};  // one product: a second accumulator halves the dependent chain
+        constexpr bool kHalve = kNTw * kMT == 1;
 #pragma unroll
-        for (int nt = 0; nt < kNTw; ++nt) {
-          x[nt][0] = x[nt][2] = off[nt][0];
-          x[nt][1] = x[nt][3] = off[nt][1];
-        }
-        float y[4] = {0.f, 0.f, 0.f, 0.f};  // one row group: a second accumulator halves the dependent chain
+        for (int t = 0; t < kMT; ++t)
 #pragma unroll
-        for (int kk = 0; kk < D / 32; ++kk) {
-          uint32_t w[4], a0, a1, a2, a3;
-          ldsm_x4(chunk_addr(sK, kk), w);
+          for (int nt = 0; nt < kNTw; ++nt) {
+            x[t][nt][0] = x[t][nt][2] = off[nt][0];
+            x[t][nt][1] = x[t][nt][3] = off[nt][1];
+          }
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            k_pairs<kE4m3>(w[2 * h], a0, a2);
-            k_pairs<kE4m3>(w[2 * h + 1], a1, a3);
+        for (int kk = 0; kk < D / 32; ++kk)
 #pragma unroll
-            for (int nt = 0; nt < kNTw; ++nt) {
-              if (kNTw == 1 && h == 1) mma_f16(y, a0, a1, a2, a3, qf[nt][2 * kk + h][0], qf[nt][2 * kk + h][1]);
-              else mma_f16(x[nt], a0, a1, a2, a3, qf[nt][2 * kk + h][0], qf[nt][2 * kk + h][1]);
+          for (int t = 0; t < kMT; ++t) {
+            uint32_t w[4], a0, a1, a2, a3;
+            ldsm_x4(chunk_addr(sK, kk, t), w);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              k_pairs<kE4m3>(w[2 * h], a0, a2);
+              k_pairs<kE4m3>(w[2 * h + 1], a1, a3);
+#pragma unroll
+              for (int nt = 0; nt < kNTw; ++nt) {
+                if (kHalve && h == 1) mma_f16(y, a0, a1, a2, a3, qf[nt][2 * kk + h][0], qf[nt][2 * kk + h][1]);
+                else mma_f16(x[t][nt], a0, a1, a2, a3, qf[nt][2 * kk + h][0], qf[nt][2 * kk + h][1]);
+              }
             }
           }
-        }
-        const float svx = sv > 0.f ? sv : kScaleFloor;
-        const float lsv = log2f(svx), rsv = 1.f / svx;
-        const int pr = pos0 + gq;
-        uint32_t pb[kNTw][2];
-        float al[kNTw][2];
-        bool grew = false;
+        // scores, with V's scale; does one pass its row's m by more than the slack?
+        float rsv[kMT];
+        bool up = false;
 #pragma unroll
-        for (int nt = 0; nt < kNTw; ++nt) {
-          const float a[2] = {rq[nt][0] * sk, rq[nt][1] * sk};
-          float w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float d = x[nt][e];
-            if (kNTw == 1) d += y[e];
-            if (!kE4m3) d *= 16777216.f;
-            w[e] = pr + (e >> 1) * 8 < lim[nt][e & 1] ? fmaf(d, a[e & 1], lsv) : -INFINITY;
-          }
-          float nm[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float mx = fmaxf(w[k], w[k + 2]);
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            nm[k] = fmaxf(m[nt][k], mx);
-            al[nt][k] = exp2f(m[nt][k] - nm[k]);
-            grew |= al[nt][k] != 1.f;
-            m[nt][k] = nm[k];
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = exp2f(w[e] - nm[e & 1] + kWeightBits);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) l[nt][k] = fmaf(w[k] + w[k + 2], rsv, l[nt][k] * al[nt][k]);
-          // P^T as the B operand: rows (k) = positions, columns (n) = query rows
-          pb[nt][0] = movmatrix_trans(pack_f16(w[0], w[1]));
-          pb[nt][1] = movmatrix_trans(pack_f16(w[2], w[3]));
-        }
-        if (__any_sync(0xffffffffu, grew)) {
+        for (int t = 0; t < kMT; ++t) {
+          const float svx = sv[t] > 0.f ? sv[t] : kScaleFloor;
+          const float lsv = __log2f(svx);
+          rsv[t] = __fdividef(1.f, svx);
+          const int pr = pos0 + 16 * t + gq;
 #pragma unroll
           for (int nt = 0; nt < kNTw; ++nt)
 #pragma unroll
-            for (int mt = 0; mt < D / 16; ++mt) {
-              acc[nt][mt][0] *= al[nt][0];
-              acc[nt][mt][1] *= al[nt][1];
-              acc[nt][mt][2] *= al[nt][0];
-              acc[nt][mt][3] *= al[nt][1];
+            for (int e = 0; e < 4; ++e) {
+              float d = x[t][nt][e];
+              if (kHalve) d += y[e];
+              if (!kE4m3) d *= 16777216.f;
+              x[t][nt][e] = pr + (e >> 1) * 8 < lim[nt][e & 1] ? fmaf(d, rq[nt][e & 1] * sk[t], lsv) : -INFINITY;
+              up |= x[t][nt][e] > m[nt][e & 1] + kSlack;
             }
         }
-        // V bytes past the context may hold anything, a NaN of e4m3 included: zero them
-        const bool tail = pos0 + 16 > cur.len;
-        const int kp = pos0 + 2 * m4;
-        const uint32_t mlo = (kp < cur.len ? 0x0000FFFFu : 0u) | (kp + 1 < cur.len ? 0xFFFF0000u : 0u);
-        const uint32_t mhi = (kp + 8 < cur.len ? 0x0000FFFFu : 0u) | (kp + 9 < cur.len ? 0xFFFF0000u : 0u);
+        if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-        for (int kk = 0; kk < D / 32; ++kk) {
-          uint32_t w[4], a0, a1, a2, a3;
-          ldsm_x4_trans(chunk_addr(sV, kk), w);
+          for (int nt = 0; nt < kNTw; ++nt) {
+            float al[2];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            v_pairs<kE4m3>(w[2 * h], a0, a1);      // positions 0-7: dims 2g, 2g + 1
-            v_pairs<kE4m3>(w[2 * h + 1], a2, a3);  // positions 8-15
-            if (kE4m3 && tail) {
-              a0 &= mlo;
-              a1 &= mlo;
-              a2 &= mhi;
-              a3 &= mhi;
+            for (int k = 0; k < 2; ++k) {
+              float mx = m[nt][k];
+#pragma unroll
+              for (int t = 0; t < kMT; ++t) mx = fmaxf(mx, fmaxf(x[t][nt][k], x[t][nt][k + 2]));
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              al[k] = ex2(m[nt][k] - mx);
+              m[nt][k] = mx;
+              l[nt][k] *= al[k];
             }
 #pragma unroll
-            for (int nt = 0; nt < kNTw; ++nt) mma_f16(acc[nt][2 * kk + h], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+            for (int mt = 0; mt < D / 16; ++mt) {
+              acc[nt][mt][0] *= al[0];
+              acc[nt][mt][1] *= al[1];
+              acc[nt][mt][2] *= al[0];
+              acc[nt][mt][3] *= al[1];
+            }
           }
         }
+        // weights; P^T as the B operand: rows (k) = positions, columns (n) = query rows
+        uint32_t pb[kMT][kNTw][2];
+#pragma unroll
+        for (int t = 0; t < kMT; ++t)
+#pragma unroll
+          for (int nt = 0; nt < kNTw; ++nt) {
+            float w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = ex2(x[t][nt][e] - (m[nt][e & 1] - kWeightBits));
+#pragma unroll
+            for (int k = 0; k < 2; ++k) l[nt][k] = fmaf(w[k] + w[k + 2], rsv[t], l[nt][k]);
+            pb[t][nt][0] = movmatrix_trans(pack_f16(w[0], w[1]));
+            pb[t][nt][1] = movmatrix_trans(pack_f16(w[2], w[3]));
+          }
+        // V bytes past the context may hold anything, a NaN of e4m3 included: zero them
+        const bool tail = pos0 + 16 * kMT > cur.len;
+#pragma unroll
+        for (int kk = 0; kk < D / 32; ++kk)
+#pragma unroll
+          for (int t = 0; t < kMT; ++t) {
+            uint32_t w[4], a0, a1, a2, a3;
+            ldsm_x4_trans(chunk_addr(sV, kk, t), w);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              v_pairs<kE4m3>(w[2 * h], a0, a1);      // positions 0-7: dims 2g, 2g + 1
+              v_pairs<kE4m3>(w[2 * h + 1], a2, a3);  // positions 8-15
+              if (kE4m3 && tail) {
+                const int kp = pos0 + 16 * t + 2 * m4;
+                const uint32_t mlo = (kp < cur.len ? 0x0000FFFFu : 0u) | (kp + 1 < cur.len ? 0xFFFF0000u : 0u);
+                const uint32_t mhi = (kp + 8 < cur.len ? 0x0000FFFFu : 0u) | (kp + 9 < cur.len ? 0xFFFF0000u : 0u);
+                a0 &= mlo;
+                a1 &= mlo;
+                a2 &= mhi;
+                a3 &= mhi;
+              }
+#pragma unroll
+              for (int nt = 0; nt < kNTw; ++nt)
+                mma_f16(acc[nt][2 * kk + h], a0, a1, a2, a3, pb[t][nt][0], pb[t][nt][1]);
+            }
+          }
       }
       __syncwarp();
       if (mine && lane == 0) mbar_arrive(&ctl->empty[s]);
@@ -641,94 +699,98 @@ __global__ void __launch_bounds__(kThreads, 1)
         ph ^= 1;
       }
 
-      if (cur.i == cur.nb - 1 || j == hi - 1) {
-        // ---- the run leaves this tile: fold the warps' states of the same
-        // rows. They have the same lane layout, so a warp folds another's
-        // state in lane by lane: the upper half into the lower, and so on (a
-        // fixed order). In later steps a warp writes the slot it has read.
+      if (nxt.tile != cur.tile || j == hi - 1) {
+        // ---- the run leaves this tile: fold the states of the warps with the
+        // same rows. All take the largest m; then, lane by lane, the upper half
+        // of the warps hands its accumulators to the lower, and every thread
+        // sums a part of what is left (a fixed order).
+        const int idx = S::kRowSplit == 2 ? pw : warp, set0 = warp - idx;  // set0: the first warp of these rows
 #pragma unroll
         for (int nt = 0; nt < kNTw; ++nt)
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
+          for (int k = 0; k < 2; ++k) {
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], o);
-        auto put = [&](float* st) {
-#pragma unroll
-          for (int nt = 0; nt < kNTw; ++nt) {
-            float* sn = st + nt * (D / 4 + 4) * 32 + lane;
-#pragma unroll
-            for (int mt = 0; mt < D / 16; ++mt)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) sn[(4 * mt + k) * 32] = acc[nt][mt][k];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              sn[(D / 4 + k) * 32] = m[nt][k];
-              sn[(D / 4 + 2 + k) * 32] = l[nt][k];
-            }
+            if (lane < 4) ctl->m[warp][8 * nt + 2 * lane + k] = m[nt][k];
           }
-        };
-        auto take = [&](const float* st) {
+        if (!together()) break;
 #pragma unroll
-          for (int nt = 0; nt < kNTw; ++nt) {
-            const float* sn = st + nt * (D / 4 + 4) * 32 + lane;
-            float f1[2], f2[2];
+        for (int nt = 0; nt < kNTw; ++nt) {
+          float f[2];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float m2 = sn[(D / 4 + k) * 32], nm = fmaxf(m[nt][k], m2);
-              f1[k] = exp2f(m[nt][k] - nm);
-              f2[k] = exp2f(m2 - nm);
-              m[nt][k] = nm;
-              l[nt][k] = l[nt][k] * f1[k] + sn[(D / 4 + 2 + k) * 32] * f2[k];
-            }
+          for (int k = 0; k < 2; ++k) {
+            float top = m[nt][k];
 #pragma unroll
-            for (int mt = 0; mt < D / 16; ++mt)
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                acc[nt][mt][k] = acc[nt][mt][k] * f1[k & 1] + sn[(4 * mt + k) * 32] * f2[k & 1];
+            for (int w = 0; w < S::kFold; ++w) top = fmaxf(top, ctl->m[set0 + w][8 * nt + 2 * m4 + k]);
+            f[k] = ex2(m[nt][k] - top);
+            m[nt][k] = top;
+            if (lane < 4) ctl->l[warp][8 * nt + 2 * lane + k] = l[nt][k] * f[k];
           }
-        };
-        const int idx = S::kRowSplit == 2 ? pw : warp;
-        float* slots = mrg + (S::kRowSplit == 2 ? part : 0) * (S::kFold / 2) * S::kStateFloats * 32;
-        bool ok = together();  // nobody reads the last fold's slots any more
-#pragma unroll 1
-        for (int half = S::kFold / 2; half >= 1; half /= 2) {
-          const int base = half == S::kFold / 2 ? half : 0;  // the first step's writers have no slots of their own
-          if (ok && idx >= half && idx < 2 * half) put(slots + (idx - base) * S::kStateFloats * 32);
-          ok = ok && together();
-          if (ok && idx < half) take(slots + (idx + half - base) * S::kStateFloats * 32);
+#pragma unroll
+          for (int mt = 0; mt < D / 16; ++mt) {
+            acc[nt][mt][0] *= f[0];
+            acc[nt][mt][1] *= f[1];
+            acc[nt][mt][2] *= f[0];
+            acc[nt][mt][3] *= f[1];
+          }
         }
-        if (!ok) break;
-        if (idx == 0) {
-          const size_t slot = (size_t)c + cur.tile;
-          float* pm = p.part + slot * RT + rows0;
-          float* pl = p.part + (size_t)p.slots * RT + slot * RT + rows0;
-          float* po = p.part + (size_t)2 * p.slots * RT + (slot * RT + rows0) * D;
+        constexpr int kHalf = S::kFold / 2;  // slots of a set of rows
+        float4* slots = reinterpret_cast<float4*>(smem + S::kFoldOffset);
+        float4* own = slots + (set0 / 2 + (idx < kHalf ? idx : idx - kHalf)) * S::kFoldItems + lane;
+        if (idx >= kHalf) {
 #pragma unroll
-          for (int nt = 0; nt < kNTw; ++nt) {
-            const int r0 = 8 * nt + 2 * m4;
+          for (int nt = 0; nt < kNTw; ++nt)
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt)
+              own[(nt * (D / 16) + mt) * 32] =
+                  make_float4(acc[nt][mt][0], acc[nt][mt][1], acc[nt][mt][2], acc[nt][mt][3]);
+        }
+        if (!together()) break;
+        if (idx < kHalf) {
+#pragma unroll
+          for (int nt = 0; nt < kNTw; ++nt)
 #pragma unroll
             for (int mt = 0; mt < D / 16; ++mt) {
-              const int d = 16 * mt + 2 * gq;
-              *reinterpret_cast<float2*>(po + r0 * D + d) = make_float2(acc[nt][mt][0], acc[nt][mt][2]);
-              *reinterpret_cast<float2*>(po + (r0 + 1) * D + d) = make_float2(acc[nt][mt][1], acc[nt][mt][3]);
+              const float4 o = own[(nt * (D / 16) + mt) * 32];
+              own[(nt * (D / 16) + mt) * 32] = make_float4(acc[nt][mt][0] + o.x, acc[nt][mt][1] + o.y,
+                                                           acc[nt][mt][2] + o.z, acc[nt][mt][3] + o.w);
             }
-            if (lane < 4) {
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                pm[r0 + k] = m[nt][k];
-                pl[r0 + k] = l[nt][k];
-              }
-            }
-          }
         }
-        reset();
+        if (!together()) break;
+        const size_t slot = (size_t)c + cur.tile;
+        float* po = p.part + (size_t)2 * p.slots * RT + slot * RT * D;
+#pragma unroll
+        for (int it = 0; it < S::kRowSplit * S::kFoldItems; it += kConsumers * 32) {
+          const int item = it + warp * 32 + lane, set = item / S::kFoldItems, in = item % S::kFoldItems;
+          if (item >= S::kRowSplit * S::kFoldItems) break;
+          float4 o = slots[set * kHalf * S::kFoldItems + in];
+#pragma unroll
+          for (int w = 1; w < kHalf; ++w) {
+            const float4 a = slots[(set * kHalf + w) * S::kFoldItems + in];
+            o = make_float4(o.x + a.x, o.y + a.y, o.z + a.z, o.w + a.w);
+          }
+          const int ln = in & 31, nt = (in >> 5) / (D / 16), mt = (in >> 5) % (D / 16);
+          float* at = po + (size_t)(set * 8 * kNTw + 8 * nt + 2 * (ln & 3)) * D + 16 * mt + 2 * (ln >> 2);
+          *reinterpret_cast<float2*>(at) = make_float2(o.x, o.z);
+          *reinterpret_cast<float2*>(at + D) = make_float2(o.y, o.w);
+        }
+        if (idx == 0 && lane < 8 * kNTw) {
+          float sum = 0.f;
+#pragma unroll
+          for (int w = 0; w < S::kFold; ++w) sum += ctl->l[set0 + w][lane];
+          p.part[(size_t)p.slots * RT + slot * RT + rows0 + lane] = sum;
+        }
+        if (idx == 0 && lane < 4) {
+#pragma unroll
+          for (int nt = 0; nt < kNTw; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) p.part[slot * RT + rows0 + 8 * nt + 2 * lane + k] = m[nt][k];
+        }
         cur = nxt;
-        if (j + 1 < hi) good = load_q();
+        if (j + 1 < hi) good = place_q(cur);
       } else {
         cur = nxt;
       }
-      sk = skn;
-      sv = svn;
     }
   }
   __syncthreads();
@@ -746,11 +808,12 @@ struct MergeParams {
   int B, T, Hq, Hkv, D, L_max, RT, C;
 };
 
-// The block's 8 warps take the covering grid blocks c0 + warp, c0 + 8 + warp,
-// ..., a lane two head dims: every load of up to kMergeBatch states is issued
-// before any is used. Then the 8 are merged in shared memory.
+// Thread t holds dims 4 (t % 16) .. + 3 of the slice and takes the covering grid
+// blocks c0 + t / 16, c0 + 16 + t / 16, ...: all loads of kMergeBatch states are
+// issued before any is used. Then the 16 are merged in shared memory.
 constexpr int kMergeWarps = 8;
-constexpr int kMergeBatch = 10;  // 8 warps times 10: the 76 states of a pair of two on 152 SMs at once
+constexpr int kMergeLanes = 16;
+constexpr int kMergeBatch = 5;  // 16 times 5: the 76 states of a pair of two on 152 SMs at once
 
 __global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_kernel(const MergeParams p) {
   // The next call's split kernel may launch now: it waits for this grid to
@@ -760,8 +823,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_kernel(const Merge
   // split kernel does not write: it overlaps that kernel's tail.
   const int r = p.Hq / p.Hkv, RT = p.RT, C = p.C, D = p.D;
   const int t = blockIdx.x / p.Hq, h = blockIdx.x - t * p.Hq;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  __shared__ float s_m[kMergeWarps], s_l[kMergeWarps], s_o[kMergeWarps][64];
+  const int lane = threadIdx.x & 31, f4 = threadIdx.x & 15, sl = threadIdx.x >> 4;
+  __shared__ float s_m[kMergeLanes], s_l[kMergeLanes], s_o[kMergeLanes][64];
+  const int kPos = unit_positions(D);
   __shared__ int s_first;
   // every warp: the sequence, and the units and tiles before it
   long long before = 0, total = 0;
@@ -778,7 +842,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_kernel(const Merge
       if (offsets_bad(lo1, hi1, bb, p.B, p.T) || len1 < 0 || len1 > p.L_max) {
         bad = true;
       } else {
-        v = seq_units(hi1 - lo1, len1, r, RT);
+        v = seq_units(hi1 - lo1, len1, r, RT, kPos);
         nt = seq_tiles(hi1 - lo1, r, RT);
       }
     }
@@ -808,7 +872,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_kernel(const Merge
   if (!bad && b >= 0) {
     const int g = h / r, row = (t - lo) * r + h - g * r, rt = row / RT, nb = tile_units(n, len, r, RT, kPos, rt);
     const Runs runs(total * p.Hkv, C);
-    const long long start = before * p.Hkv + seq_units(n, len, r, RT) * g + units_before(n, len, r, RT, kPos, rt);
+    const long long start = before * p.Hkv + seq_units(n, len, r, RT, kPos) * g + units_before(n, len, r, RT, kPos, rt);
     slot0 = ((size_t)tiles * p.Hkv + (size_t)g * seq_tiles(n, r, RT) + rt) * RT + row - rt * RT;
     if (nb > 0 && len - n + (t - lo) >= 0) {
       c0 = runs.of(start);
@@ -830,57 +894,55 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_kernel(const Merge
 
   const float* pm = p.part;
   const float* pl = p.part + (size_t)p.slots * RT;
-  const float* po = p.part + (size_t)2 * p.slots * RT + blockIdx.y * 64 + 2 * lane;
-  float M = kMinusBig, L = 0.f, Ox = 0.f, Oy = 0.f;
+  const float* po = p.part + (size_t)2 * p.slots * RT + blockIdx.y * 64 + 4 * f4;
+  float M = kMinusBig, L = 0.f;
+  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
   int failed = 0;
 #pragma unroll 1
-  for (int base = c0 + warp; base <= c1; base += kMergeWarps * kMergeBatch) {
+  for (int base = c0 + sl; base <= c1; base += kMergeLanes * kMergeBatch) {
     float mc[kMergeBatch], lc[kMergeBatch];
-    float2 oc[kMergeBatch];
+    float4 oc[kMergeBatch];
 #pragma unroll
     for (int u = 0; u < kMergeBatch; ++u) {
-      const int cc = base + u * kMergeWarps;
+      const int cc = base + u * kMergeLanes;
       mc[u] = kMinusBig;
       lc[u] = 0.f;
-      oc[u] = make_float2(0.f, 0.f);
+      oc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (cc <= c1) {
         const size_t at = (size_t)cc * RT + slot0;
         failed |= __ldcg(p.flags + cc);
         mc[u] = __ldcg(pm + at);
         lc[u] = __ldcg(pl + at);
-        oc[u] = __ldcg(reinterpret_cast<const float2*>(po + at * D));
+        oc[u] = __ldcg(reinterpret_cast<const float4*>(po + at * D));
       }
     }
     float nm = M;
 #pragma unroll
     for (int u = 0; u < kMergeBatch; ++u) nm = fmaxf(nm, mc[u]);
-    const float f = exp2f(M - nm);
+    const float f = ex2(M - nm);
     L *= f;
-    Ox *= f;
-    Oy *= f;
+    O = make_float4(O.x * f, O.y * f, O.z * f, O.w * f);
     M = nm;
 #pragma unroll
     for (int u = 0; u < kMergeBatch; ++u) {
-      const float e = exp2f(mc[u] - M);
+      const float e = ex2(mc[u] - M);
       L = fmaf(lc[u], e, L);
-      Ox = fmaf(oc[u].x, e, Ox);
-      Oy = fmaf(oc[u].y, e, Oy);
+      O = make_float4(fmaf(oc[u].x, e, O.x), fmaf(oc[u].y, e, O.y), fmaf(oc[u].z, e, O.z), fmaf(oc[u].w, e, O.w));
     }
   }
-  s_o[warp][2 * lane] = Ox;
-  s_o[warp][2 * lane + 1] = Oy;
-  if (lane == 0) {
-    s_m[warp] = M;
-    s_l[warp] = L;
+  *reinterpret_cast<float4*>(&s_o[sl][4 * f4]) = O;
+  if (f4 == 0) {
+    s_m[sl] = M;
+    s_l[sl] = L;
   }
   if (__syncthreads_or(failed)) return;  // a covering grid block gave up: o is left as it was
   if (threadIdx.x < 64) {
     float Mt = kMinusBig, Lt = 0.f, Ot = 0.f;
 #pragma unroll
-    for (int w = 0; w < kMergeWarps; ++w) Mt = fmaxf(Mt, s_m[w]);
+    for (int w = 0; w < kMergeLanes; ++w) Mt = fmaxf(Mt, s_m[w]);
 #pragma unroll
-    for (int w = 0; w < kMergeWarps; ++w) {
-      const float e = exp2f(s_m[w] - Mt);
+    for (int w = 0; w < kMergeLanes; ++w) {
+      const float e = ex2(s_m[w] - Mt);
       Lt = fmaf(e, s_l[w], Lt);
       Ot = fmaf(e, s_o[w][threadIdx.x], Ot);
     }
@@ -904,14 +966,14 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// 3-D map of codes [pairs][L_max][D] with boxes of 64 rows by up to 128
+// 3-D map of codes [pairs][L_max][D] with boxes of a unit's rows by up to 128
 // bytes, swizzled by their row length; rows past L_max read as zeros.
 cudaError_t codes_map(CUtensorMap* m, const void* base, int D, int L_max, int pairs) {
   auto fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)L_max, (cuuint64_t)pairs};
   const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)L_max * D};
-  const cuuint32_t box[3] = {(cuuint32_t)(D < 128 ? D : 128), (cuuint32_t)kPos, 1};
+  const cuuint32_t box[3] = {(cuuint32_t)(D < 128 ? D : 128), (cuuint32_t)unit_positions(D), 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, D < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
@@ -997,7 +1059,8 @@ moe_status launch_split(const AttnArgs& a, cudaStream_t stream) {
   e = a.e4m3 ? go(std::true_type{}) : go(std::false_type{});
   if (e != cudaSuccess) return cuda_fail(e, "split kernel launch");
 
-  const MergeParams mp{a.offsets, a.lens, part, flags, a.o, status, slots, a.B, a.T, a.Hq, a.Hkv, a.D, a.L_max, RT, grid};
+  const MergeParams mp{a.offsets, a.lens, part, flags, a.o, status, slots, a.B, a.T, a.Hq, a.Hkv, a.D, a.L_max, RT,
+                       grid};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.T * (unsigned)a.Hq, (unsigned)(a.D / 64));
   cfg.blockDim = dim3(kMergeWarps * 32);

@@ -75,7 +75,7 @@ typedef enum moe_kv8_format {
 } moe_kv8_format;
 
 /* Shape of one call. Supported: 1 <= B <= 4096; 0 <= T <= 2^24; 1 <= Hkv <=
- * 4096, B * Hkv <= 65536; Hq a multiple of Hkv with Hq / Hkv <= 64; D in {64,
+ * 4096, B * Hkv <= 65536, T * Hkv <= 2^30; Hq a multiple of Hkv with Hq / Hkv <= 64; D in {64,
  * 128, 256}; 1 <= L_max <= 2^26; block in {16, 32, 64}. Strides: 0 for packed
  * tokens, or a multiple of 8 elements of at least one token's (Hq D, Hkv D).
  * Write and read do not use Hq and q_stride, attention not kv_stride; they

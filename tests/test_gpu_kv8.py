@@ -525,8 +525,28 @@ def _plain_attention_gpu(p, q, news, lens):
             hide = torch.arange(ln, device=DEV) > ln - n + torch.arange(n, device=DEV)[:, None]
             w = torch.softmax(s.masked_fill(hide[:, None], -torch.inf), -1)
             o[:, g], oa[:, g] = w @ V[g], w @ V[g].abs()
-        out.append(o.view(n, -1, D)), out_abs.append(oa.view(n, -1, D))
+        out.append(o.view(n, Hkv * r, D)), out_abs.append(oa.view(n, Hkv * r, D))
     return torch.cat(out).cpu().numpy(), torch.cat(out_abs).cpu().numpy()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("Hq,Hkv,D,block,lens,news", [
+    (16, 4, 128, 32, [700 + 491 * i for i in range(16)], [1 + i % 5 for i in range(16)]),
+    (16, 2, 256, 64, [4000 - 333 * i for i in range(11)], [1 + i % 3 for i in range(11)]),
+    (32, 2, 256, 64, [1500, 77, 3000], [1, 1, 1]),
+    (12, 3, 64, 16, [3000 - 100 * i for i in range(24)], [i % 9 for i in range(24)]),
+])
+def test_attention_of_many_drafts(moelib, cuda_dev, Hq, Hkv, D, block, lens, news, fmt):
+    """Several row tiles in every block's run, some of one unit, over long
+    rings, against fp64, and the same bits every time."""
+    p = Pair(moelib, len(lens), Hkv, D, max(lens), block, fmt, seed=73)
+    gen = p.fill(lens, seed=74)
+    q = (_rand(gen, sum(news), Hq, D) * 1.5).to(torch.bfloat16)
+    got = p.attend(q, news, lens)
+    want, o_abs = _plain_attention_gpu(p, q, news, lens)
+    p.compare(got.double().cpu().numpy(), want, o_abs, q, lens)
+    for _ in range(50):
+        assert torch.equal(got, p.attend(q, news, lens))
 
 
 @pytest.mark.parametrize("fmt", FMTS)

@@ -11,7 +11,7 @@ ADDR = [0x100000 * (i + 1) for i in range(8)]
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(), 0), (dict(B=0), 2), (dict(B=4097), 2), (dict(T=-1), 2), (dict(T=(1 << 24) + 1), 2), (dict(T=1 << 24), 0),
+    (dict(), 0), (dict(B=0), 2), (dict(B=4097), 2), (dict(T=-1), 2), (dict(T=(1 << 24) + 1), 2), (dict(T=1 << 24), 0), (dict(T=1 << 24, B=1, Hkv=64, Hq=64), 0), (dict(T=1 << 24, B=1, Hkv=65, Hq=65), 2),
     (dict(Hkv=0), 2), (dict(Hkv=3), 2), (dict(Hq=0), 2), (dict(Hq=130), 2), (dict(Hq=128), 0), (dict(Hq=258), 2),
     (dict(B=4096, Hkv=32, Hq=32), 2), (dict(B=16, Hkv=4096, Hq=4096), 0), (dict(B=1, Hkv=4097, Hq=4097), 2),
     (dict(D=64), 0), (dict(D=128), 0), (dict(D=96), 2), (dict(D=512), 2), (dict(L_max=0), 2), (dict(L_max=1 << 26), 0),
