@@ -105,5 +105,115 @@ struct Runs {
   }
 };
 
+// Runs are cut on a scale of places, where a tile with units takes `cost` more
+// places than units, before its first: what beginning and ending a tile costs
+// a run.
+__device__ inline long long places_before(int n, int len, int r, int RT, int KT, int cost, int k) {
+  return units_before(n, len, r, RT, KT, k) + (long long)cost * max(k - empty_tiles(n, len, r, RT), 0);
+}
+
+// The first unit at or after a place: unit i of the nb of row tile rt of KV head
+// g of sequence b (b = -1: past the last), the units before it, and its tile's
+// number in the order (sequence, KV head, row tile).
+struct Place {
+  int b, g, rt, i, nb, tile;
+  long long units;
+};
+
+// By one warp: checks the tables (false if they break the rules), counts the
+// call's places and finds that of run c's start.
+__device__ inline bool find_run(const int32_t* offsets, const int32_t* lens, int B, int T, int Hkv, int L_max, int r,
+                                int RT, int KT, int cost, int c, int C, Place* out, long long* start) {
+  const int lane = threadIdx.x & 31;
+  long long total = 0, before = 0, units = 0, at = 0;
+  int tiles = 0;
+  bool bad = false;
+  Place k{-1, 0, 0, 0, 0, 0, 0};
+  // Pass 0 counts, pass 1 searches: one copy of the code, which runs cold.
+#pragma unroll 1
+  for (int base = 0, pass = 0; base < B;) {
+    const int b = base + lane;
+    long long v = 0, w = 0;  // this lane's sequence: places, units
+    int nt = 0;
+    if (b < B) {
+      const int lo = __ldg(offsets + b), hi = __ldg(offsets + b + 1), len = __ldg(lens + b);
+      if (offsets_bad(lo, hi, b, B, T) || len < 0 || len > L_max) {
+        bad = true;
+      } else {
+        nt = seq_tiles(hi - lo, r, RT);
+        w = units_before(hi - lo, len, r, RT, KT, nt) * Hkv;
+        v = w + (long long)cost * (nt - empty_tiles(hi - lo, len, r, RT)) * Hkv;
+        nt *= Hkv;
+      }
+    }
+    long long vi = v, wi = w;
+    int ti = nt;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, vi, o), y = __shfl_up_sync(0xffffffffu, wi, o);
+      const int z = __shfl_up_sync(0xffffffffu, ti, o);
+      if (lane >= o) {
+        vi += x;
+        wi += y;
+        ti += z;
+      }
+    }
+    const long long all = __shfl_sync(0xffffffffu, vi, 31);
+    base += 32;
+    if (pass == 0) {
+      total += all;
+      if (base < B) continue;
+      bad = __any_sync(0xffffffffu, bad);
+      if (bad) break;
+      at = Runs(total, C).start(c);
+      pass = 1;
+      if (B > 32) {  // else the search goes on with this chunk
+        base = 0;
+        continue;
+      }
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, before + vi > at);
+    if (hit) {
+      const int L = __ffs(hit) - 1;
+      k.b = base - 32 + L;
+      long long off = at - (before + __shfl_sync(0xffffffffu, vi - v, L));
+      const long long per = div_small(__shfl_sync(0xffffffffu, v, L), Hkv);
+      units += __shfl_sync(0xffffffffu, wi - w, L);
+      tiles += __shfl_sync(0xffffffffu, ti - nt, L);
+      const long long per_units = div_small(__shfl_sync(0xffffffffu, w, L), Hkv);
+      const int lo = __ldg(offsets + k.b), n = __ldg(offsets + k.b + 1) - lo, len = __ldg(lens + k.b);
+      const int all_tiles = seq_tiles(n, r, RT);
+      k.g = (int)div_small(off, per);
+      off -= k.g * per;
+      // the last tile whose first place is at or before off, 32 candidates a
+      // round (tiles without units share their successor's first place: the
+      // search ends on the last of them, which has some)
+      int a = 0, z = all_tiles;
+#pragma unroll 1
+      while (z - a > 1) {
+        const int step = (z - a + 31) / 32, cand = a + lane * step;
+        const bool in = cand < z && places_before(n, len, r, RT, KT, cost, cand) <= off;
+        const int last = 31 - __clz(__ballot_sync(0xffffffffu, in));
+        a += last * step;
+        z = min(z, a + step);
+      }
+      k.rt = a;
+      k.nb = tile_units(n, len, r, RT, KT, a);
+      const long long first = units_before(n, len, r, RT, KT, a);
+      k.i = max((int)(off - first) - cost * (max(a - empty_tiles(n, len, r, RT), 0) + 1), 0);
+      units += k.g * per_units + first + k.i;
+      k.tile = tiles + k.g * all_tiles + a;
+      break;
+    }
+    before += all;
+    units += __shfl_sync(0xffffffffu, wi, 31);
+    tiles += __shfl_sync(0xffffffffu, ti, 31);
+  }
+  k.units = units;
+  *out = k;
+  *start = at;
+  return !bad;
+}
+
 }  // namespace kv8
 }  // namespace bgmoe

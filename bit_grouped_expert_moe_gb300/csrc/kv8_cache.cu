@@ -13,7 +13,7 @@ namespace kv8 {
 
 constexpr int kThreads = 256;
 constexpr int kReadTokens = 64;  // packed tokens per tile of the read kernel
-constexpr int kReadBlocks = 6;   // its thread blocks per SM, at most
+constexpr int kReadBlocks = 4;   // its thread blocks per SM, at most
 
 struct CacheArgs {
   uint8_t* codes[2];    // K, V
@@ -26,6 +26,14 @@ struct CacheArgs {
   int B, T, Hkv, L_max, nblk;
   int stride;           // elements from token to token of x
 };
+
+// Launched with programmatic dependent launch: everything below may read what
+// earlier kernels wrote or overwrite what they read, so it waits for them;
+// then the next kernel's blocks may be set up (they wait in turn).
+__device__ __forceinline__ void after_predecessors() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
 
 __device__ __forceinline__ void flag(int32_t* status, int32_t what) {
   if (status) atomicCAS(status, 0, what);
@@ -68,6 +76,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_write_kernel(const CacheArgs 
   constexpr int kPer = W::kPer, kTU = W::kUnitThreads;
   __shared__ int s_b[W::kUnits], s_lo[W::kUnits], s_n[W::kUnits], s_start[W::kUnits];
   __shared__ uint32_t s_max[2][kThreads / 32];
+  after_predecessors();
   // units in the order (number, head, K or V)
   const int per = 2 * p.Hkv, first = blockIdx.x * W::kUnits, local = threadIdx.x / kTU, tu = threadIdx.x % kTU;
   const int item = first + local, unit = item / per, g = (item - unit * per) >> 1, kv = item & 1;
@@ -195,15 +204,16 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_write_kernel(const CacheArgs 
 
 // Thread blocks walk over tiles of 64 packed tokens of one KV head, K or V. The
 // tables are checked once; a tile's tokens find their sequence and position
-// (by bisection of the offsets), then each thread turns 16-byte pieces of
-// codes into 32 bytes of bf16. The next tile's codes are asked for before
+// (by bisection of the offsets), then each thread turns 8-byte pieces of codes
+// into 16 bytes of bf16, so a warp's stores fill whole sectors. The next tile's codes are asked for before
 // this one's are converted.
 template <int D, int kBlock, bool kE4m3>
 __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const CacheArgs p) {
-  constexpr int kRow = D / 16;                          // pieces per token
+  constexpr int kRow = D / 8;                           // pieces per token
   constexpr int kPer = kReadTokens * kRow / kThreads;   // pieces per thread
   __shared__ long long s_code[2][kReadTokens];          // first code of each token (head g), in bytes
   __shared__ long long s_scale[2][kReadTokens];         // its scale
+  after_predecessors();
   if (tables_bad(p, [](int, int, int, int) {})) {
     if (threadIdx.x == 0) flag(p.status, (int32_t)MOE_ERR_INVALID_ARG);
     return;
@@ -223,7 +233,7 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const CacheArgs p) {
     s_code[buf][threadIdx.x] = (pair * p.L_max + pos) * D;
     s_scale[buf][threadIdx.x] = pair * p.nblk + pos / kBlock;
   };
-  uint4 w[kPer];
+  uint2 w[kPer];
   float s[kPer];
   auto load = [&](int tile, int buf) {
     const int nt = min(kReadTokens, p.T - tile / per * kReadTokens);
@@ -232,10 +242,10 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const CacheArgs p) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int piece = threadIdx.x + i * kThreads, t = piece / kRow, c = piece % kRow;
-      w[i] = make_uint4(0, 0, 0, 0);
+      w[i] = make_uint2(0, 0);
       s[i] = 0.f;
       if (t < nt) {
-        w[i] = __ldcs(reinterpret_cast<const uint4*>(codes + s_code[buf][t] + c * 16));
+        w[i] = __ldcs(reinterpret_cast<const uint2*>(codes + s_code[buf][t] + c * 8));
         s[i] = __ldg(scales + s_scale[buf][t]);
       }
     }
@@ -254,20 +264,18 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const CacheArgs p) {
     for (int i = 0; i < kPer; ++i) {
       const int piece = threadIdx.x + i * kThreads, t = piece / kRow, c = piece % kRow;
       if (t0 + t >= p.T) continue;
-      const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-      uint32_t o[8];
+      uint32_t o[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 2; ++j) {
         float f[4];
-        decode4<kE4m3>(in[j], f);
+        decode4<kE4m3>(j ? w[i].y : w[i].x, f);
         const __nv_bfloat162 a = __floats2bfloat162_rn(f[0] * s[i], f[1] * s[i]);
         const __nv_bfloat162 z = __floats2bfloat162_rn(f[2] * s[i], f[3] * s[i]);
         o[2 * j] = *reinterpret_cast<const uint32_t*>(&a);
         o[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&z);
       }
-      uint4* to = reinterpret_cast<uint4*>(out + ((size_t)(t0 + t) * p.Hkv + g) * D + c * 16);
-      __stcs(to, make_uint4(o[0], o[1], o[2], o[3]));
-      __stcs(to + 1, make_uint4(o[4], o[5], o[6], o[7]));
+      __stcs(reinterpret_cast<uint4*>(out + ((size_t)(t0 + t) * p.Hkv + g) * D + c * 8),
+             make_uint4(o[0], o[1], o[2], o[3]));
     }
     if (next < tiles) load(next, buf ^ 1);
   }
@@ -295,24 +303,37 @@ bool cache_ok(const moe_kv8_cache* c) {
 
 namespace {
 
+template <typename Kernel>
+cudaError_t launch(Kernel kernel, long long grid, const CacheArgs& p, cudaStream_t s) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 template <int D, int kBlock, bool kE4m3>
-void launch_one(const CacheArgs& p, bool write, int sms, cudaStream_t s) {
+cudaError_t launch_one(const CacheArgs& p, bool write, int sms, cudaStream_t s) {
   if (write) {
     const long long items = ((long long)p.T / kBlock + 2 * p.B) * 2 * p.Hkv;
     constexpr int kUnits = WriteCfg<D, kBlock>::kUnits;
-    kv8_write_kernel<D, kBlock, kE4m3><<<(unsigned)((items + kUnits - 1) / kUnits), kThreads, 0, s>>>(p);
-  } else {
-    const long long tiles = (long long)((p.T + kReadTokens - 1) / kReadTokens) * 2 * p.Hkv;
-    const long long most = (long long)sms * kReadBlocks;
-    kv8_read_kernel<D, kBlock, kE4m3><<<(unsigned)(tiles < most ? tiles : most), kThreads, 0, s>>>(p);
+    return launch(kv8_write_kernel<D, kBlock, kE4m3>, (items + kUnits - 1) / kUnits, p, s);
   }
+  const long long tiles = (long long)((p.T + kReadTokens - 1) / kReadTokens) * 2 * p.Hkv;
+  const long long most = (long long)sms * kReadBlocks;
+  return launch(kv8_read_kernel<D, kBlock, kE4m3>, tiles < most ? tiles : most, p, s);
 }
 
 template <int D, bool kE4m3>
-void launch_block(const CacheArgs& p, bool write, int block, int sms, cudaStream_t s) {
-  if (block == 16) launch_one<D, 16, kE4m3>(p, write, sms, s);
-  else if (block == 32) launch_one<D, 32, kE4m3>(p, write, sms, s);
-  else launch_one<D, 64, kE4m3>(p, write, sms, s);
+cudaError_t launch_block(const CacheArgs& p, bool write, int block, int sms, cudaStream_t s) {
+  return block == 16   ? launch_one<D, 16, kE4m3>(p, write, sms, s)
+         : block == 32 ? launch_one<D, 32, kE4m3>(p, write, sms, s)
+                       : launch_one<D, 64, kE4m3>(p, write, sms, s);
 }
 
 moe_status cache_call(const moe_kv8_shape* shape, const moe_kv8_cache* cache, const int32_t* offsets,
@@ -352,13 +373,11 @@ moe_status cache_call(const moe_kv8_shape* shape, const moe_kv8_cache* cache, co
   if (sms <= 0) return cuda_fail(cudaErrorInvalidDevice, "device query");
   auto go = [&](auto d) {
     constexpr int D = decltype(d)::value;
-    if (e4m3) launch_block<D, true>(p, write, s.block, sms, st);
-    else launch_block<D, false>(p, write, s.block, sms, st);
+    return e4m3 ? launch_block<D, true>(p, write, s.block, sms, st) : launch_block<D, false>(p, write, s.block, sms, st);
   };
-  if (s.D == 64) go(std::integral_constant<int, 64>{});
-  else if (s.D == 128) go(std::integral_constant<int, 128>{});
-  else go(std::integral_constant<int, 256>{});
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = s.D == 64    ? go(std::integral_constant<int, 64>{})
+                        : s.D == 128 ? go(std::integral_constant<int, 128>{})
+                                     : go(std::integral_constant<int, 256>{});
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, write ? "cache write launch" : "cache read launch");
 }
 

@@ -68,6 +68,9 @@ constexpr int unit_positions(int D) { return D == 256 ? 64 : 128; }
 constexpr int kConsumers = 8;       // warps
 constexpr int kThreads = (kConsumers + 1) * 32;
 constexpr int kMaxCtas = 256;       // workspace bound on the grid
+// Beginning and ending a tile (Q, the warps' fold, the partial state) costs a
+// run about as much as four units: 3 us against 0.7 us a unit of 32 KB.
+constexpr int kTileCost = 4;
 constexpr long long kTimeoutNs = 1000000000ll;
 constexpr float kMinusBig = -1e30f; // running-max start: finite, so 2^(m - m_new) is never NaN
 // A row's m is raised to its largest score only when a score passes it by
@@ -121,17 +124,13 @@ struct Params {
   const int32_t* offsets;
   const int32_t* lens;
   float* part;       // [slots][RT] m, then [slots][RT] l, then [slots][RT][D] O
+  int4* info;        // [C]: the tile and unit a block's run starts at: {tile, has units, unit}
   int32_t* flags;    // [C]: every grid block's outcome (0 or a moe_status), written each call
   long long slots;
   float scale_log2;
   int B, T, Hq, Hkv, L_max, nblk, shift, q_stride;  // shift: log2 of the cache's block
   long long timeout_ns;
 };
-
-// Units of a whole sequence and KV head.
-__device__ __forceinline__ long long seq_units(int n, int len, int r, int RT, int kPos) {
-  return units_before(n, len, r, RT, kPos, seq_tiles(n, r, RT));
-}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -258,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Ctl<kStages>* ctl = reinterpret_cast<Ctl<kStages>*>(smem + S::kCtlOffset);
   static_assert(sizeof(Ctl<kStages>) <= 2816, "control block");
   float* mrg = reinterpret_cast<float*>(smem + S::kFoldOffset);
-  __shared__ long long s_lo, s_hi;
+  __shared__ long long s_unit[2];  // units before the run's start and end
   __shared__ Cursor s_cur;
   __shared__ int s_bad;
 
@@ -287,91 +286,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   // reads the tables before its own wait.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (warp == 0) {
-    // Check the tables and count the units (pass 0), then find where this
-    // block's run starts (pass 1): one copy of the code, which runs cold.
-    long long total = 0, acc = 0, lo = 0, hi = 0;
-    int tiles = 0;
-    bool bad = false;
-#pragma unroll 1
-    for (int base = 0, pass = 0; base < p.B;) {
-      const int b = base + lane;
-      long long v = 0;
-      int nt = 0;
-      if (b < p.B) {
-        const int at = __ldg(p.offsets + b), end = __ldg(p.offsets + b + 1), len = __ldg(p.lens + b);
-        if (offsets_bad(at, end, b, p.B, p.T) || len < 0 || len > p.L_max) {
-          bad = true;
-        } else {
-          v = seq_units(end - at, len, r, RT, kPos) * p.Hkv;
-          nt = seq_tiles(end - at, r, RT) * p.Hkv;
-        }
-      }
-      long long incl = v;
-      int tincl = nt;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long t = __shfl_up_sync(0xffffffffu, incl, o);
-        const int u = __shfl_up_sync(0xffffffffu, tincl, o);
-        if (lane >= o) {
-          incl += t;
-          tincl += u;
-        }
-      }
-      const long long all = __shfl_sync(0xffffffffu, incl, 31);
-      base += 32;
-      if (pass == 0) {
-        total += all;
-        if (base < p.B) continue;
-        // the last chunk: the runs are known; with one chunk the search goes on with it
-        bad = __any_sync(0xffffffffu, bad);
-        const Runs runs(total, C);
-        lo = runs.start(c);
-        hi = runs.start(c + 1);
-        if (bad || lo >= hi) break;
-        pass = 1;
-        if (p.B > 32) {
-          base = 0;
-          continue;
-        }
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, acc + incl > lo);
-      if (hit) {
-        if (lane == __ffs(hit) - 1) {
-          Cursor k;
-          k.b = b;
-          k.sequence(p);
-          long long off = lo - (acc + incl - v);
-          const long long per = div_small(v, p.Hkv);
-          k.g = (int)div_small(off, per);
-          off -= k.g * per;
-          k.rt = 0;
-          k.nb = tile_units(k.n, k.len, r, RT, kPos, 0);
-          while (off >= k.nb) {
-            off -= k.nb;
-            k.nb = tile_units(k.n, k.len, r, RT, kPos, ++k.rt);
-          }
-          k.i = (int)off;
-          k.tile = tiles + tincl - nt + k.g * (nt / p.Hkv) + k.rt;
-          s_cur = k;
-        }
-        break;
-      }
-      acc += all;
-      tiles += __shfl_sync(0xffffffffu, tincl, 31);
-    }
+  if (warp < 2) {  // the run's start and its end
+    Place k;
+    long long at;
+    const bool ok = find_run(p.offsets, p.lens, p.B, p.T, p.Hkv, p.L_max, r, RT, kPos, kTileCost, c + warp, C, &k, &at);
     if (lane == 0) {
-      s_lo = lo;
-      s_hi = hi;
-      s_bad = bad;
+      s_unit[warp] = k.units;
+      if (warp == 0) {
+        s_bad = !ok;
+        Cursor cur{};
+        if (ok && k.b >= 0) {
+          cur.b = k.b;
+          cur.sequence(p);
+          cur.g = k.g;
+          cur.rt = k.rt;
+          cur.i = k.i;
+          cur.nb = k.nb;
+          cur.tile = k.tile;
+        }
+        s_cur = cur;
+      }
     }
   }
   __syncthreads();
-  if (s_bad || s_lo >= s_hi) {
-    if (threadIdx.x == 0) p.flags[c] = s_bad ? (int32_t)MOE_ERR_INVALID_ARG : 0;
-    return;
+  const bool live = !s_bad && s_unit[0] < s_unit[1];
+  if (threadIdx.x == 0) {
+    p.info[c] = make_int4(s_cur.tile, live, s_cur.i, 0);
+    if (!live) p.flags[c] = s_bad ? (int32_t)MOE_ERR_INVALID_ARG : 0;
   }
-  const long long lo = s_lo, hi = s_hi;
+  if (!live) return;
+  const int U = (int)(s_unit[1] - s_unit[0]);
   Cursor cur = s_cur;
 
   volatile int* abort_flag = &ctl->abort;
@@ -390,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int s = 0, ph = 0, issued = 0;
     bool go = warp_wait(&ctl->go, 0);
 #pragma unroll 1
-    for (long long j = lo; go && j < hi; ++j) {
+    for (int j = 0; go && j < U; ++j) {
       if (issued >= kStages && !warp_wait(&ctl->empty[s], ph ^ 1)) break;
       if (elect_one()) {
         uint8_t* st = smem + s * S::kStageBytes;
@@ -541,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fetch_q(cur);
     {
       Cursor own = cur;
-      if (S::kRowSplit == 1 && part == 1 && lo + 1 < hi) own.advance(p, r, RT, kPos);
+      if (S::kRowSplit == 1 && part == 1 && U > 1) own.advance(p, r, RT, kPos);
       load_scales(own, skn, svn);
     }
     __syncwarp();
@@ -550,13 +494,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     int s = 0, ph = 0;
 #pragma unroll 1
-    for (long long j = lo; good && j < hi; ++j) {
+    for (int j = 0; good && j < U; ++j) {
       Cursor nxt = cur;
-      if (j + 1 < hi) {
+      if (j + 1 < U) {
         nxt.advance(p, r, RT, kPos);
         if (nxt.tile != cur.tile) fetch_q(nxt);  // it travels while this unit is computed
       }
-      const bool mine = S::kRowSplit == 2 || ((int)(j - lo) & 1) == part;
+      const bool mine = S::kRowSplit == 2 || (j & 1) == part;
       float sk[kMT], sv[kMT];
       if (mine) {
 #pragma unroll
@@ -564,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           sk[t] = skn[t];
           sv[t] = svn[t];
         }
-        if (j + S::kStride < hi) {  // the scales of this warp's next unit travel, too
+        if (j + S::kStride < U) {  // the scales of this warp's next unit travel, too
           Cursor own = nxt;
           if (S::kStride == 2) own.advance(p, r, RT, kPos);
           load_scales(own, skn, svn);
@@ -699,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ph ^= 1;
       }
 
-      if (nxt.tile != cur.tile || j == hi - 1) {
+      if (nxt.tile != cur.tile || j == U - 1) {
         // ---- the run leaves this tile: fold the states of the warps with the
         // same rows. All take the largest m; then, lane by lane, the upper half
         // of the warps hands its accumulators to the lower, and every thread
@@ -787,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 2; ++k) p.part[slot * RT + rows0 + 8 * nt + 2 * lane + k] = m[nt][k];
         }
         cur = nxt;
-        if (j + 1 < hi) good = place_q(cur);
+        if (j + 1 < U) good = place_q(cur);
       } else {
         cur = nxt;
       }
@@ -801,6 +745,7 @@ struct MergeParams {
   const int32_t* offsets;
   const int32_t* lens;
   const float* part;
+  const int4* info;
   const int32_t* flags;
   uint16_t* o;
   int32_t* status;
@@ -825,39 +770,22 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_kernel(const Merge
   const int t = blockIdx.x / p.Hq, h = blockIdx.x - t * p.Hq;
   const int lane = threadIdx.x & 31, f4 = threadIdx.x & 15, sl = threadIdx.x >> 4;
   __shared__ float s_m[kMergeLanes], s_l[kMergeLanes], s_o[kMergeLanes][64];
-  const int kPos = unit_positions(D);
-  __shared__ int s_first;
-  // every warp: the sequence, and the units and tiles before it
-  long long before = 0, total = 0;
+  __shared__ int s_range[2], s_first;
+  // every warp: the sequence, and the tiles before it
   int tiles = 0, b = -1, lo = 0, n = 0, len = 0;
   bool bad = false;
+#pragma unroll 1
   for (int base = 0; base < p.B; base += 32) {
     const int bb = base + lane;
-    int lo1 = 0, hi1 = 0, len1 = 0, nt = 0;
-    long long v = 0;
+    int lo1 = 0, hi1 = 0, len1 = 0;
     if (bb < p.B) {
       lo1 = __ldg(p.offsets + bb);
       hi1 = __ldg(p.offsets + bb + 1);
       len1 = __ldg(p.lens + bb);
-      if (offsets_bad(lo1, hi1, bb, p.B, p.T) || len1 < 0 || len1 > p.L_max) {
-        bad = true;
-      } else {
-        v = seq_units(hi1 - lo1, len1, r, RT, kPos);
-        nt = seq_tiles(hi1 - lo1, r, RT);
-      }
+      bad |= offsets_bad(lo1, hi1, bb, p.B, p.T) || len1 < 0 || len1 > p.L_max;
     }
     const unsigned hit = __ballot_sync(0xffffffffu, lo1 <= t && t < hi1);
-    long long vb = hi1 <= t ? v : 0;
-    int tb = hi1 <= t ? nt : 0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      v += __shfl_xor_sync(0xffffffffu, v, o);
-      vb += __shfl_xor_sync(0xffffffffu, vb, o);
-      tb += __shfl_xor_sync(0xffffffffu, tb, o);
-    }
-    total += v;
-    before += vb;
-    tiles += tb;
+    tiles += __reduce_add_sync(0xffffffffu, hi1 <= t ? seq_tiles(hi1 - lo1, r, RT) : 0);
     if (hit) {
       const int L = __ffs(hit) - 1;
       b = base + L;
@@ -866,30 +794,33 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_kernel(const Merge
       len = __shfl_sync(0xffffffffu, len1, L);
     }
   }
-  bad = __any_sync(0xffffffffu, bad);
-  int c0 = 0, c1 = -1;
-  size_t slot0 = 0;
-  if (!bad && b >= 0) {
-    const int g = h / r, row = (t - lo) * r + h - g * r, rt = row / RT, nb = tile_units(n, len, r, RT, kPos, rt);
-    const Runs runs(total * p.Hkv, C);
-    const long long start = before * p.Hkv + seq_units(n, len, r, RT, kPos) * g + units_before(n, len, r, RT, kPos, rt);
-    slot0 = ((size_t)tiles * p.Hkv + (size_t)g * seq_tiles(n, r, RT) + rt) * RT + row - rt * RT;
-    if (nb > 0 && len - n + (t - lo) >= 0) {
-      c0 = runs.of(start);
-      c1 = runs.of(start + nb - 1);
-    }
+  bad = __any_sync(0xffffffffu, bad) || b < 0;
+  const int g = h / r, row = (t - lo) * r + h - g * r, rt = row / RT;
+  const int tile = bad ? 0 : tiles * p.Hkv + g * seq_tiles(n, r, RT) + rt;
+  const size_t slot0 = bad ? 0 : (size_t)tile * RT + row - rt * RT;
+  if (threadIdx.x == 0) {
+    s_range[0] = s_range[1] = -1;
+    s_first = C;
   }
+  __syncthreads();
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (blockIdx.x == 0 && blockIdx.y == 0) {
-    // the call's status: the outcome of the lowest-numbered grid block that failed
-    if (threadIdx.x == 0) s_first = C;
-    __syncthreads();
-    for (int cc = threadIdx.x; cc < C; cc += kMergeWarps * 32)
-      if (__ldcg(p.flags + cc) != 0) atomicMin(&s_first, cc);
-    __syncthreads();
-    if (threadIdx.x == 0) *p.status = s_first == C ? 0 : __ldcg(p.flags + s_first);
+  // The runs that cover the tile: from the last one that starts at or before
+  // its first unit to the last one that starts in it. And the call's status:
+  // the outcome of the lowest-numbered grid block that failed.
+#pragma unroll 1
+  for (int cc = threadIdx.x; cc < C; cc += kMergeWarps * 32) {
+    const int4 x = __ldcg(p.info + cc);
+    if (__ldcg(p.flags + cc) != 0) atomicMin(&s_first, cc);
+    if (x.y && x.x <= tile) {
+      atomicMax(&s_range[1], cc);
+      if (x.x < tile || x.z == 0) atomicMax(&s_range[0], cc);
+    }
   }
+  __syncthreads();
+  if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) *p.status = s_first == C ? 0 : __ldcg(p.flags + s_first);
+  const bool seen = len - n + (t - lo) >= 0;  // else no visible position
+  const int c0 = seen ? s_range[0] : 0, c1 = seen ? s_range[1] : -1;
   if (bad) return;
 
   const float* pm = p.part;
@@ -1029,7 +960,7 @@ size_t split_workspace_bytes(const moe_kv8_shape& s) {
   using namespace split;
   const int r = s.Hq / s.Hkv, RT = 8 * groups(s.B, s.T, r, s.D);
   const size_t slots = (size_t)kMaxCtas + max_tiles(s.B, s.T, r, s.Hkv, RT);
-  return 256 + kMaxCtas * sizeof(int32_t) + slots * RT * (2 + (size_t)s.D) * sizeof(float);
+  return 256 + kMaxCtas * (sizeof(int32_t) + sizeof(int4)) + slots * RT * (2 + (size_t)s.D) * sizeof(float);
 }
 
 moe_status launch_split(const AttnArgs& a, cudaStream_t stream) {
@@ -1045,10 +976,11 @@ moe_status launch_split(const AttnArgs& a, cudaStream_t stream) {
 
   int32_t* status = static_cast<int32_t*>(a.workspace);
   int32_t* flags = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(a.workspace) + 256);
-  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + 256 + kMaxCtas * sizeof(int32_t));
+  int4* info = reinterpret_cast<int4*>(flags + kMaxCtas);
+  float* part = reinterpret_cast<float*>(info + kMaxCtas);
   const long long slots = kMaxCtas + max_tiles(a.B, a.T, r, a.Hkv, RT);
   const int shift = a.block == 16 ? 4 : a.block == 32 ? 5 : 6;
-  const Params prm{a.q, a.ks, a.vs, a.offsets, a.lens, part, flags, slots, a.scale_log2, a.B, a.T, a.Hq, a.Hkv,
+  const Params prm{a.q, a.ks, a.vs, a.offsets, a.lens, part, info, flags, slots, a.scale_log2, a.B, a.T, a.Hq, a.Hkv,
                    a.L_max, a.nblk, shift, a.q_stride, kTimeoutNs};
   auto go = [&](auto fp8) {
     constexpr bool kE4m3 = decltype(fp8)::value;
@@ -1059,7 +991,7 @@ moe_status launch_split(const AttnArgs& a, cudaStream_t stream) {
   e = a.e4m3 ? go(std::true_type{}) : go(std::false_type{});
   if (e != cudaSuccess) return cuda_fail(e, "split kernel launch");
 
-  const MergeParams mp{a.offsets, a.lens, part, flags, a.o, status, slots, a.B, a.T, a.Hq, a.Hkv, a.D, a.L_max, RT,
+  const MergeParams mp{a.offsets, a.lens, part, info, flags, a.o, status, slots, a.B, a.T, a.Hq, a.Hkv, a.D, a.L_max, RT,
                        grid};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.T * (unsigned)a.Hq, (unsigned)(a.D / 64));

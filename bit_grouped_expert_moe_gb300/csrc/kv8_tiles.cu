@@ -121,18 +121,12 @@ struct Ctl {
   float mx[2][2][kRows];  // [unit parity][half]
 };
 
-struct RunInfo {  // where a block's run starts, for the merge kernel
-  long long places; // of the call (0: nothing to do or bad tables)
-  long long lo;     // the run's first place
-  int b, g, rt, i, nb;
-  int live;         // there is a unit at or after it
+// Where a block's run starts, for the merge kernel.
+struct RunInfo {
+  int tile;  // number of its first unit's tile
+  int live;  // the run has units
+  int b, g, rt, i;
 };
-
-// Places of the tiles before tile k of a sequence: their units, and kTileCost
-// for each that has units.
-__device__ __forceinline__ long long places_before(int n, int len, int r, int k) {
-  return units_before(n, len, r, kRows, kKeys, k) + (long long)kTileCost * max(k - empty_tiles(n, len, r, kRows), 0);
-}
 
 struct Params {
   const uint16_t* q;
@@ -397,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
   static_assert(sizeof(Ctl) <= 5120, "control block");
   __shared__ long long s_unit[2];  // units before the run's start and end
   __shared__ Cursor s_cur;
-  __shared__ int s_bad;
+  __shared__ int s_bad, s_tile;
 
   // The warp's number through a shuffle, which the compiler knows to be
   // uniform: the roles' loops then run on uniform registers, where the MMA
@@ -430,96 +424,36 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
   // this one, then let this call's merge launch (it waits in turn).
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (warp == 1 || warp == 2) {
-    // Check the tables, count the call's places and find the unit at the run's
-    // start (warp 1) and end (warp 2).
-    long long total = 0;
-    bool bad = false;
-    for (int base = 0; base < p.B; base += 32) {
-      const int b = base + lane;
-      long long v = 0;
-      if (b < p.B) {
-        const int lo = __ldg(p.offsets + b), hi = __ldg(p.offsets + b + 1), len = __ldg(p.lens + b);
-        if (offsets_bad(lo, hi, b, p.B, p.T) || len < 0 || len > p.L_max) bad = true;
-        else v = places_before(hi - lo, len, r, seq_tiles(hi - lo, r, kRows));
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      total += v;
-    }
-    bad = __any_sync(0xffffffffu, bad);
-    total *= p.Hkv;
-    const long long at = Runs(total, C).start(c + warp - 1);
-    Cursor k{};
-    long long before = 0;  // units before the place
-    if (!bad) {
-      long long acc = 0, off = 0, per = 0, units = 0;
-      k.b = -1;            // at == total: past the last
-      for (int base = 0; base < p.B; base += 32) {
-        const int b = base + lane;
-        long long v = 0, w = 0;
-        if (b < p.B) {
-          const int n = __ldg(p.offsets + b + 1) - __ldg(p.offsets + b), len = __ldg(p.lens + b);
-          w = units_before(n, len, r, kRows, kKeys, seq_tiles(n, r, kRows)) * p.Hkv;
-          v = places_before(n, len, r, seq_tiles(n, r, kRows)) * p.Hkv;
-        }
-        long long incl = v, wincl = w;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long x = __shfl_up_sync(0xffffffffu, incl, o), y = __shfl_up_sync(0xffffffffu, wincl, o);
-          if (lane >= o) {
-            incl += x;
-            wincl += y;
-          }
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, acc + incl > at);
-        if (hit) {
-          const int L = __ffs(hit) - 1;
-          k.b = base + L;
-          off = at - (acc + __shfl_sync(0xffffffffu, incl - v, L));
-          per = __shfl_sync(0xffffffffu, v, L) / p.Hkv;
-          units = __shfl_sync(0xffffffffu, w, L) / p.Hkv;
-          before += __shfl_sync(0xffffffffu, wincl - w, L);
-          break;
-        }
-        acc += __shfl_sync(0xffffffffu, incl, 31);
-        before += __shfl_sync(0xffffffffu, wincl, 31);
-      }
-      if (k.b >= 0) {
-        k.sequence(p);
-        k.g = (int)(off / per);
-        off -= k.g * per;
-        // the last tile whose first place is at or before off, 32 candidates a round
-        int a = 0, z = seq_tiles(k.n, r, kRows);
-        while (z - a > 1) {
-          const int step = (z - a + 31) / 32, cand = a + lane * step;
-          const bool in = cand < z && places_before(k.n, k.len, r, cand) <= off;
-          const int last = 31 - __clz(__ballot_sync(0xffffffffu, in));
-          a += last * step;
-          z = min(z, a + step);
-        }
-        // tiles without units share their successor's first place: the
-        // search ends on the last of them, which has some
-        k.rt = a;
-        k.i = max((int)(off - places_before(k.n, k.len, r, a)) - kTileCost, 0);
-        k.nb = tile_units(k.n, k.len, r, kRows, kKeys, a);
-        before += k.g * units + units_before(k.n, k.len, r, kRows, kKeys, a) + k.i;
-      }
-    }
+  if (warp == 1 || warp == 2) {  // the run's start and its end
+    Place k;
+    long long at;
+    const bool ok = find_run(p.offsets, p.lens, p.B, p.T, p.Hkv, p.L_max, r, kRows, kKeys, kTileCost, c + warp - 1, C,
+                             &k, &at);
     if (lane == 0) {
-      s_unit[warp - 1] = before;
+      s_unit[warp - 1] = k.units;
       if (warp == 1) {
-        s_bad = bad;
-        s_cur = k;
-        p.info[c] = RunInfo{bad ? 0 : total, at, k.b, k.g, k.rt, k.i, k.nb, !bad && k.b >= 0};
+        s_bad = !ok;
+        Cursor cur{};
+        if (ok && k.b >= 0) {
+          cur.b = k.b;
+          cur.sequence(p);
+          cur.g = k.g;
+          cur.rt = k.rt;
+          cur.i = k.i;
+          cur.nb = k.nb;
+        }
+        s_cur = cur;
+        s_tile = k.tile;
       }
     }
   }
   __syncthreads();
-  if (s_bad) {
-    if (threadIdx.x == 0) p.flags[c] = (int32_t)MOE_ERR_INVALID_ARG;
-    return;
+  if (threadIdx.x == 0) {
+    const bool live = !s_bad && s_unit[0] < s_unit[1];
+    p.info[c] = RunInfo{s_tile, live, s_cur.b, s_cur.g, s_cur.rt, s_cur.i};
+    if (!live) p.flags[c] = s_bad ? (int32_t)MOE_ERR_INVALID_ARG : 0;
   }
+  if (s_bad) return;
   // Queries that see nothing (more queries than positions): o = 0.
   for (int b = c; b < p.B; b += C) {
     const int lo = __ldg(p.offsets + b), hi = __ldg(p.offsets + b + 1), len = __ldg(p.lens + b);
@@ -527,10 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
     uint4* z = reinterpret_cast<uint4*>(p.o + (size_t)lo * p.Hq * D);
     for (size_t i = threadIdx.x; i < pieces; i += kThreads) z[i] = make_uint4(0u, 0u, 0u, 0u);
   }
-  if (s_unit[0] >= s_unit[1]) {
-    if (threadIdx.x == 0) p.flags[c] = 0;
-    return;
-  }
+  if (s_unit[0] >= s_unit[1]) return;
   if (warp == kMmaWarp) {
     tmem_alloc(&ctl->tmem, kTmemCols);
     tmem_relinquish();
@@ -1010,7 +941,7 @@ constexpr int kMergeThreads = 32 * kMergeRows;
 // tile's rows 8 y .. + 7. The first run of a tile left its state in its second
 // slot (a tile that the run's end cuts), the others in their first.
 __global__ void __launch_bounds__(kMergeThreads) kv8_tiles_merge_kernel(const MergeParams p) {
-  __shared__ int s_first;
+  __shared__ int s_first, s_c0, s_later;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x, C = p.C, t = threadIdx.x, lane = t & 31;
@@ -1023,13 +954,28 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_tiles_merge_kernel(const Me
     __syncthreads();
     if (t == 0) *p.status = s_first == C ? 0 : __ldcg(p.flags + s_first);
   }
+  // Run c is the tile's second if it starts inside the tile and the last live
+  // run before it does not, or does at the first unit; the runs after it that
+  // start in the tile follow one another.
   const RunInfo f = p.info[c];
   if (!f.live || f.i == 0) return;
-  const long long N = f.places, start = f.lo - f.i;  // the place of the tile's first unit
-  const Runs runs(N, C);
-  const int c0 = runs.of(start);
-  if (c != c0 + 1) return;             // a later one of the tile's runs
-  const int c1 = runs.of(start + f.nb - 1);
+  if (t == 0) s_c0 = -1;
+  __syncthreads();
+  int later = 0;
+  for (int cc = t; cc < C; cc += kMergeThreads) {
+    const int2 x = __ldcg(reinterpret_cast<const int2*>(&p.info[cc]));  // tile, live
+    if (!x.y) continue;
+    if (cc < c) atomicMax(&s_c0, cc);
+    else if (x.x == f.tile) ++later;
+  }
+  if (t == 0) s_later = 0;
+  __syncthreads();
+  if (later) atomicAdd(&s_later, later);
+  __syncthreads();
+  const int c0 = s_c0, c1 = c + s_later - 1;
+  if (c0 < 0) return;
+  const RunInfo f0 = p.info[c0];
+  if (f0.tile == f.tile && f0.i > 0) return;  // a later one of the tile's runs
   const int r = p.Hq / p.Hkv, D = p.D, row = blockIdx.y * kMergeRows + (t >> 5);
   const int lo = __ldg(p.offsets + f.b), n = __ldg(p.offsets + f.b + 1) - lo, len = __ldg(p.lens + f.b);
   const int rho = f.rt * kRows + row, tok = rho / r;
