@@ -30,6 +30,7 @@
 //                registers, converted and stored with the 128-byte swizzle
 //   warps 12-15  the same for V; both bring Q in (bf16 -> fp16, a warp per row)
 //   warp 16      TMEM allocation and the single MMA-issuing thread
+//   warp 17      per unit, its scales and place in shared memory for the softmax
 // A stage is 128 positions x 128 head dims of K or V (32 KB of fp16; 64 dims
 // at D = 64), two of each, the same layout for both. Every role is one warp's
 // chain of dependent instructions per scheduler, at 4 to 5 cycles each, so
@@ -59,7 +60,7 @@ using namespace tc;
 constexpr int kRows = 128;          // rows of a tile (MMA M)
 constexpr int kKeys = 128;          // positions of a unit
 constexpr int kSoftWarps = 8;
-constexpr int kMmaWarp = 16;
+constexpr int kMmaWarp = 16, kNoteWarp = 17;
 constexpr int kThreads = 20 * 32;
 // Registers per thread: 96 at launch (640 x 96 in all), then 120 for the 8
 // softmax warps, 96 for the 8 converting ones and 48 for the rest:
@@ -93,7 +94,7 @@ struct Cfg {
   static constexpr int kOutBytes = kSoftWarps * 32 * kOutPitch;
   static constexpr int kOutOffset = kQBytes + 4 * kStageBytes;
   static constexpr int kCtlOffset = kOutOffset + kOutBytes;
-  static constexpr int kBytes = kCtlOffset + 5120 + 1024;  // + alignment slack
+  static constexpr int kBytes = kCtlOffset + 4096 + 1024;  // + alignment slack
   static_assert(kStep % 8 == 0, "a thread's rows share their swizzle");
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
@@ -102,7 +103,17 @@ struct RowConst {  // of a tile's rows, written with its Q
   uint8_t e[kRows];     // biased exponent of the row's largest magnitude
 };
 
+// What the softmax has to know of a unit, put down by a warp of its own.
+struct UnitNote {
+  float4 scale[8];  // of every 16 positions: s_k, log2 s_v, 1 / s_v
+  int4 tile;        // lo, n, len, g of its sequence and head
+  int4 place;       // first position, row tile, is the tile's last, -
+};
+constexpr int kNotes = 4;
+
 struct Ctl {
+  UnitNote note[kNotes];
+  uint64_t note_full[kNotes], note_empty[kNotes];
   uint64_t full[2][2], empty[2][2];  // [K, V][stage]
   uint64_t q_full, q_empty;
   uint64_t rc_full[2], rc_empty[2];  // row constants of every second tile
@@ -388,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
   uint8_t* sQ = smem;                  // 64-dim slabs of 128 rows x 128 bytes
   uint8_t* sR = smem + F::kQBytes;     // stages: two of K, two of V
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + F::kCtlOffset);
-  static_assert(sizeof(Ctl) <= 5120, "control block");
+  static_assert(sizeof(Ctl) <= 4096, "control block");
   __shared__ long long s_unit[2];  // units before the run's start and end
   __shared__ Cursor s_cur;
   __shared__ int s_bad, s_tile;
@@ -402,6 +413,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
 
   if (threadIdx.x == 32) {
     mbar_init(&ctl->q_full, 2 * kGroupWarps);
+    for (int i = 0; i < kNotes; ++i) {
+      mbar_init(&ctl->note_full[i], 1);
+      mbar_init(&ctl->note_empty[i], kSoftWarps);
+    }
     mbar_init(&ctl->q_empty, 1);
     for (int i = 0; i < 2; ++i) {
       for (int s = 0; s < 2; ++s) {
@@ -562,6 +577,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
         }
       }
       commit(&ctl->mma_done, leader);
+    } else if (warp == kNoteWarp) {
+      // ----------------------------------------------------- unit notes
+      Cursor k = cur;
+#pragma unroll 1
+      for (int u = 0; u < U; ++u) {
+        const int s = u % kNotes;
+        const int pos = min(k.i * kKeys + 16 * (lane & 7), k.len - 1);
+        const size_t at = (size_t)(k.b * p.Hkv + k.g) * p.nblk + (pos >> p.shift);
+        const float sk = __ldg(p.ks + at), v = __ldg(p.vs + at), sv = v > 0.f ? v : kScaleFloor;
+        if (u >= kNotes && !warp_wait(&ctl->note_empty[s], (u / kNotes - 1) & 1)) break;
+        if (lane < 8) ctl->note[s].scale[lane] = make_float4(sk, __log2f(sv), __fdividef(1.f, sv), 0.f);
+        if (lane == 8) ctl->note[s].tile = make_int4(k.lo, k.n, k.len, k.g);
+        if (lane == 9) ctl->note[s].place = make_int4(k.i * kKeys, k.rt, k.last(), 0);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->note_full[s]);
+        if (u + 1 < U) k.advance(p, r);
+      }
     }
   } else if (warp < kSoftWarps) {
     // --------------------------------------------------------- softmax
@@ -582,36 +614,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
       ++met;
       return true;
     };
-    // scales of this half of a unit: lane k holds those of its k-th 16 positions
-    auto load_scales = [&](const Cursor& k, float& sk, float& sv) {
-      const int pos = min(k.i * kKeys + 64 * half + 16 * (lane & 3), k.len - 1);
-      const size_t at = (size_t)(k.b * p.Hkv + k.g) * p.nblk + (pos >> p.shift);
-      sk = __ldg(p.ks + at);
-      sv = __ldg(p.vs + at);
-    };
-    float sk, sv;
-    load_scales(cur, sk, sv);
+    int4 seq = make_int4(0, 0, 0, 0);  // lo, n, len, g of the tile
 #pragma unroll 1
     for (int u = 0; u < U; ++u) {
-      Cursor nxt = cur;
-      float skn = 0.f, svn = 0.f;
-      if (u + 1 < U) {
-        nxt.advance(p, r);
-        load_scales(nxt, skn, svn);
-      }
+      const int ns = u % kNotes;
+      if (!warp_wait(&ctl->note_full[ns], (u / kNotes) & 1)) break;
+      const int4 place = ctl->note[ns].place;
+      float4 sc[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) sc[h] = ctl->note[ns].scale[4 * half + h];
       if (fresh) {
+        seq = ctl->note[ns].tile;
         if (!warp_wait(&ctl->rc_full[tile & 1], (tile >> 1) & 1)) break;
         const RowConst& rc = ctl->rc[tile & 1];
-        const int e = rc.e[row], rho = cur.rt * kRows + row;
+        const int e = rc.e[row], rho = place.y * kRows + row;
         __syncwarp();
         rs = p.scale_log2 * __uint_as_float(e > 0 ? (uint32_t)e << 23 : 0x00400000u);  // 2^(e - 127)
-        see = rho < cur.n * r ? max(cur.len - cur.n + div_r(rho, p.rmagic) + 1, 0) : 0;
+        see = rho < seq.y * r ? max(seq.z - seq.y + div_r(rho, p.rmagic) + 1, 0) : 0;
         if (lane == 0) mbar_arrive(&ctl->rc_empty[tile & 1]);
         m = kMinusBig;
         l = 0.f;
       }
-      const float svx = sv > 0.f ? sv : kScaleFloor;
-      const float lsv = __log2f(svx), rsv = __fdividef(1.f, svx);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->note_empty[ns]);
       if (!warp_wait(&ctl->s_full[u & 1], (u >> 1) & 1)) break;
       tc_fence_after();
       const uint32_t ts = lane_addr + kColS + 128 * (u & 1);
@@ -620,23 +645,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
       // Scores on the base-2 scale, with V's scale: a x + b, a and b per 16
       // positions. a is kept above zero, so hidden positions (x = -inf) stay
       // hidden and a group's largest x gives its largest score.
-      const int left = see - cur.i * kKeys - 64 * half;  // visible positions from this half's first on
+      const int left = see - place.x - 64 * half;  // visible positions from this half's first on
       if (__any_sync(0xffffffffu, left < 64)) {
 #pragma unroll
         for (int e = 0; e < 64; ++e)
           if (e >= left) x[e] = 0xFF800000u;  // -inf
       }
       float mx = -INFINITY;
-      float a[4], b[4];
+      float a[4];
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
-        a[h] = fmaxf(rs * __shfl_sync(0xffffffffu, sk, h), 1e-35f);
-        b[h] = __shfl_sync(0xffffffffu, lsv, h);
+        a[h] = fmaxf(rs * sc[h].x, 1e-35f);
         float g = fmaxf(__uint_as_float(x[16 * h]), __uint_as_float(x[16 * h + 1]));
 #pragma unroll
         for (int e = 16 * h + 2; e < 16 * h + 16; e += 2)
           g = fmaxf(g, fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
-        mx = fmaxf(mx, fmaf(g, a[h], b[h]));
+        mx = fmaxf(mx, fmaf(g, a[h], sc[h].y));
       }
       float other;
       if (!meet(mx, other)) break;
@@ -665,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         uint64_t s2 = 0ull;
-        const float bt = b[h] + top;
+        const float bt = sc[h].y + top;
         const uint64_t a2 = pack2(a[h], a[h]), b2 = pack2(bt, bt);
 #pragma unroll
         for (int e = 16 * h; e < 16 * h + 16; e += 2) {
@@ -675,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
           w[e / 2] = pack_f16(w0, w1);
         }
         const float2 s = unpack2(s2);
-        l = fmaf(s.x + s.y, __shfl_sync(0xffffffffu, rsv, h), l);
+        l = fmaf(s.x + s.y, sc[h].z, l);
       }
       tmem_st_32(ts + 32 * half, w);
       tmem_st_wait();
@@ -683,15 +707,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->p_full[u & 1]);
 
-      fresh = cur.last();
-      if (cur.last() || u + 1 == U) {
+      const bool ends = place.z != 0;
+      fresh = ends;
+      if (ends || u + 1 == U) {
         // ---- the run leaves this tile: its rows' outputs, or the partial state
         if (!meet(l, other)) break;
         l += other;
         if (!warp_wait(&ctl->pv_done[u & 1], (u >> 1) & 1)) break;
         tc_fence_after();
         const int d0 = half * (D / 2);
-        if (!mid && cur.last()) {
+        if (!mid && ends) {
           const float inv = see > 0 ? 1.f / l : 0.f;
           // 32 rows by 32 dims at a time through shared memory: 4 lanes write
           // a row's 64 bytes, 8 rows at once
@@ -699,9 +724,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
           uint16_t* orow[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int rk = cur.rt * kRows + quad * 32 + 8 * k + (lane >> 2), tok = div_r(rk, p.rmagic);
-            const bool live = rk < cur.n * r && cur.len - cur.n + tok >= 0;
-            orow[k] = live ? p.o + ((size_t)(cur.lo + tok) * p.Hq + (size_t)cur.g * r + rk - tok * r) * D + 8 * (lane & 3)
+            const int rk = place.y * kRows + quad * 32 + 8 * k + (lane >> 2), tok = div_r(rk, p.rmagic);
+            const bool live = rk < seq.y * r && seq.z - seq.y + tok >= 0;
+            orow[k] = live ? p.o + ((size_t)(seq.x + tok) * p.Hq + (size_t)seq.w * r + rk - tok * r) * D + 8 * (lane & 3)
                            : nullptr;
           }
 #pragma unroll 1
@@ -757,9 +782,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
         mid = false;
         fresh = true;
       }
-      cur = nxt;
-      sk = skn;
-      sv = svn;
     }
   } else {
     // ---------------------------------------------- codes -> fp16 operands
@@ -767,14 +789,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
     const int kv = (warp - kSoftWarps) / kGroupWarps;            // 0: K (and Q), 1: V
     const int t = threadIdx.x - 32 * (kSoftWarps + kv * kGroupWarps);
     // This thread's pieces of a stage: head dims 16 piece .. + 15 of rows key,
-    // key + kStep, ... Of the 8 lanes that store together, the upper 4 (the
-    // next 64-dim slab, whose rows lie on the same banks) store their second
-    // 16-byte chunk first.
-    const int piece = t % F::kPieces, key = t / F::kPieces;
-    const bool flip = D >= 128 && (lane & 4);
+    // key + kStep, ... Of 8 lanes that store together, 4 are in one 64-dim slab
+    // and 4 in the next, whose rows lie on the same banks: at an odd distance
+    // between the two rows the swizzle keeps them apart.
+    int piece = t % F::kPieces, key = t / F::kPieces;
+    if (D >= 128) key = 2 * (t >> 4) + (((t >> 2) ^ (t >> 3)) & 1);
     const uint32_t stage0 = smem_u32(sR) + kv * (2 * F::kStageBytes) + (uint32_t)(piece >> 2) * (kKeys * 128) + key * 128;
     const uint32_t ch = (uint32_t)(piece & 3) * 2, sw = key & 7;
-    const uint32_t b0 = stage0 + (((ch + (flip ? 1 : 0)) ^ sw) << 4), b1 = stage0 + (((ch + (flip ? 0 : 1)) ^ sw) << 4);
+    const uint32_t b0 = stage0 + ((ch ^ sw) << 4), b1 = stage0 + (((ch + 1) ^ sw) << 4);
 
     // The place of the loads, one stage ahead of the stores.
     Cursor cn = cur;
@@ -897,10 +919,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
         auto piece_of = [&](auto index) {
           constexpr int i = decltype(index)::value;
           uint32_t x[8];
-          convert4<kE4m3>(flip ? w[i].z : w[i].x, x[0], x[1]);
-          convert4<kE4m3>(flip ? w[i].w : w[i].y, x[2], x[3]);
-          convert4<kE4m3>(flip ? w[i].x : w[i].z, x[4], x[5]);
-          convert4<kE4m3>(flip ? w[i].y : w[i].w, x[6], x[7]);
+          convert4<kE4m3>(w[i].x, x[0], x[1]);
+          convert4<kE4m3>(w[i].y, x[2], x[3]);
+          convert4<kE4m3>(w[i].z, x[4], x[5]);
+          convert4<kE4m3>(w[i].w, x[6], x[7]);
           sts128<i * F::kStep * 128>(b0 + to, x[0], x[1], x[2], x[3]);
           sts128<i * F::kStep * 128>(b1 + to, x[4], x[5], x[6], x[7]);
           if (more) load1(index, h == F::kParts - 1 ? 0 : h + 1);
