@@ -57,7 +57,7 @@ namespace tiles {
 
 using namespace tc;
 
-constexpr int kRows = 128;          // rows of a tile (MMA M)
+constexpr int kRows = 128;          // rows of a block (TMEM lanes)
 constexpr int kKeys = 128;          // positions of a unit
 constexpr int kSoftWarps = 8;
 constexpr int kMmaWarp = 16, kNoteWarp = 17;
@@ -68,7 +68,6 @@ constexpr int kThreads = 20 * 32;
 constexpr int kSoftRegs = 120, kConvRegs = 96, kMmaRegs = 48;
 static_assert(256 * kSoftRegs + 256 * kConvRegs + 128 * kMmaRegs <= kThreads * 96, "register shares");
 constexpr int kGroupWarps = 4;      // converting warps of K, and of V
-constexpr int kGroupThreads = kGroupWarps * 32;
 constexpr int kMaxCtas = 256;       // workspace bound on the grid
 constexpr long long kTimeoutNs = 1000000000ll;
 // A run also pays for every tile it begins (Q, the first unit's chain, the
@@ -81,21 +80,31 @@ constexpr float kSlack = 8.f;       // ... which scores may pass by this much
 constexpr int kTmemCols = 512;
 constexpr uint32_t kColS = 256;     // S buffers at columns 256 and 384, O from 0
 
+// Blocks that share a tile: at 128 head dims and more a cluster of two, each
+// with 128 of its 256 rows.
+constexpr int tile_blocks(int D) { return D >= 128 ? 2 : 1; }
+
 template <int D>
 struct Cfg {
-  static constexpr int kDims = D < 128 ? D : 128;        // head dims of a ring stage
+  static constexpr int kCtas = tile_blocks(D);
+  static constexpr int kTileRows = kRows * kCtas;        // MMA M
+  static constexpr int kDims = D < 128 ? D : 128;        // head dims of a stage
   static constexpr int kParts = D / kDims;               // stages of a unit's K (and V)
-  static constexpr int kStageBytes = kKeys * kDims * 2;
+  static constexpr int kStages = 3;                      // of K, and of V
+  static constexpr int kRaw = D == 256 ? 2 : 4;          // stages of codes on their way, of K and of V
+  // A block's part of a stage: of K 128 / kCtas positions, of V kDims / kCtas
+  // head dims; in slabs of 64 head dims, a 128-byte row per position.
+  static constexpr int kKeyRows = kKeys / kCtas;
+  static constexpr int kStageBytes = kKeyRows * kDims * 2;
   static constexpr int kQBytes = kRows * D * 2;
-  static constexpr int kPieces = kDims / 16;             // 16-code pieces of a stage's row
-  static constexpr int kStep = kGroupThreads / kPieces;  // rows between a thread's pieces
-  static constexpr int kLoads = kKeys / kStep;           // pieces per thread and stage
   static constexpr int kOutPitch = 80;                   // bytes: 32 bf16 and padding
   static constexpr int kOutBytes = kSoftWarps * 32 * kOutPitch;
-  static constexpr int kOutOffset = kQBytes + 4 * kStageBytes;
+  static constexpr int kRawBytes = kStageBytes / 2;
+  static constexpr int kRawOffset = kQBytes + 2 * kStages * kStageBytes;
+  static constexpr int kOutOffset = kRawOffset + 2 * kRaw * kRawBytes;
   static constexpr int kCtlOffset = kOutOffset + kOutBytes;
   static constexpr int kBytes = kCtlOffset + 4096 + 1024;  // + alignment slack
-  static_assert(kStep % 8 == 0, "a thread's rows share their swizzle");
+  static_assert(kStageBytes == 128 * 128 && kKeys * (kDims / kCtas) * 2 == kStageBytes, "4 pieces of a thread");
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -114,7 +123,7 @@ constexpr int kNotes = 4;
 struct Ctl {
   UnitNote note[kNotes];
   uint64_t note_full[kNotes], note_empty[kNotes];
-  uint64_t full[2][2], empty[2][2];  // [K, V][stage]
+  uint64_t full[2][4], empty[2][4];  // [K, V][stage]
   uint64_t q_full, q_empty;
   uint64_t rc_full[2], rc_empty[2];  // row constants of every second tile
   uint64_t s_full[2], p_full[2];
@@ -124,6 +133,7 @@ struct Ctl {
   // wait for its weights.
   uint64_t pv_done[2];
   uint64_t o_empty;       // O of a finished tile has been read
+  uint64_t peer_s[2], peer_o[2];  // the other block is ready for a unit's S, for its O
   uint64_t mx_full[4];    // both halves of a lane quadrant have stored their maxima (or sums)
   uint64_t mma_done;
   uint32_t tmem;
@@ -147,8 +157,8 @@ struct Params {
   const int32_t* offsets;
   const int32_t* lens;
   uint16_t* o;
-  float* part;       // [2 C] slots of [128][D] O, then [128] m, [128] L
-  RunInfo* info;     // [C]
+  float* part;       // two slots per run of [tile rows][D] O, then [tile rows] m and L
+  RunInfo* info;     // per run
   int32_t* flags;    // [C]
   float scale_log2;
   int B, T, Hq, Hkv, L_max, nblk, shift, q_stride;
@@ -163,7 +173,7 @@ __device__ __forceinline__ int div_r(int x, unsigned long long rmagic) {
   return (int)(((unsigned long long)(unsigned)x * rmagic) >> 36);
 }
 
-constexpr size_t slot_floats(int D) { return (size_t)kRows * (D + 2); }
+constexpr size_t slot_floats(int D) { return (size_t)kRows * tile_blocks(D) * (D + 2); }
 
 // Place in the run: unit i of the nb units of row tile rt of KV head g of
 // sequence b.
@@ -176,11 +186,11 @@ struct Cursor {
   }
   __device__ bool first() const { return i == 0; }
   __device__ bool last() const { return i == nb - 1; }
-  __device__ void advance(const Params& p, int r) {
+  __device__ void advance(const Params& p, int r, int RT) {
     if (++i < nb) return;
     i = 0;
     do {
-      if (++rt >= seq_tiles(n, r, kRows)) {
+      if (++rt >= seq_tiles(n, r, RT)) {
         rt = 0;
         if (++g >= p.Hkv) {
           g = 0;
@@ -190,7 +200,7 @@ struct Cursor {
           } while (n == 0);
         }
       }
-      nb = tile_units(n, len, r, kRows, kKeys, rt);
+      nb = tile_units(n, len, r, RT, kKeys, rt);
     } while (nb == 0);
   }
 };
@@ -302,31 +312,104 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 // in uniform registers, and each instruction is predicated on the one lane that
 // issues it: a branch around the instructions would move every operand through
 // vector registers first.
+// With two blocks (cta_group::2) the leader's thread issues for both: each
+// tensor core reads its half of A, and both halves of B from the two shared
+// memories, all at the same addresses.
 // D[tmem] (+)= A[smem] B[smem]
+template <int kCtas>
 __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                        uint32_t accumulate, uint32_t leader) {
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
-      : "memory");
+  if (kCtas == 2)
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
 }
 // D[tmem] (+)= A[tmem] B[smem]
+template <int kCtas>
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                        uint32_t accumulate, uint32_t leader) {
+  if (kCtas == 2)
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+// Arrives on `bar` (of both blocks) once every MMA the leader has issued so far
+// is done.
+template <int kCtas>
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t leader) {
+  if (kCtas == 2)
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n}\n" ::
+            "r"(smem_u32(bar)),
+        "r"(leader), "h"((uint16_t)3)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+        "r"(leader)
+        : "memory");
+}
+// Arrives on the leading block's `bar`, with what this thread has seen.
+__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, 0;\n"
+      " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}\n" ::"r"(smem_u32(bar))
       : "memory");
 }
-// Arrives on `bar` once every MMA the leader has issued so far is done.
-__device__ __forceinline__ void commit(uint64_t* bar, uint32_t leader) {
+// mbar_test_wait for a barrier that the other block arrives on.
+__device__ __forceinline__ bool test_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
   asm volatile(
-      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
-      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
-      "r"(leader)
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
+  return ok != 0;
+}
+// All threads of the tile's blocks (every thread comes here: all other waits are limited).
+template <int kCtas>
+__device__ __forceinline__ void tile_barrier() {
+  if (kCtas == 2)
+    asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+  else
+    __syncthreads();
+}
+template <int kCtas>
+__device__ __forceinline__ void alloc_columns(uint32_t* dst) {
+  if (kCtas == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tmem_alloc(dst, kTmemCols);
+    tmem_relinquish();
+  }
+}
+template <int kCtas>
+__device__ __forceinline__ void free_columns(uint32_t tmem) {
+  if (kCtas == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  else
+    tmem_dealloc(tmem, kTmemCols);
 }
 
 // Descriptor of an MN-major operand in the 128-byte swizzle: 64 values along
@@ -351,6 +434,10 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
   return v;
+}
+// 16 bytes from global to shared memory, or 16 zero bytes.
+__device__ __forceinline__ void load16(uint32_t to, const uint8_t* from, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
 }
 // v <- 16 bytes at p + kOffset, if `on` (a predicate: no branch).
 template <int kOffset>
@@ -397,7 +484,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;                  // 64-dim slabs of 128 rows x 128 bytes
-  uint8_t* sR = smem + F::kQBytes;     // stages: two of K, two of V
+  uint8_t* sR = smem + F::kQBytes;     // stages of K, then of V
+  constexpr int kCtas = F::kCtas, kTileRows = F::kTileRows;
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + F::kCtlOffset);
   static_assert(sizeof(Ctl) <= 4096, "control block");
   __shared__ long long s_unit[2];  // units before the run's start and end
@@ -408,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
   // uniform: the roles' loops then run on uniform registers, where the MMA
   // instructions take their descriptors from.
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-  const int C = gridDim.x, c = blockIdx.x;
+  const int C = gridDim.x / kCtas, c = blockIdx.x / kCtas, rank = blockIdx.x % kCtas;  // runs, run, block of its tiles
   const int r = p.Hq / p.Hkv;
 
   if (threadIdx.x == 32) {
@@ -419,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
     }
     mbar_init(&ctl->q_empty, 1);
     for (int i = 0; i < 2; ++i) {
-      for (int s = 0; s < 2; ++s) {
+      for (int s = 0; s < F::kStages; ++s) {
         mbar_init(&ctl->full[i][s], kGroupWarps);
         mbar_init(&ctl->empty[i][s], 1);
       }
@@ -428,6 +516,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
       mbar_init(&ctl->s_full[i], 1);
       mbar_init(&ctl->p_full[i], kSoftWarps);
       mbar_init(&ctl->pv_done[i], 1);
+      mbar_init(&ctl->peer_s[i], 1);
+      mbar_init(&ctl->peer_o[i], 1);
     }
     mbar_init(&ctl->o_empty, kSoftWarps);
     for (int i = 0; i < 4; ++i) mbar_init(&ctl->mx_full[i], 2);
@@ -442,8 +532,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
   if (warp == 1 || warp == 2) {  // the run's start and its end
     Place k;
     long long at;
-    const bool ok = find_run(p.offsets, p.lens, p.B, p.T, p.Hkv, p.L_max, r, kRows, kKeys, kTileCost, c + warp - 1, C,
-                             &k, &at);
+    const bool ok = find_run(p.offsets, p.lens, p.B, p.T, p.Hkv, p.L_max, r, kTileRows, kKeys, kTileCost, c + warp - 1,
+                             C, &k, &at);
     if (lane == 0) {
       s_unit[warp - 1] = k.units;
       if (warp == 1) {
@@ -465,24 +555,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
   __syncthreads();
   if (threadIdx.x == 0) {
     const bool live = !s_bad && s_unit[0] < s_unit[1];
-    p.info[c] = RunInfo{s_tile, live, s_cur.b, s_cur.g, s_cur.rt, s_cur.i};
-    if (!live) p.flags[c] = s_bad ? (int32_t)MOE_ERR_INVALID_ARG : 0;
+    if (rank == 0) p.info[c] = RunInfo{s_tile, live, s_cur.b, s_cur.g, s_cur.rt, s_cur.i};
+    if (!live) p.flags[blockIdx.x] = s_bad ? (int32_t)MOE_ERR_INVALID_ARG : 0;
   }
   if (s_bad) return;
   // Queries that see nothing (more queries than positions): o = 0.
-  for (int b = c; b < p.B; b += C) {
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
     const int lo = __ldg(p.offsets + b), hi = __ldg(p.offsets + b + 1), len = __ldg(p.lens + b);
     const size_t pieces = (size_t)max(0, hi - lo - len) * p.Hq * (D / 8);
     uint4* z = reinterpret_cast<uint4*>(p.o + (size_t)lo * p.Hq * D);
     for (size_t i = threadIdx.x; i < pieces; i += kThreads) z[i] = make_uint4(0u, 0u, 0u, 0u);
   }
-  if (s_unit[0] >= s_unit[1]) return;
-  if (warp == kMmaWarp) {
-    tmem_alloc(&ctl->tmem, kTmemCols);
-    tmem_relinquish();
-  }
+  if (s_unit[0] >= s_unit[1]) return;  // both blocks of a run alike
+  if (warp == kMmaWarp) alloc_columns<kCtas>(&ctl->tmem);
   tc_fence_before();
-  __syncthreads();
+  tile_barrier<kCtas>();  // the barriers and the columns of both blocks are there
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
   const int U = (int)(s_unit[1] - s_unit[0]);
@@ -496,43 +583,80 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
     if (!ok) ok = mbar_wait(bar, parity, abort_flag, global_timer_ns() + (uint64_t)p.timeout_ns);
     return __all_sync(0xffffffffu, ok) != 0;
   };
+  // The same for a barrier that the other block arrives on.
+  auto peer_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    bool ok = test_cluster(bar, parity);
+    if (!ok) {
+      ok = mbar_wait(bar, parity, abort_flag, global_timer_ns() + (uint64_t)p.timeout_ns);
+      if (ok) ok = test_cluster(bar, parity);
+    }
+    return __all_sync(0xffffffffu, ok) != 0;
+  };
 
   if (warp >= kMmaWarp) {
     fewer_registers<kMmaRegs>();
     if (warp == kMmaWarp) {
       // ----------------------------------------------------- MMA issuer
-      constexpr uint32_t idesc_s = idesc_f16_f32(kRows, kKeys);
-      constexpr uint32_t idesc_o = idesc_f16_f32(kRows, F::kDims) | (1u << 16);  // B is MN-major
+      // With two blocks the leader's warp issues for both; the other's goes
+      // through the same steps, waits for what its own block has to have ready
+      // and passes that on as one arrival. (Were the block's warps to arrive on
+      // the leader's barriers themselves, each such arrival would first wait
+      // for the warp's loads: 630 us instead of XXX for 2048 queries after
+      // 16,384 positions at 256 head dims.)
+      constexpr uint32_t idesc_s = idesc_f16_f32(kTileRows, kKeys);
+      constexpr uint32_t idesc_o = idesc_f16_f32(kTileRows, F::kDims) | (1u << 16);  // B is MN-major
       const uint64_t dq = sw128_desc(smem_u32(sQ));
       const uint32_t leader = elect_one();
       const uint64_t dk = sw128_desc(smem_u32(sR));
-      const uint64_t dv = sw128_mn_desc(smem_u32(sR) + 2 * F::kStageBytes, kKeys * 128);
+      const uint64_t dv = sw128_mn_desc(smem_u32(sR) + F::kStages * F::kStageBytes, kKeys * 128);
       int tq = 0, to = 0;              // tiles whose Q has been waited for, whose O has been started
       Cursor nxt = cur;
+      // stage h of unit u, and its phase
+      auto stage = [](int u, int h) { return (u * F::kParts + h) % F::kStages; };
+      auto phase = [](int u, int h) { return (uint32_t)((u * F::kParts + h) / F::kStages) & 1u; };
       // both stages of a unit's K or V (D <= 128: its one), tested together
       auto wait_stages = [&](int kv, int u) -> bool {
-        if (F::kParts == 1) return warp_wait(&ctl->full[kv][u & 1], (u >> 1) & 1);
-        const bool both = mbar_test_wait(&ctl->full[kv][0], u & 1) && mbar_test_wait(&ctl->full[kv][1], u & 1);
-        return __all_sync(0xffffffffu, both) || (warp_wait(&ctl->full[kv][0], u & 1) && warp_wait(&ctl->full[kv][1], u & 1));
+        bool all = true;
+#pragma unroll
+        for (int h = 0; h < F::kParts; ++h) all = mbar_test_wait(&ctl->full[kv][stage(u, h)], phase(u, h)) && all;
+        if (__all_sync(0xffffffffu, all)) return true;
+        for (int h = 0; h < F::kParts; ++h)
+          if (!warp_wait(&ctl->full[kv][stage(u, h)], phase(u, h))) return false;
+        return true;
+      };
+      // Both blocks are ready for a step of unit u. (An arrival for unit u + 2
+      // comes after the leader's step of unit u: two barriers in turn will do.)
+      auto together = [&](uint64_t* bar, int u) -> bool {
+        tc_fence_after();
+        if (kCtas == 2 && rank == 0) {
+          if (!peer_wait(bar, (u >> 1) & 1)) return false;
+          tc_fence_after();
+        } else if (kCtas == 2) {
+          tc_fence_before();
+          if (lane == 0) arrive_leader(bar);
+        }
+        return true;
       };
       auto score = [&](int u, bool first, bool ends) -> bool {  // S of unit u
         if (first && !warp_wait(&ctl->q_full, tq++ & 1)) return false;
         if (!wait_stages(0, u)) return false;
-        tc_fence_after();
+        if (!together(&ctl->peer_s[u & 1], u)) return false;
+        if (rank != 0) return true;
         const uint32_t d = tmem + kColS + 128 * (u & 1);
 #pragma unroll
         for (int h = 0; h < F::kParts; ++h) {
-          const int st = F::kParts == 2 ? h : u & 1;
+          const int st = stage(u, h);
 #pragma unroll
           for (int kk = 0; kk < F::kDims / 16; ++kk) {
-            const uint32_t in = (kk >> 2) * (kKeys * 128 / 16) + (kk & 3) * 2;  // 64-dim slabs of 128 rows
-            mma_ss(d, dq + h * (F::kDims / 64) * (kRows * 128 / 16) + in, dk + st * (F::kStageBytes / 16) + in, idesc_s,
-                   kk > 0 || h > 0, leader);
+            const uint32_t slab = kk >> 2, in = (kk & 3) * 2;  // 64-dim slabs
+            mma_ss<kCtas>(d, dq + (h * (F::kDims / 64) + slab) * (kRows * 128 / 16) + in,
+                          dk + st * (F::kStageBytes / 16) + slab * (F::kKeyRows * 128 / 16) + in, idesc_s,
+                          kk > 0 || h > 0, leader);
           }
-          commit(&ctl->empty[0][st], leader);
+          commit<kCtas>(&ctl->empty[0][st], leader);
         }
-        commit(&ctl->s_full[u & 1], leader);
-        if (ends) commit(&ctl->q_empty, leader);
+        commit<kCtas>(&ctl->s_full[u & 1], leader);
+        if (ends) commit<kCtas>(&ctl->q_empty, leader);
         return true;
       };
       auto output = [&](int u, bool first) -> bool {  // O of unit u
@@ -542,18 +666,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
           ++to;
         }
         if (!wait_stages(1, u)) return false;
-        tc_fence_after();
+        if (!together(&ctl->peer_o[u & 1], u)) return false;
+        if (rank != 0) return true;
         const uint32_t a = tmem + kColS + 128 * (u & 1);
 #pragma unroll
         for (int h = 0; h < F::kParts; ++h) {
-          const int st = F::kParts == 2 ? h : u & 1;
+          const int st = stage(u, h);
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_ts(tmem + h * F::kDims, a + kk * 8, dv + st * (F::kStageBytes / 16) + kk * (16 * 128 / 16), idesc_o,
-                   kk > 0 ? 1u : (uint32_t)!first, leader);
-          commit(&ctl->empty[1][st], leader);
+            mma_ts<kCtas>(tmem + h * F::kDims, a + kk * 8, dv + st * (F::kStageBytes / 16) + kk * (16 * 128 / 16), idesc_o,
+                          kk > 0 ? 1u : (uint32_t)!first, leader);
+          commit<kCtas>(&ctl->empty[1][st], leader);
         }
-        commit(&ctl->pv_done[u & 1], leader);
+        commit<kCtas>(&ctl->pv_done[u & 1], leader);
         return true;
       };
       // S of unit u + 1 goes ahead of O of unit u, whose weights the softmax
@@ -567,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
           const bool last = nxt.last();
           ok = score(su, sfirst, last || su + 1 == U);
           sfirst = last;
-          if (++su < U) nxt.advance(p, r);
+          if (++su < U) nxt.advance(p, r, F::kTileRows);
         } else {
           ok = output(ou, ofirst);
           // with su == ou + 1 the next unit's sfirst is this one's end; with
@@ -576,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
           ofirst = su == ou && sfirst;
         }
       }
-      commit(&ctl->mma_done, leader);
+      if (rank == 0) commit<kCtas>(&ctl->mma_done, leader);
     } else if (warp == kNoteWarp) {
       // ----------------------------------------------------- unit notes
       Cursor k = cur;
@@ -592,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
         if (lane == 9) ctl->note[s].place = make_int4(k.i * kKeys, k.rt, k.last(), 0);
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->note_full[s]);
-        if (u + 1 < U) k.advance(p, r);
+        if (u + 1 < U) k.advance(p, r, F::kTileRows);
       }
     }
   } else if (warp < kSoftWarps) {
@@ -627,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
         seq = ctl->note[ns].tile;
         if (!warp_wait(&ctl->rc_full[tile & 1], (tile >> 1) & 1)) break;
         const RowConst& rc = ctl->rc[tile & 1];
-        const int e = rc.e[row], rho = place.y * kRows + row;
+        const int e = rc.e[row], rho = place.y * kTileRows + rank * kRows + row;
         __syncwarp();
         rs = p.scale_log2 * __uint_as_float(e > 0 ? (uint32_t)e << 23 : 0x00400000u);  // 2^(e - 127)
         see = rho < seq.y * r ? max(seq.z - seq.y + div_r(rho, p.rmagic) + 1, 0) : 0;
@@ -724,10 +849,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
           uint16_t* orow[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int rk = place.y * kRows + quad * 32 + 8 * k + (lane >> 2), tok = div_r(rk, p.rmagic);
+            const int rk = place.y * kTileRows + rank * kRows + quad * 32 + 8 * k + (lane >> 2);
+            const int tok = div_r(rk, p.rmagic);
             const bool live = rk < seq.y * r && seq.z - seq.y + tok >= 0;
-            orow[k] = live ? p.o + ((size_t)(seq.x + tok) * p.Hq + (size_t)seq.w * r + rk - tok * r) * D + 8 * (lane & 3)
-                           : nullptr;
+            uint16_t* at = p.o + ((size_t)(seq.x + tok) * p.Hq + (size_t)seq.w * r + rk - tok * r) * D + 8 * (lane & 3);
+            orow[k] = live ? at : nullptr;
           }
 #pragma unroll 1
           for (int j = d0; j < d0 + D / 2; j += 32) {
@@ -755,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
           // 32 rows by 16 dims at a time, the same way
           float* part = p.part + (size_t)(2 * c + (mid ? 0 : 1)) * slot_floats(D);
           const uint32_t stage = smem_u32(smem + F::kOutOffset) + warp * (32 * F::kOutPitch);
-          float* prow = part + (size_t)(quad * 32 + (lane >> 2)) * D + 4 * (lane & 3);
+          float* prow = part + (size_t)(rank * kRows + quad * 32 + (lane >> 2)) * D + 4 * (lane & 3);
 #pragma unroll 1
           for (int j = d0; j < d0 + D / 2; j += 16) {
             uint32_t v[16];
@@ -771,8 +897,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
                   lds128(stage + (8 * k + (lane >> 2)) * F::kOutPitch + 16 * (lane & 3));
           }
           if (half == 0) {
-            part[(size_t)D * kRows + row] = m;
-            part[(size_t)(D + 1) * kRows + row] = l;
+            part[(size_t)D * kTileRows + rank * kRows + row] = m;
+            part[(size_t)(D + 1) * kTileRows + rank * kRows + row] = l;
           }
         }
         tc_fence_before();
@@ -788,47 +914,65 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
     fewer_registers<kConvRegs>();
     const int kv = (warp - kSoftWarps) / kGroupWarps;            // 0: K (and Q), 1: V
     const int t = threadIdx.x - 32 * (kSoftWarps + kv * kGroupWarps);
-    // This thread's pieces of a stage: head dims 16 piece .. + 15 of rows key,
-    // key + kStep, ... Of 8 lanes that store together, 4 are in one 64-dim slab
-    // and 4 in the next, whose rows lie on the same banks: at an odd distance
-    // between the two rows the swizzle keeps them apart.
-    int piece = t % F::kPieces, key = t / F::kPieces;
-    if (D >= 128) key = 2 * (t >> 4) + (((t >> 2) ^ (t >> 3)) & 1);
-    const uint32_t stage0 = smem_u32(sR) + kv * (2 * F::kStageBytes) + (uint32_t)(piece >> 2) * (kKeys * 128) + key * 128;
-    const uint32_t ch = (uint32_t)(piece & 3) * 2, sw = key & 7;
+    // This thread's four pieces of a stage, 16 head dims of a position each, 4096
+    // bytes apart in the stage: of V (and at D = 64) positions key, key + 32, +
+    // 64, + 96 of the block's 64 head dims; of K positions key and key + 32 of
+    // the block's 64, then the same of the next 64 head dims. 8 lanes that
+    // store together have two neighbouring positions, which the swizzle keeps
+    // on different banks.
+    const int piece = t & 3, key = t >> 2;
+    const bool by_dims = kCtas == 2 && kv == 0;
+    const uint32_t stage0 = smem_u32(sR) + kv * (F::kStages * F::kStageBytes) + key * 128;
+    const uint32_t ch = (uint32_t)piece * 2, sw = key & 7;
     const uint32_t b0 = stage0 + ((ch ^ sw) << 4), b1 = stage0 + (((ch + 1) ^ sw) << 4);
+    const int key0 = by_dims ? rank * F::kKeyRows : 0;                // the block's first position and head dim
+    const int dim0 = kCtas == 2 && kv == 1 ? rank * (F::kDims / kCtas) : 0;
+    const int second = by_dims ? 64 : 64 * D;                         // from the first two pieces to the others
 
-    // The place of the loads, one stage ahead of the stores.
-    Cursor cn = cur;
-    const uint8_t* src;  // this thread's first piece of the unit
-    int keys;            // positions of the unit from the thread's first on
-    bool whole;          // all of the unit's positions exist
-    auto each_piece = [&](auto f) {
-      f(std::integral_constant<int, 0>{});
-      f(std::integral_constant<int, 1>{});
-      f(std::integral_constant<int, 2>{});
-      f(std::integral_constant<int, 3>{});
-      if constexpr (F::kLoads == 8) {
-        f(std::integral_constant<int, 4>{});
-        f(std::integral_constant<int, 5>{});
-        f(std::integral_constant<int, 6>{});
-        f(std::integral_constant<int, 7>{});
-      }
+    // A thread's codes come through shared memory of its own (cp.async), kRaw
+    // stages ahead: loads into registers are waited for together with those
+    // issued after them. Positions past the context are code 0 of the format
+    // or, as INT8, -128: finite and not seen either way.
+    const uint32_t raw = smem_u32(smem + F::kRawOffset) + kv * (F::kRaw * F::kRawBytes) + t * 16;
+    Cursor cn = cur;             // unit of the next load
+    int hn = 0, left = U * F::kParts;  // its stage; stages to load
+    const uint8_t* src;          // this thread's first piece of the unit
+    int keys, keys2;             // positions from its first piece, and from its third, on
+    auto limits = [&]() {
+      keys = cn.len - cn.i * kKeys - key0 - key;
+      keys2 = by_dims ? keys : keys - 64;
     };
     auto place = [&]() {
-      src = p.codes[kv] + ((size_t)(cn.b * p.Hkv + cn.g) * p.L_max + (size_t)cn.i * kKeys + key) * D + piece * 16;
-      keys = cn.len - cn.i * kKeys - key;
-      whole = keys + key >= kKeys;
+      src = p.codes[kv] + ((size_t)(cn.b * p.Hkv + cn.g) * p.L_max + (size_t)cn.i * kKeys + key0 + key) * D + dim0 +
+            piece * 16;
+      limits();
     };
     place();
-    const uint32_t none = kE4m3 ? 0u : 0x80808080u;  // positions past the context: code 0
-    uint4 w[F::kLoads];
-    auto load1 = [&](auto index, int h) {
-      constexpr int i = decltype(index)::value;
-      if (!whole) w[i] = make_uint4(none, none, none, none);
-      ldg128_if<i * F::kStep * D>(w[i], src + h * F::kDims, i * F::kStep < keys);
+    auto load_stage = [&](int j) {
+      if (left > 0) {
+        const uint32_t to = raw + (j % F::kRaw) * F::kRawBytes;
+        const uint8_t* from = src + hn * F::kDims;
+        load16(to, from, keys > 0);
+        load16(to + 2048, from + 32 * D, keys > 32);
+        load16(to + 4096, from + second, keys2 > 0);
+        load16(to + 6144, from + second + 32 * D, keys2 > 32);
+        --left;
+        if (++hn == F::kParts && left > 0) {
+          hn = 0;
+          if (cn.last()) {
+            cn.advance(p, r, F::kTileRows);
+            place();
+          } else {
+            ++cn.i;
+            src += kKeys * D;
+            limits();
+          }
+        }
+      }
+      cp_async_commit();  // an empty group at the end: the count of groups stays
     };
-    each_piece([&](auto index) { load1(index, 0); });
+#pragma unroll 1
+    for (int j = 0; j < F::kRaw; ++j) load_stage(j);
 
     // Q of the tile at a cursor: D / 8 lanes per row, 16 bytes each
     int tile = 0;
@@ -838,7 +982,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
     auto load_rows = [&](const Cursor& k, int base, uint4 (&v)[kBatch]) {
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const int rho = k.rt * kRows + qrow + (base + i) * kAtOnce, tok = div_r(rho, p.rmagic);
+        const int rho = k.rt * kTileRows + rank * kRows + qrow + (base + i) * kAtOnce, tok = div_r(rho, p.rmagic);
         v[i] = make_uint4(0u, 0u, 0u, 0u);
         ldg128_if<0>(v[i], reinterpret_cast<const uint8_t*>(p.q + (size_t)(k.lo + tok) * p.q_stride +
                                                             (size_t)(k.g * r + rho - tok * r) * D + ln * 8),
@@ -890,59 +1034,58 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
     };
 
     bool ok = true, fresh = true;
+    Cursor k = cur;
+    int st = 0;
+    uint32_t free = 1;           // parity of a stage's last use (a first use waits for nothing)
 #pragma unroll 1
     for (int u = 0; ok && u < U; ++u) {
-      if (fresh && !load_q(cn)) break;
-      fresh = cn.last();
-#pragma unroll
+      if (fresh && !load_q(k)) break;
+      fresh = k.last();
+      if (u + 1 < U) k.advance(p, r, F::kTileRows);
+#pragma unroll 1
       for (int h = 0; h < F::kParts; ++h) {
-        const int j = u * F::kParts + h, st = F::kParts == 2 ? h : j & 1;
-        ok = ok && (j < 2 || warp_wait(&ctl->empty[kv][st], ((j >> 1) - 1) & 1));
+        const int j = u * F::kParts + h;
+        cp_async_wait<F::kRaw - 1>();
+        const uint32_t from = raw + (j % F::kRaw) * F::kRawBytes;
+        uint4 w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = lds128(from + 2048 * i);
+        ok = warp_wait(&ctl->empty[kv][st], free);
         if (!ok) break;
         tc_fence_after();
         const uint32_t to = st * F::kStageBytes;
-        bool more = true;                    // a next stage to load
-        if (h == F::kParts - 1) {
-          more = u + 1 < U;
-          if (more) {
-            if (cn.last()) {
-              cn.advance(p, r);
-              place();
-            } else {
-              ++cn.i;
-              src += kKeys * D;
-              keys -= kKeys;
-              whole = keys + key >= kKeys;
-            }
-          }
-        }
-        auto piece_of = [&](auto index) {
-          constexpr int i = decltype(index)::value;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
           uint32_t x[8];
           convert4<kE4m3>(w[i].x, x[0], x[1]);
           convert4<kE4m3>(w[i].y, x[2], x[3]);
           convert4<kE4m3>(w[i].z, x[4], x[5]);
           convert4<kE4m3>(w[i].w, x[6], x[7]);
-          sts128<i * F::kStep * 128>(b0 + to, x[0], x[1], x[2], x[3]);
-          sts128<i * F::kStep * 128>(b1 + to, x[4], x[5], x[6], x[7]);
-          if (more) load1(index, h == F::kParts - 1 ? 0 : h + 1);
-        };
-        each_piece(piece_of);
+          sts128(b0 + to + 4096 * i, x[0], x[1], x[2], x[3]);
+          sts128(b1 + to + 4096 * i, x[4], x[5], x[6], x[7]);
+        }
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->full[kv][st]);
+        load_stage(j);           // into the slot just read
+        if (++st == F::kStages) {
+          st = 0;
+          free ^= 1;
+        }
       }
     }
+    cp_async_wait_all();
   }
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
     int dummy = 0;  // no MMA may still be running when TMEM is freed
-    mbar_wait(&ctl->mma_done, 0, &dummy, global_timer_ns() + 100000000ull);
+    mbar_wait(&ctl->mma_done, 0, &dummy, global_timer_ns() + 2 * (uint64_t)p.timeout_ns);
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
   }
-  if (threadIdx.x == 0) p.flags[c] = *abort_flag ? (int32_t)MOE_ERR_DEVICE_TIMEOUT : 0;
+  tile_barrier<kCtas>();  // nor a block's shared memory and barriers be gone while the other uses them
+  if (warp == kMmaWarp) free_columns<kCtas>(tmem);
+  if (threadIdx.x == 0) p.flags[blockIdx.x] = *abort_flag ? (int32_t)MOE_ERR_DEVICE_TIMEOUT : 0;
 }
 
 struct MergeParams {
@@ -953,7 +1096,7 @@ struct MergeParams {
   const int32_t* flags;
   uint16_t* o;
   int32_t* status;
-  int Hq, Hkv, D, C;
+  int Hq, Hkv, D, C, ctas;  // C: runs
 };
 
 constexpr int kMergeRows = 8;       // rows of a block, a warp each
@@ -969,12 +1112,13 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_tiles_merge_kernel(const Me
   const int c = blockIdx.x, C = p.C, t = threadIdx.x, lane = t & 31;
   if (c == 0 && blockIdx.y == 0) {
     // the call's status: the outcome of the lowest-numbered grid block that failed
-    if (t == 0) s_first = C;
+    const int blocks = C * p.ctas;
+    if (t == 0) s_first = blocks;
     __syncthreads();
-    for (int cc = t; cc < C; cc += kMergeThreads)
+    for (int cc = t; cc < blocks; cc += kMergeThreads)
       if (__ldcg(p.flags + cc) != 0) atomicMin(&s_first, cc);
     __syncthreads();
-    if (t == 0) *p.status = s_first == C ? 0 : __ldcg(p.flags + s_first);
+    if (t == 0) *p.status = s_first == blocks ? 0 : __ldcg(p.flags + s_first);
   }
   // Run c is the tile's second if it starts inside the tile and the last live
   // run before it does not, or does at the first unit; the runs after it that
@@ -1000,15 +1144,15 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_tiles_merge_kernel(const Me
   if (f0.tile == f.tile && f0.i > 0) return;  // a later one of the tile's runs
   const int r = p.Hq / p.Hkv, D = p.D, row = blockIdx.y * kMergeRows + (t >> 5);
   const int lo = __ldg(p.offsets + f.b), n = __ldg(p.offsets + f.b + 1) - lo, len = __ldg(p.lens + f.b);
-  const int rho = f.rt * kRows + row, tok = rho / r;
+  const int rows = kRows * p.ctas, rho = f.rt * rows + row, tok = rho / r;
   if (rho >= n * r || len - n + tok < 0) return;
   auto slot = [&](int cc) { return p.part + (size_t)(2 * cc + (cc == c0 ? 1 : 0)) * slot_floats(D); };
   // lane k weighs the states of runs c0 + k, c0 + 32 + k, ...
   float M = kMinusBig;
   bool failed = false;
   for (int cc = c0 + lane; cc <= c1; cc += 32) {
-    failed |= __ldcg(p.flags + cc) != 0;
-    M = fmaxf(M, __ldcg(slot(cc) + (size_t)D * kRows + row));
+    for (int k = 0; k < p.ctas; ++k) failed |= __ldcg(p.flags + cc * p.ctas + k) != 0;
+    M = fmaxf(M, __ldcg(slot(cc) + (size_t)D * rows + row));
   }
   if (__any_sync(0xffffffffu, failed)) return;  // a run gave up: o is left as it was
 #pragma unroll
@@ -1019,8 +1163,8 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_tiles_merge_kernel(const Me
   const int per = D / 32;
   for (int base = c0; base <= c1; base += 32) {
     const int mine = base + lane;
-    const float e = mine <= c1 ? exp2f(__ldcg(slot(mine) + (size_t)D * kRows + row) - M) : 0.f;
-    float l = mine <= c1 ? e * __ldcg(slot(mine) + (size_t)(D + 1) * kRows + row) : 0.f;
+    const float e = mine <= c1 ? exp2f(__ldcg(slot(mine) + (size_t)D * rows + row) - M) : 0.f;
+    float l = mine <= c1 ? e * __ldcg(slot(mine) + (size_t)(D + 1) * rows + row) : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     L += l;
@@ -1047,14 +1191,16 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_tiles_merge_kernel(const Me
 
 size_t tiles_workspace_bytes(const moe_kv8_shape& s) {
   using namespace tiles;
-  return 256 + kMaxCtas * (sizeof(int32_t) + sizeof(RunInfo)) + 2 * kMaxCtas * slot_floats(s.D) * sizeof(float);
+  return 256 + kMaxCtas * (sizeof(int32_t) + sizeof(RunInfo)) +
+         2 * (kMaxCtas / tile_blocks(s.D)) * slot_floats(s.D) * sizeof(float);
 }
 
 moe_status launch_tiles(const AttnArgs& a, cudaStream_t stream) {
   using namespace tiles;
   const int sms = sm_count();
   if (sms <= 0) return cuda_fail(cudaErrorInvalidDevice, "device query");
-  const int grid = sms < kMaxCtas ? sms : kMaxCtas;
+  const int ctas = tile_blocks(a.D), runs = (sms < kMaxCtas ? sms : kMaxCtas) / ctas;
+  if (runs < 1) return cuda_fail(cudaErrorInvalidDevice, "multiprocessors");
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   int32_t* status = reinterpret_cast<int32_t*>(ws);
   int32_t* flags = reinterpret_cast<int32_t*>(ws + 256);
@@ -1064,15 +1210,19 @@ moe_status launch_tiles(const AttnArgs& a, cudaStream_t stream) {
   const Params prm{a.q, {a.k, a.v}, a.ks, a.vs, a.offsets, a.lens, a.o, part, info, flags, a.scale_log2,
                    a.B, a.T, a.Hq, a.Hkv, a.L_max, a.nblk, shift, a.q_stride,
                    ((1ull << 36) + a.Hq / a.Hkv - 1) / (a.Hq / a.Hkv), kTimeoutNs};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)ctas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = dim3((unsigned)(runs * ctas));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   auto go = [&](auto d, auto fp8) -> cudaError_t {
     constexpr int D = decltype(d)::value;
     constexpr bool kE4m3 = decltype(fp8)::value;
@@ -1089,8 +1239,9 @@ moe_status launch_tiles(const AttnArgs& a, cudaStream_t stream) {
   };
   cudaError_t e = a.e4m3 ? pick(std::true_type{}) : pick(std::false_type{});
   if (e != cudaSuccess) return cuda_fail(e, "tile kernel launch");
-  const MergeParams mp{a.offsets, a.lens, part, info, flags, a.o, status, a.Hq, a.Hkv, a.D, grid};
-  cfg.gridDim = dim3((unsigned)grid, (unsigned)(kRows / kMergeRows));
+  const MergeParams mp{a.offsets, a.lens, part, info, flags, a.o, status, a.Hq, a.Hkv, a.D, runs, ctas};
+  cfg.gridDim = dim3((unsigned)runs, (unsigned)(kRows * ctas / kMergeRows));
+  cfg.numAttrs = 1;
   cfg.blockDim = dim3(kMergeThreads);
   cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, kv8_tiles_merge_kernel, mp);
