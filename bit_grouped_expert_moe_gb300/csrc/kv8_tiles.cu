@@ -367,23 +367,30 @@ __device__ __forceinline__ void commit(uint64_t* bar, uint32_t leader) {
         "r"(leader)
         : "memory");
 }
-// Arrives on the leading block's `bar`, with what this thread has seen.
+// Arrives on the leading block's `bar`. What the arrival releases lies in
+// shared memory (and TMEM, by the tcgen05 fences): a fence that is restricted
+// to that does not wait for global memory, as a release at cluster scope does.
 __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
   asm volatile(
       "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, 0;\n"
-      " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}\n" ::"r"(smem_u32(bar))
+      " fence.release.sync_restrict::shared::cta.cluster;\n"
+      " mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [a];\n}\n" ::"r"(smem_u32(bar))
       : "memory");
 }
-// mbar_test_wait for a barrier that the other block arrives on.
+// mbar_test_wait for a barrier that the other block arrives on; to be followed
+// by acquire_peer once it has succeeded.
 __device__ __forceinline__ bool test_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n"
       " selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return ok != 0;
+}
+__device__ __forceinline__ void acquire_peer() {
+  asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
 }
 // All threads of the tile's blocks (every thread comes here: all other waits are limited).
 template <int kCtas>
@@ -590,6 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
       ok = mbar_wait(bar, parity, abort_flag, global_timer_ns() + (uint64_t)p.timeout_ns);
       if (ok) ok = test_cluster(bar, parity);
     }
+    acquire_peer();
     return __all_sync(0xffffffffu, ok) != 0;
   };
 
