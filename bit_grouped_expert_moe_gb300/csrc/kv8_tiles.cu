@@ -590,16 +590,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
     if (!ok) ok = mbar_wait(bar, parity, abort_flag, global_timer_ns() + (uint64_t)p.timeout_ns);
     return __all_sync(0xffffffffu, ok) != 0;
   };
-  // The same for a barrier that the other block arrives on.
-  auto peer_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    bool ok = test_cluster(bar, parity);
-    if (!ok) {
-      ok = mbar_wait(bar, parity, abort_flag, global_timer_ns() + (uint64_t)p.timeout_ns);
-      if (ok) ok = test_cluster(bar, parity);
-    }
-    acquire_peer();
-    return __all_sync(0xffffffffu, ok) != 0;
-  };
 
   if (warp >= kMmaWarp) {
     fewer_registers<kMmaRegs>();
@@ -622,33 +612,36 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
       // stage h of unit u, and its phase
       auto stage = [](int u, int h) { return (u * F::kParts + h) % F::kStages; };
       auto phase = [](int u, int h) { return (uint32_t)((u * F::kParts + h) / F::kStages) & 1u; };
-      // both stages of a unit's K or V (D <= 128: its one), tested together
-      auto wait_stages = [&](int kv, int u) -> bool {
-        bool all = true;
+      // Waits until a step of unit u may begin: its stages of K or V, the
+      // softmax's or Q's barrier `own` (if any), the other block's arrival;
+      // all tested together. The other block's warp passes its readiness on.
+      // (An arrival for unit u + 2 comes after the leader's step of unit u: two
+      // barriers in turn will do.)
+      auto ready = [&](int kv, int u, uint64_t* own, uint32_t parity, uint64_t* peer) -> bool {
+        bool all = own == nullptr || mbar_test_wait(own, parity);
 #pragma unroll
         for (int h = 0; h < F::kParts; ++h) all = mbar_test_wait(&ctl->full[kv][stage(u, h)], phase(u, h)) && all;
-        if (__all_sync(0xffffffffu, all)) return true;
-        for (int h = 0; h < F::kParts; ++h)
-          if (!warp_wait(&ctl->full[kv][stage(u, h)], phase(u, h))) return false;
-        return true;
-      };
-      // Both blocks are ready for a step of unit u. (An arrival for unit u + 2
-      // comes after the leader's step of unit u: two barriers in turn will do.)
-      auto together = [&](uint64_t* bar, int u) -> bool {
+        const bool listens = kCtas == 2 && rank == 0;
+        if (listens) all = test_cluster(peer, (u >> 1) & 1) && all;
+        if (!__all_sync(0xffffffffu, all)) {
+          if (own != nullptr && !warp_wait(own, parity)) return false;
+          for (int h = 0; h < F::kParts; ++h)
+            if (!warp_wait(&ctl->full[kv][stage(u, h)], phase(u, h))) return false;
+          if (listens && !warp_wait(peer, (u >> 1) & 1)) return false;
+          // (a test at cluster scope, for the fence below to follow on)
+          if (listens && !__all_sync(0xffffffffu, test_cluster(peer, (u >> 1) & 1))) return false;
+        }
         tc_fence_after();
-        if (kCtas == 2 && rank == 0) {
-          if (!peer_wait(bar, (u >> 1) & 1)) return false;
-          tc_fence_after();
-        } else if (kCtas == 2) {
+        if (listens) acquire_peer();
+        if (kCtas == 2 && rank != 0) {
           tc_fence_before();
-          if (lane == 0) arrive_leader(bar);
+          if (lane == 0) arrive_leader(peer);
         }
         return true;
       };
       auto score = [&](int u, bool first, bool ends) -> bool {  // S of unit u
-        if (first && !warp_wait(&ctl->q_full, tq++ & 1)) return false;
-        if (!wait_stages(0, u)) return false;
-        if (!together(&ctl->peer_s[u & 1], u)) return false;
+        if (!ready(0, u, first ? &ctl->q_full : nullptr, tq & 1, &ctl->peer_s[u & 1])) return false;
+        tq += first;
         if (rank != 0) return true;
         const uint32_t d = tmem + kColS + 128 * (u & 1);
 #pragma unroll
@@ -668,13 +661,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
         return true;
       };
       auto output = [&](int u, bool first) -> bool {  // O of unit u
-        if (!warp_wait(&ctl->p_full[u & 1], (u >> 1) & 1)) return false;
-        if (first) {
-          if (to > 0 && !warp_wait(&ctl->o_empty, (to - 1) & 1)) return false;
-          ++to;
-        }
-        if (!wait_stages(1, u)) return false;
-        if (!together(&ctl->peer_o[u & 1], u)) return false;
+        if (first && to++ > 0 && !warp_wait(&ctl->o_empty, (to - 2) & 1)) return false;
+        if (!ready(1, u, &ctl->p_full[u & 1], (u >> 1) & 1, &ctl->peer_o[u & 1])) return false;
         if (rank != 0) return true;
         const uint32_t a = tmem + kColS + 128 * (u & 1);
 #pragma unroll
