@@ -19,8 +19,21 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Few query tokens per sequence: the split-context kernels; more: the tiles.
-bool few(const moe_kv8_shape& s) { return s.T <= 8 * s.B; }
+// Which kernels serve a call: the split-context ones read the cache once per 8
+// to 32 rows (query heads of a KV head x tokens), the tiles once per 128 or 256
+// but with a longer chain in front. So a call is the former's with up to 16
+// rows per sequence and KV head, or somewhat more where few of those pairs
+// keep the GPU's blocks from filling up. (The host knows the tokens of the
+// batch, not each sequence's.) Measured, split / tiles in us, INT8, n tokens of
+// each of B sequences over L positions:
+//   16 heads / 2 x 256, B = 1, L = 32,768:   n = 8 38.7 / 56.7, n = 16 69.9 / 58.7
+//                       B = 1, L = 2048:     n = 16 17.3 / 28.9, n = 64 41.5 / 34.0
+//                       B = 16, L = 4096:    n = 2 33.6 / 51.8, n = 4 56.5 / 51.4
+//   8 heads / 8 x 128,  B = 1, L = 32,768:   n = 32 35.2 / 60.8, n = 64 60.7 / 61.0
+//                       B = 16, L = 512:     n = 8 17.9 / 30.4, n = 24 42.4 / 30.8
+//   4 heads / 1 x 64,   B = 1, L = 32,768:   n = 32 25.1 / 60.3, n = 64 37.1 / 44.7
+//                       B = 16, L = 4096:    n = 8 18.4 / 19.5, n = 12 27.9 / 19.6
+bool few(const moe_kv8_shape& s) { return (long long)s.T * s.Hq <= 16ll * s.B * s.Hkv + 192; }
 
 size_t workspace_bytes(const moe_kv8_shape& s) {
   return s.T == 0 ? 256 : few(s) ? split_workspace_bytes(s) : tiles_workspace_bytes(s);

@@ -62,18 +62,22 @@ constexpr int kKeys = 128;          // positions of a unit
 constexpr int kSoftWarps = 8;
 constexpr int kMmaWarp = 16, kNoteWarp = 17;
 constexpr int kThreads = 20 * 32;
-// Registers per thread: 96 at launch (640 x 96 in all), then 120 for the 8
-// softmax warps, 96 for the 8 converting ones and 48 for the rest:
-// 256 x 120 + 256 x 96 + 128 x 48 = 640 x 96.
-constexpr int kSoftRegs = 120, kConvRegs = 96, kMmaRegs = 48;
+// Registers per thread: 96 at launch (640 x 96 in all), then 128 for the 8
+// softmax warps, 88 for the 8 converting ones and 48 for the rest:
+// 256 x 128 + 256 x 88 + 128 x 48 = 640 x 96. (With 120 and 96 the chunk of the
+// table below takes 417 us for 401; with 136 and 80 the prompt 171 for 148.)
+constexpr int kSoftRegs = 128, kConvRegs = 88, kMmaRegs = 48;
 static_assert(256 * kSoftRegs + 256 * kConvRegs + 128 * kMmaRegs <= kThreads * 96, "register shares");
+static_assert(kSoftRegs >= 96 && kConvRegs <= 96 && kMmaRegs <= 96, "the first takes what the others give");
 constexpr int kGroupWarps = 4;      // converting warps of K, and of V
 constexpr int kMaxCtas = 256;       // workspace bound on the grid
 constexpr long long kTimeoutNs = 1000000000ll;
 // A run also pays for every tile it begins (Q, the first unit's chain, the
-// output), about as much as two units: the runs are cut on a scale where a
+// output), about as much as three units: the runs are cut on a scale where a
 // tile with units takes kTileCost more places than units, before its first.
-constexpr int kTileCost = 2;
+// A prompt of 4096 (16 heads on 2 x 256): 173, 149, 137, 140 us at 1 to 4; 16
+// sequences' 8 queries over 4096 positions 53, 52, 50, 50 us.
+constexpr int kTileCost = 3;
 constexpr float kMinusBig = -1e30f;
 constexpr float kWeightBits = 7.f;  // weights are 2^7 at the row's m ...
 constexpr float kSlack = 8.f;       // ... which scores may pass by this much

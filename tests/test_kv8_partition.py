@@ -72,7 +72,7 @@ def _sequences(rng, count):
         yield rng.randint(1, 900), rng.choice([0, 1, rng.randint(0, 300), rng.randint(0, 5000)]), r
 
 
-@pytest.mark.parametrize("RT,KT", [(128, 128), (8, 64), (16, 64), (32, 64)])
+@pytest.mark.parametrize("RT,KT", [(128, 128), (256, 128), (8, 64), (16, 64), (32, 64)])
 def test_closed_form(RT, KT):
     for n, ln, r in _sequences(random.Random(RT), 300):
         units = [tile_units(n, ln, r, RT, KT, rt) for rt in range(seq_tiles(n, r, RT))]
