@@ -215,5 +215,23 @@ __device__ inline bool find_run(const int32_t* offsets, const int32_t* lens, int
   return !bad;
 }
 
+// Moves registers between a block's warpgroups: every warp of a group calls one
+// of the two. A share above a thread's registers at launch waits until the
+// other groups have given theirs, so the shares add up to what the block was
+// launched with, which launches_with checks before the first launch.
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <class Kernel>
+bool launches_with(Kernel kernel, int regs) {
+  cudaFuncAttributes a;
+  return cudaFuncGetAttributes(&a, kernel) == cudaSuccess && a.numRegs == regs;
+}
+
 }  // namespace kv8
 }  // namespace bgmoe

@@ -66,7 +66,15 @@ using tc::smem_u32;
 // sizes, where two independent products hide one another's latency.
 constexpr int unit_positions(int D) { return D == 256 ? 64 : 128; }
 constexpr int kConsumers = 8;       // warps
-constexpr int kThreads = (kConsumers + 1) * 32;
+// Three warpgroups, of which the third has one working warp: 9 warps would
+// leave each thread 168 registers (three warps on one scheduler), so the third
+// gives most of its own away: 256 x 232 + 128 x 40 = 384 x 168. (The consumers
+// of 16 rows by 128 head dims spilled 45 words otherwise.)
+constexpr int kThreads = (kConsumers + 4) * 32;
+constexpr int kLaunchRegs = 168, kConsumerRegs = 232, kProducerRegs = 40;
+static_assert(kConsumers * kConsumerRegs + 4 * kProducerRegs <= (kConsumers + 4) * kLaunchRegs &&
+                  kConsumerRegs >= kLaunchRegs && kProducerRegs <= kLaunchRegs,
+              "register shares");
 constexpr int kMaxCtas = 256;       // workspace bound on the grid
 // Beginning and ending a tile (Q, the warps' fold, the partial state) costs a
 // run about as much as four units: 3 us against 0.7 us a unit of 32 KB.
@@ -327,41 +335,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     return __all_sync(0xffffffffu, ok) != 0;
   };
 
-  if (warp == kConsumers) {
+  if (warp >= kConsumers) {
+    fewer_registers<kProducerRegs>();
     // ------------------------------------------------------------ producer
-    // The first tile's Q and scales ask first: behind a ring's worth of codes
-    // from every SM they took 3 us more.
-    int s = 0, ph = 0, issued = 0;
-    bool go = warp_wait(&ctl->go, 0);
+    if (warp == kConsumers) {
+      // The first tile's Q and scales ask first: behind a ring's worth of codes
+      // from every SM they took 3 us more.
+      int s = 0, ph = 0, issued = 0;
+      bool go = warp_wait(&ctl->go, 0);
 #pragma unroll 1
-    for (int j = 0; go && j < U; ++j) {
-      if (issued >= kStages && !warp_wait(&ctl->empty[s], ph ^ 1)) break;
-      if (elect_one()) {
-        uint8_t* st = smem + s * S::kStageBytes;
-        const int pair = cur.b * p.Hkv + cur.g;
-        mbar_arrive_expect_tx(&ctl->full[s], (uint32_t)S::kStageBytes);
+      for (int j = 0; go && j < U; ++j) {
+        if (issued >= kStages && !warp_wait(&ctl->empty[s], ph ^ 1)) break;
+        if (elect_one()) {
+          uint8_t* st = smem + s * S::kStageBytes;
+          const int pair = cur.b * p.Hkv + cur.g;
+          mbar_arrive_expect_tx(&ctl->full[s], (uint32_t)S::kStageBytes);
 #pragma unroll
-        for (int sl = 0; sl < S::kSlabs; ++sl) {
-          tma_load_3d(st + sl * S::kSlab, &tm_k, sl * 128, cur.i * kPos, pair, &ctl->full[s]);
-          tma_load_3d(st + (S::kSlabs + sl) * S::kSlab, &tm_v, sl * 128, cur.i * kPos, pair, &ctl->full[s]);
+          for (int sl = 0; sl < S::kSlabs; ++sl) {
+            tma_load_3d(st + sl * S::kSlab, &tm_k, sl * 128, cur.i * kPos, pair, &ctl->full[s]);
+            tma_load_3d(st + (S::kSlabs + sl) * S::kSlab, &tm_v, sl * 128, cur.i * kPos, pair, &ctl->full[s]);
+          }
         }
+        __syncwarp();
+        ++issued;
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1;
+        }
+        cur.advance(p, r, RT, kPos);
       }
-      __syncwarp();
-      ++issued;
-      if (++s == kStages) {
-        s = 0;
-        ph ^= 1;
+      if (lane == 0 && *abort_flag) {  // let this block's own copies land before it exits
+        int dummy = 0;
+        const uint64_t dl = global_timer_ns() + 100000000ull;
+        for (int k = issued - kStages < 0 ? 0 : issued - kStages; k < issued; ++k)
+          mbar_wait(&ctl->full[k % kStages], (k / kStages) & 1, &dummy, dl);
       }
-      cur.advance(p, r, RT, kPos);
-    }
-    if (lane == 0 && *abort_flag) {  // let this block's own copies land before it exits
-      int dummy = 0;
-      const uint64_t dl = global_timer_ns() + 100000000ull;
-      for (int k = issued - kStages < 0 ? 0 : issued - kStages; k < issued; ++k)
-        mbar_wait(&ctl->full[k % kStages], (k / kStages) & 1, &dummy, dl);
     }
   } else {
     // ----------------------------------------------------------- consumers
+    more_registers<kConsumerRegs>();
     const int gq = lane >> 2, m4 = lane & 3;
     // ldmatrix row addresses (relative to a slab): lanes 0-7, 8-15, 16-23,
     // 24-31 address the four 8 x 16-byte matrices (positions +0, +8 of the
@@ -932,6 +944,8 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const Params& p
   static SmemLimitMemo smem_memo;
   cudaError_t e = ensure_smem(kv8_split_kernel<D, kNT, kE4m3>, Cfg<D, kNT>::kBytes, &smem_memo);
   if (e != cudaSuccess) return e;
+  static const bool shares = launches_with(kv8_split_kernel<D, kNT, kE4m3>, kLaunchRegs);
+  if (!shares) return cudaErrorInvalidKernelImage;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kThreads);

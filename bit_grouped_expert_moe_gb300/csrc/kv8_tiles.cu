@@ -66,9 +66,10 @@ constexpr int kThreads = 20 * 32;
 // softmax warps, 88 for the 8 converting ones and 48 for the rest:
 // 256 x 128 + 256 x 88 + 128 x 48 = 640 x 96. (With 120 and 96 the chunk of the
 // table below takes 417 us for 401; with 136 and 80 the prompt 171 for 148.)
-constexpr int kSoftRegs = 128, kConvRegs = 88, kMmaRegs = 48;
-static_assert(256 * kSoftRegs + 256 * kConvRegs + 128 * kMmaRegs <= kThreads * 96, "register shares");
-static_assert(kSoftRegs >= 96 && kConvRegs <= 96 && kMmaRegs <= 96, "the first takes what the others give");
+constexpr int kLaunchRegs = 96, kSoftRegs = 128, kConvRegs = 88, kMmaRegs = 48;
+static_assert(256 * kSoftRegs + 256 * kConvRegs + 128 * kMmaRegs <= kThreads * kLaunchRegs, "register shares");
+static_assert(kSoftRegs >= kLaunchRegs && kConvRegs <= kLaunchRegs && kMmaRegs <= kLaunchRegs,
+              "the first takes what the others give");
 constexpr int kGroupWarps = 4;      // converting warps of K, and of V
 constexpr int kMaxCtas = 256;       // workspace bound on the grid
 constexpr long long kTimeoutNs = 1000000000ll;
@@ -457,15 +458,6 @@ __device__ __forceinline__ void ldg128_if(uint4& v, const uint8_t* p, bool on) {
       "{\n .reg .pred q;\n setp.ne.b32 q, %5, 0;\n @q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4 + %6];\n}\n"
       : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
       : "l"(p), "r"((int)on), "n"(kOffset));
-}
-
-template <int kRegs>
-__device__ __forceinline__ void more_registers() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-template <int kRegs>
-__device__ __forceinline__ void fewer_registers() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -1229,6 +1221,8 @@ moe_status launch_tiles(const AttnArgs& a, cudaStream_t stream) {
     static SmemLimitMemo smem_memo;
     const cudaError_t e = ensure_smem(kv8_tiles_kernel<D, kE4m3>, Cfg<D>::kBytes, &smem_memo);
     if (e != cudaSuccess) return e;
+    static const bool shares = launches_with(kv8_tiles_kernel<D, kE4m3>, kLaunchRegs);
+    if (!shares) return cudaErrorInvalidKernelImage;
     cfg.dynamicSmemBytes = Cfg<D>::kBytes;
     return cudaLaunchKernelEx(&cfg, kv8_tiles_kernel<D, kE4m3>, prm);
   };
