@@ -121,7 +121,9 @@ def lib() -> ctypes.CDLL:
         L.moe_kv8_read.argtypes = [kp, cp, P, P, P, P, P, P]
         L.moe_kv8_workspace_bytes.argtypes = [kp, ctypes.POINTER(sz)]
         L.moe_kv8_attn.argtypes = [kp, P, cp, P, P, ctypes.c_float, P, P, sz, P]
-        for f in ("moe_kv8_write", "moe_kv8_read", "moe_kv8_workspace_bytes", "moe_kv8_attn"):
+        L.moe_kv8_attn_test_stall.argtypes = [kp, P, cp, P, P, ctypes.c_float, P, P, sz, i32, ctypes.c_int64, P]
+        for f in ("moe_kv8_write", "moe_kv8_read", "moe_kv8_workspace_bytes", "moe_kv8_attn",
+                  "moe_kv8_attn_test_stall"):
             getattr(L, f).restype = i32
         for f in ("moe_workspace_bytes", "moe_max_tiles", "moe_route_blocks", "moe_route", "moe_forward",
                   "moe_forward_timed", "moe_forward_residual",
@@ -430,8 +432,8 @@ class Kv8Cache:
         L = shape.L_max
         if self._dims != (shape.B, shape.Hkv, L, shape.D) or self._nblk != -(-L // max(shape.block, 1)) or (
                 self._e4m3 and shape.format != KV8_E4M3):
-            _kv8_refuse(where, f"the cache holds {self._t[0].dtype} codes {self._dims} in {self._nblk} blocks, the shape "
-                               f"says otherwise")
+            _kv8_refuse(where, f"the cache holds {self._t[0].dtype} codes {self._dims} in {self._nblk} blocks, the "
+                               "shape says otherwise")
         if self._dev != torch.cuda.current_device():
             _kv8_refuse(where, f"the cache is on {self._t[0].device}, not on the current device")
         return self._dev
@@ -513,3 +515,13 @@ def kv8_attn(shape, q, cache: Kv8Cache, offsets, lens, o, workspace, scale=None,
                             _kv8_stream(stream, dev))
     if rc:
         _check(rc, w)
+
+
+def kv8_attn_test_stall(shape, q, cache: Kv8Cache, offsets, lens, o, workspace, stalled_block: int, timeout_ns: int,
+                        scale=None, stream=None):
+    """moe_kv8_attn_test_stall: kv8_attn with one grid block that never brings
+    its operands and a short device timeout (test only)."""
+    _check(lib().moe_kv8_attn_test_stall(shape, _ptr(q), cache._c, _ptr(offsets), _ptr(lens),
+                                         shape.D ** -0.5 if scale is None else scale, _ptr(o), _ptr(workspace),
+                                         workspace.numel(), int(stalled_block), int(timeout_ns), _stream(stream)),
+           "moe_kv8_attn_test_stall")

@@ -40,7 +40,8 @@ size_t workspace_bytes(const moe_kv8_shape& s) {
 }
 
 moe_status attn(const moe_kv8_shape* shape, const void* q, const moe_kv8_cache* cache, const int32_t* offsets,
-                const int32_t* lens, float scale, void* o, void* workspace, size_t ws_bytes, void* stream) {
+                const int32_t* lens, float scale, void* o, void* workspace, size_t ws_bytes, void* stream,
+                int stalled = -1, long long timeout_ns = kTimeoutNs) {
   if (!shape) return MOE_ERR_INVALID_ARG;
   const moe_kv8_shape s = *shape;
   if (!shape_ok(s)) return MOE_ERR_UNSUPPORTED_SHAPE;
@@ -58,7 +59,7 @@ moe_status attn(const moe_kv8_shape* shape, const void* q, const moe_kv8_cache* 
   const AttnArgs a{static_cast<const uint16_t*>(q), cache->k_codes, cache->v_codes, cache->k_scales, cache->v_scales,
                    offsets, lens, static_cast<uint16_t*>(o), workspace, s.B, s.T, s.Hq, s.Hkv, s.D, s.L_max,
                    (s.L_max + s.block - 1) / s.block, s.block, s.format == MOE_KV8_E4M3,
-                   s.q_stride ? s.q_stride : s.Hq * s.D, scale * kLog2e};
+                   s.q_stride ? s.q_stride : s.Hq * s.D, scale * kLog2e, stalled, timeout_ns};
   return few(s) ? launch_split(a, st) : launch_tiles(a, st);
 }
 
@@ -78,6 +79,14 @@ moe_status moe_kv8_workspace_bytes(const moe_kv8_shape* shape, size_t* bytes) {
 moe_status moe_kv8_attn(const moe_kv8_shape* shape, const void* q, const moe_kv8_cache* cache, const int32_t* offsets,
                         const int32_t* lens, float scale, void* o, void* workspace, size_t ws_bytes, void* stream) {
   return bgmoe::kv8::attn(shape, q, cache, offsets, lens, scale, o, workspace, ws_bytes, stream);
+}
+
+moe_status moe_kv8_attn_test_stall(const moe_kv8_shape* shape, const void* q, const moe_kv8_cache* cache,
+                                   const int32_t* offsets, const int32_t* lens, float scale, void* o, void* workspace,
+                                   size_t ws_bytes, int32_t stalled_block, int64_t timeout_ns, void* stream) {
+  if (stalled_block < 0 || timeout_ns <= 0 || timeout_ns > bgmoe::kv8::kTimeoutNs) return MOE_ERR_INVALID_ARG;
+  return bgmoe::kv8::attn(shape, q, cache, offsets, lens, scale, o, workspace, ws_bytes, stream, stalled_block,
+                          timeout_ns);
 }
 
 }  // extern "C"

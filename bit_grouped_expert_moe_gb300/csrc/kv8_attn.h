@@ -18,7 +18,11 @@ struct AttnArgs {
   void* workspace;
   int B, T, Hq, Hkv, D, L_max, nblk, block, e4m3, q_stride;
   float scale_log2;  // scale * log2(e)
+  int stalled;       // grid block that never brings its operands (tests), or -1
+  long long timeout_ns;  // limit of every wait
 };
+
+constexpr long long kTimeoutNs = 1000000000ll;
 
 // Split-context kernels (kv8_split.cu), for few query tokens per sequence.
 size_t split_workspace_bytes(const moe_kv8_shape& s);

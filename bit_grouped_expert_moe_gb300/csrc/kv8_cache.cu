@@ -373,7 +373,8 @@ moe_status cache_call(const moe_kv8_shape* shape, const moe_kv8_cache* cache, co
   if (sms <= 0) return cuda_fail(cudaErrorInvalidDevice, "device query");
   auto go = [&](auto d) {
     constexpr int D = decltype(d)::value;
-    return e4m3 ? launch_block<D, true>(p, write, s.block, sms, st) : launch_block<D, false>(p, write, s.block, sms, st);
+    return e4m3 ? launch_block<D, true>(p, write, s.block, sms, st)
+                : launch_block<D, false>(p, write, s.block, sms, st);
   };
   const cudaError_t e = s.D == 64    ? go(std::integral_constant<int, 64>{})
                         : s.D == 128 ? go(std::integral_constant<int, 128>{})

@@ -79,7 +79,6 @@ constexpr int kMaxCtas = 256;       // workspace bound on the grid
 // Beginning and ending a tile (Q, the warps' fold, the partial state) costs a
 // run about as much as four units: 3 us against 0.7 us a unit of 32 KB.
 constexpr int kTileCost = 4;
-constexpr long long kTimeoutNs = 1000000000ll;
 constexpr float kMinusBig = -1e30f; // running-max start: finite, so 2^(m - m_new) is never NaN
 // A row's m is raised to its largest score only when a score passes it by
 // more than kSlack: weights are 2^kWeightBits at m and fit fp16 up to there.
@@ -137,6 +136,7 @@ struct Params {
   long long slots;
   float scale_log2;
   int B, T, Hq, Hkv, L_max, nblk, shift, q_stride;  // shift: log2 of the cache's block
+  int stalled;
   long long timeout_ns;
 };
 
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The first tile's Q and scales ask first: behind a ring's worth of codes
       // from every SM they took 3 us more.
       int s = 0, ph = 0, issued = 0;
-      bool go = warp_wait(&ctl->go, 0);
+      bool go = c != p.stalled && warp_wait(&ctl->go, 0);
 #pragma unroll 1
       for (int j = 0; go && j < U; ++j) {
         if (issued >= kStages && !warp_wait(&ctl->empty[s], ph ^ 1)) break;
@@ -995,7 +995,7 @@ moe_status launch_split(const AttnArgs& a, cudaStream_t stream) {
   const long long slots = kMaxCtas + max_tiles(a.B, a.T, r, a.Hkv, RT);
   const int shift = a.block == 16 ? 4 : a.block == 32 ? 5 : 6;
   const Params prm{a.q, a.ks, a.vs, a.offsets, a.lens, part, info, flags, slots, a.scale_log2, a.B, a.T, a.Hq, a.Hkv,
-                   a.L_max, a.nblk, shift, a.q_stride, kTimeoutNs};
+                   a.L_max, a.nblk, shift, a.q_stride, a.stalled, a.timeout_ns};
   auto go = [&](auto fp8) {
     constexpr bool kE4m3 = decltype(fp8)::value;
     return a.D == 64    ? launch_groups<64, kE4m3>(nt, tk, tv, prm, grid, stream)
@@ -1005,8 +1005,8 @@ moe_status launch_split(const AttnArgs& a, cudaStream_t stream) {
   e = a.e4m3 ? go(std::true_type{}) : go(std::false_type{});
   if (e != cudaSuccess) return cuda_fail(e, "split kernel launch");
 
-  const MergeParams mp{a.offsets, a.lens, part, info, flags, a.o, status, slots, a.B, a.T, a.Hq, a.Hkv, a.D, a.L_max, RT,
-                       grid};
+  const MergeParams mp{a.offsets, a.lens, part, info, flags, a.o,     status, slots,
+                       a.B,       a.T,    a.Hq, a.Hkv, a.D,  a.L_max, RT,     grid};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.T * (unsigned)a.Hq, (unsigned)(a.D / 64));
   cfg.blockDim = dim3(kMergeWarps * 32);

@@ -1,41 +1,55 @@
 // Attention over the 8-bit KV cache for many query tokens per sequence
 // (prompts, chunks of prompts), on the 5th-generation tensor cores, sm_103a.
 //
-// A row is one (query token, query head of a KV head); a row tile is 128
-// consecutive rows of one (sequence, KV head), so the query heads that share
-// keys share a tile whatever Hq / Hkv is. The positions that a tile's last
-// row sees are cut into units of 128, and all units of the call, laid end to
-// end in the order (sequence, KV head, row tile, position), are dealt out in
-// equal contiguous runs, one per block of a one-block-per-SM grid: a triangle
-// of causal tiles and a few tiles over a long context both fill every SM. A
-// tile that lies in one run is finished by its block; one that a run's border
-// cuts leaves partial states (m, L, O) in the workspace, at most two per
-// block, which kv8_tiles_merge_kernel joins in a fixed order.
+// A row is one (query token, query head of a KV head); a row tile is 256
+// consecutive rows of one (sequence, KV head), 128 at 64 head dims, so the
+// query heads that share keys share a tile whatever Hq / Hkv is. The positions
+// that a tile's last row sees are cut into units of 128, and all units of the
+// call, laid end to end in the order (sequence, KV head, row tile, position),
+// are dealt out in equal contiguous runs, one per pair of blocks (per block at
+// 64 head dims) of a grid with a block on every SM: a triangle of causal tiles
+// and a few tiles over a long context both fill every SM. A tile that lies in
+// one run is finished there; one that a run's border cuts leaves partial
+// states (m, L, O) in the workspace, at most two per run, which
+// kv8_tiles_merge_kernel joins in a fixed order.
 //
-// Per unit and tile, 4 * 128 * 128 * D flops:
-//   S = Q K^T  128 x 128 x D, both operands in shared memory, S in TMEM;
+// A pair of blocks is a cluster of two whose tensor cores work as one
+// (cta_group::2): each holds 128 of the tile's rows (Q, S, P, O) and half of
+// every K and V operand, so the codes are read from L2, converted and stored
+// once per 256 rows: 412 us instead of 556 for the chunk below, 135 instead of
+// 198 for the prompt. At 64 head dims a stage would be too small to halve.
+//
+// Per unit and 128 rows, 4 * 128 * 128 * D flops:
+//   S = Q K^T  N = 128 positions, both operands in shared memory, S in TMEM;
 //   P = 2^(x - m + 7) in fp16, written over S in TMEM;
-//   O += P V   128 x D x 128, A = P from TMEM, B = V from shared memory as it
-//              lies in the cache, position by position (an MN-major operand)
-// (N in halves of 128 head dims at D = 256, which share a stage's layout
-// with K.) S is double buffered, so the product S of the next unit runs while the
-// softmax of this one is computed (TMEM: D columns of O, 2 x 128 of S).
+//   O += P V   N = D (in halves of 128 at D = 256), A = P from TMEM, B = V from
+//              shared memory as it lies in the cache, position by position (an
+//              MN-major operand)
+// S is double buffered, so the product S of the next unit runs while the softmax
+// of this one is computed (TMEM: D columns of O, 2 x 128 of S).
 //
 // Warp roles (640 threads; setmaxnreg moves registers to the softmax):
 //   warps 0-7    softmax: a thread has one row (TMEM lane) and half of the unit's
 //                positions, which stay in registers from the maximum to the
 //                weights; the two halves' maxima meet in shared memory. At a
 //                tile's end, half of the output row each
-//   warps 8-11   K codes -> fp16 operands: 16-byte global loads a stage ahead in
-//                registers, converted and stored with the 128-byte swizzle
+//   warps 8-11   K codes -> fp16 operands: every thread copies its own codes into
+//                shared memory stages ahead (cp.async), converts them and stores
+//                them with the 128-byte swizzle
 //   warps 12-15  the same for V; both bring Q in (bf16 -> fp16, a warp per row)
-//   warp 16      TMEM allocation and the single MMA-issuing thread
+//   warp 16      TMEM allocation; the MMA-issuing thread (of a pair, the first
+//                block's; the other block's warp tells it what is ready there)
 //   warp 17      per unit, its scales and place in shared memory for the softmax
-// A stage is 128 positions x 128 head dims of K or V (32 KB of fp16; 64 dims
-// at D = 64), two of each, the same layout for both. Every role is one warp's
-// chain of dependent instructions per scheduler, at 4 to 5 cycles each, so
-// what counts is how few a unit takes: few and large stages, fixed addresses,
-// one loop body per role, and the unit's work spread over the roles.
+// A stage is a block's part of 128 positions x 128 head dims of K or V (16 KB of
+// fp16), three of each.
+//
+// Bound: for 2048 queries after 16,384 positions (16 heads on 2 x 256, INT8)
+// the tensor cores run 57% of a unit's 3600 cycles: a product S or O takes 1024
+// and about 500 from its issue to the softmax's first read, and the softmax
+// (2400) leaves the two products no more overlap. 1.42 PFLOP/s, 75% of the
+// measured bf16 rate; a prompt of 4096 1.02 PFLOP/s, 54%: 60 units per pair are
+// few beside the tiles' beginnings and ends. At 128 head dims the softmax
+// bounds a unit: 2000 queries after 28,000 positions, 555 us, 0.86 PFLOP/s.
 //
 // Codes are exact in fp16: 1024 + u (u = code + 128, by a byte permute) minus
 // 1152 for int8, the conversion instruction for e4m3. Scales as in
@@ -59,6 +73,7 @@ using namespace tc;
 
 constexpr int kRows = 128;          // rows of a block (TMEM lanes)
 constexpr int kKeys = 128;          // positions of a unit
+constexpr int kStages = 3;          // of K, and of V
 constexpr int kSoftWarps = 8;
 constexpr int kMmaWarp = 16, kNoteWarp = 17;
 constexpr int kThreads = 20 * 32;
@@ -72,7 +87,6 @@ static_assert(kSoftRegs >= kLaunchRegs && kConvRegs <= kLaunchRegs && kMmaRegs <
               "the first takes what the others give");
 constexpr int kGroupWarps = 4;      // converting warps of K, and of V
 constexpr int kMaxCtas = 256;       // workspace bound on the grid
-constexpr long long kTimeoutNs = 1000000000ll;
 // A run also pays for every tile it begins (Q, the first unit's chain, the
 // output), about as much as three units: the runs are cut on a scale where a
 // tile with units takes kTileCost more places than units, before its first.
@@ -95,7 +109,6 @@ struct Cfg {
   static constexpr int kTileRows = kRows * kCtas;        // MMA M
   static constexpr int kDims = D < 128 ? D : 128;        // head dims of a stage
   static constexpr int kParts = D / kDims;               // stages of a unit's K (and V)
-  static constexpr int kStages = 3;                      // of K, and of V
   static constexpr int kRaw = D == 256 ? 2 : 4;          // stages of codes on their way, of K and of V
   // A block's part of a stage: of K 128 / kCtas positions, of V kDims / kCtas
   // head dims; in slabs of 64 head dims, a 128-byte row per position.
@@ -128,7 +141,7 @@ constexpr int kNotes = 4;
 struct Ctl {
   UnitNote note[kNotes];
   uint64_t note_full[kNotes], note_empty[kNotes];
-  uint64_t full[2][4], empty[2][4];  // [K, V][stage]
+  uint64_t full[2][kStages], empty[2][kStages];  // [K, V][stage]
   uint64_t q_full, q_empty;
   uint64_t rc_full[2], rc_empty[2];  // row constants of every second tile
   uint64_t s_full[2], p_full[2];
@@ -168,6 +181,7 @@ struct Params {
   float scale_log2;
   int B, T, Hq, Hkv, L_max, nblk, shift, q_stride;
   unsigned long long rmagic;  // ceil(2^36 / r), r = Hq / Hkv
+  int stalled;
   long long timeout_ns;
 };
 
@@ -189,7 +203,6 @@ struct Cursor {
     n = __ldg(p.offsets + b + 1) - lo;
     len = __ldg(p.lens + b);
   }
-  __device__ bool first() const { return i == 0; }
   __device__ bool last() const { return i == nb - 1; }
   __device__ void advance(const Params& p, int r, int RT) {
     if (++i < nb) return;
@@ -296,7 +309,8 @@ __device__ __forceinline__ void tmem_ld_64(uint32_t taddr, uint32_t (&r)[64]) {
 
 __device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
@@ -408,7 +422,8 @@ __device__ __forceinline__ void tile_barrier() {
 template <int kCtas>
 __device__ __forceinline__ void alloc_columns(uint32_t* dst) {
   if (kCtas == 2) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(kTmemCols)
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)),
+                 "r"(kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   } else {
@@ -444,7 +459,10 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
   return v;
 }
 // 16 bytes from global to shared memory, or 16 zero bytes.
@@ -510,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
     }
     mbar_init(&ctl->q_empty, 1);
     for (int i = 0; i < 2; ++i) {
-      for (int s = 0; s < F::kStages; ++s) {
+      for (int s = 0; s < kStages; ++s) {
         mbar_init(&ctl->full[i][s], kGroupWarps);
         mbar_init(&ctl->empty[i][s], 1);
       }
@@ -593,21 +611,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
       // ----------------------------------------------------- MMA issuer
       // With two blocks the leader's warp issues for both; the other's goes
       // through the same steps, waits for what its own block has to have ready
-      // and passes that on as one arrival. (Were the block's warps to arrive on
-      // the leader's barriers themselves, each such arrival would first wait
-      // for the warp's loads: 630 us instead of XXX for 2048 queries after
-      // 16,384 positions at 256 head dims.)
+      // and passes that on as one arrival. (With the block's warps arriving on
+      // the leader's barriers themselves, each by a release at cluster scope
+      // that waited for its loads first, the chunk took 549 us; through this
+      // warp 470; with the restricted release of arrive_leader 436.)
       constexpr uint32_t idesc_s = idesc_f16_f32(kTileRows, kKeys);
       constexpr uint32_t idesc_o = idesc_f16_f32(kTileRows, F::kDims) | (1u << 16);  // B is MN-major
       const uint64_t dq = sw128_desc(smem_u32(sQ));
       const uint32_t leader = elect_one();
       const uint64_t dk = sw128_desc(smem_u32(sR));
-      const uint64_t dv = sw128_mn_desc(smem_u32(sR) + F::kStages * F::kStageBytes, kKeys * 128);
+      const uint64_t dv = sw128_mn_desc(smem_u32(sR) + kStages * F::kStageBytes, kKeys * 128);
       int tq = 0, to = 0;              // tiles whose Q has been waited for, whose O has been started
       Cursor nxt = cur;
       // stage h of unit u, and its phase
-      auto stage = [](int u, int h) { return (u * F::kParts + h) % F::kStages; };
-      auto phase = [](int u, int h) { return (uint32_t)((u * F::kParts + h) / F::kStages) & 1u; };
+      auto stage = [](int u, int h) { return (u * F::kParts + h) % kStages; };
+      auto phase = [](int u, int h) { return (uint32_t)((u * F::kParts + h) / kStages) & 1u; };
       // Waits until a step of unit u may begin: its stages of K or V, the
       // softmax's or Q's barrier `own` (if any), the other block's arrival;
       // all tested together. The other block's warp passes its readiness on.
@@ -666,8 +684,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
           const int st = stage(u, h);
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_ts<kCtas>(tmem + h * F::kDims, a + kk * 8, dv + st * (F::kStageBytes / 16) + kk * (16 * 128 / 16), idesc_o,
-                          kk > 0 ? 1u : (uint32_t)!first, leader);
+            mma_ts<kCtas>(tmem + h * F::kDims, a + kk * 8, dv + st * (F::kStageBytes / 16) + kk * (16 * 128 / 16),
+                          idesc_o, kk > 0 ? 1u : (uint32_t)!first, leader);
           commit<kCtas>(&ctl->empty[1][st], leader);
         }
         commit<kCtas>(&ctl->pv_done[u & 1], leader);
@@ -914,7 +932,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
     // on different banks.
     const int piece = t & 3, key = t >> 2;
     const bool by_dims = kCtas == 2 && kv == 0;
-    const uint32_t stage0 = smem_u32(sR) + kv * (F::kStages * F::kStageBytes) + key * 128;
+    const uint32_t stage0 = smem_u32(sR) + kv * (kStages * F::kStageBytes) + key * 128;
     const uint32_t ch = (uint32_t)piece * 2, sw = key & 7;
     const uint32_t b0 = stage0 + ((ch ^ sw) << 4), b1 = stage0 + (((ch + 1) ^ sw) << 4);
     const int key0 = by_dims ? rank * F::kKeyRows : 0;                // the block's first position and head dim
@@ -1025,7 +1043,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
       return true;
     };
 
-    bool ok = true, fresh = true;
+    bool ok = kv == 0 || (int)blockIdx.x != p.stalled, fresh = true;
     Cursor k = cur;
     int st = 0;
     uint32_t free = 1;           // parity of a stage's last use (a first use waits for nothing)
@@ -1060,7 +1078,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->full[kv][st]);
         load_stage(j);           // into the slot just read
-        if (++st == F::kStages) {
+        if (++st == kStages) {
           st = 0;
           free ^= 1;
         }
@@ -1201,7 +1219,7 @@ moe_status launch_tiles(const AttnArgs& a, cudaStream_t stream) {
   const int shift = a.block == 16 ? 4 : a.block == 32 ? 5 : 6;
   const Params prm{a.q, {a.k, a.v}, a.ks, a.vs, a.offsets, a.lens, a.o, part, info, flags, a.scale_log2,
                    a.B, a.T, a.Hq, a.Hkv, a.L_max, a.nblk, shift, a.q_stride,
-                   ((1ull << 36) + a.Hq / a.Hkv - 1) / (a.Hq / a.Hkv), kTimeoutNs};
+                   ((1ull << 36) + a.Hq / a.Hkv - 1) / (a.Hq / a.Hkv), a.stalled, a.timeout_ns};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

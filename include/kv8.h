@@ -75,9 +75,10 @@ typedef enum moe_kv8_format {
 } moe_kv8_format;
 
 /* Shape of one call. Supported: 1 <= B <= 4096; 0 <= T <= 2^24; 1 <= Hkv <=
- * 4096, B * Hkv <= 65536, T * Hkv <= 2^30; Hq a multiple of Hkv with Hq / Hkv <= 64; D in {64,
- * 128, 256}; 1 <= L_max <= 2^26; block in {16, 32, 64}. Strides: 0 for packed
- * tokens, or a multiple of 8 elements of at least one token's (Hq D, Hkv D).
+ * 4096, B * Hkv <= 65536, T * Hkv <= 2^30; Hq a multiple of Hkv with Hq / Hkv
+ * <= 64; D in {64, 128, 256}; 1 <= L_max <= 2^26; block in {16, 32, 64}.
+ * Strides: 0 for packed tokens, or a multiple of 8 elements of at least one
+ * token's (Hq D, Hkv D).
  * Write and read do not use Hq and q_stride, attention not kv_stride; they
  * are checked all the same. */
 typedef struct moe_kv8_shape {
@@ -122,11 +123,30 @@ moe_status moe_kv8_workspace_bytes(const moe_kv8_shape* shape, size_t* bytes);
  * must be finite and > 0 (1/sqrt(D) is the usual value). The int32 at the
  * start of the workspace is the call's status word (read it with
  * moe_status_read): MOE_OK, MOE_ERR_INVALID_ARG or MOE_ERR_DEVICE_TIMEOUT (a
- * bounded wait ran out; o is not valid). T == 0 writes nothing.
+ * bounded wait ran out; o is not valid). T == 0 writes the status word only.
  *
- * Numerics: fp32 scores, softmax and sums; o is rounded once to bf16. */
+ * Numerics: q goes to fp16 with its row's largest magnitude in [1, 2) (values
+ * 2^-14 below that lose bits), codes are exact; the weights go to fp16 with
+ * the row's running maximum at 2^7 to 2^15; products, softmax and sums are
+ * fp32, and o is rounded once to bf16. So o is within
+ * 2^-8 |o| + 2.1 * 2^-11 sum_j p_j |V_j| of the formula, and what the rounding
+ * of q does to the scores. A score or an output past fp32's range is an
+ * infinity or a NaN. */
 moe_status moe_kv8_attn(const moe_kv8_shape* shape, const void* q, const moe_kv8_cache* cache, const int32_t* offsets,
                         const int32_t* lens, float scale, void* o, void* workspace, size_t ws_bytes, void* stream);
+
+/* Test hook for the bounded waits (failure detection): moe_kv8_attn in which
+ * grid block `stalled_block` (0-based, below the grid of one block per SM; a
+ * block past the grid or without work changes nothing) never brings its
+ * operands, so that the waits of its other warps run out after `timeout_ns`
+ * (0 < timeout_ns <= 1 s), as do those of a block that works with it. The
+ * call's status word then reads MOE_ERR_DEVICE_TIMEOUT, no block exits with a
+ * copy or a product in flight, o is not valid, and the context stays usable.
+ * INVALID_ARG for a negative block or a timeout out of range; the other
+ * checks are moe_kv8_attn's. */
+moe_status moe_kv8_attn_test_stall(const moe_kv8_shape* shape, const void* q, const moe_kv8_cache* cache,
+                                   const int32_t* offsets, const int32_t* lens, float scale, void* o, void* workspace,
+                                   size_t ws_bytes, int32_t stalled_block, int64_t timeout_ns, void* stream);
 
 #ifdef __cplusplus
 }

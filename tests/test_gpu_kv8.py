@@ -106,7 +106,8 @@ class Pair:
         _, Hkv, D, _ = self.dims
         T = sum(lens)
         gain = torch.exp(0.5 * _rand(gen, 1, Hkv, D))
-        x = [(_rand(gen, T, Hkv, D) * gain * k_std).to(torch.bfloat16), (_rand(gen, T, Hkv, D) * v_std).to(torch.bfloat16)]
+        x = [(_rand(gen, T, Hkv, D) * gain * k_std).to(torch.bfloat16),
+             (_rand(gen, T, Hkv, D) * v_std).to(torch.bfloat16)]
         self.write(x, lens, [0] * len(lens))
         return gen
 
@@ -210,7 +211,8 @@ def test_write_of_extreme_values(moelib, cuda_dev, kind, fmt):
     gen = torch.Generator().manual_seed(11)
     x = _rand(gen, 80, 2, 64)
     x = {"zeros": x * 0, "tiny": x * 2.0 ** -66, "huge": x.clamp(-3, 3) * 2.0 ** 126, "subnormal": x * 2.0 ** -130,
-         "edges": torch.sign(x) * torch.tensor([448.0, 450.0, 1.0, 127.0, 63.5, 0.5]).repeat(80 * 2 * 64 // 6 + 1)[:80 * 2 * 64].view(80, 2, 64)}[kind]
+         "edges": torch.sign(x) * torch.tensor([448.0, 450.0, 1.0, 127.0, 63.5, 0.5])
+          .repeat(80 * 2 * 64 // 6 + 1)[:80 * 2 * 64].view(80, 2, 64)}[kind]
     x = x.to(torch.bfloat16)
     p.write([x, -x], [80], [0])
     p.check()
@@ -499,7 +501,8 @@ def test_cache_offsets_past_32_bits(moelib, cuda_dev):
     moelib.kv8_attn(sh, q.to(DEV), big, off, _i32([0] * 8 + [L]), o, ws)
     assert moelib.status_read(ws[:4].view(torch.int32)) == 0
     # q = 0: o is the mean of the visible values, those before the tail zero
-    V = kv8.value_of(ref.codes[1][0], ref.scales[1][0][:, np.arange(320) // block][:, :, None].astype(np.float64), "int8")
+    scale = ref.scales[1][0][:, np.arange(320) // block][:, :, None].astype(np.float64)
+    V = kv8.value_of(ref.codes[1][0], scale, "int8")
     # the weights are equal and the sums of codes exact, so what is off is the
     # rounding of o and of the probabilities
     n = (start + 301 + np.arange(20))[:, None, None]
@@ -516,8 +519,8 @@ def _plain_attention_gpu(p, q, news, lens):
     at = np.arange(L) // p.block
     off = _packed(news)
     for b, (n, ln) in enumerate(zip(news, lens)):
-        K, V = (torch.from_numpy(kv8.value_of(p.codes[i][b, :, :ln], p.scales[i][b][:, at[:ln]][:, :, None], p.fmt)).to(DEV)
-                for i in range(2))
+        K, V = (kv8.value_of(p.codes[i][b, :, :ln], p.scales[i][b][:, at[:ln]][:, :, None], p.fmt) for i in range(2))
+        K, V = torch.from_numpy(K).to(DEV), torch.from_numpy(V).to(DEV)
         x = q[off[b]:off[b + 1]].to(DEV).double().view(n, Hkv, r, D)
         o, oa = (torch.zeros(n, Hkv, r, D, dtype=torch.float64, device=DEV) for _ in range(2))
         for g in range(Hkv):
@@ -571,3 +574,26 @@ def test_attention_of_long_prompts(moelib, cuda_dev, Hq, Hkv, D, block, lens, ne
     p.compare(got.double().cpu().numpy(), want, o_abs, q, lens)
     for _ in range(20):
         assert torch.equal(got, p.attend(q, news, lens))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,lens,news,block", [
+    (16, 2, 256, [20000], [1], 3),       # the split-context kernel
+    (16, 2, 256, [3000], [600], 0),      # the tiles: the first block of a pair, which issues the products,
+    (16, 2, 256, [3000], [600], 1),      # the second,
+    (8, 2, 64, [3000], [900], 2),        # a block on its own
+])
+def test_timeout_is_reported_not_hung(moelib, cuda_dev, Hq, Hkv, D, lens, news, block):
+    """One grid block never brings its operands: the waits run out after 20 ms,
+    the call reports it, and the next one on the same workspace is as before."""
+    p = Pair(moelib, 1, Hkv, D, max(lens), 64, "int8", seed=81)
+    gen = p.fill(lens, seed=82)
+    q = _rand(gen, sum(news), Hq, D).to(torch.bfloat16)
+    want = p.attend(q, news, lens)
+    sh = moelib.kv8_shape(1, sum(news), Hq, Hkv, D, max(lens), 64)
+    ws, x, o = moelib.kv8_alloc_workspace(sh, DEV), q.to(DEV), torch.empty_like(want)
+    off, ln = _i32(_packed(news)), _i32(lens)
+    moelib.kv8_attn_test_stall(sh, x, p.gpu, off, ln, o, ws, block, 20_000_000)
+    assert moelib.status_read(ws[:4].view(torch.int32)) == moelib.MOE_ERR_DEVICE_TIMEOUT
+    moelib.kv8_attn(sh, x, p.gpu, off, ln, o, ws)
+    assert moelib.status_read(ws[:4].view(torch.int32)) == moelib.MOE_OK
+    assert torch.equal(o, want)

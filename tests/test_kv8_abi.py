@@ -11,7 +11,8 @@ ADDR = [0x100000 * (i + 1) for i in range(8)]
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(), 0), (dict(B=0), 2), (dict(B=4097), 2), (dict(T=-1), 2), (dict(T=(1 << 24) + 1), 2), (dict(T=1 << 24), 0), (dict(T=1 << 24, B=1, Hkv=64, Hq=64), 0), (dict(T=1 << 24, B=1, Hkv=65, Hq=65), 2),
+    (dict(), 0), (dict(B=0), 2), (dict(B=4097), 2), (dict(T=-1), 2), (dict(T=(1 << 24) + 1), 2),
+    (dict(T=1 << 24), 0), (dict(T=1 << 24, B=1, Hkv=64, Hq=64), 0), (dict(T=1 << 24, B=1, Hkv=65, Hq=65), 2),
     (dict(Hkv=0), 2), (dict(Hkv=3), 2), (dict(Hq=0), 2), (dict(Hq=130), 2), (dict(Hq=128), 0), (dict(Hq=258), 2),
     (dict(B=4096, Hkv=32, Hq=32), 2), (dict(B=16, Hkv=4096, Hq=4096), 0), (dict(B=1, Hkv=4097, Hq=4097), 2),
     (dict(D=64), 0), (dict(D=128), 0), (dict(D=96), 2), (dict(D=512), 2), (dict(L_max=0), 2), (dict(L_max=1 << 26), 0),
@@ -75,6 +76,8 @@ def test_attention_arguments(moelib):
     for kw in BAD_CACHES:
         assert attn(c=_cache(moelib, **kw)) == 1, kw
     assert attn(n=need - 1) == 3
+    for block, limit in [(-1, 10 ** 6), (0, 0), (0, -5), (0, 10 ** 10)]:
+        assert L.moe_kv8_attn_test_stall(REF(sh), q, REF(c), off, ln, 0.0625, o, ws, need, block, limit, None) == 1
     assert L.moe_kv8_workspace_bytes(None, REF(ctypes.c_size_t())) == 1
     assert L.moe_kv8_workspace_bytes(REF(sh), None) == 1
 
