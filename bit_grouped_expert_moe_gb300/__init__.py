@@ -10,12 +10,13 @@ route_blocks, route, forward, forward_residual, forward_timed, route_noalloc,
 status_read, status_string, test_route_stall, test_decode_stall) and
 include/attention.h (attn_workspace_bytes, attn_decode, attn_decode_timed) and
 include/gdn.h (gdn_scan, gdn_scan_timed) and include/kv8.h (kv8_write,
-kv8_read, kv8_workspace_bytes, kv8_attn).
+kv8_read, kv8_workspace_bytes, kv8_attn, kv8_attn_test_stall).
 """
 from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -381,11 +382,10 @@ def _kv8_refuse(where, what):
 
 
 def _kv8_tensor(where, name, t, dev, dtype, dims, strides):
-    """t's address, after the checks the C entry points cannot make: type,
-    sizes, strides (of dimensions longer than one) and device. The usual
-    tensor passes the first line; a call makes four of these checks."""
-    if t.dtype is dtype and t.shape == dims and t.stride() == strides and t.get_device() == dev:
-        return t.data_ptr()
+    """Refuses a tensor of the wrong type, sizes, strides (of dimensions longer
+    than one) or device: what the C entry points cannot check. The wrappers
+    call this only for a tensor that the usual one's quick test did not pass:
+    at 0.5 us for each of a call's tensors it was a third of a short call."""
     if t.dtype is not dtype:
         _kv8_refuse(where, f"{name} is {t.dtype}, not {dtype}")
     if t.shape != dims:
@@ -395,6 +395,10 @@ def _kv8_tensor(where, name, t, dev, dtype, dims, strides):
     if t.get_device() != dev:
         _kv8_refuse(where, f"{name} is on {t.device}, not on cuda:{dev}")
     return t.data_ptr()
+
+
+_kv8_fields = struct.Struct("10i").unpack  # of a Kv8Shape
+_BF16, _I32 = torch.bfloat16, torch.int32
 
 
 class Kv8Cache:
@@ -427,16 +431,14 @@ class Kv8Cache:
     v_scale = property(lambda self: self._t[3])
 
     def _device(self, where, shape):
-        """The cache's device, after checking that it is the current one and
-        that the cache is one of `shape`."""
-        L = shape.L_max
-        if self._dims != (shape.B, shape.Hkv, L, shape.D) or self._nblk != -(-L // max(shape.block, 1)) or (
-                self._e4m3 and shape.format != KV8_E4M3):
+        """Refuses a cache that is not one of `shape` on the current device; as
+        _kv8_tensor, called where the wrapper's quick test did not pass."""
+        if self._dims != (shape.B, shape.Hkv, shape.L_max, shape.D) or (
+                self._nblk != -(-shape.L_max // max(shape.block, 1))) or (self._e4m3 and shape.format != KV8_E4M3):
             _kv8_refuse(where, f"the cache holds {self._t[0].dtype} codes {self._dims} in {self._nblk} blocks, the "
                                "shape says otherwise")
         if self._dev != torch.cuda.current_device():
             _kv8_refuse(where, f"the cache is on {self._t[0].device}, not on the current device")
-        return self._dev
 
 
 def kv8_alloc_cache(shape: Kv8Shape, device) -> Kv8Cache:
@@ -447,9 +449,7 @@ def kv8_alloc_cache(shape: Kv8Shape, device) -> Kv8Cache:
     return Kv8Cache(*codes, *[torch.empty(shape.B, shape.Hkv, nblk, device=device) for _ in range(2)])
 
 
-def _kv8_stream(stream, dev):
-    # the handle of torch.cuda.current_stream(), without making a Stream object
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+_current_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream()'s handle, without a Stream object
 
 
 def kv8_write(shape, k_new, v_new, offsets, starts, cache: Kv8Cache, status=None, stream=None):
@@ -458,15 +458,23 @@ def kv8_write(shape, k_new, v_new, offsets, starts, cache: Kv8Cache, status=None
     starts[b] .. (int32 [B+1] and [B]). status: an optional zeroed int32
     device word."""
     w = "moe_kv8_write"
-    dev = cache._device(w, shape)
-    T, H, D, B = shape.T, shape.Hkv, shape.D, shape.B
-    dims, strides = (T, H, D), (shape.kv_stride or H * D, D, 1)
-    rc = lib().moe_kv8_write(shape, _kv8_tensor(w, "k_new", k_new, dev, torch.bfloat16, dims, strides),
-                             _kv8_tensor(w, "v_new", v_new, dev, torch.bfloat16, dims, strides),
-                             _kv8_tensor(w, "offsets", offsets, dev, torch.int32, (B + 1,), (1,)),
-                             _kv8_tensor(w, "starts", starts, dev, torch.int32, (B,), (1,)), cache._c,
-                             None if status is None else _kv8_tensor(w, "status", status, dev, torch.int32, (1,), (1,)),
-                             _kv8_stream(stream, dev))
+    B, T, _, H, D, L, block, fmt, _, stride = _kv8_fields(shape)
+    dev, dims, strides = cache._dev, (T, H, D), (stride or H * D, D, 1)
+    if not (cache._dims == (B, H, L, D) and 0 <= cache._nblk * block - L < block and (fmt or not cache._e4m3)
+            and torch.cuda.current_device() == dev):
+        cache._device(w, shape)
+    if not (k_new.dtype is _BF16 and k_new.shape == dims and k_new.stride() == strides and k_new.get_device() == dev):
+        _kv8_tensor(w, "k_new", k_new, dev, _BF16, dims, strides)
+    if not (v_new.dtype is _BF16 and v_new.shape == dims and v_new.stride() == strides and v_new.get_device() == dev):
+        _kv8_tensor(w, "v_new", v_new, dev, _BF16, dims, strides)
+    if not (offsets.dtype is _I32 and offsets.shape == (B + 1,) and offsets.is_contiguous()
+            and offsets.get_device() == dev):
+        _kv8_tensor(w, "offsets", offsets, dev, _I32, (B + 1,), (1,))
+    if not (starts.dtype is _I32 and starts.shape == (B,) and starts.is_contiguous() and starts.get_device() == dev):
+        _kv8_tensor(w, "starts", starts, dev, _I32, (B,), (1,))
+    rc = lib().moe_kv8_write(shape, k_new.data_ptr(), v_new.data_ptr(), offsets.data_ptr(), starts.data_ptr(), cache._c,
+                             None if status is None else _kv8_tensor(w, "status", status, dev, _I32, (1,), (1,)),
+                             _current_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(rc, w)
 
@@ -475,15 +483,23 @@ def kv8_read(shape, cache: Kv8Cache, offsets, starts, k_out, v_out, status=None,
     """moe_kv8_read: positions starts[b] .. of every sequence as bf16, packed
     in k_out, v_out [T, Hkv, D]."""
     w = "moe_kv8_read"
-    dev = cache._device(w, shape)
-    T, H, D, B = shape.T, shape.Hkv, shape.D, shape.B
-    dims, strides = (T, H, D), (H * D, D, 1)
-    rc = lib().moe_kv8_read(shape, cache._c, _kv8_tensor(w, "offsets", offsets, dev, torch.int32, (B + 1,), (1,)),
-                            _kv8_tensor(w, "starts", starts, dev, torch.int32, (B,), (1,)),
-                            _kv8_tensor(w, "k_out", k_out, dev, torch.bfloat16, dims, strides),
-                            _kv8_tensor(w, "v_out", v_out, dev, torch.bfloat16, dims, strides),
-                            None if status is None else _kv8_tensor(w, "status", status, dev, torch.int32, (1,), (1,)),
-                            _kv8_stream(stream, dev))
+    B, T, _, H, D, L, block, fmt, _, _ = _kv8_fields(shape)
+    dev, dims = cache._dev, (T, H, D)
+    if not (cache._dims == (B, H, L, D) and 0 <= cache._nblk * block - L < block and (fmt or not cache._e4m3)
+            and torch.cuda.current_device() == dev):
+        cache._device(w, shape)
+    if not (offsets.dtype is _I32 and offsets.shape == (B + 1,) and offsets.is_contiguous()
+            and offsets.get_device() == dev):
+        _kv8_tensor(w, "offsets", offsets, dev, _I32, (B + 1,), (1,))
+    if not (starts.dtype is _I32 and starts.shape == (B,) and starts.is_contiguous() and starts.get_device() == dev):
+        _kv8_tensor(w, "starts", starts, dev, _I32, (B,), (1,))
+    if not (k_out.dtype is _BF16 and k_out.shape == dims and k_out.is_contiguous() and k_out.get_device() == dev):
+        _kv8_tensor(w, "k_out", k_out, dev, _BF16, dims, (H * D, D, 1))
+    if not (v_out.dtype is _BF16 and v_out.shape == dims and v_out.is_contiguous() and v_out.get_device() == dev):
+        _kv8_tensor(w, "v_out", v_out, dev, _BF16, dims, (H * D, D, 1))
+    rc = lib().moe_kv8_read(shape, cache._c, offsets.data_ptr(), starts.data_ptr(), k_out.data_ptr(), v_out.data_ptr(),
+                            None if status is None else _kv8_tensor(w, "status", status, dev, _I32, (1,), (1,)),
+                            _current_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(rc, w)
 
@@ -503,16 +519,25 @@ def kv8_attn(shape, q, cache: Kv8Cache, offsets, lens, o, workspace, scale=None,
     (offsets int32 [B+1]) over its lens[b] cached positions (int32 [B]); o bf16
     [T, Hq, D]. The workspace's first int32 is the call's device status word."""
     w = "moe_kv8_attn"
-    dev = cache._device(w, shape)
-    T, H, D, B, n = shape.T, shape.Hq, shape.D, shape.B, workspace.numel()
-    dims = (T, H, D)
-    rc = lib().moe_kv8_attn(shape, _kv8_tensor(w, "q", q, dev, torch.bfloat16, dims, (shape.q_stride or H * D, D, 1)),
-                            cache._c, _kv8_tensor(w, "offsets", offsets, dev, torch.int32, (B + 1,), (1,)),
-                            _kv8_tensor(w, "lens", lens, dev, torch.int32, (B,), (1,)),
-                            D ** -0.5 if scale is None else scale,
-                            _kv8_tensor(w, "o", o, dev, torch.bfloat16, dims, (H * D, D, 1)),
-                            _kv8_tensor(w, "workspace", workspace, dev, torch.uint8, (n,), (1,)), n,
-                            _kv8_stream(stream, dev))
+    B, T, H, Hkv, D, L, block, fmt, stride, _ = _kv8_fields(shape)
+    dev, dims, strides, n = cache._dev, (T, H, D), (stride or H * D, D, 1), workspace.numel()
+    if not (cache._dims == (B, Hkv, L, D) and 0 <= cache._nblk * block - L < block and (fmt or not cache._e4m3)
+            and torch.cuda.current_device() == dev):
+        cache._device(w, shape)
+    if not (q.dtype is _BF16 and q.shape == dims and q.stride() == strides and q.get_device() == dev):
+        _kv8_tensor(w, "q", q, dev, _BF16, dims, strides)
+    if not (offsets.dtype is _I32 and offsets.shape == (B + 1,) and offsets.is_contiguous()
+            and offsets.get_device() == dev):
+        _kv8_tensor(w, "offsets", offsets, dev, _I32, (B + 1,), (1,))
+    if not (lens.dtype is _I32 and lens.shape == (B,) and lens.is_contiguous() and lens.get_device() == dev):
+        _kv8_tensor(w, "lens", lens, dev, _I32, (B,), (1,))
+    if not (o.dtype is _BF16 and o.shape == dims and o.is_contiguous() and o.get_device() == dev):
+        _kv8_tensor(w, "o", o, dev, _BF16, dims, (H * D, D, 1))
+    if not (workspace.dtype is torch.uint8 and workspace.is_contiguous() and workspace.get_device() == dev):
+        _kv8_tensor(w, "workspace", workspace, dev, torch.uint8, (n,), (1,))
+    rc = lib().moe_kv8_attn(shape, q.data_ptr(), cache._c, offsets.data_ptr(), lens.data_ptr(),
+                            D ** -0.5 if scale is None else scale, o.data_ptr(), workspace.data_ptr(), n,
+                            _current_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(rc, w)
 
