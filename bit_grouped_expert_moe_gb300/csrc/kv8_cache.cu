@@ -3,6 +3,11 @@
 // Both move bytes and compute almost nothing: a value costs one multiply and
 // one conversion, so they are bound by memory, and at a decode step's sizes
 // by the latency of one dependent chain (tables, values, scale, codes).
+// Measured (2 KV heads of 256, INT8, in a graph):
+//   read of 32,768 positions  101 MB in 19.2 us, 5.2 TB/s, 77% of the measured
+//                             copy rate; instructions take 64% of the issue slots
+//   write of 4096 tokens, and 128 of them read back   8.6 us for 13 and 0.4 MB
+//   write of a token of 64 sequences, and their open blocks read back   8.5 us
 #include "kernels.h"
 #include "kv8_attn.h"
 
@@ -13,7 +18,10 @@ namespace kv8 {
 
 constexpr int kThreads = 256;
 constexpr int kReadTokens = 64;  // packed tokens per tile of the read kernel
-constexpr int kReadBlocks = 4;   // its thread blocks per SM, at most
+// Its thread blocks per SM, at most: as many as a tile each would be 2048 for
+// 32,768 positions, each with the tables and the bisection in front of it: 30.7
+// us, against 19.6 with blocks that walk and ask for a tile ahead.
+constexpr int kReadBlocks = 4;
 
 struct CacheArgs {
   uint8_t* codes[2];    // K, V
@@ -205,8 +213,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_write_kernel(const CacheArgs 
 // Thread blocks walk over tiles of 64 packed tokens of one KV head, K or V. The
 // tables are checked once; a tile's tokens find their sequence and position
 // (by bisection of the offsets), then each thread turns 8-byte pieces of codes
-// into 16 bytes of bf16, so a warp's stores fill whole sectors. The next tile's codes are asked for before
-// this one's are converted.
+// into 16 bytes of bf16, so a warp's stores fill whole sectors. The next tile's
+// codes are asked for before this one's are converted.
 template <int D, int kBlock, bool kE4m3>
 __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const CacheArgs p) {
   constexpr int kRow = D / 8;                           // pieces per token

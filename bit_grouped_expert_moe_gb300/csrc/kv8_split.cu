@@ -4,10 +4,22 @@
 // What bounds it is the cache's bytes: every position is read once per
 // (sequence, KV head, row tile), where a row tile is 8 kNT rows and a row one
 // (query token, query head of the KV head). The positions a tile can see are
-// cut into units of 64 (D = 256) or 128 and all units of the call are laid end to end in the
-// order (sequence, KV head, row tile, position) and dealt out in equal
-// contiguous runs, one per block of a one-block-per-SM grid, so the bytes
+// cut into units of 64 (D = 256) or 128 and all units of the call are laid end
+// to end in the order (sequence, KV head, row tile, position) and dealt out in
+// equal contiguous runs, one per block of a one-block-per-SM grid, so the bytes
 // spread evenly over the SMs whatever the lengths are.
+//
+// Measured (16 heads on 2 x 256 but for the drafts, both kernels, in a run of calls):
+//   one token after 131,072 positions, E4M3    30.9 us, 4.3 TB/s (64% of the
+//                            measured copy rate; 8 us of it do not grow)
+//   one token after 32,768 positions, INT8     15.1 us, 2.2 TB/s
+//   a ragged batch of 8, 148,369 positions     34.0 us, 4.5 TB/s
+//   1 to 5 drafts of 16 sequences, 70,120 positions, 4 x 128, E4M3   34.2 us,
+//                            2.1 TB/s: 12 rows a tile, bound by the consumers,
+//                            two warps a scheduler at 0.37 instructions a cycle
+// What does not grow: the tables, Q and the first codes, three dependent trips
+// to memory, the warps' fold and the merge. A simple kernel, a block per row
+// with plain loads, took 15.9 ms at 32,768 positions.
 //
 // kv8_split_kernel — warp 8 streams each unit's K and V codes into a
 // shared-memory ring by TMA. Four warps take 16 or 32 positions each;
@@ -77,7 +89,9 @@ static_assert(kConsumers * kConsumerRegs + 4 * kProducerRegs <= (kConsumers + 4)
               "register shares");
 constexpr int kMaxCtas = 256;       // workspace bound on the grid
 // Beginning and ending a tile (Q, the warps' fold, the partial state) costs a
-// run about as much as four units: 3 us against 0.7 us a unit of 32 KB.
+// run about as much as four units: 3 us against 0.7 us a unit of 32 KB. A
+// ragged batch of 8 takes 37.9, 33.4, 32.9 us at 2, 4 and 6, the drafts of 16
+// sequences 34.0, 33.3, 34.3.
 constexpr int kTileCost = 4;
 constexpr float kMinusBig = -1e30f; // running-max start: finite, so 2^(m - m_new) is never NaN
 // A row's m is raised to its largest score only when a score passes it by
@@ -924,12 +938,21 @@ cudaError_t codes_map(CUtensorMap* m, const void* base, int D, int L_max, int pa
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Groups of 8 rows per tile: as many as the average sequence's rows fill, up
-// to what two warps have registers for (a wider tile
-// reads the cache fewer times, a narrower one holds fewer idle rows).
+// Groups of 8 rows per tile: as many as the average sequence's rows fill (a
+// wider tile reads and converts the codes fewer times, a narrower one holds
+// fewer idle rows), up to what a warp has registers for at 256 head dims, and
+// up to 2 at 64, whose conversion is the smaller part. Measured, 1 / 2 / 4
+// groups in us, INT8:
+//   12 rows, D = 128, 64 pairs of 4096 positions   33.3 / 28.8 / 35.7
+//   24 rows, D = 128, 64 pairs of 4096 positions   49.4 / 47.5 / 42.0
+//   32 rows, D = 128, 4 pairs of 131,072           78.1 / 56.9 / 47.3
+//   32 rows, D = 128, 4 pairs of 2048               9.7 / 10.6 / 10.7
+//   24 rows, D = 64, 64 pairs of 4096              34.9 / 33.7 / 32.7
+//   24 rows, D = 64, one pair of 20,000            10.2 / 11.3 / 14.3
+//   32 rows, D = 256, 2 pairs of 100,000           60.1 / 50.0
 int groups(int B, int T, int r, int D) {
   const long long rows = (long long)((T + B - 1) / B) * r;
-  const int most = D == 256 ? 2 : 4;
+  const int most = D == 128 ? 4 : 2;
   return rows <= 8 ? 1 : rows <= 16 || most == 2 ? 2 : 4;
 }
 
@@ -964,7 +987,7 @@ cudaError_t launch_groups(int nt, const CUtensorMap& tk, const CUtensorMap& tv, 
                           cudaStream_t stream) {
   if (nt == 1) return launch<D, 1, kE4m3>(tk, tv, prm, grid, stream);
   if (nt == 2) return launch<D, 2, kE4m3>(tk, tv, prm, grid, stream);
-  if constexpr (D < 256) return launch<D, 4, kE4m3>(tk, tv, prm, grid, stream);
+  if constexpr (D == 128) return launch<D, 4, kE4m3>(tk, tv, prm, grid, stream);
   return cudaErrorInvalidValue;
 }
 
