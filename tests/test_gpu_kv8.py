@@ -325,7 +325,7 @@ def test_attention_with_blocks_of_very_different_size(moelib, cuda_dev, news, fm
     assert (o == 0).all()
 
 
-@pytest.mark.parametrize("news", [1, 50])
+@pytest.mark.parametrize("news", [1, 50, 90])
 def test_attention_of_queries_that_are_not_finite(moelib, cuda_dev, news):
     """A NaN or an infinity in one query row stays in that row."""
     p = Pair(moelib, 1, 2, 128, 300, 32, "int8")
