@@ -449,7 +449,9 @@ def kv8_alloc_cache(shape: Kv8Shape, device) -> Kv8Cache:
     return Kv8Cache(*codes, *[torch.empty(shape.B, shape.Hkv, nblk, device=device) for _ in range(2)])
 
 
-_current_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream()'s handle, without a Stream object
+# torch.cuda.current_device() and the handle of torch.cuda.current_stream(),
+# without looking whether CUDA is up (the cache is on it) and a Stream object.
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def kv8_write(shape, k_new, v_new, offsets, starts, cache: Kv8Cache, status=None, stream=None):
@@ -461,7 +463,7 @@ def kv8_write(shape, k_new, v_new, offsets, starts, cache: Kv8Cache, status=None
     B, T, _, H, D, L, block, fmt, _, stride = _kv8_fields(shape)
     dev, dims, strides = cache._dev, (T, H, D), (stride or H * D, D, 1)
     if not (cache._dims == (B, H, L, D) and 0 <= cache._nblk * block - L < block and (fmt or not cache._e4m3)
-            and torch.cuda.current_device() == dev):
+            and dev >= 0 and _current_device() == dev):
         cache._device(w, shape)
     if not (k_new.dtype is _BF16 and k_new.shape == dims and k_new.stride() == strides and k_new.get_device() == dev):
         _kv8_tensor(w, "k_new", k_new, dev, _BF16, dims, strides)
@@ -486,7 +488,7 @@ def kv8_read(shape, cache: Kv8Cache, offsets, starts, k_out, v_out, status=None,
     B, T, _, H, D, L, block, fmt, _, _ = _kv8_fields(shape)
     dev, dims = cache._dev, (T, H, D)
     if not (cache._dims == (B, H, L, D) and 0 <= cache._nblk * block - L < block and (fmt or not cache._e4m3)
-            and torch.cuda.current_device() == dev):
+            and dev >= 0 and _current_device() == dev):
         cache._device(w, shape)
     if not (offsets.dtype is _I32 and offsets.shape == (B + 1,) and offsets.is_contiguous()
             and offsets.get_device() == dev):
@@ -522,7 +524,7 @@ def kv8_attn(shape, q, cache: Kv8Cache, offsets, lens, o, workspace, scale=None,
     B, T, H, Hkv, D, L, block, fmt, stride, _ = _kv8_fields(shape)
     dev, dims, strides, n = cache._dev, (T, H, D), (stride or H * D, D, 1), workspace.numel()
     if not (cache._dims == (B, Hkv, L, D) and 0 <= cache._nblk * block - L < block and (fmt or not cache._e4m3)
-            and torch.cuda.current_device() == dev):
+            and dev >= 0 and _current_device() == dev):
         cache._device(w, shape)
     if not (q.dtype is _BF16 and q.shape == dims and q.stride() == strides and q.get_device() == dev):
         _kv8_tensor(w, "q", q, dev, _BF16, dims, strides)

@@ -4,10 +4,10 @@
 // one conversion, so they are bound by memory, and at a decode step's sizes
 // by the latency of one dependent chain (tables, values, scale, codes).
 // Measured (2 KV heads of 256, INT8, in a graph):
-//   read of 32,768 positions  101 MB in 19.2 us, 5.2 TB/s, 77% of the measured
+//   read of 32,768 positions  101 MB in 18.7 us, 5.4 TB/s, 79% of the measured
 //                             copy rate; instructions take 64% of the issue slots
 //   write of 4096 tokens, and 128 of them read back   8.6 us for 13 and 0.4 MB
-//   write of a token of 64 sequences, and their open blocks read back   8.5 us
+//   write of a token of 64 sequences, and their open blocks read back   9.2 us
 #include "kernels.h"
 #include "kv8_attn.h"
 
@@ -17,7 +17,6 @@ namespace bgmoe {
 namespace kv8 {
 
 constexpr int kThreads = 256;
-constexpr int kReadTokens = 64;  // packed tokens per tile of the read kernel
 // Its thread blocks per SM, at most: as many as a tile each would be 2048 for
 // 32,768 positions, each with the tables and the bisection in front of it: 30.7
 // us, against 19.6 with blocks that walk and ask for a tile ahead.
@@ -70,7 +69,10 @@ __device__ __forceinline__ bool tables_bad(const CacheArgs& p, Hit hit) {
 // A unit has 64 values per thread, kPer 16-byte pieces, which stay in registers
 // between the maximum and the codes, so they are read once, with all loads in
 // flight together: a warp for a block of 16 x 64 values, the whole thread block
-// of 256 for one of 64 x 256.
+// of 256 for one of 64 x 256. The rare values that are not finite are read
+// again instead, in loops of their own: 80 registers for 128, so that three
+// thread blocks fit an SM. 5617 tokens of 5 sequences, 8 heads of 128, written
+// and read back: 20.9 -> 16.0 us.
 template <int D, int kBlock>
 struct WriteCfg {
   static constexpr int kUnitThreads = kBlock * D / 64 < 32 ? 32 : kBlock * D / 64;
@@ -79,7 +81,7 @@ struct WriteCfg {
 };
 
 template <int D, int kBlock, bool kE4m3>
-__global__ void __launch_bounds__(kThreads, 2) kv8_write_kernel(const CacheArgs p) {
+__global__ void __launch_bounds__(kThreads, 3) kv8_write_kernel(const CacheArgs p) {
   using W = WriteCfg<D, kBlock>;
   constexpr int kPer = W::kPer, kTU = W::kUnitThreads;
   __shared__ int s_b[W::kUnits], s_lo[W::kUnits], s_n[W::kUnits], s_start[W::kUnits];
@@ -150,31 +152,23 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_write_kernel(const CacheArgs 
     return m;
   };
   uint32_t m = unit_max(mx, 0);
-  if (m >= 0x7F80u) {  // an infinity or a NaN: the maximum again over finite values, then replace them
+  const bool odd = m >= 0x7F80u;  // an infinity or a NaN: the maximum again over finite values, and they are replaced
+  auto reload = [&](int piece) { return ldg_nc_v4(x + (size_t)(piece / (D / 8)) * p.stride + piece % (D / 8) * 8); };
+  const int pieces = (r1 - r0) * (D / 8);
+  if (odd) {
     if (tu == 0) flag(p.status, (int32_t)MOE_ERR_RANGE);
     mx = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll 1
+    for (int piece = tu; piece < pieces; piece += kTU) {
+      const uint4 y = reload(piece);
+      const uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t a = w[j] & 0x7FFFu, z = (w[j] >> 16) & 0x7FFFu;
-        if (a < 0x7F80u) mx = max(mx & 0xFFFFu, a) | (mx & 0xFFFF0000u);
-        if (z < 0x7F80u) mx = max(mx >> 16, z) << 16 | (mx & 0xFFFFu);
+        const uint32_t lo2 = w[j] & 0x7FFFu, hi2 = (w[j] >> 16) & 0x7FFFu;
+        mx = __vmaxu2(mx, (lo2 < 0x7F80u ? lo2 : 0u) | (hi2 < 0x7F80u ? hi2 : 0u) << 16);
       }
     }
     m = unit_max(mx, 1);
-    auto finite = [&](uint32_t h) -> uint32_t {        // one bf16
-      const uint32_t a = h & 0x7FFFu;
-      return a < 0x7F80u ? h : a == 0x7F80u ? (h & 0x8000u) | m : 0u;
-    };
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      v[i].x = finite(v[i].x & 0xFFFFu) | finite(v[i].x >> 16) << 16;
-      v[i].y = finite(v[i].y & 0xFFFFu) | finite(v[i].y >> 16) << 16;
-      v[i].z = finite(v[i].z & 0xFFFFu) | finite(v[i].z >> 16) << 16;
-      v[i].w = finite(v[i].w & 0xFFFFu) | finite(v[i].w >> 16) << 16;
-    }
   }
   const float s_new = fmaxf(s_old, scale_of<kE4m3>(__uint_as_float(m << 16)));
   const float inv = inverse_scale(s_new);
@@ -193,12 +187,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_write_kernel(const CacheArgs 
   }
   if (kTU == 32) __syncwarp();  // s_old has been read by all
   if (tu == 0 && (p0 == base || s_new != s_old)) *scale = s_new;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int piece = tu + i * kTU;
-    const int row = piece / (D / 8), c = piece % (D / 8);
-    if (row >= r1 - r0) continue;
-    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+  // 8 new values to codes (the new rows' codes follow one another)
+  auto put = [&](int piece, const uint32_t (&w)[4]) {
     uint32_t o[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -206,16 +196,36 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_write_kernel(const CacheArgs 
       const float f2 = __uint_as_float(w[2 * j + 1] << 16), f3 = __uint_as_float(w[2 * j + 1] & 0xFFFF0000u);
       o[j] = encode4<kE4m3>(f0 * inv, f1 * inv, f2 * inv, f3 * inv);
     }
-    *reinterpret_cast<uint2*>(codes + (size_t)(r0 + row) * D + c * 8) = make_uint2(o[0], o[1]);
+    *reinterpret_cast<uint2*>(codes + (size_t)r0 * D + (size_t)piece * 8) = make_uint2(o[0], o[1]);
+  };
+  if (odd) {
+    auto finite = [&](uint32_t h) -> uint32_t {  // one bf16
+      const uint32_t a = h & 0x7FFFu;
+      return a < 0x7F80u ? h : a == 0x7F80u ? (h & 0x8000u) | m : 0u;
+    };
+#pragma unroll 1
+    for (int piece = tu; piece < pieces; piece += kTU) {
+      const uint4 y = reload(piece);
+      uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = finite(w[j] & 0xFFFFu) | finite(w[j] >> 16) << 16;
+      put(piece, w);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    if (tu + i * kTU < pieces) put(tu + i * kTU, w);
   }
 }
 
-// Thread blocks walk over tiles of 64 packed tokens of one KV head, K or V. The
+// Thread blocks walk over tiles of kReadTokens packed tokens of one KV head, K or V. The
 // tables are checked once; a tile's tokens find their sequence and position
 // (by bisection of the offsets), then each thread turns 8-byte pieces of codes
 // into 16 bytes of bf16, so a warp's stores fill whole sectors. The next tile's
 // codes are asked for before this one's are converted.
-template <int D, int kBlock, bool kE4m3>
+template <int D, int kBlock, bool kE4m3, int kReadTokens>
 __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const CacheArgs p) {
   constexpr int kRow = D / 8;                           // pieces per token
   constexpr int kPer = kReadTokens * kRow / kThreads;   // pieces per thread
@@ -227,7 +237,7 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const CacheArgs p) {
     return;
   }
   const int per = 2 * p.Hkv, tiles = (p.T + kReadTokens - 1) / kReadTokens * per;
-  auto find = [&](int tile, int buf) {                  // by the first 64 threads
+  auto find = [&](int tile, int buf) {                  // by the first kReadTokens threads
     const int t = tile / per * kReadTokens + threadIdx.x, g = (tile % per) >> 1;
     if (threadIdx.x >= kReadTokens || t >= p.T) return;
     int b = 0, z = p.B;                                 // the last sequence that starts at or before t
@@ -332,9 +342,15 @@ cudaError_t launch_one(const CacheArgs& p, bool write, int sms, cudaStream_t s) 
     constexpr int kUnits = WriteCfg<D, kBlock>::kUnits;
     return launch(kv8_write_kernel<D, kBlock, kE4m3>, (items + kUnits - 1) / kUnits, p, s);
   }
-  const long long tiles = (long long)((p.T + kReadTokens - 1) / kReadTokens) * 2 * p.Hkv;
+  // Tiles of 64 tokens, or larger ones where those fill the grid as well (64
+  // and larger, in us): 1000 tokens of 2 sequences, one head of 64, 2.2 and 3.0;
+  // 131,072 tokens of such a head 12.3 and 9.5; 12,000 of 8 heads of 128 17.0
+  // and 14.7; 32,768 of 2 heads of 256 19.3 and 18.7.
+  constexpr int kSmall = 64, kLarge = D == 64 ? 256 : 128;
+  auto tiles = [&](int tokens) { return (long long)((p.T + tokens - 1) / tokens) * 2 * p.Hkv; };
   const long long most = (long long)sms * kReadBlocks;
-  return launch(kv8_read_kernel<D, kBlock, kE4m3>, tiles < most ? tiles : most, p, s);
+  if (tiles(kLarge) >= most) return launch(kv8_read_kernel<D, kBlock, kE4m3, kLarge>, most, p, s);
+  return launch(kv8_read_kernel<D, kBlock, kE4m3, kSmall>, tiles(kSmall) < most ? tiles(kSmall) : most, p, s);
 }
 
 template <int D, bool kE4m3>
