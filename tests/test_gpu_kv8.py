@@ -188,6 +188,17 @@ def test_write_and_read_are_the_oracles(moelib, cuda_dev, case, fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,lens", [(64, [7001, 0, 1, 3333]), (128, [2500, 2777]), (256, [5003, 64, 1])])
+def test_write_and_read_of_many_tokens(moelib, cuda_dev, D, lens, fmt):
+    """More tiles than the read kernel's blocks, of the larger kind."""
+    p = Pair(moelib, len(lens), 8, D, max(lens), 32, fmt, seed=5)
+    p.fill(lens, seed=6)
+    p.check()
+    p.read(lens, [0] * len(lens))
+    p.read([max(n - 17, 0) for n in lens], [min(n, 17) for n in lens])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_write_of_strided_tokens(moelib, cuda_dev, fmt):
     """Keys and values as column ranges of one projection output."""
     p = Pair(moelib, 2, 2, 128, 100, 32, fmt)
