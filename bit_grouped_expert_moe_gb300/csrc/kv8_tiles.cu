@@ -867,18 +867,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
           }
 #pragma unroll 1
           for (int j = d0; j < d0 + D / 2; j += 32) {
-            float v[32];
-            tmem_ld_32(lane_addr + j, v);
             __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint32_t z[4];
+            for (int h = 0; h < 32; h += 16) {
+              uint32_t v[16];
+              tmem_ld_16(lane_addr + j + h, v);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const __nv_bfloat162 y = __floats2bfloat162_rn(v[e + 2 * k] * inv, v[e + 2 * k + 1] * inv);
-                z[k] = *reinterpret_cast<const uint32_t*>(&y);
+              for (int e = 0; e < 16; e += 8) {
+                uint32_t z[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(v[e + 2 * k]) * inv,
+                                                                 __uint_as_float(v[e + 2 * k + 1]) * inv);
+                  z[k] = *reinterpret_cast<const uint32_t*>(&y);
+                }
+                sts128(stage + lane * F::kOutPitch + 2 * (h + e), z[0], z[1], z[2], z[3]);
               }
-              sts128(stage + lane * F::kOutPitch + 2 * e, z[0], z[1], z[2], z[3]);
             }
             __syncwarp();
 #pragma unroll
