@@ -1,6 +1,8 @@
 // Host-side launchers of the 8-bit cache's attention kernels.
 #pragma once
 
+#include <atomic>
+
 #include "kv8.cuh"
 
 namespace bgmoe {
@@ -222,7 +224,7 @@ __device__ inline bool find_run(const int32_t* offsets, const int32_t* lens, int
 // Moves registers between a block's warpgroups: every warp of a group calls one
 // of the two. A share above a thread's registers at launch waits until the
 // other groups have given theirs, so the shares add up to what the block was
-// launched with, which launches_with checks before the first launch.
+// launched with, which launch_registers checks before the first launch.
 template <int kRegs>
 __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
@@ -232,9 +234,14 @@ __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 template <class Kernel>
-bool launches_with(Kernel kernel, int regs) {
+cudaError_t launch_registers(Kernel kernel, int regs, std::atomic<bool>* known) {
+  if (known->load(std::memory_order_relaxed)) return cudaSuccess;
   cudaFuncAttributes a;
-  return cudaFuncGetAttributes(&a, kernel) == cudaSuccess && a.numRegs == regs;
+  const cudaError_t e = cudaFuncGetAttributes(&a, kernel);
+  if (e != cudaSuccess) return e;
+  if (a.numRegs != regs) return cudaErrorInvalidKernelImage;
+  known->store(true, std::memory_order_relaxed);
+  return cudaSuccess;
 }
 
 }  // namespace kv8

@@ -966,9 +966,9 @@ template <int D, int kNT, bool kE4m3>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const Params& prm, int grid, cudaStream_t stream) {
   static SmemLimitMemo smem_memo;
   cudaError_t e = ensure_smem(kv8_split_kernel<D, kNT, kE4m3>, Cfg<D, kNT>::kBytes, &smem_memo);
+  static std::atomic<bool> known{false};
+  if (e == cudaSuccess) e = launch_registers(kv8_split_kernel<D, kNT, kE4m3>, kLaunchRegs, &known);
   if (e != cudaSuccess) return e;
-  static const bool shares = launches_with(kv8_split_kernel<D, kNT, kE4m3>, kLaunchRegs);
-  if (!shares) return cudaErrorInvalidKernelImage;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kThreads);

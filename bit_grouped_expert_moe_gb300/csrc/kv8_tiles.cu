@@ -1241,10 +1241,10 @@ moe_status launch_tiles(const AttnArgs& a, cudaStream_t stream) {
     constexpr int D = decltype(d)::value;
     constexpr bool kE4m3 = decltype(fp8)::value;
     static SmemLimitMemo smem_memo;
-    const cudaError_t e = ensure_smem(kv8_tiles_kernel<D, kE4m3>, Cfg<D>::kBytes, &smem_memo);
+    static std::atomic<bool> known{false};
+    cudaError_t e = ensure_smem(kv8_tiles_kernel<D, kE4m3>, Cfg<D>::kBytes, &smem_memo);
+    if (e == cudaSuccess) e = launch_registers(kv8_tiles_kernel<D, kE4m3>, kLaunchRegs, &known);
     if (e != cudaSuccess) return e;
-    static const bool shares = launches_with(kv8_tiles_kernel<D, kE4m3>, kLaunchRegs);
-    if (!shares) return cudaErrorInvalidKernelImage;
     cfg.dynamicSmemBytes = Cfg<D>::kBytes;
     return cudaLaunchKernelEx(&cfg, kv8_tiles_kernel<D, kE4m3>, prm);
   };

@@ -18,6 +18,10 @@ Attention, per element, from the arithmetic (u = 2^-24):
   * the sum over positions runs in chains of at most L / 16 + 64 additions,
     each off by 2 u of at most the largest stored V magnitude.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -608,3 +612,32 @@ def test_timeout_is_reported_not_hung(moelib, cuda_dev, Hq, Hkv, D, lens, news, 
     moelib.kv8_attn(sh, x, p.gpu, off, ln, o, ws)
     assert moelib.status_read(ws[:4].view(torch.int32)) == moelib.MOE_OK
     assert torch.equal(o, want)
+
+
+FIRST_CALL = """
+import torch
+import bit_grouped_expert_moe_gb300 as m
+i32 = dict(dtype=torch.int32, device="cuda")
+for n in (1, 200):
+    sh = m.kv8_shape(1, n, 8, 2, 128, 256, 32)
+    cache, off, st = m.kv8_alloc_cache(sh, "cuda"), torch.tensor([0, n], **i32), torch.zeros(1, **i32)
+    x = torch.ones(n, 2, 128, dtype=torch.bfloat16, device="cuda")
+    q, ws, ln = torch.zeros(n, 8, 128, dtype=torch.bfloat16, device="cuda"), m.kv8_alloc_workspace(sh, "cuda"), st + n
+    o, y, z = torch.zeros_like(q), torch.zeros_like(x), torch.zeros_like(x)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        m.kv8_write(sh, x, x, off, st, cache)
+        m.kv8_read(sh, cache, off, st, y, z)
+        m.kv8_attn(sh, q, cache, off, ln, o, ws)
+    g.replay()
+    torch.cuda.synchronize()
+    assert m.status_read(ws[:4].view(torch.int32)) == 0
+    assert (y == 1).all() and (z == 1).all() and (o == 1).all()
+"""
+
+
+def test_first_calls_may_be_captured(moelib, cuda_dev):
+    """In a process of its own, whose first calls are made during a capture."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
