@@ -119,10 +119,11 @@ __device__ inline long long places_before(int n, int len, int r, int RT, int KT,
 }
 
 // The first unit at or after a place: unit i of the nb of row tile rt of KV head
-// g of sequence b (b = -1: past the last), the units before it, and its tile's
-// number in the order (sequence, KV head, row tile).
+// g of sequence b (b = -1: past the last), which owns tokens lo .. lo + n - 1 and
+// len positions; the units before it, and its tile's number in the order
+// (sequence, KV head, row tile).
 struct Place {
-  int b, g, rt, i, nb, tile;
+  int b, g, rt, i, nb, tile, lo, n, len;
   long long units;
 };
 
@@ -134,28 +135,30 @@ __device__ inline bool find_run(const int32_t* offsets, const int32_t* lens, int
   long long total = 0, before = 0, units = 0, at = 0;
   int tiles = 0;
   bool bad = false;
-  Place k{-1, 0, 0, 0, 0, 0, 0};
+  Place k{};
+  k.b = -1;
   // Pass 0 counts, pass 1 searches: one copy of the code, which runs cold.
 #pragma unroll 1
   for (int base = 0, pass = 0; base < B;) {
     const int b = base + lane;
-    long long v = 0, w = 0;  // this lane's sequence: places, units
-    int nt = 0;
+    long long v1 = 0, w1 = 0;  // this lane's sequence, per KV head: places, units
+    int nt1 = 0, lo = 0, hi = 0, len = 0;
     if (b < B) {
-      const int lo = __ldg(offsets + b), hi = __ldg(offsets + b + 1), len = __ldg(lens + b);
+      lo = __ldg(offsets + b), hi = __ldg(offsets + b + 1), len = __ldg(lens + b);
       if (offsets_bad(lo, hi, b, B, T) || len < 0 || len > L_max) {
         bad = true;
       } else {
-        nt = seq_tiles(hi - lo, r, RT);
-        w = units_before(hi - lo, len, r, RT, KT, nt) * Hkv;
-        v = w + (long long)cost * (nt - empty_tiles(hi - lo, len, r, RT)) * Hkv;
-        nt *= Hkv;
+        nt1 = seq_tiles(hi - lo, r, RT);
+        w1 = units_before(hi - lo, len, r, RT, KT, nt1);
+        v1 = w1 + (long long)cost * (nt1 - empty_tiles(hi - lo, len, r, RT));
       }
     }
+    const long long v = v1 * Hkv, w = w1 * Hkv;
+    const int nt = nt1 * Hkv;
     long long vi = v, wi = w;
     int ti = nt;
 #pragma unroll 1
-    for (int o = 1; o < 32; o <<= 1) {
+    for (int o = 1; o < min(B, 32); o <<= 1) {
       const long long x = __shfl_up_sync(0xffffffffu, vi, o), y = __shfl_up_sync(0xffffffffu, wi, o);
       const int z = __shfl_up_sync(0xffffffffu, ti, o);
       if (lane >= o) {
@@ -164,7 +167,8 @@ __device__ inline bool find_run(const int32_t* offsets, const int32_t* lens, int
         ti += z;
       }
     }
-    const long long all = __shfl_sync(0xffffffffu, vi, 31);
+    const int end = min(B, 32) - 1;  // the last lane that the sums reach
+    const long long all = __shfl_sync(0xffffffffu, vi, end);
     base += 32;
     if (pass == 0) {
       total += all;
@@ -183,12 +187,13 @@ __device__ inline bool find_run(const int32_t* offsets, const int32_t* lens, int
       const int L = __ffs(hit) - 1;
       k.b = base - 32 + L;
       long long off = at - (before + __shfl_sync(0xffffffffu, vi - v, L));
-      const long long per = div_small(__shfl_sync(0xffffffffu, v, L), Hkv);
+      const long long per = __shfl_sync(0xffffffffu, v1, L), per_units = __shfl_sync(0xffffffffu, w1, L);
       units += __shfl_sync(0xffffffffu, wi - w, L);
       tiles += __shfl_sync(0xffffffffu, ti - nt, L);
-      const long long per_units = div_small(__shfl_sync(0xffffffffu, w, L), Hkv);
-      const int lo = __ldg(offsets + k.b), n = __ldg(offsets + k.b + 1) - lo, len = __ldg(lens + k.b);
-      const int all_tiles = seq_tiles(n, r, RT);
+      k.lo = __shfl_sync(0xffffffffu, lo, L);
+      k.n = __shfl_sync(0xffffffffu, hi, L) - k.lo;
+      k.len = __shfl_sync(0xffffffffu, len, L);
+      const int all_tiles = __shfl_sync(0xffffffffu, nt1, L);
       k.g = (int)div_small(off, per);
       off -= k.g * per;
       // the last tile whose first place is at or before off, 32 candidates a
@@ -198,22 +203,22 @@ __device__ inline bool find_run(const int32_t* offsets, const int32_t* lens, int
 #pragma unroll 1
       while (z - a > 1) {
         const int step = (z - a + 31) / 32, cand = a + lane * step;
-        const bool in = cand < z && places_before(n, len, r, RT, KT, cost, cand) <= off;
+        const bool in = cand < z && places_before(k.n, k.len, r, RT, KT, cost, cand) <= off;
         const int last = 31 - __clz(__ballot_sync(0xffffffffu, in));
         a += last * step;
         z = min(z, a + step);
       }
       k.rt = a;
-      k.nb = tile_units(n, len, r, RT, KT, a);
-      const long long first = units_before(n, len, r, RT, KT, a);
-      k.i = max((int)(off - first) - cost * (max(a - empty_tiles(n, len, r, RT), 0) + 1), 0);
+      k.nb = tile_units(k.n, k.len, r, RT, KT, a);
+      const long long first = units_before(k.n, k.len, r, RT, KT, a);
+      k.i = max((int)(off - first) - cost * (max(a - empty_tiles(k.n, k.len, r, RT), 0) + 1), 0);
       units += k.g * per_units + first + k.i;
       k.tile = tiles + k.g * all_tiles + a;
       break;
     }
     before += all;
-    units += __shfl_sync(0xffffffffu, wi, 31);
-    tiles += __shfl_sync(0xffffffffu, ti, 31);
+    units += __shfl_sync(0xffffffffu, wi, end);
+    tiles += __shfl_sync(0xffffffffu, ti, end);
   }
   k.units = units;
   *out = k;

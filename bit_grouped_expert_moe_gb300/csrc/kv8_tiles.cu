@@ -562,7 +562,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
         Cursor cur{};
         if (ok && k.b >= 0) {
           cur.b = k.b;
-          cur.sequence(p);
+          cur.lo = k.lo;
+          cur.n = k.n;
+          cur.len = k.len;
           cur.g = k.g;
           cur.rt = k.rt;
           cur.i = k.i;
