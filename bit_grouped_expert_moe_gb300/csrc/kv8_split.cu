@@ -10,16 +10,18 @@
 // spread evenly over the SMs whatever the lengths are.
 //
 // Measured (16 heads on 2 x 256 but for the drafts, both kernels, in a run of calls):
-//   one token after 131,072 positions, E4M3    30.9 us, 4.3 TB/s (64% of the
-//                            measured copy rate; 8 us of it do not grow)
-//   one token after 32,768 positions, INT8     15.1 us, 2.2 TB/s
-//   a ragged batch of 8, 148,369 positions     34.0 us, 4.5 TB/s
-//   1 to 5 drafts of 16 sequences, 70,120 positions, 4 x 128, E4M3   34.2 us,
+//   one token after 131,072 positions, E4M3    30.1 us, 4.5 TB/s (66% of the
+//                            measured copy rate; 7.5 us of it do not grow)
+//   one token after 32,768 positions, INT8     14.6 us, 2.3 TB/s
+//   a ragged batch of 8, 148,369 positions     33.5 us, 4.5 TB/s
+//   1 to 5 drafts of 16 sequences, 70,120 positions, 4 x 128, E4M3   33.6 us,
 //                            2.1 TB/s: 12 rows a tile, bound by the consumers,
 //                            two warps a scheduler at 0.37 instructions a cycle
-// What does not grow: the tables, Q and the first codes, three dependent trips
-// to memory, the warps' fold and the merge. A simple kernel, a block per row
-// with plain loads, took 15.9 ms at 32,768 positions.
+// What does not grow (one token after 300 positions, from the wait for the
+// predecessors): 1.6 us the tables and the run's start, 0.8 Q, 1.1 the first
+// codes and their unit, 1.3 the fold, 0.9 to the merge's start, 1.5 the merge.
+// A simple kernel, a block per row with plain loads, took 15.9 ms at 32,768
+// positions.
 //
 // kv8_split_kernel — warp 8 streams each unit's K and V codes into a
 // shared-memory ring by TMA. Four warps take 16 or 32 positions each;
