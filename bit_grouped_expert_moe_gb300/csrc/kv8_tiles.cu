@@ -47,7 +47,7 @@
 // the tensor cores run 57% of a unit's 3600 cycles: a product S or O takes 1024
 // and about 500 from its issue to the softmax's first read, and the softmax
 // (2400) leaves the two products no more overlap. 1.42 PFLOP/s, 75% of the
-// measured bf16 rate; a prompt of 4096 1.02 PFLOP/s, 54%: 60 units per pair are
+// measured bf16 rate; a prompt of 4096 1.02 PFLOP/s, 54%: 56 units per pair are
 // few beside the tiles' beginnings and ends. At 128 head dims the softmax
 // bounds a unit: 2000 queries after 28,000 positions, 555 us, 0.86 PFLOP/s.
 //
@@ -81,8 +81,8 @@ constexpr int kMmaWarp = 16, kNoteWarp = 17;
 constexpr int kThreads = 20 * 32;
 // Registers per thread: 96 at launch (640 x 96 in all), then 128 for the 8
 // softmax warps, 88 for the 8 converting ones and 48 for the rest:
-// 256 x 128 + 256 x 88 + 128 x 48 = 640 x 96. (With 120 and 96 the chunk of the
-// table below takes 417 us for 401; with 136 and 80 the prompt 171 for 148.)
+// 256 x 128 + 256 x 88 + 128 x 48 = 640 x 96. (With 120 and 96 the chunk above
+// takes 417 us for 401; with 136 and 80 the prompt 171 for 148.)
 constexpr int kLaunchRegs = 96, kSoftRegs = 128, kConvRegs = 88, kMmaRegs = 48;
 static_assert(256 * kSoftRegs + 256 * kConvRegs + 128 * kMmaRegs <= kThreads * kLaunchRegs, "register shares");
 static_assert(kSoftRegs >= kLaunchRegs && kConvRegs <= kLaunchRegs && kMmaRegs <= kLaunchRegs,
