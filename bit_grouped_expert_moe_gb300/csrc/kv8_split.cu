@@ -784,13 +784,15 @@ struct MergeParams {
 };
 
 // Thread t holds dims 4 (t % 16) .. + 3 of the slice and takes the covering grid
-// blocks c0 + t / 16, c0 + 16 + t / 16, ...: all loads of kMergeBatch states are
-// issued before any is used. Then the 16 are merged in shared memory.
-constexpr int kMergeWarps = 8;
-constexpr int kMergeLanes = 16;
+// blocks c0 + t / 16, c0 + kLanes + t / 16, ...: all loads of kMergeBatch states
+// are issued before any is used. Then the kLanes sums are merged in shared memory.
+// 16 of them, or 4 where the SMs do not hold that many threads for every row and
+// slice at once (many rows have few states each): see launch_split.
 constexpr int kMergeBatch = 5;  // 16 times 5: the 76 states of a pair of two on 152 SMs at once
 
-__global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_kernel(const MergeParams p) {
+template <int kLanes>
+__global__ void __launch_bounds__(kLanes * 16) kv8_merge_kernel(const MergeParams p) {
+  constexpr int kMergeWarps = kLanes / 2;
   // The next call's split kernel may launch now: it waits for this grid to
   // finish before it touches the workspace.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -799,7 +801,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_kernel(const Merge
   const int r = p.Hq / p.Hkv, RT = p.RT, C = p.C, D = p.D;
   const int t = blockIdx.x / p.Hq, h = blockIdx.x - t * p.Hq;
   const int lane = threadIdx.x & 31, f4 = threadIdx.x & 15, sl = threadIdx.x >> 4;
-  __shared__ float s_m[kMergeLanes], s_l[kMergeLanes], s_o[kMergeLanes][64];
+  __shared__ float s_m[kLanes], s_l[kLanes], s_o[kLanes][64];
   __shared__ int s_range[2], s_first;
   // every warp: the sequence, and the tiles before it
   int tiles = 0, b = -1, lo = 0, n = 0, len = 0;
@@ -860,12 +862,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_kernel(const Merge
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
   int failed = 0;
 #pragma unroll 1
-  for (int base = c0 + sl; base <= c1; base += kMergeLanes * kMergeBatch) {
+  for (int base = c0 + sl; base <= c1; base += kLanes * kMergeBatch) {
     float mc[kMergeBatch], lc[kMergeBatch];
     float4 oc[kMergeBatch];
 #pragma unroll
     for (int u = 0; u < kMergeBatch; ++u) {
-      const int cc = base + u * kMergeLanes;
+      const int cc = base + u * kLanes;
       mc[u] = kMinusBig;
       lc[u] = 0.f;
       oc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -900,9 +902,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_kernel(const Merge
   if (threadIdx.x < 64) {
     float Mt = kMinusBig, Lt = 0.f, Ot = 0.f;
 #pragma unroll
-    for (int w = 0; w < kMergeLanes; ++w) Mt = fmaxf(Mt, s_m[w]);
+    for (int w = 0; w < kLanes; ++w) Mt = fmaxf(Mt, s_m[w]);
 #pragma unroll
-    for (int w = 0; w < kMergeLanes; ++w) {
+    for (int w = 0; w < kLanes; ++w) {
       const float e = ex2(s_m[w] - Mt);
       Lt = fmaf(e, s_l[w], Lt);
       Ot = fmaf(e, s_o[w][threadIdx.x], Ot);
@@ -1036,14 +1038,20 @@ moe_status launch_split(const AttnArgs& a, cudaStream_t stream) {
                        a.B,       a.T,    a.Hq, a.Hkv, a.D,  a.L_max, RT,     grid};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.T * (unsigned)a.Hq, (unsigned)(a.D / 64));
-  cfg.blockDim = dim3(kMergeWarps * 32);
+  // An SM holds four blocks of 256 threads, or 16 of 64: more than one wave of
+  // the larger would wait for the split kernel and look up the tables again.
+  // Larger / smaller, both kernels in us: drafts of 16 sequences (1472 rows and
+  // slices) 32.7 / 29.6; a token of 64 sequences, 2 heads of 256 (4096) 48.8 /
+  // 37.1; of 8 (512) 32.6 / 35.4; one token after 32,768 positions 12.7 / 18.2.
+  const bool wide = (long long)a.T * a.Hq * (a.D / 64) <= 4ll * sms;
+  cfg.blockDim = dim3(wide ? 256 : 64);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kv8_merge_kernel, mp);
+  e = wide ? cudaLaunchKernelEx(&cfg, kv8_merge_kernel<16>, mp) : cudaLaunchKernelEx(&cfg, kv8_merge_kernel<4>, mp);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "merge kernel launch");
 }
 
