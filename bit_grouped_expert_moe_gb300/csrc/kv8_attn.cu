@@ -21,22 +21,23 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // Which kernels serve a call: the split-context ones read the cache once per 8
 // to 32 rows (query heads of a KV head x tokens), the tiles once per 128 or 256
-// but with a longer chain in front. So a call is the former's with up to 24
+// but with a longer chain in front. So a call is the former's with up to 36
 // rows per sequence and KV head, or somewhat more where few of those pairs
 // keep the GPU's blocks from filling up. (The host knows the tokens of the
 // batch, not each sequence's.) Measured, split / tiles in us, INT8, n tokens of
 // each of B sequences over L positions:
-//   16 heads / 2 x 256, B = 1, L = 32,768:   n = 12 49.2 / 55.9, n = 16 62.5 / 57.4
-//                       B = 1, L = 2048:     n = 32 24.2 / 30.1, n = 64 39.1 / 33.0
-//                       B = 16, L = 4096:    n = 2 31.4 / 47.7, n = 4 52.5 / 47.1
-//   16 heads / 4 x 128, B = 1, L = 32,768:   n = 24 39.1 / 43.6, n = 32 48.6 / 44.5
-//                       B = 16, L = 4096:    n = 8 46.2 / 59.2, n = 12 72.8 / 59.3
-//                       B = 16, L = 512:     n = 4 18.3 / 22.2, n = 8 28.8 / 22.3
-//   8 heads / 8 x 128,  B = 1, L = 32,768:   n = 64 50.1 / 60.2
-//                       B = 16, L = 512:     n = 12 25.0 / 29.0, n = 24 39.9 / 29.2
-//   4 heads / 1 x 64,   B = 1, L = 32,768:   n = 64 25.5 / 44.9
-//                       B = 16, L = 4096:    n = 12 17.9 / 19.6, n = 24 27.7 / 20.9
-bool few(const moe_kv8_shape& s) { return (long long)s.T * s.Hq <= 24ll * s.B * s.Hkv + 192; }
+//   16 heads / 2 x 256, B = 1, L = 32,768:   n = 12 48.5 / 55.9, n = 16 60.8 / 57.3
+//                       B = 1, L = 2048:     n = 64 28.4 / 32.8
+//                       B = 16, L = 4096:    n = 4 41.9 / 47.6, n = 8 73.0 / 48.0
+//                       B = 16, L = 512:     n = 4 18.5 / 23.2, n = 8 27.6 / 23.7
+//   16 heads / 4 x 128, B = 1, L = 32,768:   n = 24 38.2 / 43.3, n = 32 47.0 / 44.3
+//                       B = 16, L = 4096:    n = 12 57.4 / 59.2, n = 24 84.6 / 61.3
+//                       B = 16, L = 512:     n = 8 18.4 / 21.9, n = 12 24.2 / 22.1
+//   8 heads / 8 x 128,  B = 1, L = 32,768:   n = 64 48.7 / 60.5
+//                       B = 16, L = 512:     n = 32 26.5 / 28.6, n = 64 43.0 / 28.8
+//   4 heads / 1 x 64,   B = 16, L = 4096:    n = 12 16.5 / 19.1, n = 24 24.5 / 20.3
+//   40 heads / 8 x 128, B = 16, L = 4096:    n = 4 57.2 / 107, n = 8 102 / 100
+bool few(const moe_kv8_shape& s) { return (long long)s.T * s.Hq <= 36ll * s.B * s.Hkv + 192; }
 
 size_t workspace_bytes(const moe_kv8_shape& s) {
   return s.T == 0 ? 256 : few(s) ? split_workspace_bytes(s) : tiles_workspace_bytes(s);

@@ -14,9 +14,10 @@
 //                            measured copy rate; 7.5 us of it do not grow)
 //   one token after 32,768 positions, INT8     14.6 us, 2.3 TB/s
 //   a ragged batch of 8, 148,369 positions     33.5 us, 4.5 TB/s
-//   1 to 5 drafts of 16 sequences, 70,120 positions, 4 x 128, E4M3   33.6 us,
-//                            2.1 TB/s: 12 rows a tile, bound by the consumers,
-//                            two warps a scheduler at 0.37 instructions a cycle
+//   1 to 5 drafts of 16 sequences, 70,120 positions, 4 x 128, E4M3   30.6 us,
+//                            2.4 TB/s: 0.87 us a unit of 32 KB (0.74 at the copy
+//                            rate), a fifth more of them than positions (second
+//                            tiles, ragged ends), 3.3 us a tile begun and ended
 // What does not grow (one token after 300 positions, from the wait for the
 // predecessors): 1.6 us the tables and the run's start, 0.8 Q, 1.1 the first
 // codes and their unit, 1.3 the fold, 0.9 to the merge's start, 1.5 the merge.
