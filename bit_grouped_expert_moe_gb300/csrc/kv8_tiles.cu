@@ -1117,7 +1117,9 @@ struct MergeParams {
   int Hq, Hkv, D, C, ctas;  // C: runs
 };
 
-constexpr int kMergeRows = 8;       // rows of a block, a warp each
+// Rows of a block, a warp each. 4, 8, 16, 32: a prompt of 4096 takes 133.1,
+// 132.8, 133.0, 140.9 us, 16 sequences' 8 queries 48.2, 47.4, 48.4, 48.2.
+constexpr int kMergeRows = 8;
 constexpr int kMergeThreads = 32 * kMergeRows;
 
 // Block (c, y): if run c is the second of the runs that share a tile, the
