@@ -144,7 +144,7 @@ __device__ inline bool find_run(const int32_t* offsets, const int32_t* lens, int
     long long v1 = 0, w1 = 0;  // this lane's sequence, per KV head: places, units
     int nt1 = 0, lo = 0, hi = 0, len = 0;
     if (b < B) {
-      lo = __ldg(offsets + b), hi = __ldg(offsets + b + 1), len = __ldg(lens + b);
+      lo = ld(offsets + b), hi = ld(offsets + b + 1), len = ld(lens + b);
       if (offsets_bad(lo, hi, b, B, T) || len < 0 || len > L_max) {
         bad = true;
       } else {

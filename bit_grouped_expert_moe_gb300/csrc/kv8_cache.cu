@@ -53,7 +53,7 @@ template <typename Hit>
 __device__ __forceinline__ bool tables_bad(const CacheArgs& p, Hit hit) {
   bool bad = false;
   for (int b = threadIdx.x; b < p.B; b += kThreads) {
-    const int lo = __ldg(p.offsets + b), hi = __ldg(p.offsets + b + 1), start = __ldg(p.starts + b);
+    const int lo = ld(p.offsets + b), hi = ld(p.offsets + b + 1), start = ld(p.starts + b);
     if (offsets_bad(lo, hi, b, p.B, p.T) || range_bad(start, hi - lo, p.L_max)) bad = true;
     else hit(b, lo, hi, start);
   }
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_write_kernel(const CacheArgs 
     const int piece = tu + i * kTU;                    // piece of the new rows, from row r0
     const int row = piece / (D / 8), c = piece % (D / 8);
     v[i] = make_uint4(0, 0, 0, 0);
-    if (row < r1 - r0) v[i] = ldg_nc_v4(x + (size_t)row * p.stride + c * 8);
+    if (row < r1 - r0) v[i] = ld_once_v4(x + (size_t)row * p.stride + c * 8);
   }
   const float s_old = p0 > base ? *scale : 0.f;
 #pragma unroll
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_write_kernel(const CacheArgs 
   };
   uint32_t m = unit_max(mx, 0);
   const bool odd = m >= 0x7F80u;  // an infinity or a NaN: the maximum again over finite values, and they are replaced
-  auto reload = [&](int piece) { return ldg_nc_v4(x + (size_t)(piece / (D / 8)) * p.stride + piece % (D / 8) * 8); };
+  auto reload = [&](int piece) { return ld_once_v4(x + (size_t)(piece / (D / 8)) * p.stride + piece % (D / 8) * 8); };
   const int pieces = (r1 - r0) * (D / 8);
   if (odd) {
     if (tu == 0) flag(p.status, (int32_t)MOE_ERR_RANGE);
@@ -243,10 +243,10 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const CacheArgs p) {
     int b = 0, z = p.B;                                 // the last sequence that starts at or before t
     while (z - b > 1) {
       const int mid = (b + z) >> 1;
-      if (__ldg(p.offsets + mid) <= t) b = mid;
+      if (ld(p.offsets + mid) <= t) b = mid;
       else z = mid;
     }
-    const int pos = __ldg(p.starts + b) + t - __ldg(p.offsets + b);
+    const int pos = ld(p.starts + b) + t - ld(p.offsets + b);
     const long long pair = (long long)b * p.Hkv + g;
     s_code[buf][threadIdx.x] = (pair * p.L_max + pos) * D;
     s_scale[buf][threadIdx.x] = pair * p.nblk + pos / kBlock;
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const CacheArgs p) {
       s[i] = 0.f;
       if (t < nt) {
         w[i] = __ldcs(reinterpret_cast<const uint2*>(codes + s_code[buf][t] + c * 8));
-        s[i] = __ldg(scales + s_scale[buf][t]);
+        s[i] = ld(scales + s_scale[buf][t]);
       }
     }
   };

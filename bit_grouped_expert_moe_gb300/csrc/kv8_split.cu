@@ -244,9 +244,9 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
 struct Cursor {
   int b, g, rt, i, nb, n, len, lo, tile;
   __device__ void sequence(const Params& p) {  // tables of sequence b (b < B)
-    lo = __ldg(p.offsets + b);
-    n = __ldg(p.offsets + b + 1) - lo;
-    len = __ldg(p.lens + b);
+    lo = ld(p.offsets + b);
+    n = ld(p.offsets + b + 1) - lo;
+    len = ld(p.lens + b);
   }
   // The next unit; the caller knows that there is one.
   __device__ void advance(const Params& p, int r, int RT, int kPos) {
@@ -431,13 +431,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint16_t* src = p.q + (size_t)(k.lo + (live ? tok : 0)) * p.q_stride +
                               (size_t)(k.g * r + (live ? rr - tok * r : 0)) * D + kPer * lane;
         if constexpr (kPer == 8)
-          asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
+          asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(raw[i][0]), "=r"(raw[i][1]), "=r"(raw[i][2]), "=r"(raw[i][3])
-                       : "l"(src));
+                       : "l"(src)
+                       : "memory");
         else if constexpr (kPer == 4)
-          asm volatile("ld.global.nc.v2.b32 {%0, %1}, [%2];" : "=r"(raw[i][0]), "=r"(raw[i][1]) : "l"(src));
+          asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(raw[i][0]), "=r"(raw[i][1]) : "l"(src) : "memory");
         else
-          asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(raw[i][0]) : "l"(src));
+          asm volatile("ld.global.b32 %0, [%1];" : "=r"(raw[i][0]) : "l"(src) : "memory");
       }
     };
     const uint32_t sQ = smem_u32(smem + S::kQOffset);
@@ -508,8 +509,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = 0; t < kMT; ++t) {
         const int pos = min(k.i * kPos + 16 * (kMT * pw + t), k.len - 1);
         const size_t at = (size_t)(k.b * p.Hkv + k.g) * p.nblk + (pos >> p.shift);
-        asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(sk[t]) : "l"(p.ks + at));
-        asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(sv[t]) : "l"(p.vs + at));
+        sk[t] = ld(p.ks + at);
+        sv[t] = ld(p.vs + at);
       }
     };
     float skn[kMT], svn[kMT];  // of the next unit that is this warp's
@@ -798,7 +799,9 @@ __global__ void __launch_bounds__(kLanes * 16) kv8_merge_kernel(const MergeParam
   // finish before it touches the workspace.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // Everything up to the dependency wait reads only the tables, which the
-  // split kernel does not write: it overlaps that kernel's tail.
+  // split kernel does not write: it overlaps that kernel's tail. Whatever wrote
+  // them ended before the split kernel let this one launch, so L2 has them; L1,
+  // which nobody invalidates before the wait, is not asked.
   const int r = p.Hq / p.Hkv, RT = p.RT, C = p.C, D = p.D;
   const int t = blockIdx.x / p.Hq, h = blockIdx.x - t * p.Hq;
   const int lane = threadIdx.x & 31, f4 = threadIdx.x & 15, sl = threadIdx.x >> 4;
@@ -812,9 +815,9 @@ __global__ void __launch_bounds__(kLanes * 16) kv8_merge_kernel(const MergeParam
     const int bb = base + lane;
     int lo1 = 0, hi1 = 0, len1 = 0;
     if (bb < p.B) {
-      lo1 = __ldg(p.offsets + bb);
-      hi1 = __ldg(p.offsets + bb + 1);
-      len1 = __ldg(p.lens + bb);
+      lo1 = __ldcg(p.offsets + bb);
+      hi1 = __ldcg(p.offsets + bb + 1);
+      len1 = __ldcg(p.lens + bb);
       bad |= offsets_bad(lo1, hi1, bb, p.B, p.T) || len1 < 0 || len1 > p.L_max;
     }
     const unsigned hit = __ballot_sync(0xffffffffu, lo1 <= t && t < hi1);

@@ -201,9 +201,9 @@ constexpr size_t slot_floats(int D) { return (size_t)kRows * tile_blocks(D) * (D
 struct Cursor {
   int b, g, rt, i, nb, n, len, lo;
   __device__ void sequence(const Params& p) {
-    lo = __ldg(p.offsets + b);
-    n = __ldg(p.offsets + b + 1) - lo;
-    len = __ldg(p.lens + b);
+    lo = ld(p.offsets + b);
+    n = ld(p.offsets + b + 1) - lo;
+    len = ld(p.lens + b);
   }
   __device__ bool last() const { return i == nb - 1; }
   __device__ void advance(const Params& p, int r, int RT) {
@@ -475,9 +475,10 @@ __device__ __forceinline__ void load16(uint32_t to, const uint8_t* from, bool on
 template <int kOffset>
 __device__ __forceinline__ void ldg128_if(uint4& v, const uint8_t* p, bool on) {
   asm volatile(
-      "{\n .reg .pred q;\n setp.ne.b32 q, %5, 0;\n @q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4 + %6];\n}\n"
+      "{\n .reg .pred q;\n setp.ne.b32 q, %5, 0;\n @q ld.global.v4.u32 {%0, %1, %2, %3}, [%4 + %6];\n}\n"
       : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
-      : "l"(p), "r"((int)on), "n"(kOffset));
+      : "l"(p), "r"((int)on), "n"(kOffset)
+      : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -586,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
   if (s_bad) return;
   // Queries that see nothing (more queries than positions): o = 0.
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    const int lo = __ldg(p.offsets + b), hi = __ldg(p.offsets + b + 1), len = __ldg(p.lens + b);
+    const int lo = ld(p.offsets + b), hi = ld(p.offsets + b + 1), len = ld(p.lens + b);
     const size_t pieces = (size_t)max(0, hi - lo - len) * p.Hq * (D / 8);
     uint4* z = reinterpret_cast<uint4*>(p.o + (size_t)lo * p.Hq * D);
     for (size_t i = threadIdx.x; i < pieces; i += kThreads) z[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -724,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
         const int s = u % kNotes;
         const int pos = min(k.i * kKeys + 16 * (lane & 7), k.len - 1);
         const size_t at = (size_t)(k.b * p.Hkv + k.g) * p.nblk + (pos >> p.shift);
-        const float sk = __ldg(p.ks + at), v = __ldg(p.vs + at), sv = v > 0.f ? v : kScaleFloor;
+        const float sk = ld(p.ks + at), v = ld(p.vs + at), sv = v > 0.f ? v : kScaleFloor;
         if (u >= kNotes && !warp_wait(&ctl->note_empty[s], (u / kNotes - 1) & 1)) break;
         if (lane < 8) ctl->note[s].scale[lane] = make_float4(sk, __log2f(sv), __fdividef(1.f, sv), 0.f);
         if (lane == 8) ctl->note[s].tile = make_int4(k.lo, k.n, k.len, k.g);
@@ -1163,7 +1164,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_tiles_merge_kernel(const Me
   const RunInfo f0 = p.info[c0];
   if (f0.tile == f.tile && f0.i > 0) return;  // a later one of the tile's runs
   const int r = p.Hq / p.Hkv, D = p.D, row = blockIdx.y * kMergeRows + (t >> 5);
-  const int lo = __ldg(p.offsets + f.b), n = __ldg(p.offsets + f.b + 1) - lo, len = __ldg(p.lens + f.b);
+  const int lo = ld(p.offsets + f.b), n = ld(p.offsets + f.b + 1) - lo, len = ld(p.lens + f.b);
   const int rows = kRows * p.ctas, rho = f.rt * rows + row, tok = rho / r;
   if (rho >= n * r || len - n + tok < 0) return;
   auto slot = [&](int cc) { return p.part + (size_t)(2 * cc + (cc == c0 ? 1 : 0)) * slot_floats(D); };
