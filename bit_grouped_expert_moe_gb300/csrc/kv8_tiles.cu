@@ -1015,7 +1015,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
       if (tile > 1 && !warp_wait(&ctl->rc_empty[tile & 1], ((tile >> 1) - 1) & 1)) return false;
       tc_fence_after();
       RowConst& rc = ctl->rc[tile & 1];
-#pragma unroll
+#pragma unroll 2  // with all at once, a value of the stages' loop is spilled (the chunk above 412 us for 399)
       for (int base = 0; base < kQRows; base += kBatch) {
         if (base > 0) load_rows(k, base, v);
 #pragma unroll
