@@ -34,6 +34,19 @@ moe_status launch_split(const AttnArgs& a, cudaStream_t stream);
 size_t tiles_workspace_bytes(const moe_kv8_shape& s);
 moe_status launch_tiles(const AttnArgs& a, cudaStream_t stream);
 
+// V scales far apart. With x = score + log2 s_v, a row's sum L = sum w / s_v comes
+// from weights w = 2^(x - m + 7), which are zero below 2^-126. Let S be the
+// largest V scale that the tile's units have shown so far: L is 2^7 / S at least,
+// and a position whose weight was lost had less than 2^-126 / s_v in it. Where
+// s_v >= kFar S that is less than 2^-45 of L, and there is no more to do. Positions
+// below (blocks of zeros have the smallest scale) are summed without the detour,
+// as 2^(x - m + 7 - log2 s_v), and kLift times that, so that what is lost of them
+// is less than 2^-158 against 2^7 / 2^121, 2^-44 of L. (x <= m + 8 and s_v >= 2^-60
+// keep it below 2^108.) For the same reason L goes from one m to another in two
+// steps, by the square root of the factor: the factor itself may be below 2^-126.
+constexpr float kFar = 3.2311742677852644e-27f;       // 2^-88
+constexpr float kLiftBits = 32.f, kUnlift = 2.3283064365386963e-10f;  // 2^-32
+
 int sm_count();  // of the current device, or 0 (kv8_attn.cu)
 
 // How the work is laid out, by both kinds: the rows of a (sequence, KV head)

@@ -49,8 +49,9 @@
 //   x_j = score_j + log2 s_v(j),  w_j = 2^(x_j - m + 7),  m >= max x - 8,
 // O = sum w_j code_j and L = sum w_j / s_v(j) give o = O / L. w <= 2^15 fits
 // fp16, whose subnormals reach 2^-31 below a weight at m; L sums the
-// fp32 weights, so it also keeps blocks whose values are all zero (s_v taken
-// as the smallest scale there). q goes to fp16 with its row's largest
+// fp32 weights, or what they stand for where those would vanish (kFar), so it
+// also keeps blocks whose values are all zero (s_v taken as the smallest scale
+// there). q goes to fp16 with its row's largest
 // magnitude in [1, 2), an exact step apart from values 2^-14 and more below it.
 //
 // kv8_merge_kernel — one block per (query token, query head, 64 head dims)
@@ -410,6 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float m[kNTw][2], l[kNTw][2];    // of rows 8 nt + 2 m4, + 1
     float rq[kNTw][2], off[kNTw][2]; // score factor of the row's power of two; -128 sum(q) 2^-24 (int8)
     int lim[kNTw][2];                // visible positions
+    float top_sv = 0.f;              // the largest V scale of the tile's units so far
     int folds = 0;
     // All consumer warps have come this far.
     auto together = [&]() -> bool {
@@ -479,6 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!together()) return false;
+      top_sv = 0.f;
 #pragma unroll
       for (int nt = 0; nt < kNTw; ++nt) {
         const uint32_t at = sQ + (rows0 + 8 * nt + gq) * S::kQPitch + 8 * m4;
@@ -585,12 +588,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         // scores, with V's scale; does one pass its row's m by more than the slack?
         float rsv[kMT];
-        bool up = false;
+        bool up = false, far = false;
+#pragma unroll
+        for (int t = 0; t < kMT; ++t) top_sv = fmaxf(top_sv, sv[t]);
 #pragma unroll
         for (int t = 0; t < kMT; ++t) {
           const float svx = sv[t] > 0.f ? sv[t] : kScaleFloor;
           const float lsv = __log2f(svx);
           rsv[t] = __fdividef(1.f, svx);
+          far |= svx < kFar * top_sv;
           const int pr = pos0 + 16 * t + gq;
 #pragma unroll
           for (int nt = 0; nt < kNTw; ++nt)
@@ -614,9 +620,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int t = 0; t < kMT; ++t) mx = fmaxf(mx, fmaxf(x[t][nt][k], x[t][nt][k + 2]));
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-              al[k] = ex2(m[nt][k] - mx);
+              const float root = ex2(0.5f * (m[nt][k] - mx));
+              al[k] = root * root;
               m[nt][k] = mx;
-              l[nt][k] *= al[k];
+              l[nt][k] = l[nt][k] * root * root;
             }
 #pragma unroll
             for (int mt = 0; mt < D / 16; ++mt) {
@@ -624,6 +631,23 @@ __global__ void __launch_bounds__(kThreads, 1)
               acc[nt][mt][1] *= al[1];
               acc[nt][mt][2] *= al[0];
               acc[nt][mt][3] *= al[1];
+            }
+          }
+        }
+        if (far) {  // the whole warp alike
+#pragma unroll
+          for (int t = 0; t < kMT; ++t) {
+            const float svx = sv[t] > 0.f ? sv[t] : kScaleFloor;
+            if (svx < kFar * top_sv) {
+              const float lift = kLiftBits - __log2f(svx);
+#pragma unroll
+              for (int nt = 0; nt < kNTw; ++nt)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const float mk = m[nt][k] - kWeightBits;
+                  l[nt][k] = fmaf(ex2(x[t][nt][k] - mk + lift) + ex2(x[t][nt][k + 2] - mk + lift), kUnlift, l[nt][k]);
+                }
+              rsv[t] = 0.f;
             }
           }
         }
@@ -698,9 +722,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             float top = m[nt][k];
 #pragma unroll
             for (int w = 0; w < S::kFold; ++w) top = fmaxf(top, ctl->m[set0 + w][8 * nt + 2 * m4 + k]);
-            f[k] = ex2(m[nt][k] - top);
+            const float root = ex2(0.5f * (m[nt][k] - top));
+            f[k] = root * root;
             m[nt][k] = top;
-            if (lane < 4) ctl->l[warp][8 * nt + 2 * lane + k] = l[nt][k] * f[k];
+            if (lane < 4) ctl->l[warp][8 * nt + 2 * lane + k] = l[nt][k] * root * root;
           }
 #pragma unroll
           for (int mt = 0; mt < D / 16; ++mt) {
@@ -896,14 +921,14 @@ __global__ void __launch_bounds__(kLanes * 16) kv8_merge_kernel(const MergeParam
     float nm = M;
 #pragma unroll
     for (int u = 0; u < kMergeBatch; ++u) nm = fmaxf(nm, mc[u]);
-    const float f = ex2(M - nm);
-    L *= f;
+    const float fr = ex2(0.5f * (M - nm)), f = fr * fr;  // (L in two steps, as in the split kernel)
+    L = L * fr * fr;
     O = make_float4(O.x * f, O.y * f, O.z * f, O.w * f);
     M = nm;
 #pragma unroll
     for (int u = 0; u < kMergeBatch; ++u) {
-      const float e = ex2(mc[u] - M);
-      L = fmaf(lc[u], e, L);
+      const float er = ex2(0.5f * (mc[u] - M)), e = er * er;
+      L = fmaf(lc[u] * er, er, L);
       O = make_float4(fmaf(oc[u].x, e, O.x), fmaf(oc[u].y, e, O.y), fmaf(oc[u].z, e, O.z), fmaf(oc[u].w, e, O.w));
     }
   }
@@ -919,8 +944,8 @@ __global__ void __launch_bounds__(kLanes * 16) kv8_merge_kernel(const MergeParam
     for (int w = 0; w < kLanes; ++w) Mt = fmaxf(Mt, s_m[w]);
 #pragma unroll
     for (int w = 0; w < kLanes; ++w) {
-      const float e = ex2(s_m[w] - Mt);
-      Lt = fmaf(e, s_l[w], Lt);
+      const float er = ex2(0.5f * (s_m[w] - Mt)), e = er * er;
+      Lt = fmaf(s_l[w] * er, er, Lt);
       Ot = fmaf(e, s_o[w][threadIdx.x], Ot);
     }
     // c1 < c0: no visible position

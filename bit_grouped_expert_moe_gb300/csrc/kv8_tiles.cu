@@ -54,9 +54,9 @@
 // Codes are exact in fp16: 1024 + u (u = code + 128, by a byte permute) minus
 // 1152 for int8, the conversion instruction for e4m3. Scales as in
 // kv8_split.cu: with x = score + log2 s_v the weights carry V's scale and
-// L = sum w / s_v. The running maximum m of a row is raised only when a score
-// passes it by more than 8 (on the base-2 scale), so that O in TMEM is
-// rarely rescaled: w <= 2^15.
+// L = sum w / s_v (kFar: where a weight would vanish, what it stands for). The
+// running maximum m of a row is raised only when a score passes it by more than
+// 8 (on the base-2 scale), so that O in TMEM is rarely rescaled: w <= 2^15.
 #include <cuda.h>
 
 #include <type_traits>
@@ -134,9 +134,9 @@ struct RowConst {  // of a tile's rows, written with its Q
 
 // What the softmax has to know of a unit, put down by a warp of its own.
 struct UnitNote {
-  float4 scale[8];  // of every 16 positions: s_k, log2 s_v, 1 / s_v
+  float4 scale[8];  // of every 16 positions: s_k, log2 s_v, 1 / s_v (0 where s_v is far below others: kFar)
   int4 tile;        // lo, n, len, g of its sequence and head
-  int4 place;       // first position, row tile, is the tile's last, -
+  int4 place;       // first position, row tile, is the tile's last, not 0: some 1 / s_v are
 };
 constexpr int kNotes = 4;
 
@@ -720,18 +720,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
     } else if (warp == kNoteWarp) {
       // ----------------------------------------------------- unit notes
       Cursor k = cur;
+      uint32_t top = 0u;  // the tile's largest V scale so far (positive floats compare as their bits)
 #pragma unroll 1
       for (int u = 0; u < U; ++u) {
         const int s = u % kNotes;
         const int pos = min(k.i * kKeys + 16 * (lane & 7), k.len - 1);
         const size_t at = (size_t)(k.b * p.Hkv + k.g) * p.nblk + (pos >> p.shift);
         const float sk = ld(p.ks + at), v = ld(p.vs + at), sv = v > 0.f ? v : kScaleFloor;
+        top = max(top, __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(v, 0.f))));
+        const int far = __ballot_sync(0xffffffffu, sv < kFar * __uint_as_float(top)) & 0xFF;
         if (u >= kNotes && !warp_wait(&ctl->note_empty[s], (u / kNotes - 1) & 1)) break;
-        if (lane < 8) ctl->note[s].scale[lane] = make_float4(sk, __log2f(sv), __fdividef(1.f, sv), 0.f);
+        const float rsv = far >> lane & 1 ? 0.f : __fdividef(1.f, sv);
+        if (lane < 8) ctl->note[s].scale[lane] = make_float4(sk, __log2f(sv), rsv, 0.f);
         if (lane == 8) ctl->note[s].tile = make_int4(k.lo, k.n, k.len, k.g);
-        if (lane == 9) ctl->note[s].place = make_int4(k.i * kKeys, k.rt, k.last(), 0);
+        if (lane == 9) ctl->note[s].place = make_int4(k.i * kKeys, k.rt, k.last(), far);
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->note_full[s]);
+        if (k.last()) top = 0u;
         if (u + 1 < U) k.advance(p, r, F::kTileRows);
       }
     }
@@ -809,9 +814,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
         m = fmaxf(mx, kMinusBig);
       } else if (__any_sync(0xffffffffu, mx > m + kSlack)) {
         // O and L to the new maximum, once the products of the last unit are in
-        const float nm = mx > m + kSlack ? mx : m, f = ex2(m - nm);
+        const float nm = mx > m + kSlack ? mx : m, root = ex2(0.5f * (m - nm)), f = root * root;
         m = nm;
-        l *= f;
+        l = l * root * root;
         if (!warp_wait(&ctl->pv_done[(u - 1) & 1], ((u - 1) >> 1) & 1)) break;
         tc_fence_after();
 #pragma unroll 1
@@ -825,6 +830,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
       }
       // weights, over S (both halves have read it)
       const float top = kWeightBits - m;
+      if (place.w) {  // the whole warp alike
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          if (sc[h].z == 0.f) {
+            const float lift = kLiftBits - sc[h].y;
+            float s = 0.f;
+#pragma unroll
+            for (int e = 16 * h; e < 16 * h + 16; ++e)
+              s += ex2(fmaf(__uint_as_float(x[e]), a[h], sc[h].y) + top + lift);
+            l = fmaf(s, kUnlift, l);
+          }
+      }
       uint32_t w[32];
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
@@ -1184,8 +1201,9 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_tiles_merge_kernel(const Me
   const int per = D / 32;
   for (int base = c0; base <= c1; base += 32) {
     const int mine = base + lane;
-    const float e = mine <= c1 ? exp2f(__ldcg(slot(mine) + (size_t)D * rows + row) - M) : 0.f;
-    float l = mine <= c1 ? e * __ldcg(slot(mine) + (size_t)(D + 1) * rows + row) : 0.f;
+    const float root = mine <= c1 ? exp2f(0.5f * (__ldcg(slot(mine) + (size_t)D * rows + row) - M)) : 0.f;
+    const float e = root * root;
+    float l = mine <= c1 ? __ldcg(slot(mine) + (size_t)(D + 1) * rows + row) * root * root : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     L += l;

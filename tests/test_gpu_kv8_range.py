@@ -1,0 +1,148 @@
+"""The 8-bit KV cache over the range of values that its header allows, on the GPU
+against the fp64 oracle: blocks whose V scales lie far apart, scores far from
+zero, magnitudes up to bf16's largest.
+
+Tolerance of attention per element, from the arithmetic (u = 2^-24, codes c,
+softmax weights p, V scales s, sums over the row's visible positions):
+  * o is rounded to bf16: 2^-8 of the value before;
+  * a weight goes to fp16: 2^-11 of it, and as much again for the sums and the
+    exponentials below; or 2^-25 where that is more, with the row's largest
+    p_j s(j) at 2^7 at least: 2^-32 max_j(p_j s(j)) sum_j |c_j|;
+  * q goes to fp16 with its row's largest magnitude in [1, 2): nothing is lost
+    above 2^-14, and below at most 2^-25: of a score,
+    scale * 2 max|q| * 2^-25 * sum_d |K_d|;
+  * a score: D + 8 operations, each off by at most 2 u of
+    amp = scale * sum_d |q_d| * (255 code steps of int8, or 448) * K scale;
+    on the base-2 scale, with log2 s added and m taken off, three roundings of
+    at most u (|score| + 128) each, twice (a weight, and their sum);
+  * a row's scores off by ds change its weights by a factor within e^(2 ds);
+  * sums of at most L / 16 + 64 terms in fp32, each addition off by 2 u of at
+    most the sum of magnitudes.
+Every figure is the row's own: a block that other sequences hold has no part."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv8
+from oracle.moe import bf16_bits_to_f64
+from tests._util import bits16
+from tests.test_gpu_kv8 import FMTS, Pair, _packed, _rand
+
+pytestmark = pytest.mark.gpu
+
+
+def _bf16(x):
+    return torch.as_tensor(x).to(torch.bfloat16)
+
+
+def _tolerance(p, q, news, lens):
+    """o of the formula and what the kernels may be off by, fp64 [T, Hq, D]."""
+    off = _packed(news)
+    T, Hq, D = q.shape
+    r = Hq // p.dims[1]
+    x = bf16_bits_to_f64(bits16(q))
+    scale, u = D ** -0.5, 2.0 ** -24
+    o, tol = np.zeros((T, Hq, D)), np.zeros((T, Hq, D))
+    for b, (n, ln) in enumerate(zip(news, lens)):
+        at = np.arange(ln) // p.block
+        for g in range(p.dims[1]):
+            sk, sv = (p.scales[i][b, g][at].astype(np.float64) for i in range(2))
+            K = kv8.value_of(p.codes[0][b, g, :ln], sk[:, None], p.fmt)
+            c = kv8.value_of(p.codes[1][b, g, :ln], 1.0, p.fmt)
+            step = 255.0 if p.fmt == "int8" else 448.0
+            for i in range(n):
+                see = ln - n + i + 1
+                if see <= 0:
+                    continue
+                for h in range(g * r, (g + 1) * r):
+                    y = x[off[b] + i, h]
+                    z = scale * (K[:see] @ y)
+                    w = np.exp(z - z.max())
+                    w /= w.sum()
+                    amp = scale * np.abs(y).sum() * step * sk[:see].max()
+                    ds = (D + 8) * 2 * u * amp
+                    ds += scale * 2 * np.abs(y).max() * 2.0 ** -25 * np.abs(K[:see]).sum(1).max()
+                    ds += 6 * u * (np.abs(z).max() * np.log2(np.e) + 128) * np.log(2)
+                    assert ds < 0.05
+                    weighed = (w * sv[:see])
+                    absolute = weighed @ np.abs(c[:see])
+                    e = (2.1 * 2.0 ** -11 + 2.1 * ds + (see / 16 + 64) * 2 * u) * absolute
+                    e += 2.0 ** -32 * weighed.max() * np.abs(c[:see]).sum(0)
+                    o[off[b] + i, h] = weighed @ c[:see]
+                    tol[off[b] + i, h] = e + 2.0 ** -8 * (np.abs(o[off[b] + i, h]) + e)
+    return o, tol
+
+
+def _check(p, q, news, lens):
+    got = p.attend(q, news, lens).double().cpu().numpy()
+    want, tol = _tolerance(p, q, news, lens)
+    assert np.isfinite(got).all()
+    err = np.abs(got - want)
+    assert (err <= tol).all(), (float((err / np.maximum(tol, 1e-300)).max()), np.argwhere(err > tol)[:4],
+                                got[err > tol][:4], want[err > tol][:4])
+
+
+# the few-query kernels with 8, 16 and (at 128 head dims) 32 rows a tile, and the tiles
+FORMS = [(64, 2, 1), (64, 4, 70), (128, 2, 1), (128, 8, 3), (128, 16, 3), (128, 4, 70), (256, 2, 1), (256, 8, 2),
+         (256, 4, 70)]
+
+
+def _blocks(gen, exponents, rows, D, Hkv=1):
+    """Values whose block i is about 2^exponents[i] in size (None: zeros)."""
+    out = []
+    for e in exponents:
+        v = _rand(gen, rows, Hkv, D).clamp(-3, 3)
+        out.append(v * 0 if e is None else v * 2.0 ** e)
+    return torch.cat(out)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("exponents", [
+    [None, 100, None], [118, None, None, 118, None], [None, 74, 0], [60, None, -58, None, 60], [-50, 118, -50, 118],
+    [118, -58, None, -58], [-58, -58, None, None, -58], [80, -40, 80, 0, None], [118, 118, 118]])
+@pytest.mark.parametrize("D,r,news", FORMS)
+def test_v_blocks_far_apart(moelib, cuda_dev, D, r, news, exponents, fmt):
+    """Every position counts in a row's sum of weights, however small its V
+    scale is beside another's, zeros among them."""
+    block = 64 if D == 256 else 16
+    L = block * len(exponents)
+    p = Pair(moelib, 1, 1, D, L, block, fmt)
+    gen = torch.Generator().manual_seed(7)
+    v = _blocks(gen, exponents, block, D)
+    p.write([_bf16(_rand(gen, L, 1, D)), _bf16(v)], [L], [0])
+    p.check()
+    for size in (0.0, 1.0):  # equal weights, then others
+        _check(p, _bf16(_rand(gen, news, r, D) * size), [news], [L])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,r,news", FORMS)
+def test_v_blocks_far_apart_across_runs(moelib, cuda_dev, D, r, news, fmt):
+    """The same where many blocks of the grid share a sequence and their states
+    are merged, and where a warp sees many units."""
+    block, count = 64, 90
+    L = block * count
+    p = Pair(moelib, 1, 1, D, L, block, fmt)
+    gen = torch.Generator().manual_seed(8)
+    exponents = [[None, 110, -55, 3][int(i)] for i in torch.randint(0, 4, (count,), generator=gen)]
+    v = _blocks(gen, exponents, block, D)
+    p.write([_bf16(_rand(gen, L, 1, D)), _bf16(v)], [L], [0])
+    _check(p, _bf16(_rand(gen, news, r, D)), [news], [L])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,r,news", FORMS)
+def test_a_peaked_row_whose_top_value_is_zero(moelib, cuda_dev, D, r, news, fmt):
+    """One position has nearly all the weight and zeros in some head dims: what
+    the others add there is within the bound's term for weights that fp16 holds
+    as subnormals or not at all."""
+    L = 300
+    p = Pair(moelib, 1, 1, D, L, 32, fmt)
+    gen = torch.Generator().manual_seed(9)
+    k, v, q = _rand(gen, L, 1, D) * 0.05, _rand(gen, L, 1, D), _rand(gen, news, r, D) * 0.05
+    k[10, :, :8] = 4.0
+    v[10, :, ::3] = 0
+    for peak in (4.0, 8.0, 16.0, 24.0):  # of the score
+        q[:, :, :8] = peak * D ** 0.5 / 32
+        p.write([_bf16(k), _bf16(v)], [L], [0])
+        _check(p, _bf16(q), [news], [L])
