@@ -100,6 +100,8 @@ constexpr int kTileCost = 4;
 constexpr float kMinusBig = -1e30f; // running-max start: finite, so 2^(m - m_new) is never NaN
 // A row's m is raised to its largest score only when a score passes it by
 // more than kSlack: weights are 2^kWeightBits at m and fit fp16 up to there.
+// From 2^23 on, where an fp32 step is 1 and more and m + 8 or m - 7 may be
+// rounded away from each other, whenever a score passes it.
 constexpr float kWeightBits = 7.f, kSlack = 8.f;
 
 template <int D, int kNT>
@@ -587,8 +589,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         // scores, with V's scale; does one pass its row's m by more than the slack?
-        float rsv[kMT];
+        float rsv[kMT], bar[kNTw][2];
         bool up = false, far = false;
+#pragma unroll
+        for (int nt = 0; nt < kNTw; ++nt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) bar[nt][k] = fabsf(m[nt][k]) < 8388608.f ? m[nt][k] + kSlack : m[nt][k];
 #pragma unroll
         for (int t = 0; t < kMT; ++t) top_sv = fmaxf(top_sv, sv[t]);
 #pragma unroll
@@ -606,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (kHalve) d += y[e];
               if (!kE4m3) d *= 16777216.f;
               x[t][nt][e] = pr + (e >> 1) * 8 < lim[nt][e & 1] ? fmaf(d, rq[nt][e & 1] * sk[t], lsv) : -INFINITY;
-              up |= x[t][nt][e] > m[nt][e & 1] + kSlack;
+              up |= x[t][nt][e] > bar[nt][e & 1];
             }
         }
         if (__any_sync(0xffffffffu, up)) {

@@ -98,6 +98,11 @@ constexpr int kTileCost = 3;
 constexpr float kMinusBig = -1e30f;
 constexpr float kWeightBits = 7.f;  // weights are 2^7 at the row's m ...
 constexpr float kSlack = 8.f;       // ... which scores may pass by this much
+// x - m is computed in one step from the product, a x + (log2 s_v - m), so m's own
+// rounding stays in it: half an fp32 step of m, which up to here is 2^-4 at most.
+// Rows past it take two, the score first, rounded as m was, and the units that
+// may hold such rows are told apart by a bound on their scores.
+constexpr float kLargeScore = 1048576.f;  // 2^20
 constexpr int kTmemCols = 512;
 constexpr uint32_t kColS = 256;     // S buffers at columns 256 and 384, O from 0
 
@@ -136,7 +141,7 @@ struct RowConst {  // of a tile's rows, written with its Q
 struct UnitNote {
   float4 scale[8];  // of every 16 positions: s_k, log2 s_v, 1 / s_v (0 where s_v is far below others: kFar)
   int4 tile;        // lo, n, len, g of its sequence and head
-  int4 place;       // first position, row tile, is the tile's last, not 0: some 1 / s_v are
+  int4 place;       // first position, row tile, is the tile's last, not 0: 1 / s_v = 0, or large scores
 };
 constexpr int kNotes = 4;
 
@@ -721,6 +726,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
       // ----------------------------------------------------- unit notes
       Cursor k = cur;
       uint32_t top = 0u;  // the tile's largest V scale so far (positive floats compare as their bits)
+      float most = 0.f;   // its scores' bound, but for the K scale: 2 is q's largest magnitude, 448 the codes'
+      int tile = 0;
+      bool begins = true;
 #pragma unroll 1
       for (int u = 0; u < U; ++u) {
         const int s = u % kNotes;
@@ -729,14 +737,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
         const float sk = ld(p.ks + at), v = ld(p.vs + at), sv = v > 0.f ? v : kScaleFloor;
         top = max(top, __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(v, 0.f))));
         const int far = __ballot_sync(0xffffffffu, sv < kFar * __uint_as_float(top)) & 0xFF;
+        if (begins) {  // the rows' exponents come with Q; the softmax reads them after this note
+          if (!warp_wait(&ctl->rc_full[tile & 1], (tile >> 1) & 1)) break;
+          const uint32_t e = reinterpret_cast<const uint32_t*>(ctl->rc[tile & 1].e)[lane];  // of four rows
+          const uint32_t e2 = __vmaxu4(e, e >> 16), e1 = __vmaxu4(e2, e2 >> 8) & 0xFF;
+          most = p.scale_log2 * (2.f * 448.f * D) * __uint_as_float(max(__reduce_max_sync(0xffffffffu, e1), 1u) << 23);
+          ++tile;
+        }
+        begins = k.last();
+        const int large = __any_sync(0xffffffffu, !(most * sk < kLargeScore)) ? 0x100 : 0;
         if (u >= kNotes && !warp_wait(&ctl->note_empty[s], (u / kNotes - 1) & 1)) break;
         const float rsv = far >> lane & 1 ? 0.f : __fdividef(1.f, sv);
         if (lane < 8) ctl->note[s].scale[lane] = make_float4(sk, __log2f(sv), rsv, 0.f);
         if (lane == 8) ctl->note[s].tile = make_int4(k.lo, k.n, k.len, k.g);
-        if (lane == 9) ctl->note[s].place = make_int4(k.i * kKeys, k.rt, k.last(), far);
+        if (lane == 9) ctl->note[s].place = make_int4(k.i * kKeys, k.rt, k.last(), far | large);
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->note_full[s]);
-        if (k.last()) top = 0u;
+        if (begins) top = 0u;
         if (u + 1 < U) k.advance(p, r, F::kTileRows);
       }
     }
@@ -841,6 +858,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
               s += ex2(fmaf(__uint_as_float(x[e]), a[h], sc[h].y) + top + lift);
             l = fmaf(s, kUnlift, l);
           }
+        // Rows of large scores: a x + b with a = 1, b = 0 from here on. (A score
+        // that m + kSlack, rounded, let pass stays within fp16.)
+        if (fabsf(m) > kLargeScore && m > kMinusBig) {
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+#pragma unroll
+            for (int e = 16 * h; e < 16 * h + 16; ++e)
+              x[e] = __float_as_uint(
+                  fminf(fmaf(__uint_as_float(x[e]), a[h], sc[h].y) + top, kWeightBits + kSlack));
+            a[h] = 1.f;
+            sc[h].y = -top;
+          }
+        }
       }
       uint32_t w[32];
 #pragma unroll

@@ -146,3 +146,92 @@ def test_a_peaked_row_whose_top_value_is_zero(moelib, cuda_dev, D, r, news, fmt)
         q[:, :, :8] = peak * D ** 0.5 / 32
         p.write([_bf16(k), _bf16(v)], [L], [0])
         _check(p, _bf16(q), [news], [L])
+
+
+# ---------------------------------------------------------------- scores ---
+
+def _top(p, q, news, ln):
+    """What a row does whose scores are more than 1000 from the top one or as near
+    to it as fp32 tells apart. A score is rounded to fp32 after log2 of its block's
+    V scale is added, so that equal scores come out up to 2^-23 of their size apart
+    and the tops share the weight in some way: o lies between their values. With
+    one V scale they stay equal. Returns the least and largest of the tops' values,
+    and the largest magnitude."""
+    T, Hq, D = q.shape
+    x = bf16_bits_to_f64(bits16(q))
+    sk, sv = (p.scales[i][0, 0][np.arange(ln) // p.block].astype(np.float64)[:, None] for i in range(2))
+    K, V = kv8.value_of(p.codes[0][0, 0, :ln], sk, p.fmt), kv8.value_of(p.codes[1][0, 0, :ln], sv, p.fmt)
+    lo, hi = np.zeros((T, Hq, D)), np.zeros((T, Hq, D))
+    for i in range(news):
+        for h in range(Hq):
+            see = ln - news + i + 1
+            z = (K[:see] @ x[i, h]) * D ** -0.5
+            top = z == z.max()
+            assert top.all() or z.max() - z[~top].max() > 1000 + 2.0 ** -20 * np.abs(z.max())
+            one = (sv[:see][top] == sv[:see][top][0]).all()
+            tops = V[:see][top].mean(0, keepdims=True) if one else V[:see][top]
+            lo[i, h], hi[i, h] = tops.min(0), tops.max(0)
+            total = np.abs(V[:see][top]).max(0)
+            lo[i, h] -= 2.0 ** -8 * np.abs(lo[i, h]) + 2.2 * 2.0 ** -11 * total
+            hi[i, h] += 2.0 ** -8 * np.abs(hi[i, h]) + 2.2 * 2.0 ** -11 * total
+    return lo, hi
+
+
+def _check_top(p, q, news, ln):
+    got = p.attend(q, [news], [ln]).double().cpu().numpy()
+    lo, hi = _top(p, q, news, ln)
+    assert np.isfinite(got).all()
+    bad = (got < lo) | (got > hi)
+    assert not bad.any(), (bad.mean(), got[bad][:4], lo[bad][:4], hi[bad][:4])
+
+
+SCORES = [(12, 11), (12, 14), (13, 16), (20, 20)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("a,b", SCORES)
+@pytest.mark.parametrize("D,r,news", FORMS)
+def test_scores_far_from_zero(moelib, cuda_dev, D, r, news, a, b, fmt):
+    """Scores of both signs up to 2^40 and more, each more than 1000 from the
+    next or equal to it. (The products are whole multiples of a power of two, so
+    equal scores are equal in fp32; every block has the same K scale.)"""
+    L, block = 200, 16
+    p = Pair(moelib, 1, 1, D, L, block, fmt)
+    gen = torch.Generator().manual_seed(10)
+    k = (1 + torch.randint(0, 8, (L, 1, 1), generator=gen) / 8.0).expand(L, 1, D).clone()
+    k[::block] = 1.875
+    p.write([_bf16(k * 2.0 ** b), _bf16(_rand(gen, L, 1, D))], [L], [0])
+    sign = torch.where(torch.arange(r) % 2 == 1, -1.0, 1.0)[None, :, None]
+    q = _bf16((sign * 2.0 ** a).expand(news, r, D).clone())
+    _check_top(p, q, news, L)
+    k[5], k[37] = 2.0, 0.5  # one largest and one smallest, which every row sees
+    p.write([_bf16(k * 2.0 ** b), _bf16(_rand(gen, L, 1, D))], [L], [0])
+    _check_top(p, q, news, L)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("size", [2.0 ** 21, 2.0 ** 24.5, 2.0 ** 25.2, 2.0 ** 26.1, 2.0 ** 28])
+@pytest.mark.parametrize("D,r,news", FORMS)
+def test_scores_that_rise_by_a_little(moelib, cuda_dev, D, r, news, size, fmt):
+    """Each block's scores lie 4 to 16 (on the base-2 scale) above the last one's,
+    next to a maximum of up to 2^28, where that is an fp32 step or less: o lies
+    between the visible values. K's scales are set by hand."""
+    block, count = 16, 80
+    L = block * count
+    p = Pair(moelib, 1, 1, D, L, block, fmt)
+    gen = torch.Generator().manual_seed(14)
+    p.write([_bf16(torch.ones(L, 1, D)), _bf16(_rand(gen, L, 1, D))], [L], [0])
+    code = 127.0 if fmt == "int8" else 256.0  # of 1.0
+    for step in (4.0, 8.0, 16.0):
+        base2 = size + step * np.arange(count)
+        p.scales[0][0, 0] = (base2 / (code * D * D ** -0.5 * np.log2(np.e))).astype(np.float32)
+        p.gpu.k_scale.copy_(torch.from_numpy(p.scales[0]))
+        got = p.attend(_bf16(torch.ones(news, r, D)), [news], [L]).double().cpu().numpy()
+        V = kv8.value_of(p.codes[1][0, 0], p.scales[1][0, 0][np.arange(L) // block].astype(np.float64)[:, None], fmt)
+        edge = 2.0 ** -7 * np.abs(V).max(0)
+        assert np.isfinite(got).all()
+        assert (got >= V.min(0) - edge).all() and (got <= V.max(0) + edge).all()
+        # no more than 256 fp32 steps below the top takes part
+        near = base2 > base2[(L - news) // block] - 40 - 256 * 2.0 ** -23 * size
+        V = V[np.repeat(near, block)]
+        assert (got >= V.min(0) - edge).all() and (got <= V.max(0) + edge).all()
