@@ -97,7 +97,7 @@ constexpr int kMaxCtas = 256;       // workspace bound on the grid
 // ragged batch of 8 takes 37.9, 33.4, 32.9 us at 2, 4 and 6, the drafts of 16
 // sequences 34.0, 33.3, 34.3.
 constexpr int kTileCost = 4;
-constexpr float kMinusBig = -1e30f; // running-max start: finite, so 2^(m - m_new) is never NaN
+constexpr float kMinusBig = -3.402823466e38f;  // running-max start, finite: 2^(m - m_new) is never NaN
 // A row's m is raised to its largest score only when a score passes it by
 // more than kSlack: weights are 2^kWeightBits at m and fit fp16 up to there.
 // From 2^23 on, where an fp32 step is 1 and more and m + 8 or m - 7 may be

@@ -95,7 +95,7 @@ constexpr int kMaxCtas = 256;       // workspace bound on the grid
 // A prompt of 4096 (16 heads on 2 x 256): 173, 149, 137, 140 us at 1 to 4; 16
 // sequences' 8 queries over 4096 positions 53, 52, 50, 50 us.
 constexpr int kTileCost = 3;
-constexpr float kMinusBig = -1e30f;
+constexpr float kMinusBig = -3.402823466e38f;  // running-max start, finite: 2^(m - m_new) is never NaN
 constexpr float kWeightBits = 7.f;  // weights are 2^7 at the row's m ...
 constexpr float kSlack = 8.f;       // ... which scores may pass by this much
 // x - m is computed in one step from the product, a x + (log2 s_v - m), so m's own

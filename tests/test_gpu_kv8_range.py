@@ -185,14 +185,14 @@ def _check_top(p, q, news, ln):
     assert not bad.any(), (bad.mean(), got[bad][:4], lo[bad][:4], hi[bad][:4])
 
 
-SCORES = [(12, 11), (12, 14), (13, 16), (20, 20)]
+SCORES = [(12, 11), (12, 14), (13, 16), (20, 20), (50, 52), (60, 61)]
 
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("a,b", SCORES)
 @pytest.mark.parametrize("D,r,news", FORMS)
 def test_scores_far_from_zero(moelib, cuda_dev, D, r, news, a, b, fmt):
-    """Scores of both signs up to 2^40 and more, each more than 1000 from the
+    """Scores of both signs up to 2^121 and more, each more than 1000 from the
     next or equal to it. (The products are whole multiples of a power of two, so
     equal scores are equal in fp32; every block has the same K scale.)"""
     L, block = 200, 16
@@ -207,6 +207,24 @@ def test_scores_far_from_zero(moelib, cuda_dev, D, r, news, a, b, fmt):
     k[5], k[37] = 2.0, 0.5  # one largest and one smallest, which every row sees
     p.write([_bf16(k * 2.0 ** b), _bf16(_rand(gen, L, 1, D))], [L], [0])
     _check_top(p, q, news, L)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("a,b", [(50, 52), (56, 57), (60, 61)])
+@pytest.mark.parametrize("D,r,news", FORMS)
+def test_all_scores_far_below_zero(moelib, cuda_dev, D, r, news, a, b, fmt):
+    """Every visible score lies below -1e30 and all are equal; the first query of
+    a prompt sees one position only and returns its value."""
+    p = Pair(moelib, 1, 1, D, max(news, 2), 16, fmt)
+    L = news
+    gen = torch.Generator().manual_seed(11)
+    v = _rand(gen, L, 1, D)
+    q = _bf16(torch.full((news, r, D), 2.0 ** a))
+    for values in (v, torch.cat([v[:1].sign(), v[1:].clamp(-1, 1)])):
+        if values is not v:
+            values[::16] = values[::16].sign()  # every block's largest is 1: one V scale
+        p.write([_bf16(torch.full((L, 1, D), -2.0 ** b)), _bf16(values)], [L], [0])
+        _check_top(p, q, news, L)
 
 
 @pytest.mark.parametrize("fmt", FMTS)
