@@ -152,11 +152,16 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_write_kernel(const CacheArgs 
     return m;
   };
   uint32_t m = unit_max(mx, 0);
-  const bool odd = m >= 0x7F80u;  // an infinity or a NaN: the maximum again over finite values, and they are replaced
+  // Rare values: an infinity or a NaN (the maximum again over finite values, and
+  // they are replaced); in E4M3, from 1.9375 * 2^127 on, those next to code 256 of
+  // the scale 2^120, whose value is 2^128: they take 240, which is nearer than half
+  // a step of theirs (2^-4).
+  constexpr uint32_t kTop = kE4m3 ? 0x7F77u : 0x7F7Fu;
+  const bool odd = m > kTop;
   auto reload = [&](int piece) { return ld_once_v4(x + (size_t)(piece / (D / 8)) * p.stride + piece % (D / 8) * 8); };
   const int pieces = (r1 - r0) * (D / 8);
   if (odd) {
-    if (tu == 0) flag(p.status, (int32_t)MOE_ERR_RANGE);
+    if (tu == 0 && m >= 0x7F80u) flag(p.status, (int32_t)MOE_ERR_RANGE);
     mx = 0;
 #pragma unroll 1
     for (int piece = tu; piece < pieces; piece += kTU) {
@@ -201,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_write_kernel(const CacheArgs 
   if (odd) {
     auto finite = [&](uint32_t h) -> uint32_t {  // one bf16
       const uint32_t a = h & 0x7FFFu;
-      return a < 0x7F80u ? h : a == 0x7F80u ? (h & 0x8000u) | m : 0u;
+      return a > 0x7F80u ? 0u : (h & 0x8000u) | min(a == 0x7F80u ? m : a, kTop);
     };
 #pragma unroll 1
     for (int piece = tu; piece < pieces; piece += kTU) {

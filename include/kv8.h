@@ -10,7 +10,8 @@
  *   MOE_KV8_INT8  code -127 .. 127, stored as the byte code + 128; the scale
  *                 of a block with largest magnitude a is fp32(a / 127);
  *   MOE_KV8_E4M3  code an e4m3 number (finite, |code| <= 448); the scale is
- *                 the smallest power of two with a / scale <= 448.
+ *                 the smallest power of two with a / scale <= 448 (2^120 at
+ *                 most, where codes stop at 240: 256 would be 2^128).
  * A scale is at least 2^-60, or 0 for a block of zeros only. Three bytes are
  * never stored: 0 in int8, which would be code -128, and 0x7F and 0xFF in
  * e4m3, which write and read take as +-480 and attention as NaN. Bytes past a

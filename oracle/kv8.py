@@ -7,7 +7,8 @@ of positions). A stored value is code * scale:
   int8  code in -127..127, stored as code + 128; scale = fp32(a / 127) for a
         block whose largest magnitude is a;
   e4m3  4 exponent bits of bias 7, 3 mantissa bits, largest value 448; scale
-        = the smallest power of two with a / scale <= 448.
+        = the smallest power of two with a / scale <= 448; at 2^120, the
+        largest there is, codes stop at 240 (256 would be 2^128, past bf16).
 Bytes that a write never stores count as what their bits say without special
 cases: 0 in int8 is -128, 0x7F and 0xFF (the NaNs of e4m3) are +-480.
 A scale is at least 2^-60, and 0 for a block of zeros. The stored scale is an
@@ -79,7 +80,7 @@ def code_of(x, scale, fmt) -> np.ndarray:
     y = np.asarray(x, dtype=np.float32) * inv
     if fmt == "int8":
         return (np.clip(np.rint(y), -127, 127) + 128).astype(np.uint8)
-    return e4m3_code(y)
+    return e4m3_code(np.clip(y, -240, 240) if scale == np.float32(2.0 ** 120) else y)
 
 
 def write(x_bits, offsets, starts, codes, scales, block, fmt):

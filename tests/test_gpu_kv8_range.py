@@ -253,3 +253,54 @@ def test_scores_that_rise_by_a_little(moelib, cuda_dev, D, r, news, size, fmt):
         near = base2 > base2[(L - news) // block] - 40 - 256 * 2.0 ** -23 * size
         V = V[np.repeat(near, block)]
         assert (got >= V.min(0) - edge).all() and (got <= V.max(0) + edge).all()
+
+
+# ------------------------------------------------------- largest magnitudes ---
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,block", [(64, 16), (128, 32), (256, 64)])
+def test_values_up_to_the_largest_of_bf16(moelib, cuda_dev, D, block, fmt):
+    """Everything finite that is written reads back finite, within half a step:
+    of a code (a / 254, and what the fp32 scale and product round) for int8,
+    2^-4 relative for e4m3."""
+    L = 5 * block + 3
+    p = Pair(moelib, 1, 2, D, L, block, fmt)
+    gen = torch.Generator().manual_seed(12)
+    big = torch.finfo(torch.bfloat16).max
+    x = _bf16((1 - 0.06 * torch.rand(L, 2, D, generator=gen)) * big * torch.sign(_rand(gen, L, 2, D)))
+    x[0, 0, 0], x[0, 1, 1] = big, -big
+    x[block:block + 5] = _bf16(torch.tensor(1.9375 * 2.0 ** 127))  # between two codes
+    x[2 * block:3 * block] *= 2.0 ** -9
+    y = x.clone()
+    y[3, 0, 2:4], y[3, 1, 5] = float("inf"), float("nan")  # an infinity is as large as its block's largest
+    first = 2 * block + 3  # the second call starts inside a block and makes its scale grow
+    for v, status in ((x, moelib.MOE_OK), (y, moelib.MOE_ERR_RANGE)):
+        p.write([v[:first], -v[:first]], [first], [0], expect=status)
+        p.write([v[first:], -v[first:]], [L - first], [first])
+        p.check()
+        p.read([L], [0])
+        for codes, scales, sign in zip((p.gpu.k, p.gpu.v), p.scales, (1, -1)):
+            s = scales[0][:, np.arange(L) // block][:, :, None].astype(np.float64)
+            stored = kv8.value_of(codes.view(torch.uint8).cpu().numpy()[0], s, fmt).transpose(1, 0, 2)
+            assert (np.abs(stored) < 2.0 ** 128 * (1 - 2.0 ** -9)).all()  # rounds to a finite bf16
+            want = sign * x.double().numpy()
+            keep = np.isfinite(v.double().numpy())
+            err = np.abs(stored - want)[keep]
+            half = big / 254 * (1 + 2.0 ** -20) if fmt == "int8" else np.abs(want[keep]) * 2.0 ** -4
+            grown = (np.arange(L)[:, None, None] >= 2 * block) & (np.arange(L)[:, None, None] < first)
+            half = np.where(np.broadcast_to(grown, want.shape)[keep], big / 64, half)  # quantised twice
+            assert (err <= half).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,r,news", FORMS)
+def test_attention_over_the_largest_of_bf16(moelib, cuda_dev, D, r, news, fmt):
+    L, block = 130, 16
+    p = Pair(moelib, 1, 1, D, L, block, fmt)
+    gen = torch.Generator().manual_seed(13)
+    big = torch.finfo(torch.bfloat16).max
+    v = _bf16((1 - 0.06 * torch.rand(L, 1, D, generator=gen)) * big)
+    v[5:9] = big
+    p.write([_bf16(_rand(gen, L, 1, D)), v], [L], [0])
+    p.check()
+    _check(p, _bf16(_rand(gen, news, r, D)), [news], [L])
