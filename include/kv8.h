@@ -22,15 +22,17 @@
  *   new values; one that did takes the larger of that and the scale it had
  *   (a scale never shrinks while its block fills). If the scale grew, the
  *   block's earlier codes are quantised again, from code * old scale. A code
- *   is x * fp32(1 / scale) rounded to nearest, ties to even. Positions past
- *   the new tokens keep their bytes. Writing the same tokens again at the
- *   same positions changes nothing.
+ *   is x * fp32(1 / scale) rounded to nearest, ties to even. Repeating a
+ *   sequence's last write changes nothing. Positions past the new tokens keep
+ *   their bytes, but a write over earlier positions may leave their block
+ *   another scale: what follows the new tokens in it is lost and has to be
+ *   written again.
  *   Every finite input is allowed. A NaN is stored as 0 and an infinity as
  *   its sign times the largest finite magnitude of the block's new values,
  *   and MOE_ERR_RANGE is written to *status: the other values stay good.
  *
- * Read: the values of positions starts[b] .. of sequence b, code * scale
- *   rounded once to bf16.
+ * Read: the values of positions starts[b] .. of sequence b, the fp32 product
+ *   code * scale rounded to bf16.
  *
  * Attention: the queries of sequence b are its last n = offsets[b+1] -
  *   offsets[b] positions; query i sees positions 0 .. lens[b] - n + i (its own
@@ -127,12 +129,20 @@ moe_status moe_kv8_workspace_bytes(const moe_kv8_shape* shape, size_t* bytes);
  * bounded wait ran out; o is not valid). T == 0 writes the status word only.
  *
  * Numerics: q goes to fp16 with its row's largest magnitude in [1, 2) (values
- * 2^-14 below that lose bits), codes are exact; the weights go to fp16 with
- * the row's running maximum at 2^7 to 2^15; products, softmax and sums are
- * fp32, and o is rounded once to bf16. So o is within
- * 2^-8 |o| + 2.1 * 2^-11 sum_j p_j |V_j| of the formula, and what the rounding
- * of q does to the scores. A score or an output past fp32's range is an
- * infinity or a NaN. */
+ * 2^-14 below that lose bits), codes are exact; the weights, softmax times V's
+ * scale, go to fp16 with the row's running maximum at 2^7 to 2^15; products,
+ * softmax and sums are fp32, and o is rounded once to bf16. So o is within
+ *   2^-8 |o| + 2.1 * 2^-11 sum_j p_j |V_j|
+ *            + 2^-32 max_j (p_j s_v(j)) sum_j |c_j|
+ * of the formula (c_j: V's code, s_v(j): its scale, 2^-60 for zeros; the last
+ * term is for weights 2^-21 and more below the largest, where fp16's steps no
+ * longer shrink), and of what errors of the scores do to p: q's rounding, and
+ * fp32's of a sum of D products and of adding log2 s_v(j), up to 2^-22 of the
+ * score's size (positions whose scores are nearer to one another than that
+ * share their weight in some way). V's scales may lie any distance apart. Where
+ * scale * log2(e) * max|q| * k_scale, a score or an output passes fp32's range,
+ * the row has infinities or NaN.
+ */
 moe_status moe_kv8_attn(const moe_kv8_shape* shape, const void* q, const moe_kv8_cache* cache, const int32_t* offsets,
                         const int32_t* lens, float scale, void* o, void* workspace, size_t ws_bytes, void* stream);
 

@@ -304,3 +304,50 @@ def test_attention_over_the_largest_of_bf16(moelib, cuda_dev, D, r, news, fmt):
     p.write([_bf16(_rand(gen, L, 1, D)), v], [L], [0])
     p.check()
     _check(p, _bf16(_rand(gen, news, r, D)), [news], [L])
+
+
+# ------------------------------------------------------- words of the header ---
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_read_rounds_the_fp32_product(moelib, cuda_dev, D):
+    """INT8 codes times scales whose product lies next to the middle of two bf16:
+    fp32 rounds it to the middle, and that goes to the even one."""
+    block, L = 16, 16 * 200
+    p = Pair(moelib, 1, 1, D, L, block, "int8")
+    rng = np.random.default_rng(15)
+    code = rng.integers(64, 128, L // block)
+    middle = (rng.integers(128, 256, L // block) + 0.5) * 2.0 ** -7
+    scale = np.float32(middle / code)
+    product = scale * code.astype(np.float32)
+    exact = scale.astype(np.float64) * code
+    assert ((product == middle) & (exact != middle)).sum() > 50
+    p.codes = [np.repeat(128 + code, block).astype(np.uint8)[None, None, :, None] * np.ones((1, 1, 1, D), np.uint8)] * 2
+    p.scales = [scale[None, None]] * 2
+    p.gpu.k.copy_(torch.from_numpy(p.codes[0])), p.gpu.v.copy_(torch.from_numpy(p.codes[1]))
+    p.gpu.k_scale.copy_(torch.from_numpy(p.scales[0])), p.gpu.v_scale.copy_(torch.from_numpy(p.scales[1]))
+    p.read([L], [0])
+    out = torch.empty(L, 1, D, dtype=torch.bfloat16, device="cuda:0")
+    off, st = (torch.tensor(v, dtype=torch.int32, device="cuda:0") for v in ([0, L], [0]))
+    moelib.kv8_read(p.shape(L), p.gpu, off, st, out, torch.empty_like(out))
+    want = torch.from_numpy(product).to(torch.bfloat16).repeat_interleave(block)
+    assert torch.equal(out[:, 0].cpu(), want[:, None].expand(L, D))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_writing_over_earlier_positions(moelib, cuda_dev, fmt):
+    """A write at a block's start takes the scale of its own values: what follows
+    in the block keeps its bytes and is written again, as the header says."""
+    p = Pair(moelib, 1, 2, 64, 48, 16, fmt)
+    gen = torch.Generator().manual_seed(16)
+    a, b = (_bf16(_rand(gen, n, 2, 64) * s) for n, s in ((5, 1.0), (14, 9.0)))
+    p.write([a, -a], [5], [0])
+    p.write([b, -b], [14], [5])
+    p.write([b, -b], [14], [5])  # the last write repeated
+    p.check()
+    before = p.bytes()
+    p.write([a, -a], [5], [0])
+    p.check()
+    assert all(np.array_equal(x[:, :, 5:], y[:, :, 5:]) for x, y in zip(before, p.bytes()))
+    p.write([b, -b], [14], [5])
+    p.check()
+    p.read([19], [0])
