@@ -39,8 +39,24 @@ constexpr float kLog2e = 1.4426950408889634f;
 //   40 heads / 8 x 128, B = 16, L = 4096:    n = 4 57.2 / 107, n = 8 102 / 100
 bool few(const moe_kv8_shape& s) { return (long long)s.T * s.Hq <= 36ll * s.B * s.Hkv + 192; }
 
+// For up to s.T tokens: what the tiles need does not grow with T, while the split
+// kernels' partial states do, so fewer tokens may need more. Theirs grow while
+// the rows per tile stay the same; split_steps are the T at which those change.
 size_t workspace_bytes(const moe_kv8_shape& s) {
-  return s.T == 0 ? 256 : few(s) ? split_workspace_bytes(s) : tiles_workspace_bytes(s);
+  if (s.T == 0) return 256;
+  size_t most = few(s) ? 0 : tiles_workspace_bytes(s);
+  const long long last = (36ll * s.B * s.Hkv + 192) / s.Hq;  // the most tokens that few() takes
+  long long T[3] = {last};
+  split_steps(s, T + 1);
+  for (const long long t : T) {
+    moe_kv8_shape fewer = s;
+    fewer.T = (int32_t)(t < s.T ? t : s.T);
+    if (fewer.T > 0 && few(fewer)) {
+      const size_t n = split_workspace_bytes(fewer);
+      most = n > most ? n : most;
+    }
+  }
+  return most;
 }
 
 moe_status attn(const moe_kv8_shape* shape, const void* q, const moe_kv8_cache* cache, const int32_t* offsets,

@@ -28,6 +28,7 @@ constexpr long long kTimeoutNs = 1000000000ll;
 
 // Split-context kernels (kv8_split.cu), for few query tokens per sequence.
 size_t split_workspace_bytes(const moe_kv8_shape& s);
+void split_steps(const moe_kv8_shape& s, long long* T);  // the most tokens with 8, and with 16 rows per tile
 moe_status launch_split(const AttnArgs& a, cudaStream_t stream);
 
 // Tensor-core tile kernels (kv8_tiles.cu), for many.

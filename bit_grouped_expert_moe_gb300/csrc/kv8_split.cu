@@ -1051,6 +1051,12 @@ size_t split_workspace_bytes(const moe_kv8_shape& s) {
   return 256 + kMaxCtas * (sizeof(int32_t) + sizeof(int4)) + slots * RT * (2 + (size_t)s.D) * sizeof(float);
 }
 
+void split_steps(const moe_kv8_shape& s, long long* T) {
+  const int r = s.Hq / s.Hkv;
+  T[0] = (long long)(8 / r) * s.B;
+  T[1] = (long long)(16 / r) * s.B;
+}
+
 moe_status launch_split(const AttnArgs& a, cudaStream_t stream) {
   using namespace split;
   const int sms = sm_count();

@@ -116,7 +116,8 @@ moe_status moe_kv8_write(const moe_kv8_shape* shape, const void* k_new, const vo
 moe_status moe_kv8_read(const moe_kv8_shape* shape, const moe_kv8_cache* cache, const int32_t* offsets,
                         const int32_t* starts, void* k_out, void* v_out, int32_t* status, void* stream);
 
-/* Bytes of device workspace moe_kv8_attn needs for `shape`. */
+/* Bytes of device workspace moe_kv8_attn needs for `shape`, or with fewer tokens
+ * (T): a workspace for the largest T serves all steps of one cache. */
 moe_status moe_kv8_workspace_bytes(const moe_kv8_shape* shape, size_t* bytes);
 
 /* Causal attention of T query tokens over the cache (the formula above). q,
