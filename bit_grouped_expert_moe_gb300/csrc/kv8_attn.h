@@ -118,11 +118,6 @@ struct Runs {
   int more;       // N % C
   __device__ Runs(long long N, int C) : per(div_small(N, C)), more((int)(N - per * C)) {}
   __device__ long long start(int c) const { return c * per + min(c, more); }
-  __device__ bool empty(int c) const { return per == 0 && c >= more; }
-  __device__ int of(long long s) const {  // the run that holds place s
-    const long long lead = more * (per + 1);
-    return s < lead ? (int)div_small(s, per + 1) : more + (int)div_small(s - lead, per);
-  }
 };
 
 // Runs are cut on a scale of places, where a tile with units takes `cost` more
@@ -144,7 +139,7 @@ struct Place {
 // By one warp: checks the tables (false if they break the rules), counts the
 // call's places and finds that of run c's start.
 __device__ inline bool find_run(const int32_t* offsets, const int32_t* lens, int B, int T, int Hkv, int L_max, int r,
-                                int RT, int KT, int cost, int c, int C, Place* out, long long* start) {
+                                int RT, int KT, int cost, int c, int C, Place* out) {
   const int lane = threadIdx.x & 31;
   long long total = 0, before = 0, units = 0, at = 0;
   int tiles = 0;
@@ -236,7 +231,6 @@ __device__ inline bool find_run(const int32_t* offsets, const int32_t* lens, int
   }
   k.units = units;
   *out = k;
-  *start = at;
   return !bad;
 }
 

@@ -316,8 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp < 2) {  // the run's start and its end
     Place k;
-    long long at;
-    const bool ok = find_run(p.offsets, p.lens, p.B, p.T, p.Hkv, p.L_max, r, RT, kPos, kTileCost, c + warp, C, &k, &at);
+    const bool ok = find_run(p.offsets, p.lens, p.B, p.T, p.Hkv, p.L_max, r, RT, kPos, kTileCost, c + warp, C, &k);
     if (lane == 0) {
       s_unit[warp] = k.units;
       if (warp == 0) {

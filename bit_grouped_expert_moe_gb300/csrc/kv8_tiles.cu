@@ -560,9 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 1 || warp == 2) {  // the run's start and its end
     Place k;
-    long long at;
     const bool ok = find_run(p.offsets, p.lens, p.B, p.T, p.Hkv, p.L_max, r, kTileRows, kKeys, kTileCost, c + warp - 1,
-                             C, &k, &at);
+                             C, &k);
     if (lane == 0) {
       s_unit[warp - 1] = k.units;
       if (warp == 1) {
