@@ -158,7 +158,7 @@ struct Cursor {
     g = 0;
     do {
       ++b;
-      n = b < p.B ? __ldg(p.lens + b) : 0;
+      n = b < p.B ? ld(p.lens + b) : 0;
       nb = nblocks(n);
     } while (nb == 0 && b < p.B);
   }
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool bad = false;
     for (int base = 0; base < p.B; base += 32) {
       const int b = base + lane;
-      const int n = b < p.B ? __ldg(p.lens + b) : 0;
+      const int n = b < p.B ? ld(p.lens + b) : 0;
       bad |= n < 0 || n > p.L_max;
       long long v = n > 0 && n <= p.L_max ? nblocks(n) : 0;
 #pragma unroll
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       long long acc = 0;
       for (int base = 0; base < p.B; base += 32) {
         const int b = base + lane;
-        const long long v = b < p.B ? (long long)nblocks(__ldg(p.lens + b)) * p.Hkv : 0;
+        const long long v = b < p.B ? (long long)nblocks(ld(p.lens + b)) * p.Hkv : 0;
         long long incl = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (hit) {
           const int L = __ffs(hit) - 1;
           const long long before = acc + __shfl_sync(0xffffffffu, incl - v, L);
-          const int nbL = nblocks(__ldg(p.lens + base + L));
+          const int nbL = nblocks(ld(p.lens + base + L));
           const long long off = lo - before;
           fb = base + L;
           fg = (int)(off / nbL);
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   const long long lo = s_lo, hi = s_hi;
-  Cursor cur{s_b, s_g, s_i, __ldg(p.lens + s_b), 0};
+  Cursor cur{s_b, s_g, s_i, ld(p.lens + s_b), 0};
   cur.nb = nblocks(cur.n);
 
   volatile int* abort_flag = &ctl->abort;
@@ -317,8 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint16_t* qrow = p.q + ((size_t)cur.b * p.Hq + (size_t)cur.g * r + (live ? qh : 0)) * D;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
-        qf[ks][0] = live ? __ldg(reinterpret_cast<const uint32_t*>(qrow + 16 * ks + hA)) : 0u;
-        qf[ks][1] = live ? __ldg(reinterpret_cast<const uint32_t*>(qrow + 16 * ks + 8 + hA)) : 0u;
+        qf[ks][0] = live ? ld(reinterpret_cast<const uint32_t*>(qrow + 16 * ks + hA)) : 0u;
+        qf[ks][1] = live ? ld(reinterpret_cast<const uint32_t*>(qrow + 16 * ks + 8 + hA)) : 0u;
       }
     };
     auto reset = [&]() {
@@ -541,7 +541,9 @@ __global__ void __launch_bounds__(128) attn_merge_kernel(const MergeParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // Everything up to the dependency wait reads only the lengths, which the
   // block kernel does not write (and which were final before it launched
-  // this grid): it overlaps the block kernel's tail.
+  // this grid): it overlaps the block kernel's tail. They come from L2: L1 may
+  // still hold lengths of an earlier call, which nothing invalidates before the
+  // wait.
   const int r = p.Hq / p.Hkv;
   const int nslice = p.D / 64;
   const int slice = blockIdx.x % nslice;
@@ -559,7 +561,7 @@ __global__ void __launch_bounds__(128) attn_merge_kernel(const MergeParams p) {
   long long before = 0, total = 0;
   bool bad = false;
   for (int bb = threadIdx.x; bb < p.B; bb += blockDim.x) {
-    const int nbb = __ldg(p.lens + bb);
+    const int nbb = __ldcg(p.lens + bb);
     bad |= nbb < 0 || nbb > p.L_max;
     const long long v = nblocks(nbb);
     total += v;
@@ -577,7 +579,7 @@ __global__ void __launch_bounds__(128) attn_merge_kernel(const MergeParams p) {
   bad = __syncthreads_or(bad);
   before = s_before[0] + s_before[1] + s_before[2] + s_before[3];
   total = s_total[0] + s_total[1] + s_total[2] + s_total[3];
-  const int n = __ldg(p.lens + b);
+  const int n = __ldcg(p.lens + b);
   const int nb = bad ? 0 : nblocks(n);
   const long long N = total * p.Hkv, start = before * p.Hkv + (long long)g * nb;
   const int c0 = nb ? cta_of(start, N, p.C) : 0, c1 = nb ? cta_of(start + nb - 1, N, p.C) : -1;

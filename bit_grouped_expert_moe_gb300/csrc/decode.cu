@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_layer_kernel(const Deco
     for (int t = 0; t < kDecodeMaxTokens; ++t)
       if (t < T && tid < H / 8) {
         const int v = tid;
-        const uint4 u = ldg_nc_v4(a.x + (size_t)t * H + (size_t)v * 8);
+        const uint4 u = ld_once_v4(a.x + (size_t)t * H + (size_t)v * 8);
         const uint32_t wv[4] = {u.x, u.y, u.z, u.w};
         float f[8];
 #pragma unroll

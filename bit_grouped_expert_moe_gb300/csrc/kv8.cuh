@@ -10,31 +10,6 @@ namespace kv8 {
 
 constexpr float kScaleFloor = 8.673617379884035e-19f;  // 2^-60: the smallest scale of a block not all zero
 
-// Loads of what an earlier kernel on the stream may have written: the tables,
-// scales, q and the new tokens. The kernels are launched with programmatic
-// dependent launch, so a block may be on its SM while that kernel still writes;
-// these loads stand behind the dependency wait and take the coherent path. (The
-// non-coherent one asks for data that is constant for the grid's whole life, and
-// a line that another kernel left in the SM's L1 cache may serve it.)
-__device__ __forceinline__ int32_t ld(const int32_t* p) {
-  int32_t v;
-  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
-}
-__device__ __forceinline__ float ld(const float* p) {
-  float v;
-  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint4 ld_once_v4(const void* p) {  // 16 bytes that are read once
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p)
-               : "memory");
-  return v;
-}
-
 // Host checks shared by the entry points (kv8_cache.cu).
 bool shape_ok(const moe_kv8_shape& s);
 bool cache_ok(const moe_kv8_cache* c);
