@@ -15,7 +15,8 @@ softmax weights p, V scales s, sums over the row's visible positions):
     amp = scale * sum_d |q_d| * (255 code steps of int8, or 448) * K scale;
     on the base-2 scale, with log2 s added and m taken off, three roundings of
     at most u (|score| + 128) each, twice (a weight, and their sum);
-  * a row's scores off by ds change its weights by a factor within e^(2 ds);
+  * a row's scores off by ds change its weights by a factor within e^(2 ds), and
+    o by e^(2 ds) - 1 of the sum of magnitudes;
   * sums of at most L / 16 + 64 terms in fp32, each addition off by 2 u of at
     most the sum of magnitudes.
 Every figure is the row's own: a block that other sequences hold has no part."""
@@ -63,10 +64,10 @@ def _tolerance(p, q, news, lens):
                     ds = (D + 8) * 2 * u * amp
                     ds += scale * 2 * np.abs(y).max() * 2.0 ** -25 * np.abs(K[:see]).sum(1).max()
                     ds += 6 * u * (np.abs(z).max() * np.log2(np.e) + 128) * np.log(2)
-                    assert ds < 0.05
+                    assert ds < 0.5
                     weighed = (w * sv[:see])
                     absolute = weighed @ np.abs(c[:see])
-                    e = (2.1 * 2.0 ** -11 + 2.1 * ds + (see / 16 + 64) * 2 * u) * absolute
+                    e = (2.1 * 2.0 ** -11 + np.expm1(2 * ds) + (see / 16 + 64) * 2 * u) * absolute
                     e += 2.0 ** -32 * weighed.max() * np.abs(c[:see]).sum(0)
                     o[off[b] + i, h] = weighed @ c[:see]
                     tol[off[b] + i, h] = e + 2.0 ** -8 * (np.abs(o[off[b] + i, h]) + e)
@@ -224,6 +225,30 @@ def test_all_scores_far_below_zero(moelib, cuda_dev, D, r, news, a, b, fmt):
         if values is not v:
             values[::16] = values[::16].sign()  # every block's largest is 1: one V scale
         p.write([_bf16(torch.full((L, 1, D), -2.0 ** b)), _bf16(values)], [L], [0])
+        _check_top(p, q, news, L)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("a,b", [(4, 3), (10, 9), (12, 14), (20, 20), (60, 61)])
+@pytest.mark.parametrize("D,r,news", FORMS)
+def test_large_scores_over_v_blocks_far_apart(moelib, cuda_dev, D, r, news, a, b, fmt):
+    """Both at once, over several units and runs: the tops share the weight, and
+    their values lie up to 2^176 apart."""
+    block, count = 16, 100
+    L = block * count
+    p = Pair(moelib, 1, 1, D, L, block, fmt)
+    gen = torch.Generator().manual_seed(17)
+    exponents = [[None, 115, -58, 3][int(i)] for i in torch.randint(0, 4, (count,), generator=gen)]
+    k = (1 + torch.randint(0, 8, (L, 1, 1), generator=gen) / 8.0).expand(L, 1, D).clone()
+    k[::block] = 1.875
+    p.write([_bf16(k * 2.0 ** b), _bf16(_blocks(gen, exponents, block, D))], [L], [0])
+    sign = torch.where(torch.arange(r) % 2 == 1, -1.0, 1.0)[None, :, None]
+    q = _bf16((sign * 2.0 ** a).expand(news, r, D).clone())
+    if (a, b) == (4, 3):  # scores below 2^13: fp32 tells them from their neighbours
+        got = p.attend(q, [news], [L]).double().cpu().numpy()
+        want, tol = _tolerance(p, q, [news], [L])
+        assert np.isfinite(got).all() and (np.abs(got - want) <= tol).all()
+    else:
         _check_top(p, q, news, L)
 
 
