@@ -23,20 +23,25 @@ constexpr float kLog2e = 1.4426950408889634f;
 // to 32 rows (query heads of a KV head x tokens), the tiles once per 128 or 256
 // but with a longer chain in front. So a call is the former's with up to 36
 // rows per sequence and KV head, or somewhat more where few of those pairs
-// keep the GPU's blocks from filling up. (The host knows the tokens of the
-// batch, not each sequence's.) Measured, split / tiles in us, INT8, n tokens of
-// each of B sequences over L positions:
-//   16 heads / 2 x 256, B = 1, L = 32,768:   n = 12 48.5 / 55.9, n = 16 60.8 / 57.3
-//                       B = 1, L = 2048:     n = 64 28.4 / 32.8
-//                       B = 16, L = 4096:    n = 4 41.9 / 47.6, n = 8 73.0 / 48.0
-//                       B = 16, L = 512:     n = 4 18.5 / 23.2, n = 8 27.6 / 23.7
-//   16 heads / 4 x 128, B = 1, L = 32,768:   n = 24 38.2 / 43.3, n = 32 47.0 / 44.3
-//                       B = 16, L = 4096:    n = 12 57.4 / 59.2, n = 24 84.6 / 61.3
-//                       B = 16, L = 512:     n = 8 18.4 / 21.9, n = 12 24.2 / 22.1
-//   8 heads / 8 x 128,  B = 1, L = 32,768:   n = 64 48.7 / 60.5
-//                       B = 16, L = 512:     n = 32 26.5 / 28.6, n = 64 43.0 / 28.8
-//   4 heads / 1 x 64,   B = 16, L = 4096:    n = 12 16.5 / 19.1, n = 24 24.5 / 20.3
-//   40 heads / 8 x 128, B = 16, L = 4096:    n = 4 57.2 / 107, n = 8 102 / 100
+// keep the GPU's blocks from filling up. Measured, split / tiles in us, INT8, n
+// tokens of each of B sequences over L positions:
+//   16 heads / 2 x 256, B = 1, L = 32,768:   n = 12 49.0 / 55.8, n = 16 61.9 / 56.6
+//                       B = 1, L = 2048:     n = 64 29.1 / 32.3
+//                       B = 16, L = 4096:    n = 4 42.6 / 47.2, n = 8 73.8 / 47.8
+//                       B = 16, L = 512:     n = 4 18.9 / 23.2, n = 8 28.6 / 23.7
+//   16 heads / 4 x 128, B = 1, L = 32,768:   n = 24 39.5 / 43.7, n = 32 48.5 / 44.6
+//                       B = 16, L = 4096:    n = 12 59.4 / 60.7, n = 24 87.9 / 62.4
+//                       B = 16, L = 512:     n = 8 19.2 / 22.2, n = 12 25.6 / 22.4
+//   8 heads / 8 x 128,  B = 1, L = 32,768:   n = 64 50.0 / 61.1
+//                       B = 16, L = 512:     n = 32 28.1 / 28.9, n = 64 45.7 / 29.2
+//   4 heads / 1 x 64,   B = 16, L = 4096:    n = 12 16.9 / 19.6, n = 24 25.0 / 20.7
+//   40 heads / 8 x 128, B = 16, L = 4096:    n = 4 58.4 / 110, n = 8 105 / 103
+// The host knows the tokens of the batch, not each sequence's, so one long chunk
+// among many single tokens goes with them, at either side of the rule to its or
+// their cost (16 heads / 2 x 256, one call / the two alone, in us):
+//   63 tokens over 4000 each and 100 over 20,000:      274 (split)  / 58 + 58
+//   63 tokens over 4000 each and 1000 over 20,000:     358 (tiles)  / 58 + 251
+//   255 tokens over 1000 each and 800 over 32,768:    2781 (split)  / 123 + 298
 bool few(const moe_kv8_shape& s) { return (long long)s.T * s.Hq <= 36ll * s.B * s.Hkv + 192; }
 
 // For up to s.T tokens: what the tiles need does not grow with T, while the split

@@ -4,10 +4,10 @@
 // one conversion, so they are bound by memory, and at a decode step's sizes
 // by the latency of one dependent chain (tables, values, scale, codes).
 // Measured (2 KV heads of 256, INT8, in a graph):
-//   read of 32,768 positions  101 MB in 18.7 us, 5.4 TB/s, 79% of the measured
-//                             copy rate; instructions take 64% of the issue slots
-//   write of 4096 tokens, and 128 of them read back   8.6 us for 13 and 0.4 MB
-//   write of a token of 64 sequences, and their open blocks read back   9.2 us
+//   read of 32,768 positions  101 MB in 18.6 us, 5.4 TB/s, 80% of the measured
+//                             copy rate; instructions take 53% of the issue slots
+//   write of 4096 tokens, and 128 of them read back   8.7 us for 13 and 0.4 MB
+//   write of a token of 64 sequences, and their open blocks read back   9.0 us
 #include "kernels.h"
 #include "kv8_attn.h"
 
@@ -17,9 +17,11 @@ namespace bgmoe {
 namespace kv8 {
 
 constexpr int kThreads = 256;
-// Its thread blocks per SM, at most: as many as a tile each would be 2048 for
-// 32,768 positions, each with the tables and the bisection in front of it: 30.7
-// us, against 19.6 with blocks that walk and ask for a tile ahead.
+// Its grid per SM, at most: as many blocks as a tile each would be 2048 for 32,768
+// positions, each with the tables and the bisection in front of it: 30.7 us,
+// against 19.6 with blocks that walk and ask for a tile ahead. (Of the larger
+// tiles at 256 head dims, with 105 registers, two fit an SM at once: that grid
+// runs in two waves.)
 constexpr int kReadBlocks = 4;
 
 struct CacheArgs {

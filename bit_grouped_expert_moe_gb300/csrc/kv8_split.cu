@@ -10,12 +10,12 @@
 // spread evenly over the SMs whatever the lengths are.
 //
 // Measured (16 heads on 2 x 256 but for the drafts, both kernels, in a run of calls):
-//   one token after 131,072 positions, E4M3    30.1 us, 4.5 TB/s (66% of the
-//                            measured copy rate; 7.5 us of it do not grow)
-//   one token after 32,768 positions, INT8     14.6 us, 2.3 TB/s
-//   a ragged batch of 8, 148,369 positions     33.5 us, 4.5 TB/s
-//   1 to 5 drafts of 16 sequences, 70,120 positions, 4 x 128, E4M3   30.6 us,
-//                            2.4 TB/s: 0.87 us a unit of 32 KB (0.74 at the copy
+//   one token after 131,072 positions, E4M3    30.6 us, 4.4 TB/s (65% of the
+//                            measured copy rate; 7.6 us of it do not grow)
+//   one token after 32,768 positions, INT8     14.8 us, 2.3 TB/s
+//   a ragged batch of 8, 148,369 positions     34.0 us, 4.5 TB/s
+//   1 to 5 drafts of 16 sequences, 70,120 positions, 4 x 128, E4M3   31.0 us,
+//                            2.3 TB/s: 0.87 us a unit of 32 KB (0.74 at the copy
 //                            rate), a fifth more of them than positions (second
 //                            tiles, ragged ends), 3.3 us a tile begun and ended
 // What does not grow (one token after 300 positions, from the wait for the

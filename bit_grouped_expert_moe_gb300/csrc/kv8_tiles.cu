@@ -44,12 +44,14 @@
 // fp16), three of each.
 //
 // Bound: for 2048 queries after 16,384 positions (16 heads on 2 x 256, INT8)
-// the tensor cores run 57% of a unit's 3600 cycles: a product S or O takes 1024
+// the tensor cores run 56% of a unit's 3660 cycles: a product S or O takes 1024
 // and about 500 from its issue to the softmax's first read, and the softmax
-// (2400) leaves the two products no more overlap. 1.42 PFLOP/s, 75% of the
-// measured bf16 rate; a prompt of 4096 1.02 PFLOP/s, 54%: 56 units per pair are
+// (2400) leaves the two products no more overlap. 1.39 PFLOP/s, 73% of the
+// measured bf16 rate; a prompt of 4096 1.01 PFLOP/s, 53%: 56 units per pair are
 // few beside the tiles' beginnings and ends. At 128 head dims the softmax
-// bounds a unit: 2000 queries after 28,000 positions, 555 us, 0.86 PFLOP/s.
+// bounds a unit: 2000 queries after 28,000 positions, 574 us, 0.83 PFLOP/s. (What
+// is rare in a unit, large scores and V scales far apart, costs the softmax a
+// branch: 2% of the chunk, 3% at 128 head dims, by how the code around it falls.)
 //
 // Codes are exact in fp16: 1024 + u (u = code + 128, by a byte permute) minus
 // 1152 for int8, the conversion instruction for e4m3. Scales as in

@@ -128,6 +128,9 @@ moe_status moe_kv8_workspace_bytes(const moe_kv8_shape* shape, size_t* bytes);
  * start of the workspace is the call's status word (read it with
  * moe_status_read): MOE_OK, MOE_ERR_INVALID_ARG or MOE_ERR_DEVICE_TIMEOUT (a
  * bounded wait ran out; o is not valid). T == 0 writes the status word only.
+ * The kernels are chosen by the tokens per sequence on average: a batch of
+ * single tokens and a long chunk is quicker as two calls, the chunk's on the
+ * cache rows of its sequences alone (any range of B is a cache).
  *
  * Numerics: q goes to fp16 with its row's largest magnitude in [1, 2) (values
  * 2^-14 below that lose bits), codes are exact; the weights, softmax times V's

@@ -58,3 +58,25 @@ def test_many_ragged_sequences(moelib, cuda_dev, Hq, Hkv, D, B, fmt):
     p.compare(got.double().cpu().numpy(), want, o_abs, q, lens)
     for _ in range(5):
         assert torch.equal(got, p.attend(q, news, lens))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_a_long_chunk_among_single_tokens(moelib, cuda_dev, fmt):
+    """In one call, and as two on ranges of the same cache."""
+    B, Hq, Hkv, D, L = 20, 8, 2, 128, 700
+    lens, news = [100 + 7 * i for i in range(B - 1)] + [L], [1] * (B - 1) + [300]
+    p = Pair(moelib, B, Hkv, D, L, 32, fmt, seed=5)
+    gen = p.fill(lens, seed=6)
+    q = _rand(gen, sum(news), Hq, D).to(torch.bfloat16)
+    want, o_abs = _plain_attention_gpu(p, q, news, lens)
+    p.compare(p.attend(q, news, lens).double().cpu().numpy(), want, o_abs, q, lens)
+    c, x = p.gpu, q.to("cuda:0")
+    o = torch.empty_like(x)
+    for at, rows in ((slice(0, B - 1), slice(0, B - 1)), (slice(B - 1, B), slice(B - 1, None))):
+        part = moelib.Kv8Cache(c.k[at], c.v[at], c.k_scale[at], c.v_scale[at])
+        counts = news[at]
+        sh = moelib.kv8_shape(len(counts), sum(counts), Hq, Hkv, D, L, 32, p.shape(1).format)
+        ws = moelib.kv8_alloc_workspace(sh, "cuda:0")
+        moelib.kv8_attn(sh, x[rows], part, _i32(_packed(counts)), _i32(lens[at]), o[rows], ws)
+        assert moelib.status_read(ws[:4].view(torch.int32)) == 0
+    p.compare(o.double().cpu().numpy(), want, o_abs, q, lens)
