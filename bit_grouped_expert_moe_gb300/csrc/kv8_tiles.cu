@@ -859,8 +859,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tiles_kernel(const Params p) 
               s += ex2(fmaf(__uint_as_float(x[e]), a[h], sc[h].y) + top + lift);
             l = fmaf(s, kUnlift, l);
           }
-        // Rows of large scores: a x + b with a = 1, b = 0 from here on. (A score
-        // that m + kSlack, rounded, let pass stays within fp16.)
+        // Rows of large scores: a x + b with a = 1, b = 0 from here on, or NaN where m
+        // is infinite. (A score that m + kSlack, rounded, let pass stays within fp16.)
         if (fabsf(m) > kLargeScore && m > kMinusBig) {
 #pragma unroll
           for (int h = 0; h < 4; ++h) {

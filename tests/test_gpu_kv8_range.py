@@ -280,6 +280,28 @@ def test_scores_that_rise_by_a_little(moelib, cuda_dev, D, r, news, size, fmt):
         assert (got >= V.min(0) - edge).all() and (got <= V.max(0) + edge).all()
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("size", [0, 14])
+@pytest.mark.parametrize("D,r,news", FORMS)
+def test_queries_that_are_not_finite(moelib, cuda_dev, D, r, news, size, fmt):
+    """A row with a NaN or an infinity is NaN; the rows beside it, whose scores are
+    ordinary or large, are what they are without it but for the last rounding."""
+    L = 300
+    p = Pair(moelib, 1, 1, D, L, 32, fmt)
+    gen = torch.Generator().manual_seed(18)
+    p.write([_bf16(_rand(gen, L, 1, D) * 2.0 ** size), _bf16(_rand(gen, L, 1, D))], [L], [0])
+    q = _bf16(_rand(gen, news, r, D) * 2.0 ** size)
+    good = p.attend(q, [news], [L]).double().cpu()
+    assert good.isfinite().all()
+    for k, value in enumerate((float("nan"), float("inf"), float("-inf"))):
+        x = q.clone()
+        x[news // 2, 1, 5 + k] = value
+        got = p.attend(x, [news], [L]).double().cpu()
+        assert got[news // 2, 1].isnan().all()
+        got[news // 2, 1] = good[news // 2, 1]
+        assert ((got - good).abs() <= 2.0 ** -7 * good.abs() + 2.0 ** -10 * 4).all()
+
+
 # ------------------------------------------------------- largest magnitudes ---
 
 @pytest.mark.parametrize("fmt", FMTS)
