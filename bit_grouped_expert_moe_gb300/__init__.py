@@ -10,7 +10,9 @@ route_blocks, route, forward, forward_residual, forward_timed, route_noalloc,
 status_read, status_string, test_route_stall, test_decode_stall) and
 include/attention.h (attn_workspace_bytes, attn_decode, attn_decode_timed) and
 include/gdn.h (gdn_scan, gdn_scan_timed) and include/kv8.h (kv8_write,
-kv8_read, kv8_workspace_bytes, kv8_attn, kv8_attn_test_stall).
+kv8_read, kv8_workspace_bytes, kv8_attn, kv8_attn_test_stall) and
+include/rope.h (rope_table, rope) and include/paged.h (paged_append,
+paged_workspace_bytes, paged_attn, paged_attn_test_stall, paged_keep).
 """
 from __future__ import annotations
 
@@ -49,6 +51,31 @@ class Kv8Shape(ctypes.Structure):
 
 class Kv8CacheC(ctypes.Structure):
     _fields_ = [(n, P) for n in ("k_codes", "v_codes", "k_scales", "v_scales")]
+
+
+class RopeFrequencies(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("rot", "scaling", "original", "reserved")]
+                + [(n, ctypes.c_double) for n in ("base", "factor", "low", "high")]
+                + [("given", ctypes.POINTER(ctypes.c_double))])
+
+
+class RopeSpecC(ctypes.Structure):
+    _fields_ = ([(n, P) for n in ("turns", "q_gain", "k_gain")]
+                + [(n, ctypes.c_int32) for n in ("rot", "layout", "norm")]
+                + [(n, ctypes.c_float) for n in ("eps", "gain_offset", "magnitude")])
+
+
+class RopeShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "Hq", "Hk", "D", "q_stride", "k_stride", "qo_stride", "ko_stride")]
+
+
+class PagedShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "Hq", "Hkv", "D", "page", "n_pages", "max_pages", "tree_words",
+                                              "q_stride", "kv_stride")]
+
+
+class PagedCacheC(ctypes.Structure):
+    _fields_ = [(n, P) for n in ("k_pages", "v_pages", "tables")]
 
 
 class QMat(ctypes.Structure):
@@ -125,6 +152,18 @@ def lib() -> ctypes.CDLL:
         L.moe_kv8_attn_test_stall.argtypes = [kp, P, cp, P, P, ctypes.c_float, P, P, sz, i32, ctypes.c_int64, P]
         for f in ("moe_kv8_write", "moe_kv8_read", "moe_kv8_workspace_bytes", "moe_kv8_attn",
                   "moe_kv8_attn_test_stall"):
+            getattr(L, f).restype = i32
+        fp, sp_, hp = ctypes.POINTER(RopeFrequencies), ctypes.POINTER(RopeSpecC), ctypes.POINTER(RopeShape)
+        L.moe_rope_table.argtypes = [fp, ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_float)]
+        L.moe_rope.argtypes = [hp, sp_, P, P, P, P, P, P]
+        pp, qp = ctypes.POINTER(PagedShape), ctypes.POINTER(PagedCacheC)
+        L.moe_paged_append.argtypes = [pp, sp_, P, P, P, P, P, P, qp, P, P, P]
+        L.moe_paged_workspace_bytes.argtypes = [pp, ctypes.POINTER(sz)]
+        L.moe_paged_attn.argtypes = [pp, P, qp, P, P, P, ctypes.c_float, P, P, sz, P]
+        L.moe_paged_attn_test_stall.argtypes = [pp, P, qp, P, P, P, ctypes.c_float, P, P, sz, i32, ctypes.c_int64, P]
+        L.moe_paged_keep.argtypes = [pp, qp, P, P, P, i32, P, P, P]
+        for f in ("moe_rope_table", "moe_rope", "moe_paged_append", "moe_paged_workspace_bytes", "moe_paged_attn",
+                  "moe_paged_attn_test_stall", "moe_paged_keep"):
             getattr(L, f).restype = i32
         for f in ("moe_workspace_bytes", "moe_max_tiles", "moe_route_blocks", "moe_route", "moe_forward",
                   "moe_forward_timed", "moe_forward_residual",
@@ -552,3 +591,291 @@ def kv8_attn_test_stall(shape, q, cache: Kv8Cache, offsets, lens, o, workspace, 
                                          shape.D ** -0.5 if scale is None else scale, _ptr(o), _ptr(workspace),
                                          workspace.numel(), int(stalled_block), int(timeout_ns), _stream(stream)),
            "moe_kv8_attn_test_stall")
+
+
+# ----------------------------------------------------- rotary positions ---
+
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BANDS, ROPE_RAMP = 0, 1, 2, 3
+ROPE_HALF, ROPE_PAIRS = 0, 1
+ROPE_NORM_Q, ROPE_NORM_K, ROPE_NORM_QK = 1, 2, 3
+_I64 = torch.int64
+
+
+def _usual(t, dtype, dims, strides, dev) -> bool:
+    """The quick test of a call's tensor; _kv8_tensor says what is wrong (or
+    that nothing is: strides of dimensions of one element are any)."""
+    return t.dtype is dtype and t.shape == dims and t.stride() == strides and t.get_device() == dev
+
+
+class RopeTable:
+    """The turns per position of rot / 2 pairs (.turns, an int64 tensor of
+    64-bit fixed-point fractions) and the .magnitude of their scaling."""
+
+    __slots__ = ("turns", "rot", "magnitude")
+
+    def __init__(self, turns, magnitude):
+        self.turns, self.rot, self.magnitude = turns, 2 * turns.numel(), magnitude
+
+
+def rope_table(rot, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, original=0, low=1.0, high=None, freqs=None,
+               device="cuda") -> RopeTable:
+    """moe_rope_table: the frequencies base^(-2 i / rot), or `freqs` (rot / 2
+    radians per position), scaled for long contexts (include/rope.h), on
+    `device`. high: 4 turns for ROPE_BANDS, 32 for ROPE_RAMP unless given."""
+    w = "moe_rope_table"
+    if high is None:
+        high = 32.0 if scaling == ROPE_RAMP else 4.0
+    given = None
+    if freqs is not None:
+        values = [float(v) for v in freqs]
+        if len(values) != rot // 2:
+            _kv8_refuse(w, f"{len(values)} frequencies for {rot // 2} pairs")
+        given = (ctypes.c_double * len(values))(*values)
+    f = RopeFrequencies(rot, scaling, original, 0, base, factor, low, high, given)
+    turns, magnitude = (ctypes.c_uint64 * 128)(), ctypes.c_float()
+    _check(lib().moe_rope_table(ctypes.byref(f), turns, ctypes.byref(magnitude)), w)
+    signed = [v - (1 << 64) if v >> 63 else v for v in turns[:rot // 2]]
+    return RopeTable(torch.tensor(signed, dtype=_I64, device=device), magnitude.value)
+
+
+class RopeSpec:
+    """How heads are normed and rotated; made by rope_spec, which checks its
+    tensors once. They belong to the spec from then on."""
+
+    __slots__ = ("_c", "_t", "_dev", "_D")
+
+
+def rope_spec(table: RopeTable = None, layout=ROPE_HALF, norm=0, q_gain=None, k_gain=None, eps=1e-6, gain_offset=0.0,
+              magnitude=None) -> RopeSpec:
+    """table: None for no rotation. norm: ROPE_NORM_Q, ROPE_NORM_K or both
+    (ROPE_NORM_QK), with gains bf16 [D] (None: 1) to which gain_offset is added.
+    magnitude: the table's unless given."""
+    w = "moe_rope"
+    turns = None if table is None else table.turns
+    dev, D = None, None
+    for name, t in (("turns", turns), ("q_gain", q_gain), ("k_gain", k_gain)):
+        if t is None:
+            continue
+        dev = t.get_device() if dev is None else dev
+        n = t.numel()
+        if name != "turns":
+            D = n if D is None else D
+        _kv8_tensor(w, name, t, dev, _I64 if name == "turns" else _BF16, (n if name == "turns" else D,), (1,))
+    s = RopeSpec()
+    s._c = RopeSpecC(_ptr(turns), _ptr(q_gain), _ptr(k_gain), 0 if table is None else table.rot, layout, norm, eps,
+                     gain_offset, (1.0 if table is None else table.magnitude) if magnitude is None else magnitude)
+    s._t, s._dev, s._D = (turns, q_gain, k_gain), dev, D
+    return s
+
+
+def _spec_fits(where, spec, D, dev):
+    if (spec._D is not None and spec._D != D) or (spec._dev is not None and spec._dev != dev):
+        _kv8_refuse(where, f"the spec's tensors are for heads of {spec._D} on cuda:{spec._dev}, not {D} on cuda:{dev}")
+
+
+_rope_fields = struct.Struct("8i").unpack
+
+
+def rope_shape(T, Hq, Hk, D, q_stride=0, k_stride=0, qo_stride=0, ko_stride=0) -> RopeShape:
+    """T tokens with Hq query and Hk key heads (either may be 0). Strides:
+    elements between tokens of q, k, q_out, k_out (0: packed)."""
+    return RopeShape(T, Hq, Hk, D, q_stride, k_stride, qo_stride, ko_stride)
+
+
+def rope(shape, spec: RopeSpec, q, k, positions, q_out, k_out, stream=None):
+    """moe_rope: q bf16 [T, Hq, D] and k bf16 [T, Hk, D] normed and rotated by
+    positions (int32 [T]) into q_out and k_out, which may be q and k."""
+    w = "moe_rope"
+    T, Hq, Hk, D, qs, ks, qos, kos = _rope_fields(shape)
+    dev = (q if Hq else k).get_device()
+    if dev < 0 or _current_device() != dev:
+        _kv8_refuse(w, f"{'q' if Hq else 'k'} is not on the current device")
+    if (spec._D or D) != D or (spec._dev if spec._dev is not None else dev) != dev:
+        _spec_fits(w, spec, D, dev)
+    if Hq:
+        dims = (T, Hq, D)
+        if not _usual(q, _BF16, dims, (qs or Hq * D, D, 1), dev):
+            _kv8_tensor(w, "q", q, dev, _BF16, dims, (qs or Hq * D, D, 1))
+        if not _usual(q_out, _BF16, dims, (qos or Hq * D, D, 1), dev):
+            _kv8_tensor(w, "q_out", q_out, dev, _BF16, dims, (qos or Hq * D, D, 1))
+    if Hk:
+        dims = (T, Hk, D)
+        if not _usual(k, _BF16, dims, (ks or Hk * D, D, 1), dev):
+            _kv8_tensor(w, "k", k, dev, _BF16, dims, (ks or Hk * D, D, 1))
+        if not _usual(k_out, _BF16, dims, (kos or Hk * D, D, 1), dev):
+            _kv8_tensor(w, "k_out", k_out, dev, _BF16, dims, (kos or Hk * D, D, 1))
+    if positions is not None and not _usual(positions, _I32, (T,), (1,), dev):
+        _kv8_tensor(w, "positions", positions, dev, _I32, (T,), (1,))
+    rc = lib().moe_rope(shape, spec._c, q.data_ptr() if Hq else None, k.data_ptr() if Hk else None, _ptr(positions),
+                        q_out.data_ptr() if Hq else None, k_out.data_ptr() if Hk else None,
+                        _current_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        _check(rc, w)
+
+
+# -------------------------------------------------------- paged KV cache ---
+
+def paged_shape(B, T, Hq, Hkv, D, page, n_pages, max_pages, tree_words=0, q_stride=0, kv_stride=0) -> PagedShape:
+    """A call over B sequences with T packed tokens in all, on pools of n_pages
+    pages of `page` positions; max_pages: entries of a sequence's row of the
+    table. tree_words: 64-bit words of a draft's mask (0: causal). Strides as in
+    kv8_shape."""
+    return PagedShape(B, T, Hq, Hkv, D, page, n_pages, max_pages, tree_words, q_stride, kv_stride)
+
+
+_paged_fields = struct.Struct("11i").unpack
+
+
+class PagedCache:
+    """Pools of pages bf16 [n_pages, Hkv, page, D] and the table int32 [B,
+    max_pages] of the pages of every sequence's positions, contiguous, on one
+    device. Checked here, once; the contents are the caller's to change."""
+
+    __slots__ = ("k", "v", "tables", "_c", "_dims", "_tdims", "_dev")
+
+    def __init__(self, k, v, tables):
+        w = "PagedCache"
+        if k.dim() != 4 or tables.dim() != 2:
+            _kv8_refuse(w, f"k has shape {tuple(k.shape)}, tables {tuple(tables.shape)}: pages are [n_pages, Hkv, page, "
+                           "D], tables [B, max_pages]")
+        dims, tdims, dev = tuple(k.shape), tuple(tables.shape), k.get_device()
+        strides = (dims[1] * dims[2] * dims[3], dims[2] * dims[3], dims[3], 1)
+        self._c = PagedCacheC(_kv8_tensor(w, "k", k, dev, _BF16, dims, strides),
+                              _kv8_tensor(w, "v", v, dev, _BF16, dims, strides),
+                              _kv8_tensor(w, "tables", tables, dev, _I32, tdims, (tdims[1], 1)))
+        self.k, self.v, self.tables = k, v, tables
+        self._dims, self._tdims, self._dev = dims, tdims, dev
+
+    def _device(self, where, f):
+        """Refuses a cache that is not one of the shape on the current device."""
+        if self._dims != (f[6], f[3], f[5], f[4]) or self._tdims != (f[0], f[7]):
+            _kv8_refuse(where, f"the cache holds pages {self._dims} and tables {self._tdims}, the shape says otherwise")
+        if self._dev < 0 or self._dev != torch.cuda.current_device():
+            _kv8_refuse(where, f"the cache is on {self.k.device}, not on the current device")
+
+
+def paged_alloc_cache(shape: PagedShape, device) -> PagedCache:
+    """Empty pools for `shape` and a table of zeros (the pages need no
+    initialisation; the table is the caller's to fill)."""
+    pages = [torch.empty(shape.n_pages, shape.Hkv, shape.page, shape.D, dtype=_BF16, device=device) for _ in range(2)]
+    return PagedCache(*pages, torch.zeros(shape.B, shape.max_pages, dtype=_I32, device=device))
+
+
+def paged_append(shape, spec, q, k_new, v_new, offsets, starts, cache: PagedCache, q_out=None, positions=None,
+                 status=None, stream=None):
+    """moe_paged_append: k_new, v_new bf16 [T, Hkv, D] to positions starts[b] ..
+    of every sequence (offsets int32 [B+1], starts int32 [B]), keys normed and
+    rotated by `spec` (None: as they are) at positions[t] (int32 [T]; None:
+    where they go); q bf16 [T, Hq, D], or None, alongside into q_out. status: an
+    optional zeroed int32 device word."""
+    w = "moe_paged_append"
+    f = _paged_fields(shape)
+    B, T, Hq, H, D, page, n, mp, _, qs, kvs = f
+    dev, dims, strides = cache._dev, (T, H, D), (kvs or H * D, D, 1)
+    if not (cache._dims == (n, H, page, D) and cache._tdims == (B, mp) and dev >= 0 and _current_device() == dev):
+        cache._device(w, f)
+    if spec is not None and ((spec._D or D) != D or (spec._dev if spec._dev is not None else dev) != dev):
+        _spec_fits(w, spec, D, dev)
+    if q is not None:
+        if q_out is None:
+            _kv8_refuse(w, "q without q_out")
+        if not _usual(q, _BF16, (T, Hq, D), (qs or Hq * D, D, 1), dev):
+            _kv8_tensor(w, "q", q, dev, _BF16, (T, Hq, D), (qs or Hq * D, D, 1))
+        if not _usual(q_out, _BF16, (T, Hq, D), (Hq * D, D, 1), dev):
+            _kv8_tensor(w, "q_out", q_out, dev, _BF16, (T, Hq, D), (Hq * D, D, 1))
+    if not _usual(k_new, _BF16, dims, strides, dev):
+        _kv8_tensor(w, "k_new", k_new, dev, _BF16, dims, strides)
+    if not _usual(v_new, _BF16, dims, strides, dev):
+        _kv8_tensor(w, "v_new", v_new, dev, _BF16, dims, strides)
+    if not _usual(offsets, _I32, (B + 1,), (1,), dev):
+        _kv8_tensor(w, "offsets", offsets, dev, _I32, (B + 1,), (1,))
+    if not _usual(starts, _I32, (B,), (1,), dev):
+        _kv8_tensor(w, "starts", starts, dev, _I32, (B,), (1,))
+    if positions is not None and not _usual(positions, _I32, (T,), (1,), dev):
+        _kv8_tensor(w, "positions", positions, dev, _I32, (T,), (1,))
+    rc = lib().moe_paged_append(shape, None if spec is None else spec._c, None if q is None else q.data_ptr(),
+                                k_new.data_ptr(), v_new.data_ptr(), offsets.data_ptr(), starts.data_ptr(),
+                                None if positions is None else positions.data_ptr(), cache._c,
+                                None if q is None else q_out.data_ptr(),
+                                None if status is None else _kv8_tensor(w, "status", status, dev, _I32, (1,), (1,)),
+                                _current_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        _check(rc, w)
+
+
+def paged_workspace_bytes(shape: PagedShape) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().moe_paged_workspace_bytes(ctypes.byref(shape), ctypes.byref(n)), "moe_paged_workspace_bytes")
+    return n.value
+
+
+def paged_alloc_workspace(shape: PagedShape, device) -> torch.Tensor:
+    return torch.empty(paged_workspace_bytes(shape), dtype=torch.uint8, device=device)
+
+
+def paged_attn(shape, q, cache: PagedCache, offsets, lens, o, workspace, tree=None, scale=None, stream=None):
+    """moe_paged_attn: q bf16 [T, Hq, D], the last tokens of every sequence
+    (offsets int32 [B+1]) over its lens[b] cached positions (int32 [B]); o bf16
+    [T, Hq, D]. tree: int64 [T, tree_words], the bits of the drafts that each
+    query sees (bit d % 64 of word d / 64), with shape.tree_words > 0. The
+    workspace's first int32 is the call's device status word."""
+    w = "moe_paged_attn"
+    f = _paged_fields(shape)
+    B, T, H, Hkv, D, page, n, mp, words, stride, _ = f
+    dev, dims, strides, size = cache._dev, (T, H, D), (stride or H * D, D, 1), workspace.numel()
+    if not (cache._dims == (n, Hkv, page, D) and cache._tdims == (B, mp) and dev >= 0 and _current_device() == dev):
+        cache._device(w, f)
+    if not _usual(q, _BF16, dims, strides, dev):
+        _kv8_tensor(w, "q", q, dev, _BF16, dims, strides)
+    if not _usual(offsets, _I32, (B + 1,), (1,), dev):
+        _kv8_tensor(w, "offsets", offsets, dev, _I32, (B + 1,), (1,))
+    if not _usual(lens, _I32, (B,), (1,), dev):
+        _kv8_tensor(w, "lens", lens, dev, _I32, (B,), (1,))
+    if not _usual(o, _BF16, dims, (H * D, D, 1), dev):
+        _kv8_tensor(w, "o", o, dev, _BF16, dims, (H * D, D, 1))
+    if tree is not None and not _usual(tree, _I64, (T, words), (words, 1), dev):
+        _kv8_tensor(w, "tree", tree, dev, _I64, (T, words), (words, 1))
+    if not (workspace.dtype is torch.uint8 and workspace.is_contiguous() and workspace.get_device() == dev):
+        _kv8_tensor(w, "workspace", workspace, dev, torch.uint8, (size,), (1,))
+    rc = lib().moe_paged_attn(shape, q.data_ptr(), cache._c, offsets.data_ptr(), lens.data_ptr(),
+                              None if tree is None else tree.data_ptr(), D ** -0.5 if scale is None else scale,
+                              o.data_ptr(), workspace.data_ptr(), size,
+                              _current_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        _check(rc, w)
+
+
+def paged_attn_test_stall(shape, q, cache: PagedCache, offsets, lens, o, workspace, stalled_block: int, timeout_ns: int,
+                          tree=None, scale=None, stream=None):
+    """moe_paged_attn_test_stall: paged_attn with one grid block that never
+    brings its keys and values and a short device timeout (test only)."""
+    _check(lib().moe_paged_attn_test_stall(shape, _ptr(q), cache._c, _ptr(offsets), _ptr(lens), _ptr(tree),
+                                           shape.D ** -0.5 if scale is None else scale, _ptr(o), _ptr(workspace),
+                                           workspace.numel(), int(stalled_block), int(timeout_ns), _stream(stream)),
+           "moe_paged_attn_test_stall")
+
+
+def paged_keep(shape, cache: PagedCache, starts, kept, path, lens_out=None, status=None, stream=None):
+    """moe_paged_keep: of every sequence, the drafts path[b, :kept[b]] (int32
+    [B, width], increasing) at positions starts[b] + path[b, k] move to starts[b]
+    + k; lens_out[b] = starts[b] + kept[b]. starts, kept, lens_out int32 [B]."""
+    w = "moe_paged_keep"
+    f = _paged_fields(shape)
+    B, _, _, H, D, page, n, mp, _, _, _ = f
+    dev, width = cache._dev, path.shape[-1]
+    if not (cache._dims == (n, H, page, D) and cache._tdims == (B, mp) and dev >= 0 and _current_device() == dev):
+        cache._device(w, f)
+    if not _usual(starts, _I32, (B,), (1,), dev):
+        _kv8_tensor(w, "starts", starts, dev, _I32, (B,), (1,))
+    if not _usual(kept, _I32, (B,), (1,), dev):
+        _kv8_tensor(w, "kept", kept, dev, _I32, (B,), (1,))
+    if not _usual(path, _I32, (B, width), (width, 1), dev):
+        _kv8_tensor(w, "path", path, dev, _I32, (B, width), (width, 1))
+    if lens_out is not None and not _usual(lens_out, _I32, (B,), (1,), dev):
+        _kv8_tensor(w, "lens_out", lens_out, dev, _I32, (B,), (1,))
+    rc = lib().moe_paged_keep(shape, cache._c, starts.data_ptr(), kept.data_ptr(), path.data_ptr(), width,
+                              None if lens_out is None else lens_out.data_ptr(),
+                              None if status is None else _kv8_tensor(w, "status", status, dev, _I32, (1,), (1,)),
+                              _current_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        _check(rc, w)

@@ -1,0 +1,1152 @@
+// Attention over the paged bf16 cache (include/paged.h): causal, or for trees
+// of drafts, from one query token per sequence to whole prompts, on the
+// 5th-generation tensor cores, sm_103a.
+//
+// A row is one (query token, query head of a KV head); a row tile is 128
+// consecutive rows of one (sequence, KV head), or 256 on a pair of blocks. The
+// positions that a tile's last row sees are cut into units of 128, and all
+// units of the call, laid end to end in the order (sequence, KV head, row tile,
+// position), are dealt out in equal contiguous runs, one per block (per pair)
+// of a grid with a block on every SM (kv8_attn.h has the arithmetic). A tile that
+// lies in one run is finished there; one that a run's border cuts leaves partial
+// states (m, L, O) in the workspace, at most two per run, which
+// paged_merge_kernel joins in a fixed order.
+//
+// Per unit and 128 rows, 4 * 128 * 128 * D flops:
+//   S = Q K^T  N = 128 positions, both operands in shared memory, S in TMEM;
+//   P = 2^(scale log2(e) (S - m)) in bf16, written over S in TMEM;
+//   O += P V   N = D, A = P from TMEM, B = V from shared memory as it lies in
+//              its page, position by position (an MN-major operand)
+// S is double buffered, so the product S of the next unit runs while the softmax
+// of this one is computed (TMEM: D columns of O, 2 x 128 of S).
+//
+// One row or 128: a product costs the same, and its 2 x 1024 cycles of a unit at
+// D = 256 are less than half of what its 128 KB take to come from HBM. So a
+// single token of a sequence runs here, too, with the rows that are not there
+// left out of the softmax and of the partial states.
+//
+// Warp roles (512 threads):
+//   warps 0-7    softmax: a thread has one row (TMEM lane) and half of the unit's
+//                positions, which stay in registers from the maximum to the
+//                weights; the two halves' maxima meet in shared memory. At a
+//                tile's end, half of the output row each
+//   warps 8-11   Q into shared memory; values of V that no row, or not every row,
+//                sees and that are no finite numbers out of it (0 * NaN is NaN)
+//   warp 12      TMEM allocation; the MMA-issuing thread (of a pair, the first
+//                block's; the other block's warp tells it what is ready there)
+//   warp 13      K and V by TMA, a box per page and 64 head dims: page numbers from
+//                the table one unit ahead, positions past the context as zeros
+//   warp 14      per unit, its place in shared memory for the softmax
+// The ring's stages (16 KB) hold K of a unit in D / 64 parts by head dims and V in
+// as many by positions (half as many per block of a pair, which holds half of
+// the positions of K and half of the head dims of V), in the order of their use.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <type_traits>
+
+#include "kernels.h"
+#include "kv8_attn.h"
+#include "paged.cuh"
+#include "tiles_ptx.cuh"
+
+namespace bgmoe {
+namespace paged {
+
+using namespace tc;
+using kv8::empty_tiles;
+using kv8::find_run;
+using kv8::Place;
+using kv8::seq_tiles;
+using kv8::tile_units;
+
+constexpr int kRows = 128;  // rows of a block (TMEM lanes)
+constexpr int kKeys = 128;  // positions of a unit
+constexpr int kStages = 8;
+constexpr int kStageBytes = 16384;
+constexpr int kSoftWarps = 8, kAuxWarps = 4;
+constexpr int kMmaWarp = 12, kLoadWarp = 13, kNoteWarp = 14;
+constexpr int kThreads = 512;
+constexpr int kMaxCtas = 256;  // workspace bound on the grid
+// A run also pays for every tile it begins (Q, the first unit's chain, the
+// output): the runs are cut on a scale where a tile with units takes kTileCost
+// more places than units, before its first.
+constexpr int kTileCost = 3;
+constexpr float kMinusBig = -3.402823466e38f;  // running-max start, finite: m - m_new is never NaN
+constexpr float kSlack = 8.f;                  // a row's scores may pass its m by this much (base 2): weights to 2^8
+// x a - m a is computed in one step, so m a's own rounding, half an fp32 step,
+// is in all of a row's weights: up to here 2^-4 of a power of two. Rows past it
+// take two, the difference first.
+constexpr float kLargeScore = 1048576.f;  // 2^20
+constexpr uint32_t kColS = 256;           // S buffers at columns 256 and 384, O from 0
+constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);  // A and B format in an instruction descriptor
+
+template <int D, int kCtas>
+struct Cfg {
+  static constexpr int kTileRows = kRows * kCtas;     // MMA M
+  static constexpr int kParts = D / 64 / kCtas;       // stages of a unit's K, and of its V
+  static constexpr int kKeyRows = kKeys / kCtas;      // positions of K in a block ...
+  static constexpr int kSlabsK = kCtas;               // ... in a stage, of 64 head dims each
+  static constexpr int kDimsV = D / kCtas;            // head dims of V in a block ...
+  static constexpr int kKeysV = kKeys / kParts;       // ... and positions of it in a stage
+  static constexpr int kQBytes = kRows * D * 2;
+  static constexpr int kOutPitch = 80;                // bytes: 32 bf16 and padding
+  static constexpr int kOutOffset = kQBytes + kStages * kStageBytes;
+  static constexpr int kCtlOffset = kOutOffset + kSoftWarps * 32 * kOutPitch;
+  static constexpr int kBytes = kCtlOffset + 4096 + 1024;  // + alignment slack
+  static_assert(kKeyRows * kSlabsK * 128 == kStageBytes && kKeysV * kDimsV * 2 == kStageBytes, "stages");
+  static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+struct UnitNote {
+  int4 tile;   // lo, n, len, g of its sequence and head
+  int4 place;  // first position, row tile, is the tile's last, 0
+};
+constexpr int kNotes = 4;
+
+// Positions of a tile whose V is not finite, of those that not every row sees,
+// as bits per unit from the first that has some. There are less than 257 of
+// them (causal) or 513 (trees), so at most 6 units. Four tiles' bits: while
+// the softmax ends tile t, V of t + 3 may come (S of t + 2 waits for the O of t
+// + 1, which waits until O of t has been read); the MMA warp clears a tile's
+// bits once its O has been read.
+constexpr int kBadTiles = 4, kBadUnits = 8;
+
+struct Ctl {
+  UnitNote note[kNotes];
+  uint64_t note_full[kNotes], note_empty[kNotes];
+  uint64_t full[kStages], empty[kStages];
+  // V of a unit that is to be looked through has come; it has been. The MMA
+  // warp, which sees every phase of the stages, says the one and waits for the
+  // other (a warp that skipped phases could take one for another).
+  uint64_t look, fixed;
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_full[2];
+  // One arrival per unit, on alternate barriers. A waiter's parity is safe if
+  // it cannot be two phases off: the softmax of unit u has seen S of unit u,
+  // whose commit covers the products of u - 2, and those of u + 1 and u + 2
+  // wait for its weights.
+  uint64_t pv_done[2];
+  uint64_t o_empty;               // O of a finished tile has been read
+  uint64_t peer_s[2], peer_o[2];  // the other block is ready for a unit's S, for its O
+  uint64_t mx_full[4];            // both halves of a lane quadrant have stored their maxima (or sums)
+  uint64_t mma_done;
+  uint32_t tmem;
+  int abort;
+  int bad_page;
+  int bad_any[kBadTiles];
+  uint32_t bad[kBadTiles][kBadUnits][kKeys / 32];
+  float mx[2][2][kRows];  // [unit parity][half]
+};
+
+// Where a block's run starts, for the merge kernel.
+struct RunInfo {
+  int tile;  // number of its first unit's tile
+  int live;  // the run has units
+  int b, g, rt, i;
+};
+
+struct Params {
+  const uint16_t* q;
+  const int32_t* offsets;
+  const int32_t* lens;
+  const int32_t* tables;
+  const unsigned long long* tree;  // null: causal
+  uint16_t* o;
+  float* part;    // two slots per run of [tile rows][D] O, then [tile rows] m and L
+  RunInfo* info;  // per run
+  int32_t* flags;  // per block
+  float scale_log2;
+  int B, T, Hq, Hkv, shift, n_pages, max_pages, words, q_stride;
+  unsigned long long rmagic;  // ceil(2^36 / r), r = Hq / Hkv
+  int stalled;
+  long long timeout_ns;
+};
+
+// x / r for rows x < n r of n <= 2^24 tokens and r <= 64: with the magic off by
+// less than r / r from 2^36 / r, x (magic - 2^36 / r) < 2^30 < 2^36 / r keeps the
+// floor, and x magic < 2^24 (2^36 + r) stays in 64 bits.
+__device__ __forceinline__ int div_r(int x, unsigned long long rmagic) {
+  return (int)(((unsigned long long)(unsigned)x * rmagic) >> 36);
+}
+
+constexpr size_t slot_floats(int D, int tile_rows) { return (size_t)tile_rows * (D + 2); }
+
+// Place in the run: unit i of the nb units of row tile rt of KV head g of
+// sequence b.
+struct Cursor {
+  int b, g, rt, i, nb, n, len, lo;
+  __device__ void sequence(const Params& p) {
+    lo = ld(p.offsets + b);
+    n = ld(p.offsets + b + 1) - lo;
+    len = ld(p.lens + b);
+  }
+  __device__ bool last() const { return i == nb - 1; }
+  __device__ void advance(const Params& p, int r, int RT) {
+    if (++i < nb) return;
+    i = 0;
+    do {
+      if (++rt >= seq_tiles(n, r, RT)) {
+        rt = 0;
+        if (++g >= p.Hkv) {
+          g = 0;
+          do {
+            if (++b >= p.B) return;
+            sequence(p);
+          } while (n == 0);
+        }
+      }
+      nb = tile_units(n, len, r, RT, kKeys, rt);
+    } while (nb == 0);
+  }
+  // The tile's first position that some row does not see.
+  __device__ int partial(const Params& p, int RT) const {
+    return max(len - n + (p.tree != nullptr ? 0 : div_r(rt * RT, p.rmagic) + 1), 0);
+  }
+  // V of the unit is looked through.
+  __device__ bool fix(const Params& p, int RT) const { return (i + 1) * kKeys > partial(p, RT); }
+};
+
+// Places in the ring, in units of a K or V block: S of unit u + 1 goes before O
+// of unit u unless u ends a tile or the run (`ahead`).
+__device__ __forceinline__ int place_k(int u, bool ahead_before) { return 2 * u - (ahead_before ? 1 : 0); }
+__device__ __forceinline__ int place_v(int u, bool ahead) { return 2 * u + 1 + (ahead ? 1 : 0); }
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// *at |= bits in this block's and (of a pair) the other's shared memory, in
+// front of what this thread releases after it.
+template <int kCtas>
+__device__ __forceinline__ void or_both(uint32_t* at, uint32_t bits, int rank) {
+  atomicOr(at, bits);
+  if (kCtas == 2) {
+    asm volatile(
+        "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, %1;\n red.relaxed.cluster.shared::cluster.or.b32 [a], %2;\n}\n" ::
+            "r"(smem_u32(at)),
+        "r"(rank ^ 1), "r"(bits)
+        : "memory");
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  }
+}
+
+__device__ __forceinline__ unsigned long long ld_u64(const unsigned long long* p) {
+  unsigned long long v;
+  asm volatile("ld.global.b64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// Bits of the 64 positions from `first` on that the tree lets a draft see,
+// whose words are at w: all of the context's (before ctx), then its own.
+__device__ __forceinline__ uint64_t tree_bits(const unsigned long long* w, int words, int first, int ctx) {
+  const int j = first - ctx;
+  if (j <= -64) return ~0ull;
+  if (j < 0) return (ld_u64(w) << -j) | ((1ull << -j) - 1);
+  const int k = j >> 6, s = j & 63;
+  uint64_t v = k < words ? ld_u64(w + k) >> s : 0ull;
+  if (s > 0 && k + 1 < words) v |= ld_u64(w + k + 1) << (64 - s);
+  return v;
+}
+
+template <int D, int kCtas>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const Params p) {
+  using F = Cfg<D, kCtas>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;               // 64-dim slabs of 128 rows x 128 bytes
+  uint8_t* sR = smem + F::kQBytes;  // the ring
+  constexpr int kTileRows = F::kTileRows;
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + F::kCtlOffset);
+  static_assert(sizeof(Ctl) <= 4096, "control block");
+  __shared__ long long s_unit[2];  // units before the run's start and end
+  __shared__ Cursor s_cur;
+  __shared__ int s_bad, s_tile;
+
+  // The warp's number through a shuffle, which the compiler knows to be
+  // uniform: the roles' loops then run on uniform registers, where the MMA
+  // instructions take their descriptors from.
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int C = gridDim.x / kCtas, c = blockIdx.x / kCtas, rank = blockIdx.x % kCtas;  // runs, run, block of its tiles
+  const int r = p.Hq / p.Hkv;
+
+  if (threadIdx.x == 32) {
+    mbar_init(&ctl->q_full, kAuxWarps);
+    mbar_init(&ctl->q_empty, 1);
+    for (int i = 0; i < kNotes; ++i) {
+      mbar_init(&ctl->note_full[i], 1);
+      mbar_init(&ctl->note_empty[i], kSoftWarps);
+    }
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&ctl->full[s], 1);
+      mbar_init(&ctl->empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->s_full[i], 1);
+      mbar_init(&ctl->p_full[i], kSoftWarps);
+      mbar_init(&ctl->pv_done[i], 1);
+      mbar_init(&ctl->peer_s[i], 1);
+      mbar_init(&ctl->peer_o[i], 1);
+    }
+    mbar_init(&ctl->o_empty, kSoftWarps);
+    for (int i = 0; i < 4; ++i) mbar_init(&ctl->mx_full[i], 2);
+    mbar_init(&ctl->look, 1);
+    mbar_init(&ctl->fixed, kAuxWarps);
+    mbar_init(&ctl->mma_done, 1);
+    ctl->abort = 0;
+    ctl->bad_page = 0;
+    fence_barrier_init();
+  }
+  if (warp == kAuxWarps + kSoftWarps - 1) {
+    uint32_t* z = &ctl->bad[0][0][0];
+    for (int i = lane; i < kBadTiles * kBadUnits * (kKeys / 32); i += 32) z[i] = 0u;
+    if (lane < kBadTiles) ctl->bad_any[lane] = 0;
+  }
+  // Launched with programmatic dependent launch: wait for the kernels before
+  // this one, then let this call's merge launch (it waits in turn).
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (warp == 1 || warp == 2) {  // the run's start and its end
+    Place k;
+    const bool ok = find_run(p.offsets, p.lens, p.B, p.T, p.Hkv, p.max_pages << p.shift, r, kTileRows, kKeys, kTileCost,
+                             c + warp - 1, C, &k);
+    if (lane == 0) {
+      s_unit[warp - 1] = k.units;
+      if (warp == 1) {
+        s_bad = !ok;
+        Cursor cur{};
+        if (ok && k.b >= 0) {
+          cur.b = k.b;
+          cur.lo = k.lo;
+          cur.n = k.n;
+          cur.len = k.len;
+          cur.g = k.g;
+          cur.rt = k.rt;
+          cur.i = k.i;
+          cur.nb = k.nb;
+        }
+        s_cur = cur;
+        s_tile = k.tile;
+      }
+    }
+  }
+  int wide = 0;  // a sequence has more drafts than its words have bits
+  if (p.tree != nullptr && warp > 2)
+    for (int b = threadIdx.x - 96; b < p.B; b += kThreads - 96)
+      wide |= ld(p.offsets + b + 1) - ld(p.offsets + b) > 64 * p.words;
+  if (__syncthreads_or(wide)) {
+    if (threadIdx.x == 0) s_bad = 1;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    const bool live = !s_bad && s_unit[0] < s_unit[1];
+    if (rank == 0) p.info[c] = RunInfo{s_tile, live, s_cur.b, s_cur.g, s_cur.rt, s_cur.i};
+    if (!live) p.flags[blockIdx.x] = s_bad ? (int32_t)MOE_ERR_INVALID_ARG : 0;
+  }
+  if (s_bad) return;
+  // Queries that see nothing (more queries than positions): o = 0.
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    const int lo = ld(p.offsets + b), hi = ld(p.offsets + b + 1), len = ld(p.lens + b);
+    const size_t pieces = (size_t)max(0, hi - lo - len) * p.Hq * (D / 8);
+    uint4* z = reinterpret_cast<uint4*>(p.o + (size_t)lo * p.Hq * D);
+    for (size_t i = threadIdx.x; i < pieces; i += kThreads) z[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  if (s_unit[0] >= s_unit[1]) return;  // both blocks of a run alike
+  if (warp == kMmaWarp) alloc_columns<kCtas>(&ctl->tmem);
+  tc_fence_before();
+  tile_barrier<kCtas>();  // the barriers and the columns of both blocks are there
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+  const int U = (int)(s_unit[1] - s_unit[0]);
+  Cursor cur = s_cur;
+
+  volatile int* abort_flag = &ctl->abort;
+  // Each wait has its own limit (a long call may run for longer than one), set
+  // only where the phase has not completed already.
+  auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    bool ok = mbar_test_wait(bar, parity);
+    if (!ok) ok = mbar_wait(bar, parity, abort_flag, global_timer_ns() + (uint64_t)p.timeout_ns);
+    return __all_sync(0xffffffffu, ok) != 0;
+  };
+  // Stage h of the block at a place of the ring, and its phase there.
+  auto stage = [](int place, int h) { return (place * F::kParts + h) % kStages; };
+  auto phase = [](int place, int h) { return (uint32_t)((place * F::kParts + h) / kStages) & 1u; };
+
+  if (warp == kMmaWarp) {
+    // ------------------------------------------------------- MMA issuer
+    // With two blocks the leader's warp issues for both; the other's goes
+    // through the same steps, waits for what its own block has to have ready
+    // and passes that on as one arrival.
+    constexpr uint32_t idesc_s = idesc_f16_f32(kTileRows, kKeys) | kBf16;
+    constexpr uint32_t idesc_o = idesc_f16_f32(kTileRows, D) | kBf16 | (1u << 16);  // B is MN-major
+    const uint64_t dq = sw128_desc(smem_u32(sQ));
+    const uint32_t leader = elect_one();
+    const uint64_t dk = sw128_desc(smem_u32(sR));
+    const uint64_t dv = sw128_mn_desc(smem_u32(sR), F::kKeysV * 128);
+    int tq = 0, to = 0;     // tiles whose Q has been waited for, whose O has been started
+    uint32_t fixes = 0u;    // units whose V was looked through
+    uint32_t fix = 0u, ahead = 0u;  // of units su - 1, su - 2, a bit each by parity
+    Cursor nxt = cur;
+    // Waits until a step of unit u may begin: its stages, the softmax's or Q's
+    // barrier `own` (if any), the other block's arrival; all tested together.
+    // The other block's warp passes its readiness on. (An arrival for unit u + 2
+    // comes after the leader's step of unit u: two barriers in turn will do.)
+    auto ready = [&](int place, int u, uint64_t* own, uint32_t parity, uint64_t* peer, bool fixed) -> bool {
+      bool all = own == nullptr || mbar_test_wait(own, parity);
+#pragma unroll
+      for (int h = 0; h < F::kParts; ++h) all = mbar_test_wait(&ctl->full[stage(place, h)], phase(place, h)) && all;
+      const bool listens = kCtas == 2 && rank == 0;
+      if (listens) all = test_cluster(peer, (u >> 1) & 1) && all;
+      if (fixed || !__all_sync(0xffffffffu, all)) {
+        for (int h = 0; h < F::kParts; ++h)
+          if (!warp_wait(&ctl->full[stage(place, h)], phase(place, h))) return false;
+        if (fixed && lane == 0) mbar_arrive(&ctl->look);
+        if (own != nullptr && !warp_wait(own, parity)) return false;
+        if (fixed && !warp_wait(&ctl->fixed, fixes++ & 1u)) return false;
+        if (listens && !warp_wait(peer, (u >> 1) & 1)) return false;
+        // (a test at cluster scope, for the fence below to follow on)
+        if (listens && !__all_sync(0xffffffffu, test_cluster(peer, (u >> 1) & 1))) return false;
+      }
+      tc_fence_after();
+      if (listens) acquire_peer();
+      if (kCtas == 2 && rank != 0) {
+        tc_fence_before();
+        if (lane == 0) arrive_leader(peer);
+      }
+      return true;
+    };
+    auto score = [&](int u, bool first, bool ends) -> bool {  // S of unit u
+      const int place = place_k(u, ahead >> ((u - 1) & 1) & 1u);
+      if (!ready(place, u, first ? &ctl->q_full : nullptr, tq & 1, &ctl->peer_s[u & 1], false)) return false;
+      tq += first;
+      if (rank != 0) return true;
+      const uint32_t d = tmem + kColS + 128 * (u & 1);
+#pragma unroll
+      for (int h = 0; h < F::kParts; ++h) {
+        const int st = stage(place, h);
+#pragma unroll
+        for (int kk = 0; kk < 4 * F::kSlabsK; ++kk) {
+          const uint32_t slab = kk >> 2, in = (kk & 3) * 2;  // 64-dim slabs
+          mma_ss<kCtas>(d, dq + (h * F::kSlabsK + slab) * (kRows * 128 / 16) + in,
+                        dk + st * (kStageBytes / 16) + slab * (F::kKeyRows * 128 / 16) + in, idesc_s, kk > 0 || h > 0,
+                        leader);
+        }
+        commit<kCtas>(&ctl->empty[st], leader);
+      }
+      commit<kCtas>(&ctl->s_full[u & 1], leader);
+      if (ends) commit<kCtas>(&ctl->q_empty, leader);
+      return true;
+    };
+    auto output = [&](int u, bool first) -> bool {  // O of unit u
+      if (first && to++ > 0) {
+        if (!warp_wait(&ctl->o_empty, (to - 2) & 1)) return false;
+        const int t = (to - 2) % kBadTiles;
+        if (ctl->bad_any[t]) {
+          for (int i = lane; i < kBadUnits * (kKeys / 32); i += 32) (&ctl->bad[t][0][0])[i] = 0u;
+          __syncwarp();
+          if (lane == 0) ctl->bad_any[t] = 0;
+          __syncwarp();
+        }
+      }
+      const int place = place_v(u, ahead >> (u & 1) & 1u);
+      if (!ready(place, u, &ctl->p_full[u & 1], (u >> 1) & 1, &ctl->peer_o[u & 1], fix >> (u & 1) & 1u)) return false;
+      if (rank != 0) return true;
+      const uint32_t a = tmem + kColS + 128 * (u & 1);
+#pragma unroll
+      for (int h = 0; h < F::kParts; ++h) {
+        const int st = stage(place, h);
+#pragma unroll
+        for (int kk = 0; kk < F::kKeysV / 16; ++kk)
+          mma_ts<kCtas>(tmem, a + (h * F::kKeysV + kk * 16) / 2, dv + st * (kStageBytes / 16) + kk * (16 * 128 / 16),
+                        idesc_o, kk > 0 || h > 0 ? 1u : (uint32_t)!first, leader);
+        commit<kCtas>(&ctl->empty[st], leader);
+      }
+      commit<kCtas>(&ctl->pv_done[u & 1], leader);
+      return true;
+    };
+    // S of unit u + 1 goes ahead of O of unit u, whose weights the softmax
+    // makes meanwhile; not where u + 1 starts a tile, whose Q may be long in
+    // coming. (One call site each: the code stays short.)
+    bool ok = true, sfirst = true, ofirst = true;  // unit su, ou starts a tile (in this run)
+    int su = 0, ou = 0;                            // units scored and put out so far
+#pragma unroll 1
+    while (ok && ou < U) {
+      if (su < U && su <= ou + 1 && (su == ou || !sfirst)) {
+        const bool last = nxt.last();
+        ok = score(su, sfirst, last || su + 1 == U);
+        const uint32_t bit = 1u << (su & 1);
+        fix = nxt.fix(p, kTileRows) ? fix | bit : fix & ~bit;
+        ahead = !last && su + 1 < U ? ahead | bit : ahead & ~bit;
+        sfirst = last;
+        if (++su < U) nxt.advance(p, r, kTileRows);
+      } else {
+        ok = output(ou, ofirst);
+        // with su == ou + 1 the next unit's sfirst is this one's end; with
+        // su == ou + 2 unit ou + 1 is of the same tile
+        ++ou;
+        ofirst = su == ou && sfirst;
+      }
+    }
+    if (rank == 0) commit<kCtas>(&ctl->mma_done, leader);
+  } else if (warp == kLoadWarp) {
+    // ---------------------------------------------------- K and V by TMA
+    const int outside = p.n_pages * p.Hkv;  // a page that reads as zeros
+    const int rows = 1 << p.shift;
+    const int box_k = min(rows, F::kKeyRows), box_v = min(rows, F::kKeysV);  // positions of a box
+    const int per_k = F::kKeyRows / box_k, per_v = F::kKeysV / box_v;        // boxes of 64 head dims of a stage
+    const bool many = rows < kKeys;  // a unit has several pages
+    int issued = 0;
+    bool bad = false;
+    // This lane's page of a unit, as read: -2 where the unit has no position in it.
+    auto look_up = [&](const Cursor& k) -> int {
+      const int pos = k.i * kKeys + (lane << p.shift);
+      if ((lane > 0 && (lane << p.shift) >= kKeys) || pos >= k.len) return -2;
+      return ld(p.tables + (size_t)k.b * p.max_pages + (pos >> p.shift));
+    };
+    auto settle = [&](int id, int g) -> int {  // its place in the pools
+      if (id != -2 && (id < 0 || id >= p.n_pages)) bad = true;
+      return id < 0 || id >= p.n_pages ? outside : id * p.Hkv + g;
+    };
+    auto load = [&](const CUtensorMap* map, int place, int h, int first, int z, int key0, int box, int per, int boxes,
+                    int dim0, int slab_bytes) -> bool {
+      const int st = stage(place, h);
+      if (!warp_wait(&ctl->empty[st], phase(place, h) ^ 1u)) return false;
+      if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], kStageBytes);
+      __syncwarp();
+      const int slab = lane / per, n = lane - slab * per, key = key0 + n * box;
+      const int at = __shfl_sync(0xffffffffu, z, many ? (key >> p.shift) & 31 : 0);
+      if (lane < boxes)
+        tma_load_3d(sR + st * kStageBytes + slab * slab_bytes + n * box * 128, map, dim0 + slab * 64,
+                    (first + key) & (rows - 1), at, &ctl->full[st]);
+      issued = max(issued, place * F::kParts + h + 1);
+      return true;
+    };
+    auto load_k = [&](int place, int first, int z) -> bool {
+      for (int h = 0; h < F::kParts; ++h)
+        if (!load(&tm_k, place, h, first, z, rank * F::kKeyRows, box_k, per_k, per_k * F::kSlabsK, h * F::kSlabsK * 64,
+                  F::kKeyRows * 128))
+          return false;
+      return true;
+    };
+    auto load_v = [&](int place, int first, int z) -> bool {
+      for (int h = 0; h < F::kParts; ++h)
+        if (!load(&tm_v, place, h, first, z, h * F::kKeysV, box_v, per_v, per_v * (F::kDimsV / 64), rank * F::kDimsV,
+                  F::kKeysV * 128))
+          return false;
+      return true;
+    };
+    if ((int)blockIdx.x != p.stalled) {
+      Cursor k = cur;  // the unit after u
+      int first = k.i * kKeys, z = settle(look_up(k), k.g);
+      bool last = k.last(), ahead = false;
+      int id = -2;
+      auto step = [&](int u) {  // to the unit after u
+        if (u + 1 < U) {
+          k.advance(p, r, kTileRows);
+          id = look_up(k);
+        }
+      };
+      bool ok = load_k(0, first, z);
+      step(0);
+#pragma unroll 1
+      for (int u = 0; ok && u < U; ++u) {
+        const bool more = u + 1 < U;
+        const int first1 = k.i * kKeys, z1 = more ? settle(id, k.g) : 0;
+        const bool last1 = k.last();
+        ahead = more && !last;
+        if (ahead) ok = load_k(place_k(u + 1, true), first1, z1);
+        step(u + 1);  // its page numbers come while this unit's V waits for room
+        ok = ok && load_v(place_v(u, ahead), first, z);
+        if (ok && more && !ahead) ok = load_k(place_k(u + 1, false), first1, z1);
+        first = first1;
+        z = z1;
+        last = last1;
+      }
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0) ctl->bad_page = 1;
+    // No copy may be in flight when the block ends, whatever ended the loops.
+    int dummy = 0;
+    for (int j = max(issued - kStages, 0); j < issued; ++j)
+      mbar_wait(&ctl->full[j % kStages], (uint32_t)(j / kStages) & 1u, &dummy,
+                global_timer_ns() + (uint64_t)kv8::kTimeoutNs);
+  } else if (warp == kNoteWarp) {
+    // ------------------------------------------------------- unit notes
+    Cursor k = cur;
+#pragma unroll 1
+    for (int u = 0; u < U; ++u) {
+      const int s = u % kNotes;
+      if (u >= kNotes && !warp_wait(&ctl->note_empty[s], (u / kNotes - 1) & 1)) break;
+      if (lane == 0) {
+        ctl->note[s].tile = make_int4(k.lo, k.n, k.len, k.g);
+        ctl->note[s].place = make_int4(k.i * kKeys, k.rt, k.last(), 0);
+        mbar_arrive(&ctl->note_full[s]);
+      }
+      if (u + 1 < U) k.advance(p, r, kTileRows);
+    }
+  } else if (warp < kSoftWarps) {
+    // --------------------------------------------------------- softmax
+    const int quad = warp & 3, half = warp >> 2;
+    const int row = quad * 32 + lane;
+    const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
+    const float a = fmaxf(p.scale_log2, 1e-35f);
+    float m = kMinusBig, l = 0.f;
+    int see = 0, tile = 0, met = 0, tok = 0;
+    bool fresh = true, mid = cur.i > 0;  // the tile's first unit in this run; the tile began in an earlier run
+    bool act = false;                    // some row of the warp's is there
+    // this thread's value and its partner's, once both are there
+    auto meet = [&](float v, float& other) -> bool {
+      ctl->mx[met & 1][half][row] = v;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->mx_full[quad]);
+      if (!warp_wait(&ctl->mx_full[quad], met & 1)) return false;
+      other = ctl->mx[met & 1][half ^ 1][row];
+      ++met;
+      return true;
+    };
+    int4 seq = make_int4(0, 0, 0, 0);  // lo, n, len, g of the tile
+#pragma unroll 1
+    for (int u = 0; u < U; ++u) {
+      const int ns = u % kNotes;
+      if (!warp_wait(&ctl->note_full[ns], (u / kNotes) & 1)) break;
+      const int4 place = ctl->note[ns].place;
+      if (fresh) {
+        seq = ctl->note[ns].tile;
+        const int rho = place.y * kTileRows + rank * kRows + row;
+        tok = div_r(rho, p.rmagic);
+        see = rho < seq.y * r ? max(seq.z - seq.y + tok + 1, 0) : 0;
+        act = __any_sync(0xffffffffu, see > 0);
+        m = kMinusBig;
+        l = 0.f;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->note_empty[ns]);
+      if (!warp_wait(&ctl->s_full[u & 1], (u >> 1) & 1)) break;
+      const int ctx = seq.z - seq.y;  // positions before the new ones
+      float other;
+      if (act) {
+        tc_fence_after();
+        const uint32_t ts = lane_addr + kColS + 128 * (u & 1);
+        uint32_t x[64];
+        tmem_ld_64(ts + 64 * half, x);
+        const int first = place.x + 64 * half;
+        const int left = see - first;  // visible positions from this half's first on (but for the tree)
+        if (__any_sync(0xffffffffu, left < 64)) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (e >= left) x[e] = 0xFF800000u;  // -inf
+        }
+        if (p.tree != nullptr && first + 64 > ctx) {  // the whole warp alike
+          const uint64_t bits =
+              see > 0 ? tree_bits(p.tree + (size_t)(seq.x + tok) * p.words, p.words, first, ctx) : 0ull;
+          const uint32_t b0 = (uint32_t)bits, b1 = (uint32_t)(bits >> 32);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            if (!(b0 >> e & 1u)) x[e] = 0xFF800000u;
+            if (!(b1 >> e & 1u)) x[32 + e] = 0xFF800000u;
+          }
+        }
+        float mx = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+#pragma unroll
+        for (int e = 2; e < 64; e += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+        if (!meet(mx, other)) break;
+        mx = fmaxf(mx, other);
+        if (fresh) {
+          m = fmaxf(mx, kMinusBig);
+        } else if (__any_sync(0xffffffffu, (mx - m) * a > kSlack)) {
+          // O and L to the new maximum, once the products of the last unit are in
+          const float nm = (mx - m) * a > kSlack ? mx : m, f = ex2((m - nm) * a);
+          m = nm;
+          l *= f;
+          if (!warp_wait(&ctl->pv_done[(u - 1) & 1], ((u - 1) >> 1) & 1)) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int j = half * (D / 2); j < (half + 1) * (D / 2); j += 16) {
+            uint32_t w[16];
+            tmem_ld_16(lane_addr + j, w);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
+            tmem_st_16(lane_addr + j, w);
+          }
+        }
+        // weights, over S (both halves have read it)
+        float slope = a, base = m > kMinusBig ? -m * a : 0.f;
+        if (__any_sync(0xffffffffu, fabsf(base) > kLargeScore)) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e) x[e] = __float_as_uint((__uint_as_float(x[e]) - m) * a);
+          slope = 1.f;
+          base = 0.f;
+        }
+        const uint64_t a2 = pack2(slope, slope), b2 = pack2(base, base);
+        uint64_t s2 = 0ull;
+        uint32_t w[32];
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) {
+          const float2 y = unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), a2, b2));
+          const float w0 = ex2(y.x), w1 = ex2(y.y);
+          s2 = add2(s2, pack2(w0, w1));
+          w[e / 2] = pack_bf16(w0, w1);
+        }
+        const float2 s = unpack2(s2);
+        l += s.x + s.y;
+        tmem_st_32(ts + 32 * half, w);
+        tmem_st_wait();
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->p_full[u & 1]);
+
+      const bool ends = place.z != 0;
+      fresh = ends;
+      if (ends || u + 1 == U) {
+        // ---- the run leaves this tile: its rows' outputs, or the partial state
+        if (act) {
+          if (!meet(l, other)) break;
+          l += other;
+        }
+        if (!warp_wait(&ctl->pv_done[u & 1], (u >> 1) & 1)) break;
+        tc_fence_after();
+        if (act) {
+          const int bt = tile % kBadTiles;
+          if (ctl->bad_any[bt]) {
+            // a row that sees one of these is NaN, as its products would have made it
+            const int b0 = max(ctx + (p.tree != nullptr ? 0 : div_r(place.y * kTileRows, p.rmagic) + 1), 0) / kKeys;
+            for (int k = 0; k < kBadUnits * (kKeys / 32); ++k) {
+              uint32_t bits = (&ctl->bad[bt][0][0])[k];
+              const int pos = b0 * kKeys + 32 * k;
+              if (bits == 0u || see <= pos) continue;
+              if (see - pos < 32) bits &= (1u << (see - pos)) - 1u;
+              if (p.tree != nullptr)
+                bits &= (uint32_t)tree_bits(p.tree + (size_t)(seq.x + tok) * p.words, p.words, pos, ctx);
+              if (bits != 0u) l = __uint_as_float(0x7FC00000u);
+            }
+          }
+          const int d0 = half * (D / 2);
+          const uint32_t out = smem_u32(smem + F::kOutOffset) + warp * (32 * F::kOutPitch);
+          if (!mid && ends) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            // 32 rows by 32 dims at a time through shared memory: 4 lanes write
+            // a row's 64 bytes, 8 rows at once
+            uint16_t* orow[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int rk = place.y * kTileRows + rank * kRows + quad * 32 + 8 * k + (lane >> 2);
+              const int tk = div_r(rk, p.rmagic);
+              const bool live = rk < seq.y * r && ctx + tk >= 0;
+              uint16_t* at = p.o + ((size_t)(seq.x + tk) * p.Hq + (size_t)seq.w * r + rk - tk * r) * D + 8 * (lane & 3);
+              orow[k] = live ? at : nullptr;
+            }
+#pragma unroll 1
+            for (int j = d0; j < d0 + D / 2; j += 32) {
+              __syncwarp();
+#pragma unroll
+              for (int h = 0; h < 32; h += 16) {
+                uint32_t v[16];
+                tmem_ld_16(lane_addr + j + h, v);
+#pragma unroll
+                for (int e = 0; e < 16; e += 8) {
+                  uint32_t z[4];
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    z[k] = pack_bf16(__uint_as_float(v[e + 2 * k]) * inv, __uint_as_float(v[e + 2 * k + 1]) * inv);
+                  sts128(out + lane * F::kOutPitch + 2 * (h + e), z[0], z[1], z[2], z[3]);
+                }
+              }
+              __syncwarp();
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint4 y = lds128(out + (8 * k + (lane >> 2)) * F::kOutPitch + 16 * (lane & 3));
+                if (orow[k]) *reinterpret_cast<uint4*>(orow[k] + j) = y;
+              }
+            }
+          } else {
+            // 32 rows by 16 dims at a time, the same way; of rows that are there
+            float* part = p.part + (size_t)(2 * c + (mid ? 0 : 1)) * slot_floats(D, kTileRows);
+            const int rows = seq.y * r - place.y * kTileRows - rank * kRows - quad * 32;
+            float* prow = part + (size_t)(rank * kRows + quad * 32 + (lane >> 2)) * D + 4 * (lane & 3);
+#pragma unroll 1
+            for (int j = d0; j < d0 + D / 2; j += 16) {
+              uint32_t v[16];
+              tmem_ld_16(lane_addr + j, v);
+              __syncwarp();
+#pragma unroll
+              for (int e = 0; e < 16; e += 4)
+                sts128(out + lane * F::kOutPitch + 4 * e, v[e], v[e + 1], v[e + 2], v[e + 3]);
+              __syncwarp();
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (8 * k + (lane >> 2) < rows)
+                  *reinterpret_cast<uint4*>(prow + (size_t)(8 * k) * D + j) =
+                      lds128(out + (8 * k + (lane >> 2)) * F::kOutPitch + 16 * (lane & 3));
+            }
+            if (half == 0 && lane < rows) {
+              part[(size_t)D * kTileRows + rank * kRows + row] = m;
+              part[(size_t)(D + 1) * kTileRows + rank * kRows + row] = l;
+            }
+          }
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->o_empty);
+        ++tile;
+        mid = false;
+        fresh = true;
+      }
+    }
+  } else if (warp < kSoftWarps + kAuxWarps) {
+    // ------------------------------------------- Q, and V that is not finite
+    const int t = threadIdx.x - 32 * kSoftWarps;
+    constexpr int kThr = 32 * kAuxWarps, kLanes = D / 8, kAtOnce = kThr / kLanes;  // lanes per row, rows per step
+    const int ln = t % kLanes, row0 = t / kLanes;
+    const uint32_t q0 = smem_u32(sQ) + (ln >> 3) * (kRows * 128);
+    Cursor k = cur;
+    bool fresh = true, ok = true, last;
+    int tile = 0;
+    uint32_t fixes = 0u;
+#pragma unroll 1
+    for (int u = 0; ok && u < U; ++u) {
+      if (fresh) {
+        if (tile > 0 && !warp_wait(&ctl->q_empty, (tile - 1) & 1)) break;
+        tc_fence_after();
+        const int rho0 = k.rt * kTileRows + rank * kRows, rows = min(kRows, k.n * r - rho0);
+#pragma unroll 4
+        for (int i = row0; i < rows; i += kAtOnce) {
+          const int rho = rho0 + i, tok = div_r(rho, p.rmagic);
+          const uint16_t* from = p.q + (size_t)(k.lo + tok) * p.q_stride + (size_t)(k.g * r + rho - tok * r) * D + ln * 8;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(q0 + i * 128 + (((ln & 7) ^ (i & 7)) << 4)),
+                       "l"(from)
+                       : "memory");
+        }
+        cp_async_wait_all();
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->q_full);
+      }
+      last = k.last();
+      if (k.fix(p, kTileRows)) {
+        const int place = place_v(u, !last && u + 1 < U), first = k.i * kKeys, part = k.partial(p, kTileRows);
+        const int bt = tile % kBadTiles;
+        if (!warp_wait(&ctl->look, fixes & 1u)) break;
+        constexpr int kPieces = F::kDimsV / 8;  // of 16 bytes of a position
+#pragma unroll 1
+        for (int h = 0; ok && h < F::kParts; ++h) {
+          const int st = stage(place, h);
+          ok = warp_wait(&ctl->full[st], phase(place, h));
+          if (!ok) break;
+          const int key0 = max(part - first - h * F::kKeysV, 0);
+          const uint32_t base = smem_u32(sR) + st * kStageBytes;
+#pragma unroll 1
+          for (int i = key0 * kPieces + t; i < F::kKeysV * kPieces; i += kThr) {
+            const int key = i / kPieces, piece = i % kPieces, pos = first + h * F::kKeysV + key;
+            const uint32_t at = base + (piece >> 3) * (F::kKeysV * 128) + key * 128 + (((piece & 7) ^ (key & 7)) << 4);
+            if (pos >= k.len) {
+              sts128(at, 0u, 0u, 0u, 0u);
+              continue;
+            }
+            const uint4 v = lds128(at);
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            bool found = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              // halves whose exponent is all ones
+              if ((w[e] & 0x7F80u) == 0x7F80u) {
+                w[e] &= 0xFFFF0000u;
+                found = true;
+              }
+              if ((w[e] & 0x7F800000u) == 0x7F800000u) {
+                w[e] &= 0xFFFFu;
+                found = true;
+              }
+            }
+            if (found) {
+              sts128(at, w[0], w[1], w[2], w[3]);
+              const int bu = k.i - part / kKeys, key_u = h * F::kKeysV + key;
+              or_both<kCtas>(&ctl->bad[bt][bu][key_u >> 5], 1u << (key_u & 31), rank);
+              or_both<kCtas>(reinterpret_cast<uint32_t*>(&ctl->bad_any[bt]), 1u, rank);
+            }
+          }
+        }
+        if (!ok) break;
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->fixed);
+        ++fixes;
+      }
+      fresh = last;
+      tile += last;
+      if (u + 1 < U) k.advance(p, r, kTileRows);
+    }
+    cp_async_wait_all();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    int dummy = 0;  // no MMA may still be running when TMEM is freed
+    mbar_wait(&ctl->mma_done, 0, &dummy, global_timer_ns() + 2 * (uint64_t)p.timeout_ns);
+    tc_fence_after();
+  }
+  tile_barrier<kCtas>();  // nor a block's shared memory and barriers be gone while the other uses them
+  if (warp == kMmaWarp) free_columns<kCtas>(tmem);
+  if (threadIdx.x == 0)
+    p.flags[blockIdx.x] = *abort_flag ? (int32_t)MOE_ERR_DEVICE_TIMEOUT
+                          : ctl->bad_page ? (int32_t)MOE_ERR_INVALID_ARG
+                                          : 0;
+}
+
+struct MergeParams {
+  const int32_t* offsets;
+  const int32_t* lens;
+  const float* part;
+  const RunInfo* info;
+  const int32_t* flags;
+  uint16_t* o;
+  int32_t* status;
+  float scale_log2;
+  int Hq, Hkv, D, C, ctas;  // C: runs
+};
+
+constexpr int kMergeRows = 8;  // rows of a block at once, a warp each
+constexpr int kMergeThreads = 32 * kMergeRows;
+
+// Block (c, y): if run c is the second of the runs that share a tile, the
+// tile's rows 8 y .. + 7, 8 (y + gridDim.y) .. . The first run of a tile left
+// its state in its second slot (a tile that the run's end cuts), the others in
+// their first.
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const MergeParams p) {
+  __shared__ int s_first, s_c0, s_later;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x, C = p.C, t = threadIdx.x, lane = t & 31;
+  if (c == 0 && blockIdx.y == 0) {
+    // the call's status: the outcome of the lowest-numbered grid block that failed
+    const int blocks = C * p.ctas;
+    if (t == 0) s_first = blocks;
+    __syncthreads();
+    for (int cc = t; cc < blocks; cc += kMergeThreads)
+      if (__ldcg(p.flags + cc) != 0) atomicMin(&s_first, cc);
+    __syncthreads();
+    if (t == 0) *p.status = s_first == blocks ? 0 : __ldcg(p.flags + s_first);
+  }
+  // Run c is the tile's second if it starts inside the tile and the last live
+  // run before it does not, or does at the first unit; the runs after it that
+  // start in the tile follow one another.
+  const RunInfo f = p.info[c];
+  if (!f.live || f.i == 0) return;
+  if (t == 0) s_c0 = -1;
+  __syncthreads();
+  int later = 0;
+  for (int cc = t; cc < C; cc += kMergeThreads) {
+    const int2 x = __ldcg(reinterpret_cast<const int2*>(&p.info[cc]));  // tile, live
+    if (!x.y) continue;
+    if (cc < c) atomicMax(&s_c0, cc);
+    else if (x.x == f.tile) ++later;
+  }
+  if (t == 0) s_later = 0;
+  __syncthreads();
+  if (later) atomicAdd(&s_later, later);
+  __syncthreads();
+  const int c0 = s_c0, c1 = c + s_later - 1;
+  if (c0 < 0) return;
+  const RunInfo f0 = p.info[c0];
+  if (f0.tile == f.tile && f0.i > 0) return;  // a later one of the tile's runs
+  const int r = p.Hq / p.Hkv, D = p.D;
+  const int lo = ld(p.offsets + f.b), n = ld(p.offsets + f.b + 1) - lo, len = ld(p.lens + f.b);
+  const int rows = kRows * p.ctas, live = min(rows, n * r - f.rt * rows), per = D / 32;
+  auto slot = [&](int cc) { return p.part + (size_t)(2 * cc + (cc == c0 ? 1 : 0)) * slot_floats(D, rows); };
+  bool failed = false;
+  for (int cc = c0 + lane; cc <= c1; cc += 32)
+    for (int k = 0; k < p.ctas; ++k) failed |= __ldcg(p.flags + cc * p.ctas + k) != 0;
+  if (__any_sync(0xffffffffu, failed)) return;  // a run gave up: o is left as it was
+  for (int row = blockIdx.y * kMergeRows + (t >> 5); row < live; row += gridDim.y * kMergeRows) {
+    const int rho = f.rt * rows + row, tok = rho / r;
+    if (len - n + tok < 0) continue;
+    // lane k weighs the states of runs c0 + k, c0 + 32 + k, ...
+    float M = kMinusBig;
+    for (int cc = c0 + lane; cc <= c1; cc += 32) M = fmaxf(M, __ldcg(slot(cc) + (size_t)D * rows + row));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float L = 0.f, acc[8];  // head dims lane * D / 32 .. of the row
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+    for (int base = c0; base <= c1; base += 32) {
+      const int mine = base + lane;
+      const float e = mine <= c1 ? ex2((__ldcg(slot(mine) + (size_t)D * rows + row) - M) * p.scale_log2) : 0.f;
+      float l = mine <= c1 ? __ldcg(slot(mine) + (size_t)(D + 1) * rows + row) * e : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      L += l;
+      for (int cc = base; cc <= min(c1, base + 31); ++cc) {
+        const float w = __shfl_sync(0xffffffffu, e, cc - base);
+        const float* o = slot(cc) + (size_t)row * D + lane * per;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2)
+          if (i < per) {
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(o + i));
+            acc[i] = fmaf(w, x.x, acc[i]);
+            acc[i + 1] = fmaf(w, x.y, acc[i + 1]);
+          }
+      }
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    uint16_t* out = p.o + ((size_t)(lo + tok) * p.Hq + (size_t)f.g * r + rho - tok * r) * D + lane * per;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2)
+      if (i < per) *reinterpret_cast<__nv_bfloat162*>(out + i) = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
+  }
+}
+
+// ================================================================= host ===
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Blocks that share a tile.
+int tile_blocks(const moe_paged_shape& s) {
+  return s.D >= 128 && (long long)s.T * s.Hq > 128ll * s.B * s.Hkv ? 2 : 1;
+}
+
+size_t workspace_bytes(const moe_paged_shape& s) {
+  // as many slots of 128 rows for pairs as for single blocks
+  return 256 + kMaxCtas * (sizeof(int32_t) + sizeof(RunInfo)) + 2 * kMaxCtas * slot_floats(s.D, kRows) * sizeof(float);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      ptr = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }();
+  return fn;
+}
+
+// 3-D map of a pool [n_pages Hkv][page][D] with boxes of `rows` positions by 64
+// head dims in the 128-byte swizzle; pages past the pool read as zeros.
+cudaError_t pool_map(CUtensorMap* m, const void* base, const moe_paged_shape& s, int rows) {
+  auto fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {(cuuint64_t)s.D, (cuuint64_t)s.page, (cuuint64_t)s.n_pages * s.Hkv};
+  const cuuint64_t strides[2] = {(cuuint64_t)s.D * 2, (cuuint64_t)s.page * s.D * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)(rows < s.page ? rows : s.page), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+moe_status attn(const moe_paged_shape* shape, const void* q, const moe_paged_cache* cache, const int32_t* offsets,
+                const int32_t* lens, const uint64_t* tree, float scale, void* o, void* workspace, size_t ws_bytes,
+                void* stream, int stalled = -1, long long timeout_ns = kv8::kTimeoutNs) {
+  if (!shape) return MOE_ERR_INVALID_ARG;
+  const moe_paged_shape s = *shape;
+  if (!shape_ok(s)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!cache_ok(cache) || !aligned(offsets, 4) || !aligned(lens, 4) || !aligned(q, 16) || !aligned(o, 16) ||
+      !aligned(tree, 8) || !workspace || !aligned(workspace, 256))
+    return MOE_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !(scale < INFINITY)) return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < workspace_bytes(s)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (s.T == 0) {
+    const cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(int32_t), st);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "status clear");
+  }
+  if (!q || !offsets || !lens || !o || (s.tree_words > 0) != (tree != nullptr)) return MOE_ERR_INVALID_ARG;
+  const int sms = kv8::sm_count(), ctas = tile_blocks(s);
+  if (sms <= 0) return cuda_fail(cudaErrorInvalidDevice, "device query");
+  const int runs = (sms < kMaxCtas ? sms : kMaxCtas) / ctas;
+  if (runs < 1) return cuda_fail(cudaErrorInvalidDevice, "multiprocessors");
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  int32_t* status = reinterpret_cast<int32_t*>(ws);
+  int32_t* flags = reinterpret_cast<int32_t*>(ws + 256);
+  RunInfo* info = reinterpret_cast<RunInfo*>(ws + 256 + kMaxCtas * sizeof(int32_t));
+  float* part = reinterpret_cast<float*>(ws + 256 + kMaxCtas * (sizeof(int32_t) + sizeof(RunInfo)));
+  const int r = s.Hq / s.Hkv;
+  const Params prm{static_cast<const uint16_t*>(q), offsets, lens, cache->tables,
+                   reinterpret_cast<const unsigned long long*>(tree), static_cast<uint16_t*>(o), part, info, flags,
+                   scale * kLog2e, s.B, s.T, s.Hq, s.Hkv, page_shift(s.page), s.n_pages, s.max_pages, s.tree_words,
+                   s.q_stride ? s.q_stride : s.Hq * s.D, ((1ull << 36) + r - 1) / r, stalled, timeout_ns};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)ctas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(runs * ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const auto go = [&](auto d, auto n) -> cudaError_t {
+    using F = Cfg<decltype(d)::value, decltype(n)::value>;
+    const auto kernel = paged_attn_kernel<decltype(d)::value, decltype(n)::value>;
+    static SmemLimitMemo smem_memo;
+    CUtensorMap tk, tv;
+    cudaError_t e = pool_map(&tk, cache->k_pages, s, F::kKeyRows);
+    if (e == cudaSuccess) e = pool_map(&tv, cache->v_pages, s, F::kKeysV);
+    if (e == cudaSuccess) e = ensure_smem(kernel, F::kBytes, &smem_memo);
+    if (e != cudaSuccess) return e;
+    cfg.dynamicSmemBytes = F::kBytes;
+    return cudaLaunchKernelEx(&cfg, kernel, tk, tv, prm);
+  };
+  using One = std::integral_constant<int, 1>;
+  using Two = std::integral_constant<int, 2>;
+  cudaError_t e;
+  if (s.D == 64) e = go(std::integral_constant<int, 64>{}, One{});
+  else if (s.D == 128) e = ctas == 2 ? go(std::integral_constant<int, 128>{}, Two{}) : go(std::integral_constant<int, 128>{}, One{});
+  else e = ctas == 2 ? go(std::integral_constant<int, 256>{}, Two{}) : go(std::integral_constant<int, 256>{}, One{});
+  if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
+  const MergeParams mp{offsets, lens, part, info, flags, static_cast<uint16_t*>(o), status, scale * kLog2e,
+                       s.Hq, s.Hkv, s.D, runs, ctas};
+  cfg.gridDim = dim3((unsigned)runs, (unsigned)(kRows * ctas / kMergeRows));
+  cfg.numAttrs = 1;
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.dynamicSmemBytes = 0;
+  e = cudaLaunchKernelEx(&cfg, paged_merge_kernel, mp);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "paged merge launch");
+}
+
+}  // namespace
+}  // namespace paged
+}  // namespace bgmoe
+
+extern "C" {
+
+moe_status moe_paged_workspace_bytes(const moe_paged_shape* shape, size_t* bytes) {
+  if (!shape || !bytes) return MOE_ERR_INVALID_ARG;
+  if (!bgmoe::paged::shape_ok(*shape)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  *bytes = bgmoe::paged::workspace_bytes(*shape);
+  return MOE_OK;
+}
+
+moe_status moe_paged_attn(const moe_paged_shape* shape, const void* q, const moe_paged_cache* cache,
+                          const int32_t* offsets, const int32_t* lens, const uint64_t* tree, float scale, void* o,
+                          void* workspace, size_t ws_bytes, void* stream) {
+  return bgmoe::paged::attn(shape, q, cache, offsets, lens, tree, scale, o, workspace, ws_bytes, stream);
+}
+
+moe_status moe_paged_attn_test_stall(const moe_paged_shape* shape, const void* q, const moe_paged_cache* cache,
+                                     const int32_t* offsets, const int32_t* lens, const uint64_t* tree, float scale,
+                                     void* o, void* workspace, size_t ws_bytes, int32_t stalled_block,
+                                     int64_t timeout_ns, void* stream) {
+  if (stalled_block < 0 || timeout_ns <= 0 || timeout_ns > bgmoe::kv8::kTimeoutNs) return MOE_ERR_INVALID_ARG;
+  return bgmoe::paged::attn(shape, q, cache, offsets, lens, tree, scale, o, workspace, ws_bytes, stream, stalled_block,
+                            timeout_ns);
+}
+
+}  // extern "C"

@@ -1,0 +1,282 @@
+// Writing the paged cache (include/paged.h): appending new tokens, and moving
+// the accepted drafts of a tree behind the context.
+//
+// Append is the pass of rope.cu with other ends: a slot takes heads of one
+// token, queries, keys and values in turn; keys and values go to the token's
+// row of a page. The chain offsets -> start -> page is what a decode step
+// waits for, so the token's sequence is guessed first (token t is sequence t's
+// where every sequence has one) and searched for only where the guess is wrong.
+#include <type_traits>
+
+#include "kernels.h"
+#include "paged.cuh"
+#include "rope.cuh"
+
+namespace bgmoe {
+namespace paged {
+
+bool shape_ok(const moe_paged_shape& s) {
+  if (s.B < 1 || s.B > 4096 || s.T < 0 || s.T > (1 << 24)) return false;
+  if (s.Hkv < 1 || s.Hkv > 4096 || s.Hq < 1 || s.Hq % s.Hkv != 0 || (long long)s.T * s.Hkv > (1 << 30)) return false;
+  if (s.Hq / s.Hkv > 64 || (long long)s.B * s.Hkv > 65536) return false;
+  if (s.D != 64 && s.D != 128 && s.D != 256) return false;
+  if (s.page != 16 && s.page != 32 && s.page != 64 && s.page != 128 && s.page != 256) return false;
+  if (s.n_pages < 1 || (long long)s.n_pages * s.Hkv > 0x7FFFFFFFll) return false;
+  if (s.max_pages < 1 || (long long)s.max_pages * s.page > (1 << 26)) return false;
+  if (s.tree_words < 0 || s.tree_words > 8) return false;
+  const auto stride_ok = [](int v, long long least) { return v == 0 || (v % 8 == 0 && v >= least); };
+  return stride_ok(s.q_stride, (long long)s.Hq * s.D) && stride_ok(s.kv_stride, (long long)s.Hkv * s.D);
+}
+
+bool cache_ok(const moe_paged_cache* c) {
+  return c && c->k_pages && c->v_pages && c->tables && aligned(c->k_pages, 16) && aligned(c->v_pages, 16) &&
+         aligned(c->tables, 4);
+}
+
+namespace {
+
+constexpr int kThreads = 256;
+
+struct AppendParams {
+  rope::Spec s;
+  const uint16_t* q;
+  const uint16_t* kv[2];
+  uint16_t* q_out;
+  uint16_t* pages[2];
+  const int32_t* offsets;
+  const int32_t* starts;
+  const int32_t* positions;
+  const int32_t* tables;
+  int32_t* status;
+  long long qs, kvs;  // elements from token to token
+  int B, T, Hq, Hkv, H, D, shift, n_pages, max_pages, per;  // H: heads in all (Hq = 0 without queries)
+};
+
+// Token t's sequence b and its position there; false where the tables break
+// the rules for it.
+__device__ __forceinline__ bool find_token(const AppendParams& p, int t, int* b, int* position) {
+  int at = min(t, p.B - 1);
+  int lo = ld(p.offsets + at), hi = ld(p.offsets + at + 1), start = ld(p.starts + at);
+  if (t < lo || t >= hi) {
+    // the last sequence that starts at or before t
+    int a = 0, z = p.B;
+    while (z - a > 1) {
+      const int m = (a + z) >> 1;
+      if (ld(p.offsets + m) <= t) a = m;
+      else z = m;
+    }
+    at = a;
+    lo = ld(p.offsets + at);
+    hi = ld(p.offsets + at + 1);
+    start = ld(p.starts + at);
+  }
+  *b = at;
+  const long long pos = (long long)start + (t - (long long)lo);
+  *position = (int)pos;
+  return lo >= 0 && t >= lo && t < hi && start >= 0 && pos < ((long long)p.max_pages << p.shift);
+}
+
+template <int kLanes, int kHeads>
+__global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const long long slot = ((long long)blockIdx.x * kThreads + threadIdx.x) / kLanes;
+  const int l = threadIdx.x % kLanes;
+  const int t = (int)min(slot / p.per, (long long)p.T), h0 = (int)(slot % p.per);
+  const rope::Pieces pc(l, p.D, p.s);
+  const bool live = t < p.T;
+  uint4 a[kHeads], b[kHeads];
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    const int h = h0 + i * p.per;
+    a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (live && h < p.H) {
+      const int j = h - p.Hq, v = j >= p.Hkv;
+      const uint16_t* x = j < 0 ? p.q + (long long)t * p.qs + (long long)h * p.D
+                                : p.kv[v] + (long long)t * p.kvs + (long long)(v ? j - p.Hkv : j) * p.D;
+      a[i] = ld_once_v4(x + pc.a);
+      b[i] = ld_once_v4(x + pc.b);
+    }
+  }
+  int seq = 0, pos = 0, page = 0, turn = 0;
+  bool ok = live && find_token(p, t, &seq, &pos);
+  if (ok) {
+    page = ld(p.tables + (long long)seq * p.max_pages + (pos >> p.shift));
+    ok = page >= 0 && page < p.n_pages;
+    turn = p.positions != nullptr ? ld(p.positions + t) : pos;
+  }
+  if (live && !ok && p.status != nullptr && l == 0) atomicCAS(p.status, 0, (int32_t)MOE_ERR_INVALID_ARG);
+  rope::Angles ang;
+  if (ok && pc.turns) ang.at(p.s, l, turn);
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    const int h = h0 + i * p.per, j = h - p.Hq, v = j >= p.Hkv, k = j >= 0;
+    uint4 x = a[i], y = b[i];
+    rope::apply<kLanes>(p.s, pc, ang, (p.s.norm >> k) & 1, p.s.gain[k], p.D, x, y);
+    if (v) {  // values as they are
+      x = a[i];
+      y = b[i];
+    }
+    if (ok && h < p.H) {
+      uint16_t* out = k ? p.pages[v] + ((((long long)page * p.Hkv + (v ? j - p.Hkv : j)) << p.shift) +
+                                        (pos & ((1 << p.shift) - 1))) * p.D
+                        : p.q_out + ((long long)t * p.Hq + h) * p.D;
+      *reinterpret_cast<uint4*>(out + pc.a) = x;
+      *reinterpret_cast<uint4*>(out + pc.b) = y;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ keep ---
+
+constexpr int kMaxPath = 512;
+constexpr int kKeepThreads = 128;
+constexpr int kAhead = 8;  // rows in flight per thread
+
+struct KeepParams {
+  uint16_t* pages[2];
+  const int32_t* tables;
+  const int32_t* starts;
+  const int32_t* kept;
+  const int32_t* path;
+  int32_t* lens_out;
+  int32_t* status;
+  int path_stride, Hkv, D, shift, n_pages, max_pages;
+};
+
+// Block (b, y): sequence b, the y-th 128 of its 2 Hkv D / 8 columns of 16
+// bytes, a thread each. Row k comes from row path[k] >= k, and the rows are
+// read in order, so a row is never written before all that read it have: a
+// thread may read as far ahead as it likes, and columns do not meet.
+__global__ void __launch_bounds__(kKeepThreads) paged_keep_kernel(const KeepParams p) {
+  __shared__ long long s_row[2][kMaxPath];  // from, to: rows of the pools at KV head 0, in rows
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int b = blockIdx.x, t = threadIdx.x;
+  const int start = ld(p.starts + b), kept = ld(p.kept + b);
+  bool bad = start < 0 || kept < 0 || kept > p.path_stride;
+  const long long limit = (long long)p.max_pages << p.shift;
+  bad = bad || start > limit;
+  if (!bad) {
+    for (int k = t; k < kept; k += kKeepThreads) {
+      const int32_t* path = p.path + (long long)b * p.path_stride + k;
+      const int from = ld(path), before = k > 0 ? ld(path - 1) : -1;
+      if (from <= before || start + (long long)from >= limit) {
+        bad = true;
+        continue;
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int pos = start + (e ? k : from);
+        const int page = ld(p.tables + (long long)b * p.max_pages + (pos >> p.shift));
+        if (page < 0 || page >= p.n_pages) bad = true;
+        s_row[e][k] = ((long long)page * p.Hkv << p.shift) + (pos & ((1 << p.shift) - 1));
+      }
+    }
+  }
+  if (__syncthreads_or(bad)) {
+    if (t == 0 && blockIdx.y == 0 && p.status != nullptr) atomicCAS(p.status, 0, (int32_t)MOE_ERR_INVALID_ARG);
+    return;
+  }
+  if (t == 0 && blockIdx.y == 0 && p.lens_out != nullptr) p.lens_out[b] = start + kept;
+  const int half = p.Hkv * (p.D / 8), c = blockIdx.y * kKeepThreads + t;
+  if (c >= 2 * half) return;
+  const int v = c >= half, in = v ? c - half : c, h = in / (p.D / 8), d = (in % (p.D / 8)) * 8;
+  uint16_t* base = (v ? p.pages[1] : p.pages[0]) + ((long long)h << p.shift) * p.D + d;
+  for (int k0 = 0; k0 < kept; k0 += kAhead) {
+    uint4 x[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (k0 + i < kept && s_row[0][k0 + i] != s_row[1][k0 + i])
+        x[i] = ld_once_v4(base + s_row[0][k0 + i] * p.D);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (k0 + i < kept && s_row[0][k0 + i] != s_row[1][k0 + i])
+        *reinterpret_cast<uint4*>(base + s_row[1][k0 + i] * p.D) = x[i];
+  }
+}
+
+cudaLaunchConfig_t config(dim3 grid, int threads, cudaStream_t stream, cudaLaunchAttribute* attr) {
+  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr->val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+}  // namespace
+}  // namespace paged
+}  // namespace bgmoe
+
+extern "C" {
+
+moe_status moe_paged_append(const moe_paged_shape* shape, const moe_rope_spec* spec, const void* q, const void* k_new,
+                            const void* v_new, const int32_t* offsets, const int32_t* starts, const int32_t* positions,
+                            const moe_paged_cache* cache, void* q_out, int32_t* status, void* stream) {
+  using namespace bgmoe;
+  using namespace bgmoe::paged;
+  if (!shape) return MOE_ERR_INVALID_ARG;
+  const moe_paged_shape s = *shape;
+  if (!shape_ok(s) || (spec && !rope::spec_ok(*spec, s.D))) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!cache_ok(cache) || !aligned(q, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(q_out, 16) ||
+      !aligned(offsets, 4) || !aligned(starts, 4) || !aligned(positions, 4) || !aligned(status, 4) ||
+      (spec && !rope::spec_pointers_ok(*spec)) || (q == nullptr) != (q_out == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (s.T == 0) return MOE_OK;
+  if (!k_new || !v_new || !offsets || !starts) return MOE_ERR_INVALID_ARG;
+  const int Hq = q ? s.Hq : 0;
+  AppendParams p{rope::device_spec(spec),
+                 static_cast<const uint16_t*>(q),
+                 {static_cast<const uint16_t*>(k_new), static_cast<const uint16_t*>(v_new)},
+                 static_cast<uint16_t*>(q_out),
+                 {static_cast<uint16_t*>(cache->k_pages), static_cast<uint16_t*>(cache->v_pages)},
+                 offsets, starts, positions, cache->tables, status,
+                 s.q_stride ? s.q_stride : (long long)s.Hq * s.D, s.kv_stride ? s.kv_stride : (long long)s.Hkv * s.D,
+                 s.B, s.T, Hq, s.Hkv, Hq + 2 * s.Hkv, s.D, page_shift(s.page), s.n_pages, s.max_pages, 0};
+  const int lanes = rope::head_lanes(s.D);
+  // Heads per slot as in moe_rope.
+  const bool one = (long long)s.T * p.H * lanes <= 152 * 2048;
+  p.per = one ? p.H : (p.H + 3) / 4;
+  const long long threads = (long long)s.T * p.per * lanes;
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg = config(dim3((unsigned)((threads + kThreads - 1) / kThreads)), kThreads,
+                                        static_cast<cudaStream_t>(stream), &attr);
+  const auto go = [&](auto n) {
+    constexpr int kLanes = decltype(n)::value;
+    return one ? cudaLaunchKernelEx(&cfg, paged_append_kernel<kLanes, 1>, p)
+               : cudaLaunchKernelEx(&cfg, paged_append_kernel<kLanes, 4>, p);
+  };
+  const cudaError_t e = lanes == 4   ? go(std::integral_constant<int, 4>{})
+                        : lanes == 8 ? go(std::integral_constant<int, 8>{})
+                                     : go(std::integral_constant<int, 16>{});
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "append launch");
+}
+
+moe_status moe_paged_keep(const moe_paged_shape* shape, const moe_paged_cache* cache, const int32_t* starts,
+                          const int32_t* kept, const int32_t* path, int32_t path_stride, int32_t* lens_out,
+                          int32_t* status, void* stream) {
+  using namespace bgmoe;
+  using namespace bgmoe::paged;
+  if (!shape) return MOE_ERR_INVALID_ARG;
+  const moe_paged_shape s = *shape;
+  if (!shape_ok(s) || path_stride < 0 || path_stride > kMaxPath) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!cache_ok(cache) || !aligned(starts, 4) || !aligned(kept, 4) || !aligned(path, 4) || !aligned(lens_out, 4) ||
+      !aligned(status, 4) || !starts || !kept || (path_stride > 0 && !path))
+    return MOE_ERR_INVALID_ARG;
+  const KeepParams p{{static_cast<uint16_t*>(cache->k_pages), static_cast<uint16_t*>(cache->v_pages)},
+                     cache->tables, starts, kept, path, lens_out, status, path_stride, s.Hkv, s.D,
+                     page_shift(s.page), s.n_pages, s.max_pages};
+  const int columns = 2 * s.Hkv * (s.D / 8);
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg =
+      config(dim3((unsigned)s.B, (unsigned)((columns + kKeepThreads - 1) / kKeepThreads)), kKeepThreads,
+             static_cast<cudaStream_t>(stream), &attr);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_keep_kernel, p);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "keep launch");
+}
+
+}  // extern "C"
