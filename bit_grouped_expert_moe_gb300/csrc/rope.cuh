@@ -103,16 +103,21 @@ __device__ __forceinline__ void apply(const Spec& s, const Pieces& p, const Angl
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     float f = rsqrtf(sum / (float)D + s.eps);
-    // A finite head whose squares pass fp32: the same of 2^-66 times its values,
-    // beside whose squares eps is nothing.
+    // A finite head whose squares pass fp32: the same of 2^-72 times its values,
+    // beside whose squares (2^-24 at least, 2^120 at most in all) eps is nothing.
     if (__any_sync(0xffffffffu, !(sum < 3e38f))) {
-      const float d = 1.3552527156068805e-20f;  // 2^-66
+      const bool large = !(sum < 3e38f);
+      const float d = large ? 2.117582368135751e-22f : 1.f;  // 2^-72
       float t = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t = fmaf(a[i] * d, a[i] * d, fmaf(b[i] * d, b[i] * d, t));
+      for (int i = 0; i < 8; ++i) {
+        a[i] *= norm ? d : 1.f;
+        b[i] *= norm ? d : 1.f;
+        t = fmaf(a[i], a[i], fmaf(b[i], b[i], t));
+      }
 #pragma unroll
       for (int o = kLanes / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-      if (!(sum < 3e38f)) f = rsqrtf(t / (float)D) * d;
+      if (large) f = rsqrtf(t / (float)D);
     }
     if (norm) {
       float ga[8], gb[8];
