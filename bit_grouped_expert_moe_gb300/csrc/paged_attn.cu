@@ -240,21 +240,15 @@ __device__ __forceinline__ void or_both(uint32_t* at, uint32_t bits, int rank) {
   }
 }
 
-__device__ __forceinline__ unsigned long long ld_u64(const unsigned long long* p) {
-  unsigned long long v;
-  asm volatile("ld.global.b64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
-  return v;
-}
-
 // Bits of the 64 positions from `first` on that the tree lets a draft see,
 // whose words are at w: all of the context's (before ctx), then its own.
 __device__ __forceinline__ uint64_t tree_bits(const unsigned long long* w, int words, int first, int ctx) {
   const int j = first - ctx;
   if (j <= -64) return ~0ull;
-  if (j < 0) return (ld_u64(w) << -j) | ((1ull << -j) - 1);
+  if (j < 0) return (ld(w) << -j) | ((1ull << -j) - 1);
   const int k = j >> 6, s = j & 63;
-  uint64_t v = k < words ? ld_u64(w + k) >> s : 0ull;
-  if (s > 0 && k + 1 < words) v |= ld_u64(w + k + 1) << (64 - s);
+  uint64_t v = k < words ? ld(w + k) >> s : 0ull;
+  if (s > 0 && k + 1 < words) v |= ld(w + k + 1) << (64 - s);
   return v;
 }
 

@@ -1,9 +1,8 @@
 // Writing the paged cache (include/paged.h): appending new tokens, and moving
 // the accepted drafts of a tree behind the context.
 //
-// Append is the pass of rope.cu with other ends: a slot takes heads of one
-// token, queries, keys and values in turn; keys and values go to the token's
-// row of a page. The chain offsets -> start -> page is what a decode step
+// Append is the pass of rope.cuh over queries, keys and values; keys and values
+// go to the token's row of a page. The chain offsets -> start -> page is what a decode step
 // waits for, so the token's sequence is guessed first (token t is sequence t's
 // where every sequence has one) and searched for only where the guess is wrong.
 #include <type_traits>
@@ -35,10 +34,9 @@ bool cache_ok(const moe_paged_cache* c) {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kAhead = 4, kBlocks = 6;  // as in rope.cu
 
-struct AppendParams {
-  rope::Spec s;
+struct Append {
   const uint16_t* q;
   const uint16_t* kv[2];
   uint16_t* q_out;
@@ -49,89 +47,67 @@ struct AppendParams {
   const int32_t* tables;
   int32_t* status;
   long long qs, kvs;  // elements from token to token
-  int B, T, Hq, Hkv, H, D, shift, n_pages, max_pages, per;  // H: heads in all (Hq = 0 without queries)
+  int B, Hq, Hkv, D, shift, n_pages, max_pages;  // Hq = 0 without queries
+  struct Token {
+    long long row;  // of KV head 0 in the pools
+  };
+  // The token's sequence and its position there; false where the tables break
+  // the rules for it.
+  __device__ bool token(int t, Token* k, int* position) const {
+    int b = min(t, B - 1);
+    int lo = ld(offsets + b), hi = ld(offsets + b + 1), start = ld(starts + b);
+    if (t < lo || t >= hi) {
+      // the last sequence that starts at or before t
+      int a = 0, z = B;
+      while (z - a > 1) {
+        const int m = (a + z) >> 1;
+        if (ld(offsets + m) <= t) a = m;
+        else z = m;
+      }
+      b = a;
+      lo = ld(offsets + b);
+      hi = ld(offsets + b + 1);
+      start = ld(starts + b);
+    }
+    const long long pos = (long long)start + (t - (long long)lo);
+    if (lo < 0 || t < lo || t >= hi || start < 0 || pos >= ((long long)max_pages << shift)) return false;
+    const int page = ld(tables + (long long)b * max_pages + (pos >> shift));
+    if (page < 0 || page >= n_pages) return false;
+    k->row = ((long long)page * Hkv << shift) + (pos & ((1 << shift) - 1));
+    *position = positions != nullptr ? ld(positions + t) : (int)pos;
+    return true;
+  }
+  __device__ int kind(int h) const { return h < Hq ? 0 : h < Hq + Hkv ? 1 : 2; }
+  __device__ const uint16_t* from(int t, int h) const {
+    const int j = h - Hq;
+    return j < 0      ? q + t * qs + (long long)h * D
+           : j < Hkv ? kv[0] + t * kvs + (long long)j * D
+                     : kv[1] + t * kvs + (long long)(j - Hkv) * D;
+  }
+  __device__ uint16_t* to(const Token& k, int t, int h) const {
+    const int j = h - Hq;
+    return j < 0      ? q_out + ((long long)t * Hq + h) * D
+           : j < Hkv ? pages[0] + (k.row + ((long long)j << shift)) * D
+                     : pages[1] + (k.row + ((long long)(j - Hkv) << shift)) * D;
+  }
+  __device__ void refuse() const {
+    if (status != nullptr) atomicCAS(status, 0, (int32_t)MOE_ERR_INVALID_ARG);
+  }
 };
 
-// Token t's sequence b and its position there; false where the tables break
-// the rules for it.
-__device__ __forceinline__ bool find_token(const AppendParams& p, int t, int* b, int* position) {
-  int at = min(t, p.B - 1);
-  int lo = ld(p.offsets + at), hi = ld(p.offsets + at + 1), start = ld(p.starts + at);
-  if (t < lo || t >= hi) {
-    // the last sequence that starts at or before t
-    int a = 0, z = p.B;
-    while (z - a > 1) {
-      const int m = (a + z) >> 1;
-      if (ld(p.offsets + m) <= t) a = m;
-      else z = m;
-    }
-    at = a;
-    lo = ld(p.offsets + at);
-    hi = ld(p.offsets + at + 1);
-    start = ld(p.starts + at);
-  }
-  *b = at;
-  const long long pos = (long long)start + (t - (long long)lo);
-  *position = (int)pos;
-  return lo >= 0 && t >= lo && t < hi && start >= 0 && pos < ((long long)p.max_pages << p.shift);
-}
-
-template <int kLanes, int kHeads>
-__global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendParams p) {
+template <int kLanes>
+__global__ void __launch_bounds__(rope::kThreads, kBlocks)
+    paged_append_kernel(const Append io, const rope::Spec spec, const rope::Split split) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const long long slot = ((long long)blockIdx.x * kThreads + threadIdx.x) / kLanes;
-  const int l = threadIdx.x % kLanes;
-  const int t = (int)min(slot / p.per, (long long)p.T), h0 = (int)(slot % p.per);
-  const rope::Pieces pc(l, p.D, p.s);
-  const bool live = t < p.T;
-  uint4 a[kHeads], b[kHeads];
-#pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    const int h = h0 + i * p.per;
-    a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (live && h < p.H) {
-      const int j = h - p.Hq, v = j >= p.Hkv;
-      const uint16_t* x = j < 0 ? p.q + (long long)t * p.qs + (long long)h * p.D
-                                : p.kv[v] + (long long)t * p.kvs + (long long)(v ? j - p.Hkv : j) * p.D;
-      a[i] = ld_once_v4(x + pc.a);
-      b[i] = ld_once_v4(x + pc.b);
-    }
-  }
-  int seq = 0, pos = 0, page = 0, turn = 0;
-  bool ok = live && find_token(p, t, &seq, &pos);
-  if (ok) {
-    page = ld(p.tables + (long long)seq * p.max_pages + (pos >> p.shift));
-    ok = page >= 0 && page < p.n_pages;
-    turn = p.positions != nullptr ? ld(p.positions + t) : pos;
-  }
-  if (live && !ok && p.status != nullptr && l == 0) atomicCAS(p.status, 0, (int32_t)MOE_ERR_INVALID_ARG);
-  rope::Angles ang;
-  if (ok && pc.turns) ang.at(p.s, l, turn);
-#pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    const int h = h0 + i * p.per, j = h - p.Hq, v = j >= p.Hkv, k = j >= 0;
-    uint4 x = a[i], y = b[i];
-    rope::apply<kLanes>(p.s, pc, ang, (p.s.norm >> k) & 1, p.s.gain[k], p.D, x, y);
-    if (v) {  // values as they are
-      x = a[i];
-      y = b[i];
-    }
-    if (ok && h < p.H) {
-      uint16_t* out = k ? p.pages[v] + ((((long long)page * p.Hkv + (v ? j - p.Hkv : j)) << p.shift) +
-                                        (pos & ((1 << p.shift) - 1))) * p.D
-                        : p.q_out + ((long long)t * p.Hq + h) * p.D;
-      *reinterpret_cast<uint4*>(out + pc.a) = x;
-      *reinterpret_cast<uint4*>(out + pc.b) = y;
-    }
-  }
+  rope::turn<kLanes, kAhead>(io, spec, split);
 }
 
 // ------------------------------------------------------------------ keep ---
 
 constexpr int kMaxPath = 512;
 constexpr int kKeepThreads = 128;
-constexpr int kAhead = 8;  // rows in flight per thread
+constexpr int kRowsAhead = 8;  // rows in flight per thread
 
 struct KeepParams {
   uint16_t* pages[2];
@@ -183,14 +159,14 @@ __global__ void __launch_bounds__(kKeepThreads) paged_keep_kernel(const KeepPara
   if (c >= 2 * half) return;
   const int v = c >= half, in = v ? c - half : c, h = in / (p.D / 8), d = (in % (p.D / 8)) * 8;
   uint16_t* base = (v ? p.pages[1] : p.pages[0]) + ((long long)h << p.shift) * p.D + d;
-  for (int k0 = 0; k0 < kept; k0 += kAhead) {
-    uint4 x[kAhead];
+  for (int k0 = 0; k0 < kept; k0 += kRowsAhead) {
+    uint4 x[kRowsAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
+    for (int i = 0; i < kRowsAhead; ++i)
       if (k0 + i < kept && s_row[0][k0 + i] != s_row[1][k0 + i])
         x[i] = ld_once_v4(base + s_row[0][k0 + i] * p.D);
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
+    for (int i = 0; i < kRowsAhead; ++i)
       if (k0 + i < kept && s_row[0][k0 + i] != s_row[1][k0 + i])
         *reinterpret_cast<uint4*>(base + s_row[1][k0 + i] * p.D) = x[i];
   }
@@ -229,26 +205,21 @@ moe_status moe_paged_append(const moe_paged_shape* shape, const moe_rope_spec* s
   if (s.T == 0) return MOE_OK;
   if (!k_new || !v_new || !offsets || !starts) return MOE_ERR_INVALID_ARG;
   const int Hq = q ? s.Hq : 0;
-  AppendParams p{rope::device_spec(spec),
-                 static_cast<const uint16_t*>(q),
-                 {static_cast<const uint16_t*>(k_new), static_cast<const uint16_t*>(v_new)},
-                 static_cast<uint16_t*>(q_out),
-                 {static_cast<uint16_t*>(cache->k_pages), static_cast<uint16_t*>(cache->v_pages)},
-                 offsets, starts, positions, cache->tables, status,
-                 s.q_stride ? s.q_stride : (long long)s.Hq * s.D, s.kv_stride ? s.kv_stride : (long long)s.Hkv * s.D,
-                 s.B, s.T, Hq, s.Hkv, Hq + 2 * s.Hkv, s.D, page_shift(s.page), s.n_pages, s.max_pages, 0};
+  const Append io{static_cast<const uint16_t*>(q),
+                  {static_cast<const uint16_t*>(k_new), static_cast<const uint16_t*>(v_new)},
+                  static_cast<uint16_t*>(q_out),
+                  {static_cast<uint16_t*>(cache->k_pages), static_cast<uint16_t*>(cache->v_pages)},
+                  offsets, starts, positions, cache->tables, status,
+                  s.q_stride ? s.q_stride : (long long)s.Hq * s.D, s.kv_stride ? s.kv_stride : (long long)s.Hkv * s.D,
+                  s.B, Hq, s.Hkv, s.D, page_shift(s.page), s.n_pages, s.max_pages};
+  long long blocks = 0;
+  const rope::Split sl = rope::split(s.T, Hq + 2 * s.Hkv, s.D, spec ? spec->rot : 0, kAhead, &blocks);
   const int lanes = rope::head_lanes(s.D);
-  // Heads per slot as in moe_rope.
-  const bool one = (long long)s.T * p.H * lanes <= 152 * 2048;
-  p.per = one ? p.H : (p.H + 3) / 4;
-  const long long threads = (long long)s.T * p.per * lanes;
   cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = config(dim3((unsigned)((threads + kThreads - 1) / kThreads)), kThreads,
-                                        static_cast<cudaStream_t>(stream), &attr);
+  const cudaLaunchConfig_t cfg =
+      config(dim3((unsigned)blocks), rope::kThreads, static_cast<cudaStream_t>(stream), &attr);
   const auto go = [&](auto n) {
-    constexpr int kLanes = decltype(n)::value;
-    return one ? cudaLaunchKernelEx(&cfg, paged_append_kernel<kLanes, 1>, p)
-               : cudaLaunchKernelEx(&cfg, paged_append_kernel<kLanes, 4>, p);
+    return cudaLaunchKernelEx(&cfg, paged_append_kernel<decltype(n)::value>, io, rope::device_spec(spec), sl);
   };
   const cudaError_t e = lanes == 4   ? go(std::integral_constant<int, 4>{})
                         : lanes == 8 ? go(std::integral_constant<int, 8>{})

@@ -1,10 +1,7 @@
 // Rotary positions (include/rope.h): the table of turns (host) and the pass
 // that norms and rotates queries and keys.
 //
-// A slot is the lanes of one head (rope.cuh). It takes up to kHeads heads of
-// one token, far enough apart that neighbouring slots take neighbouring heads,
-// asks for all of them before it computes the token's angles, and so keeps
-// 32 kHeads bytes per lane in flight.
+// rope.cuh has the pass itself.
 #include <cmath>
 #include <type_traits>
 
@@ -29,57 +26,43 @@ bool spec_pointers_ok(const moe_rope_spec& s) {
 
 Spec device_spec(const moe_rope_spec* s) {
   if (s == nullptr) return Spec{};
-  return Spec{s->turns, {static_cast<const uint16_t*>(s->q_gain), static_cast<const uint16_t*>(s->k_gain)}, s->rot,
+  return Spec{reinterpret_cast<const unsigned long long*>(s->turns), {static_cast<const uint16_t*>(s->q_gain), static_cast<const uint16_t*>(s->k_gain)}, s->rot,
               s->layout == MOE_ROPE_PAIRS, s->norm, s->eps, s->gain_offset, s->magnitude};
 }
 
 namespace {
 
-constexpr int kThreads = 256;
+// Heads in flight per slot, and blocks per SM (registers). us for 8192 tokens of 40
+// and 8 heads of 128, and for 4096 of 16 and 2 of 256: 4, 4 41 and 23; 4, 5 38 and 20;
+// 4, 6 35 and 19; 3, 6 37 and 18; 3, 7 37 and 17; 2, 8 40 and 19.
+constexpr int kAhead = 4, kBlocks = 6;
 
-struct Params {
-  Spec s;
+struct Io {
   const uint16_t* x[2];  // q, k
   uint16_t* y[2];
   long long xs[2], ys[2];  // elements from token to token
   const int32_t* positions;
-  int T, Hq, H, D, per;  // H = Hq + Hk; per: slots of a token
+  int Hq, D;
+  struct Token {};
+  __device__ bool token(int t, Token*, int* position) const {
+    if (positions != nullptr) *position = ld(positions + t);
+    return true;
+  }
+  __device__ int kind(int h) const { return h >= Hq; }
+  __device__ const uint16_t* from(int t, int h) const {
+    return h < Hq ? x[0] + t * xs[0] + (long long)h * D : x[1] + t * xs[1] + (long long)(h - Hq) * D;
+  }
+  __device__ uint16_t* to(const Token&, int t, int h) const {
+    return h < Hq ? y[0] + t * ys[0] + (long long)h * D : y[1] + t * ys[1] + (long long)(h - Hq) * D;
+  }
+  __device__ void refuse() const {}
 };
 
-template <int kLanes, int kHeads>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
+template <int kLanes>
+__global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const Io io, const Spec spec, const Split split) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const long long slot = ((long long)blockIdx.x * kThreads + threadIdx.x) / kLanes;
-  const int l = threadIdx.x % kLanes;
-  const int t = (int)min(slot / p.per, (long long)p.T), h0 = (int)(slot % p.per);
-  const Pieces pc(l, p.D, p.s);
-  uint4 a[kHeads], b[kHeads];
-  bool on[kHeads];
-#pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    const int h = h0 + i * p.per;
-    on[i] = t < p.T && h < p.H && pc.on;
-    a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (on[i]) {
-      const int k = h >= p.Hq;
-      const uint16_t* x = p.x[k] + (long long)t * p.xs[k] + (long long)(h - (k ? p.Hq : 0)) * p.D;
-      a[i] = ld_once_v4(x + pc.a);
-      b[i] = ld_once_v4(x + pc.b);
-    }
-  }
-  Angles ang;
-  if (t < p.T && pc.turns) ang.at(p.s, l, ld(p.positions + t));
-#pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    const int h = h0 + i * p.per, k = h >= p.Hq;
-    apply<kLanes>(p.s, pc, ang, (p.s.norm >> k) & 1, p.s.gain[k], p.D, a[i], b[i]);
-    if (on[i]) {
-      uint16_t* y = p.y[k] + (long long)t * p.ys[k] + (long long)(h - (k ? p.Hq : 0)) * p.D;
-      *reinterpret_cast<uint4*>(y + pc.a) = a[i];
-      *reinterpret_cast<uint4*>(y + pc.b) = b[i];
-    }
-  }
+  turn<kLanes, kAhead>(io, spec, split);
 }
 
 bool shape_ok(const moe_rope_shape& s) {
@@ -151,30 +134,25 @@ moe_status moe_rope(const moe_rope_shape* shape, const moe_rope_spec* spec, cons
   if (s.T == 0) return MOE_OK;
   if ((s.Hq > 0 && (!q || !q_out)) || (s.Hk > 0 && (!k || !k_out)) || (spec->rot > 0 && !positions))
     return MOE_ERR_INVALID_ARG;
-  Params p{device_spec(spec),
-           {static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k)},
-           {static_cast<uint16_t*>(q_out), static_cast<uint16_t*>(k_out)},
-           {s.q_stride ? s.q_stride : (long long)s.Hq * s.D, s.k_stride ? s.k_stride : (long long)s.Hk * s.D},
-           {s.qo_stride ? s.qo_stride : (long long)s.Hq * s.D, s.ko_stride ? s.ko_stride : (long long)s.Hk * s.D},
-           positions, s.T, s.Hq, s.Hq + s.Hk, s.D, 0};
+  const Io io{{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k)},
+              {static_cast<uint16_t*>(q_out), static_cast<uint16_t*>(k_out)},
+              {s.q_stride ? s.q_stride : (long long)s.Hq * s.D, s.k_stride ? s.k_stride : (long long)s.Hk * s.D},
+              {s.qo_stride ? s.qo_stride : (long long)s.Hq * s.D, s.ko_stride ? s.ko_stride : (long long)s.Hk * s.D},
+              spec->rot > 0 ? positions : nullptr, s.Hq, s.D};
+  long long blocks = 0;
+  const Split sl = split(s.T, s.Hq + s.Hk, s.D, spec->rot, kAhead, &blocks);
   const int lanes = head_lanes(s.D);
-  // Heads per slot: one while the call's heads are fewer than the GPU's slots
-  // (latency), else four.
-  const bool one = (long long)s.T * p.H * lanes <= 152 * 2048;
-  p.per = one ? p.H : (p.H + 3) / 4;
-  const long long threads = (long long)s.T * p.per * lanes;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((threads + kThreads - 1) / kThreads));
+  cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const auto go = [&](auto n) {
-    constexpr int kLanes = decltype(n)::value;
-    return one ? cudaLaunchKernelEx(&cfg, rope_kernel<kLanes, 1>, p) : cudaLaunchKernelEx(&cfg, rope_kernel<kLanes, 4>, p);
+    return cudaLaunchKernelEx(&cfg, rope_kernel<decltype(n)::value>, io, device_spec(spec), sl);
   };
   const cudaError_t e = lanes == 1   ? go(std::integral_constant<int, 1>{})
                         : lanes == 2 ? go(std::integral_constant<int, 2>{})
