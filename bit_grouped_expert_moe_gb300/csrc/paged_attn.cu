@@ -909,93 +909,172 @@ struct MergeParams {
   int Hq, Hkv, D, C, ctas;  // C: runs
 };
 
-constexpr int kMergeRows = 8;  // rows of a block at once, a warp each
-constexpr int kMergeThreads = 32 * kMergeRows;
+constexpr int kMergeWarps = 8;
+constexpr int kMergeThreads = 32 * kMergeWarps;
+constexpr int kMergeBlocks = 4;  // per SM
+constexpr int kFewStates = 4;    // of a row, up to which a warp joins them alone
+static_assert(kMaxCtas <= kMergeThreads, "a thread per run");
 
-// Block (c, y): if run c is the second of the runs that share a tile, the
-// tile's rows 8 y .. + 7, 8 (y + gridDim.y) .. . The first run of a tile left
-// its state in its second slot (a tile that the run's end cuts), the others in
-// their first.
-__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const MergeParams p) {
-  __shared__ int s_first, s_c0, s_later;
+// Joins the partial states of the tiles that runs' borders cut. Every block
+// finds out from the runs' starts which tiles those are, and takes its share of
+// their rows: a row by the whole block, the states dealt out to its warps
+// (decode over a long context has few rows and many states), or 8 rows, a
+// warp each (cut tiles of a prompt have many rows and few states). The first
+// run of a tile left its state in its second slot (a tile that the run's end
+// cuts), the others in their first.
+__global__ void __launch_bounds__(kMergeThreads, kMergeBlocks) paged_merge_kernel(const MergeParams p) {
+  __shared__ RunInfo s_info[kMergeThreads];
+  __shared__ int s_items[kMergeThreads + 1];  // before a run's tile's
+  __shared__ int s_c0[kMergeThreads], s_c1[kMergeThreads];
+  __shared__ int s_scan[2][kMergeWarps];
+  __shared__ int s_first;
+  __shared__ float s_l[kMergeWarps];
+  __shared__ __align__(16) float s_acc[kMergeWarps][256];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.x, C = p.C, t = threadIdx.x, lane = t & 31;
-  if (c == 0 && blockIdx.y == 0) {
-    // the call's status: the outcome of the lowest-numbered grid block that failed
-    const int blocks = C * p.ctas;
-    if (t == 0) s_first = blocks;
-    __syncthreads();
+  const int C = p.C, t = threadIdx.x, lane = t & 31, warp = t >> 5, blocks = C * p.ctas;
+  int failed = 0;
+  if (t == 0) s_first = blocks;
+  const RunInfo f = t < C ? p.info[t] : RunInfo{};
+  for (int cc = t; cc < blocks; cc += kMergeThreads) failed |= __ldcg(p.flags + cc) != 0;
+  s_info[t] = f;
+  s_c1[t] = -1;
+  // A call in which a block gave up or met a bad page joins nothing: o is not
+  // valid. Its status is the outcome of the lowest-numbered block that failed.
+  if (__syncthreads_or(failed)) {
+    if (blockIdx.x != 0) return;
     for (int cc = t; cc < blocks; cc += kMergeThreads)
       if (__ldcg(p.flags + cc) != 0) atomicMin(&s_first, cc);
     __syncthreads();
-    if (t == 0) *p.status = s_first == blocks ? 0 : __ldcg(p.flags + s_first);
+    if (t == 0) *p.status = __ldcg(p.flags + s_first);
+    return;
   }
-  // Run c is the tile's second if it starts inside the tile and the last live
-  // run before it does not, or does at the first unit; the runs after it that
+  if (t == 0 && blockIdx.x == 0) *p.status = 0;
+  const bool live = t < C && f.live;
+  // the last live run before this one
+  int before = live ? t : -1;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before = max(before, x);
+  }
+  if (lane == 31) s_scan[0][warp] = before;
+  before = __shfl_up_sync(0xffffffffu, before, 1);
+  if (lane == 0) before = -1;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) before = max(before, s_scan[0][w]);
+  // Run t is its tile's second if it starts inside the tile and the live run
+  // before it does not, or does at the first unit; the runs after it that
   // start in the tile follow one another.
-  const RunInfo f = p.info[c];
-  if (!f.live || f.i == 0) return;
-  if (t == 0) s_c0 = -1;
-  __syncthreads();
-  int later = 0;
-  for (int cc = t; cc < C; cc += kMergeThreads) {
-    const int2 x = __ldcg(reinterpret_cast<const int2*>(&p.info[cc]));  // tile, live
-    if (!x.y) continue;
-    if (cc < c) atomicMax(&s_c0, cc);
-    else if (x.x == f.tile) ++later;
+  const bool inside = live && f.i > 0 && before >= 0;
+  const bool second = inside && !(s_info[max(before, 0)].tile == f.tile && s_info[max(before, 0)].i > 0);
+  int head = second ? t : -1;  // the second run of the tile that run t starts inside
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, head, o);
+    if (lane >= o) head = max(head, x);
   }
-  if (t == 0) s_later = 0;
+  if (lane == 31) s_scan[1][warp] = head;
   __syncthreads();
-  if (later) atomicAdd(&s_later, later);
+  for (int w = 0; w < warp; ++w) head = max(head, s_scan[1][w]);
+  if (inside && head >= 0) atomicMax(&s_c1[head], t);
   __syncthreads();
-  const int c0 = s_c0, c1 = c + s_later - 1;
-  if (c0 < 0) return;
-  const RunInfo f0 = p.info[c0];
-  if (f0.tile == f.tile && f0.i > 0) return;  // a later one of the tile's runs
-  const int r = p.Hq / p.Hkv, D = p.D;
-  const int lo = ld(p.offsets + f.b), n = ld(p.offsets + f.b + 1) - lo, len = ld(p.lens + f.b);
-  const int rows = kRows * p.ctas, live = min(rows, n * r - f.rt * rows), per = D / 32;
-  auto slot = [&](int cc) { return p.part + (size_t)(2 * cc + (cc == c0 ? 1 : 0)) * slot_floats(D, rows); };
-  bool failed = false;
-  for (int cc = c0 + lane; cc <= c1; cc += 32)
-    for (int k = 0; k < p.ctas; ++k) failed |= __ldcg(p.flags + cc * p.ctas + k) != 0;
-  if (__any_sync(0xffffffffu, failed)) return;  // a run gave up: o is left as it was
-  for (int row = blockIdx.y * kMergeRows + (t >> 5); row < live; row += gridDim.y * kMergeRows) {
-    const int rho = f.rt * rows + row, tok = rho / r;
-    if (len - n + tok < 0) continue;
-    // lane k weighs the states of runs c0 + k, c0 + 32 + k, ...
-    float M = kMinusBig;
-    for (int cc = c0 + lane; cc <= c1; cc += 32) M = fmaxf(M, __ldcg(slot(cc) + (size_t)D * rows + row));
+  const int r = p.Hq / p.Hkv, D = p.D, rows = kRows * p.ctas;
+  int items = 0;
+  if (second) {
+    const int n = ld(p.offsets + f.b + 1) - ld(p.offsets + f.b), there = min(rows, n * r - f.rt * rows);
+    s_c0[t] = before;
+    items = s_c1[t] - before + 1 > kFewStates ? there : (there + kMergeWarps - 1) / kMergeWarps;
+  }
+  int sum = items;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float L = 0.f, acc[8];  // head dims lane * D / 32 .. of the row
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += x;
+  }
+  if (lane == 31) s_scan[0][warp] = sum;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) sum += s_scan[0][w];
+  s_items[t + 1] = sum;
+  if (t == 0) s_items[0] = 0;
+  __syncthreads();
+  for (int item = blockIdx.x; item < s_items[kMergeThreads]; item += gridDim.x) {
+    int c = 0;  // the last run with s_items[c] <= item
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-    for (int base = c0; base <= c1; base += 32) {
-      const int mine = base + lane;
-      const float e = mine <= c1 ? ex2((__ldcg(slot(mine) + (size_t)D * rows + row) - M) * p.scale_log2) : 0.f;
-      float l = mine <= c1 ? __ldcg(slot(mine) + (size_t)(D + 1) * rows + row) * e : 0.f;
+    for (int o = kMergeThreads / 2; o > 0; o >>= 1)
+      if (s_items[c + o] <= item) c += o;
+    const RunInfo g = s_info[c];
+    const int c0 = s_c0[c], c1 = s_c1[c], lo = ld(p.offsets + g.b), n = ld(p.offsets + g.b + 1) - lo;
+    const bool shared = c1 - c0 + 1 > kFewStates;
+    const int row = shared ? item - s_items[c] : (item - s_items[c]) * kMergeWarps + warp;
+    const int rho = g.rt * rows + row, tok = rho / r;
+    const bool there = row < rows && rho < n * r && ld(p.lens + g.b) - n + tok >= 0;
+    const float* first = p.part + (size_t)(2 * c0 + 1) * slot_floats(D, rows);
+    const float* rest = p.part + (size_t)(2 * c0) * slot_floats(D, rows);
+    auto state = [&](int k) {  // of run c0 + k
+      return k == 0 ? first : rest + (size_t)2 * k * slot_floats(D, rows);
+    };
+    float M = kMinusBig, L = 0.f;
+    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    const int states = c1 - c0 + 1;
+    if (there) {
+      // lane k weighs states k, 32 + k, ...
+      for (int k = lane; k < states; k += 32) M = fmaxf(M, __ldcg(state(k) + (size_t)D * rows + row));
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-      L += l;
-      for (int cc = base; cc <= min(c1, base + 31); ++cc) {
-        const float w = __shfl_sync(0xffffffffu, e, cc - base);
-        const float* o = slot(cc) + (size_t)row * D + lane * per;
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const int from = shared ? warp : 0, step = shared ? kMergeWarps : 1;
+      for (int base = 0; base < states; base += 32 * step) {
+        const int mine = base + from + lane * step;
+        float e = 0.f;
+        if (mine < states) {
+          e = ex2((__ldcg(state(mine) + (size_t)D * rows + row) - M) * p.scale_log2);
+          L += __ldcg(state(mine) + (size_t)(D + 1) * rows + row) * e;
+        }
+        const int count = min(32, (states - base - from + step - 1) / step);
+#pragma unroll 4
+        for (int k = 0; k < count; ++k) {
+          const float w = __shfl_sync(0xffffffffu, e, k);
+          const float* o = state(base + from + k * step) + (size_t)row * D;
 #pragma unroll
-        for (int i = 0; i < 8; i += 2)
-          if (i < per) {
-            const float2 x = __ldcg(reinterpret_cast<const float2*>(o + i));
-            acc[i] = fmaf(w, x.x, acc[i]);
-            acc[i + 1] = fmaf(w, x.y, acc[i + 1]);
+          for (int i = 0; i < 2; ++i) {
+            const int d = 4 * lane + 128 * i;
+            if (d < D) {
+              const float4 x = __ldcg(reinterpret_cast<const float4*>(o + d));
+              acc[i].x = fmaf(w, x.x, acc[i].x), acc[i].y = fmaf(w, x.y, acc[i].y);
+              acc[i].z = fmaf(w, x.z, acc[i].z), acc[i].w = fmaf(w, x.w, acc[i].w);
+            }
           }
+        }
       }
-    }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    uint16_t* out = p.o + ((size_t)(lo + tok) * p.Hq + (size_t)f.g * r + rho - tok * r) * D + lane * per;
 #pragma unroll
-    for (int i = 0; i < 8; i += 2)
-      if (i < per) *reinterpret_cast<__nv_bfloat162*>(out + i) = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
+      for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    }
+    uint16_t* out = p.o + ((size_t)(lo + tok) * p.Hq + (size_t)g.g * r + rho - tok * r) * D;
+    if (!shared) {
+      if (!there) continue;
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (4 * lane + 128 * i < D)
+          *reinterpret_cast<uint2*>(out + 4 * lane + 128 * i) =
+              make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv), pack_bf16(acc[i].z * inv, acc[i].w * inv));
+      continue;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (4 * lane + 128 * i < D) *reinterpret_cast<float4*>(&s_acc[warp][4 * lane + 128 * i]) = acc[i];
+    if (lane == 0) s_l[warp] = L;
+    __syncthreads();
+    if (there && t < D) {
+      float l = 0.f, o = 0.f;
+#pragma unroll
+      for (int w = 0; w < kMergeWarps; ++w) {
+        l += s_l[w];
+        o += s_acc[w][t];
+      }
+      out[t] = __bfloat16_as_ushort(__float2bfloat16_rn(l == 0.f ? 0.f : o * (1.f / l)));
+    }
+    __syncthreads();
   }
 }
 
@@ -1107,7 +1186,7 @@ moe_status attn(const moe_paged_shape* shape, const void* q, const moe_paged_cac
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
   const MergeParams mp{offsets, lens, part, info, flags, static_cast<uint16_t*>(o), status, scale * kLog2e,
                        s.Hq, s.Hkv, s.D, runs, ctas};
-  cfg.gridDim = dim3((unsigned)runs, (unsigned)(kRows * ctas / kMergeRows));
+  cfg.gridDim = dim3((unsigned)(sms * kMergeBlocks));
   cfg.numAttrs = 1;
   cfg.blockDim = dim3(kMergeThreads);
   cfg.dynamicSmemBytes = 0;
