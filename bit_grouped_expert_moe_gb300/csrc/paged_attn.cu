@@ -74,10 +74,6 @@ constexpr int kMaxCtas = 256;  // workspace bound on the grid
 constexpr int kTileCost = 3;
 constexpr float kMinusBig = -3.402823466e38f;  // running-max start, finite: m - m_new is never NaN
 constexpr float kSlack = 8.f;                  // a row's scores may pass its m by this much (base 2): weights to 2^8
-// x a - m a is computed in one step, so m a's own rounding, half an fp32 step,
-// is in all of a row's weights: up to here 2^-4 of a power of two. Rows past it
-// take two, the difference first.
-constexpr float kLargeScore = 1048576.f;  // 2^20
 constexpr uint32_t kColS = 256;           // S buffers at columns 256 and 384, O from 0
 constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);  // A and B format in an instruction descriptor
 
@@ -634,19 +630,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t x[64];
         tmem_ld_64(ts + 64 * half, x);
         const int first = place.x + 64 * half;
-        const int left = see - first;  // visible positions from this half's first on (but for the tree)
-        if (__any_sync(0xffffffffu, left < 64)) {
-#pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (e >= left) x[e] = 0xFF800000u;  // -inf
-        }
-        if (p.tree != nullptr && first + 64 > ctx) {  // the whole warp alike
-          const uint64_t bits =
-              see > 0 ? tree_bits(p.tree + (size_t)(seq.x + tok) * p.words, p.words, first, ctx) : 0ull;
+        // Rows that are not there, or see nothing, are left to themselves: nothing
+        // of theirs is written, and a warp may have one row and 31 such.
+        const int left = see > 0 ? see - first : kKeys;  // visible positions from this half's first on (but for the tree)
+        if (__any_sync(0xffffffffu, left < 64 || (p.tree != nullptr && first + 64 > ctx))) {
+          uint64_t bits = left >= 64 ? ~0ull : left > 0 ? (1ull << left) - 1 : 0ull;
+          if (p.tree != nullptr && see > 0)
+            bits &= tree_bits(p.tree + (size_t)(seq.x + tok) * p.words, p.words, first, ctx);
           const uint32_t b0 = (uint32_t)bits, b1 = (uint32_t)(bits >> 32);
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            if (!(b0 >> e & 1u)) x[e] = 0xFF800000u;
+            if (!(b0 >> e & 1u)) x[e] = 0xFF800000u;  // -inf
             if (!(b1 >> e & 1u)) x[32 + e] = 0xFF800000u;
           }
         }
@@ -657,9 +651,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mx = fmaxf(mx, other);
         if (fresh) {
           m = fmaxf(mx, kMinusBig);
-        } else if (__any_sync(0xffffffffu, (mx - m) * a > kSlack)) {
+        } else if (__any_sync(0xffffffffu, see > 0 && (mx - m) * a > kSlack)) {
           // O and L to the new maximum, once the products of the last unit are in
-          const float nm = (mx - m) * a > kSlack ? mx : m, f = ex2((m - nm) * a);
+          const float nm = see > 0 && (mx - m) * a > kSlack ? mx : m, f = ex2((m - nm) * a);
           m = nm;
           l *= f;
           if (!warp_wait(&ctl->pv_done[(u - 1) & 1], ((u - 1) >> 1) & 1)) break;
@@ -674,19 +668,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // weights, over S (both halves have read it)
-        float slope = a, base = m > kMinusBig ? -m * a : 0.f;
-        if (__any_sync(0xffffffffu, fabsf(base) > kLargeScore)) {
-#pragma unroll
-          for (int e = 0; e < 64; ++e) x[e] = __float_as_uint((__uint_as_float(x[e]) - m) * a);
-          slope = 1.f;
-          base = 0.f;
-        }
-        const uint64_t a2 = pack2(slope, slope), b2 = pack2(base, base);
+        // (the difference first: one step, x a - m a, would save an instruction of
+        // two values, but a row's m a, rounded, would be off by more than a weight's
+        // exponent holds where scores pass 2^30)
+        const uint64_t a2 = pack2(a, a), b2 = pack2(-m, -m);
         uint64_t s2 = 0ull;
         uint32_t w[32];
 #pragma unroll
         for (int e = 0; e < 64; e += 2) {
-          const float2 y = unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), a2, b2));
+          const float2 y = unpack2(mul2(add2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), b2), a2));
           const float w0 = ex2(y.x), w1 = ex2(y.y);
           s2 = add2(s2, pack2(w0, w1));
           w[e / 2] = pack_bf16(w0, w1);
