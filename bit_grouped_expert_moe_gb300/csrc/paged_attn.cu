@@ -34,8 +34,9 @@
 //                sees and that are no finite numbers out of it (0 * NaN is NaN)
 //   warp 12      TMEM allocation; the MMA-issuing thread (of a pair, the first
 //                block's; the other block's warp tells it what is ready there)
-//   warp 13      K and V by TMA, a box per page and 64 head dims: page numbers from
-//                the table one unit ahead, positions past the context as zeros
+//   warp 13      K and V by TMA, a box per page (and per 64 head dims, where a stage
+//                has several pages): page numbers from the table one unit ahead,
+//                positions past the context as zeros
 //   warp 14      per unit, its place in shared memory for the softmax
 // The ring's stages (16 KB) hold K of a unit in D / 64 parts by head dims and V in
 // as many by positions (half as many per block of a pair, which holds half of
@@ -65,13 +66,15 @@ constexpr int kKeys = 128;  // positions of a unit
 constexpr int kStages = 8;
 constexpr int kStageBytes = 16384;
 constexpr int kSoftWarps = 8, kAuxWarps = 4;
-constexpr int kMmaWarp = 12, kLoadWarp = 13, kNoteWarp = 14;
+constexpr int kMmaWarp = 12, kLoadWarp = 13, kNoteWarp = 14;  // (with 15 for the MMA warp the chunk below takes 392 us for 336)
 constexpr int kThreads = 512;
 constexpr int kMaxCtas = 256;  // workspace bound on the grid
 // A run also pays for every tile it begins (Q, the first unit's chain, the
-// output): the runs are cut on a scale where a tile with units takes kTileCost
-// more places than units, before its first.
-constexpr int kTileCost = 3;
+// output): the runs are cut on a scale where a tile with units takes some more
+// places than units, before its first. A prompt of 4096 (16 heads on 2 x 256)
+// takes 153, 136, 121, 122 us with 1, 2, 3, 5 of them; with few rows beginning
+// and ending are cheap: a token of 64 sequences 44, 46, 47, 48.
+constexpr int kTileCost = 3, kFewRowsCost = 1;
 constexpr float kMinusBig = -3.402823466e38f;  // running-max start, finite: m - m_new is never NaN
 constexpr float kSlack = 8.f;                  // a row's scores may pass its m by this much (base 2): weights to 2^8
 constexpr uint32_t kColS = 256;           // S buffers at columns 256 and 384, O from 0
@@ -155,6 +158,7 @@ struct Params {
   float scale_log2;
   int B, T, Hq, Hkv, shift, n_pages, max_pages, words, q_stride;
   unsigned long long rmagic;  // ceil(2^36 / r), r = Hq / Hkv
+  int cost;  // places of a tile beyond its units
   int stalled;
   long long timeout_ns;
 };
@@ -208,12 +212,101 @@ struct Cursor {
 __device__ __forceinline__ int place_k(int u, bool ahead_before) { return 2 * u - (ahead_before ? 1 : 0); }
 __device__ __forceinline__ int place_v(int u, bool ahead) { return 2 * u + 1 + (ahead ? 1 : 0); }
 
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
+// find_run for calls of up to 256 sequences of one row tile each, by one warp: the
+// starts of runs c and c + 1. Its sums are those of find_run in 32 bits; calls
+// that it does not take (more tiles, larger sums, more sequences) are left to
+// find_run. Lane k has kPer sequences from kPer k on, all asked for at once. (A
+// decode step of 64 sequences: TODO us.)
+__device__ __forceinline__ bool find_small(const Params& p, int r, int RT, int cost, int c, int C, Place* out,
+                                           long long* next, bool* ok) {
+  constexpr int kPer = 8;
+  const int lane = threadIdx.x & 31;
+  if (p.B > 32 * kPer) return false;
+  const int per = (p.B + 31) >> 5, b0 = lane * per;
+  int at[kPer + 1], len[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    at[j] = len[j] = 0;
+    if (j < per && b0 + j < p.B) at[j] = ld(p.offsets + b0 + j), len[j] = ld(p.lens + b0 + j);
+  }
+  const int end = b0 < p.B ? ld(p.offsets + min(b0 + per, p.B)) : 0;
+  bool bad = false, wide = false;
+  int v = 0, w = 0, t = 0;  // this lane's places, units, tiles, per KV head
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+    if (j < per && b0 + j < p.B) {
+      const int hi = j + 1 < per && b0 + j + 1 < p.B ? at[j + 1 < kPer ? j + 1 : j] : end, n = hi - at[j];
+      bad |= kv8::offsets_bad(at[j], hi, b0 + j, p.B, p.T) || len[j] < 0 || len[j] > p.max_pages << p.shift;
+      wide |= n * (long long)r > RT;
+      const int nb = n > 0 && len[j] > 0 ? (len[j] + kKeys - 1) / kKeys : 0;  // the last row sees len positions
+      v += nb > 0 ? nb + cost : 0;
+      w += nb;
+      t += n > 0;
+    }
+  *ok = !__any_sync(0xffffffffu, bad);
+  if (!*ok) return true;
+  const long long most = (long long)((p.max_pages << p.shift) / kKeys + 1 + cost) * p.Hkv * p.B;
+  if (__any_sync(0xffffffffu, wide) || most > 0x7FFFFFFFll) return false;
+  int vi = v, wi = w, ti = t;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, vi, o), y = __shfl_up_sync(0xffffffffu, wi, o);
+    const int z = __shfl_up_sync(0xffffffffu, ti, o);
+    if (lane >= o) vi += x, wi += y, ti += z;
+  }
+  const int N = __shfl_sync(0xffffffffu, vi, 31) * p.Hkv, each = N / C, more = N - each * C;
+  Place k{};
+  k.b = -1;
+  k.units = *next = (long long)__shfl_sync(0xffffffffu, wi, 31) * p.Hkv;
+#pragma unroll 1
+  for (int e = 0; e < 2; ++e) {
+    const int from = (c + e) * each + min(c + e, more);
+    const unsigned hit = __ballot_sync(0xffffffffu, vi * p.Hkv > from);
+    if (hit == 0u) break;  // the end: all units are before it
+    const int L = __ffs(hit) - 1;
+    // the lane that has the sequence goes through its own
+    int places = (vi - v) * p.Hkv, units = (wi - w) * p.Hkv, tiles = (ti - t) * p.Hkv, b = -1, lo = 0, nn = 0, ln = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (j < per && b0 + j < p.B && b < 0) {
+        const int hi = j + 1 < per && b0 + j + 1 < p.B ? at[j + 1 < kPer ? j + 1 : j] : end, n = hi - at[j];
+        const int nb = n > 0 && len[j] > 0 ? (len[j] + kKeys - 1) / kKeys : 0, size = nb > 0 ? (nb + cost) * p.Hkv : 0;
+        if (places + size > from) {
+          b = b0 + j, lo = at[j], nn = n, ln = len[j];
+        } else {
+          places += size, units += nb * p.Hkv, tiles += n > 0 ? p.Hkv : 0;
+        }
+      }
+    ln = __shfl_sync(0xffffffffu, ln, L);
+    const int nb = (ln + kKeys - 1) / kKeys, size = nb + cost, off = from - __shfl_sync(0xffffffffu, places, L);
+    const int g = off / size, i = max(off - g * size - cost, 0);
+    const int before = __shfl_sync(0xffffffffu, units, L) + g * nb + i;
+    if (e == 0) {
+      k.b = __shfl_sync(0xffffffffu, b, L), k.g = g, k.rt = 0, k.i = i, k.nb = nb;
+      k.tile = __shfl_sync(0xffffffffu, tiles, L) + g;
+      k.lo = __shfl_sync(0xffffffffu, lo, L), k.n = __shfl_sync(0xffffffffu, nn, L), k.len = ln;
+      k.units = before;
+    } else {
+      *next = before;
+    }
+  }
+  *out = k;
+  return true;
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                            uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-      "[%5];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
       : "memory");
+}
+
+// What is left of a wait that outlasted a suspension: out of line, as it hardly
+// ever runs and every wait has a call of it.
+__device__ __noinline__ bool long_wait(uint64_t* bar, uint32_t parity, int* abort, long long timeout_ns) {
+  return mbar_wait(bar, parity, abort, global_timer_ns() + (uint64_t)timeout_ns);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -303,16 +396,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = lane; i < kBadTiles * kBadUnits * (kKeys / 32); i += 32) z[i] = 0u;
     if (lane < kBadTiles) ctl->bad_any[lane] = 0;
   }
+  if (warp == kMmaWarp) alloc_columns<kCtas>(&ctl->tmem);
+  if (warp == kLoadWarp && lane < 2) prefetch_tmap(lane == 0 ? &tm_k : &tm_v);
   // Launched with programmatic dependent launch: wait for the kernels before
-  // this one, then let this call's merge launch (it waits in turn).
+  // this one, then let this call's merge launch (it waits in turn). A block that
+  // waits here holds its columns, but those it waits for have theirs: they all
+  // run, or have ended, before it starts.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 1 || warp == 2) {  // the run's start and its end
     Place k;
-    const bool ok = find_run(p.offsets, p.lens, p.B, p.T, p.Hkv, p.max_pages << p.shift, r, kTileRows, kKeys, kTileCost,
-                             c + warp - 1, C, &k);
+    long long next;
+    bool ok;
+    const bool small = find_small(p, r, kTileRows, p.cost, c, C, &k, &next, &ok);
+    if (!small)
+      ok = find_run(p.offsets, p.lens, p.B, p.T, p.Hkv, p.max_pages << p.shift, r, kTileRows, kKeys, p.cost, c + warp - 1, C,
+                    &k);
     if (lane == 0) {
-      s_unit[warp - 1] = k.units;
+      s_unit[warp - 1] = warp == 2 && small ? next : k.units;
       if (warp == 1) {
         s_bad = !ok;
         Cursor cur{};
@@ -344,29 +445,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (rank == 0) p.info[c] = RunInfo{s_tile, live, s_cur.b, s_cur.g, s_cur.rt, s_cur.i};
     if (!live) p.flags[blockIdx.x] = s_bad ? (int32_t)MOE_ERR_INVALID_ARG : 0;
   }
-  if (s_bad) return;
+  const bool idle = s_bad || s_unit[0] >= s_unit[1];  // both blocks of a run alike
   // Queries that see nothing (more queries than positions): o = 0.
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+  for (int b = blockIdx.x; !s_bad && b < p.B; b += gridDim.x) {
     const int lo = ld(p.offsets + b), hi = ld(p.offsets + b + 1), len = ld(p.lens + b);
     const size_t pieces = (size_t)max(0, hi - lo - len) * p.Hq * (D / 8);
     uint4* z = reinterpret_cast<uint4*>(p.o + (size_t)lo * p.Hq * D);
     for (size_t i = threadIdx.x; i < pieces; i += kThreads) z[i] = make_uint4(0u, 0u, 0u, 0u);
   }
-  if (s_unit[0] >= s_unit[1]) return;  // both blocks of a run alike
-  if (warp == kMmaWarp) alloc_columns<kCtas>(&ctl->tmem);
+  // A lane's page of a unit, as the table has it: -2 where the unit has no position in it.
+  auto look_up = [&](const Cursor& k) -> int {
+    const int pos = k.i * kKeys + (lane << p.shift);
+    if ((lane > 0 && (lane << p.shift) >= kKeys) || pos >= k.len) return -2;
+    return ld(p.tables + (size_t)k.b * p.max_pages + (pos >> p.shift));
+  };
+  const int first_page = warp == kLoadWarp && !idle ? look_up(s_cur) : 0;  // on its way over the barrier
   tc_fence_before();
   tile_barrier<kCtas>();  // the barriers and the columns of both blocks are there
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
+  if (idle) {
+    tile_barrier<kCtas>();  // (columns of a pair are freed by both)
+    if (warp == kMmaWarp) free_columns<kCtas>(tmem);
+    return;
+  }
   const int U = (int)(s_unit[1] - s_unit[0]);
   Cursor cur = s_cur;
 
-  volatile int* abort_flag = &ctl->abort;
   // Each wait has its own limit (a long call may run for longer than one), set
-  // only where the phase has not completed already.
+  // only once it has lasted for a suspension (up to 0.5 ms) already.
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    bool ok = mbar_test_wait(bar, parity);
-    if (!ok) ok = mbar_wait(bar, parity, abort_flag, global_timer_ns() + (uint64_t)p.timeout_ns);
+    bool ok = mbar_test_wait(bar, parity) || mbar_try_wait(bar, parity);
+    if (!ok) ok = long_wait(bar, parity, &ctl->abort, p.timeout_ns);
     return __all_sync(0xffffffffu, ok) != 0;
   };
   // Stage h of the block at a place of the ring, and its phase there.
@@ -493,52 +603,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------- K and V by TMA
     const int outside = p.n_pages * p.Hkv;  // a page that reads as zeros
     const int rows = 1 << p.shift;
-    const int box_k = min(rows, F::kKeyRows), box_v = min(rows, F::kKeysV);  // positions of a box
-    const int per_k = F::kKeyRows / box_k, per_v = F::kKeysV / box_v;        // boxes of 64 head dims of a stage
     const bool many = rows < kKeys;  // a unit has several pages
+    // This lane's box of a stage of K, of V: all of the stage's head dims where a
+    // page holds all of its positions, else 64 of them by a page's
+    struct Box {
+      int key, slab, to;  // its first position and 64 head dims, its place in the stage
+      bool on;
+      __device__ Box(int page_shift, int keys_shift, int slabs, int key0, int slab0) {
+        const int box_shift = min(page_shift, keys_shift), per_shift = keys_shift - box_shift;
+        const int lane = threadIdx.x & 31, s = lane >> per_shift, n = lane & ((1 << per_shift) - 1);
+        on = s < (per_shift == 0 ? 1 : slabs);
+        key = key0 + (n << box_shift);
+        slab = slab0 + s;
+        to = (s << (keys_shift + 7)) + (n << (box_shift + 7));
+      }
+    };
+    constexpr int kShiftK = F::kKeyRows == 128 ? 7 : 6;
+    constexpr int kShiftV = F::kKeysV == 128 ? 7 : F::kKeysV == 64 ? 6 : 5;
+    static_assert((1 << kShiftK) == F::kKeyRows && (1 << kShiftV) == F::kKeysV, "shifts");
+    const Box bk(p.shift, kShiftK, F::kSlabsK, rank * F::kKeyRows, 0);
+    const Box bv(p.shift, kShiftV, F::kDimsV / 64, 0, rank * (F::kDimsV / 64));
     int issued = 0;
     bool bad = false;
-    // This lane's page of a unit, as read: -2 where the unit has no position in it.
-    auto look_up = [&](const Cursor& k) -> int {
-      const int pos = k.i * kKeys + (lane << p.shift);
-      if ((lane > 0 && (lane << p.shift) >= kKeys) || pos >= k.len) return -2;
-      return ld(p.tables + (size_t)k.b * p.max_pages + (pos >> p.shift));
-    };
     auto settle = [&](int id, int g) -> int {  // its place in the pools
       if (id != -2 && (id < 0 || id >= p.n_pages)) bad = true;
       return id < 0 || id >= p.n_pages ? outside : id * p.Hkv + g;
     };
-    auto load = [&](const CUtensorMap* map, int place, int h, int first, int z, int key0, int box, int per, int boxes,
-                    int dim0, int slab_bytes) -> bool {
+    auto load = [&](const CUtensorMap* map, const Box& b, int place, int h, int key, int slab, int first, int z) -> bool {
       const int st = stage(place, h);
       if (!warp_wait(&ctl->empty[st], phase(place, h) ^ 1u)) return false;
       if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], kStageBytes);
-      __syncwarp();
-      const int slab = lane / per, n = lane - slab * per, key = key0 + n * box;
       const int at = __shfl_sync(0xffffffffu, z, many ? (key >> p.shift) & 31 : 0);
-      if (lane < boxes)
-        tma_load_3d(sR + st * kStageBytes + slab * slab_bytes + n * box * 128, map, dim0 + slab * 64,
-                    (first + key) & (rows - 1), at, &ctl->full[st]);
-      issued = max(issued, place * F::kParts + h + 1);
+      if (b.on) tma_load_4d(sR + st * kStageBytes + b.to, map, 0, (first + key) & (rows - 1), slab, at, &ctl->full[st]);
+      issued = place * F::kParts + h + 1;
       return true;
     };
     auto load_k = [&](int place, int first, int z) -> bool {
+      bool ok = true;
+#pragma unroll
       for (int h = 0; h < F::kParts; ++h)
-        if (!load(&tm_k, place, h, first, z, rank * F::kKeyRows, box_k, per_k, per_k * F::kSlabsK, h * F::kSlabsK * 64,
-                  F::kKeyRows * 128))
-          return false;
-      return true;
+        ok = ok && load(&tm_k, bk, place, h, bk.key, bk.slab + h * F::kSlabsK, first, z);
+      return ok;
     };
     auto load_v = [&](int place, int first, int z) -> bool {
-      for (int h = 0; h < F::kParts; ++h)
-        if (!load(&tm_v, place, h, first, z, h * F::kKeysV, box_v, per_v, per_v * (F::kDimsV / 64), rank * F::kDimsV,
-                  F::kKeysV * 128))
-          return false;
-      return true;
+      bool ok = true;
+#pragma unroll
+      for (int h = 0; h < F::kParts; ++h) ok = ok && load(&tm_v, bv, place, h, bv.key + h * F::kKeysV, bv.slab, first, z);
+      return ok;
     };
     if ((int)blockIdx.x != p.stalled) {
       Cursor k = cur;  // the unit after u
-      int first = k.i * kKeys, z = settle(look_up(k), k.g);
+      int first = k.i * kKeys, z = settle(first_page, k.g);
       bool last = k.last(), ahead = false;
       int id = -2;
       auto step = [&](int u) {  // to the unit after u
@@ -882,7 +997,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tile_barrier<kCtas>();  // nor a block's shared memory and barriers be gone while the other uses them
   if (warp == kMmaWarp) free_columns<kCtas>(tmem);
   if (threadIdx.x == 0)
-    p.flags[blockIdx.x] = *abort_flag ? (int32_t)MOE_ERR_DEVICE_TIMEOUT
+    p.flags[blockIdx.x] = *reinterpret_cast<volatile int*>(&ctl->abort) ? (int32_t)MOE_ERR_DEVICE_TIMEOUT
                           : ctl->bad_page ? (int32_t)MOE_ERR_INVALID_ARG
                                           : 0;
 }
@@ -901,147 +1016,101 @@ struct MergeParams {
 
 constexpr int kMergeWarps = 8;
 constexpr int kMergeThreads = 32 * kMergeWarps;
-constexpr int kMergeBlocks = 4;  // per SM
-constexpr int kFewStates = 4;    // of a row, up to which a warp joins them alone
-static_assert(kMaxCtas <= kMergeThreads, "a thread per run");
+constexpr int kMergeBlocks = 16;  // of a run
+constexpr int kFewRows = 16;     // of a tile, each a whole block's ...
+constexpr int kFewStates = 4;    // ... if it has more states than these
 
-// Joins the partial states of the tiles that runs' borders cut. Every block
-// finds out from the runs' starts which tiles those are, and takes its share of
-// their rows: a row by the whole block, the states dealt out to its warps
-// (decode over a long context has few rows and many states), or 8 rows, a
-// warp each (cut tiles of a prompt have many rows and few states). The first
-// run of a tile left its state in its second slot (a tile that the run's end
-// cuts), the others in their first.
-__global__ void __launch_bounds__(kMergeThreads, kMergeBlocks) paged_merge_kernel(const MergeParams p) {
-  __shared__ RunInfo s_info[kMergeThreads];
-  __shared__ int s_items[kMergeThreads + 1];  // before a run's tile's
-  __shared__ int s_c0[kMergeThreads], s_c1[kMergeThreads];
-  __shared__ int s_scan[2][kMergeWarps];
-  __shared__ int s_first;
+// Joins the partial states of the tiles that runs' borders cut: blocks (c, *) of
+// the tile that run c is the second in, a row by a whole block, the states dealt
+// out to its warps (decode over a long context has few rows and many states),
+// or 8 rows, a warp each (cut tiles of a prompt have many rows and few states).
+// The first run of a tile left its state in its second slot (a tile that the
+// run's end cuts), the others in their first. Blocks (C, 0) put down the call's
+// status.
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const MergeParams p) {
   __shared__ float s_l[kMergeWarps];
   __shared__ __align__(16) float s_acc[kMergeWarps][256];
+  __shared__ int s_first;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int C = p.C, t = threadIdx.x, lane = t & 31, warp = t >> 5, blocks = C * p.ctas;
-  int failed = 0;
-  if (t == 0) s_first = blocks;
-  const RunInfo f = t < C ? p.info[t] : RunInfo{};
-  for (int cc = t; cc < blocks; cc += kMergeThreads) failed |= __ldcg(p.flags + cc) != 0;
-  s_info[t] = f;
-  s_c1[t] = -1;
-  // A call in which a block gave up or met a bad page joins nothing: o is not
-  // valid. Its status is the outcome of the lowest-numbered block that failed.
-  if (__syncthreads_or(failed)) {
-    if (blockIdx.x != 0) return;
-    for (int cc = t; cc < blocks; cc += kMergeThreads)
-      if (__ldcg(p.flags + cc) != 0) atomicMin(&s_first, cc);
+  const int C = p.C, c = blockIdx.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  if (c == C) {
+    // the outcome of the lowest-numbered grid block that failed
+    if (blockIdx.y != 0) return;
+    const int blocks = C * p.ctas;
+    if (t == 0) s_first = blocks;
     __syncthreads();
-    if (t == 0) *p.status = __ldcg(p.flags + s_first);
+    for (int k = t; k < blocks; k += kMergeThreads)
+      if (__ldcg(p.flags + k) != 0) atomicMin(&s_first, k);
+    __syncthreads();
+    if (t == 0) *p.status = s_first == blocks ? 0 : __ldcg(p.flags + s_first);
     return;
   }
-  if (t == 0 && blockIdx.x == 0) *p.status = 0;
-  const bool live = t < C && f.live;
-  // the last live run before this one
-  int before = live ? t : -1;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before = max(before, x);
+  // Run c is a tile's second if it starts inside it and run c - 1, which has the
+  // unit before, does not, or does at the first unit; the runs after it that start
+  // in the tile follow one another. (Lane k looks at run c - 1 + k.)
+  RunInfo f{};
+  if (c - 1 + lane >= 0 && c - 1 + lane < C) f = p.info[c - 1 + lane];
+  const int tile = __shfl_sync(0xffffffffu, f.tile, 1);
+  const unsigned same = __ballot_sync(0xffffffffu, f.live && f.tile == tile), inside = __ballot_sync(0xffffffffu, f.i > 0);
+  if (c == 0 || !(same & inside & 2u) || (same & inside & 1u)) return;
+  int more = __ffs(~(same >> 1)) - 1, c1 = c - 1 + more;  // ones from bit 1 on, of 31
+  for (bool all = more == 31; all;) {
+    const int k = c1 + 1 + lane;
+    const unsigned ones = __ballot_sync(0xffffffffu, k < C && p.info[k].live && p.info[k].tile == tile);
+    all = ones == 0xFFFFFFFFu;
+    more = all ? 32 : __ffs(~ones) - 1;
+    c1 += more;
   }
-  if (lane == 31) s_scan[0][warp] = before;
-  before = __shfl_up_sync(0xffffffffu, before, 1);
-  if (lane == 0) before = -1;
-  __syncthreads();
-  for (int w = 0; w < warp; ++w) before = max(before, s_scan[0][w]);
-  // Run t is its tile's second if it starts inside the tile and the live run
-  // before it does not, or does at the first unit; the runs after it that
-  // start in the tile follow one another.
-  const bool inside = live && f.i > 0 && before >= 0;
-  const bool second = inside && !(s_info[max(before, 0)].tile == f.tile && s_info[max(before, 0)].i > 0);
-  int head = second ? t : -1;  // the second run of the tile that run t starts inside
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, head, o);
-    if (lane >= o) head = max(head, x);
-  }
-  if (lane == 31) s_scan[1][warp] = head;
-  __syncthreads();
-  for (int w = 0; w < warp; ++w) head = max(head, s_scan[1][w]);
-  if (inside && head >= 0) atomicMax(&s_c1[head], t);
-  __syncthreads();
-  const int r = p.Hq / p.Hkv, D = p.D, rows = kRows * p.ctas;
-  int items = 0;
-  if (second) {
-    const int n = ld(p.offsets + f.b + 1) - ld(p.offsets + f.b), there = min(rows, n * r - f.rt * rows);
-    s_c0[t] = before;
-    items = s_c1[t] - before + 1 > kFewStates ? there : (there + kMergeWarps - 1) / kMergeWarps;
-  }
-  int sum = items;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, sum, o);
-    if (lane >= o) sum += x;
-  }
-  if (lane == 31) s_scan[0][warp] = sum;
-  __syncthreads();
-  for (int w = 0; w < warp; ++w) sum += s_scan[0][w];
-  s_items[t + 1] = sum;
-  if (t == 0) s_items[0] = 0;
-  __syncthreads();
-  for (int item = blockIdx.x; item < s_items[kMergeThreads]; item += gridDim.x) {
-    int c = 0;  // the last run with s_items[c] <= item
-#pragma unroll
-    for (int o = kMergeThreads / 2; o > 0; o >>= 1)
-      if (s_items[c + o] <= item) c += o;
-    const RunInfo g = s_info[c];
-    const int c0 = s_c0[c], c1 = s_c1[c], lo = ld(p.offsets + g.b), n = ld(p.offsets + g.b + 1) - lo;
-    const bool shared = c1 - c0 + 1 > kFewStates;
-    const int row = shared ? item - s_items[c] : (item - s_items[c]) * kMergeWarps + warp;
-    const int rho = g.rt * rows + row, tok = rho / r;
-    const bool there = row < rows && rho < n * r && ld(p.lens + g.b) - n + tok >= 0;
-    const float* first = p.part + (size_t)(2 * c0 + 1) * slot_floats(D, rows);
-    const float* rest = p.part + (size_t)(2 * c0) * slot_floats(D, rows);
-    auto state = [&](int k) {  // of run c0 + k
-      return k == 0 ? first : rest + (size_t)2 * k * slot_floats(D, rows);
-    };
+  const int g_b = __shfl_sync(0xffffffffu, f.b, 1), g_g = __shfl_sync(0xffffffffu, f.g, 1);
+  const int g_rt = __shfl_sync(0xffffffffu, f.rt, 1), c0 = c - 1;
+  const int r = p.Hq / p.Hkv, D = p.D, rows = kRows * p.ctas, states = c1 - c0 + 1;
+  const int lo = ld(p.offsets + g_b), n = ld(p.offsets + g_b + 1) - lo, len = ld(p.lens + g_b);
+  const int live = min(rows, n * r - g_rt * rows);
+  const bool shared = live <= kFewRows && states > kFewStates;
+  const float* first = p.part + (size_t)(2 * c0 + 1) * slot_floats(D, rows);
+  const float* rest = p.part + (size_t)(2 * c0) * slot_floats(D, rows);
+  auto state = [&](int k) {  // of run c0 + k
+    return k == 0 ? first : rest + (size_t)2 * k * slot_floats(D, rows);
+  };
+  const int from = shared ? warp : 0, step = shared ? kMergeWarps : 1;
+  for (int row = shared ? (int)blockIdx.y : (int)blockIdx.y * kMergeWarps + warp; row < live;
+       row += shared ? kMergeBlocks : kMergeBlocks * kMergeWarps) {
+    const int rho = g_rt * rows + row, tok = rho / r;
+    if (len - n + tok < 0) continue;
     float M = kMinusBig, L = 0.f;
     float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-    const int states = c1 - c0 + 1;
-    if (there) {
-      // lane k weighs states k, 32 + k, ...
-      for (int k = lane; k < states; k += 32) M = fmaxf(M, __ldcg(state(k) + (size_t)D * rows + row));
+    // lane k weighs states k, 32 + k, ...
+    for (int k = lane; k < states; k += 32) M = fmaxf(M, __ldcg(state(k) + (size_t)D * rows + row));
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      const int from = shared ? warp : 0, step = shared ? kMergeWarps : 1;
-      for (int base = 0; base < states; base += 32 * step) {
-        const int mine = base + from + lane * step;
-        float e = 0.f;
-        if (mine < states) {
-          e = ex2((__ldcg(state(mine) + (size_t)D * rows + row) - M) * p.scale_log2);
-          L += __ldcg(state(mine) + (size_t)(D + 1) * rows + row) * e;
-        }
-        const int count = min(32, (states - base - from + step - 1) / step);
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int base = 0; base < states; base += 32 * step) {
+      const int mine = base + from + lane * step;
+      float e = 0.f;
+      if (mine < states) {
+        e = ex2((__ldcg(state(mine) + (size_t)D * rows + row) - M) * p.scale_log2);
+        L += __ldcg(state(mine) + (size_t)(D + 1) * rows + row) * e;
+      }
+      const int count = min(32, (states - base - from + step - 1) / step);
 #pragma unroll 4
-        for (int k = 0; k < count; ++k) {
-          const float w = __shfl_sync(0xffffffffu, e, k);
-          const float* o = state(base + from + k * step) + (size_t)row * D;
+      for (int k = 0; k < count; ++k) {
+        const float w = __shfl_sync(0xffffffffu, e, k);
+        const float* o = state(base + from + k * step) + (size_t)row * D;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int d = 4 * lane + 128 * i;
-            if (d < D) {
-              const float4 x = __ldcg(reinterpret_cast<const float4*>(o + d));
-              acc[i].x = fmaf(w, x.x, acc[i].x), acc[i].y = fmaf(w, x.y, acc[i].y);
-              acc[i].z = fmaf(w, x.z, acc[i].z), acc[i].w = fmaf(w, x.w, acc[i].w);
-            }
+        for (int i = 0; i < 2; ++i) {
+          const int d = 4 * lane + 128 * i;
+          if (d < D) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(o + d));
+            acc[i].x = fmaf(w, x.x, acc[i].x), acc[i].y = fmaf(w, x.y, acc[i].y);
+            acc[i].z = fmaf(w, x.z, acc[i].z), acc[i].w = fmaf(w, x.w, acc[i].w);
           }
         }
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     }
-    uint16_t* out = p.o + ((size_t)(lo + tok) * p.Hq + (size_t)g.g * r + rho - tok * r) * D;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    uint16_t* out = p.o + ((size_t)(lo + tok) * p.Hq + (size_t)g_g * r + rho - tok * r) * D;
     if (!shared) {
-      if (!there) continue;
       const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -1055,7 +1124,7 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeBlocks) paged_merge_kerne
       if (4 * lane + 128 * i < D) *reinterpret_cast<float4*>(&s_acc[warp][4 * lane + 128 * i]) = acc[i];
     if (lane == 0) s_l[warp] = L;
     __syncthreads();
-    if (there && t < D) {
+    if (t < D) {
       float l = 0.f, o = 0.f;
 #pragma unroll
       for (int w = 0; w < kMergeWarps; ++w) {
@@ -1096,16 +1165,18 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// 3-D map of a pool [n_pages Hkv][page][D] with boxes of `rows` positions by 64
-// head dims in the 128-byte swizzle; pages past the pool read as zeros.
-cudaError_t pool_map(CUtensorMap* m, const void* base, const moe_paged_shape& s, int rows) {
+// 4-D map of a pool [n_pages Hkv][page][D], the head dims as D / 64 slabs of 64
+// outside the positions, with boxes of `rows` positions by `slabs` slabs, or of a
+// page's by one where it has fewer, in the 128-byte swizzle; pages past the pool
+// read as zeros.
+cudaError_t pool_map(CUtensorMap* m, const void* base, const moe_paged_shape& s, int rows, int slabs) {
   auto fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
-  const cuuint64_t dims[3] = {(cuuint64_t)s.D, (cuuint64_t)s.page, (cuuint64_t)s.n_pages * s.Hkv};
-  const cuuint64_t strides[2] = {(cuuint64_t)s.D * 2, (cuuint64_t)s.page * s.D * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)(rows < s.page ? rows : s.page), 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+  const cuuint64_t dims[4] = {64, (cuuint64_t)s.page, (cuuint64_t)s.D / 64, (cuuint64_t)s.n_pages * s.Hkv};
+  const cuuint64_t strides[3] = {(cuuint64_t)s.D * 2, 128, (cuuint64_t)s.page * s.D * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)(rows < s.page ? rows : s.page), (cuuint32_t)(rows <= s.page ? slabs : 1), 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
@@ -1141,7 +1212,8 @@ moe_status attn(const moe_paged_shape* shape, const void* q, const moe_paged_cac
   const Params prm{static_cast<const uint16_t*>(q), offsets, lens, cache->tables,
                    reinterpret_cast<const unsigned long long*>(tree), static_cast<uint16_t*>(o), part, info, flags,
                    scale * kLog2e, s.B, s.T, s.Hq, s.Hkv, page_shift(s.page), s.n_pages, s.max_pages, s.tree_words,
-                   s.q_stride ? s.q_stride : s.Hq * s.D, ((1ull << 36) + r - 1) / r, stalled, timeout_ns};
+                   s.q_stride ? s.q_stride : s.Hq * s.D, ((1ull << 36) + r - 1) / r,
+                   (long long)s.T * s.Hq > 32ll * s.B * s.Hkv ? kTileCost : kFewRowsCost, stalled, timeout_ns};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1160,8 +1232,8 @@ moe_status attn(const moe_paged_shape* shape, const void* q, const moe_paged_cac
     const auto kernel = paged_attn_kernel<decltype(d)::value, decltype(n)::value>;
     static SmemLimitMemo smem_memo;
     CUtensorMap tk, tv;
-    cudaError_t e = pool_map(&tk, cache->k_pages, s, F::kKeyRows);
-    if (e == cudaSuccess) e = pool_map(&tv, cache->v_pages, s, F::kKeysV);
+    cudaError_t e = pool_map(&tk, cache->k_pages, s, F::kKeyRows, F::kSlabsK);
+    if (e == cudaSuccess) e = pool_map(&tv, cache->v_pages, s, F::kKeysV, F::kDimsV / 64);
     if (e == cudaSuccess) e = ensure_smem(kernel, F::kBytes, &smem_memo);
     if (e != cudaSuccess) return e;
     cfg.dynamicSmemBytes = F::kBytes;
@@ -1176,7 +1248,7 @@ moe_status attn(const moe_paged_shape* shape, const void* q, const moe_paged_cac
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
   const MergeParams mp{offsets, lens, part, info, flags, static_cast<uint16_t*>(o), status, scale * kLog2e,
                        s.Hq, s.Hkv, s.D, runs, ctas};
-  cfg.gridDim = dim3((unsigned)(sms * kMergeBlocks));
+  cfg.gridDim = dim3((unsigned)runs + 1, kMergeBlocks);
   cfg.numAttrs = 1;
   cfg.blockDim = dim3(kMergeThreads);
   cfg.dynamicSmemBytes = 0;
