@@ -77,6 +77,7 @@ constexpr int kMaxCtas = 256;  // workspace bound on the grid
 constexpr int kTileCost = 3, kFewRowsCost = 1;
 constexpr float kMinusBig = -3.402823466e38f;  // running-max start, finite: m - m_new is never NaN
 constexpr float kSlack = 8.f;                  // a row's scores may pass its m by this much (base 2): weights to 2^8
+constexpr int kFewRows = 16;              // up to which rows of a tile are written, and joined, one by one
 constexpr uint32_t kColS = 256;           // S buffers at columns 256 and 384, O from 0
 constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);  // A and B format in an instruction descriptor
 
@@ -138,11 +139,15 @@ struct Ctl {
   float mx[2][2][kRows];  // [unit parity][half]
 };
 
-// Where a block's run starts, for the merge kernel.
-struct RunInfo {
+// Where a block's run starts, for the merge kernel: what every block of it reads
+// of every run, and what it reads of the tiles that it joins.
+struct __align__(8) RunHead {
   int tile;  // number of its first unit's tile
-  int live;  // the run has units
-  int b, g, rt, i;
+  int what;  // 0: no units; else 1, + 2 if it starts inside the tile, + 4 x the tile's rows
+};
+struct __align__(16) RunInfo {
+  int g, rt, unused0, unused1;
+  int lo, n, len, unused2;  // of its sequence
 };
 
 struct Params {
@@ -153,7 +158,8 @@ struct Params {
   const unsigned long long* tree;  // null: causal
   uint16_t* o;
   float* part;    // two slots per run of [tile rows][D] O, then [tile rows] m and L
-  RunInfo* info;  // per run
+  RunHead* head;  // per run
+  RunInfo* info;
   int32_t* flags;  // per block
   float scale_log2;
   int B, T, Hq, Hkv, shift, n_pages, max_pages, words, q_stride;
@@ -212,82 +218,68 @@ struct Cursor {
 __device__ __forceinline__ int place_k(int u, bool ahead_before) { return 2 * u - (ahead_before ? 1 : 0); }
 __device__ __forceinline__ int place_v(int u, bool ahead) { return 2 * u + 1 + (ahead ? 1 : 0); }
 
-// find_run for calls of up to 256 sequences of one row tile each, by one warp: the
-// starts of runs c and c + 1. Its sums are those of find_run in 32 bits; calls
-// that it does not take (more tiles, larger sums, more sequences) are left to
-// find_run. Lane k has kPer sequences from kPer k on, all asked for at once. (A
-// decode step of 64 sequences: TODO us.)
-__device__ __forceinline__ bool find_small(const Params& p, int r, int RT, int cost, int c, int C, Place* out,
-                                           long long* next, bool* ok) {
-  constexpr int kPer = 8;
-  const int lane = threadIdx.x & 31;
-  if (p.B > 32 * kPer) return false;
-  const int per = (p.B + 31) >> 5, b0 = lane * per;
-  int at[kPer + 1], len[kPer];
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    at[j] = len[j] = 0;
-    if (j < per && b0 + j < p.B) at[j] = ld(p.offsets + b0 + j), len[j] = ld(p.lens + b0 + j);
-  }
-  const int end = b0 < p.B ? ld(p.offsets + min(b0 + per, p.B)) : 0;
+// find_run for calls of up to kSmall sequences of one row tile each, by one warp:
+// the starts of runs c and c + 1, from the tables in shared memory. Its sums are
+// those of find_run in 32 bits; calls that it does not take (more tiles, larger
+// sums) are left to find_run. Lane k has `per` sequences from per k on.
+constexpr int kSmall = 256;
+__device__ __forceinline__ bool find_small(const Params& p, const int* offsets, const int* lens, int r, int RT, int cost,
+                                           int c, int C, Place* out, long long* next, bool* ok) {
+  const int lane = threadIdx.x & 31, per = (p.B + 31) >> 5, b0 = lane * per, b1 = min(b0 + per, p.B);
   bool bad = false, wide = false;
   int v = 0, w = 0, t = 0;  // this lane's places, units, tiles, per KV head
-#pragma unroll
-  for (int j = 0; j < kPer; ++j)
-    if (j < per && b0 + j < p.B) {
-      const int hi = j + 1 < per && b0 + j + 1 < p.B ? at[j + 1 < kPer ? j + 1 : j] : end, n = hi - at[j];
-      bad |= kv8::offsets_bad(at[j], hi, b0 + j, p.B, p.T) || len[j] < 0 || len[j] > p.max_pages << p.shift;
-      wide |= n * (long long)r > RT;
-      const int nb = n > 0 && len[j] > 0 ? (len[j] + kKeys - 1) / kKeys : 0;  // the last row sees len positions
-      v += nb > 0 ? nb + cost : 0;
-      w += nb;
-      t += n > 0;
-    }
+  auto units_of = [&](int b) {  // the last row sees len positions
+    return offsets[b + 1] > offsets[b] ? (lens[b] + kKeys - 1) / kKeys : 0;
+  };
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    const int lo = offsets[b], hi = offsets[b + 1], len = lens[b];
+    bad |= kv8::offsets_bad(lo, hi, b, p.B, p.T) || len < 0 || len > p.max_pages << p.shift;
+    wide |= (hi - lo) * (long long)r > RT;
+    const int nb = units_of(b);
+    v += nb > 0 ? nb + cost : 0;
+    w += nb;
+    t += hi > lo;
+  }
   *ok = !__any_sync(0xffffffffu, bad);
   if (!*ok) return true;
   const long long most = (long long)((p.max_pages << p.shift) / kKeys + 1 + cost) * p.Hkv * p.B;
   if (__any_sync(0xffffffffu, wide) || most > 0x7FFFFFFFll) return false;
   int vi = v, wi = w, ti = t;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll 1
+  for (int o = 1; o < min(p.B, 32); o <<= 1) {
     const int x = __shfl_up_sync(0xffffffffu, vi, o), y = __shfl_up_sync(0xffffffffu, wi, o);
     const int z = __shfl_up_sync(0xffffffffu, ti, o);
     if (lane >= o) vi += x, wi += y, ti += z;
   }
-  const int N = __shfl_sync(0xffffffffu, vi, 31) * p.Hkv, each = N / C, more = N - each * C;
+  const int last = min(p.B, 32) - 1;  // the last lane that the sums reach
+  const int N = __shfl_sync(0xffffffffu, vi, last) * p.Hkv, each = N / C, more = N - each * C;
   Place k{};
   k.b = -1;
-  k.units = *next = (long long)__shfl_sync(0xffffffffu, wi, 31) * p.Hkv;
+  k.units = *next = (long long)__shfl_sync(0xffffffffu, wi, last) * p.Hkv;
 #pragma unroll 1
   for (int e = 0; e < 2; ++e) {
     const int from = (c + e) * each + min(c + e, more);
     const unsigned hit = __ballot_sync(0xffffffffu, vi * p.Hkv > from);
     if (hit == 0u) break;  // the end: all units are before it
     const int L = __ffs(hit) - 1;
-    // the lane that has the sequence goes through its own
-    int places = (vi - v) * p.Hkv, units = (wi - w) * p.Hkv, tiles = (ti - t) * p.Hkv, b = -1, lo = 0, nn = 0, ln = 0;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (j < per && b0 + j < p.B && b < 0) {
-        const int hi = j + 1 < per && b0 + j + 1 < p.B ? at[j + 1 < kPer ? j + 1 : j] : end, n = hi - at[j];
-        const int nb = n > 0 && len[j] > 0 ? (len[j] + kKeys - 1) / kKeys : 0, size = nb > 0 ? (nb + cost) * p.Hkv : 0;
-        if (places + size > from) {
-          b = b0 + j, lo = at[j], nn = n, ln = len[j];
-        } else {
-          places += size, units += nb * p.Hkv, tiles += n > 0 ? p.Hkv : 0;
-        }
-      }
-    ln = __shfl_sync(0xffffffffu, ln, L);
-    const int nb = (ln + kKeys - 1) / kKeys, size = nb + cost, off = from - __shfl_sync(0xffffffffu, places, L);
-    const int g = off / size, i = max(off - g * size - cost, 0);
-    const int before = __shfl_sync(0xffffffffu, units, L) + g * nb + i;
+    // through lane L's sequences, by all lanes alike
+    int off = from - __shfl_sync(0xffffffffu, vi - v, L) * p.Hkv, units = __shfl_sync(0xffffffffu, wi - w, L) * p.Hkv;
+    int tiles = __shfl_sync(0xffffffffu, ti - t, L) * p.Hkv, b = L * per, nb = units_of(b);
+    while (nb == 0 || off >= (nb + cost) * p.Hkv) {
+      off -= nb > 0 ? (nb + cost) * p.Hkv : 0;
+      units += nb * p.Hkv;
+      tiles += offsets[b + 1] > offsets[b] ? p.Hkv : 0;
+      nb = units_of(++b);
+    }
+    const int g = off / (nb + cost), i = max(off - g * (nb + cost) - cost, 0);
+    units += g * nb + i;
     if (e == 0) {
-      k.b = __shfl_sync(0xffffffffu, b, L), k.g = g, k.rt = 0, k.i = i, k.nb = nb;
-      k.tile = __shfl_sync(0xffffffffu, tiles, L) + g;
-      k.lo = __shfl_sync(0xffffffffu, lo, L), k.n = __shfl_sync(0xffffffffu, nn, L), k.len = ln;
-      k.units = before;
+      k.b = b, k.g = g, k.rt = 0, k.i = i, k.nb = nb, k.tile = tiles + g;
+      k.lo = offsets[b], k.n = offsets[b + 1] - k.lo, k.len = lens[b];
+      k.units = units;
     } else {
-      *next = before;
+      *next = units;
     }
   }
   *out = k;
@@ -356,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ long long s_unit[2];  // units before the run's start and end
   __shared__ Cursor s_cur;
   __shared__ int s_bad, s_tile;
+  __shared__ int s_offsets[kSmall + 1], s_lens[kSmall];
 
   // The warp's number through a shuffle, which the compiler knows to be
   // uniform: the roles' loops then run on uniform registers, where the MMA
@@ -404,11 +397,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   // run, or have ended, before it starts.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (p.B <= kSmall) {
+    if (threadIdx.x <= p.B) s_offsets[threadIdx.x] = ld(p.offsets + threadIdx.x);
+    if (threadIdx.x < p.B) s_lens[threadIdx.x] = ld(p.lens + threadIdx.x);
+    __syncthreads();
+  }
   if (warp == 1 || warp == 2) {  // the run's start and its end
     Place k;
-    long long next;
-    bool ok;
-    const bool small = find_small(p, r, kTileRows, p.cost, c, C, &k, &next, &ok);
+    long long next = 0;
+    bool ok = false;
+    const bool small = p.B <= kSmall && find_small(p, s_offsets, s_lens, r, kTileRows, p.cost, c, C, &k, &next, &ok);
     if (!small)
       ok = find_run(p.offsets, p.lens, p.B, p.T, p.Hkv, p.max_pages << p.shift, r, kTileRows, kKeys, p.cost, c + warp - 1, C,
                     &k);
@@ -442,7 +440,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     const bool live = !s_bad && s_unit[0] < s_unit[1];
-    if (rank == 0) p.info[c] = RunInfo{s_tile, live, s_cur.b, s_cur.g, s_cur.rt, s_cur.i};
+    if (rank == 0) {
+      p.head[c] = RunHead{s_tile, live ? 1 + (s_cur.i > 0 ? 2 : 0) + 4 * min(kTileRows, s_cur.n * r - s_cur.rt * kTileRows) : 0};
+      p.info[c] = RunInfo{s_cur.g, s_cur.rt, 0, 0, s_cur.lo, s_cur.n, s_cur.len, 0};
+    }
     if (!live) p.flags[blockIdx.x] = s_bad ? (int32_t)MOE_ERR_INVALID_ARG : 0;
   }
   const bool idle = s_bad || s_unit[0] >= s_unit[1];  // both blocks of a run alike
@@ -629,54 +630,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (id != -2 && (id < 0 || id >= p.n_pages)) bad = true;
       return id < 0 || id >= p.n_pages ? outside : id * p.Hkv + g;
     };
-    auto load = [&](const CUtensorMap* map, const Box& b, int place, int h, int key, int slab, int first, int z) -> bool {
-      const int st = stage(place, h);
-      if (!warp_wait(&ctl->empty[st], phase(place, h) ^ 1u)) return false;
-      if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], kStageBytes);
-      const int at = __shfl_sync(0xffffffffu, z, many ? (key >> p.shift) & 31 : 0);
-      if (b.on) tma_load_4d(sR + st * kStageBytes + b.to, map, 0, (first + key) & (rows - 1), slab, at, &ctl->full[st]);
-      issued = place * F::kParts + h + 1;
-      return true;
-    };
-    auto load_k = [&](int place, int first, int z) -> bool {
-      bool ok = true;
-#pragma unroll
-      for (int h = 0; h < F::kParts; ++h)
-        ok = ok && load(&tm_k, bk, place, h, bk.key, bk.slab + h * F::kSlabsK, first, z);
-      return ok;
-    };
-    auto load_v = [&](int place, int first, int z) -> bool {
-      bool ok = true;
-#pragma unroll
-      for (int h = 0; h < F::kParts; ++h) ok = ok && load(&tm_v, bv, place, h, bv.key + h * F::kKeysV, bv.slab, first, z);
-      return ok;
-    };
     if ((int)blockIdx.x != p.stalled) {
-      Cursor k = cur;  // the unit after u
-      int first = k.i * kKeys, z = settle(first_page, k.g);
-      bool last = k.last(), ahead = false;
-      int id = -2;
-      auto step = [&](int u) {  // to the unit after u
-        if (u + 1 < U) {
-          k.advance(p, r, kTileRows);
-          id = look_up(k);
-        }
-      };
-      bool ok = load_k(0, first, z);
-      step(0);
+      // K and V of every unit in the order of their use, one copy of the code:
+      // it runs cold.
+      Cursor k = cur;        // unit ku
+      int id = first_page;   // its page
+      int ku = 0, vu = 0;    // units whose K, whose V has been asked for
+      bool kfirst = true;    // unit ku starts a tile (in this run)
+      int f0 = 0, z0 = 0, f1 = 0, z1 = 0;  // first position and page of units vu, vu + 1
+      bool ok = true;
 #pragma unroll 1
-      for (int u = 0; ok && u < U; ++u) {
-        const bool more = u + 1 < U;
-        const int first1 = k.i * kKeys, z1 = more ? settle(id, k.g) : 0;
-        const bool last1 = k.last();
-        ahead = more && !last;
-        if (ahead) ok = load_k(place_k(u + 1, true), first1, z1);
-        step(u + 1);  // its page numbers come while this unit's V waits for room
-        ok = ok && load_v(place_v(u, ahead), first, z);
-        if (ok && more && !ahead) ok = load_k(place_k(u + 1, false), first1, z1);
-        first = first1;
-        z = z1;
-        last = last1;
+      for (int place = 0; ok && place < 2 * U; ++place) {
+        const bool is_k = ku < U && (ku == vu || (ku == vu + 1 && !kfirst));
+        if (is_k) {
+          const int first = k.i * kKeys, z = settle(id, k.g);
+          if (ku == vu) f0 = first, z0 = z;
+          else f1 = first, z1 = z;
+        }
+        const bool second = is_k && ku != vu;
+        const int first = second ? f1 : f0, z = second ? z1 : z0;
+        const CUtensorMap* map = is_k ? &tm_k : &tm_v;
+        const int to = is_k ? bk.to : bv.to;
+        const bool on = is_k ? bk.on : bv.on;
+        int key = is_k ? bk.key : bv.key, slab = is_k ? bk.slab : bv.slab;
+#pragma unroll 1
+        for (int h = 0; h < F::kParts; ++h) {
+          const int st = stage(place, h);
+          ok = warp_wait(&ctl->empty[st], phase(place, h) ^ 1u);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], kStageBytes);
+          const int at = __shfl_sync(0xffffffffu, z, many ? (key >> p.shift) & 31 : 0);
+          if (on) tma_load_4d(sR + st * kStageBytes + to, map, 0, (first + key) & (rows - 1), slab, at, &ctl->full[st]);
+          issued = place * F::kParts + h + 1;
+          if (is_k) slab += F::kSlabsK;
+          else key += F::kKeysV;
+        }
+        if (is_k) {
+          kfirst = k.last();
+          if (++ku < U) {  // its page numbers come while this unit's V waits for room
+            k.advance(p, r, kTileRows);
+            id = look_up(k);
+          }
+        } else {
+          ++vu;
+          f0 = f1, z0 = z1;
+        }
       }
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) ctl->bad_page = 1;
@@ -872,21 +870,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             // 32 rows by 16 dims at a time, the same way; of rows that are there
             float* part = p.part + (size_t)(2 * c + (mid ? 0 : 1)) * slot_floats(D, kTileRows);
             const int rows = seq.y * r - place.y * kTileRows - rank * kRows - quad * 32;
-            float* prow = part + (size_t)(rank * kRows + quad * 32 + (lane >> 2)) * D + 4 * (lane & 3);
+            if (rows <= kFewRows) {  // a lane writes its own
 #pragma unroll 1
-            for (int j = d0; j < d0 + D / 2; j += 16) {
-              uint32_t v[16];
-              tmem_ld_16(lane_addr + j, v);
-              __syncwarp();
+              for (int j = d0; j < d0 + D / 2; j += 32) {
+                float v[32];
+                tmem_ld_32(lane_addr + j, v);
+                float4* to = reinterpret_cast<float4*>(part + (size_t)(rank * kRows + row) * D + j);
+                if (lane < rows) {
 #pragma unroll
-              for (int e = 0; e < 16; e += 4)
-                sts128(out + lane * F::kOutPitch + 4 * e, v[e], v[e + 1], v[e + 2], v[e + 3]);
-              __syncwarp();
+                  for (int e = 0; e < 8; ++e) to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                }
+              }
+            } else {
+              float* prow = part + (size_t)(rank * kRows + quad * 32 + (lane >> 2)) * D + 4 * (lane & 3);
+#pragma unroll 1
+              for (int j = d0; j < d0 + D / 2; j += 16) {
+                uint32_t v[16];
+                tmem_ld_16(lane_addr + j, v);
+                __syncwarp();
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (8 * k + (lane >> 2) < rows)
-                  *reinterpret_cast<uint4*>(prow + (size_t)(8 * k) * D + j) =
-                      lds128(out + (8 * k + (lane >> 2)) * F::kOutPitch + 16 * (lane & 3));
+                for (int e = 0; e < 16; e += 4)
+                  sts128(out + lane * F::kOutPitch + 4 * e, v[e], v[e + 1], v[e + 2], v[e + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  if (8 * k + (lane >> 2) < rows)
+                    *reinterpret_cast<uint4*>(prow + (size_t)(8 * k) * D + j) =
+                        lds128(out + (8 * k + (lane >> 2)) * F::kOutPitch + 16 * (lane & 3));
+              }
             }
             if (half == 0 && lane < rows) {
               part[(size_t)D * kTileRows + rank * kRows + row] = m;
@@ -1003,9 +1014,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 struct MergeParams {
-  const int32_t* offsets;
-  const int32_t* lens;
   const float* part;
+  const RunHead* head;
   const RunInfo* info;
   const int32_t* flags;
   uint16_t* o;
@@ -1014,117 +1024,167 @@ struct MergeParams {
   int Hq, Hkv, D, C, ctas;  // C: runs
 };
 
-constexpr int kMergeWarps = 8;
+constexpr int kMergeWarps = 16;
 constexpr int kMergeThreads = 32 * kMergeWarps;
-constexpr int kMergeBlocks = 16;  // of a run
-constexpr int kFewRows = 16;     // of a tile, each a whole block's ...
-constexpr int kFewStates = 4;    // ... if it has more states than these
+constexpr int kFewStates = 4;  // of a row, up to which a warp joins them alone
+static_assert(kMaxCtas <= kMergeThreads, "a thread per run");
 
-// Joins the partial states of the tiles that runs' borders cut: blocks (c, *) of
-// the tile that run c is the second in, a row by a whole block, the states dealt
-// out to its warps (decode over a long context has few rows and many states),
-// or 8 rows, a warp each (cut tiles of a prompt have many rows and few states).
-// The first run of a tile left its state in its second slot (a tile that the
-// run's end cuts), the others in their first. Blocks (C, 0) put down the call's
-// status.
-__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const MergeParams p) {
+// Joins the partial states of the tiles that runs' borders cut. Every block
+// finds out from the runs' heads which tiles those are, a run per thread, and
+// takes its share of their rows: a row by the whole block, the states dealt out
+// to its warps (decode over a long context has few rows and many states), or 16
+// rows, a warp each (cut tiles of a prompt have many rows and few states). The
+// first run of a tile left its state in its second slot (a tile that the run's
+// end cuts), the others in their first. A row's chain is two trips to memory:
+// the heads, then maxima, sums and the first values together. (A trip takes 0.7
+// us here, and more where many blocks read the same lines: 3 blocks per SM that read
+// all of the runs' places took a decode call of 26 us to 31.)
+__global__ void __launch_bounds__(kMergeThreads, 1) paged_merge_kernel(const MergeParams p) {
   __shared__ float s_l[kMergeWarps];
   __shared__ __align__(16) float s_acc[kMergeWarps][256];
+  __shared__ RunHead s_head[kMergeThreads + 1];
+  __shared__ unsigned s_ends[kMergeWarps];  // of runs: the next is not of the same tile
+  __shared__ int s_sum[kMergeWarps];
+  __shared__ int s_items[kMergeThreads + 1], s_c1[kMergeThreads];  // items before a run's tile's, the tile's last run
   __shared__ int s_first;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int C = p.C, c = blockIdx.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  if (c == C) {
-    // the outcome of the lowest-numbered grid block that failed
-    if (blockIdx.y != 0) return;
-    const int blocks = C * p.ctas;
-    if (t == 0) s_first = blocks;
+  const int C = p.C, t = threadIdx.x, lane = t & 31, warp = t >> 5, blocks = C * p.ctas;
+  int2 h = make_int2(-1, 0);
+  if (t < C) h = __ldcg(reinterpret_cast<const int2*>(p.head + t));
+  s_head[t + 1] = RunHead{h.x, h.y};
+  if (t == 0) s_head[0] = RunHead{-1, 0}, s_first = kMergeThreads, s_items[0] = 0;
+  if (blockIdx.x == 0) {
+    // the call's status: the outcome of the lowest-numbered block that failed
+    const int failed = t < blocks ? __ldcg(p.flags + t) : 0;
     __syncthreads();
-    for (int k = t; k < blocks; k += kMergeThreads)
-      if (__ldcg(p.flags + k) != 0) atomicMin(&s_first, k);
+    if (failed) atomicMin(&s_first, t);
     __syncthreads();
-    if (t == 0) *p.status = s_first == blocks ? 0 : __ldcg(p.flags + s_first);
-    return;
+    if (t == s_first) *p.status = failed;
+    if (t == 0 && s_first == kMergeThreads) *p.status = 0;
   }
-  // Run c is a tile's second if it starts inside it and run c - 1, which has the
-  // unit before, does not, or does at the first unit; the runs after it that start
-  // in the tile follow one another. (Lane k looks at run c - 1 + k.)
-  RunInfo f{};
-  if (c - 1 + lane >= 0 && c - 1 + lane < C) f = p.info[c - 1 + lane];
-  const int tile = __shfl_sync(0xffffffffu, f.tile, 1);
-  const unsigned same = __ballot_sync(0xffffffffu, f.live && f.tile == tile), inside = __ballot_sync(0xffffffffu, f.i > 0);
-  if (c == 0 || !(same & inside & 2u) || (same & inside & 1u)) return;
-  int more = __ffs(~(same >> 1)) - 1, c1 = c - 1 + more;  // ones from bit 1 on, of 31
-  for (bool all = more == 31; all;) {
-    const int k = c1 + 1 + lane;
-    const unsigned ones = __ballot_sync(0xffffffffu, k < C && p.info[k].live && p.info[k].tile == tile);
-    all = ones == 0xFFFFFFFFu;
-    more = all ? 32 : __ffs(~ones) - 1;
-    c1 += more;
+  __syncthreads();
+  // Run t is its tile's second if it starts inside the tile and run t - 1, which
+  // has the unit before, does not, or does at the first unit; the runs after it that
+  // start in the tile follow one another.
+  const RunHead before = s_head[t], next = t + 1 < kMergeThreads ? s_head[t + 2] : RunHead{-1, 0};
+  const bool second = (h.y & 2) != 0 && !((before.what & 2) != 0 && before.tile == h.x);
+  const unsigned ends = __ballot_sync(0xffffffffu, !(next.what != 0 && next.tile == h.x));
+  if (lane == 0) s_ends[warp] = ends;
+  __syncthreads();
+  int items = 0, c1 = t;
+  if (second) {
+    unsigned e = s_ends[warp] & (~0u << lane);
+    int w = warp;
+    while (e == 0u) e = s_ends[++w];  // (the last thread's next is none)
+    c1 = 32 * w + __ffs(e) - 1;
+    const int there = h.y >> 2;
+    items = there <= kFewRows && c1 - t + 2 > kFewStates ? there : (there + kMergeWarps - 1) / kMergeWarps;
   }
-  const int g_b = __shfl_sync(0xffffffffu, f.b, 1), g_g = __shfl_sync(0xffffffffu, f.g, 1);
-  const int g_rt = __shfl_sync(0xffffffffu, f.rt, 1), c0 = c - 1;
-  const int r = p.Hq / p.Hkv, D = p.D, rows = kRows * p.ctas, states = c1 - c0 + 1;
-  const int lo = ld(p.offsets + g_b), n = ld(p.offsets + g_b + 1) - lo, len = ld(p.lens + g_b);
-  const int live = min(rows, n * r - g_rt * rows);
-  const bool shared = live <= kFewRows && states > kFewStates;
-  const float* first = p.part + (size_t)(2 * c0 + 1) * slot_floats(D, rows);
-  const float* rest = p.part + (size_t)(2 * c0) * slot_floats(D, rows);
-  auto state = [&](int k) {  // of run c0 + k
-    return k == 0 ? first : rest + (size_t)2 * k * slot_floats(D, rows);
-  };
-  const int from = shared ? warp : 0, step = shared ? kMergeWarps : 1;
-  for (int row = shared ? (int)blockIdx.y : (int)blockIdx.y * kMergeWarps + warp; row < live;
-       row += shared ? kMergeBlocks : kMergeBlocks * kMergeWarps) {
-    const int rho = g_rt * rows + row, tok = rho / r;
-    if (len - n + tok < 0) continue;
-    float M = kMinusBig, L = 0.f;
-    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-    // lane k weighs states k, 32 + k, ...
-    for (int k = lane; k < states; k += 32) M = fmaxf(M, __ldcg(state(k) + (size_t)D * rows + row));
+  int sum = items;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    for (int base = 0; base < states; base += 32 * step) {
-      const int mine = base + from + lane * step;
-      float e = 0.f;
-      if (mine < states) {
-        e = ex2((__ldcg(state(mine) + (size_t)D * rows + row) - M) * p.scale_log2);
-        L += __ldcg(state(mine) + (size_t)(D + 1) * rows + row) * e;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += x;
+  }
+  if (lane == 31) s_sum[warp] = sum;
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    if (w == warp) sum += total;
+    total += s_sum[w];
+  }
+  s_items[t + 1] = sum;
+  s_c1[t] = c1;
+  __syncthreads();
+  const int r = p.Hq / p.Hkv, D = p.D, rows = kRows * p.ctas, wide = D > 128 ? 2 : 1;
+  const bool on = 4 * lane < D;
+  constexpr int kAhead = 8;  // states whose values are asked for at once
+  for (int item = blockIdx.x; item < total; item += gridDim.x) {
+    int c = 0;  // the last run with s_items[c] <= item
+#pragma unroll
+    for (int o = kMergeThreads / 2; o > 0; o >>= 1)
+      if (s_items[c + o] <= item) c += o;
+    const int c0 = c - 1, states = s_c1[c] - c0 + 1, there = s_head[c + 1].what >> 2;
+    const bool shared = there <= kFewRows && states > kFewStates;
+    const int row = shared ? item - s_items[c] : (item - s_items[c]) * kMergeWarps + warp;
+    if (row >= there) continue;  // (not where the block shares a row)
+    const int4 i0 = __ldcg(reinterpret_cast<const int4*>(p.info + c));  // g, rt
+    const int4 i1 = __ldcg(reinterpret_cast<const int4*>(p.info + c) + 1);  // lo, n, len
+    const float* first = p.part + (size_t)(2 * c0 + 1) * slot_floats(D, rows);
+    const float* rest = p.part + (size_t)(2 * c0) * slot_floats(D, rows);
+    auto state = [&](int k) {  // of run c0 + k
+      return k == 0 ? first : rest + (size_t)2 * k * slot_floats(D, rows);
+    };
+    const int from = shared ? warp : 0, step = shared ? kMergeWarps : 1;
+    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    float M = kMinusBig, L = 0.f;
+#pragma unroll 1
+    for (int base = 0; base < states; base += kAhead * step) {
+      float4 x[kAhead][2];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int s = base + from + k * step;
+        x[k][0] = x[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s < states && on) {
+          const float* o = state(s) + (size_t)row * D + 4 * lane;
+          x[k][0] = __ldcg(reinterpret_cast<const float4*>(o));
+          if (wide == 2) x[k][1] = __ldcg(reinterpret_cast<const float4*>(o + 128));
+        }
       }
-      const int count = min(32, (states - base - from + step - 1) / step);
-#pragma unroll 4
-      for (int k = 0; k < count; ++k) {
+      // lane k < kAhead: maximum and sum of the k-th of these
+      const int mine = base + from + lane * step;
+      const bool has = lane < kAhead && mine < states;
+      float m = kMinusBig, l = 0.f;
+      if (has) {
+        m = __ldcg(state(mine) + (size_t)D * rows + row);
+        l = __ldcg(state(mine) + (size_t)(D + 1) * rows + row);
+      }
+      if (base == 0) {  // the row's maximum, of all states
+#pragma unroll 1
+        for (int k = lane; k < states; k += 128) {
+          float top[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            top[q] = k + 32 * q < states ? __ldcg(state(k + 32 * q) + (size_t)D * rows + row) : kMinusBig;
+          M = fmaxf(fmaxf(M, fmaxf(top[0], top[1])), fmaxf(top[2], top[3]));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      }
+      const float e = has ? ex2((m - M) * p.scale_log2) : 0.f;
+      L += l * e;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
         const float w = __shfl_sync(0xffffffffu, e, k);
-        const float* o = state(base + from + k * step) + (size_t)row * D;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int d = 4 * lane + 128 * i;
-          if (d < D) {
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(o + d));
-            acc[i].x = fmaf(w, x.x, acc[i].x), acc[i].y = fmaf(w, x.y, acc[i].y);
-            acc[i].z = fmaf(w, x.z, acc[i].z), acc[i].w = fmaf(w, x.w, acc[i].w);
-          }
+          acc[i].x = fmaf(w, x[k][i].x, acc[i].x), acc[i].y = fmaf(w, x[k][i].y, acc[i].y);
+          acc[i].z = fmaf(w, x[k][i].z, acc[i].z), acc[i].w = fmaf(w, x[k][i].w, acc[i].w);
         }
       }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    uint16_t* out = p.o + ((size_t)(lo + tok) * p.Hq + (size_t)g_g * r + rho - tok * r) * D;
+    const int rho = i0.y * rows + row, tok = rho / r;
+    const bool sees = i1.z - i1.y + tok >= 0;  // (a query that sees nothing has its zeros already)
+    uint16_t* out = p.o + ((size_t)(i1.x + tok) * p.Hq + (size_t)i0.x * r + rho - tok * r) * D;
     if (!shared) {
       const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        if (4 * lane + 128 * i < D)
+        if (on && i < wide && sees)
           *reinterpret_cast<uint2*>(out + 4 * lane + 128 * i) =
               make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv), pack_bf16(acc[i].z * inv, acc[i].w * inv));
       continue;
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      if (4 * lane + 128 * i < D) *reinterpret_cast<float4*>(&s_acc[warp][4 * lane + 128 * i]) = acc[i];
+      if (on && i < wide) *reinterpret_cast<float4*>(&s_acc[warp][4 * lane + 128 * i]) = acc[i];
     if (lane == 0) s_l[warp] = L;
     __syncthreads();
-    if (t < D) {
+    if (t < D && sees) {
       float l = 0.f, o = 0.f;
 #pragma unroll
       for (int w = 0; w < kMergeWarps; ++w) {
@@ -1150,7 +1210,7 @@ int tile_blocks(const moe_paged_shape& s) {
 
 size_t workspace_bytes(const moe_paged_shape& s) {
   // as many slots of 128 rows for pairs as for single blocks
-  return 256 + kMaxCtas * (sizeof(int32_t) + sizeof(RunInfo)) + 2 * kMaxCtas * slot_floats(s.D, kRows) * sizeof(float);
+  return 256 + kMaxCtas * (sizeof(int32_t) + sizeof(RunHead) + sizeof(RunInfo)) + 2 * kMaxCtas * slot_floats(s.D, kRows) * sizeof(float);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -1206,11 +1266,12 @@ moe_status attn(const moe_paged_shape* shape, const void* q, const moe_paged_cac
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   int32_t* status = reinterpret_cast<int32_t*>(ws);
   int32_t* flags = reinterpret_cast<int32_t*>(ws + 256);
-  RunInfo* info = reinterpret_cast<RunInfo*>(ws + 256 + kMaxCtas * sizeof(int32_t));
-  float* part = reinterpret_cast<float*>(ws + 256 + kMaxCtas * (sizeof(int32_t) + sizeof(RunInfo)));
+  RunHead* head = reinterpret_cast<RunHead*>(flags + kMaxCtas);
+  RunInfo* info = reinterpret_cast<RunInfo*>(head + kMaxCtas);
+  float* part = reinterpret_cast<float*>(info + kMaxCtas);
   const int r = s.Hq / s.Hkv;
   const Params prm{static_cast<const uint16_t*>(q), offsets, lens, cache->tables,
-                   reinterpret_cast<const unsigned long long*>(tree), static_cast<uint16_t*>(o), part, info, flags,
+                   reinterpret_cast<const unsigned long long*>(tree), static_cast<uint16_t*>(o), part, head, info, flags,
                    scale * kLog2e, s.B, s.T, s.Hq, s.Hkv, page_shift(s.page), s.n_pages, s.max_pages, s.tree_words,
                    s.q_stride ? s.q_stride : s.Hq * s.D, ((1ull << 36) + r - 1) / r,
                    (long long)s.T * s.Hq > 32ll * s.B * s.Hkv ? kTileCost : kFewRowsCost, stalled, timeout_ns};
@@ -1246,9 +1307,10 @@ moe_status attn(const moe_paged_shape* shape, const void* q, const moe_paged_cac
   else if (s.D == 128) e = ctas == 2 ? go(std::integral_constant<int, 128>{}, Two{}) : go(std::integral_constant<int, 128>{}, One{});
   else e = ctas == 2 ? go(std::integral_constant<int, 256>{}, Two{}) : go(std::integral_constant<int, 256>{}, One{});
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
-  const MergeParams mp{offsets, lens, part, info, flags, static_cast<uint16_t*>(o), status, scale * kLog2e,
+  const MergeParams mp{part, head, info, flags, static_cast<uint16_t*>(o), status, scale * kLog2e,
                        s.Hq, s.Hkv, s.D, runs, ctas};
-  cfg.gridDim = dim3((unsigned)runs + 1, kMergeBlocks);
+  const long long most = (long long)s.T * s.Hq;  // rows that may have to be joined
+  cfg.gridDim = dim3((unsigned)(most < sms ? most : sms));
   cfg.numAttrs = 1;
   cfg.blockDim = dim3(kMergeThreads);
   cfg.dynamicSmemBytes = 0;
