@@ -505,12 +505,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     // comes after the leader's step of unit u: two barriers in turn will do.)
     auto ready = [&](int place, int u, uint64_t* own, uint32_t parity, uint64_t* peer, bool fixed) -> bool {
       bool all = own == nullptr || mbar_test_wait(own, parity);
+      // A block on its own takes its stages one by one, as they come (part()).
+      if (kCtas == 2) {
 #pragma unroll
-      for (int h = 0; h < F::kParts; ++h) all = mbar_test_wait(&ctl->full[stage(place, h)], phase(place, h)) && all;
+        for (int h = 0; h < F::kParts; ++h) all = mbar_test_wait(&ctl->full[stage(place, h)], phase(place, h)) && all;
+      }
       const bool listens = kCtas == 2 && rank == 0;
       if (listens) all = test_cluster(peer, (u >> 1) & 1) && all;
       if (fixed || !__all_sync(0xffffffffu, all)) {
-        for (int h = 0; h < F::kParts; ++h)
+        for (int h = 0; (kCtas == 2 || fixed) && h < F::kParts; ++h)
           if (!warp_wait(&ctl->full[stage(place, h)], phase(place, h))) return false;
         if (fixed && lane == 0) mbar_arrive(&ctl->look);
         if (own != nullptr && !warp_wait(own, parity)) return false;
@@ -527,6 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return true;
     };
+    auto part = [&](int place, int h) { return kCtas == 2 || warp_wait(&ctl->full[stage(place, h)], phase(place, h)); };
     auto score = [&](int u, bool first, bool ends) -> bool {  // S of unit u
       const int place = place_k(u, ahead >> ((u - 1) & 1) & 1u);
       if (!ready(place, u, first ? &ctl->q_full : nullptr, tq & 1, &ctl->peer_s[u & 1], false)) return false;
@@ -536,6 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int h = 0; h < F::kParts; ++h) {
         const int st = stage(place, h);
+        if (!part(place, h)) return false;
 #pragma unroll
         for (int kk = 0; kk < 4 * F::kSlabsK; ++kk) {
           const uint32_t slab = kk >> 2, in = (kk & 3) * 2;  // 64-dim slabs
@@ -567,6 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int h = 0; h < F::kParts; ++h) {
         const int st = stage(place, h);
+        if (!part(place, h)) return false;
 #pragma unroll
         for (int kk = 0; kk < F::kKeysV / 16; ++kk)
           mma_ts<kCtas>(tmem, a + (h * F::kKeysV + kk * 16) / 2, dv + st * (kStageBytes / 16) + kk * (16 * 128 / 16),
