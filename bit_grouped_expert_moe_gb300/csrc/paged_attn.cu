@@ -164,7 +164,8 @@ struct Params {
   float scale_log2;
   int B, T, Hq, Hkv, shift, n_pages, max_pages, words, q_stride;
   unsigned long long rmagic;  // ceil(2^36 / r), r = Hq / Hkv
-  int cost;  // places of a tile beyond its units
+  int cost;    // places of a tile beyond its units
+  int narrow;  // find_small and find_tiles serve the call
   int stalled;
   long long timeout_ns;
 };
@@ -218,10 +219,14 @@ struct Cursor {
 __device__ __forceinline__ int place_k(int u, bool ahead_before) { return 2 * u - (ahead_before ? 1 : 0); }
 __device__ __forceinline__ int place_v(int u, bool ahead) { return 2 * u + 1 + (ahead ? 1 : 0); }
 
-// find_run for calls of up to kSmall sequences of one row tile each, by one warp:
-// the starts of runs c and c + 1, from the tables in shared memory. Its sums are
-// those of find_run in 32 bits; calls that it does not take (more tiles, larger
-// sums) are left to find_run. Lane k has `per` sequences from per k on.
+// find_run for calls whose tables the block has in shared memory and whose sums
+// the host knows to fit 32 bits (Params::narrow): the starts of runs c and c + 1, by
+// one warp. Every instruction here runs once, and cold, which is 5 to 10 cycles
+// each; find_run's closed forms and 64-bit divisions are 1.6 us of a token's call
+// and 5 of a prompt's.
+//
+// This one is for sequences of one row tile each (false: some have more). Lane k
+// has `per` sequences from per k on.
 constexpr int kSmall = 256;
 __device__ __forceinline__ bool find_small(const Params& p, const int* offsets, const int* lens, int r, int RT, int cost,
                                            int c, int C, Place* out, long long* next, bool* ok) {
@@ -243,8 +248,7 @@ __device__ __forceinline__ bool find_small(const Params& p, const int* offsets, 
   }
   *ok = !__any_sync(0xffffffffu, bad);
   if (!*ok) return true;
-  const long long most = (long long)((p.max_pages << p.shift) / kKeys + 1 + cost) * p.Hkv * p.B;
-  if (__any_sync(0xffffffffu, wide) || most > 0x7FFFFFFFll) return false;
+  if (__any_sync(0xffffffffu, wide)) return false;
   int vi = v, wi = w, ti = t;
 #pragma unroll 1
   for (int o = 1; o < min(p.B, 32); o <<= 1) {
@@ -284,6 +288,86 @@ __device__ __forceinline__ bool find_small(const Params& p, const int* offsets, 
   }
   *out = k;
   return true;
+}
+
+// The same for sequences of several tiles, up to kSmallTiles in all, which the warp
+// goes through 32 at a time: first for every sequence's sums, then for the tile
+// of either start.
+constexpr int kSmallTiles = 2048;
+__device__ __forceinline__ void find_tiles(const Params& p, const int* offsets, const int* lens, int2* sums, int r, int RT,
+                                           int cost, int c, int C, Place* out, long long* next) {
+  const int lane = threadIdx.x & 31;
+  int N = 0, all_units = 0;
+#pragma unroll 1
+  for (int b = 0; b < p.B; ++b) {
+    const int n = offsets[b + 1] - offsets[b], len = lens[b], tiles = seq_tiles(n, r, RT);
+    int v = 0, w = 0;
+#pragma unroll 1
+    for (int rt = lane; rt < tiles; rt += 32) {
+      const int nb = tile_units(n, len, r, RT, kKeys, rt);
+      v += nb > 0 ? nb + cost : 0;
+      w += nb;
+    }
+    v = __reduce_add_sync(0xffffffffu, v);
+    w = __reduce_add_sync(0xffffffffu, w);
+    if (lane == 0) sums[b] = make_int2(v, w);
+    N += v * p.Hkv;
+    all_units += w * p.Hkv;
+  }
+  __syncwarp();
+  const int each = N / C, more = N - each * C;
+  Place k{};
+  k.b = -1;
+  k.units = *next = all_units;
+#pragma unroll 1
+  for (int e = 0; e < 2; ++e) {
+    int off = (c + e) * each + min(c + e, more);
+    if (off >= N) break;  // the end: all units are before it
+    int b = 0, units = 0, tile = 0, n, len, tiles;
+    int2 sum;
+    while (true) {
+      n = offsets[b + 1] - offsets[b], len = lens[b], tiles = seq_tiles(n, r, RT), sum = sums[b];
+      if (off < sum.x * p.Hkv) break;
+      off -= sum.x * p.Hkv, units += sum.y * p.Hkv, tile += tiles * p.Hkv;
+      ++b;
+    }
+    const int g = off / sum.x;
+    off -= g * sum.x, units += g * sum.y, tile += g * tiles;
+    int nb, before, rt = 0;
+    unsigned hit;
+#pragma unroll 1
+    while (true) {
+      nb = rt + lane < tiles ? tile_units(n, len, r, RT, kKeys, rt + lane) : 0;
+      const int v = nb > 0 ? nb + cost : 0;
+      int vi = v;
+      before = nb;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, vi, o), y = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) vi += x, before += y;
+      }
+      before -= nb;
+      hit = __ballot_sync(0xffffffffu, vi > off);
+      const int at = hit != 0u ? __ffs(hit) - 1 : 31;
+      if (hit != 0u) {
+        off -= __shfl_sync(0xffffffffu, vi - v, at);
+        break;
+      }
+      off -= __shfl_sync(0xffffffffu, vi, 31);
+      units += __shfl_sync(0xffffffffu, before + nb, 31);
+      rt += 32;
+    }
+    const int at = __ffs(hit) - 1, i = max(off - cost, 0);
+    units += __shfl_sync(0xffffffffu, before, at) + i;
+    if (e == 0) {
+      k.b = b, k.g = g, k.rt = rt + at, k.i = i, k.nb = __shfl_sync(0xffffffffu, nb, at), k.tile = tile + rt + at;
+      k.lo = offsets[b], k.n = n, k.len = len;
+      k.units = units;
+    } else {
+      *next = units;
+    }
+  }
+  *out = k;
 }
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
@@ -349,6 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Cursor s_cur;
   __shared__ int s_bad, s_tile;
   __shared__ int s_offsets[kSmall + 1], s_lens[kSmall];
+  __shared__ int2 s_sums[kSmall];
 
   // The warp's number through a shuffle, which the compiler knows to be
   // uniform: the roles' loops then run on uniform registers, where the MMA
@@ -397,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // run, or have ended, before it starts.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (p.B <= kSmall) {
+  if (p.narrow) {
     if (threadIdx.x <= p.B) s_offsets[threadIdx.x] = ld(p.offsets + threadIdx.x);
     if (threadIdx.x < p.B) s_lens[threadIdx.x] = ld(p.lens + threadIdx.x);
     __syncthreads();
@@ -406,12 +491,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     Place k;
     long long next = 0;
     bool ok = false;
-    const bool small = p.B <= kSmall && find_small(p, s_offsets, s_lens, r, kTileRows, p.cost, c, C, &k, &next, &ok);
-    if (!small)
+    if (!p.narrow) {
       ok = find_run(p.offsets, p.lens, p.B, p.T, p.Hkv, p.max_pages << p.shift, r, kTileRows, kKeys, p.cost, c + warp - 1, C,
                     &k);
+    } else if (warp == 1) {
+      if (!find_small(p, s_offsets, s_lens, r, kTileRows, p.cost, c, C, &k, &next, &ok))
+        find_tiles(p, s_offsets, s_lens, s_sums, r, kTileRows, p.cost, c, C, &k, &next);
+      if (lane == 0) s_unit[1] = next;
+    }
     if (lane == 0) {
-      s_unit[warp - 1] = warp == 2 && small ? next : k.units;
+      if (warp == 1 || !p.narrow) s_unit[warp - 1] = k.units;
       if (warp == 1) {
         s_bad = !ok;
         Cursor cur{};
@@ -1214,6 +1303,13 @@ int tile_blocks(const moe_paged_shape& s) {
   return s.D >= 128 && (long long)s.T * s.Hq > 128ll * s.B * s.Hkv ? 2 : 1;
 }
 
+// Whether find_small and find_tiles serve a call: their tables hold its sequences,
+// its tiles are few enough and the places of all of them stay below 2^31.
+bool narrow(const moe_paged_shape& s, int rows) {
+  const long long tiles = (long long)s.T * (s.Hq / s.Hkv) / rows + s.B, units = (long long)s.max_pages * s.page / kKeys + 2;
+  return s.B <= kSmall && tiles <= kSmallTiles && tiles * s.Hkv * (units + kTileCost) <= 0x7FFFFFFFll;
+}
+
 size_t workspace_bytes(const moe_paged_shape& s) {
   // as many slots of 128 rows for pairs as for single blocks
   return 256 + kMaxCtas * (sizeof(int32_t) + sizeof(RunHead) + sizeof(RunInfo)) + 2 * kMaxCtas * slot_floats(s.D, kRows) * sizeof(float);
@@ -1280,7 +1376,8 @@ moe_status attn(const moe_paged_shape* shape, const void* q, const moe_paged_cac
                    reinterpret_cast<const unsigned long long*>(tree), static_cast<uint16_t*>(o), part, head, info, flags,
                    scale * kLog2e, s.B, s.T, s.Hq, s.Hkv, page_shift(s.page), s.n_pages, s.max_pages, s.tree_words,
                    s.q_stride ? s.q_stride : s.Hq * s.D, ((1ull << 36) + r - 1) / r,
-                   (long long)s.T * s.Hq > 32ll * s.B * s.Hkv ? kTileCost : kFewRowsCost, stalled, timeout_ns};
+                   (long long)s.T * s.Hq > 32ll * s.B * s.Hkv ? kTileCost : kFewRowsCost, narrow(s, kRows * ctas), stalled,
+                   timeout_ns};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
