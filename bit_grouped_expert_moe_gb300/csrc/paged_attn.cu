@@ -77,7 +77,6 @@ constexpr int kMaxCtas = 256;  // workspace bound on the grid
 constexpr int kTileCost = 3, kFewRowsCost = 1;
 constexpr float kMinusBig = -3.402823466e38f;  // running-max start, finite: m - m_new is never NaN
 constexpr float kSlack = 8.f;                  // a row's scores may pass its m by this much (base 2): weights to 2^8
-constexpr int kFewRows = 16;              // up to which rows of a tile are written, and joined, one by one
 constexpr uint32_t kColS = 256;           // S buffers at columns 256 and 384, O from 0
 constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);  // A and B format in an instruction descriptor
 
@@ -165,6 +164,7 @@ struct Params {
   int B, T, Hq, Hkv, shift, n_pages, max_pages, words, q_stride;
   unsigned long long rmagic;  // ceil(2^36 / r), r = Hq / Hkv
   int cost;    // places of a tile beyond its units
+  int by_row;  // layout of the partial states
   int narrow;  // find_small and find_tiles serve the call
   int stalled;
   long long timeout_ns;
@@ -527,22 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) s_bad = 1;
     __syncthreads();
   }
-  if (threadIdx.x == 0) {
-    const bool live = !s_bad && s_unit[0] < s_unit[1];
-    if (rank == 0) {
-      p.head[c] = RunHead{s_tile, live ? 1 + (s_cur.i > 0 ? 2 : 0) + 4 * min(kTileRows, s_cur.n * r - s_cur.rt * kTileRows) : 0};
-      p.info[c] = RunInfo{s_cur.g, s_cur.rt, 0, 0, s_cur.lo, s_cur.n, s_cur.len, 0};
-    }
-    if (!live) p.flags[blockIdx.x] = s_bad ? (int32_t)MOE_ERR_INVALID_ARG : 0;
-  }
   const bool idle = s_bad || s_unit[0] >= s_unit[1];  // both blocks of a run alike
-  // Queries that see nothing (more queries than positions): o = 0.
-  for (int b = blockIdx.x; !s_bad && b < p.B; b += gridDim.x) {
-    const int lo = ld(p.offsets + b), hi = ld(p.offsets + b + 1), len = ld(p.lens + b);
-    const size_t pieces = (size_t)max(0, hi - lo - len) * p.Hq * (D / 8);
-    uint4* z = reinterpret_cast<uint4*>(p.o + (size_t)lo * p.Hq * D);
-    for (size_t i = threadIdx.x; i < pieces; i += kThreads) z[i] = make_uint4(0u, 0u, 0u, 0u);
-  }
   // A lane's page of a unit, as the table has it: -2 where the unit has no position in it.
   auto look_up = [&](const Cursor& k) -> int {
     const int pos = k.i * kKeys + (lane << p.shift);
@@ -554,6 +539,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   tile_barrier<kCtas>();  // the barriers and the columns of both blocks are there
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
+  if (threadIdx.x == 0) {
+    const bool live = !s_bad && s_unit[0] < s_unit[1];
+    if (rank == 0) {
+      p.head[c] = RunHead{s_tile, live ? 1 + (s_cur.i > 0 ? 2 : 0) + 4 * min(kTileRows, s_cur.n * r - s_cur.rt * kTileRows) : 0};
+      p.info[c] = RunInfo{s_cur.g, s_cur.rt, 0, 0, s_cur.lo, s_cur.n, s_cur.len, 0};
+    }
+    if (!live) p.flags[blockIdx.x] = s_bad ? (int32_t)MOE_ERR_INVALID_ARG : 0;
+  }
+  // Queries that see nothing (more queries than positions): o = 0.
+  for (int b = blockIdx.x; !s_bad && b < p.B; b += gridDim.x) {
+    const int lo = ld(p.offsets + b), hi = ld(p.offsets + b + 1), len = ld(p.lens + b);
+    const size_t pieces = (size_t)max(0, hi - lo - len) * p.Hq * (D / 8);
+    uint4* z = reinterpret_cast<uint4*>(p.o + (size_t)lo * p.Hq * D);
+    for (size_t i = threadIdx.x; i < pieces; i += kThreads) z[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
   if (idle) {
     tile_barrier<kCtas>();  // (columns of a pair are freed by both)
     if (warp == kMmaWarp) free_columns<kCtas>(tmem);
@@ -964,37 +964,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             // 32 rows by 16 dims at a time, the same way; of rows that are there
             float* part = p.part + (size_t)(2 * c + (mid ? 0 : 1)) * slot_floats(D, kTileRows);
-            const int rows = seq.y * r - place.y * kTileRows - rank * kRows - quad * 32;
-            if (rows <= kFewRows) {  // a lane writes its own
+            // row by row, or 4 head dims of all rows side by side
+            const size_t step = p.by_row ? 1 : kTileRows;
+            float4* to = reinterpret_cast<float4*>(part) + (p.by_row ? (size_t)(rank * kRows + row) * (D / 4) + d0 / 4
+                                                                     : (size_t)(d0 / 4) * kTileRows + rank * kRows + row);
+            const bool there = place.y * kTileRows + rank * kRows + row < seq.y * r;
 #pragma unroll 1
-              for (int j = d0; j < d0 + D / 2; j += 32) {
-                float v[32];
-                tmem_ld_32(lane_addr + j, v);
-                float4* to = reinterpret_cast<float4*>(part + (size_t)(rank * kRows + row) * D + j);
-                if (lane < rows) {
+            for (int j = 0; j < D / 2; j += 32) {
+              float v[32];
+              tmem_ld_32(lane_addr + d0 + j, v);
+              if (there) {
 #pragma unroll
-                  for (int e = 0; e < 8; ++e) to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-                }
+                for (int e = 0; e < 8; ++e)
+                  to[e * step] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
               }
-            } else {
-              float* prow = part + (size_t)(rank * kRows + quad * 32 + (lane >> 2)) * D + 4 * (lane & 3);
-#pragma unroll 1
-              for (int j = d0; j < d0 + D / 2; j += 16) {
-                uint32_t v[16];
-                tmem_ld_16(lane_addr + j, v);
-                __syncwarp();
-#pragma unroll
-                for (int e = 0; e < 16; e += 4)
-                  sts128(out + lane * F::kOutPitch + 4 * e, v[e], v[e + 1], v[e + 2], v[e + 3]);
-                __syncwarp();
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  if (8 * k + (lane >> 2) < rows)
-                    *reinterpret_cast<uint4*>(prow + (size_t)(8 * k) * D + j) =
-                        lds128(out + (8 * k + (lane >> 2)) * F::kOutPitch + 16 * (lane & 3));
-              }
+              to += 8 * step;
             }
-            if (half == 0 && lane < rows) {
+            if (half == 0 && there) {
               part[(size_t)D * kTileRows + rank * kRows + row] = m;
               part[(size_t)(D + 1) * kTileRows + rank * kRows + row] = l;
             }
@@ -1121,22 +1107,29 @@ struct MergeParams {
 
 constexpr int kMergeWarps = 16;
 constexpr int kMergeThreads = 32 * kMergeWarps;
-constexpr int kFewStates = 4;  // of a row, up to which a warp joins them alone
+constexpr int kByRowRows = 16;  // rows of a (sequence, KV head), on average, up to which states lie row by row
+constexpr int kFewRows = 16, kFewStates = 4;
 static_assert(kMaxCtas <= kMergeThreads, "a thread per run");
 
 // Joins the partial states of the tiles that runs' borders cut. Every block
 // finds out from the runs' heads which tiles those are, a run per thread, and
-// takes its share of their rows: a row by the whole block, the states dealt out
-// to its warps (decode over a long context has few rows and many states), or 16
-// rows, a warp each (cut tiles of a prompt have many rows and few states). The
-// first run of a tile left its state in its second slot (a tile that the run's
-// end cuts), the others in their first. A row's chain is two trips to memory:
-// the heads, then maxima, sums and the first values together. (A trip takes 0.7
-// us here, and more where many blocks read the same lines: 3 blocks per SM that read
-// all of the runs' places took a decode call of 26 us to 31.)
+// takes its share of them, in items:
+//   kByRow (calls of few rows per tile, whose states lie row by row): a row by the
+//     whole block, the states dealt out to its warps, which join theirs first and
+//     then one another's in shared memory (decode over a long context: few rows,
+//     many states), or 16 rows, a warp each, where there are few states;
+//   else (cut tiles of prompts: many rows, few states; 4 head dims of all rows side by
+//     side): 32 rows, a lane each, a warp per 16th of the head dims, state by state.
+// The first run of a tile left its state in its second slot (a tile that the run's
+// end cuts), the others in their first. An item's chain is two trips to memory, the
+// heads, then all else. (A trip takes 0.7 us here, and more where many blocks read
+// the same lines: 3 blocks per SM that read all of the runs' places took a decode
+// call of 26 us to 31. The second form for all calls: a token after 300 positions
+// 14.2 us for 12.4; the first for all: a prompt of 4096 119 for 114.)
+template <bool kByRow>
 __global__ void __launch_bounds__(kMergeThreads, 1) paged_merge_kernel(const MergeParams p) {
-  __shared__ float s_l[kMergeWarps];
   __shared__ __align__(16) float s_acc[kMergeWarps][256];
+  __shared__ float s_m[kMergeWarps], s_l[kMergeWarps];
   __shared__ RunHead s_head[kMergeThreads + 1];
   __shared__ unsigned s_ends[kMergeWarps];  // of runs: the next is not of the same tile
   __shared__ int s_sum[kMergeWarps];
@@ -1174,7 +1167,9 @@ __global__ void __launch_bounds__(kMergeThreads, 1) paged_merge_kernel(const Mer
     while (e == 0u) e = s_ends[++w];  // (the last thread's next is none)
     c1 = 32 * w + __ffs(e) - 1;
     const int there = h.y >> 2;
-    items = there <= kFewRows && c1 - t + 2 > kFewStates ? there : (there + kMergeWarps - 1) / kMergeWarps;
+    items = !kByRow ? (there + 31) / 32
+            : there <= kFewRows && c1 - t + 2 > kFewStates ? there
+                                                           : (there + kMergeWarps - 1) / kMergeWarps;
   }
   int sum = items;
 #pragma unroll
@@ -1193,102 +1188,155 @@ __global__ void __launch_bounds__(kMergeThreads, 1) paged_merge_kernel(const Mer
   s_items[t + 1] = sum;
   s_c1[t] = c1;
   __syncthreads();
-  const int r = p.Hq / p.Hkv, D = p.D, rows = kRows * p.ctas, wide = D > 128 ? 2 : 1;
-  const bool on = 4 * lane < D;
-  constexpr int kAhead = 8;  // states whose values are asked for at once
+  const int r = p.Hq / p.Hkv, D = p.D, rows = kRows * p.ctas;
   for (int item = blockIdx.x; item < total; item += gridDim.x) {
     int c = 0;  // the last run with s_items[c] <= item
 #pragma unroll
     for (int o = kMergeThreads / 2; o > 0; o >>= 1)
       if (s_items[c + o] <= item) c += o;
-    const int c0 = c - 1, states = s_c1[c] - c0 + 1, there = s_head[c + 1].what >> 2;
-    const bool shared = there <= kFewRows && states > kFewStates;
-    const int row = shared ? item - s_items[c] : (item - s_items[c]) * kMergeWarps + warp;
-    if (row >= there) continue;  // (not where the block shares a row)
-    const int4 i0 = __ldcg(reinterpret_cast<const int4*>(p.info + c));  // g, rt
+    const int c0 = c - 1, states = s_c1[c] - c0 + 1, there = s_head[c + 1].what >> 2, part = item - s_items[c];
+    const int4 i0 = __ldcg(reinterpret_cast<const int4*>(p.info + c));      // g, rt
     const int4 i1 = __ldcg(reinterpret_cast<const int4*>(p.info + c) + 1);  // lo, n, len
     const float* first = p.part + (size_t)(2 * c0 + 1) * slot_floats(D, rows);
     const float* rest = p.part + (size_t)(2 * c0) * slot_floats(D, rows);
     auto state = [&](int k) {  // of run c0 + k
       return k == 0 ? first : rest + (size_t)2 * k * slot_floats(D, rows);
     };
-    const int from = shared ? warp : 0, step = shared ? kMergeWarps : 1;
-    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-    float M = kMinusBig, L = 0.f;
+    auto output = [&](int row) -> uint16_t* {  // null: a query that sees nothing has its zeros already
+      const int rho = i0.y * rows + row, tok = rho / r;
+      return i1.z - i1.y + tok < 0 ? nullptr
+                                   : p.o + ((size_t)(i1.x + tok) * p.Hq + (size_t)i0.x * r + rho - tok * r) * D;
+    };
+    if (kByRow) {
+      const bool shared = there <= kFewRows && states > kFewStates;
+      const int row = shared ? part : part * kMergeWarps + warp, from = shared ? warp : 0, step = shared ? kMergeWarps : 1;
+      if (row >= there) continue;  // (not where the block shares a row)
+      const int wide = D > 128 ? 2 : 1;
+      const bool on = 4 * lane < D;
+      constexpr int kAhead = 5;  // states that are asked for at once
+      float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+      float M = kMinusBig, L = 0.f;  // (all lanes alike)
 #pragma unroll 1
-    for (int base = 0; base < states; base += kAhead * step) {
-      float4 x[kAhead][2];
+      for (int base = from; base < states; base += kAhead * step) {
+        float4 x[kAhead][2];
+        float m[kAhead], l[kAhead];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int s = base + from + k * step;
-        x[k][0] = x[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (s < states && on) {
-          const float* o = state(s) + (size_t)row * D + 4 * lane;
-          x[k][0] = __ldcg(reinterpret_cast<const float4*>(o));
-          if (wide == 2) x[k][1] = __ldcg(reinterpret_cast<const float4*>(o + 128));
+        for (int k = 0; k < kAhead; ++k) {
+          const int s = base + k * step;
+          x[k][0] = x[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+          m[k] = kMinusBig;
+          l[k] = 0.f;
+          if (s < states) {
+            const float* o = state(s);
+            const float4* v = reinterpret_cast<const float4*>(o + (size_t)row * D) + lane;
+            if (on) x[k][0] = __ldcg(v);
+            if (wide == 2) x[k][1] = __ldcg(v + 32);
+            m[k] = __ldcg(o + (size_t)D * rows + row);
+            l[k] = __ldcg(o + (size_t)(D + 1) * rows + row);
+          }
+        }
+        const float old = M;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) M = fmaxf(M, m[k]);
+        const float f = ex2((old - M) * p.scale_log2);
+        L *= f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) acc[i].x *= f, acc[i].y *= f, acc[i].z *= f, acc[i].w *= f;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const float e = ex2((m[k] - M) * p.scale_log2);
+          L = fmaf(e, l[k], L);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            acc[i].x = fmaf(e, x[k][i].x, acc[i].x), acc[i].y = fmaf(e, x[k][i].y, acc[i].y);
+            acc[i].z = fmaf(e, x[k][i].z, acc[i].z), acc[i].w = fmaf(e, x[k][i].w, acc[i].w);
+          }
         }
       }
-      // lane k < kAhead: maximum and sum of the k-th of these
-      const int mine = base + from + lane * step;
-      const bool has = lane < kAhead && mine < states;
-      float m = kMinusBig, l = 0.f;
-      if (has) {
-        m = __ldcg(state(mine) + (size_t)D * rows + row);
-        l = __ldcg(state(mine) + (size_t)(D + 1) * rows + row);
+      uint16_t* out = output(row);
+      if (!shared) {
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (on && i < wide && out != nullptr)
+            *reinterpret_cast<uint2*>(out + 4 * lane + 128 * i) =
+                make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv), pack_bf16(acc[i].z * inv, acc[i].w * inv));
+        continue;
       }
-      if (base == 0) {  // the row's maximum, of all states
-#pragma unroll 1
-        for (int k = lane; k < states; k += 128) {
-          float top[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            top[q] = k + 32 * q < states ? __ldcg(state(k + 32 * q) + (size_t)D * rows + row) : kMinusBig;
-          M = fmaxf(fmaxf(M, fmaxf(top[0], top[1])), fmaxf(top[2], top[3]));
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      }
-      const float e = has ? ex2((m - M) * p.scale_log2) : 0.f;
-      L += l * e;
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const float w = __shfl_sync(0xffffffffu, e, k);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          acc[i].x = fmaf(w, x[k][i].x, acc[i].x), acc[i].y = fmaf(w, x[k][i].y, acc[i].y);
-          acc[i].z = fmaf(w, x[k][i].z, acc[i].z), acc[i].w = fmaf(w, x[k][i].w, acc[i].w);
-        }
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    const int rho = i0.y * rows + row, tok = rho / r;
-    const bool sees = i1.z - i1.y + tok >= 0;  // (a query that sees nothing has its zeros already)
-    uint16_t* out = p.o + ((size_t)(i1.x + tok) * p.Hq + (size_t)i0.x * r + rho - tok * r) * D;
-    if (!shared) {
-      const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        if (on && i < wide && sees)
-          *reinterpret_cast<uint2*>(out + 4 * lane + 128 * i) =
-              make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv), pack_bf16(acc[i].z * inv, acc[i].w * inv));
-      continue;
-    }
+        if (on && i < wide) *reinterpret_cast<float4*>(&s_acc[warp][4 * lane + 128 * i]) = acc[i];
+      if (lane == 0) s_m[warp] = M, s_l[warp] = L;
+      __syncthreads();
+      if (t < D && out != nullptr) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (on && i < wide) *reinterpret_cast<float4*>(&s_acc[warp][4 * lane + 128 * i]) = acc[i];
-    if (lane == 0) s_l[warp] = L;
-    __syncthreads();
-    if (t < D && sees) {
-      float l = 0.f, o = 0.f;
+        for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, s_m[w]);
+        float l = 0.f, o = 0.f;
 #pragma unroll
-      for (int w = 0; w < kMergeWarps; ++w) {
-        l += s_l[w];
-        o += s_acc[w][t];
+        for (int w = 0; w < kMergeWarps; ++w) {
+          const float e = ex2((s_m[w] - M) * p.scale_log2);
+          l = fmaf(e, s_l[w], l);
+          o = fmaf(e, s_acc[w][t], o);
+        }
+        out[t] = __bfloat16_as_ushort(__float2bfloat16_rn(l == 0.f ? 0.f : o * (1.f / l)));
       }
-      out[t] = __bfloat16_as_ushort(__float2bfloat16_rn(l == 0.f ? 0.f : o * (1.f / l)));
+      __syncthreads();
+    } else {
+      const int row = 32 * part + lane, per = D / 64;  // chunks of 4 head dims of a warp: 1, 2 or 4
+      if (row >= there) continue;                      // (nobody waits for anyone here)
+      constexpr int kAhead = 4;
+      float4 acc[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      float M = kMinusBig, L = 0.f;
+#pragma unroll 1
+      for (int base = 0; base < states; base += kAhead) {
+        float4 x[kAhead][4];
+        float m[kAhead], l[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          m[k] = kMinusBig;
+          l[k] = 0.f;
+          const bool on = base + k < states;
+          const float* o = state(on ? base + k : 0);
+          if (on) {
+            m[k] = __ldcg(o + (size_t)D * rows + row);
+            l[k] = __ldcg(o + (size_t)(D + 1) * rows + row);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (on && i < per) x[k][i] = __ldcg(reinterpret_cast<const float4*>(o) + (size_t)(warp * per + i) * rows + row);
+          }
+        }
+        const float old = M;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) M = fmaxf(M, m[k]);
+        const float f = ex2((old - M) * p.scale_log2);
+        L *= f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i].x *= f, acc[i].y *= f, acc[i].z *= f, acc[i].w *= f;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const float e = ex2((m[k] - M) * p.scale_log2);
+          L = fmaf(e, l[k], L);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            acc[i].x = fmaf(e, x[k][i].x, acc[i].x), acc[i].y = fmaf(e, x[k][i].y, acc[i].y);
+            acc[i].z = fmaf(e, x[k][i].z, acc[i].z), acc[i].w = fmaf(e, x[k][i].w, acc[i].w);
+          }
+        }
+      }
+      uint16_t* out = output(row);
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      if (out != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < per)
+            *reinterpret_cast<uint2*>(out + 4 * (warp * per + i)) =
+                make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv), pack_bf16(acc[i].z * inv, acc[i].w * inv));
+      }
     }
-    __syncthreads();
   }
 }
 
@@ -1372,11 +1420,12 @@ moe_status attn(const moe_paged_shape* shape, const void* q, const moe_paged_cac
   RunInfo* info = reinterpret_cast<RunInfo*>(head + kMaxCtas);
   float* part = reinterpret_cast<float*>(info + kMaxCtas);
   const int r = s.Hq / s.Hkv;
+  const bool by_row = (long long)s.T * s.Hq <= kByRowRows * (long long)s.B * s.Hkv;
   const Params prm{static_cast<const uint16_t*>(q), offsets, lens, cache->tables,
                    reinterpret_cast<const unsigned long long*>(tree), static_cast<uint16_t*>(o), part, head, info, flags,
                    scale * kLog2e, s.B, s.T, s.Hq, s.Hkv, page_shift(s.page), s.n_pages, s.max_pages, s.tree_words,
                    s.q_stride ? s.q_stride : s.Hq * s.D, ((1ull << 36) + r - 1) / r,
-                   (long long)s.T * s.Hq > 32ll * s.B * s.Hkv ? kTileCost : kFewRowsCost, narrow(s, kRows * ctas), stalled,
+                   (long long)s.T * s.Hq > 32ll * s.B * s.Hkv ? kTileCost : kFewRowsCost, by_row, narrow(s, kRows * ctas), stalled,
                    timeout_ns};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1412,12 +1461,12 @@ moe_status attn(const moe_paged_shape* shape, const void* q, const moe_paged_cac
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
   const MergeParams mp{part, head, info, flags, static_cast<uint16_t*>(o), status, scale * kLog2e,
                        s.Hq, s.Hkv, s.D, runs, ctas};
-  const long long most = (long long)s.T * s.Hq;  // rows that may have to be joined
+  const long long most = by_row ? (long long)s.T * s.Hq : sms;  // no more items than rows
   cfg.gridDim = dim3((unsigned)(most < sms ? most : sms));
   cfg.numAttrs = 1;
   cfg.blockDim = dim3(kMergeThreads);
   cfg.dynamicSmemBytes = 0;
-  e = cudaLaunchKernelEx(&cfg, paged_merge_kernel, mp);
+  e = by_row ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<true>, mp) : cudaLaunchKernelEx(&cfg, paged_merge_kernel<false>, mp);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "paged merge launch");
 }
 
