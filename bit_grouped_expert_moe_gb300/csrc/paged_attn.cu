@@ -37,7 +37,6 @@
 //   warp 13      K and V by TMA, a box per page (and per 64 head dims, where a stage
 //                has several pages): page numbers from the table one unit ahead,
 //                positions past the context as zeros
-//   warp 14      per unit, its place in shared memory for the softmax
 // The ring's stages (16 KB) hold K of a unit in D / 64 parts by head dims and V in
 // as many by positions (half as many per block of a pair, which holds half of
 // the positions of K and half of the head dims of V), in the order of their use.
@@ -66,7 +65,7 @@ constexpr int kKeys = 128;  // positions of a unit
 constexpr int kStages = 8;
 constexpr int kStageBytes = 16384;
 constexpr int kSoftWarps = 8, kAuxWarps = 4;
-constexpr int kMmaWarp = 12, kLoadWarp = 13, kNoteWarp = 14;  // (with 15 for the MMA warp the chunk below takes 392 us for 336)
+constexpr int kMmaWarp = 12, kLoadWarp = 13;  // (with 15 for the MMA warp the chunk below takes 392 us for 336)
 constexpr int kThreads = 512;
 constexpr int kMaxCtas = 256;  // workspace bound on the grid
 // A run also pays for every tile it begins (Q, the first unit's chain, the
@@ -97,12 +96,6 @@ struct Cfg {
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
-struct UnitNote {
-  int4 tile;   // lo, n, len, g of its sequence and head
-  int4 place;  // first position, row tile, is the tile's last, 0
-};
-constexpr int kNotes = 4;
-
 // Positions of a tile whose V is not finite, of those that not every row sees,
 // as bits per unit from the first that has some. There are less than 257 of
 // them (causal) or 513 (trees), so at most 6 units. Four tiles' bits: while
@@ -112,8 +105,6 @@ constexpr int kNotes = 4;
 constexpr int kBadTiles = 4, kBadUnits = 8;
 
 struct Ctl {
-  UnitNote note[kNotes];
-  uint64_t note_full[kNotes], note_empty[kNotes];
   uint64_t full[kStages], empty[kStages];
   // V of a unit that is to be looked through has come; it has been. The MMA
   // warp, which sees every phase of the stages, says the one and waits for the
@@ -445,10 +436,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 32) {
     mbar_init(&ctl->q_full, kAuxWarps);
     mbar_init(&ctl->q_empty, 1);
-    for (int i = 0; i < kNotes; ++i) {
-      mbar_init(&ctl->note_full[i], 1);
-      mbar_init(&ctl->note_empty[i], kSoftWarps);
-    }
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&ctl->full[s], 1);
       mbar_init(&ctl->empty[s], 1);
@@ -778,20 +765,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int j = max(issued - kStages, 0); j < issued; ++j)
       mbar_wait(&ctl->full[j % kStages], (uint32_t)(j / kStages) & 1u, &dummy,
                 global_timer_ns() + (uint64_t)kv8::kTimeoutNs);
-  } else if (warp == kNoteWarp) {
-    // ------------------------------------------------------- unit notes
-    Cursor k = cur;
-#pragma unroll 1
-    for (int u = 0; u < U; ++u) {
-      const int s = u % kNotes;
-      if (u >= kNotes && !warp_wait(&ctl->note_empty[s], (u / kNotes - 1) & 1)) break;
-      if (lane == 0) {
-        ctl->note[s].tile = make_int4(k.lo, k.n, k.len, k.g);
-        ctl->note[s].place = make_int4(k.i * kKeys, k.rt, k.last(), 0);
-        mbar_arrive(&ctl->note_full[s]);
-      }
-      if (u + 1 < U) k.advance(p, r, kTileRows);
-    }
   } else if (warp < kSoftWarps) {
     // --------------------------------------------------------- softmax
     const int quad = warp & 3, half = warp >> 2;
@@ -812,39 +785,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++met;
       return true;
     };
-    int4 seq = make_int4(0, 0, 0, 0);  // lo, n, len, g of the tile
+    Cursor un = cur;
 #pragma unroll 1
     for (int u = 0; u < U; ++u) {
-      const int ns = u % kNotes;
-      if (!warp_wait(&ctl->note_full[ns], (u / kNotes) & 1)) break;
-      const int4 place = ctl->note[ns].place;
       if (fresh) {
-        seq = ctl->note[ns].tile;
-        const int rho = place.y * kTileRows + rank * kRows + row;
+        const int rho = un.rt * kTileRows + rank * kRows + row;
         tok = div_r(rho, p.rmagic);
-        see = rho < seq.y * r ? max(seq.z - seq.y + tok + 1, 0) : 0;
+        see = rho < un.n * r ? max(un.len - un.n + tok + 1, 0) : 0;
         act = __any_sync(0xffffffffu, see > 0);
         m = kMinusBig;
         l = 0.f;
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->note_empty[ns]);
       if (!warp_wait(&ctl->s_full[u & 1], (u >> 1) & 1)) break;
-      const int ctx = seq.z - seq.y;  // positions before the new ones
+      const int ctx = un.len - un.n;  // positions before the new ones
       float other;
       if (act) {
         tc_fence_after();
         const uint32_t ts = lane_addr + kColS + 128 * (u & 1);
         uint32_t x[64];
         tmem_ld_64(ts + 64 * half, x);
-        const int first = place.x + 64 * half;
+        const int first = un.i * kKeys + 64 * half;
         // Rows that are not there, or see nothing, are left to themselves: nothing
         // of theirs is written, and a warp may have one row and 31 such.
         const int left = see > 0 ? see - first : kKeys;  // visible positions from this half's first on (but for the tree)
         if (__any_sync(0xffffffffu, left < 64 || (p.tree != nullptr && first + 64 > ctx))) {
           uint64_t bits = left >= 64 ? ~0ull : left > 0 ? (1ull << left) - 1 : 0ull;
           if (p.tree != nullptr && see > 0)
-            bits &= tree_bits(p.tree + (size_t)(seq.x + tok) * p.words, p.words, first, ctx);
+            bits &= tree_bits(p.tree + (size_t)(un.lo + tok) * p.words, p.words, first, ctx);
           const uint32_t b0 = (uint32_t)bits, b1 = (uint32_t)(bits >> 32);
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
@@ -898,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->p_full[u & 1]);
 
-      const bool ends = place.z != 0;
+      const bool ends = un.last();
       fresh = ends;
       if (ends || u + 1 == U) {
         // ---- the run leaves this tile: its rows' outputs, or the partial state
@@ -912,14 +879,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int bt = tile % kBadTiles;
           if (ctl->bad_any[bt]) {
             // a row that sees one of these is NaN, as its products would have made it
-            const int b0 = max(ctx + (p.tree != nullptr ? 0 : div_r(place.y * kTileRows, p.rmagic) + 1), 0) / kKeys;
-            for (int k = 0; k < kBadUnits * (kKeys / 32); ++k) {
-              uint32_t bits = (&ctl->bad[bt][0][0])[k];
-              const int pos = b0 * kKeys + 32 * k;
+            const int b0 = max(ctx + (p.tree != nullptr ? 0 : div_r(un.rt * kTileRows, p.rmagic) + 1), 0) / kKeys;
+            for (int q = 0; q < kBadUnits * (kKeys / 32); ++q) {
+              uint32_t bits = (&ctl->bad[bt][0][0])[q];
+              const int pos = b0 * kKeys + 32 * q;
               if (bits == 0u || see <= pos) continue;
               if (see - pos < 32) bits &= (1u << (see - pos)) - 1u;
               if (p.tree != nullptr)
-                bits &= (uint32_t)tree_bits(p.tree + (size_t)(seq.x + tok) * p.words, p.words, pos, ctx);
+                bits &= (uint32_t)tree_bits(p.tree + (size_t)(un.lo + tok) * p.words, p.words, pos, ctx);
               if (bits != 0u) l = __uint_as_float(0x7FC00000u);
             }
           }
@@ -932,10 +899,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint16_t* orow[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const int rk = place.y * kTileRows + rank * kRows + quad * 32 + 8 * k + (lane >> 2);
+              const int rk = un.rt * kTileRows + rank * kRows + quad * 32 + 8 * k + (lane >> 2);
               const int tk = div_r(rk, p.rmagic);
-              const bool live = rk < seq.y * r && ctx + tk >= 0;
-              uint16_t* at = p.o + ((size_t)(seq.x + tk) * p.Hq + (size_t)seq.w * r + rk - tk * r) * D + 8 * (lane & 3);
+              const bool live = rk < un.n * r && ctx + tk >= 0;
+              uint16_t* at = p.o + ((size_t)(un.lo + tk) * p.Hq + (size_t)un.g * r + rk - tk * r) * D + 8 * (lane & 3);
               orow[k] = live ? at : nullptr;
             }
 #pragma unroll 1
@@ -962,13 +929,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           } else {
-            // 32 rows by 16 dims at a time, the same way; of rows that are there
             float* part = p.part + (size_t)(2 * c + (mid ? 0 : 1)) * slot_floats(D, kTileRows);
             // row by row, or 4 head dims of all rows side by side
             const size_t step = p.by_row ? 1 : kTileRows;
             float4* to = reinterpret_cast<float4*>(part) + (p.by_row ? (size_t)(rank * kRows + row) * (D / 4) + d0 / 4
                                                                      : (size_t)(d0 / 4) * kTileRows + rank * kRows + row);
-            const bool there = place.y * kTileRows + rank * kRows + row < seq.y * r;
+            const bool there = un.rt * kTileRows + rank * kRows + row < un.n * r;
 #pragma unroll 1
             for (int j = 0; j < D / 2; j += 32) {
               float v[32];
@@ -993,6 +959,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mid = false;
         fresh = true;
       }
+      if (u + 1 < U) un.advance(p, r, kTileRows);
     }
   } else if (warp < kSoftWarps + kAuxWarps) {
     // ------------------------------------------- Q, and V that is not finite
