@@ -87,6 +87,9 @@ struct Cfg {
   static constexpr int kSlabsK = kCtas;               // ... in a stage, of 64 head dims each
   static constexpr int kDimsV = D / kCtas;            // head dims of V in a block ...
   static constexpr int kKeysV = kKeys / kParts;       // ... and positions of it in a stage
+  static constexpr int kSlabsV = kDimsV / 64;
+  static constexpr int kShiftK = kKeyRows == 128 ? 7 : 6, kShiftV = kKeysV == 128 ? 7 : kKeysV == 64 ? 6 : 5;
+  static_assert((1 << kShiftK) == kKeyRows && (1 << kShiftV) == kKeysV, "shifts");
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kOutPitch = 80;                // bytes: 32 bf16 and padding
   static constexpr int kOutOffset = kQBytes + kStages * kStageBytes;
@@ -570,7 +573,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dq = sw128_desc(smem_u32(sQ));
     const uint32_t leader = elect_one();
     const uint64_t dk = sw128_desc(smem_u32(sR));
-    const uint64_t dv = sw128_mn_desc(smem_u32(sR), F::kKeysV * 128);
+    // V of a stage lies page by page (or its part of one), of each the 64 head dims
+    // side by side
+    const int vs = min(p.shift, F::kShiftV);  // positions of a box, as a shift
+    const uint64_t dv = sw128_mn_desc(smem_u32(sR), 128u << vs);
     int tq = 0, to = 0;     // tiles whose Q has been waited for, whose O has been started
     uint32_t fixes = 0u;    // units whose V was looked through
     uint32_t fix = 0u, ahead = 0u;  // of units su - 1, su - 2, a bit each by parity
@@ -651,7 +657,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!part(place, h)) return false;
 #pragma unroll
         for (int kk = 0; kk < F::kKeysV / 16; ++kk)
-          mma_ts<kCtas>(tmem, a + (h * F::kKeysV + kk * 16) / 2, dv + st * (kStageBytes / 16) + kk * (16 * 128 / 16),
+          mma_ts<kCtas>(tmem, a + (h * F::kKeysV + kk * 16) / 2,
+                        dv + st * (kStageBytes / 16) +
+                            ((((kk * 16) >> vs) * F::kSlabsV << (vs + 3)) + (((kk * 16) & ((1 << vs) - 1)) << 3)),
                         idesc_o, kk > 0 || h > 0 ? 1u : (uint32_t)!first, leader);
         commit<kCtas>(&ctl->empty[st], leader);
       }
@@ -687,25 +695,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int outside = p.n_pages * p.Hkv;  // a page that reads as zeros
     const int rows = 1 << p.shift;
     const bool many = rows < kKeys;  // a unit has several pages
-    // This lane's box of a stage of K, of V: all of the stage's head dims where a
-    // page holds all of its positions, else 64 of them by a page's
+    // This lane's box of a stage: of V all of the stage's head dims of a page's
+    // positions, as of K where a page holds all of the stage's positions, else 64
+    // (a product takes all positions of K at once, but 16 of V).
     struct Box {
       int key, slab, to;  // its first position and 64 head dims, its place in the stage
       bool on;
-      __device__ Box(int page_shift, int keys_shift, int slabs, int key0, int slab0) {
+      __device__ Box(int page_shift, int keys_shift, int slabs, bool whole, int key0, int slab0) {
         const int box_shift = min(page_shift, keys_shift), per_shift = keys_shift - box_shift;
         const int lane = threadIdx.x & 31, s = lane >> per_shift, n = lane & ((1 << per_shift) - 1);
-        on = s < (per_shift == 0 ? 1 : slabs);
+        on = s < (whole || per_shift == 0 ? 1 : slabs);
         key = key0 + (n << box_shift);
         slab = slab0 + s;
-        to = (s << (keys_shift + 7)) + (n << (box_shift + 7));
+        to = whole ? (n * slabs) << (box_shift + 7) : (s << (keys_shift + 7)) + (n << (box_shift + 7));
       }
     };
-    constexpr int kShiftK = F::kKeyRows == 128 ? 7 : 6;
-    constexpr int kShiftV = F::kKeysV == 128 ? 7 : F::kKeysV == 64 ? 6 : 5;
-    static_assert((1 << kShiftK) == F::kKeyRows && (1 << kShiftV) == F::kKeysV, "shifts");
-    const Box bk(p.shift, kShiftK, F::kSlabsK, rank * F::kKeyRows, 0);
-    const Box bv(p.shift, kShiftV, F::kDimsV / 64, 0, rank * (F::kDimsV / 64));
+    const Box bk(p.shift, F::kShiftK, F::kSlabsK, false, rank * F::kKeyRows, 0);
+    const Box bv(p.shift, F::kShiftV, F::kSlabsV, true, 0, rank * F::kSlabsV);
     int issued = 0;
     bool bad = false;
     auto settle = [&](int id, int g) -> int {  // its place in the pools
@@ -996,6 +1002,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int bt = tile % kBadTiles;
         if (!warp_wait(&ctl->look, fixes & 1u)) break;
         constexpr int kPieces = F::kDimsV / 8;  // of 16 bytes of a position
+        const int vs = min(p.shift, F::kShiftV);
 #pragma unroll 1
         for (int h = 0; ok && h < F::kParts; ++h) {
           const int st = stage(place, h);
@@ -1006,7 +1013,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int i = key0 * kPieces + t; i < F::kKeysV * kPieces; i += kThr) {
             const int key = i / kPieces, piece = i % kPieces, pos = first + h * F::kKeysV + key;
-            const uint32_t at = base + (piece >> 3) * (F::kKeysV * 128) + key * 128 + (((piece & 7) ^ (key & 7)) << 4);
+            const uint32_t at = base + (((key >> vs) * F::kSlabsV + (piece >> 3)) << (vs + 7)) +
+                                ((key & ((1 << vs) - 1)) << 7) + (((piece & 7) ^ (key & 7)) << 4);
             if (pos >= k.len) {
               sts128(at, 0u, 0u, 0u, 0u);
               continue;
@@ -1343,15 +1351,15 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 // 4-D map of a pool [n_pages Hkv][page][D], the head dims as D / 64 slabs of 64
-// outside the positions, with boxes of `rows` positions by `slabs` slabs, or of a
-// page's by one where it has fewer, in the 128-byte swizzle; pages past the pool
-// read as zeros.
-cudaError_t pool_map(CUtensorMap* m, const void* base, const moe_paged_shape& s, int rows, int slabs) {
+// outside the positions, with boxes of `rows` positions, or a page's where it has
+// fewer, by `slabs` slabs (by one there, unless `whole`), in the 128-byte swizzle;
+// pages past the pool read as zeros.
+cudaError_t pool_map(CUtensorMap* m, const void* base, const moe_paged_shape& s, int rows, int slabs, bool whole) {
   auto fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
   const cuuint64_t dims[4] = {64, (cuuint64_t)s.page, (cuuint64_t)s.D / 64, (cuuint64_t)s.n_pages * s.Hkv};
   const cuuint64_t strides[3] = {(cuuint64_t)s.D * 2, 128, (cuuint64_t)s.page * s.D * 2};
-  const cuuint32_t box[4] = {64, (cuuint32_t)(rows < s.page ? rows : s.page), (cuuint32_t)(rows <= s.page ? slabs : 1), 1};
+  const cuuint32_t box[4] = {64, (cuuint32_t)(rows < s.page ? rows : s.page), (cuuint32_t)(whole || rows <= s.page ? slabs : 1), 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1412,8 +1420,8 @@ moe_status attn(const moe_paged_shape* shape, const void* q, const moe_paged_cac
     const auto kernel = paged_attn_kernel<decltype(d)::value, decltype(n)::value>;
     static SmemLimitMemo smem_memo;
     CUtensorMap tk, tv;
-    cudaError_t e = pool_map(&tk, cache->k_pages, s, F::kKeyRows, F::kSlabsK);
-    if (e == cudaSuccess) e = pool_map(&tv, cache->v_pages, s, F::kKeysV, F::kDimsV / 64);
+    cudaError_t e = pool_map(&tk, cache->k_pages, s, F::kKeyRows, F::kSlabsK, false);
+    if (e == cudaSuccess) e = pool_map(&tv, cache->v_pages, s, F::kKeysV, F::kSlabsV, true);
     if (e == cudaSuccess) e = ensure_smem(kernel, F::kBytes, &smem_memo);
     if (e != cudaSuccess) return e;
     cfg.dynamicSmemBytes = F::kBytes;
