@@ -381,6 +381,21 @@ def test_long_runs_and_many_tiles_the_same_every_time(moelib, cuda_dev, Hq, Hkv,
         assert torch.equal(got, p.attend(q, news, words=words))
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,lens,news,tree", [
+    (4, 2, 64, [1 + 7 * i % 200 for i in range(300)], [i % 2 for i in range(300)], False),      # more sequences than tables
+    (4, 2, 64, [1 + 7 * i % 200 for i in range(256)], [1] * 256, False),                        # the most that they hold
+    (16, 2, 256, [100 + 3 * i for i in range(70)], [1 + i % 40 for i in range(70)], True),       # of one and several tiles
+    (6, 2, 128, [90 * (i % 5) for i in range(33)], [60 * (i % 4) for i in range(33)], False),
+    (64, 1, 64, [4500], [4200], False),                                                          # more tiles than are counted
+    (1, 1, 128, [900, 3, 400], [900, 1, 399], False)])
+def test_every_search_for_a_runs_start(moelib, cuda_dev, Hq, Hkv, D, lens, news, tree):
+    rng = random.Random(64)
+    p = Paged(moelib, lens, Hkv, D, 32, seed=65)
+    words = [w for n in news for w in words_of(parents(rng, n))] if tree else None
+    q = _rand(torch.Generator().manual_seed(66), sum(news), Hq, D)
+    p.check(q, news, words=words)
+
+
 def test_a_run_of_random_calls(moelib, cuda_dev):
     rng = random.Random(29)
     for i in range(40):
