@@ -601,12 +601,6 @@ ROPE_NORM_Q, ROPE_NORM_K, ROPE_NORM_QK = 1, 2, 3
 _I64 = torch.int64
 
 
-def _usual(t, dtype, dims, strides, dev) -> bool:
-    """The quick test of a call's tensor; _kv8_tensor says what is wrong (or
-    that nothing is: strides of dimensions of one element are any)."""
-    return t.dtype is dtype and t.shape == dims and t.stride() == strides and t.get_device() == dev
-
-
 class RopeTable:
     """The turns per position of rot / 2 pairs (.turns, an int64 tensor of
     64-bit fixed-point fractions) and the .magnitude of their scaling."""
@@ -694,17 +688,20 @@ def rope(shape, spec: RopeSpec, q, k, positions, q_out, k_out, stream=None):
         _spec_fits(w, spec, D, dev)
     if Hq:
         dims = (T, Hq, D)
-        if not _usual(q, _BF16, dims, (qs or Hq * D, D, 1), dev):
+        if not (q.dtype is _BF16 and q.shape == dims and q.stride() == (qs or Hq * D, D, 1) and q.get_device() == dev):
             _kv8_tensor(w, "q", q, dev, _BF16, dims, (qs or Hq * D, D, 1))
-        if not _usual(q_out, _BF16, dims, (qos or Hq * D, D, 1), dev):
+        if not (q_out.dtype is _BF16 and q_out.shape == dims
+                and q_out.stride() == (qos or Hq * D, D, 1) and q_out.get_device() == dev):
             _kv8_tensor(w, "q_out", q_out, dev, _BF16, dims, (qos or Hq * D, D, 1))
     if Hk:
         dims = (T, Hk, D)
-        if not _usual(k, _BF16, dims, (ks or Hk * D, D, 1), dev):
+        if not (k.dtype is _BF16 and k.shape == dims and k.stride() == (ks or Hk * D, D, 1) and k.get_device() == dev):
             _kv8_tensor(w, "k", k, dev, _BF16, dims, (ks or Hk * D, D, 1))
-        if not _usual(k_out, _BF16, dims, (kos or Hk * D, D, 1), dev):
+        if not (k_out.dtype is _BF16 and k_out.shape == dims
+                and k_out.stride() == (kos or Hk * D, D, 1) and k_out.get_device() == dev):
             _kv8_tensor(w, "k_out", k_out, dev, _BF16, dims, (kos or Hk * D, D, 1))
-    if positions is not None and not _usual(positions, _I32, (T,), (1,), dev):
+    if positions is not None and not (positions.dtype is _I32 and positions.shape == (T,)
+            and positions.stride() == (1,) and positions.get_device() == dev):
         _kv8_tensor(w, "positions", positions, dev, _I32, (T,), (1,))
     rc = lib().moe_rope(shape, spec._c, q.data_ptr() if Hq else None, k.data_ptr() if Hk else None, _ptr(positions),
                         q_out.data_ptr() if Hq else None, k_out.data_ptr() if Hk else None,
@@ -779,19 +776,23 @@ def paged_append(shape, spec, q, k_new, v_new, offsets, starts, cache: PagedCach
     if q is not None:
         if q_out is None:
             _kv8_refuse(w, "q without q_out")
-        if not _usual(q, _BF16, (T, Hq, D), (qs or Hq * D, D, 1), dev):
+        if not (q.dtype is _BF16 and q.shape == (T, Hq, D)
+                and q.stride() == (qs or Hq * D, D, 1) and q.get_device() == dev):
             _kv8_tensor(w, "q", q, dev, _BF16, (T, Hq, D), (qs or Hq * D, D, 1))
-        if not _usual(q_out, _BF16, (T, Hq, D), (Hq * D, D, 1), dev):
+        if not (q_out.dtype is _BF16 and q_out.shape == (T, Hq, D)
+                and q_out.stride() == (Hq * D, D, 1) and q_out.get_device() == dev):
             _kv8_tensor(w, "q_out", q_out, dev, _BF16, (T, Hq, D), (Hq * D, D, 1))
-    if not _usual(k_new, _BF16, dims, strides, dev):
+    if not (k_new.dtype is _BF16 and k_new.shape == dims and k_new.stride() == strides and k_new.get_device() == dev):
         _kv8_tensor(w, "k_new", k_new, dev, _BF16, dims, strides)
-    if not _usual(v_new, _BF16, dims, strides, dev):
+    if not (v_new.dtype is _BF16 and v_new.shape == dims and v_new.stride() == strides and v_new.get_device() == dev):
         _kv8_tensor(w, "v_new", v_new, dev, _BF16, dims, strides)
-    if not _usual(offsets, _I32, (B + 1,), (1,), dev):
+    if not (offsets.dtype is _I32 and offsets.shape == (B + 1,)
+            and offsets.stride() == (1,) and offsets.get_device() == dev):
         _kv8_tensor(w, "offsets", offsets, dev, _I32, (B + 1,), (1,))
-    if not _usual(starts, _I32, (B,), (1,), dev):
+    if not (starts.dtype is _I32 and starts.shape == (B,) and starts.stride() == (1,) and starts.get_device() == dev):
         _kv8_tensor(w, "starts", starts, dev, _I32, (B,), (1,))
-    if positions is not None and not _usual(positions, _I32, (T,), (1,), dev):
+    if positions is not None and not (positions.dtype is _I32 and positions.shape == (T,)
+            and positions.stride() == (1,) and positions.get_device() == dev):
         _kv8_tensor(w, "positions", positions, dev, _I32, (T,), (1,))
     rc = lib().moe_paged_append(shape, None if spec is None else spec._c, None if q is None else q.data_ptr(),
                                 k_new.data_ptr(), v_new.data_ptr(), offsets.data_ptr(), starts.data_ptr(),
@@ -825,15 +826,17 @@ def paged_attn(shape, q, cache: PagedCache, offsets, lens, o, workspace, tree=No
     dev, dims, strides, size = cache._dev, (T, H, D), (stride or H * D, D, 1), workspace.numel()
     if not (cache._dims == (n, Hkv, page, D) and cache._tdims == (B, mp) and dev >= 0 and _current_device() == dev):
         cache._device(w, f)
-    if not _usual(q, _BF16, dims, strides, dev):
+    if not (q.dtype is _BF16 and q.shape == dims and q.stride() == strides and q.get_device() == dev):
         _kv8_tensor(w, "q", q, dev, _BF16, dims, strides)
-    if not _usual(offsets, _I32, (B + 1,), (1,), dev):
+    if not (offsets.dtype is _I32 and offsets.shape == (B + 1,)
+            and offsets.stride() == (1,) and offsets.get_device() == dev):
         _kv8_tensor(w, "offsets", offsets, dev, _I32, (B + 1,), (1,))
-    if not _usual(lens, _I32, (B,), (1,), dev):
+    if not (lens.dtype is _I32 and lens.shape == (B,) and lens.stride() == (1,) and lens.get_device() == dev):
         _kv8_tensor(w, "lens", lens, dev, _I32, (B,), (1,))
-    if not _usual(o, _BF16, dims, (H * D, D, 1), dev):
+    if not (o.dtype is _BF16 and o.shape == dims and o.stride() == (H * D, D, 1) and o.get_device() == dev):
         _kv8_tensor(w, "o", o, dev, _BF16, dims, (H * D, D, 1))
-    if tree is not None and not _usual(tree, _I64, (T, words), (words, 1), dev):
+    if tree is not None and not (tree.dtype is _I64 and tree.shape == (T, words)
+            and tree.stride() == (words, 1) and tree.get_device() == dev):
         _kv8_tensor(w, "tree", tree, dev, _I64, (T, words), (words, 1))
     if not (workspace.dtype is torch.uint8 and workspace.is_contiguous() and workspace.get_device() == dev):
         _kv8_tensor(w, "workspace", workspace, dev, torch.uint8, (size,), (1,))
@@ -865,13 +868,15 @@ def paged_keep(shape, cache: PagedCache, starts, kept, path, lens_out=None, stat
     dev, width = cache._dev, path.shape[-1]
     if not (cache._dims == (n, H, page, D) and cache._tdims == (B, mp) and dev >= 0 and _current_device() == dev):
         cache._device(w, f)
-    if not _usual(starts, _I32, (B,), (1,), dev):
+    if not (starts.dtype is _I32 and starts.shape == (B,) and starts.stride() == (1,) and starts.get_device() == dev):
         _kv8_tensor(w, "starts", starts, dev, _I32, (B,), (1,))
-    if not _usual(kept, _I32, (B,), (1,), dev):
+    if not (kept.dtype is _I32 and kept.shape == (B,) and kept.stride() == (1,) and kept.get_device() == dev):
         _kv8_tensor(w, "kept", kept, dev, _I32, (B,), (1,))
-    if not _usual(path, _I32, (B, width), (width, 1), dev):
+    if not (path.dtype is _I32 and path.shape == (B, width)
+            and path.stride() == (width, 1) and path.get_device() == dev):
         _kv8_tensor(w, "path", path, dev, _I32, (B, width), (width, 1))
-    if lens_out is not None and not _usual(lens_out, _I32, (B,), (1,), dev):
+    if lens_out is not None and not (lens_out.dtype is _I32 and lens_out.shape == (B,)
+            and lens_out.stride() == (1,) and lens_out.get_device() == dev):
         _kv8_tensor(w, "lens_out", lens_out, dev, _I32, (B,), (1,))
     rc = lib().moe_paged_keep(shape, cache._c, starts.data_ptr(), kept.data_ptr(), path.data_ptr(), width,
                               None if lens_out is None else lens_out.data_ptr(),
