@@ -11,6 +11,11 @@
 // modulo 2^64, without a reduction of large angles and without a table of
 // sines as long as the context. A warp computes those of its tokens once, a few
 // per lane, into shared memory, for all heads that it takes.
+//
+// Bound: a call of few heads by one chain (table and values, angles, the stores:
+// 64 tokens of 16 and 2 heads of 256 2.8 us in a graph, appended to pages 3.3);
+// one of many by HBM (8192 tokens of 40 and 8 heads of 128 35 us, 5.8 TB/s of the
+// 6.8 that a copy reaches): a head is read once and written once.
 #pragma once
 
 #include "common.cuh"
