@@ -88,7 +88,6 @@ constexpr int kMaxCtas = 256;  // workspace bound on the grid
 constexpr int kTileCost = 3, kFewRowsCost = 1;
 constexpr float kMinusBig = -3.402823466e38f;  // running-max start, finite: m - m_new is never NaN
 constexpr float kSlack = 8.f;                  // a row's scores may pass its m by this much (base 2): weights to 2^8
-constexpr uint32_t kColS = 256;           // S buffers at columns 256 and 384, O from 0
 constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);  // A and B format in an instruction descriptor
 
 template <int D, int kCtas>
@@ -102,6 +101,9 @@ struct Cfg {
   static constexpr int kSlabsV = kDimsV / 64;
   static constexpr int kShiftK = kKeyRows == 128 ? 7 : 6, kShiftV = kKeysV == 128 ? 7 : kKeysV == 64 ? 6 : 5;
   static_assert((1 << kShiftK) == kKeyRows && (1 << kShiftV) == kKeysV, "shifts");
+  // TMEM: O from column 0, then as many buffers of S as there is room for
+  static constexpr int kBufs = D == 256 ? 2 : 3;
+  static constexpr uint32_t kColS = 512 - 128 * kBufs;
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kOutPitch = 80;                // bytes: 32 bf16 and padding
   static constexpr int kOutOffset = kQBytes + kStages * kStageBytes;
@@ -118,6 +120,7 @@ struct Cfg {
 // + 1, which waits until O of t has been read); the MMA warp clears a tile's
 // bits once its O has been read.
 constexpr int kBadTiles = 4, kBadUnits = 8;
+constexpr int kMaxBufs = 3;
 
 struct Ctl {
   uint64_t full[kStages], empty[kStages];
@@ -126,14 +129,14 @@ struct Ctl {
   // other (a warp that skipped phases could take one for another).
   uint64_t look, fixed;
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2];
+  uint64_t s_full[kMaxBufs], p_full[kMaxBufs];
   // One arrival per unit, on alternate barriers. A waiter's parity is safe if
   // it cannot be two phases off: the softmax of unit u has seen S of unit u,
   // whose commit covers the products of u - 2, and those of u + 1 and u + 2
   // wait for its weights.
-  uint64_t pv_done[2];
+  uint64_t pv_done[kMaxBufs];
   uint64_t o_empty;               // O of a finished tile has been read
-  uint64_t peer_s[2], peer_o[2];  // the other block is ready for a unit's S, for its O
+  uint64_t peer_s[kMaxBufs], peer_o[kMaxBufs];  // the other block is ready for a unit's S, for its O
   uint64_t mx_full[4];            // both halves of a lane quadrant have stored their maxima (or sums)
   uint64_t mma_done;
   uint32_t tmem;
@@ -186,7 +189,8 @@ __device__ __forceinline__ int div_r(int x, unsigned long long rmagic) {
 constexpr size_t slot_floats(int D, int tile_rows) { return (size_t)tile_rows * (D + 2); }
 
 // Place in the run: unit i of the nb units of row tile rt of KV head g of
-// sequence b.
+// sequence b. The roles go tile by tile (what a tile's units share is computed
+// once: a warp of its own has 5 cycles for every instruction that it goes through).
 struct Cursor {
   int b, g, rt, i, nb, n, len, lo;
   __device__ void sequence(const Params& p) {
@@ -194,9 +198,8 @@ struct Cursor {
     n = ld(p.offsets + b + 1) - lo;
     len = ld(p.lens + b);
   }
-  __device__ bool last() const { return i == nb - 1; }
-  __device__ void advance(const Params& p, int r, int RT) {
-    if (++i < nb) return;
+  // The next tile that has units.
+  __device__ void next(const Params& p, int r, int RT) {
     i = 0;
     do {
       if (++rt >= seq_tiles(n, r, RT)) {
@@ -216,14 +219,19 @@ struct Cursor {
   __device__ int partial(const Params& p, int RT) const {
     return max(len - n + (p.tree != nullptr ? 0 : div_r(rt * RT, p.rmagic) + 1), 0);
   }
-  // V of the unit is looked through.
-  __device__ bool fix(const Params& p, int RT) const { return (i + 1) * kKeys > partial(p, RT); }
+  // Units from the place on that every row sees all of. V of the others is looked through.
+  __device__ int whole(const Params& p, int RT) const { return max(partial(p, RT) / kKeys - i, 0); }
 };
 
-// Places in the ring, in units of a K or V block: S of unit u + 1 goes before O
-// of unit u unless u ends a tile or the run (`ahead`).
-__device__ __forceinline__ int place_k(int u, bool ahead_before) { return 2 * u - (ahead_before ? 1 : 0); }
-__device__ __forceinline__ int place_v(int u, bool ahead) { return 2 * u + 1 + (ahead ? 1 : 0); }
+// A buffer that is used in turn with others, and the phase of its barriers.
+template <int kCount>
+struct Turn {
+  int at = 0;
+  uint32_t phase = 0u;
+  __device__ void next() {
+    if (++at == kCount) at = 0, phase ^= 1u;
+  }
+};
 
 // find_run for calls whose tables the block has in shared memory and whose sums
 // the host knows to fit 32 bits (Params::narrow): the starts of runs c and c + 1, by
@@ -432,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;               // 64-dim slabs of 128 rows x 128 bytes
   uint8_t* sR = smem + F::kQBytes;  // the ring
-  constexpr int kTileRows = F::kTileRows;
+  constexpr int kTileRows = F::kTileRows, kBufs = F::kBufs;
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + F::kCtlOffset);
   static_assert(sizeof(Ctl) <= 4096, "control block");
   __shared__ long long s_unit[2];  // units before the run's start and end
@@ -455,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->full[s], 1);
       mbar_init(&ctl->empty[s], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kMaxBufs; ++i) {
       mbar_init(&ctl->s_full[i], 1);
       mbar_init(&ctl->p_full[i], kSoftWarps);
       mbar_init(&ctl->pv_done[i], 1);
@@ -530,13 +538,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   }
   const bool idle = s_bad || s_unit[0] >= s_unit[1];  // both blocks of a run alike
-  // A lane's page of a unit, as the table has it: -2 where the unit has no position in it.
-  auto look_up = [&](const Cursor& k) -> int {
-    const int pos = k.i * kKeys + (lane << p.shift);
-    if ((lane > 0 && (lane << p.shift) >= kKeys) || pos >= k.len) return -2;
-    return ld(p.tables + (size_t)k.b * p.max_pages + (pos >> p.shift));
+  // A lane's page of the w-th 32 of a sequence, as the table has it: -2 past the context.
+  auto look_up = [&](const Cursor& k, int w) -> int {
+    const int page = 32 * w + lane;
+    return page << p.shift < k.len ? ld(p.tables + (size_t)k.b * p.max_pages + page) : -2;
   };
-  const int first_page = warp == kLoadWarp && !idle ? look_up(s_cur) : 0;  // on its way over the barrier
+  const int first_window = s_cur.i * kKeys >> p.shift >> 5;
+  const int first_pages = warp == kLoadWarp && !idle ? look_up(s_cur, first_window) : 0;  // on their way over the barrier
   tc_fence_before();
   tile_barrier<kCtas>();  // the barriers and the columns of both blocks are there
   tc_fence_after();
@@ -591,13 +599,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dv = sw128_mn_desc(smem_u32(sR), 128u << vs);
     int tq = 0, to = 0;     // tiles whose Q has been waited for, whose O has been started
     uint32_t fixes = 0u;    // units whose V was looked through
-    uint32_t fix = 0u, ahead = 0u;  // of units su - 1, su - 2, a bit each by parity
+    int place = 0;          // in the ring, in units of a K or V block
+    Turn<kBufs> sb, ob;     // S of the unit to be scored, of that to be put out
     Cursor nxt = cur;
     // Waits until a step of unit u may begin: its stages, the softmax's or Q's
     // barrier `own` (if any), the other block's arrival; all tested together.
     // The other block's warp passes its readiness on. (An arrival for unit u + 2
     // comes after the leader's step of unit u: two barriers in turn will do.)
-    auto ready = [&](int place, int u, uint64_t* own, uint32_t parity, uint64_t* peer, bool fixed) -> bool {
+    auto ready = [&](uint64_t* own, uint32_t parity, uint64_t* peer, uint32_t peer_parity, bool fixed) -> bool {
       bool all = own == nullptr || mbar_test_wait(own, parity);
       // A block on its own takes its stages one by one, as they come (part()).
       if (kCtas == 2) {
@@ -605,16 +614,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int h = 0; h < F::kParts; ++h) all = mbar_test_wait(&ctl->full[stage(place, h)], phase(place, h)) && all;
       }
       const bool listens = kCtas == 2 && rank == 0;
-      if (listens) all = test_cluster(peer, (u >> 1) & 1) && all;
+      if (listens) all = test_cluster(peer, peer_parity) && all;
       if (fixed || !__all_sync(0xffffffffu, all)) {
         for (int h = 0; (kCtas == 2 || fixed) && h < F::kParts; ++h)
           if (!warp_wait(&ctl->full[stage(place, h)], phase(place, h))) return false;
         if (fixed && lane == 0) mbar_arrive(&ctl->look);
         if (own != nullptr && !warp_wait(own, parity)) return false;
         if (fixed && !warp_wait(&ctl->fixed, fixes++ & 1u)) return false;
-        if (listens && !warp_wait(peer, (u >> 1) & 1)) return false;
+        if (listens && !warp_wait(peer, peer_parity)) return false;
         // (a test at cluster scope, for the fence below to follow on)
-        if (listens && !__all_sync(0xffffffffu, test_cluster(peer, (u >> 1) & 1))) return false;
+        if (listens && !__all_sync(0xffffffffu, test_cluster(peer, peer_parity))) return false;
       }
       tc_fence_after();
       if (listens) acquire_peer();
@@ -624,17 +633,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return true;
     };
-    auto part = [&](int place, int h) { return kCtas == 2 || warp_wait(&ctl->full[stage(place, h)], phase(place, h)); };
-    auto score = [&](int u, bool first, bool ends) -> bool {  // S of unit u
-      const int place = place_k(u, ahead >> ((u - 1) & 1) & 1u);
-      if (!ready(place, u, first ? &ctl->q_full : nullptr, tq & 1, &ctl->peer_s[u & 1], false)) return false;
+    auto part = [&](int h) { return kCtas == 2 || warp_wait(&ctl->full[stage(place, h)], phase(place, h)); };
+    auto score = [&](bool first, bool ends) -> bool {  // S of the next unit
+      const int buf = sb.at;
+      if (!ready(first ? &ctl->q_full : nullptr, tq & 1, &ctl->peer_s[buf], sb.phase, false)) return false;
+      sb.next();
       tq += first;
       if (rank != 0) return true;
-      const uint32_t d = tmem + kColS + 128 * (u & 1);
+      const uint32_t d = tmem + F::kColS + 128 * buf;
 #pragma unroll
       for (int h = 0; h < F::kParts; ++h) {
         const int st = stage(place, h);
-        if (!part(place, h)) return false;
+        if (!part(h)) return false;
 #pragma unroll
         for (int kk = 0; kk < 4 * F::kSlabsK; ++kk) {
           const uint32_t slab = kk >> 2, in = (kk & 3) * 2;  // 64-dim slabs
@@ -644,11 +654,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         commit<kCtas>(&ctl->empty[st], leader);
       }
-      commit<kCtas>(&ctl->s_full[u & 1], leader);
+      commit<kCtas>(&ctl->s_full[buf], leader);
       if (ends) commit<kCtas>(&ctl->q_empty, leader);
       return true;
     };
-    auto output = [&](int u, bool first) -> bool {  // O of unit u
+    auto output = [&](bool first, bool fix) -> bool {  // O of the next
       if (first && to++ > 0) {
         if (!warp_wait(&ctl->o_empty, (to - 2) & 1)) return false;
         const int t = (to - 2) % kBadTiles;
@@ -659,14 +669,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
       }
-      const int place = place_v(u, ahead >> (u & 1) & 1u);
-      if (!ready(place, u, &ctl->p_full[u & 1], (u >> 1) & 1, &ctl->peer_o[u & 1], fix >> (u & 1) & 1u)) return false;
+      const int buf = ob.at;
+      if (!ready(&ctl->p_full[buf], ob.phase, &ctl->peer_o[buf], ob.phase, fix)) return false;
+      ob.next();
       if (rank != 0) return true;
-      const uint32_t a = tmem + kColS + 128 * (u & 1);
+      const uint32_t a = tmem + F::kColS + 128 * buf;
 #pragma unroll
       for (int h = 0; h < F::kParts; ++h) {
         const int st = stage(place, h);
-        if (!part(place, h)) return false;
+        if (!part(h)) return false;
 #pragma unroll
         for (int kk = 0; kk < F::kKeysV / 16; ++kk)
           mma_ts<kCtas>(tmem, a + (h * F::kKeysV + kk * 16) / 2,
@@ -675,31 +686,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                         idesc_o, kk > 0 || h > 0 ? 1u : (uint32_t)!first, leader);
         commit<kCtas>(&ctl->empty[st], leader);
       }
-      commit<kCtas>(&ctl->pv_done[u & 1], leader);
+      commit<kCtas>(&ctl->pv_done[buf], leader);
       return true;
     };
-    // S of unit u + 1 goes ahead of O of unit u, whose weights the softmax
-    // makes meanwhile; not where u + 1 starts a tile, whose Q may be long in
-    // coming. (One call site each: the code stays short.)
-    bool ok = true, sfirst = true, ofirst = true;  // unit su, ou starts a tile (in this run)
-    int su = 0, ou = 0;                            // units scored and put out so far
+    // S goes ahead of O of a unit, whose weights the softmax makes meanwhile, as
+    // far as there are buffers; not over a tile's end: the next one's Q may be
+    // long in coming. (One call site each: the code stays short.)
+    bool ok = true;
 #pragma unroll 1
-    while (ok && ou < U) {
-      if (su < U && su <= ou + 1 && (su == ou || !sfirst)) {
-        const bool last = nxt.last();
-        ok = score(su, sfirst, last || su + 1 == U);
-        const uint32_t bit = 1u << (su & 1);
-        fix = nxt.fix(p, kTileRows) ? fix | bit : fix & ~bit;
-        ahead = !last && su + 1 < U ? ahead | bit : ahead & ~bit;
-        sfirst = last;
-        if (++su < U) nxt.advance(p, r, kTileRows);
-      } else {
-        ok = output(ou, ofirst);
-        // with su == ou + 1 the next unit's sfirst is this one's end; with
-        // su == ou + 2 unit ou + 1 is of the same tile
-        ++ou;
-        ofirst = su == ou && sfirst;
+    for (int u = 0, nu; ok && u < U; u += nu) {
+      nu = min(nxt.nb - nxt.i, U - u);
+      const int whole = nxt.whole(p, kTileRows);
+#pragma unroll 1
+      for (int j = 1 - kBufs; ok && j < nu; ++j) {
+        const int e = j + kBufs - 1;
+        if (e < nu) {
+          ok = score(e == 0, e == nu - 1);
+          ++place;
+        }
+        if (ok && j >= 0) {
+          ok = output(j == 0, j >= whole);
+          ++place;
+        }
       }
+      if (u + nu < U) nxt.next(p, r, kTileRows);
     }
     if (rank == 0) commit<kCtas>(&ctl->mma_done, leader);
   } else if (warp == kLoadWarp) {
@@ -733,47 +743,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     if ((int)blockIdx.x != p.stalled) {
       // K and V of every unit in the order of their use, one copy of the code:
       // it runs cold.
-      Cursor k = cur;        // unit ku
-      int id = first_page;   // its page
-      int ku = 0, vu = 0;    // units whose K, whose V has been asked for
-      bool kfirst = true;    // unit ku starts a tile (in this run)
-      int f0 = 0, z0 = 0, f1 = 0, z1 = 0;  // first position and page of units vu, vu + 1
+      Cursor k = cur;
+      int window = first_window;                            // 32 of the sequence's pages, in the lanes ...
+      int pages = first_pages, then = look_up(k, window + 1);  // ... and the 32 after them
+      int z[kBufs] = {};  // pages of the units whose V is to come, of the last K's
+      int place = 0;
       bool ok = true;
 #pragma unroll 1
-      for (int place = 0; ok && place < 2 * U; ++place) {
-        const bool is_k = ku < U && (ku == vu || (ku == vu + 1 && !kfirst));
-        if (is_k) {
-          const int first = k.i * kKeys, z = settle(id, k.g);
-          if (ku == vu) f0 = first, z0 = z;
-          else f1 = first, z1 = z;
-        }
-        const bool second = is_k && ku != vu;
-        const int first = second ? f1 : f0, z = second ? z1 : z0;
-        const CUtensorMap* map = is_k ? &tm_k : &tm_v;
-        const int to = is_k ? bk.to : bv.to;
-        const bool on = is_k ? bk.on : bv.on;
-        int key = is_k ? bk.key : bv.key, slab = is_k ? bk.slab : bv.slab;
+      for (int u = 0, nu; ok && u < U; u += nu) {
+        const int i0 = k.i;
+        nu = min(k.nb - i0, U - u);
 #pragma unroll 1
-        for (int h = 0; h < F::kParts; ++h) {
-          const int st = stage(place, h);
-          ok = warp_wait(&ctl->empty[st], phase(place, h) ^ 1u);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], kStageBytes);
-          const int at = __shfl_sync(0xffffffffu, z, many ? (key >> p.shift) & 31 : 0);
-          if (on) tma_load_4d(sR + st * kStageBytes + to, map, 0, (first + key) & (rows - 1), slab, at, &ctl->full[st]);
-          issued = place * F::kParts + h + 1;
-          if (is_k) slab += F::kSlabsK;
-          else key += F::kKeysV;
-        }
-        if (is_k) {
-          kfirst = k.last();
-          if (++ku < U) {  // its page numbers come while this unit's V waits for room
-            k.advance(p, r, kTileRows);
-            id = look_up(k);
+        for (int j = 1 - kBufs; ok && j < nu; ++j) {
+          const int e = j + kBufs - 1;
+#pragma unroll
+          for (int i = 0; i + 1 < kBufs; ++i) z[i] = z[i + 1];
+          if (e < nu) {
+            const int page = (i0 + e) * kKeys >> p.shift;
+            if (page >> 5 != window) {
+              pages = then;
+              then = look_up(k, ++window + 1);
+            }
+            const int id = __shfl_sync(0xffffffffu, pages, page + lane);
+            z[kBufs - 1] = settle(lane == 0 || lane << p.shift < kKeys ? id : -2, k.g);
           }
-        } else {
-          ++vu;
-          f0 = f1, z0 = z1;
+#pragma unroll 1
+          for (int v = e < nu ? 0 : 1; ok && v < (j < 0 ? 1 : 2); ++v, ++place) {
+            const bool is_k = v == 0;
+            const int first = (i0 + (is_k ? e : j)) * kKeys, at_page = is_k ? z[kBufs - 1] : z[0];
+            const CUtensorMap* map = is_k ? &tm_k : &tm_v;
+            const int to = is_k ? bk.to : bv.to;
+            const bool on = is_k ? bk.on : bv.on;
+            int key = is_k ? bk.key : bv.key, slab = is_k ? bk.slab : bv.slab;
+#pragma unroll 1
+            for (int h = 0; h < F::kParts; ++h) {
+              const int st = stage(place, h);
+              ok = warp_wait(&ctl->empty[st], phase(place, h) ^ 1u);
+              if (!ok) break;
+              if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], kStageBytes);
+              const int at = __shfl_sync(0xffffffffu, at_page, many ? (key >> p.shift) & 31 : 0);
+              if (on) tma_load_4d(sR + st * kStageBytes + to, map, 0, (first + key) & (rows - 1), slab, at, &ctl->full[st]);
+              issued = place * F::kParts + h + 1;
+              if (is_k) slab += F::kSlabsK;
+              else key += F::kKeysV;
+            }
+            if (is_k && e + 1 == nu && u + nu < U) {  // the next tile's pages come while this unit's V waits for room
+              k.next(p, r, kTileRows);
+              window = 0;
+              pages = look_up(k, 0);
+              then = look_up(k, 1);
+            }
+          }
         }
       }
     }
@@ -789,10 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = quad * 32 + lane;
     const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
     const float a = fmaxf(p.scale_log2, 1e-35f);
-    float m = kMinusBig, l = 0.f;
-    int see = 0, tile = 0, met = 0, tok = 0;
-    bool fresh = true, mid = cur.i > 0;  // the tile's first unit in this run; the tile began in an earlier run
-    bool act = false;                    // some row of the warp's is there
+    int met = 0;
     // this thread's value and its partner's, once both are there
     auto meet = [&](float v, float& other) -> bool {
       ctl->mx[met & 1][half][row] = v;
@@ -804,180 +821,186 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     Cursor un = cur;
+    Turn<kBufs> sb;  // the unit's S, P and barriers
+    bool ok = true;
 #pragma unroll 1
-    for (int u = 0; u < U; ++u) {
-      if (fresh) {
-        const int rho = un.rt * kTileRows + rank * kRows + row;
-        tok = div_r(rho, p.rmagic);
-        see = rho < un.n * r ? max(un.len - un.n + tok + 1, 0) : 0;
-        act = __any_sync(0xffffffffu, see > 0);
-        m = kMinusBig;
-        l = 0.f;
-      }
-      if (!warp_wait(&ctl->s_full[u & 1], (u >> 1) & 1)) break;
+    for (int u = 0, nu, tile = 0; ok && u < U; u += nu, ++tile) {
+      nu = min(un.nb - un.i, U - u);
+      const int whole = un.whole(p, kTileRows);
+      const int rho = un.rt * kTileRows + rank * kRows + row, tok = div_r(rho, p.rmagic);
+      const int see = rho < un.n * r ? max(un.len - un.n + tok + 1, 0) : 0;
+      const bool act = __any_sync(0xffffffffu, see > 0);  // some row of the warp's is there
+      float m = kMinusBig, l = 0.f;
       const int ctx = un.len - un.n;  // positions before the new ones
       float other;
-      if (act) {
-        tc_fence_after();
-        const uint32_t ts = lane_addr + kColS + 128 * (u & 1);
-        uint32_t x[64];
-        tmem_ld_64(ts + 64 * half, x);
-        const int first = un.i * kKeys + 64 * half;
-        // Rows that are not there, or see nothing, are left to themselves: nothing
-        // of theirs is written, and a warp may have one row and 31 such.
-        const int left = see > 0 ? see - first : kKeys;  // visible positions from this half's first on (but for the tree)
-        if (__any_sync(0xffffffffu, left < 64 || (p.tree != nullptr && first + 64 > ctx))) {
-          uint64_t bits = left >= 64 ? ~0ull : left > 0 ? (1ull << left) - 1 : 0ull;
-          if (p.tree != nullptr && see > 0)
-            bits &= tree_bits(p.tree + (size_t)(un.lo + tok) * p.words, p.words, first, ctx);
-          const uint32_t b0 = (uint32_t)bits, b1 = (uint32_t)(bits >> 32);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            if (!(b0 >> e & 1u)) x[e] = 0xFF800000u;  // -inf
-            if (!(b1 >> e & 1u)) x[32 + e] = 0xFF800000u;
-          }
-        }
-        float mx = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
-#pragma unroll
-        for (int e = 2; e < 64; e += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
-        if (!meet(mx, other)) break;
-        mx = fmaxf(mx, other);
-        if (fresh) {
-          m = fmaxf(mx, kMinusBig);
-        } else if (__any_sync(0xffffffffu, see > 0 && (mx - m) * a > kSlack)) {
-          // O and L to the new maximum, once the products of the last unit are in
-          const float nm = see > 0 && (mx - m) * a > kSlack ? mx : m, f = ex2((m - nm) * a);
-          m = nm;
-          l *= f;
-          if (!warp_wait(&ctl->pv_done[(u - 1) & 1], ((u - 1) >> 1) & 1)) break;
+#pragma unroll 1
+      for (int j = 0; j < nu; ++j) {
+        ok = warp_wait(&ctl->s_full[sb.at], sb.phase);
+        if (!ok) break;
+        if (act) {
           tc_fence_after();
-#pragma unroll 1
-          for (int j = half * (D / 2); j < (half + 1) * (D / 2); j += 16) {
-            uint32_t w[16];
-            tmem_ld_16(lane_addr + j, w);
+          const uint32_t ts = lane_addr + F::kColS + 128 * sb.at;
+          uint32_t x[64];
+          tmem_ld_64(ts + 64 * half, x);
+          if (j >= whole) {
+            const int first = (un.i + j) * kKeys + 64 * half;
+            // Rows that are not there, or see nothing, are left to themselves: nothing
+            // of theirs is written, and a warp may have one row and 31 such.
+            const int left = see > 0 ? see - first : kKeys;  // visible positions from this half's first on (but for the tree)
+            if (__any_sync(0xffffffffu, left < 64 || (p.tree != nullptr && first + 64 > ctx))) {
+              uint64_t bits = left >= 64 ? ~0ull : left > 0 ? (1ull << left) - 1 : 0ull;
+              if (p.tree != nullptr && see > 0)
+                bits &= tree_bits(p.tree + (size_t)(un.lo + tok) * p.words, p.words, first, ctx);
+              const uint32_t b0 = (uint32_t)bits, b1 = (uint32_t)(bits >> 32);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
-            tmem_st_16(lane_addr + j, w);
-          }
-        }
-        // weights, over S (both halves have read it)
-        // (the difference first: one step, x a - m a, would save an instruction of
-        // two values, but a row's m a, rounded, would be off by more than a weight's
-        // exponent holds where scores pass 2^30)
-        const uint64_t a2 = pack2(a, a), b2 = pack2(-m, -m);
-        uint64_t s2 = 0ull;
-        uint32_t w[32];
-#pragma unroll
-        for (int e = 0; e < 64; e += 2) {
-          const float2 y = unpack2(mul2(add2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), b2), a2));
-          const float w0 = ex2(y.x), w1 = ex2(y.y);
-          s2 = add2(s2, pack2(w0, w1));
-          w[e / 2] = pack_bf16(w0, w1);
-        }
-        const float2 s = unpack2(s2);
-        l += s.x + s.y;
-        tmem_st_32(ts + 32 * half, w);
-        tmem_st_wait();
-        tc_fence_before();
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->p_full[u & 1]);
-
-      const bool ends = un.last();
-      fresh = ends;
-      if (ends || u + 1 == U) {
-        // ---- the run leaves this tile: its rows' outputs, or the partial state
-        if (act) {
-          if (!meet(l, other)) break;
-          l += other;
-        }
-        if (!warp_wait(&ctl->pv_done[u & 1], (u >> 1) & 1)) break;
-        tc_fence_after();
-        if (act) {
-          const int bt = tile % kBadTiles;
-          if (ctl->bad_any[bt]) {
-            // a row that sees one of these is NaN, as its products would have made it
-            const int b0 = max(ctx + (p.tree != nullptr ? 0 : div_r(un.rt * kTileRows, p.rmagic) + 1), 0) / kKeys;
-            for (int q = 0; q < kBadUnits * (kKeys / 32); ++q) {
-              uint32_t bits = (&ctl->bad[bt][0][0])[q];
-              const int pos = b0 * kKeys + 32 * q;
-              if (bits == 0u || see <= pos) continue;
-              if (see - pos < 32) bits &= (1u << (see - pos)) - 1u;
-              if (p.tree != nullptr)
-                bits &= (uint32_t)tree_bits(p.tree + (size_t)(un.lo + tok) * p.words, p.words, pos, ctx);
-              if (bits != 0u) l = __uint_as_float(0x7FC00000u);
-            }
-          }
-          const int d0 = half * (D / 2);
-          const uint32_t out = smem_u32(smem + F::kOutOffset) + warp * (32 * F::kOutPitch);
-          if (!mid && ends) {
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            // 32 rows by 32 dims at a time through shared memory: 4 lanes write
-            // a row's 64 bytes, 8 rows at once
-            uint16_t* orow[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int rk = un.rt * kTileRows + rank * kRows + quad * 32 + 8 * k + (lane >> 2);
-              const int tk = div_r(rk, p.rmagic);
-              const bool live = rk < un.n * r && ctx + tk >= 0;
-              uint16_t* at = p.o + ((size_t)(un.lo + tk) * p.Hq + (size_t)un.g * r + rk - tk * r) * D + 8 * (lane & 3);
-              orow[k] = live ? at : nullptr;
-            }
-#pragma unroll 1
-            for (int j = d0; j < d0 + D / 2; j += 32) {
-              __syncwarp();
-#pragma unroll
-              for (int h = 0; h < 32; h += 16) {
-                uint32_t v[16];
-                tmem_ld_16(lane_addr + j + h, v);
-#pragma unroll
-                for (int e = 0; e < 16; e += 8) {
-                  uint32_t z[4];
-#pragma unroll
-                  for (int k = 0; k < 4; ++k)
-                    z[k] = pack_bf16(__uint_as_float(v[e + 2 * k]) * inv, __uint_as_float(v[e + 2 * k + 1]) * inv);
-                  sts128(out + lane * F::kOutPitch + 2 * (h + e), z[0], z[1], z[2], z[3]);
-                }
-              }
-              __syncwarp();
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint4 y = lds128(out + (8 * k + (lane >> 2)) * F::kOutPitch + 16 * (lane & 3));
-                if (orow[k]) *reinterpret_cast<uint4*>(orow[k] + j) = y;
+              for (int e = 0; e < 32; ++e) {
+                if (!(b0 >> e & 1u)) x[e] = 0xFF800000u;  // -inf
+                if (!(b1 >> e & 1u)) x[32 + e] = 0xFF800000u;
               }
             }
-          } else {
-            float* part = p.part + (size_t)(2 * c + (mid ? 0 : 1)) * slot_floats(D, kTileRows);
-            // row by row, or 4 head dims of all rows side by side
-            const size_t step = p.by_row ? 1 : kTileRows;
-            float4* to = reinterpret_cast<float4*>(part) + (p.by_row ? (size_t)(rank * kRows + row) * (D / 4) + d0 / 4
-                                                                     : (size_t)(d0 / 4) * kTileRows + rank * kRows + row);
-            const bool there = un.rt * kTileRows + rank * kRows + row < un.n * r;
-#pragma unroll 1
-            for (int j = 0; j < D / 2; j += 32) {
-              float v[32];
-              tmem_ld_32(lane_addr + d0 + j, v);
-              if (there) {
+          }
+          float mx = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  to[e * step] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-              }
-              to += 8 * step;
-            }
-            if (half == 0 && there) {
-              part[(size_t)D * kTileRows + rank * kRows + row] = m;
-              part[(size_t)(D + 1) * kTileRows + rank * kRows + row] = l;
+          for (int e = 2; e < 64; e += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+          ok = meet(mx, other);
+          if (!ok) break;
+          mx = fmaxf(mx, other);
+          if (j == 0) {
+            m = fmaxf(mx, kMinusBig);
+          } else if (__any_sync(0xffffffffu, see > 0 && (mx - m) * a > kSlack)) {
+            // O and L to the new maximum, once the products of the last unit are in
+            const float nm = see > 0 && (mx - m) * a > kSlack ? mx : m, f = ex2((m - nm) * a);
+            m = nm;
+            l *= f;
+            ok = warp_wait(&ctl->pv_done[sb.at > 0 ? sb.at - 1 : kBufs - 1], sb.at > 0 ? sb.phase : sb.phase ^ 1u);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int d = half * (D / 2); d < (half + 1) * (D / 2); d += 16) {
+              uint32_t w[16];
+              tmem_ld_16(lane_addr + d, w);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
+              tmem_st_16(lane_addr + d, w);
             }
           }
+          // weights, over S (both halves have read it)
+          // (the difference first: one step, x a - m a, would save an instruction of
+          // two values, but a row's m a, rounded, would be off by more than a weight's
+          // exponent holds where scores pass 2^30)
+          const uint64_t a2 = pack2(a, a), b2 = pack2(-m, -m);
+          uint64_t s2 = 0ull;
+          uint32_t w[32];
+#pragma unroll
+          for (int e = 0; e < 64; e += 2) {
+            const float2 y = unpack2(mul2(add2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), b2), a2));
+            const float w0 = ex2(y.x), w1 = ex2(y.y);
+            s2 = add2(s2, pack2(w0, w1));
+            w[e / 2] = pack_bf16(w0, w1);
+          }
+          const float2 s = unpack2(s2);
+          l += s.x + s.y;
+          tmem_st_32(ts + 32 * half, w);
+          tmem_st_wait();
           tc_fence_before();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->o_empty);
-        ++tile;
-        mid = false;
-        fresh = true;
+        if (lane == 0) mbar_arrive(&ctl->p_full[sb.at]);
+        if (j + 1 < nu) sb.next();
       }
-      if (u + 1 < U) un.advance(p, r, kTileRows);
+      if (!ok) break;
+      // ---- the run leaves this tile: its rows' outputs, or the partial state
+      const bool mid = un.i > 0, ends = un.i + nu == un.nb;  // began in an earlier run; ends in this one
+      if (act) {
+        ok = meet(l, other);
+        if (!ok) break;
+        l += other;
+      }
+      ok = warp_wait(&ctl->pv_done[sb.at], sb.phase);
+      if (!ok) break;
+      sb.next();
+      tc_fence_after();
+      if (act) {
+        const int bt = tile % kBadTiles;
+        if (ctl->bad_any[bt]) {
+          // a row that sees one of these is NaN, as its products would have made it
+          const int b0 = max(ctx + (p.tree != nullptr ? 0 : div_r(un.rt * kTileRows, p.rmagic) + 1), 0) / kKeys;
+          for (int q = 0; q < kBadUnits * (kKeys / 32); ++q) {
+            uint32_t bits = (&ctl->bad[bt][0][0])[q];
+            const int pos = b0 * kKeys + 32 * q;
+            if (bits == 0u || see <= pos) continue;
+            if (see - pos < 32) bits &= (1u << (see - pos)) - 1u;
+            if (p.tree != nullptr)
+              bits &= (uint32_t)tree_bits(p.tree + (size_t)(un.lo + tok) * p.words, p.words, pos, ctx);
+            if (bits != 0u) l = __uint_as_float(0x7FC00000u);
+          }
+        }
+        const int d0 = half * (D / 2);
+        const uint32_t out = smem_u32(smem + F::kOutOffset) + warp * (32 * F::kOutPitch);
+        if (!mid && ends) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          // 32 rows by 32 dims at a time through shared memory: 4 lanes write
+          // a row's 64 bytes, 8 rows at once
+          uint16_t* orow[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int rk = un.rt * kTileRows + rank * kRows + quad * 32 + 8 * k + (lane >> 2);
+            const int tk = div_r(rk, p.rmagic);
+            const bool live = rk < un.n * r && ctx + tk >= 0;
+            uint16_t* at = p.o + ((size_t)(un.lo + tk) * p.Hq + (size_t)un.g * r + rk - tk * r) * D + 8 * (lane & 3);
+            orow[k] = live ? at : nullptr;
+          }
+#pragma unroll 1
+          for (int j = d0; j < d0 + D / 2; j += 32) {
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < 32; h += 16) {
+              uint32_t v[16];
+              tmem_ld_16(lane_addr + j + h, v);
+#pragma unroll
+              for (int e = 0; e < 16; e += 8) {
+                uint32_t z[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  z[k] = pack_bf16(__uint_as_float(v[e + 2 * k]) * inv, __uint_as_float(v[e + 2 * k + 1]) * inv);
+                sts128(out + lane * F::kOutPitch + 2 * (h + e), z[0], z[1], z[2], z[3]);
+              }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint4 y = lds128(out + (8 * k + (lane >> 2)) * F::kOutPitch + 16 * (lane & 3));
+              if (orow[k]) *reinterpret_cast<uint4*>(orow[k] + j) = y;
+            }
+          }
+        } else {
+          float* part = p.part + (size_t)(2 * c + (mid ? 0 : 1)) * slot_floats(D, kTileRows);
+          // row by row, or 4 head dims of all rows side by side
+          const size_t step = p.by_row ? 1 : kTileRows;
+          float4* to = reinterpret_cast<float4*>(part) + (p.by_row ? (size_t)(rank * kRows + row) * (D / 4) + d0 / 4
+                                                                   : (size_t)(d0 / 4) * kTileRows + rank * kRows + row);
+          const bool there = un.rt * kTileRows + rank * kRows + row < un.n * r;
+#pragma unroll 1
+          for (int j = 0; j < D / 2; j += 32) {
+            float v[32];
+            tmem_ld_32(lane_addr + d0 + j, v);
+            if (there) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                to[e * step] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            }
+            to += 8 * step;
+          }
+          if (half == 0 && there) {
+            part[(size_t)D * kTileRows + rank * kRows + row] = m;
+            part[(size_t)(D + 1) * kTileRows + rank * kRows + row] = l;
+          }
+        }
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->o_empty);
+      if (u + nu < U) un.next(p, r, kTileRows);
     }
   } else if (warp < kSoftWarps + kAuxWarps) {
     // ------------------------------------------- Q, and V that is not finite
@@ -986,33 +1009,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ln = t % kLanes, row0 = t / kLanes;
     const uint32_t q0 = smem_u32(sQ) + (ln >> 3) * (kRows * 128);
     Cursor k = cur;
-    bool fresh = true, ok = true, last;
-    int tile = 0;
+    bool ok = true;
     uint32_t fixes = 0u;
 #pragma unroll 1
-    for (int u = 0; ok && u < U; ++u) {
-      if (fresh) {
-        if (tile > 0 && !warp_wait(&ctl->q_empty, (tile - 1) & 1)) break;
-        tc_fence_after();
-        const int rho0 = k.rt * kTileRows + rank * kRows, rows = min(kRows, k.n * r - rho0);
+    for (int u = 0, nu, tile = 0; ok && u < U; u += nu, ++tile) {
+      nu = min(k.nb - k.i, U - u);
+      if (tile > 0 && !warp_wait(&ctl->q_empty, (tile - 1) & 1)) break;
+      tc_fence_after();
+      const int rho0 = k.rt * kTileRows + rank * kRows, rows = min(kRows, k.n * r - rho0);
 #pragma unroll 4
-        for (int i = row0; i < rows; i += kAtOnce) {
-          const int rho = rho0 + i, tok = div_r(rho, p.rmagic);
-          const uint16_t* from = p.q + (size_t)(k.lo + tok) * p.q_stride + (size_t)(k.g * r + rho - tok * r) * D + ln * 8;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(q0 + i * 128 + (((ln & 7) ^ (i & 7)) << 4)),
-                       "l"(from)
-                       : "memory");
-        }
-        cp_async_wait_all();
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->q_full);
+      for (int i = row0; i < rows; i += kAtOnce) {
+        const int rho = rho0 + i, tok = div_r(rho, p.rmagic);
+        const uint16_t* from = p.q + (size_t)(k.lo + tok) * p.q_stride + (size_t)(k.g * r + rho - tok * r) * D + ln * 8;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(q0 + i * 128 + (((ln & 7) ^ (i & 7)) << 4)),
+                     "l"(from)
+                     : "memory");
       }
-      last = k.last();
-      if (k.fix(p, kTileRows)) {
-        const int place = place_v(u, !last && u + 1 < U), first = k.i * kKeys, part = k.partial(p, kTileRows);
-        const int bt = tile % kBadTiles;
-        if (!warp_wait(&ctl->look, fixes & 1u)) break;
+      cp_async_wait_all();
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->q_full);
+      const int part = k.partial(p, kTileRows), bt = tile % kBadTiles;
+#pragma unroll 1
+      for (int j = k.whole(p, kTileRows); ok && j < nu; ++j) {
+        // in the ring V of unit u + j comes after K of so many units
+        const int place = 2 * (u + j) + 1 + min(kBufs - 1, nu - 1 - j), first = (k.i + j) * kKeys;
+        ok = warp_wait(&ctl->look, fixes & 1u);
+        if (!ok) break;
         constexpr int kPieces = F::kDimsV / 8;  // of 16 bytes of a position
         const int vs = min(p.shift, F::kShiftV);
 #pragma unroll 1
@@ -1048,7 +1071,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (found) {
               sts128(at, w[0], w[1], w[2], w[3]);
-              const int bu = k.i - part / kKeys, key_u = h * F::kKeysV + key;
+              const int bu = k.i + j - part / kKeys, key_u = h * F::kKeysV + key;
               or_both<kCtas>(&ctl->bad[bt][bu][key_u >> 5], 1u << (key_u & 31), rank);
               or_both<kCtas>(reinterpret_cast<uint32_t*>(&ctl->bad_any[bt]), 1u, rank);
             }
@@ -1060,9 +1083,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&ctl->fixed);
         ++fixes;
       }
-      fresh = last;
-      tile += last;
-      if (u + 1 < U) k.advance(p, r, kTileRows);
+      if (u + nu < U) k.next(p, r, kTileRows);
     }
     cp_async_wait_all();
   }
