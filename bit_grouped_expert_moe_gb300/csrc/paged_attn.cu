@@ -34,8 +34,11 @@
 //                sees and that are no finite numbers out of it (0 * NaN is NaN)
 //   warp 12      TMEM allocation; the MMA-issuing thread (of a pair, the first
 //                block's; the other block's warp tells it what is ready there)
-//   warp 13      K and V by TMA: page numbers from the table one unit ahead,
-//                positions past the context as zeros
+//   warps 13, 14 K and V by TMA, a stage each in turn (page numbers from the table
+//                32 at a time, positions past the context as zeros). One warp has
+//                some 130 cycles a box: 2000 tokens after 28,000 positions in
+//                pages of 16, 32, 64 (16 heads on 4 of 128) 509, 425, 354 us for
+//                385, 356, 355
 // The ring's stages (16 KB) hold K of a unit in D / 64 parts by head dims and V in
 // as many by positions (half as many per block of a pair, which holds half of
 // the positions of K and half of the head dims of V), in the order of their use.
@@ -77,8 +80,9 @@ constexpr int kKeys = 128;  // positions of a unit
 constexpr int kStages = 8;
 constexpr int kStageBytes = 16384;
 constexpr int kSoftWarps = 8, kAuxWarps = 4;
-constexpr int kMmaWarp = 12, kLoadWarp = 13;  // (with 15 for the MMA warp the chunk below takes 392 us for 336)
+constexpr int kMmaWarp = 12, kLoadWarp = 13, kLoadWarps = 2;  // (with 15 for the MMA warp the chunk below takes 392 us for 336)
 constexpr int kThreads = 512;
+static_assert(kStages % kLoadWarps == 0, "a stage is one warp's");
 constexpr int kMaxCtas = 256;  // workspace bound on the grid
 // A run also pays for every tile it begins (Q, the first unit's chain, the
 // output): the runs are cut on a scale where a tile with units takes some more
@@ -543,8 +547,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int page = 32 * w + lane;
     return page << p.shift < k.len ? ld(p.tables + (size_t)k.b * p.max_pages + page) : -2;
   };
+  const bool loads = warp >= kLoadWarp && warp < kLoadWarp + kLoadWarps;
   const int first_window = s_cur.i * kKeys >> p.shift >> 5;
-  const int first_pages = warp == kLoadWarp && !idle ? look_up(s_cur, first_window) : 0;  // on their way over the barrier
+  const int first_pages = loads && !idle ? look_up(s_cur, first_window) : 0;  // on their way over the barrier
   tc_fence_before();
   tile_barrier<kCtas>();  // the barriers and the columns of both blocks are there
   tc_fence_after();
@@ -712,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (u + nu < U) nxt.next(p, r, kTileRows);
     }
     if (rank == 0) commit<kCtas>(&ctl->mma_done, leader);
-  } else if (warp == kLoadWarp) {
+  } else if (loads) {
     // ---------------------------------------------------- K and V by TMA
     const int outside = p.n_pages * p.Hkv;  // a page that reads as zeros
     const int rows = 1 << p.shift;
@@ -742,7 +747,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if ((int)blockIdx.x != p.stalled) {
       // K and V of every unit in the order of their use, one copy of the code:
-      // it runs cold.
+      // it runs cold. The warps go through the same steps, and each fills the stages
+      // that are its own (and so sees every phase of their barriers: one that did
+      // not could take one for another).
       Cursor k = cur;
       int window = first_window;                            // 32 of the sequence's pages, in the lanes ...
       int pages = first_pages, then = look_up(k, window + 1);  // ... and the 32 after them
@@ -777,13 +784,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             int key = is_k ? bk.key : bv.key, slab = is_k ? bk.slab : bv.slab;
 #pragma unroll 1
             for (int h = 0; h < F::kParts; ++h) {
-              const int st = stage(place, h);
-              ok = warp_wait(&ctl->empty[st], phase(place, h) ^ 1u);
-              if (!ok) break;
-              if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], kStageBytes);
-              const int at = __shfl_sync(0xffffffffu, at_page, many ? (key >> p.shift) & 31 : 0);
-              if (on) tma_load_4d(sR + st * kStageBytes + to, map, 0, (first + key) & (rows - 1), slab, at, &ctl->full[st]);
-              issued = place * F::kParts + h + 1;
+              if (stage(place, h) % kLoadWarps == warp - kLoadWarp) {
+                const int st = stage(place, h);
+                ok = warp_wait(&ctl->empty[st], phase(place, h) ^ 1u);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], kStageBytes);
+                const int at = __shfl_sync(0xffffffffu, at_page, many ? (key >> p.shift) & 31 : 0);
+                if (on) tma_load_4d(sR + st * kStageBytes + to, map, 0, (first + key) & (rows - 1), slab, at, &ctl->full[st]);
+                issued = place * F::kParts + h + 1;
+              }
               if (is_k) slab += F::kSlabsK;
               else key += F::kKeysV;
             }
@@ -800,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (__any_sync(0xffffffffu, bad) && lane == 0) ctl->bad_page = 1;
     // No copy may be in flight when the block ends, whatever ended the loops.
     int dummy = 0;
-    for (int j = max(issued - kStages, 0); j < issued; ++j)
+    for (int j = issued - 1; j >= max(issued - kStages, 0); j -= kLoadWarps)  // its own
       mbar_wait(&ctl->full[j % kStages], (uint32_t)(j / kStages) & 1u, &dummy,
                 global_timer_ns() + (uint64_t)kv8::kTimeoutNs);
   } else if (warp < kSoftWarps) {
