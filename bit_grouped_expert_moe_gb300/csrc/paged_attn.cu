@@ -106,6 +106,7 @@ struct Cfg {
   static constexpr int kShiftK = kKeyRows == 128 ? 7 : 6, kShiftV = kKeysV == 128 ? 7 : kKeysV == 64 ? 6 : 5;
   static_assert((1 << kShiftK) == kKeyRows && (1 << kShiftV) == kKeysV, "shifts");
   // TMEM: O from column 0, then as many buffers of S as there is room for
+  static constexpr bool kApart = D == 64;  // O of a unit's first half of positions, and of its second
   static constexpr int kBufs = D == 256 ? 2 : 3;
   static constexpr uint32_t kColS = 512 - 128 * kBufs;
   static constexpr int kQBytes = kRows * D * 2;
@@ -607,20 +608,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     int place = 0;          // in the ring, in units of a K or V block
     Turn<kBufs> sb, ob;     // S of the unit to be scored, of that to be put out
     Cursor nxt = cur;
-    // Waits until a step of unit u may begin: its stages, the softmax's or Q's
+    // Waits until a step of a unit may begin: its stages, the softmax's or Q's
     // barrier `own` (if any), the other block's arrival; all tested together.
-    // The other block's warp passes its readiness on. (An arrival for unit u + 2
-    // comes after the leader's step of unit u: two barriers in turn will do.)
+    // The other block's warp passes its readiness on. (An arrival for unit u +
+    // kBufs comes after the leader's step of unit u: as many barriers in turn will do.)
+    bool there = false;  // all stages of the step are
     auto ready = [&](uint64_t* own, uint32_t parity, uint64_t* peer, uint32_t peer_parity, bool fixed) -> bool {
       bool all = own == nullptr || mbar_test_wait(own, parity);
-      // A block on its own takes its stages one by one, as they come (part()).
-      if (kCtas == 2) {
 #pragma unroll
-        for (int h = 0; h < F::kParts; ++h) all = mbar_test_wait(&ctl->full[stage(place, h)], phase(place, h)) && all;
-      }
+      for (int h = 0; h < F::kParts; ++h) all = mbar_test_wait(&ctl->full[stage(place, h)], phase(place, h)) && all;
       const bool listens = kCtas == 2 && rank == 0;
       if (listens) all = test_cluster(peer, peer_parity) && all;
-      if (fixed || !__all_sync(0xffffffffu, all)) {
+      there = __all_sync(0xffffffffu, all);
+      if (fixed || !there) {
+        // (a block on its own takes its stages one by one, as they come: part())
         for (int h = 0; (kCtas == 2 || fixed) && h < F::kParts; ++h)
           if (!warp_wait(&ctl->full[stage(place, h)], phase(place, h))) return false;
         if (fixed && lane == 0) mbar_arrive(&ctl->look);
@@ -638,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return true;
     };
-    auto part = [&](int h) { return kCtas == 2 || warp_wait(&ctl->full[stage(place, h)], phase(place, h)); };
+    auto part = [&](int h) { return kCtas == 2 || there || warp_wait(&ctl->full[stage(place, h)], phase(place, h)); };
     auto score = [&](bool first, bool ends) -> bool {  // S of the next unit
       const int buf = sb.at;
       if (!ready(first ? &ctl->q_full : nullptr, tq & 1, &ctl->peer_s[buf], sb.phase, false)) return false;
@@ -684,11 +685,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int st = stage(place, h);
         if (!part(h)) return false;
 #pragma unroll
-        for (int kk = 0; kk < F::kKeysV / 16; ++kk)
-          mma_ts<kCtas>(tmem, a + (h * F::kKeysV + kk * 16) / 2,
+        for (int kk = 0; kk < F::kKeysV / 16; ++kk) {
+          const int key = h * F::kKeysV + kk * 16, second = F::kApart && key >= 64;
+          mma_ts<kCtas>(tmem + second * D, a + key / 2 + 32 * second,
                         dv + st * (kStageBytes / 16) +
                             ((((kk * 16) >> vs) * F::kSlabsV << (vs + 3)) + (((kk * 16) & ((1 << vs) - 1)) << 3)),
-                        idesc_o, kk > 0 || h > 0 ? 1u : (uint32_t)!first, leader);
+                        idesc_o, key > 64 * second ? 1u : (uint32_t)!first, leader);
+        }
         commit<kCtas>(&ctl->empty[st], leader);
       }
       commit<kCtas>(&ctl->pv_done[buf], leader);
@@ -818,6 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = quad * 32 + lane;
     const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
     const float a = fmaxf(p.scale_log2, 1e-35f);
+    constexpr int kOwn = F::kApart ? D : D / 2;  // columns of O that a half scales
     int met = 0;
     // this thread's value and its partner's, once both are there
     auto meet = [&](float v, float& other) -> bool {
@@ -839,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rho = un.rt * kTileRows + rank * kRows + row, tok = div_r(rho, p.rmagic);
       const int see = rho < un.n * r ? max(un.len - un.n + tok + 1, 0) : 0;
       const bool act = __any_sync(0xffffffffu, see > 0);  // some row of the warp's is there
-      float m = kMinusBig, l = 0.f;
+      float m = kMinusBig, l = 0.f, f0 = 1.f, f1 = 1.f;
       const int ctx = un.len - un.n;  // positions before the new ones
       float other;
 #pragma unroll 1
@@ -871,9 +875,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           float mx = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
 #pragma unroll
           for (int e = 2; e < 64; e += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
-          ok = meet(mx, other);
-          if (!ok) break;
-          mx = fmaxf(mx, other);
+          if (!F::kApart) {
+            ok = meet(mx, other);
+            if (!ok) break;
+            mx = fmaxf(mx, other);
+          }
           if (j == 0) {
             m = fmaxf(mx, kMinusBig);
           } else if (__any_sync(0xffffffffu, see > 0 && (mx - m) * a > kSlack)) {
@@ -885,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int d = half * (D / 2); d < (half + 1) * (D / 2); d += 16) {
+            for (int d = half * kOwn; d < (half + 1) * kOwn; d += 16) {
               uint32_t w[16];
               tmem_ld_16(lane_addr + d, w);
 #pragma unroll
@@ -893,7 +899,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st_16(lane_addr + d, w);
             }
           }
-          // weights, over S (both halves have read it)
+          // weights, over S (apart, over what this half has read, else over the first half, which
+          // both have read)
           // (the difference first: one step, x a - m a, would save an instruction of
           // two values, but a row's m a, rounded, would be off by more than a weight's
           // exponent holds where scores pass 2^30)
@@ -909,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float2 s = unpack2(s2);
           l += s.x + s.y;
-          tmem_st_32(ts + 32 * half, w);
+          tmem_st_32(ts + (F::kApart ? 64 : 32) * half, w);
           tmem_st_wait();
           tc_fence_before();
         }
@@ -923,7 +930,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (act) {
         ok = meet(l, other);
         if (!ok) break;
-        l += other;
+        if (F::kApart) {  // the two halves' states as one
+          const float l0 = half == 0 ? l : other, l1 = half == 0 ? other : l;
+          ok = meet(m, other);
+          if (!ok) break;
+          const float m0 = half == 0 ? m : other, m1 = half == 0 ? other : m;
+          m = fmaxf(m0, m1);
+          f0 = ex2((m0 - m) * a);
+          f1 = ex2((m1 - m) * a);
+          l = l0 * f0 + l1 * f1;
+        } else {
+          l += other;
+        }
       }
       ok = warp_wait(&ctl->pv_done[sb.at], sb.phase);
       if (!ok) break;
@@ -948,6 +966,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t out = smem_u32(smem + F::kOutOffset) + warp * (32 * F::kOutPitch);
         if (!mid && ends) {
           const float inv = l == 0.f ? 0.f : 1.f / l;
+          f0 *= inv, f1 *= inv;
           // 32 rows by 32 dims at a time through shared memory: 4 lanes write
           // a row's 64 bytes, 8 rows at once
           uint16_t* orow[4];
@@ -967,11 +986,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t v[16];
               tmem_ld_16(lane_addr + j + h, v);
 #pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f0);
+              if (F::kApart) {
+                uint32_t w[16];
+                tmem_ld_16(lane_addr + D + j + h, w);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(fmaf(__uint_as_float(w[e]), f1, __uint_as_float(v[e])));
+              }
+#pragma unroll
               for (int e = 0; e < 16; e += 8) {
                 uint32_t z[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  z[k] = pack_bf16(__uint_as_float(v[e + 2 * k]) * inv, __uint_as_float(v[e + 2 * k + 1]) * inv);
+                for (int k = 0; k < 4; ++k) z[k] = pack_bf16(__uint_as_float(v[e + 2 * k]), __uint_as_float(v[e + 2 * k + 1]));
                 sts128(out + lane * F::kOutPitch + 2 * (h + e), z[0], z[1], z[2], z[3]);
               }
             }
@@ -993,6 +1019,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < D / 2; j += 32) {
             float v[32];
             tmem_ld_32(lane_addr + d0 + j, v);
+            if (F::kApart) {
+              float w[32];
+              tmem_ld_32(lane_addr + D + d0 + j, w);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = fmaf(w[e], f1, v[e] * f0);
+            }
             if (there) {
 #pragma unroll
               for (int e = 0; e < 8; ++e)
