@@ -91,6 +91,7 @@ constexpr int kMaxCtas = 256;  // workspace bound on the grid
 // and ending are cheap: a token of 64 sequences 44, 46, 47, 48.
 constexpr int kTileCost = 3, kFewRowsCost = 1;
 constexpr float kMinusBig = -3.402823466e38f;  // running-max start, finite: m - m_new is never NaN
+constexpr float kLargeScore = 1048576.f;      // 2^20, in base 2
 constexpr float kSlack = 8.f;                  // a row's scores may pass its m by this much (base 2): weights to 2^8
 constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);  // A and B format in an instruction descriptor
 
@@ -901,22 +902,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // weights, over S (apart, over what this half has read, else over the first half, which
           // both have read)
-          // (the difference first: one step, x a - m a, would save an instruction of
-          // two values, but a row's m a, rounded, would be off by more than a weight's
-          // exponent holds where scores pass 2^30)
-          const uint64_t a2 = pack2(a, a), b2 = pack2(-m, -m);
-          uint64_t s2 = 0ull;
-          uint32_t w[32];
+          auto weights = [&](auto step) {  // 2^step(two values)
+            uint64_t s2 = 0ull;
+            uint32_t w[32];
 #pragma unroll
-          for (int e = 0; e < 64; e += 2) {
-            const float2 y = unpack2(mul2(add2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), b2), a2));
-            const float w0 = ex2(y.x), w1 = ex2(y.y);
-            s2 = add2(s2, pack2(w0, w1));
-            w[e / 2] = pack_bf16(w0, w1);
+            for (int e = 0; e < 64; e += 2) {
+              const float2 y = unpack2(step(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]))));
+              const float w0 = ex2(y.x), w1 = ex2(y.y);
+              s2 = add2(s2, pack2(w0, w1));
+              w[e / 2] = pack_bf16(w0, w1);
+            }
+            const float2 s = unpack2(s2);
+            l += s.x + s.y;
+            tmem_st_32(ts + (F::kApart ? 64 : 32) * half, w);
+          };
+          const uint64_t a2 = pack2(a, a);
+          const float c = m * a;
+          if (!__any_sync(0xffffffffu, see > 0 && !(fabsf(c) < kLargeScore))) {
+            // x a - c: what c, rounded, is off by, 2^-24 of it, all of the row's weights share
+            const uint64_t c2 = pack2(-c, -c);
+            weights([&](uint64_t v) { return fma2(v, a2, c2); });
+          } else {  // where that is more than 2^-4, the difference first
+            const uint64_t m2 = pack2(-m, -m);
+            weights([&](uint64_t v) { return mul2(add2(v, m2), a2); });
           }
-          const float2 s = unpack2(s2);
-          l += s.x + s.y;
-          tmem_st_32(ts + (F::kApart ? 64 : 32) * half, w);
           tmem_st_wait();
           tc_fence_before();
         }
