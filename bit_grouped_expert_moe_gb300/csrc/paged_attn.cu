@@ -1086,7 +1086,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int place = 2 * (u + j) + 1 + min(kBufs - 1, nu - 1 - j), first = (k.i + j) * kKeys;
         ok = warp_wait(&ctl->look, fixes & 1u);
         if (!ok) break;
-        constexpr int kPieces = F::kDimsV / 8;  // of 16 bytes of a position
         const int vs = min(p.shift, F::kShiftV);
 #pragma unroll 1
         for (int h = 0; ok && h < F::kParts; ++h) {
@@ -1095,21 +1094,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           const int key0 = max(part - first - h * F::kKeysV, 0);
           const uint32_t base = smem_u32(sR) + st * kStageBytes;
+          // in the order in which the stage lies, from key0's page on
+          const int i0 = ((key0 >> vs) * (8 * F::kSlabsV) << vs) + t;
+          uint32_t odd = 0u;
+#pragma unroll 4
+          for (int i = i0; i < kStageBytes / 16; i += kThr) {
+            const uint4 v = lds128(base + 16 * i);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) odd |= (w[e] & 0x7F807F80u) + 0x00800080u;  // bits 15, 31: an exponent of ones
+          }
+          if (!__any_sync(0xffffffffu, odd & 0x80008000u)) continue;
 #pragma unroll 1
-          for (int i = key0 * kPieces + t; i < F::kKeysV * kPieces; i += kThr) {
-            const int key = i / kPieces, piece = i % kPieces, pos = first + h * F::kKeysV + key;
-            const uint32_t at = base + (((key >> vs) * F::kSlabsV + (piece >> 3)) << (vs + 7)) +
-                                ((key & ((1 << vs) - 1)) << 7) + (((piece & 7) ^ (key & 7)) << 4);
-            if (pos >= k.len) {
-              sts128(at, 0u, 0u, 0u, 0u);
-              continue;
-            }
-            const uint4 v = lds128(at);
+          for (int i = i0; i < kStageBytes / 16; i += kThr) {
+            const int key = (((i >> (3 + vs)) / F::kSlabsV) << vs) + ((i >> 3) & ((1 << vs) - 1));
+            const uint4 v = lds128(base + 16 * i);
             uint32_t w[4] = {v.x, v.y, v.z, v.w};
             bool found = false;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              // halves whose exponent is all ones
               if ((w[e] & 0x7F80u) == 0x7F80u) {
                 w[e] &= 0xFFFF0000u;
                 found = true;
@@ -1119,12 +1122,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 found = true;
               }
             }
-            if (found) {
-              sts128(at, w[0], w[1], w[2], w[3]);
-              const int bu = k.i + j - part / kKeys, key_u = h * F::kKeysV + key;
-              or_both<kCtas>(&ctl->bad[bt][bu][key_u >> 5], 1u << (key_u & 31), rank);
-              or_both<kCtas>(reinterpret_cast<uint32_t*>(&ctl->bad_any[bt]), 1u, rank);
-            }
+            if (!found || key < key0) continue;
+            sts128(base + 16 * i, w[0], w[1], w[2], w[3]);
+            if (first + h * F::kKeysV + key >= k.len) continue;  // (what lies behind the context is nobody's)
+            const int bu = k.i + j - part / kKeys, key_u = h * F::kKeysV + key;
+            or_both<kCtas>(&ctl->bad[bt][bu][key_u >> 5], 1u << (key_u & 31), rank);
+            or_both<kCtas>(reinterpret_cast<uint32_t*>(&ctl->bad_any[bt]), 1u, rank);
           }
         }
         if (!ok) break;
