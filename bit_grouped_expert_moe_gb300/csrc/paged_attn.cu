@@ -240,8 +240,8 @@ struct Turn {
 };
 
 // find_run for calls whose tables the block has in shared memory and whose sums
-// the host knows to fit 32 bits (Params::narrow): the starts of runs c and c + 1, by
-// one warp. Every instruction here runs once, and cold, which is 5 to 10 cycles
+// the host knows to fit 32 bits (Params::narrow): the start of run c, by one
+// warp. Every instruction here runs once, and cold, which is 5 to 10 cycles
 // each; find_run's closed forms and 64-bit divisions are 1.6 us of a token's call
 // and 5 of a prompt's.
 //
@@ -249,7 +249,7 @@ struct Turn {
 // has `per` sequences from per k on.
 constexpr int kSmall = 256;
 __device__ __forceinline__ bool find_small(const Params& p, const int* offsets, const int* lens, int r, int RT, int cost,
-                                           int c, int C, Place* out, long long* next, bool* ok) {
+                                           int c, int C, Place* out, bool* ok) {
   const int lane = threadIdx.x & 31, per = (p.B + 31) >> 5, b0 = lane * per, b1 = min(b0 + per, p.B);
   bool bad = false, wide = false;
   int v = 0, w = 0, t = 0;  // this lane's places, units, tiles, per KV head
@@ -280,12 +280,10 @@ __device__ __forceinline__ bool find_small(const Params& p, const int* offsets, 
   const int N = __shfl_sync(0xffffffffu, vi, last) * p.Hkv, each = N / C, more = N - each * C;
   Place k{};
   k.b = -1;
-  k.units = *next = (long long)__shfl_sync(0xffffffffu, wi, last) * p.Hkv;
-#pragma unroll 1
-  for (int e = 0; e < 2; ++e) {
-    const int from = (c + e) * each + min(c + e, more);
-    const unsigned hit = __ballot_sync(0xffffffffu, vi * p.Hkv > from);
-    if (hit == 0u) break;  // the end: all units are before it
+  k.units = (long long)__shfl_sync(0xffffffffu, wi, last) * p.Hkv;
+  const int from = c * each + min(c, more);
+  const unsigned hit = __ballot_sync(0xffffffffu, vi * p.Hkv > from);
+  if (hit != 0u) {  // (none: the end, all units are before it)
     const int L = __ffs(hit) - 1;
     // through lane L's sequences, by all lanes alike
     int off = from - __shfl_sync(0xffffffffu, vi - v, L) * p.Hkv, units = __shfl_sync(0xffffffffu, wi - w, L) * p.Hkv;
@@ -297,14 +295,9 @@ __device__ __forceinline__ bool find_small(const Params& p, const int* offsets, 
       nb = units_of(++b);
     }
     const int g = off / (nb + cost), i = max(off - g * (nb + cost) - cost, 0);
-    units += g * nb + i;
-    if (e == 0) {
-      k.b = b, k.g = g, k.rt = 0, k.i = i, k.nb = nb, k.tile = tiles + g;
-      k.lo = offsets[b], k.n = offsets[b + 1] - k.lo, k.len = lens[b];
-      k.units = units;
-    } else {
-      *next = units;
-    }
+    k.b = b, k.g = g, k.rt = 0, k.i = i, k.nb = nb, k.tile = tiles + g;
+    k.lo = offsets[b], k.n = offsets[b + 1] - k.lo, k.len = lens[b];
+    k.units = units + g * nb + i;
   }
   *out = k;
   return true;
@@ -312,10 +305,10 @@ __device__ __forceinline__ bool find_small(const Params& p, const int* offsets, 
 
 // The same for sequences of several tiles, up to kSmallTiles in all, which the warp
 // goes through 32 at a time: first for every sequence's sums, then for the tile
-// of either start.
+// that the run starts in.
 constexpr int kSmallTiles = 2048;
 __device__ __forceinline__ void find_tiles(const Params& p, const int* offsets, const int* lens, int2* sums, int r, int RT,
-                                           int cost, int c, int C, Place* out, long long* next) {
+                                           int cost, int c, int C, Place* out) {
   const int lane = threadIdx.x & 31;
   int N = 0, all_units = 0;
 #pragma unroll 1
@@ -338,11 +331,9 @@ __device__ __forceinline__ void find_tiles(const Params& p, const int* offsets, 
   const int each = N / C, more = N - each * C;
   Place k{};
   k.b = -1;
-  k.units = *next = all_units;
-#pragma unroll 1
-  for (int e = 0; e < 2; ++e) {
-    int off = (c + e) * each + min(c + e, more);
-    if (off >= N) break;  // the end: all units are before it
+  k.units = all_units;
+  int off = c * each + min(c, more);
+  if (off < N) {  // (else the end: all units are before it)
     int b = 0, units = 0, tile = 0, n, len, tiles;
     int2 sum;
     while (true) {
@@ -379,13 +370,9 @@ __device__ __forceinline__ void find_tiles(const Params& p, const int* offsets, 
     }
     const int at = __ffs(hit) - 1, i = max(off - cost, 0);
     units += __shfl_sync(0xffffffffu, before, at) + i;
-    if (e == 0) {
-      k.b = b, k.g = g, k.rt = rt + at, k.i = i, k.nb = __shfl_sync(0xffffffffu, nb, at), k.tile = tile + rt + at;
-      k.lo = offsets[b], k.n = n, k.len = len;
-      k.units = units;
-    } else {
-      *next = units;
-    }
+    k.b = b, k.g = g, k.rt = rt + at, k.i = i, k.nb = __shfl_sync(0xffffffffu, nb, at), k.tile = tile + rt + at;
+    k.lo = offsets[b], k.n = n, k.len = len;
+    k.units = units;
   }
   *out = k;
 }
@@ -453,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Cursor s_cur;
   __shared__ int s_bad, s_tile;
   __shared__ int s_offsets[kSmall + 1], s_lens[kSmall];
-  __shared__ int2 s_sums[kSmall];
+  __shared__ int2 s_sums[2][kSmall];
 
   // The warp's number through a shuffle, which the compiler knows to be
   // uniform: the roles' loops then run on uniform registers, where the MMA
@@ -505,18 +492,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 1 || warp == 2) {  // the run's start and its end
     Place k;
-    long long next = 0;
-    bool ok = false;
-    if (!p.narrow) {
-      ok = find_run(p.offsets, p.lens, p.B, p.T, p.Hkv, p.max_pages << p.shift, r, kTileRows, kKeys, p.cost, c + warp - 1, C,
-                    &k);
-    } else if (warp == 1) {
-      if (!find_small(p, s_offsets, s_lens, r, kTileRows, p.cost, c, C, &k, &next, &ok))
-        find_tiles(p, s_offsets, s_lens, s_sums, r, kTileRows, p.cost, c, C, &k, &next);
-      if (lane == 0) s_unit[1] = next;
-    }
+    bool ok = true;
+    const int at = c + warp - 1;
+    if (!p.narrow)
+      ok = find_run(p.offsets, p.lens, p.B, p.T, p.Hkv, p.max_pages << p.shift, r, kTileRows, kKeys, p.cost, at, C, &k);
+    else if (!find_small(p, s_offsets, s_lens, r, kTileRows, p.cost, at, C, &k, &ok))
+      find_tiles(p, s_offsets, s_lens, s_sums[warp - 1], r, kTileRows, p.cost, at, C, &k);
     if (lane == 0) {
-      if (warp == 1 || !p.narrow) s_unit[warp - 1] = k.units;
+      s_unit[warp - 1] = k.units;
       if (warp == 1) {
         s_bad = !ok;
         Cursor cur{};
