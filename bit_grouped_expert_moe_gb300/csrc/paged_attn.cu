@@ -73,7 +73,6 @@ using kv8::empty_tiles;
 using kv8::find_run;
 using kv8::Place;
 using kv8::seq_tiles;
-using kv8::tile_units;
 
 constexpr int kRows = 128;  // rows of a block (TMEM lanes)
 constexpr int kKeys = 128;  // positions of a unit
@@ -192,6 +191,12 @@ __device__ __forceinline__ int div_r(int x, unsigned long long rmagic) {
   return (int)(((unsigned long long)(unsigned)x * rmagic) >> 36);
 }
 
+// kv8::tile_units without its division.
+__device__ __forceinline__ int tile_units(const Params& p, int n, int len, int r, int RT, int rt) {
+  const int see = len - n + div_r(min(n * r, (rt + 1) * RT) - 1, p.rmagic) + 1;
+  return see > 0 ? (see + kKeys - 1) / kKeys : 0;
+}
+
 constexpr size_t slot_floats(int D, int tile_rows) { return (size_t)tile_rows * (D + 2); }
 
 // Place in the run: unit i of the nb units of row tile rt of KV head g of
@@ -218,7 +223,7 @@ struct Cursor {
           } while (n == 0);
         }
       }
-      nb = tile_units(n, len, r, RT, kKeys, rt);
+      nb = tile_units(p, n, len, r, RT, rt);
     } while (nb == 0);
   }
   // The tile's first position that some row does not see.
@@ -317,7 +322,7 @@ __device__ __forceinline__ void find_tiles(const Params& p, const int* offsets, 
     int v = 0, w = 0;
 #pragma unroll 1
     for (int rt = lane; rt < tiles; rt += 32) {
-      const int nb = tile_units(n, len, r, RT, kKeys, rt);
+      const int nb = tile_units(p, n, len, r, RT, rt);
       v += nb > 0 ? nb + cost : 0;
       w += nb;
     }
@@ -348,7 +353,7 @@ __device__ __forceinline__ void find_tiles(const Params& p, const int* offsets, 
     unsigned hit;
 #pragma unroll 1
     while (true) {
-      nb = rt + lane < tiles ? tile_units(n, len, r, RT, kKeys, rt + lane) : 0;
+      nb = rt + lane < tiles ? tile_units(p, n, len, r, RT, rt + lane) : 0;
       const int v = nb > 0 ? nb + cost : 0;
       int vi = v;
       before = nb;
