@@ -128,7 +128,9 @@ moe_status moe_paged_workspace_bytes(const moe_paged_shape* shape, size_t* bytes
  * factor of 2^8 at most, their sum in fp32, each rounded to bf16 for the
  * product with V; o is rounded once to bf16. So o is within
  *   2^-8 |o| + 2^-8 sum_j p_j |V_j|
- * of the formula, and of what fp32's errors of the scores do to p. A query
+ * of the formula, and of what fp32's errors of the scores do to p. In calls
+ * with T * Hq <= 16 * B * Hkv the running maximum is the largest score so far,
+ * and the sum is without the position that has it (its weight is 1). A query
  * that sees a value of V which is infinite or NaN, or a score that is, has NaN
  * or infinities in its output, and is NaN throughout where that position is
  * not seen by all queries that share its tile.

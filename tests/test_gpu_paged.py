@@ -13,6 +13,7 @@ Attention, per element, from the arithmetic (u = 2^-24):
   * the sum over positions runs in chains of at most L / 16 + 64 additions, each
     off by 2 u of at most the largest |v|.
 """
+import math
 import os
 import random
 import subprocess
@@ -360,6 +361,35 @@ def test_scores_of_any_size(moelib, cuda_dev, D, L, n, scale, std):
                 lo, hi = V[h // 2][near].min(0), V[h // 2][near].max(0)
                 slack = 2.0 ** -7 * np.maximum(np.abs(lo), np.abs(hi)) + 1e-12
                 assert (got[t, h] >= lo - slack).all() and (got[t, h] <= hi + slack).all()
+
+
+@pytest.mark.parametrize("D,L,n,r", [(256, 777, 1, 16), (256, 600, 100, 8), (128, 700, 1, 16), (128, 500, 90, 4), (64, 900, 1, 16), (64, 700, 200, 2)])
+def test_a_position_that_has_most_of_a_row(moelib, cuda_dev, D, L, n, r):
+    """Scores that one position leads by much. Weights are off by 2^-8 of each at most; in calls of few rows (n r <= 16
+    here) the largest is 1, and exact."""
+    p = Paged(moelib, [L], 2, D, 32, seed=71)
+    rng = np.random.default_rng(72)
+    K = bf16_bits_to_f64(paged.rows_of(p.k, p.tables[0], L, 32))
+    V = bf16_bits_to_f64(paged.rows_of(p.v, p.tables[0], L, 32))
+    to = rng.integers(0, L - n + 1, size=(n, 2 * r))
+    q = np.empty((n, 2 * r, D))
+    for h in range(2 * r):
+        k = K[h // r][to[:, h]]
+        # the score of `to` some 9 to 14 above 0
+        q[:, h] = k * (rng.uniform(9.0, 14.0, size=n) * math.sqrt(D) / (k * k).sum(1))[:, None]
+    q = torch.from_numpy(q).to(torch.bfloat16)
+    got, qs = p.attend(q, [n]).double().cpu().numpy(), bf16_bits_to_f64(bits16(q))
+    for t in range(n):
+        for h in range(2 * r):
+            k, v = K[h // r][:L - n + t + 1], V[h // r][:L - n + t + 1]
+            z = k @ qs[t, h] / math.sqrt(D)
+            w = np.exp(z - z.max())
+            w /= w.sum()
+            o, m, all_of = w @ v, int(z.argmax()), w @ np.abs(v)
+            rounded = all_of - w[m] * np.abs(v[m]) if n * r <= 16 else all_of
+            # (1.01: second order; 1e-4: fp32's errors of scores up to 14, and of their sums)
+            tol = 2.0 ** -8 * 1.01 * (np.abs(o) + rounded) + 1e-4 * all_of
+            assert (np.abs(got[t, h] - o) <= tol).all(), (t, h, w[m], float((np.abs(got[t, h] - o) / tol).max()))
 
 
 @pytest.mark.parametrize("Hq,Hkv,D,page,lens,news,tree", [
