@@ -17,8 +17,14 @@
 //   P = 2^(scale log2(e) (S - m)) in bf16, written over S in TMEM;
 //   O += P V   N = D, A = P from TMEM, B = V from shared memory as it lies in
 //              its page, position by position (an MN-major operand)
-// S is double buffered, so the product S of the next unit runs while the softmax
-// of this one is computed (TMEM: D columns of O, 2 x 128 of S).
+// The products S of the next units run while the softmax of one is computed: TMEM
+// has D columns of O and two buffers of S, at 64 and 128 head dims three. (A
+// softmax needs 2000 cycles from S to P, and with two S of the next unit but one
+// waits in line behind O of this: 2000 tokens after 28,000 positions at 128 take
+// 376 us for 364.) At 64 head dims the two halves of a unit's positions have an
+// O each, and a maximum and a sum, which meet at a tile's end only: the halves
+// of the softmax need not wait for one another (327 -> 316 us; at 128 there
+// is room for it with two buffers of S, 372 us for 363).
 //
 // One row or 128: a product costs the same, and its 2 x 1024 cycles of a unit at
 // D = 256 are less than half of what its 128 KB take to come from HBM. So a
@@ -29,7 +35,8 @@
 //   warps 0-7    softmax: a thread has one row (TMEM lane) and half of the unit's
 //                positions, which stay in registers from the maximum to the
 //                weights; the two halves' maxima meet in shared memory. At a
-//                tile's end, half of the output row each
+//                tile's end, half of the output row each. (Whole rows of every
+//                other unit, half of them read twice, are no quicker: 366 us for 356)
 //   warps 8-11   Q into shared memory; values of V that no row, or not every row,
 //                sees and that are no finite numbers out of it (0 * NaN is NaN)
 //   warp 12      TMEM allocation; the MMA-issuing thread (of a pair, the first
@@ -48,13 +55,15 @@
 //
 // Bound (16 heads on 2 KV heads of 256 where nothing else is said; us in a graph,
 // of the 6.79 TB/s and 1.93 PFLOP/s that a copy and a library product reach):
-//   one token after 300 positions 12 us: two launches and a chain of trips to
+//   one token after 300 positions 10.5 us: two launches and a chain of trips to
 //     memory of 0.7 us each (tables, page number, K, V, states, their merge);
 //   one after 131,072 50 us, 5.4 TB/s; 64 sequences of 4096, 86 us, 6.3 TB/s: HBM;
-//   a prompt of 4096 114 us, 1.2 PFLOP/s: the tiles' beginnings, ends and cuts;
-//   2048 tokens after 16,384 323 us, 1.81 PFLOP/s, 94 %: the tensor cores;
-//   with head dims of 128 and 64 a unit's products are shorter than its softmax
-//     (1950 cycles for 1024 at 128).
+//   a prompt of 4096 103 us, 1.34 PFLOP/s: the tiles' beginnings, ends and cuts;
+//   2048 tokens after 16,384 306 us, a prompt of 16,384 1151 us, 1.91 PFLOP/s, 99 %:
+//     the tensor cores;
+//   2000 tokens after 28,000 positions, 16 heads on 4 of 128, 363 us, 1.31 PFLOP/s, of 64
+//     287 us: a unit's products are shorter than its softmax, and the issuing
+//     warp has some 1200 cycles of its own per unit.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -79,15 +88,16 @@ constexpr int kKeys = 128;  // positions of a unit
 constexpr int kStages = 8;
 constexpr int kStageBytes = 16384;
 constexpr int kSoftWarps = 8, kAuxWarps = 4;
-constexpr int kMmaWarp = 12, kLoadWarp = 13, kLoadWarps = 2;  // (with 15 for the MMA warp the chunk below takes 392 us for 336)
+constexpr int kMmaWarp = 12, kLoadWarp = 13, kLoadWarps = 2;
 constexpr int kThreads = 512;
 static_assert(kStages % kLoadWarps == 0, "a stage is one warp's");
 constexpr int kMaxCtas = 256;  // workspace bound on the grid
 // A run also pays for every tile it begins (Q, the first unit's chain, the
 // output): the runs are cut on a scale where a tile with units takes some more
 // places than units, before its first. A prompt of 4096 (16 heads on 2 x 256)
-// takes 153, 136, 121, 122 us with 1, 2, 3, 5 of them; with few rows beginning
-// and ending are cheap: a token of 64 sequences 44, 46, 47, 48.
+// takes 132, 114, 102, 103 us with 1, 2, 3, 5 of them, one of 40 heads on 8 x 128
+// 190, 174, 168, 172; with few rows beginning and ending are cheap: with 0 to 3 a
+// token of 64 sequences 36.3, 35.2, 36.7, 37.6, of 8 ragged ones 58.4, 55.3, 54.8, 54.7.
 constexpr int kTileCost = 3, kFewRowsCost = 1;
 constexpr float kMinusBig = -3.402823466e38f;  // running-max start, finite: m - m_new is never NaN
 constexpr float kLargeScore = 1048576.f;      // 2^20, in base 2
@@ -553,7 +563,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     const bool live = !s_bad && s_unit[0] < s_unit[1];
     if (rank == 0) {
-      p.head[c] = RunHead{s_tile, live ? 1 + (s_cur.i > 0 ? 2 : 0) + 4 * min(kTileRows, s_cur.n * r - s_cur.rt * kTileRows) : 0};
+      const int there = min(kTileRows, s_cur.n * r - s_cur.rt * kTileRows);
+      p.head[c] = RunHead{s_tile, live ? 1 + (s_cur.i > 0 ? 2 : 0) + 4 * there : 0};
       p.info[c] = RunInfo{s_cur.g, s_cur.rt, 0, 0, s_cur.lo, s_cur.n, s_cur.len, 0};
     }
     if (!live) p.flags[blockIdx.x] = s_bad ? (int32_t)MOE_ERR_INVALID_ARG : 0;
@@ -1182,8 +1193,8 @@ static_assert(kMaxCtas <= kMergeThreads, "a thread per run");
 // end cuts), the others in their first. An item's chain is two trips to memory, the
 // heads, then all else. (A trip takes 0.7 us here, and more where many blocks read
 // the same lines: 3 blocks per SM that read all of the runs' places took a decode
-// call of 26 us to 31. The second form for all calls: a token after 300 positions
-// 14.2 us for 12.4; the first for all: a prompt of 4096 119 for 114.)
+// call of 26 us to 31. The second form for all calls: a token of 8 ragged sequences
+// 63 us for 55; the first for all: a prompt of 4096 109 for 102.)
 template <bool kByRow>
 __global__ void __launch_bounds__(kMergeThreads, 1) paged_merge_kernel(const MergeParams p) {
   __shared__ __align__(16) float s_acc[kMergeWarps][256];
@@ -1412,13 +1423,15 @@ int tile_blocks(const moe_paged_shape& s) {
 // Whether find_small and find_tiles serve a call: their tables hold its sequences,
 // its tiles are few enough and the places of all of them stay below 2^31.
 bool narrow(const moe_paged_shape& s, int rows) {
-  const long long tiles = (long long)s.T * (s.Hq / s.Hkv) / rows + s.B, units = (long long)s.max_pages * s.page / kKeys + 2;
+  const long long tiles = (long long)s.T * (s.Hq / s.Hkv) / rows + s.B;
+  const long long units = (long long)s.max_pages * s.page / kKeys + 2;
   return s.B <= kSmall && tiles <= kSmallTiles && tiles * s.Hkv * (units + kTileCost) <= 0x7FFFFFFFll;
 }
 
 size_t workspace_bytes(const moe_paged_shape& s) {
   // as many slots of 128 rows for pairs as for single blocks
-  return 256 + kMaxCtas * (sizeof(int32_t) + sizeof(RunHead) + sizeof(RunInfo)) + 2 * kMaxCtas * slot_floats(s.D, kRows) * sizeof(float);
+  return 256 + kMaxCtas * (sizeof(int32_t) + sizeof(RunHead) + sizeof(RunInfo)) +
+         2 * kMaxCtas * slot_floats(s.D, kRows) * sizeof(float);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -1442,7 +1455,8 @@ cudaError_t pool_map(CUtensorMap* m, const void* base, const moe_paged_shape& s,
   if (!fn) return cudaErrorNotSupported;
   const cuuint64_t dims[4] = {64, (cuuint64_t)s.page, (cuuint64_t)s.D / 64, (cuuint64_t)s.n_pages * s.Hkv};
   const cuuint64_t strides[3] = {(cuuint64_t)s.D * 2, 128, (cuuint64_t)s.page * s.D * 2};
-  const cuuint32_t box[4] = {64, (cuuint32_t)(rows < s.page ? rows : s.page), (cuuint32_t)(whole || rows <= s.page ? slabs : 1), 1};
+  const cuuint32_t box[4] = {64, (cuuint32_t)(rows < s.page ? rows : s.page),
+                             (cuuint32_t)(whole || rows <= s.page ? slabs : 1), 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1483,8 +1497,8 @@ moe_status attn(const moe_paged_shape* shape, const void* q, const moe_paged_cac
                    reinterpret_cast<const unsigned long long*>(tree), static_cast<uint16_t*>(o), part, head, info, flags,
                    scale * kLog2e, by_row ? 0.f : kSlack, s.B, s.T, s.Hq, s.Hkv, page_shift(s.page), s.n_pages, s.max_pages, s.tree_words,
                    s.q_stride ? s.q_stride : s.Hq * s.D, ((1ull << 36) + r - 1) / r,
-                   (long long)s.T * s.Hq > 32ll * s.B * s.Hkv ? kTileCost : kFewRowsCost, by_row, narrow(s, kRows * ctas), stalled,
-                   timeout_ns};
+                   (long long)s.T * s.Hq > 32ll * s.B * s.Hkv ? kTileCost : kFewRowsCost, by_row,
+                   narrow(s, kRows * ctas), stalled, timeout_ns};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1514,8 +1528,10 @@ moe_status attn(const moe_paged_shape* shape, const void* q, const moe_paged_cac
   using Two = std::integral_constant<int, 2>;
   cudaError_t e;
   if (s.D == 64) e = go(std::integral_constant<int, 64>{}, One{});
-  else if (s.D == 128) e = ctas == 2 ? go(std::integral_constant<int, 128>{}, Two{}) : go(std::integral_constant<int, 128>{}, One{});
-  else e = ctas == 2 ? go(std::integral_constant<int, 256>{}, Two{}) : go(std::integral_constant<int, 256>{}, One{});
+  else if (s.D == 128 && ctas == 1) e = go(std::integral_constant<int, 128>{}, One{});
+  else if (s.D == 128) e = go(std::integral_constant<int, 128>{}, Two{});
+  else if (ctas == 1) e = go(std::integral_constant<int, 256>{}, One{});
+  else e = go(std::integral_constant<int, 256>{}, Two{});
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
   const MergeParams mp{part, head, info, flags, static_cast<uint16_t*>(o), status, scale * kLog2e,
                        s.Hq, s.Hkv, s.D, runs, ctas};
@@ -1524,7 +1540,8 @@ moe_status attn(const moe_paged_shape* shape, const void* q, const moe_paged_cac
   cfg.numAttrs = 1;
   cfg.blockDim = dim3(kMergeThreads);
   cfg.dynamicSmemBytes = 0;
-  e = by_row ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<true>, mp) : cudaLaunchKernelEx(&cfg, paged_merge_kernel<false>, mp);
+  e = by_row ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<true>, mp)
+             : cudaLaunchKernelEx(&cfg, paged_merge_kernel<false>, mp);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "paged merge launch");
 }
 

@@ -16,7 +16,8 @@ bool spec_ok(const moe_rope_spec& s, int D) {
   if (s.layout != MOE_ROPE_HALF && s.layout != MOE_ROPE_PAIRS) return false;
   if (s.norm & ~(MOE_ROPE_NORM_Q | MOE_ROPE_NORM_K)) return false;
   // (with 1e-30 beside the mean square, squares that fall below fp32 miss nothing)
-  return std::isfinite(s.eps) && (s.norm == 0 || s.eps >= 1e-30f) && std::isfinite(s.gain_offset) && std::isfinite(s.magnitude);
+  return std::isfinite(s.eps) && (s.norm == 0 || s.eps >= 1e-30f) && std::isfinite(s.gain_offset) &&
+         std::isfinite(s.magnitude);
 }
 
 bool spec_pointers_ok(const moe_rope_spec& s) {
@@ -26,7 +27,9 @@ bool spec_pointers_ok(const moe_rope_spec& s) {
 
 Spec device_spec(const moe_rope_spec* s) {
   if (s == nullptr) return Spec{};
-  return Spec{reinterpret_cast<const unsigned long long*>(s->turns), {static_cast<const uint16_t*>(s->q_gain), static_cast<const uint16_t*>(s->k_gain)}, s->rot,
+  return Spec{reinterpret_cast<const unsigned long long*>(s->turns),
+              {static_cast<const uint16_t*>(s->q_gain), static_cast<const uint16_t*>(s->k_gain)},
+              s->rot,
               s->layout == MOE_ROPE_PAIRS, s->norm, s->eps, s->gain_offset, s->magnitude};
 }
 

@@ -13,8 +13,8 @@
 // per lane, into shared memory, for all heads that it takes.
 //
 // Bound: a call of few heads by one chain (table and values, angles, the stores:
-// 64 tokens of 16 and 2 heads of 256 2.8 us in a graph, appended to pages 3.3);
-// one of many by HBM (8192 tokens of 40 and 8 heads of 128 35 us, 5.8 TB/s of the
+// 64 tokens of 16 and 2 heads of 256 2.7 us in a graph, appended to pages 3.2);
+// one of many by HBM (8192 tokens of 40 and 8 heads of 128 34 us, 6.0 TB/s of the
 // 6.8 that a copy reaches): a head is read once and written once.
 #pragma once
 
