@@ -500,6 +500,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == kMmaWarp) alloc_columns<kCtas>(&ctl->tmem);
   if (warp == kLoadWarp && lane < 2) prefetch_tmap(lane == 0 ? &tm_k : &tm_v);
+  // (the other block's barriers and columns are waited for when they are needed)
+  if (kCtas == 2) {
+    tc_fence_before();
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  }
   // Launched with programmatic dependent launch: wait for the kernels before
   // this one, then let this call's merge launch (it waits in turn). A block that
   // waits here holds its columns, but those it waits for have theirs: they all
@@ -555,9 +560,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   const bool loads = warp >= kLoadWarp && warp < kLoadWarp + kLoadWarps;
   const int first_window = s_cur.i * kKeys >> p.shift >> 5;
-  const int first_pages = loads && !idle ? look_up(s_cur, first_window) : 0;  // on their way over the barrier
-  tc_fence_before();
-  tile_barrier<kCtas>();  // the barriers and the columns of both blocks are there
+  const int first_pages = loads && !idle ? look_up(s_cur, first_window) : 0;  // on their way meanwhile
+  if (kCtas == 2) {
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+  } else {
+    tc_fence_before();
+    __syncthreads();
+  }
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
   if (threadIdx.x == 0) {
