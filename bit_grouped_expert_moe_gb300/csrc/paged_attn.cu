@@ -61,7 +61,7 @@
 //   a prompt of 4096 103 us, 1.34 PFLOP/s: the tiles' beginnings, ends and cuts;
 //   2048 tokens after 16,384 306 us, a prompt of 16,384 1151 us, 1.91 PFLOP/s, 99 %:
 //     the tensor cores;
-//   2000 tokens after 28,000 positions, 16 heads on 4 of 128, 363 us, 1.31 PFLOP/s, of 64
+//   2000 tokens after 28,000 positions, 16 heads on 4 of 128, 349 us, 1.36 PFLOP/s, of 64
 //     287 us: a unit's products are shorter than its softmax, and the issuing
 //     warp has some 1200 cycles of its own per unit.
 #include <cuda.h>
@@ -838,15 +838,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float a = fmaxf(p.scale_log2, 1e-35f);
     constexpr int kOwn = F::kApart ? D : D / 2;  // columns of O that a half scales
     int met = 0;
-    // this thread's value and its partner's, once both are there
+    // This thread's value and its partner's, once both are there. At 128 head dims,
+    // where the softmax bounds, by a barrier of the two warps alone (2000 tokens
+    // after 28,000 positions 349 us for 362; at 256 a prompt of 4096 takes 104 for
+    // 102.5 so). It has no limit of its own: either warp comes there, or gives up
+    // within the limits of its other waits, has said so by then, and arrives once
+    // in passing (below).
+    constexpr bool kAlone = D == 128;
     auto meet = [&](float v, float& other) -> bool {
       ctl->mx[met & 1][half][row] = v;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->mx_full[quad]);
-      if (!warp_wait(&ctl->mx_full[quad], met & 1)) return false;
+      if constexpr (kAlone) {
+        asm volatile("barrier.sync.aligned %0, 64;" ::"r"(1 + quad) : "memory");
+      } else {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->mx_full[quad]);
+        if (!warp_wait(&ctl->mx_full[quad], met & 1)) return false;
+      }
       other = ctl->mx[met & 1][half ^ 1][row];
       ++met;
-      return true;
+      return !kAlone || __all_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&ctl->abort) == 0);
     };
     Cursor un = cur;
     Turn<kBufs> sb;  // the unit's S, P and barriers
@@ -1070,6 +1080,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&ctl->o_empty);
       if (u + nu < U) un.next(p, r, kTileRows);
     }
+    if (kAlone && !ok) asm volatile("barrier.arrive.aligned %0, 64;" ::"r"(1 + quad) : "memory");
   } else if (warp < kSoftWarps + kAuxWarps) {
     // ------------------------------------------- Q, and V that is not finite
     const int t = threadIdx.x - 32 * kSoftWarps;
