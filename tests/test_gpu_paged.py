@@ -501,6 +501,7 @@ def test_bad_tables_are_reported(moelib, cuda_dev):
     (16, 2, 256, [20000], [1], 3),   # a block on its own
     (16, 2, 256, [3000], [600], 0),  # the first block of a pair, which issues the products,
     (16, 2, 256, [3000], [600], 1),  # the second
+    (16, 4, 128, [20000], [1], 3), (16, 4, 128, [3000], [600], 0), (16, 4, 128, [3000], [600], 1),
     (8, 2, 64, [3000], [900], 2)])
 def test_timeout_is_reported_not_hung(moelib, cuda_dev, Hq, Hkv, D, lens, news, block):
     """One grid block never brings its keys: the waits run out after 20 ms, the call reports it, and the next one on

@@ -242,29 +242,40 @@ def test_binding_refuses_tensors_of_the_wrong_kind(moelib, monkeypatch):
 
 # ------------------------------------------------------- the kernel's plan ---
 
-def _order(ends):
-    """The order of the products S and O of a run whose units end tiles where `ends` says, as the issuing warp goes."""
-    U, su, ou, sfirst, out = len(ends), 0, 0, True, []
-    while ou < U:
-        if su < U and su <= ou + 1 and (su == ou or not sfirst):
-            out.append(("S", su))
-            sfirst = ends[su]
-            su += 1
-        else:
-            out.append(("O", ou))
-            ou += 1
+def _order(tiles, bufs):
+    """The order of the products S and O of a run of tiles of so many units, as the issuing and loading warps go: S ahead
+    of O as far as there are buffers, but not over a tile's end."""
+    out, u = [], 0
+    for nu in tiles:
+        for j in range(1 - bufs, nu):
+            if j + bufs - 1 < nu:
+                out.append(("S", u + j + bufs - 1))
+            if j >= 0:
+                out.append(("O", u + j))
+        u += nu
     return out
 
 
-def test_places_in_the_ring_are_the_order_of_use():
+@pytest.mark.parametrize("bufs", [2, 3])
+def test_places_in_the_ring_are_the_order_of_use(bufs):
+    """V's place as the warps that look through it have it; no S is written before O has taken the weights that lay
+    there; a stage of the ring (one, two or four to a place) is always the same loading warp's."""
     rng = random.Random(5)
     for _ in range(500):
-        U = rng.randint(1, 12)
-        ends = [rng.random() < rng.choice([0.0, 0.2, 0.6, 1.0]) for _ in range(U)]
-        ahead = [not ends[u] and u + 1 < U for u in range(U)]
-        place = {("S", u): 2 * u - (u > 0 and ahead[u - 1]) for u in range(U)}
-        place.update({("O", u): 2 * u + 1 + ahead[u] for u in range(U)})
-        assert [place[x] for x in _order(ends)] == list(range(2 * U))
+        tiles = [rng.randint(1, rng.choice([1, 2, 12])) for _ in range(rng.randint(1, 6))]
+        order = _order(tiles, bufs)
+        at = {x: i for i, x in enumerate(order)}
+        assert len(at) == len(order) == 2 * sum(tiles)
+        u = 0
+        for nu in tiles:
+            for j in range(nu):
+                assert at["O", u + j] == 2 * (u + j) + 1 + min(bufs - 1, nu - 1 - j)
+                assert u + j < bufs or at["S", u + j] > at["O", u + j - bufs]
+                assert at["S", u + j] < at["O", u + j]
+            u += nu
+        for parts in (1, 2, 4):
+            for place in range(len(order)):
+                assert all((place * parts + h) % 8 % 2 == (place * parts + h) % 2 for h in range(parts))
 
 
 def test_bits_of_values_that_are_not_finite_fit():
