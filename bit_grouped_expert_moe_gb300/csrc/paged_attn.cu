@@ -59,8 +59,8 @@
 //     memory of 0.7 us each (tables, page number, K, V, states, their merge);
 //   one after 131,072 50 us, 5.4 TB/s; 64 sequences of 4096, 86 us, 6.3 TB/s: HBM;
 //   a prompt of 4096 103 us, 1.34 PFLOP/s: the tiles' beginnings, ends and cuts;
-//   2048 tokens after 16,384 306 us, a prompt of 16,384 1151 us, 1.91 PFLOP/s, 99 %:
-//     the tensor cores;
+//   2048 tokens after 16,384 306 to 316 us, a prompt of 16,384 1151 to 1210 us, 1.82 to
+//     1.91 PFLOP/s: the tensor cores;
 //   2000 tokens after 28,000 positions, 16 heads on 4 of 128, 349 us, 1.36 PFLOP/s, of 64
 //     287 us: a unit's products are shorter than its softmax, and the issuing
 //     warp has some 1200 cycles of its own per unit.

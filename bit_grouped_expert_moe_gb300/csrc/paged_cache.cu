@@ -128,7 +128,7 @@ struct KeepParams {
 // read in order, so a row is never written before all that read it have: a
 // thread may read as far ahead as it likes, and columns do not meet.
 // Bound: the chain kept and start -> path -> pages -> rows (64 sequences of up
-// to 8 kept rows 2.9 us in a graph); the rows themselves are read and written once.
+// to 8 kept rows 2.5 us in a graph); the rows themselves are read and written once.
 __global__ void __launch_bounds__(kKeepThreads) paged_keep_kernel(const KeepParams p) {
   __shared__ long long s_row[2][kMaxPath];  // from, to: rows of the pools at KV head 0, in rows
   asm volatile("griddepcontrol.wait;" ::: "memory");
