@@ -151,10 +151,10 @@ struct Ctl {
   uint64_t look, fixed;
   uint64_t q_full, q_empty;
   uint64_t s_full[kMaxBufs], p_full[kMaxBufs];
-  // One arrival per unit, on alternate barriers. A waiter's parity is safe if
+  // One arrival per unit, on barriers in turn (Turn). A waiter's parity is safe if
   // it cannot be two phases off: the softmax of unit u has seen S of unit u,
-  // whose commit covers the products of u - 2, and those of u + 1 and u + 2
-  // wait for its weights.
+  // whose commit covers the products of u - kBufs, and those from u on wait for
+  // its weights.
   uint64_t pv_done[kMaxBufs];
   uint64_t o_empty;               // O of a finished tile has been read
   uint64_t peer_s[kMaxBufs], peer_o[kMaxBufs];  // the other block is ready for a unit's S, for its O
@@ -165,7 +165,7 @@ struct Ctl {
   int bad_page;
   int bad_any[kBadTiles];
   uint32_t bad[kBadTiles][kBadUnits][kKeys / 32];
-  float mx[2][2][kRows];  // [unit parity][half]
+  float mx[2][2][kRows];  // [meetings in turn][half]
 };
 
 // Where a block's run starts, for the merge kernel: what every block of it reads
