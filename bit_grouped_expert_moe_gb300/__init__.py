@@ -701,7 +701,7 @@ def rope(shape, spec: RopeSpec, q, k, positions, q_out, k_out, stream=None):
                 and k_out.stride() == (kos or Hk * D, D, 1) and k_out.get_device() == dev):
             _kv8_tensor(w, "k_out", k_out, dev, _BF16, dims, (kos or Hk * D, D, 1))
     if positions is not None and not (positions.dtype is _I32 and positions.shape == (T,)
-            and positions.stride() == (1,) and positions.get_device() == dev):
+            and positions.is_contiguous() and positions.get_device() == dev):
         _kv8_tensor(w, "positions", positions, dev, _I32, (T,), (1,))
     rc = lib().moe_rope(shape, spec._c, q.data_ptr() if Hq else None, k.data_ptr() if Hk else None, _ptr(positions),
                         q_out.data_ptr() if Hq else None, k_out.data_ptr() if Hk else None,
@@ -780,19 +780,19 @@ def paged_append(shape, spec, q, k_new, v_new, offsets, starts, cache: PagedCach
                 and q.stride() == (qs or Hq * D, D, 1) and q.get_device() == dev):
             _kv8_tensor(w, "q", q, dev, _BF16, (T, Hq, D), (qs or Hq * D, D, 1))
         if not (q_out.dtype is _BF16 and q_out.shape == (T, Hq, D)
-                and q_out.stride() == (Hq * D, D, 1) and q_out.get_device() == dev):
+                and q_out.is_contiguous() and q_out.get_device() == dev):
             _kv8_tensor(w, "q_out", q_out, dev, _BF16, (T, Hq, D), (Hq * D, D, 1))
     if not (k_new.dtype is _BF16 and k_new.shape == dims and k_new.stride() == strides and k_new.get_device() == dev):
         _kv8_tensor(w, "k_new", k_new, dev, _BF16, dims, strides)
     if not (v_new.dtype is _BF16 and v_new.shape == dims and v_new.stride() == strides and v_new.get_device() == dev):
         _kv8_tensor(w, "v_new", v_new, dev, _BF16, dims, strides)
     if not (offsets.dtype is _I32 and offsets.shape == (B + 1,)
-            and offsets.stride() == (1,) and offsets.get_device() == dev):
+            and offsets.is_contiguous() and offsets.get_device() == dev):
         _kv8_tensor(w, "offsets", offsets, dev, _I32, (B + 1,), (1,))
-    if not (starts.dtype is _I32 and starts.shape == (B,) and starts.stride() == (1,) and starts.get_device() == dev):
+    if not (starts.dtype is _I32 and starts.shape == (B,) and starts.is_contiguous() and starts.get_device() == dev):
         _kv8_tensor(w, "starts", starts, dev, _I32, (B,), (1,))
     if positions is not None and not (positions.dtype is _I32 and positions.shape == (T,)
-            and positions.stride() == (1,) and positions.get_device() == dev):
+            and positions.is_contiguous() and positions.get_device() == dev):
         _kv8_tensor(w, "positions", positions, dev, _I32, (T,), (1,))
     rc = lib().moe_paged_append(shape, None if spec is None else spec._c, None if q is None else q.data_ptr(),
                                 k_new.data_ptr(), v_new.data_ptr(), offsets.data_ptr(), starts.data_ptr(),
@@ -829,14 +829,14 @@ def paged_attn(shape, q, cache: PagedCache, offsets, lens, o, workspace, tree=No
     if not (q.dtype is _BF16 and q.shape == dims and q.stride() == strides and q.get_device() == dev):
         _kv8_tensor(w, "q", q, dev, _BF16, dims, strides)
     if not (offsets.dtype is _I32 and offsets.shape == (B + 1,)
-            and offsets.stride() == (1,) and offsets.get_device() == dev):
+            and offsets.is_contiguous() and offsets.get_device() == dev):
         _kv8_tensor(w, "offsets", offsets, dev, _I32, (B + 1,), (1,))
-    if not (lens.dtype is _I32 and lens.shape == (B,) and lens.stride() == (1,) and lens.get_device() == dev):
+    if not (lens.dtype is _I32 and lens.shape == (B,) and lens.is_contiguous() and lens.get_device() == dev):
         _kv8_tensor(w, "lens", lens, dev, _I32, (B,), (1,))
-    if not (o.dtype is _BF16 and o.shape == dims and o.stride() == (H * D, D, 1) and o.get_device() == dev):
+    if not (o.dtype is _BF16 and o.shape == dims and o.is_contiguous() and o.get_device() == dev):
         _kv8_tensor(w, "o", o, dev, _BF16, dims, (H * D, D, 1))
     if tree is not None and not (tree.dtype is _I64 and tree.shape == (T, words)
-            and tree.stride() == (words, 1) and tree.get_device() == dev):
+            and tree.is_contiguous() and tree.get_device() == dev):
         _kv8_tensor(w, "tree", tree, dev, _I64, (T, words), (words, 1))
     if not (workspace.dtype is torch.uint8 and workspace.is_contiguous() and workspace.get_device() == dev):
         _kv8_tensor(w, "workspace", workspace, dev, torch.uint8, (size,), (1,))
@@ -868,15 +868,15 @@ def paged_keep(shape, cache: PagedCache, starts, kept, path, lens_out=None, stat
     dev, width = cache._dev, path.shape[-1]
     if not (cache._dims == (n, H, page, D) and cache._tdims == (B, mp) and dev >= 0 and _current_device() == dev):
         cache._device(w, f)
-    if not (starts.dtype is _I32 and starts.shape == (B,) and starts.stride() == (1,) and starts.get_device() == dev):
+    if not (starts.dtype is _I32 and starts.shape == (B,) and starts.is_contiguous() and starts.get_device() == dev):
         _kv8_tensor(w, "starts", starts, dev, _I32, (B,), (1,))
-    if not (kept.dtype is _I32 and kept.shape == (B,) and kept.stride() == (1,) and kept.get_device() == dev):
+    if not (kept.dtype is _I32 and kept.shape == (B,) and kept.is_contiguous() and kept.get_device() == dev):
         _kv8_tensor(w, "kept", kept, dev, _I32, (B,), (1,))
     if not (path.dtype is _I32 and path.shape == (B, width)
-            and path.stride() == (width, 1) and path.get_device() == dev):
+            and path.is_contiguous() and path.get_device() == dev):
         _kv8_tensor(w, "path", path, dev, _I32, (B, width), (width, 1))
     if lens_out is not None and not (lens_out.dtype is _I32 and lens_out.shape == (B,)
-            and lens_out.stride() == (1,) and lens_out.get_device() == dev):
+            and lens_out.is_contiguous() and lens_out.get_device() == dev):
         _kv8_tensor(w, "lens_out", lens_out, dev, _I32, (B,), (1,))
     rc = lib().moe_paged_keep(shape, cache._c, starts.data_ptr(), kept.data_ptr(), path.data_ptr(), width,
                               None if lens_out is None else lens_out.data_ptr(),
