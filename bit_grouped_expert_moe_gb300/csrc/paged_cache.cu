@@ -9,6 +9,7 @@
 
 #include "kernels.h"
 #include "paged.cuh"
+#include "paged_path.h"
 #include "rope.cuh"
 
 namespace bgmoe {
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(kKeepThreads) paged_keep_kernel(const KeepPara
     for (int k = t; k < kept; k += kKeepThreads) {
       const int32_t* path = p.path + (long long)b * p.path_stride + k;
       const int from = ld(path), before = k > 0 ? ld(path - 1) : -1;
-      if (from <= before || start + (long long)from >= limit) {
+      if (!path_entry_ok(from, before, k, start, limit)) {
         bad = true;
         continue;
       }
