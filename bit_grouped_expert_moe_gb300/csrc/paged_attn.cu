@@ -553,10 +553,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   }
   const bool idle = s_bad || s_unit[0] >= s_unit[1];  // both blocks of a run alike
-  // A lane's page of the w-th 32 of a sequence, as the table has it: -2 past the context.
+  // A lane's page of the w-th 32 of a sequence: -2 past the context, -1 for any negative entry.
   auto look_up = [&](const Cursor& k, int w) -> int {
     const int page = 32 * w + lane;
-    return page << p.shift < k.len ? ld(p.tables + (size_t)k.b * p.max_pages + page) : -2;
+    return page << p.shift < k.len ? max(ld(p.tables + (size_t)k.b * p.max_pages + page), -1) : -2;
   };
   const bool loads = warp >= kLoadWarp && warp < kLoadWarp + kLoadWarps;
   const int first_window = s_cur.i * kKeys >> p.shift >> 5;
