@@ -100,7 +100,12 @@ constexpr int kMaxCtas = 256;  // workspace bound on the grid
 // token of 64 sequences 36.3, 35.2, 36.7, 37.6, of 8 ragged ones 58.4, 55.3, 54.8, 54.7.
 constexpr int kTileCost = 3, kFewRowsCost = 1;
 constexpr float kMinusBig = -3.402823466e38f;  // running-max start, finite: m - m_new is never NaN
-constexpr float kLargeScore = 1048576.f;      // 2^20, in base 2
+// Weights are 2^(x a - c), c = m a rounded (a: scale log2 e), where |c| is below
+// this: c is off by up to 2^-17 there, which all weights that are made relative to one
+// m share, but not those of another m: after a row's maximum moved, in the other half
+// of a unit at 64 head dims, in another run's partial state. (Up to 2^20, where c is
+// off by 2^-5, shares of a row's weight were wrong by up to 4 %.)
+constexpr float kLargeScore = 256.f;
 // A row's scores may pass its m by this much (base 2: weights to 2^8) before O is
 // scaled to a new one, but in calls of few rows (kByRowRows): there m is the
 // largest score so far, whose weight is 1, so that where one position has most
@@ -943,10 +948,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t a2 = pack2(a, a);
           const float c = m * a;
           if (!__any_sync(0xffffffffu, see > 0 && !(fabsf(c) < kLargeScore))) {
-            // x a - c: what c, rounded, is off by, 2^-24 of it, all of the row's weights share
+            // x a - c in one step
             const uint64_t c2 = pack2(-c, -c);
             weights([&](uint64_t v) { return fma2(v, a2, c2); });
-          } else {  // where that is more than 2^-4, the difference first
+          } else {  // the difference first: off by 2^-24 of itself
             const uint64_t m2 = pack2(-m, -m);
             weights([&](uint64_t v) { return mul2(add2(v, m2), a2); });
           }

@@ -127,10 +127,11 @@ moe_status moe_paged_workspace_bytes(const moe_paged_shape* shape, size_t* bytes
  * relative to a running maximum that the row's largest score passes by a
  * factor of 2^8 at most, their sum in fp32, each rounded to bf16 for the
  * product with V; o is rounded once to bf16. So o is within
- *   2^-8 |o| + 2^-8 sum_j p_j |V_j|
- * of the formula, and of what fp32's errors of the scores do to p. In calls
+ *   2^-8 |o| + (2^-8 + 2^-15) sum_j p_j |V_j|
+ * of the formula (2^-15: the exponents, whatever the size of the scores), and of
+ * what fp32's errors of the scores and the sums do to p. In calls
  * with T * Hq <= 16 * B * Hkv the running maximum is the largest score so far,
- * and the sum is without the position that has it (its weight is 1). A query
+ * and the sum is without the position that has it (its weight is 1, to 2^-17). A query
  * that sees a value of V which is infinite or NaN, or a score that is, has NaN
  * or infinities in its output, and is NaN throughout where that position is
  * not seen by all queries that share its tile.

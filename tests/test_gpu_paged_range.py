@@ -1,0 +1,40 @@
+"""Attention over the paged cache where its numbers are far from the usual ones. Against fp64."""
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_paged import Paged
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("top", [1 << 9, 1 << 14, 1 << 18, 700_000])
+@pytest.mark.parametrize("D,Hkv,r,lens,news", [
+    (64, 1, 8, [2000], [1]), (128, 1, 8, [2000], [1]), (256, 1, 8, [2000], [1]),     # a unit per run: partial states
+    (64, 8, 2, [700] * 8, [1] * 8), (128, 8, 2, [700] * 8, [1] * 8), (256, 8, 2, [700] * 8, [1] * 8),  # units of one run
+    (64, 2, 4, [1500], [300]), (128, 2, 4, [1500], [300]), (256, 2, 4, [1500], [300])])  # many rows
+def test_large_scores_that_are_exact(moelib, cuda_dev, D, Hkv, r, lens, news, top):
+    """Scores are whole numbers near `top` (at scale 1; every product and sum is below 2^24), level + 0, 1, 2 or 3 by
+    halves of units, and V is 1 in the quarter of the head dims that belongs to its level: o is the levels' shares of
+    the weight, of which no error of a score takes anything. Every weight and o are rounded to bf16, 2^-8 of each; the
+    exponents (below 2^3 from the largest) are off by 2^-16 at most and a factor of 1 + 2^-22, so a share by 2^-15,
+    and a sum of up to 2000 positions in chains of 200 additions by 200 2^-24 < 2^-16 of it."""
+    p = Paged(moelib, lens, Hkv, D, 32, seed=81)
+    rng = np.random.default_rng(82)
+    K, V = torch.zeros_like(p.gpu.k), torch.zeros_like(p.gpu.v)
+    for b, n in enumerate(lens):
+        level = rng.integers(0, 4, size=-(-n // 64)).repeat(64)[:n]
+        for j in range(n):
+            page, row = int(p.tables[b][j // 32]), j % 32
+            K[page, :, row, 0], K[page, :, row, 1] = 64.0, float(level[j])
+            V[page, :, row, int(level[j])::4] = 1.0
+    p.gpu.k.copy_(K), p.gpu.v.copy_(V)
+    T, Hq = sum(news), Hkv * r
+    q = torch.zeros(T, Hq, D)
+    q[..., 0] = torch.from_numpy(rng.uniform(0.8, 1.0, size=(T, Hq)) * top / 64)
+    q[..., 1] = 1.0
+    q = q.to(torch.bfloat16)  # 64 times a value of 4 or more that has 8 bits is whole
+    want, o_abs = p.exact(q, news, scale=1.0)
+    got = p.attend(q, news, scale=1.0).double().cpu().numpy()
+    tol = 2.0 ** -8 * want + (2.0 ** -8 + 2.0 ** -14) * o_abs
+    assert (np.abs(got - want) <= tol).all(), float((np.abs(got - want) / np.maximum(tol, 1e-30)).max())
