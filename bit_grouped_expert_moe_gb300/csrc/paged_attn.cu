@@ -558,10 +558,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   }
   const bool idle = s_bad || s_unit[0] >= s_unit[1];  // both blocks of a run alike
-  // A lane's page of the w-th 32 of a sequence: -2 past the context, -1 for any negative entry.
+  // A lane's page of the w-th 32 of a sequence, as the table has it; anything past the context.
+  // (Whether it is there, and needed, is asked where it is used: the value is on its way until then.)
   auto look_up = [&](const Cursor& k, int w) -> int {
     const int page = 32 * w + lane;
-    return page << p.shift < k.len ? max(ld(p.tables + (size_t)k.b * p.max_pages + page), -1) : -2;
+    return page << p.shift < k.len ? ld(p.tables + (size_t)k.b * p.max_pages + page) : 0;
   };
   const bool loads = warp >= kLoadWarp && warp < kLoadWarp + kLoadWarps;
   const int first_window = s_cur.i * kKeys >> p.shift >> 5;
@@ -764,9 +765,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Box bv(p.shift, F::kShiftV, F::kSlabsV, true, 0, rank * F::kSlabsV);
     int issued = 0;
     bool bad = false;
-    auto settle = [&](int id, int g) -> int {  // its place in the pools
-      if (id != -2 && (id < 0 || id >= p.n_pages)) bad = true;
-      return id < 0 || id >= p.n_pages ? outside : id * p.Hkv + g;
+    auto settle = [&](int id, int g, bool needed) -> int {  // its place in the pools
+      const bool there = id >= 0 && id < p.n_pages;
+      bad |= needed && !there;
+      return needed && there ? id * p.Hkv + g : outside;
     };
     if ((int)blockIdx.x != p.stalled) {
       // K and V of every unit in the order of their use, one copy of the code:
@@ -795,7 +797,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               then = look_up(k, ++window + 1);
             }
             const int id = __shfl_sync(0xffffffffu, pages, page + lane);
-            z[kBufs - 1] = settle(lane == 0 || lane << p.shift < kKeys ? id : -2, k.g);
+            // the unit's, as far as the context goes
+            z[kBufs - 1] = settle(id, k.g, (lane == 0 || lane << p.shift < kKeys) && (page + lane) << p.shift < k.len);
           }
 #pragma unroll 1
           for (int v = e < nu ? 0 : 1; ok && v < (j < 0 ? 1 : 2); ++v, ++place) {
