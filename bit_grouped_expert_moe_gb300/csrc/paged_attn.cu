@@ -843,7 +843,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quad = warp & 3, half = warp >> 2;
     const int row = quad * 32 + lane;
     const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
-    const float a = fmaxf(p.scale_log2, 1e-35f);
+    // (with any a > 0 and m >= kMinusBig: what is not seen, -inf, weighs 0, and a row that has seen
+    // nothing yet has L = 0 and O = 0, whatever factor they take)
+    const float a = p.scale_log2;
     constexpr int kOwn = F::kApart ? D : D / 2;  // columns of O that a half scales
     int met = 0;
     // This thread's value and its partner's, once both are there. At 128 head dims,
@@ -1501,7 +1503,8 @@ moe_status attn(const moe_paged_shape* shape, const void* q, const moe_paged_cac
   if (!cache_ok(cache) || !aligned(offsets, 4) || !aligned(lens, 4) || !aligned(q, 16) || !aligned(o, 16) ||
       !aligned(tree, 8) || !workspace || !aligned(workspace, 256))
     return MOE_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !(scale < INFINITY)) return MOE_ERR_INVALID_ARG;
+  const float scale_log2 = scale * kLog2e;  // of all kernels of the call
+  if (!(scale > 0.f) || !(scale_log2 < INFINITY)) return MOE_ERR_INVALID_ARG;
   if (ws_bytes < workspace_bytes(s)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (s.T == 0) {
@@ -1523,7 +1526,7 @@ moe_status attn(const moe_paged_shape* shape, const void* q, const moe_paged_cac
   const bool by_row = (long long)s.T * s.Hq <= kByRowRows * (long long)s.B * s.Hkv;
   const Params prm{static_cast<const uint16_t*>(q), offsets, lens, cache->tables,
                    reinterpret_cast<const unsigned long long*>(tree), static_cast<uint16_t*>(o), part, head, info, flags,
-                   scale * kLog2e, by_row ? 0.f : kSlack, s.B, s.T, s.Hq, s.Hkv, page_shift(s.page), s.n_pages, s.max_pages, s.tree_words,
+                   scale_log2, by_row ? 0.f : kSlack, s.B, s.T, s.Hq, s.Hkv, page_shift(s.page), s.n_pages, s.max_pages, s.tree_words,
                    s.q_stride ? s.q_stride : s.Hq * s.D, ((1ull << 36) + r - 1) / r,
                    (long long)s.T * s.Hq > 32ll * s.B * s.Hkv ? kTileCost : kFewRowsCost, by_row,
                    narrow(s, kRows * ctas), stalled, timeout_ns};
@@ -1561,7 +1564,7 @@ moe_status attn(const moe_paged_shape* shape, const void* q, const moe_paged_cac
   else if (ctas == 1) e = go(std::integral_constant<int, 256>{}, One{});
   else e = go(std::integral_constant<int, 256>{}, Two{});
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
-  const MergeParams mp{part, head, info, flags, static_cast<uint16_t*>(o), status, scale * kLog2e,
+  const MergeParams mp{part, head, info, flags, static_cast<uint16_t*>(o), status, scale_log2,
                        s.Hq, s.Hkv, s.D, runs, ctas};
   const long long most = by_row ? (long long)s.T * s.Hq : sms;  // no more items than rows
   cfg.gridDim = dim3((unsigned)(most < sms ? most : sms));

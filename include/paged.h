@@ -114,8 +114,9 @@ moe_status moe_paged_workspace_bytes(const moe_paged_shape* shape, size_t* bytes
  * NULL if and only if tree_words is 0 (8-byte aligned). q, o and the pools
  * must be 16-byte aligned, the workspace 256-byte aligned with ws_bytes >=
  * moe_paged_workspace_bytes(); its contents need no initialisation, and calls
- * that may overlap on the GPU need one each. `scale` must be finite and > 0
- * (1/sqrt(D) is the usual value). The int32 at the start of the workspace is
+ * that may overlap on the GPU need one each. `scale` must be > 0 and below
+ * 2.35e38, so that scale log2(e) is finite in fp32 (1/sqrt(D) is the usual
+ * value). The int32 at the start of the workspace is
  * the call's status word (read it with moe_status_read): MOE_OK,
  * MOE_ERR_INVALID_ARG or MOE_ERR_DEVICE_TIMEOUT (a bounded wait ran out; o is
  * not valid). Where offsets or lens break the rules, or a sequence has more

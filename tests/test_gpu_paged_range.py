@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_paged import Paged
+from tests.test_gpu_paged import Paged, _rand
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +38,12 @@ def test_large_scores_that_are_exact(moelib, cuda_dev, D, Hkv, r, lens, news, to
     got = p.attend(q, news, scale=1.0).double().cpu().numpy()
     tol = 2.0 ** -8 * want + (2.0 ** -8 + 2.0 ** -14) * o_abs
     assert (np.abs(got - want) <= tol).all(), float((np.abs(got - want) / np.maximum(tol, 1e-30)).max())
+
+
+@pytest.mark.parametrize("scale,std", [(2.0 ** -120, 7e17), (1e-39, 1.5e18), (1e30, 7e-16)])
+@pytest.mark.parametrize("D,lens,news", [(64, [900], [1]), (256, [2000], [1]), (128, [700], [200]), (256, [600, 40], [100, 40])])
+def test_scales_near_the_ends_of_fp32(moelib, cuda_dev, D, lens, news, scale, std):
+    """Scores far from 1 that the scale brings back there, in single tiles and joined from partial states."""
+    p = Paged(moelib, lens, 2, D, 32, seed=83, std=(std, 1.0))
+    q = _rand(torch.Generator().manual_seed(84), sum(news), 8, D, std=std * (64 / D) ** 0.5)
+    p.check(q, news, scale=scale)

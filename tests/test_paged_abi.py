@@ -198,6 +198,14 @@ def test_attention_arguments(moelib):
     assert L.moe_paged_workspace_bytes(REF(sh), None) == 1
 
 
+@pytest.mark.parametrize("scale", [3.4028234e38, 2.36e38, 1e39])
+def test_a_scale_whose_base_2_form_passes_fp32(moelib, scale):
+    """scale log2(e) would be infinite: refused (as invalid, not for the workspace, which is too small here)."""
+    m, L, sh = moelib, moelib.lib(), moelib.paged_shape(**PAGED)
+    for s, code in ((scale, 1), (2.3e38, 3)):
+        assert L.moe_paged_attn(REF(sh), ADDR[0], REF(_cache(m)), ADDR[1], ADDR[2], None, s, ADDR[3], ADDR[4], 0, None) == code
+
+
 def test_a_workspace_serves_calls_of_any_number_of_tokens(moelib):
     sizes = {moelib.paged_workspace_bytes(moelib.paged_shape(**{**PAGED, "T": T, "tree_words": w}))
              for T in (0, 1, 50, 4000, 1 << 20) for w in (0, 4)}
