@@ -450,6 +450,22 @@ __device__ __forceinline__ uint64_t tree_bits(const unsigned long long* w, int w
   return v;
 }
 
+// 1 / l of a row, whose sum of weights l is 0 in two cases: it sees nothing, and is
+// zero; or all that it sees scores -inf, and its softmax is NaN. ctx: positions
+// before the new ones; token: of the call, the tok-th of its sequence.
+__device__ __noinline__ float inverse_of_none(const unsigned long long* tree, int words, int token, int tok, int ctx) {
+  const int see = ctx + tok + 1;
+  bool any = see > 0 && (tree == nullptr || ctx > 0);
+  if (!any && see > 0) {
+#pragma unroll 1
+    for (int first = 0; first < see && !any; first += 64) {
+      const uint64_t bits = tree_bits(tree + (size_t)token * words, words, first, ctx);
+      any = (see - first >= 64 ? bits : bits & ((1ull << (see - first)) - 1)) != 0ull;
+    }
+  }
+  return any ? __uint_as_float(0x7FC00000u) : 0.f;
+}
+
 template <int D, int kCtas>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -1008,7 +1024,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int d0 = half * (D / 2);
         const uint32_t out = smem_u32(smem + F::kOutOffset) + warp * (16 * F::kOutPitch);
         if (!mid && ends) {
-          const float inv = l == 0.f ? 0.f : 1.f / l;
+          float inv = 1.f / l;
+          if (l == 0.f) inv = see > 0 ? inverse_of_none(p.tree, p.words, un.lo + tok, tok, ctx) : 0.f;
           f0 *= inv, f1 *= inv;
           // 16 rows by 64 dims at a time through shared memory: 8 lanes write a row's
           // 128 bytes, 4 rows at once. A half has half of the dims of all rows, or
@@ -1201,8 +1218,9 @@ struct MergeParams {
   const int32_t* flags;
   uint16_t* o;
   int32_t* status;
+  const unsigned long long* tree;
   float scale_log2;
-  int Hq, Hkv, D, C, ctas;  // C: runs
+  int Hq, Hkv, D, C, ctas, words;  // C: runs
 };
 
 constexpr int kMergeWarps = 16;
@@ -1306,6 +1324,10 @@ __global__ void __launch_bounds__(kMergeThreads, 1) paged_merge_kernel(const Mer
       return i1.z - i1.y + tok < 0 ? nullptr
                                    : p.o + ((size_t)(i1.x + tok) * p.Hq + (size_t)i0.x * r + rho - tok * r) * D;
     };
+    auto inverse = [&](float L, int row) -> float {
+      const int tok = (i0.y * rows + row) / r;
+      return L != 0.f ? 1.f / L : inverse_of_none(p.tree, p.words, i1.x + tok, tok, i1.z - i1.y);
+    };
     if (kByRow) {
       const bool shared = there <= kFewRows && states > kFewStates;
       const int row = shared ? part : part * kMergeWarps + warp, from = shared ? warp : 0, step = shared ? kMergeWarps : 1;
@@ -1354,7 +1376,7 @@ __global__ void __launch_bounds__(kMergeThreads, 1) paged_merge_kernel(const Mer
       }
       uint16_t* out = output(row);
       if (!shared) {
-        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const float inv = inverse(L, row);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           if (on && i < wide && out != nullptr)
@@ -1377,7 +1399,7 @@ __global__ void __launch_bounds__(kMergeThreads, 1) paged_merge_kernel(const Mer
           l = fmaf(e, s_l[w], l);
           o = fmaf(e, s_acc[w][t], o);
         }
-        out[t] = __bfloat16_as_ushort(__float2bfloat16_rn(l == 0.f ? 0.f : o * (1.f / l)));
+        out[t] = __bfloat16_as_ushort(__float2bfloat16_rn(o * inverse(l, row)));
       }
       __syncthreads();
     } else {
@@ -1427,7 +1449,7 @@ __global__ void __launch_bounds__(kMergeThreads, 1) paged_merge_kernel(const Mer
         }
       }
       uint16_t* out = output(row);
-      const float inv = L == 0.f ? 0.f : 1.f / L;
+      const float inv = inverse(L, row);
       if (out != nullptr) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -1564,8 +1586,8 @@ moe_status attn(const moe_paged_shape* shape, const void* q, const moe_paged_cac
   else if (ctas == 1) e = go(std::integral_constant<int, 256>{}, One{});
   else e = go(std::integral_constant<int, 256>{}, Two{});
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
-  const MergeParams mp{part, head, info, flags, static_cast<uint16_t*>(o), status, scale_log2,
-                       s.Hq, s.Hkv, s.D, runs, ctas};
+  const MergeParams mp{part, head, info, flags, static_cast<uint16_t*>(o), status, prm.tree,
+                       scale_log2, s.Hq, s.Hkv, s.D, runs, ctas, s.tree_words};
   const long long most = by_row ? (long long)s.T * s.Hq : sms;  // no more items than rows
   cfg.gridDim = dim3((unsigned)(most < sms ? most : sms));
   cfg.numAttrs = 1;

@@ -132,10 +132,13 @@ moe_status moe_paged_workspace_bytes(const moe_paged_shape* shape, size_t* bytes
  * of the formula (2^-15: the exponents, whatever the size of the scores), and of
  * what fp32's errors of the scores and the sums do to p. In calls
  * with T * Hq <= 16 * B * Hkv the running maximum is the largest score so far,
- * and the sum is without the position that has it (its weight is 1, to 2^-17). A query
- * that sees a value of V which is infinite or NaN, or a score that is, has NaN
- * or infinities in its output, and is NaN throughout where that position is
- * not seen by all queries that share its tile.
+ * and the sum is without the position that has it (its weight is 1, to 2^-17).
+ * A query that sees a value of V which is infinite or NaN has NaN or infinities
+ * in its output, and is NaN throughout where that position is not seen by all
+ * queries that share its tile. One that sees a score of infinity or NaN, or no
+ * score but minus infinity, is NaN; minus infinity beside other scores weighs
+ * nothing. (Scores are formed in fp32, before the scale: from 2^126 on they may
+ * count as infinite.)
  */
 moe_status moe_paged_attn(const moe_paged_shape* shape, const void* q, const moe_paged_cache* cache,
                           const int32_t* offsets, const int32_t* lens, const uint64_t* tree, float scale, void* o,

@@ -3,7 +3,8 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_paged import Paged, _rand
+from oracle import paged
+from tests.test_gpu_paged import Paged, _packed, _rand, words_of
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +48,48 @@ def test_scales_near_the_ends_of_fp32(moelib, cuda_dev, D, lens, news, scale, st
     p = Paged(moelib, lens, 2, D, 32, seed=83, std=(std, 1.0))
     q = _rand(torch.Generator().manual_seed(84), sum(news), 8, D, std=std * (64 / D) ** 0.5)
     p.check(q, news, scale=scale)
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,D,page,lens,news", [
+    (4, 2, 64, 16, [90, 40], [1, 1]), (16, 2, 256, 64, [2000, 300], [1, 1]), (8, 2, 128, 32, [1000, 70], [40, 70]),
+    (4, 2, 64, 32, [900, 200], [150, 60]), (16, 2, 256, 64, [700, 50], [200, 50])])
+def test_a_row_whose_scores_are_all_minus_infinity(moelib, cuda_dev, Hq, Hkv, D, page, lens, news, tree):
+    """It is NaN, as its softmax is. Beside a finite score one of minus infinity weighs nothing, and a row that sees
+    nothing is zero, whatever the keys hold."""
+    p = Paged(moelib, lens, Hkv, D, page, seed=85)
+    q = _rand(torch.Generator().manual_seed(86), sum(news), Hq, D)
+    q[..., 0] = q[..., 0].abs() + 0.125
+    words = [w for n in news for w in words_of([i - 1 if i % 5 else -1 for i in range(n)])] if tree else None
+    if tree:  # rows without a bit; over no context they see nothing
+        for t in range(0, len(words), 7):
+            words[t] = 0
+    r, off = Hq // Hkv, _packed(news)
+
+    def at(b, j):
+        return int(p.tables[b][j // page]), j % page
+
+    # sequence 0, head 1: all keys; sequence 1, head 0: all but one that everybody sees, or the first draft
+    for j in range(lens[0]):
+        pg, row = at(0, j)
+        p.gpu.k[pg, 1, row, 0] = -torch.inf
+    one = 0
+    for j in range(lens[1]):
+        if j != one:
+            pg, row = at(1, j)
+            p.gpu.k[pg, 0, row, 0] = -torch.inf
+    got = p.attend(q, news, words=words).float().cpu()
+    K1, V1 = p.gpu.k[at(1, one)[0], 0, at(1, one)[1]], p.gpu.v[at(1, one)[0], 0, at(1, one)[1]].float().cpu()
+    assert torch.isfinite(K1.float()).all()
+    for b, (n, ln) in enumerate(zip(news, lens)):
+        see = paged.visible(n, ln, words[off[b]:off[b + 1]] if tree else None)
+        for i in range(n):
+            o = got[off[b] + i]
+            if not see[i].any():
+                assert (o == 0).all(), (b, i)
+            elif b == 0:
+                assert torch.isnan(o[r:2 * r]).all() and torch.isfinite(o[:r]).all(), (b, i)
+            elif see[i, one]:
+                assert (o[:r] == V1).all() and torch.isfinite(o[r:]).all(), (b, i)
+            else:
+                assert torch.isnan(o[:r]).all() and torch.isfinite(o[r:]).all(), (b, i)
