@@ -104,12 +104,14 @@ __device__ __forceinline__ uint4 pack8(const float2 (&x)[4]) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
+// The factor first: a value over the root mean square is sqrt(D) at most, while the
+// factor times a gain may pass fp32, or fall below it.
 __device__ __forceinline__ void scale8(float2 (&x)[4], const float* gain, float f) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const float4 g = *reinterpret_cast<const float4*>(gain + 4 * i);
-    x[2 * i] = mul2(x[2 * i], mul2(make_float2(g.x, g.y), make_float2(f, f)));
-    x[2 * i + 1] = mul2(x[2 * i + 1], mul2(make_float2(g.z, g.w), make_float2(f, f)));
+    x[2 * i] = mul2(mul2(x[2 * i], make_float2(f, f)), make_float2(g.x, g.y));
+    x[2 * i + 1] = mul2(mul2(x[2 * i + 1], make_float2(f, f)), make_float2(g.z, g.w));
   }
 }
 // 4 pairs side by side.
@@ -138,12 +140,14 @@ __device__ __forceinline__ void apply(const Spec& s, const Pieces& p, const floa
     float sum = two.x + two.y;
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    float f = rsqrtf(fmaf(sum, inv_D, s.eps));
-    // A finite head whose squares pass fp32: the same of 2^-72 times its values,
-    // beside whose squares (2^-24 at least, 2^120 at most in all) eps is nothing.
-    if (__any_sync(0xffffffffu, !(sum < 3e38f))) {
-      const bool large = !(sum < 3e38f);
-      const float d = large && norm ? 2.117582368135751e-22f : 1.f;  // 2^-72
+    const float mean = fmaf(sum, inv_D, s.eps);
+    float f = rsqrtf(mean);
+    // A finite head whose squares pass fp32, or whose mean with eps does: the same of
+    // 2^-72 times its values and 2^-144 times eps.
+    if (__any_sync(0xffffffffu, !(mean < 3e38f))) {
+      constexpr float kDown = 2.117582368135751e-22f;  // 2^-72
+      const bool large = !(mean < 3e38f);
+      const float d = large && norm ? kDown : 1.f;
       float t = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -153,7 +157,7 @@ __device__ __forceinline__ void apply(const Spec& s, const Pieces& p, const floa
       }
 #pragma unroll
       for (int o = kLanes / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-      if (large) f = rsqrtf(t * inv_D);
+      if (large) f = rsqrtf(fmaf(t, inv_D, s.eps * kDown * kDown));
     }
     if (norm && p.on) {
       scale8(a, gain + p.a, f);

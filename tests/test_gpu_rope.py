@@ -197,3 +197,24 @@ def test_rope_in_a_graph_follows_its_inputs(moelib, cuda_dev):
     g.replay()
     check(qo, *oracle(x[1], list(range(1000, 1009))))
     m.rope(m.rope_shape(0, 4, 0, 256), spec, q[:0], None, pos[:0], qo[:0], None)  # no tokens
+
+
+@pytest.mark.parametrize("D,eps,gain,sizes", [
+    (64, 1e37, 1.0, [1e19, 5e18, 3e19, 1.0, 0.0]),       # eps beside squares whose sum passes fp32
+    (16, 3.35e38, 1.0, [4e18, 4.2e18, 1e10, 3e38]),      # a mean that passes fp32 with eps, not without
+    (128, 1e-6, 1e37, [1e-5, 1e-3, 1e-8, 0.0]),          # gains that pass fp32 with a small head's factor
+    (128, 1e-6, 1e-30, [1e12, 1e16, 1e18, 3e38])])       # ... and fall below it with a large one's
+def test_norm_with_eps_and_gains_near_the_ends_of_fp32(moelib, cuda_dev, D, eps, gain, sizes):
+    """Every finite eps and gain. (Where values, gains or results are below fp32's normal numbers, 2^-126, the factor
+    may lose that much of them: 2^-120.)"""
+    m = moelib
+    gen = torch.Generator().manual_seed(11)
+    g = ((1 + 0.2 * torch.rand(D, generator=gen)) * gain).to(torch.bfloat16)
+    spec = m.rope_spec(None, norm=m.ROPE_NORM_Q, q_gain=g.to(DEV), eps=eps)
+    u = torch.randn(len(sizes), 3, D, generator=gen).clamp(-1, 1)
+    q = (u * torch.tensor(sizes)[:, None, None]).to(torch.bfloat16)
+    q[:, 0, 3] = 0.0
+    qo = torch.empty_like(q, device=DEV)
+    m.rope(m.rope_shape(len(sizes), 3, 0, D), spec, q.to(DEV), None, None, qo, None)
+    want = paged.normed(bf16_bits_to_f64(bits16(q)), bf16_bits_to_f64(bits16(g)), float(np.float32(eps)))
+    check(qo, want, np.abs(want) + 2.0 ** -102)
