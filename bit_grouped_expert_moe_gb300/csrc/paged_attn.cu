@@ -59,11 +59,13 @@
 //     memory of 0.7 us each (tables, page number, K, V, states, their merge);
 //   one after 131,072 50 us, 5.4 TB/s; 64 sequences of 4096, 86 us, 6.3 TB/s: HBM;
 //   a prompt of 4096 103 us, 1.34 PFLOP/s: the tiles' beginnings, ends and cuts;
-//   2048 tokens after 16,384 306 to 316 us, a prompt of 16,384 1151 to 1210 us, 1.82 to
-//     1.91 PFLOP/s: the tensor cores;
-//   2000 tokens after 28,000 positions, 16 heads on 4 of 128, 349 us, 1.36 PFLOP/s, of 64
-//     287 us: a unit's products are shorter than its softmax, and the issuing
+//   2048 tokens after 16,384 307 to 338 us, a prompt of 16,384 1205 to 1235 us, 1.73 to
+//     1.90 PFLOP/s, by the clock: the tensor cores;
+//   2000 tokens after 28,000 positions, 16 heads on 4 of 128, 349 to 355 us, 1.36 PFLOP/s,
+//     of 64 287 us: a unit's products are shorter than its softmax, and the issuing
 //     warp has some 1200 cycles of its own per unit.
+// Where two times are compared, here and below, both are of the step that chose
+// between them, so the quicker one may be above what the call takes now.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -78,7 +80,6 @@ namespace bgmoe {
 namespace paged {
 
 using namespace tc;
-using kv8::empty_tiles;
 using kv8::find_run;
 using kv8::Place;
 using kv8::seq_tiles;
@@ -104,7 +105,9 @@ constexpr float kMinusBig = -3.402823466e38f;  // running-max start, finite: m -
 // this: c is off by up to 2^-17 there, which all weights that are made relative to one
 // m share, but not those of another m: after a row's maximum moved, in the other half
 // of a unit at 64 head dims, in another run's partial state. (Up to 2^20, where c is
-// off by 2^-5, shares of a row's weight were wrong by up to 4 %.)
+// off by 2^-5, shares of a row's weight were wrong by up to 4 %.) Beyond it the
+// other form costs 1 % in a prompt of 4096, 2 % of 2000 tokens after 28,000
+// positions at 128 head dims, 3 % at 64.
 constexpr float kLargeScore = 256.f;
 // A row's scores may pass its m by this much (base 2: weights to 2^8) before O is
 // scaled to a new one, but in calls of few rows (kByRowRows): there m is the

@@ -101,7 +101,8 @@ typedef struct moe_paged_cache {
  * packed. positions may be NULL. q, k_new, v_new, q_out and the pools must be
  * 16-byte aligned, the rest 4-byte aligned. `status`: an int32 device word that the caller zeroed,
  * or NULL. A token whose sequence, position or page breaks the rules is not
- * written (nor its query). Two tokens for one row of a page leave either.
+ * written (nor its query). Two tokens for one row of a page leave either's
+ * heads, of each head one token's.
  * T == 0 is a no-op. */
 moe_status moe_paged_append(const moe_paged_shape* shape, const moe_rope_spec* spec, const void* q, const void* k_new,
                             const void* v_new, const int32_t* offsets, const int32_t* starts, const int32_t* positions,
